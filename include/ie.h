@@ -317,6 +317,51 @@ ie_status ie_bmm_nn(int32_t batch, const ie_mat *A, const ie_mat *B, const ie_ma
 ie_status ie_bmm_tn(int32_t batch, const ie_mat *A, const ie_mat *B, const ie_mat *C,
                     void *ws, size_t ws_bytes, void *stream);
 
+/*
+ * Layer norm of every row of X [M x N], with eps a (C, e) scalar:
+ *   Y = R_Y(gamma * (x - mean) / sqrt(var + eps) + beta),
+ * mean and var (divided by N) of the row.  gamma, beta: N channels as [N x 1]
+ * (one exponent, or one per channel when ROW) or [1 x N] (one exponent);
+ * NULL: 1 and 0.  X, Y: [M x N], each TENSOR or ROW.
+ * The row's sums, its deviations N C - sum C and N^2 var = N sum C^2 -
+ * (sum C)^2 are exact integers.  The rest is held to 53 bits, every operation
+ * rounded half to even once, in this order: t = N^2 var + N^2 eps 2^(-2e),
+ * r = 1 / sqrt(t) (square root, then quotient), h = (N C - sum C) r,
+ * h gamma, (h gamma) + beta.  A row without deviations is beta (0 without
+ * it), also when eps is 0 (r is 0 then).
+ * N <= 16384, eps.mant >= 0, else IE_ERR_UNSUPPORTED.
+ */
+size_t ie_layer_norm_fwd_workspace(int64_t rows, int64_t cols);
+ie_status ie_layer_norm_fwd(const ie_mat *X, const ie_mat *gamma, const ie_mat *beta, ie_scalar eps, const ie_mat *Y,
+                            void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Backward of ie_layer_norm_fwd from its input X (the statistics are computed
+ * again), any of dX, dgamma, dbeta NULL to skip that output:
+ *   dbeta = R(sum_rows dY), dgamma = R(sum_rows dY h),
+ *   dX = R((g - mean(g) - h mean(g h)) / sqrt(var + eps)),  g = dY gamma,
+ * h the normalised row.  As in every contraction, operands whose exponents
+ * vary along the summed axis are first re-expressed at the largest one: gamma
+ * over its channels, dY over the rows in dgamma and dbeta (not in dX).
+ * In the sums over a row and over the rows h is f = R(h 2^20), an integer, so
+ * that G1 = sum g, G2 = sum g f and the column sums are exact; then, to 53
+ * bits, z = (N g - G1) - f (G2 2^-40) and dX = z r, each operation rounded
+ * once (h, r as above).  dY, X, dX: [M x N], each TENSOR or ROW; gamma,
+ * dgamma, dbeta as in the forward pass.  N <= 16384, M <= 2^27.
+ */
+size_t ie_layer_norm_bwd_workspace(int64_t rows, int64_t cols);
+ie_status ie_layer_norm_bwd(const ie_mat *dY, const ie_mat *X, const ie_mat *gamma, ie_scalar eps, const ie_mat *dX,
+                            const ie_mat *dgamma, const ie_mat *dbeta, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Bias gradient of a linear layer, db = R(sum_rows dY), exact sums of dY
+ * re-expressed at the largest of its row exponents.  dY [M x N], TENSOR or
+ * ROW; db: N channels as [N x 1] (one exponent, or one per channel when ROW)
+ * or [1 x N].
+ */
+size_t ie_linear_bwd_db_workspace(int64_t M, int64_t N);
+ie_status ie_linear_bwd_db(const ie_mat *dY, const ie_mat *db, void *ws, size_t ws_bytes, void *stream);
+
 /* Wait for `stream`, then copy the workspace's sticky flags to *flags and,
  * if clear != 0, zero them. */
 ie_status ie_device_status(void *ws, void *stream, uint32_t *flags, int clear);
@@ -337,7 +382,8 @@ ie_status ie_device_status(void *ws, void *stream, uint32_t *flags, int clear);
  * alignment copies, 3210 the per-slice alignment copies of batched products,
  * 3300 split rounding by rows, 3400 the paired finalize of
  * a convolution's backward pass, 3500 / 3510 ReLU forward / backward, 3520 /
- * 3521 / 3530 the Sum's maximum, rounding and row-grouped passes) and returns how
+ * 3521 / 3530 the Sum's maximum, rounding and row-grouped passes, 3600 / 3610
+ * layer norm forward / backward, 3620 / 3630 column sums and their finish) and returns how
  * many were recorded since the last read; the records are then cleared.
  * The timing records (and their events) are the library's only process-wide
  * state; they are not thread-safe.

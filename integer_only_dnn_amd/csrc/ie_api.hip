@@ -875,6 +875,191 @@ ie_status ie_add(const ie_mat *A, const ie_mat *B, const ie_mat *Z, void *ws, si
                                  A->cols, bmax, (uint32_t *)ws, mat_q(Z), (hipStream_t)stream));
 }
 
+// ---------------------------------------------------------------------------
+// Layer norm and the bias gradient
+// ---------------------------------------------------------------------------
+
+static NormVec norm_vec(const ie_mat *v) {
+    if (!v) return NormVec{nullptr, nullptr, 0};
+    return NormVec{v->mant, v->exp, v->group == IE_GROUP_ROW && v->rows > 1};
+}
+
+static ie_status check_vector(const ie_mat *v, long long n) {
+    IE_CHECK(check_mat(v));
+    return is_vector(v, n) ? IE_OK : IE_ERR_SHAPE;
+}
+
+// Whether two matrices share their mantissas or their exponents.
+static bool share(const ie_mat *a, const ie_mat *b) {
+    return a && b && ((a->mant && a->mant == b->mant) || (a->exp && a->exp == b->exp));
+}
+
+size_t ie_layer_norm_fwd_workspace(int64_t rows, int64_t cols) {
+    if (rows < 0 || cols < 0) return 0;
+    return norm_fwd_ws(rows, cols);
+}
+
+size_t ie_layer_norm_bwd_workspace(int64_t rows, int64_t cols) {
+    if (rows < 0 || cols < 0) return 0;
+    return norm_bwd_ws(rows, cols);
+}
+
+size_t ie_linear_bwd_db_workspace(int64_t M, int64_t N) {
+    if (M < 0 || N < 0) return 0;
+    return linear_db_ws(M, N);
+}
+
+ie_status ie_layer_norm_fwd(const ie_mat *X, const ie_mat *gamma, const ie_mat *beta, ie_scalar eps, const ie_mat *Y,
+                            void *ws, size_t ws_bytes, void *stream) {
+    IE_CHECK(check_mat(X));
+    IE_CHECK(check_mat(Y));
+    if (!same_shape(X, Y)) return IE_ERR_SHAPE;
+    if (gamma) IE_CHECK(check_vector(gamma, X->cols));
+    if (beta) IE_CHECK(check_vector(beta, X->cols));
+    if (eps.mant < 0 || X->cols > NORM_COLS_MAX) return IE_ERR_UNSUPPORTED;
+    if (share(Y, X) || share(Y, gamma) || share(Y, beta)) return IE_ERR_UNSUPPORTED;
+    if (!ws) return IE_ERR_WORKSPACE;
+    if (ws_bytes < norm_fwd_ws(X->rows, X->cols)) return IE_ERR_WORKSPACE;
+    hipStream_t st = (hipStream_t)stream;
+    const int y_row = Y->group == IE_GROUP_ROW;
+    if (X->rows == 0 || X->cols == 0) return hip_status(launch_fill_i8(Y->exp, n_exps(Y), E_MIN, st));
+    Carve c{(char *)ws, HEADER};
+    const NormWs w = carve_norm_fwd(c, X->rows, X->cols);
+    const NormPlan pl = norm_plan(X->rows, X->cols, NORM_FWD_BLOCKS);
+    NormFwd a;
+    memset(&a, 0, sizeof a);
+    a.x = X->mant;
+    a.xe = X->exp;
+    a.x_row = X->group == IE_GROUP_ROW;
+    a.gamma = norm_vec(gamma);
+    a.beta = norm_vec(beta);
+    a.rows = X->rows;
+    a.cols = (int)X->cols;
+    a.n2eps = (double)X->cols * (double)X->cols * eps.mant;
+    a.eps_e = eps.exp;
+    a.out = Y->mant;
+    a.oe = Y->exp;
+    a.q = mat_q(Y);
+    a.bmax = w.bmax;
+    a.n_bmax = pl.grid;
+    a.flags = (uint32_t *)ws;
+    a.mode = y_row ? NORM_ROWS : NORM_NEED;
+    IE_TRY(launch_norm_fwd(a, pl, st));
+    if (y_row) return IE_OK;
+    a.mode = NORM_ROUND;
+    return hip_status(launch_norm_fwd(a, pl, st));
+}
+
+// A vector of column sums as an output (nullptr: not wanted).
+static ColOut col_out(const ie_mat *v, const long long *p64, const int *p32, int base, long long *sums, int *need) {
+    ColOut o;
+    memset(&o, 0, sizeof o);
+    if (!v) return o;
+    o.p64 = p64;
+    o.p32 = p32;
+    o.base = base;
+    o.m = v->mant;
+    o.e = v->exp;
+    o.per = v->group == IE_GROUP_ROW && v->rows > 1;
+    o.q = mat_q(v);
+    o.sums = sums;
+    o.need = need;
+    return o;
+}
+
+ie_status ie_layer_norm_bwd(const ie_mat *dY, const ie_mat *X, const ie_mat *gamma, ie_scalar eps, const ie_mat *dX,
+                            const ie_mat *dgamma, const ie_mat *dbeta, void *ws, size_t ws_bytes, void *stream) {
+    IE_CHECK(check_mat(dY));
+    IE_CHECK(check_mat(X));
+    if (!same_shape(dY, X)) return IE_ERR_SHAPE;
+    const long long M = X->rows, N = X->cols;
+    if (dX) {
+        IE_CHECK(check_mat(dX));
+        if (!same_shape(dX, X)) return IE_ERR_SHAPE;
+    }
+    if (gamma) IE_CHECK(check_vector(gamma, N));
+    if (dgamma) IE_CHECK(check_vector(dgamma, N));
+    if (dbeta) IE_CHECK(check_vector(dbeta, N));
+    if (eps.mant < 0 || N > NORM_COLS_MAX || M > NORM_ROWS_MAX) return IE_ERR_UNSUPPORTED;
+    for (const ie_mat *o : {dX, dgamma, dbeta})
+        if (share(o, dY) || share(o, X) || share(o, gamma)) return IE_ERR_UNSUPPORTED;
+    if (share(dX, dgamma) || share(dX, dbeta) || share(dgamma, dbeta)) return IE_ERR_UNSUPPORTED;
+    if (!ws) return IE_ERR_WORKSPACE;
+    if (ws_bytes < norm_bwd_ws(M, N)) return IE_ERR_WORKSPACE;
+    hipStream_t st = (hipStream_t)stream;
+    uint32_t *flags = (uint32_t *)ws;
+    if (N == 0 || (M == 0 && !dgamma && !dbeta)) {
+        for (const ie_mat *o : {dX, dgamma, dbeta})
+            if (o) IE_TRY(launch_fill_i8(o->exp, n_exps(o), E_MIN, st));
+        return IE_OK;
+    }
+    if (!dX && !dgamma && !dbeta) return IE_OK;
+    Carve c{(char *)ws, HEADER};
+    const NormWs w = carve_norm_bwd(c, M, N);
+    const NormPlan pl = norm_plan(M, N, NORM_BWD_BLOCKS);
+    const bool cols = dgamma || dbeta;
+    const bool dx_row = dX && dX->group == IE_GROUP_ROW;
+    IE_TRY(launch_exp_max2(dY->exp, n_exps(dY), w.c.top, gamma ? gamma->exp : nullptr, gamma ? n_exps(gamma) : 0,
+                           w.c.top + 1, st));
+    NormBwd a;
+    memset(&a, 0, sizeof a);
+    a.dy = dY->mant;
+    a.dye = dY->exp;
+    a.dy_row = dY->group == IE_GROUP_ROW;
+    a.x = X->mant;
+    a.xe = X->exp;
+    a.x_row = X->group == IE_GROUP_ROW;
+    a.gamma = norm_vec(gamma);
+    a.rows = M;
+    a.cols = (int)N;
+    a.n2eps = (double)N * (double)N * eps.mant;
+    a.eps_e = eps.exp;
+    a.out = dX ? dX->mant : nullptr;
+    a.oe = dX ? dX->exp : nullptr;
+    a.q = dX ? mat_q(dX) : 7;
+    a.bmax = w.bmax;
+    a.n_bmax = pl.grid;
+    a.top = w.c.top;
+    a.pf = cols ? w.c.p64 : nullptr;
+    a.pb = w.c.p32;
+    a.flags = flags;
+    if (M > 0) {
+        a.mode = dx_row ? NORM_ROWS : NORM_NEED;
+        IE_TRY(launch_norm_bwd(a, pl, st));
+        if (dX && !dx_row) {
+            a.mode = NORM_ROUND;
+            IE_TRY(launch_norm_bwd(a, pl, st));
+        }
+    } else if (dX) {
+        IE_TRY(launch_fill_i8(dX->exp, n_exps(dX), E_MIN, st));
+    }
+    if (!cols) return IE_OK;
+    const ColOut f = col_out(dgamma, w.c.p64, nullptr, -20, w.c.sums, w.c.need);
+    const ColOut b = col_out(dbeta, nullptr, w.c.p32, 0, w.c.sums + N, w.c.need + cdiv(N, 64));
+    return hip_status(launch_col_finish(f, b, M > 0 ? pl.grid : 0, (int)N, w.c.top, flags, st));
+}
+
+ie_status ie_linear_bwd_db(const ie_mat *dY, const ie_mat *db, void *ws, size_t ws_bytes, void *stream) {
+    IE_CHECK(check_mat(dY));
+    IE_CHECK(check_vector(db, dY->cols));
+    if (share(db, dY)) return IE_ERR_UNSUPPORTED;
+    if (!ws) return IE_ERR_WORKSPACE;
+    const long long M = dY->rows, N = dY->cols;
+    if (ws_bytes < linear_db_ws(M, N)) return IE_ERR_WORKSPACE;
+    hipStream_t st = (hipStream_t)stream;
+    uint32_t *flags = (uint32_t *)ws;
+    if (N == 0) return hip_status(launch_fill_i8(db->exp, n_exps(db), E_MIN, st));
+    Carve c{(char *)ws, HEADER};
+    const ColWs w = carve_linear_db(c, M, N);
+    const ColPlan pl = col_plan(M, N);
+    const bool row = dY->group == IE_GROUP_ROW;
+    IE_TRY(launch_exp_max2(dY->exp, n_exps(dY), w.top, nullptr, 0, nullptr, st));
+    if (M > 0) IE_TRY(launch_col_sum(dY->mant, dY->exp, row, w.top, M, (int)N, pl.chunk, pl.parts, w.p32, st));
+    return hip_status(launch_col_finish(col_out(nullptr, nullptr, nullptr, 0, nullptr, nullptr),
+                                        col_out(db, nullptr, w.p32, 0, w.sums, w.need), M > 0 ? pl.parts : 0, (int)N,
+                                        w.top, flags, st));
+}
+
 size_t ie_bmm_workspace(int32_t batch, int64_t M, int64_t N, int64_t K) {
     if (batch < 0 || M < 0 || N < 0 || K < 0) return 0;
     return bmm_ws(batch, M, N, K);

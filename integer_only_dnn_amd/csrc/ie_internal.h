@@ -137,6 +137,10 @@ constexpr int PROF_RELU_BWD = 3510;
 constexpr int PROF_ADD_NEED = 3520;
 constexpr int PROF_ADD_ROUND = 3521;
 constexpr int PROF_ADD_ROWS = 3530;
+constexpr int PROF_NORM_FWD = 3600;
+constexpr int PROF_NORM_BWD = 3610;
+constexpr int PROF_COL_SUM = 3620;
+constexpr int PROF_COL_FINISH = 3630;
 
 // Auxiliary kernels (ie_aux.hip).
 hipError_t launch_fill_i32(int *p, long long n, int v, hipStream_t st);
@@ -226,5 +230,69 @@ hipError_t launch_relu_bwd(const int8_t *dy, const int8_t *dye, int dy_row, cons
 hipError_t launch_add(const int8_t *a, const int8_t *ae, int a_row, const int8_t *b, const int8_t *be, int b_row,
                       int8_t *z, int8_t *ze, int z_row, long long rows, long long cols, int *bmax, uint32_t *flags,
                       int q, hipStream_t st);
+
+// Layer norm and column sums (ie_norm.hip).
+// A parameter vector: mantissas, and one exponent or one per channel (per);
+// m == nullptr: absent.
+struct NormVec {
+    const int8_t *m, *e;
+    int per;
+};
+// ROWS: one exponent per result row, in one pass.  NEED / ROUND: one for the
+// whole result; NEED leaves the blocks' needs in bmax, ROUND (the rows again)
+// rounds to the largest of them.
+enum NormMode { NORM_ROWS = 0, NORM_NEED = 1, NORM_ROUND = 2 };
+struct NormFwd {
+    const int8_t *x, *xe;
+    int x_row;
+    NormVec gamma, beta;
+    long long rows;
+    int cols;
+    double n2eps;  // N^2 times eps's mantissa
+    int eps_e;
+    int8_t *out, *oe;
+    int q, mode;
+    int *bmax;
+    int n_bmax;
+    uint32_t *flags;
+};
+struct NormBwd {
+    const int8_t *dy, *dye;
+    int dy_row;
+    const int8_t *x, *xe;
+    int x_row;
+    NormVec gamma;
+    long long rows;
+    int cols;
+    double n2eps;
+    int eps_e;
+    int8_t *out, *oe;  // dX, or nullptr
+    int q, mode;
+    int *bmax;
+    int n_bmax;
+    const int *top;  // largest exponents of dY and gamma
+    long long *pf;   // [grid][cols] partial sums of dgamma and dbeta, or nullptr
+    int *pb;
+    uint32_t *flags;
+};
+hipError_t launch_norm_fwd(const NormFwd &a, const NormPlan &pl, hipStream_t st);
+hipError_t launch_norm_bwd(const NormBwd &a, const NormPlan &pl, hipStream_t st);
+// pb[part][col] = sum of the part's rows of dY, re-expressed at *top.
+hipError_t launch_col_sum(const int8_t *dy, const int8_t *e, int e_row, const int *top, long long rows, int cols,
+                          int chunk, int parts, int *pb, hipStream_t st);
+// A vector of column sums: its partial sums (64 or 32 bits) at exponent
+// base + *top, rounded into m / e (per: one exponent per channel) at width
+// q + 1.  m == nullptr: not wanted.
+struct ColOut {
+    const long long *p64;
+    const int *p32;
+    int base;
+    int8_t *m, *e;
+    int per, q;
+    long long *sums;
+    int *need;
+};
+hipError_t launch_col_finish(const ColOut &f, const ColOut &b, int parts, int cols, const int *top, uint32_t *flags,
+                             hipStream_t st);
 
 }  // namespace ie

@@ -623,6 +623,87 @@ BmmWs carve_bmm(Carve &c, int form, long long Z, long long M, long long N, long 
     return w;
 }
 
+bool is_vector(const ie_mat *t, long long n) {
+    return (t->rows == n && t->cols == 1) || (t->rows == 1 && t->cols == n);
+}
+
+// The fewest threads per row that hold it in at most 16 elements each, and
+// the fewest elements (a multiple of 4) that those threads need.
+NormPlan norm_plan(long long rows, long long cols, int max_blocks) {
+    NormPlan p{16, 4, 1};
+    const int ts[] = {16, 32, 64, 256, 1024};
+    for (int t : ts) {
+        p.t = t;
+        if (cols <= 16ll * t) break;
+    }
+    p.e = 4 * cdiv(cols > 0 ? cols : 1, 4ll * p.t);
+    if (p.e < 8 && p.t > 16) p.e = 8;
+    if (p.e < 12 && (p.t == 32 || p.t == 64)) p.e = 12;
+    const long long rpb = p.t > 256 ? 1 : 256 / p.t;
+    const long long want = (rows + rpb - 1) / rpb;
+    const int cap = p.t > 256 ? max_blocks / 2 : max_blocks;
+    p.grid = (int)(want < 1 ? 1 : want > cap ? cap : want);
+    return p;
+}
+
+ColPlan col_plan(long long rows, long long cols) {
+    const long long gx = (cols + 255) / 256;
+    long long parts = 2048 / (gx > 0 ? gx : 1);
+    if (parts > (rows + 31) / 32) parts = (rows + 31) / 32;
+    const long long least = (rows + (1ll << 23) - 1) >> 23;  // 32-bit sums
+    if (parts < least) parts = least;
+    if (parts < 1) parts = 1;
+    const long long chunk = (rows + parts - 1) / parts;
+    return ColPlan{(int)(chunk > 0 ? (rows + chunk - 1) / chunk : 1), (int)(chunk > 0 ? chunk : 1)};
+}
+
+static ColWs carve_cols(Carve &c, long long parts, long long cols, bool wide) {
+    ColWs w{};
+    const size_t n = (size_t)(cols > 0 ? cols : 1);
+    w.top = c.take<int>(2);
+    if (wide) w.p64 = c.take<long long>((size_t)parts * n);
+    w.p32 = c.take<int>((size_t)parts * n);
+    w.sums = c.take<long long>(2 * n);
+    w.need = c.take<int>(2 * ((n + 63) / 64));
+    return w;
+}
+
+NormWs carve_norm_fwd(Carve &c, long long rows, long long cols) {
+    NormWs w{};
+    w.bmax = c.take<int>((size_t)norm_plan(rows, cols, NORM_FWD_BLOCKS).grid);
+    return w;
+}
+
+NormWs carve_norm_bwd(Carve &c, long long rows, long long cols) {
+    NormWs w{};
+    const NormPlan p = norm_plan(rows, cols, NORM_BWD_BLOCKS);
+    w.bmax = c.take<int>((size_t)p.grid);
+    w.c = carve_cols(c, p.grid, cols, true);
+    return w;
+}
+
+ColWs carve_linear_db(Carve &c, long long rows, long long cols) {
+    return carve_cols(c, col_plan(rows, cols).parts, cols, false);
+}
+
+size_t norm_fwd_ws(long long rows, long long cols) {
+    Carve c{nullptr, HEADER};
+    carve_norm_fwd(c, rows, cols);
+    return align256(c.off);
+}
+
+size_t norm_bwd_ws(long long rows, long long cols) {
+    Carve c{nullptr, HEADER};
+    carve_norm_bwd(c, rows, cols);
+    return align256(c.off);
+}
+
+size_t linear_db_ws(long long rows, long long cols) {
+    Carve c{nullptr, HEADER};
+    carve_linear_db(c, rows, cols);
+    return align256(c.off);
+}
+
 size_t linear_fwd_ws(long long M, long long N, long long K, const Force &f) {
     Carve c{nullptr, HEADER};
     carve_linear_fwd(c, M, N, K, f);

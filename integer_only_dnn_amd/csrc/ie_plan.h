@@ -328,6 +328,46 @@ struct BmmWs {
 };
 BmmWs carve_bmm(Carve &c, int form, long long Z, long long M, long long N, long long K);
 
+// Layer norm: t threads per row with e elements each (t * e >= cols), on a
+// persistent grid of `grid` blocks of max(t, 256) threads.
+constexpr long long NORM_COLS_MAX = 16384;
+constexpr long long NORM_ROWS_MAX = 1ll << 27;  // dgamma sums stay below 2^62
+constexpr int NORM_FWD_BLOCKS = 2048;
+constexpr int NORM_BWD_BLOCKS = 512;  // each leaves one row of partial column sums
+struct NormPlan {
+    int t, e, grid;
+};
+NormPlan norm_plan(long long rows, long long cols, int max_blocks);
+
+// Column sums of a [rows x cols] gradient: `parts` chunks of `chunk` rows.
+struct ColPlan {
+    int parts, chunk;
+};
+ColPlan col_plan(long long rows, long long cols);
+
+// 64-column blocks of the column sums' finish, each with its need when the
+// vector has one exponent.
+struct ColWs {
+    int *top;         // [2]: largest exponents of dY and gamma
+    long long *p64;   // partial sums of dgamma [parts][cols]
+    int *p32;         // partial sums of dbeta / db
+    long long *sums;  // [2][cols]
+    int *need;        // [2][ceil(cols / 64)]
+};
+struct NormWs {
+    int *bmax;  // block maxima of a whole-tensor result
+    ColWs c;
+};
+NormWs carve_norm_fwd(Carve &c, long long rows, long long cols);
+NormWs carve_norm_bwd(Carve &c, long long rows, long long cols);
+ColWs carve_linear_db(Carve &c, long long rows, long long cols);
+
+// Whether a parameter vector of n channels is [n x 1] or [1 x n].
+bool is_vector(const ie_mat *t, long long n);
+
+size_t norm_fwd_ws(long long rows, long long cols);
+size_t norm_bwd_ws(long long rows, long long cols);
+size_t linear_db_ws(long long rows, long long cols);
 size_t linear_fwd_ws(long long M, long long N, long long K, const Force &f);
 size_t linear_dx_ws(long long M, long long N, long long K, const Force &f);
 size_t linear_dw_ws(long long M, long long N, long long K, const Force &fw);

@@ -74,6 +74,13 @@ EXPORTS = [
     ("ie_relu_bwd", c_int, [POINTER(ie_mat)] * 3 + [c_int, c_void_p]),
     ("ie_add_workspace", c_size_t, [c_int64, c_int64]),
     ("ie_add", c_int, [POINTER(ie_mat)] * 3 + [c_void_p, c_size_t, c_void_p]),
+    ("ie_layer_norm_fwd_workspace", c_size_t, [c_int64, c_int64]),
+    ("ie_layer_norm_fwd", c_int, [POINTER(ie_mat)] * 3 + [ie_scalar, POINTER(ie_mat), c_void_p, c_size_t, c_void_p]),
+    ("ie_layer_norm_bwd_workspace", c_size_t, [c_int64, c_int64]),
+    ("ie_layer_norm_bwd", c_int,
+     [POINTER(ie_mat)] * 3 + [ie_scalar] + [POINTER(ie_mat)] * 3 + [c_void_p, c_size_t, c_void_p]),
+    ("ie_linear_bwd_db_workspace", c_size_t, [c_int64, c_int64]),
+    ("ie_linear_bwd_db", c_int, [POINTER(ie_mat)] * 2 + [c_void_p, c_size_t, c_void_p]),
     ("ie_device_status", c_int, [c_void_p, c_void_p, POINTER(c_uint32), c_int]),
     ("ie_profile_enable", c_int, [c_int]),
     ("ie_profile_select", c_int, [c_int]),
@@ -358,6 +365,35 @@ def ie_add(A: Mat, B: Mat, Z: Mat, ws: Workspace) -> None:
     a, b, z = A.c(), B.c(), Z.c()
     p, nb = ws.get(_ws_size("ie_add_workspace", a.rows, a.cols))
     _check(lib().ie_add(byref(a), byref(b), byref(z), p, nb, _stream(ws.device)), "ie_add")
+
+
+def _opt(m: Mat | None):
+    """The C descriptor of an optional matrix, by reference (None: NULL)."""
+    return byref(m.c()) if m is not None else None
+
+
+def ie_layer_norm_fwd(X: Mat, gamma: Mat | None, beta: Mat | None, eps, Y: Mat, ws: Workspace) -> None:
+    """Y = layer norm of X's rows, times gamma plus beta; eps is a (C, e) scalar."""
+    x, y = X.c(), Y.c()
+    p, b = ws.get(_ws_size("ie_layer_norm_fwd_workspace", x.rows, x.cols))
+    _check(lib().ie_layer_norm_fwd(byref(x), _opt(gamma), _opt(beta), ie_scalar(*eps), byref(y), p, b,
+                                   _stream(ws.device)), "ie_layer_norm_fwd")
+
+
+def ie_layer_norm_bwd(dY: Mat, X: Mat, gamma: Mat | None, eps, dX: Mat | None, dgamma: Mat | None,
+                      dbeta: Mat | None, ws: Workspace) -> None:
+    """The gradients of ie_layer_norm_fwd's input, gamma and beta (any of them None to skip it)."""
+    dy, x = dY.c(), X.c()
+    p, b = ws.get(_ws_size("ie_layer_norm_bwd_workspace", x.rows, x.cols))
+    _check(lib().ie_layer_norm_bwd(byref(dy), byref(x), _opt(gamma), ie_scalar(*eps), _opt(dX), _opt(dgamma),
+                                   _opt(dbeta), p, b, _stream(ws.device)), "ie_layer_norm_bwd")
+
+
+def ie_linear_bwd_db(dY: Mat, db: Mat, ws: Workspace) -> None:
+    """db = the sum of dY's rows (a linear layer's bias gradient)."""
+    dy, d = dY.c(), db.c()
+    p, b = ws.get(_ws_size("ie_linear_bwd_db_workspace", dy.rows, dy.cols))
+    _check(lib().ie_linear_bwd_db(byref(dy), byref(d), p, b, _stream(ws.device)), "ie_linear_bwd_db")
 
 
 def ie_profile_enable(on: bool = True) -> None:

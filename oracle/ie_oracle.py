@@ -35,6 +35,12 @@ R8  mantissa width B (Table 4, B in 8..4): a B-bit result has
     the velocity stays INT8 whatever B the weights use.  Every requantising
     function takes ``bits`` (default 8).
 
+R9  layer norm, the product with bias and residual, and dropout hold what is
+    not an integer (a row's 1 / sigma, sums of terms whose exponents lie far
+    apart) to 53 bits, every operation rounded half to even once, in the
+    order their functions give; the results are rounded into groups from
+    there (R2, R3).
+
 Integer contractions use float64 matrix products: every partial sum is an
 integer of magnitude < 2**53 (asserted), where float64 addition is exact in
 any order, so the float64 result is the exact integer sum.
@@ -667,6 +673,142 @@ def sgd_update(W: QT, V: QT, G: QT, lr: Scalar, beta: Scalar,
     cw, e_w = requant_exact(num_w, base_w, gw, ngw, w_bits)
     W_new = QT(cw.reshape(W.mant.shape), e_w, W.group)
     return W_new, V_new
+
+
+# ---------------------------------------------------------------------------
+# Layer norm, the product with bias and residual, dropout (reading R9).
+# numpy's float64 operations are the 53-bit ones: each rounds half to even.
+# ---------------------------------------------------------------------------
+
+def requant_f64(y: np.ndarray, group: int, bits: int = Q_BITS) -> QT:
+    """Finite float64 values rounded into groups (readings R2, R3)."""
+    y = np.asarray(y, dtype=np.float64)
+    rows = y.shape[0]
+    flat = np.abs(y.reshape(rows, int(np.prod(y.shape[1:], dtype=np.int64))))
+    if group == ROW:
+        mx = flat.max(axis=1) if flat.shape[1] else np.zeros(rows)
+    else:
+        mx = np.array([flat.max() if flat.size else 0.0])
+    q = q_max(bits)
+    e = np.frexp(mx)[1].astype(np.int64) - (bits - 1)
+    e += np.rint(np.ldexp(mx, -e)) > q
+    e = np.maximum(np.where(mx == 0, E_MIN, e), E_MIN)
+    if np.any(e > E_MAX):
+        raise ExpRangeError(f"group exponent {int(e.max())} > {E_MAX}")
+    sh = (e if group == ROW else np.broadcast_to(e, rows)).reshape((rows,) + (1,) * (y.ndim - 1))
+    c = np.rint(np.ldexp(y, -sh))
+    assert np.all(np.abs(c) <= q)
+    return QT(c.astype(np.int8), e.astype(np.int8), group)
+
+
+def channel_values(v: QT) -> np.ndarray:
+    """A parameter vector, [n x 1] or [1 x n], as n float64 values (exact)."""
+    return np.ldexp(v.mant.astype(np.float64), v.row_exp()[:, None]).reshape(-1)
+
+
+def _channel_align(v: QT) -> tuple:
+    """A parameter vector at its largest exponent (R5): n integers, exponent."""
+    top = int(v.row_exp().max())
+    return rne_np(v.mant.astype(np.int64), np.minimum(top - v.row_exp(), 60)[:, None]).reshape(-1), top
+
+
+def layer_norm_rows(X: QT, eps: Scalar) -> tuple:
+    """Each row's exact deviations N C - sum C, and r = 1 / sqrt(N^2 (var +
+    eps)) in units of the row's mantissas (0 where that is 0)."""
+    c = X.mant.astype(np.int64)
+    n = c.shape[1]
+    s = c.sum(axis=1, keepdims=True)
+    v = n * (c * c).sum(axis=1, keepdims=True) - s * s
+    t = v.astype(np.float64) + np.ldexp(np.float64(n * n * eps.mant), eps.exp - 2 * X.row_exp()[:, None])
+    with np.errstate(divide="ignore"):
+        r = np.where(t > 0, np.float64(1.0) / np.sqrt(t), 0.0)
+    return n * c - s, r
+
+
+def layer_norm_fwd(X: QT, gamma, beta, eps: Scalar, y_group: int, bits: int = Q_BITS) -> QT:
+    """gamma (x - mean) / sqrt(var + eps) + beta, row by row."""
+    d, r = layer_norm_rows(X, eps)
+    y = d.astype(np.float64) * r
+    if gamma is not None:
+        y = y * channel_values(gamma)[None, :]
+    if beta is not None:
+        y = y + channel_values(beta)[None, :]
+    return requant_f64(y, y_group, bits)
+
+
+def layer_norm_bwd(dY: QT, X: QT, gamma, eps: Scalar, dx_group: int, v_group: int, bits: int = Q_BITS) -> tuple:
+    """(dX, dgamma, dbeta), the vectors as [n x 1] in v_group."""
+    d, r = layer_norm_rows(X, eps)
+    n = X.mant.shape[1]
+    f = np.rint(np.ldexp(d.astype(np.float64) * r, 20)).astype(np.int64)
+    dy = dY.mant.astype(np.int64)
+    gm, top = _channel_align(gamma) if gamma is not None else (np.ones(n, dtype=np.int64), 0)
+    g = dy * gm[None, :]
+    g1, g2 = g.sum(axis=1, keepdims=True), (g * f).sum(axis=1, keepdims=True)
+    assert np.all(np.abs(g2) < _F64_EXACT)
+    z = (n * g - g1).astype(np.float64) - f.astype(np.float64) * np.ldexp(g2.astype(np.float64), -40)
+    dX = requant_f64(np.ldexp(z * r, dY.row_exp()[:, None] + top - X.row_exp()[:, None]), dx_group, bits)
+    a, e = align_rows(dY)
+    sf, sb = (a * f).sum(axis=0).reshape(-1, 1), a.sum(axis=0).reshape(-1, 1)
+    dgamma = requant_np(sf, np.full(sf.shape, int(e) - 20), v_group, bits)
+    dbeta = requant_np(sb, np.full(sb.shape, int(e)), v_group, bits)
+    return dX, dgamma, dbeta
+
+
+def linear_bwd_db(dY: QT, v_group: int, bits: int = Q_BITS) -> QT:
+    """The sum of dY's rows, aligned first (R5), as [n x 1]."""
+    a, e = align_rows(dY)
+    s = a.sum(axis=0).reshape(-1, 1)
+    return requant_np(s, np.full(s.shape, int(e)), v_group, bits)
+
+
+def linear_fwd_fused(X: QT, W: QT, bias, R, y_group: int, relu: bool = False, bits: int = Q_BITS) -> QT:
+    """X . W^T + bias + R, in this order, then the clip on the mantissas."""
+    acc, eps = linear_fwd_acc(X, W)
+    y = np.ldexp(acc.astype(np.float64), eps)
+    if bias is not None:
+        y = y + channel_values(bias)[None, :]
+    if R is not None:
+        y = y + np.ldexp(R.mant.astype(np.float64), R.row_exp()[:, None])
+    out = requant_f64(y, y_group, bits)
+    return QT(np.maximum(out.mant, 0), out.exp, out.group) if relu else out
+
+
+def philox4x32(counter, key, rounds: int = 10) -> list:
+    """Philox4x32 of Salmon, Moraes, Dror and Shaw ("Parallel random numbers:
+    as easy as 1, 2, 3", 2011): 4 words of 32 bits from a counter of 4 and a
+    key of 2."""
+    m = (1 << 32) - 1
+    c, (k0, k1) = list(counter), key
+    for _ in range(rounds):
+        p0, p1 = 0xD2511F53 * c[0], 0xCD9E8D57 * c[2]
+        c = [(p1 >> 32) ^ c[1] ^ k0, p1 & m, (p0 >> 32) ^ c[3] ^ k1, p0 & m]
+        k0, k1 = (k0 + 0x9E3779B9) & m, (k1 + 0xBB67AE85) & m
+    return c
+
+
+def dropout_draws(rows: int, cols: int, seed: int, step: int) -> np.ndarray:
+    """Sixteen random bits per element: one Philox block for eight neighbours
+    of a row (counter: column / 8, row, step; key: seed), low halves first."""
+    u = np.zeros((rows, (cols + 7) // 8 * 8), dtype=np.int64)
+    for i in range(rows):
+        for b in range((cols + 7) // 8):
+            w = philox4x32((b, i, step & 0xFFFFFFFF, step >> 32), (seed & 0xFFFFFFFF, seed >> 32))
+            for k in range(8):
+                u[i, 8 * b + k] = (w[k // 2] >> (16 * (k % 2))) & 0xFFFF
+    return u[:, :cols]
+
+
+def dropout(X: QT, R, drop: int, seed: int, step: int, y_group: int, bits: int = Q_BITS) -> QT:
+    """X where its draw is at least `drop` (of 65536), scaled by 65536 /
+    (65536 - drop) held to 24 bits, else 0; plus R."""
+    rows, cols = X.mant.shape
+    scale = np.float64(np.float32(65536.0 / (65536 - drop)))
+    y = np.ldexp(X.mant.astype(np.float64) * scale, X.row_exp()[:, None])
+    y = np.where(dropout_draws(rows, cols, seed, step) >= drop, y, 0.0)
+    if R is not None:
+        y = y + np.ldexp(R.mant.astype(np.float64), R.row_exp()[:, None])
+    return requant_f64(y, y_group, bits)
 
 
 # ---------------------------------------------------------------------------

@@ -174,3 +174,45 @@ def test_forced_plans_without_kernel_are_refused(force, monkeypatch):
     for group in (0, 1):
         st = L.ie_linear_fwd(by(X), by(W), by(_mat(M, N, group)), 256, ws_bytes, None)
         assert st == 6, (force, group, st)
+
+
+def test_layer_norm_and_bias_gradient_argument_errors():
+    """Shapes, parameter vectors, eps, shared buffers, sizes and workspaces
+    are refused before anything is enqueued."""
+    L = ie.lib()
+    by, S, big = ctypes.byref, ie.ie_scalar, 1 << 30
+    X, Y = _mat(4, 8), _mat(4, 8, mant=512, exp=512)
+    g, eps = _mat(8, 1, group=1, mant=1024, exp=1024), S(85, -23)
+    fwd, bwd, db = L.ie_layer_norm_fwd, L.ie_layer_norm_bwd, L.ie_linear_bwd_db
+    assert fwd(None, by(g), None, eps, by(Y), 1, big, None) == 1
+    assert fwd(by(X), by(g), None, eps, by(_mat(4, 9, mant=512, exp=512)), 1, big, None) == 2
+    for bad in (_mat(7, 1), _mat(2, 4), _mat(1, 9)):
+        assert fwd(by(X), by(bad), None, eps, by(Y), 1, big, None) == 2
+        assert fwd(by(X), None, by(bad), eps, by(Y), 1, big, None) == 2
+    assert fwd(by(X), by(g), None, S(-1, 0), by(Y), 1, big, None) == 6
+    assert fwd(by(X), by(g), None, eps, by(_mat(4, 8, mant=256, exp=512)), 1, big, None) == 6   # Y is X
+    assert fwd(by(X), by(g), None, eps, by(_mat(4, 8, mant=512, exp=1024)), 1, big, None) == 6  # gamma's exponents
+    assert fwd(by(_mat(2, 16385)), None, None, eps, by(_mat(2, 16385, mant=512, exp=512)), 1, big, None) == 6
+    assert fwd(by(X), by(g), None, eps, by(Y), None, big, None) == 4
+    assert fwd(by(X), by(g), None, eps, by(Y), 1, 256, None) == 4
+    assert fwd(by(X), by(g), None, eps, by(_mat(4, 8, mant=512, exp=512, bits=1)), 1, big, None) == 8
+    dX, dg = _mat(4, 8, mant=2048, exp=2048), _mat(8, 1, mant=4096, exp=4096)
+    args = lambda **k: [k.get("dY", by(Y)), by(X), by(g), k.get("eps", eps), k.get("dX", by(dX)),  # noqa: E731
+                        k.get("dg", by(dg)), k.get("db"), k.get("ws", 1), k.get("n", big), None]
+    assert bwd(*args(dY=by(_mat(5, 8)))) == 2
+    assert bwd(*args(dX=by(_mat(4, 7, mant=2048, exp=2048)))) == 2
+    assert bwd(*args(dg=by(_mat(9, 1)))) == 2
+    assert bwd(*args(db=by(_mat(2, 4)))) == 2
+    assert bwd(*args(eps=S(-3, 0))) == 6
+    assert bwd(*args(dX=by(X))) == 6
+    assert bwd(*args(dg=by(dg), db=by(dg))) == 6
+    assert bwd(*args(ws=None)) == 4 and bwd(*args(n=300)) == 4
+    tall = (1 << 27) + 1
+    assert bwd(by(_mat(tall, 1)), by(_mat(tall, 1)), None, eps, None, by(_mat(1, 1, mant=9, exp=9)), None, 1, 1 << 40,
+               None) == 6
+    assert db(by(X), None, 1, big, None) == 1
+    assert db(by(X), by(_mat(7, 1, mant=9, exp=9)), 1, big, None) == 2
+    assert db(by(X), by(_mat(8, 1)), 1, big, None) == 6
+    assert db(by(X), by(g), None, big, None) == 4 and db(by(X), by(g), 1, 256, None) == 4
+    for size in (L.ie_layer_norm_fwd_workspace, L.ie_layer_norm_bwd_workspace, L.ie_linear_bwd_db_workspace):
+        assert size(-1, 4) == 0 and size(4, -1) == 0 and 256 < size(4, 8) <= size(4000, 800)
