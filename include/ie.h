@@ -357,10 +357,36 @@ ie_status ie_layer_norm_bwd(const ie_mat *dY, const ie_mat *X, const ie_mat *gam
  * Bias gradient of a linear layer, db = R(sum_rows dY), exact sums of dY
  * re-expressed at the largest of its row exponents.  dY [M x N], TENSOR or
  * ROW; db: N channels as [N x 1] (one exponent, or one per channel when ROW)
- * or [1 x N].
+ * or [1 x N].  N <= 2^30, else IE_ERR_UNSUPPORTED.
  */
 size_t ie_linear_bwd_db_workspace(int64_t M, int64_t N);
 ie_status ie_linear_bwd_db(const ie_mat *dY, const ie_mat *db, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Dropout, with an optional residual sum: Y = R_Y(X m s + R).  Element (i, j)
+ * is kept (m = 1) when its 16 random bits are at least `drop`, so it is
+ * dropped with probability drop / 65536, and s = 65536 / (65536 - drop), held
+ * to 24 bits.  The sum is held to 53 bits (exact while its terms span no
+ * more).  X, Y, R: [M x N], each TENSOR or ROW; R may be NULL.
+ * The bits come from Philox4x32-10 (Salmon, Moraes, Dror and Shaw, 2011) with
+ * key = seed and counter = (j / 8, i, step low word, step high word): word
+ * (j / 2) % 4, its low half for even j.  Nothing is stored: the gradient
+ * passes through the same call (dX from dY, no R) with the same seed, step
+ * and drop.  Every layer and training step takes a (seed, step) of its own.
+ * step_ptr: a device word added to `step` when the kernels run, so that a
+ * captured graph can draw anew on every replay; or NULL.
+ * drop <= 65535, N <= 2^30 and step_ptr 8-byte aligned, else
+ * IE_ERR_UNSUPPORTED.
+ */
+typedef struct {
+    uint64_t seed;
+    uint64_t step;
+    const uint64_t *step_ptr;
+    uint32_t drop;
+} ie_dropout_desc;
+size_t ie_dropout_workspace(int64_t rows, int64_t cols);
+ie_status ie_dropout(const ie_mat *X, const ie_mat *R, const ie_mat *Y, const ie_dropout_desc *d, void *ws,
+                     size_t ws_bytes, void *stream);
 
 /* Wait for `stream`, then copy the workspace's sticky flags to *flags and,
  * if clear != 0, zero them. */
@@ -383,7 +409,8 @@ ie_status ie_device_status(void *ws, void *stream, uint32_t *flags, int clear);
  * 3300 split rounding by rows, 3400 the paired finalize of
  * a convolution's backward pass, 3500 / 3510 ReLU forward / backward, 3520 /
  * 3521 / 3530 the Sum's maximum, rounding and row-grouped passes, 3600 / 3610
- * layer norm forward / backward, 3620 / 3630 column sums and their finish) and returns how
+ * layer norm forward / backward, 3620 / 3630 column sums and their finish,
+ * 3700 dropout) and returns how
  * many were recorded since the last read; the records are then cleared.
  * The timing records (and their events) are the library's only process-wide
  * state; they are not thread-safe.

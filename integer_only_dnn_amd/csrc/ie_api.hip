@@ -1042,7 +1042,7 @@ ie_status ie_layer_norm_bwd(const ie_mat *dY, const ie_mat *X, const ie_mat *gam
 ie_status ie_linear_bwd_db(const ie_mat *dY, const ie_mat *db, void *ws, size_t ws_bytes, void *stream) {
     IE_CHECK(check_mat(dY));
     IE_CHECK(check_vector(db, dY->cols));
-    if (share(db, dY)) return IE_ERR_UNSUPPORTED;
+    if (share(db, dY) || dY->cols > LONG_COLS_MAX) return IE_ERR_UNSUPPORTED;
     if (!ws) return IE_ERR_WORKSPACE;
     const long long M = dY->rows, N = dY->cols;
     if (ws_bytes < linear_db_ws(M, N)) return IE_ERR_WORKSPACE;
@@ -1058,6 +1058,64 @@ ie_status ie_linear_bwd_db(const ie_mat *dY, const ie_mat *db, void *ws, size_t 
     return hip_status(launch_col_finish(col_out(nullptr, nullptr, nullptr, 0, nullptr, nullptr),
                                         col_out(db, nullptr, w.p32, 0, w.sums, w.need), M > 0 ? pl.parts : 0, (int)N,
                                         w.top, flags, st));
+}
+
+// ---------------------------------------------------------------------------
+// Dropout
+// ---------------------------------------------------------------------------
+
+size_t ie_dropout_workspace(int64_t rows, int64_t cols) {
+    if (rows < 0 || cols < 0) return 0;
+    return dropout_ws(rows, cols);
+}
+
+ie_status ie_dropout(const ie_mat *X, const ie_mat *R, const ie_mat *Y, const ie_dropout_desc *d, void *ws,
+                     size_t ws_bytes, void *stream) {
+    if (!d) return IE_ERR_NULL;
+    IE_CHECK(check_mat(X));
+    IE_CHECK(check_mat(Y));
+    if (!same_shape(X, Y)) return IE_ERR_SHAPE;
+    if (R) {
+        IE_CHECK(check_mat(R));
+        if (!same_shape(X, R)) return IE_ERR_SHAPE;
+    }
+    if (d->drop > 65535 || !aligned(d->step_ptr, 8) || X->cols > LONG_COLS_MAX) return IE_ERR_UNSUPPORTED;
+    if (share(Y, X) || share(Y, R)) return IE_ERR_UNSUPPORTED;
+    if (!ws) return IE_ERR_WORKSPACE;
+    if (ws_bytes < dropout_ws(X->rows, X->cols)) return IE_ERR_WORKSPACE;
+    hipStream_t st = (hipStream_t)stream;
+    if (X->rows == 0 || X->cols == 0) return hip_status(launch_fill_i8(Y->exp, n_exps(Y), E_MIN, st));
+    Carve c{(char *)ws, HEADER};
+    const NormPlan pl = dropout_plan(X->rows, X->cols);
+    DropArgs a;
+    memset(&a, 0, sizeof a);
+    a.x = X->mant;
+    a.xe = X->exp;
+    a.x_row = X->group == IE_GROUP_ROW;
+    if (R) {
+        a.r = R->mant;
+        a.re = R->exp;
+        a.r_row = R->group == IE_GROUP_ROW;
+    }
+    a.y = Y->mant;
+    a.ye = Y->exp;
+    a.rows = X->rows;
+    a.cols = (int)X->cols;
+    a.q = mat_q(Y);
+    a.bmax = carve_dropout(c, X->rows, X->cols);
+    a.n_bmax = pl.grid;
+    a.drop = d->drop;
+    a.scale = (double)(65536.0f / (float)(65536 - d->drop));
+    a.seed = d->seed;
+    a.step = d->step;
+    a.step_ptr = d->step_ptr;
+    a.flags = (uint32_t *)ws;
+    const bool y_row = Y->group == IE_GROUP_ROW;
+    a.mode = y_row ? NORM_ROWS : NORM_NEED;
+    IE_TRY(launch_dropout(a, pl, st));
+    if (y_row) return IE_OK;
+    a.mode = NORM_ROUND;
+    return hip_status(launch_dropout(a, pl, st));
 }
 
 size_t ie_bmm_workspace(int32_t batch, int64_t M, int64_t N, int64_t K) {

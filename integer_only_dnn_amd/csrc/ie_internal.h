@@ -141,6 +141,7 @@ constexpr int PROF_NORM_FWD = 3600;
 constexpr int PROF_NORM_BWD = 3610;
 constexpr int PROF_COL_SUM = 3620;
 constexpr int PROF_COL_FINISH = 3630;
+constexpr int PROF_DROPOUT = 3700;
 
 // Auxiliary kernels (ie_aux.hip).
 hipError_t launch_fill_i32(int *p, long long n, int v, hipStream_t st);
@@ -294,5 +295,25 @@ struct ColOut {
 };
 hipError_t launch_col_finish(const ColOut &f, const ColOut &b, int parts, int cols, const int *top, uint32_t *flags,
                              hipStream_t st);
+
+// Dropout (ie_dropout.hip); mode as for layer norm.
+struct DropArgs {
+    const int8_t *x, *xe;
+    int x_row;
+    const int8_t *r, *re;  // residual, or nullptr
+    int r_row;
+    int8_t *y, *ye;
+    long long rows;
+    int cols;
+    int q, mode;
+    int *bmax;
+    int n_bmax;
+    uint32_t drop;
+    double scale;
+    uint64_t seed, step;
+    const uint64_t *step_ptr;
+    uint32_t *flags;
+};
+hipError_t launch_dropout(const DropArgs &a, const NormPlan &pl, hipStream_t st);
 
 }  // namespace ie

@@ -646,6 +646,20 @@ NormPlan norm_plan(long long rows, long long cols, int max_blocks) {
     return p;
 }
 
+// The smallest t * e that holds a row, e a multiple of the eight elements
+// that share a block of random bits.
+NormPlan dropout_plan(long long rows, long long cols) {
+    const int ts[] = {8, 16, 32, 64, 256, 1024};
+    NormPlan p{1024, 0, 1};
+    for (int t : ts)
+        for (int e = t == 16 || t == 32 || t == 64 ? 16 : 8; e <= 24; e += 8)
+            if (cols <= (long long)t * e && (p.e == 0 || t * e < p.t * p.e)) p = NormPlan{t, e, 1};
+    const long long rpb = p.t > 256 ? 1 : 256 / p.t;
+    const long long want = (rows + rpb - 1) / rpb, cap = p.t > 256 ? 512 : 2048;
+    p.grid = (int)(want < 1 ? 1 : want > cap ? cap : want);
+    return p;
+}
+
 ColPlan col_plan(long long rows, long long cols) {
     const long long gx = (cols + 255) / 256;
     long long parts = 2048 / (gx > 0 ? gx : 1);
@@ -684,6 +698,16 @@ NormWs carve_norm_bwd(Carve &c, long long rows, long long cols) {
 
 ColWs carve_linear_db(Carve &c, long long rows, long long cols) {
     return carve_cols(c, col_plan(rows, cols).parts, cols, false);
+}
+
+int *carve_dropout(Carve &c, long long rows, long long cols) {
+    return c.take<int>((size_t)dropout_plan(rows, cols).grid);
+}
+
+size_t dropout_ws(long long rows, long long cols) {
+    Carve c{nullptr, HEADER};
+    carve_dropout(c, rows, cols);
+    return align256(c.off);
 }
 
 size_t norm_fwd_ws(long long rows, long long cols) {

@@ -332,12 +332,16 @@ BmmWs carve_bmm(Carve &c, int form, long long Z, long long M, long long N, long 
 // persistent grid of `grid` blocks of max(t, 256) threads.
 constexpr long long NORM_COLS_MAX = 16384;
 constexpr long long NORM_ROWS_MAX = 1ll << 27;  // dgamma sums stay below 2^62
+constexpr long long LONG_COLS_MAX = 1ll << 30;  // dropout, column sums: columns are walked in 32 bits
 constexpr int NORM_FWD_BLOCKS = 2048;
 constexpr int NORM_BWD_BLOCKS = 512;  // each leaves one row of partial column sums
 struct NormPlan {
     int t, e, grid;
 };
 NormPlan norm_plan(long long rows, long long cols, int max_blocks);
+
+// Dropout: the same split, with e = 0 for rows too long to be held.
+NormPlan dropout_plan(long long rows, long long cols);
 
 // Column sums of a [rows x cols] gradient: `parts` chunks of `chunk` rows.
 struct ColPlan {
@@ -361,6 +365,7 @@ struct NormWs {
 NormWs carve_norm_fwd(Carve &c, long long rows, long long cols);
 NormWs carve_norm_bwd(Carve &c, long long rows, long long cols);
 ColWs carve_linear_db(Carve &c, long long rows, long long cols);
+int *carve_dropout(Carve &c, long long rows, long long cols);  // block maxima
 
 // Whether a parameter vector of n channels is [n x 1] or [1 x n].
 bool is_vector(const ie_mat *t, long long n);
@@ -368,6 +373,7 @@ bool is_vector(const ie_mat *t, long long n);
 size_t norm_fwd_ws(long long rows, long long cols);
 size_t norm_bwd_ws(long long rows, long long cols);
 size_t linear_db_ws(long long rows, long long cols);
+size_t dropout_ws(long long rows, long long cols);
 size_t linear_fwd_ws(long long M, long long N, long long K, const Force &f);
 size_t linear_dx_ws(long long M, long long N, long long K, const Force &f);
 size_t linear_dw_ws(long long M, long long N, long long K, const Force &fw);

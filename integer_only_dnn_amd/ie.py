@@ -11,7 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, byref, c_char_p, c_int, c_int8, c_int32, c_int64, c_size_t, c_uint32, c_void_p
+from ctypes import POINTER, byref, c_char_p, c_int, c_int8, c_int32, c_int64, c_size_t, c_uint32, c_uint64, c_void_p
 
 import torch
 
@@ -43,6 +43,10 @@ class ie_conv_desc(ctypes.Structure):
 
 class ie_scalar(ctypes.Structure):
     _fields_ = [("mant", c_int8), ("exp", c_int8)]
+
+
+class ie_dropout_desc(ctypes.Structure):
+    _fields_ = [("seed", c_uint64), ("step", c_uint64), ("step_ptr", c_void_p), ("drop", c_uint32)]
 
 
 EXPORTS = [
@@ -81,6 +85,9 @@ EXPORTS = [
      [POINTER(ie_mat)] * 3 + [ie_scalar] + [POINTER(ie_mat)] * 3 + [c_void_p, c_size_t, c_void_p]),
     ("ie_linear_bwd_db_workspace", c_size_t, [c_int64, c_int64]),
     ("ie_linear_bwd_db", c_int, [POINTER(ie_mat)] * 2 + [c_void_p, c_size_t, c_void_p]),
+    ("ie_dropout_workspace", c_size_t, [c_int64, c_int64]),
+    ("ie_dropout", c_int,
+     [POINTER(ie_mat)] * 3 + [POINTER(ie_dropout_desc), c_void_p, c_size_t, c_void_p]),
     ("ie_device_status", c_int, [c_void_p, c_void_p, POINTER(c_uint32), c_int]),
     ("ie_profile_enable", c_int, [c_int]),
     ("ie_profile_select", c_int, [c_int]),
@@ -394,6 +401,21 @@ def ie_linear_bwd_db(dY: Mat, db: Mat, ws: Workspace) -> None:
     dy, d = dY.c(), db.c()
     p, b = ws.get(_ws_size("ie_linear_bwd_db_workspace", dy.rows, dy.cols))
     _check(lib().ie_linear_bwd_db(byref(dy), byref(d), p, b, _stream(ws.device)), "ie_linear_bwd_db")
+
+
+def ie_dropout(X: Mat, R: Mat | None, Y: Mat, drop: int, seed: int, step: int, ws: Workspace,
+               step_ptr: torch.Tensor | None = None) -> None:
+    """Y = X with drop of 65536 elements dropped and the others scaled, plus R.
+    step_ptr: an int64 device tensor of one element added to `step` when the
+    kernels run, or None."""
+    if not 0 <= drop < 1 << 32 or not 0 <= seed < 1 << 64 or not 0 <= step < 1 << 64:
+        raise ValueError("drop, seed or step out of range")
+    if step_ptr is not None and (step_ptr.dtype != torch.int64 or step_ptr.numel() != 1 or not step_ptr.is_cuda):
+        raise ValueError("step_ptr must be an int64 device tensor of one element")
+    x, y = X.c(), Y.c()
+    d = ie_dropout_desc(seed, step, step_ptr.data_ptr() if step_ptr is not None else None, drop)
+    p, b = ws.get(_ws_size("ie_dropout_workspace", x.rows, x.cols))
+    _check(lib().ie_dropout(byref(x), _opt(R), byref(y), byref(d), p, b, _stream(ws.device)), "ie_dropout")
 
 
 def ie_profile_enable(on: bool = True) -> None:

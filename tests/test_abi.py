@@ -216,3 +216,25 @@ def test_layer_norm_and_bias_gradient_argument_errors():
     assert db(by(X), by(g), None, big, None) == 4 and db(by(X), by(g), 1, 256, None) == 4
     for size in (L.ie_layer_norm_fwd_workspace, L.ie_layer_norm_bwd_workspace, L.ie_linear_bwd_db_workspace):
         assert size(-1, 4) == 0 and size(4, -1) == 0 and 256 < size(4, 8) <= size(4000, 800)
+
+
+def test_dropout_argument_errors():
+    """Shapes, the rate, the device step's alignment, shared buffers, row
+    lengths and workspaces are refused before anything is enqueued."""
+    L = ie.lib()
+    by, big, f = ctypes.byref, 1 << 30, L.ie_dropout
+    X, Y = _mat(4, 8), _mat(4, 8, mant=512, exp=512)
+    d = ie.ie_dropout_desc(1, 2, None, 6554)
+    assert f(by(X), None, by(Y), None, 1, big, None) == 1
+    assert f(None, None, by(Y), by(d), 1, big, None) == 1
+    assert f(by(X), None, by(_mat(4, 9, mant=512, exp=512)), by(d), 1, big, None) == 2
+    assert f(by(X), by(_mat(5, 8)), by(Y), by(d), 1, big, None) == 2
+    assert f(by(X), None, by(Y), by(ie.ie_dropout_desc(1, 2, None, 65536)), 1, big, None) == 6
+    assert f(by(X), None, by(Y), by(ie.ie_dropout_desc(1, 2, 12, 6554)), 1, big, None) == 6
+    assert f(by(X), None, by(X), by(d), 1, big, None) == 6
+    assert f(by(X), by(Y), by(Y), by(d), 1, big, None) == 6
+    wide = (1 << 30) + 1
+    assert f(by(_mat(1, wide)), None, by(_mat(1, wide, mant=512, exp=512)), by(d), 1, big, None) == 6
+    assert L.ie_linear_bwd_db(by(_mat(1, wide)), by(_mat(wide, 1, mant=512, exp=512)), 1, 1 << 40, None) == 6
+    assert f(by(X), None, by(Y), by(d), None, big, None) == 4 and f(by(X), None, by(Y), by(d), 1, 256, None) == 4
+    assert L.ie_dropout_workspace(-1, 4) == 0 and L.ie_dropout_workspace(4, 8) > 256
