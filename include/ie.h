@@ -354,6 +354,23 @@ ie_status ie_layer_norm_bwd(const ie_mat *dY, const ie_mat *X, const ie_mat *gam
                             const ie_mat *dgamma, const ie_mat *dbeta, void *ws, size_t ws_bytes, void *stream);
 
 /*
+ * Forward product with bias, residual and activation in its epilogue:
+ *   Y = R_Y(X . W^T + bias + R), then the activation on the rounded mantissas
+ * (as ie_linear_fwd_act; a ReLU also clips the residual's share).  X, W, Y as
+ * in ie_linear_fwd; bias: N channels as [N x 1] (one exponent, or one per
+ * channel when ROW) or [1 x N] (one exponent), or NULL; R: [M x N], TENSOR or
+ * ROW, or NULL.  The product is exact; the bias and then R are added to it to
+ * 53 bits (each sum exact while its terms span no more, else rounded half to
+ * even), and the result is rounded once into Y's groups.  With neither bias
+ * nor R it is ie_linear_fwd_act.  Backward: ie_linear_bwd_dx or ie_linear_bwd_dx_act,
+ * ie_linear_bwd_dw and ie_linear_bwd_db on the gradient behind the activation
+ * (ie_relu_bwd), which is also R's gradient.
+ */
+size_t ie_linear_fwd_fused_workspace(int64_t M, int64_t N, int64_t K);
+ie_status ie_linear_fwd_fused(const ie_mat *X, const ie_mat *W, const ie_mat *bias, const ie_mat *R, const ie_mat *Y,
+                              int act, void *ws, size_t ws_bytes, void *stream);
+
+/*
  * Bias gradient of a linear layer, db = R(sum_rows dY), exact sums of dY
  * re-expressed at the largest of its row exponents.  dY [M x N], TENSOR or
  * ROW; db: N channels as [N x 1] (one exponent, or one per channel when ROW)
@@ -410,7 +427,7 @@ ie_status ie_device_status(void *ws, void *stream, uint32_t *flags, int clear);
  * a convolution's backward pass, 3500 / 3510 ReLU forward / backward, 3520 /
  * 3521 / 3530 the Sum's maximum, rounding and row-grouped passes, 3600 / 3610
  * layer norm forward / backward, 3620 / 3630 column sums and their finish,
- * 3700 dropout) and returns how
+ * 3700 dropout, 3800 / 3810 products with bias and residual and their split finalize) and returns how
  * many were recorded since the last read; the records are then cleared.
  * The timing records (and their events) are the library's only process-wide
  * state; they are not thread-safe.

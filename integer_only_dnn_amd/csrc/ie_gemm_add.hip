@@ -1,0 +1,300 @@
+// Forward product with bias, residual and ReLU in its epilogue:
+//   y = (acc 2^(e_X + e_W) + bias) + R,
+// acc the exact int32 contraction, each sum rounded to 53 bits (exact while
+// its terms span no more), y rounded once into Y's groups, then the clip on
+// the rounded mantissas.
+//
+// The contraction is the dense products' (gemm_tile); its matrix
+// instructions run transposed, so that a lane holds one row of the result
+// and four neighbouring columns per accumulator quarter: a row's maximum is
+// taken in registers, the residual is read and the result written four bytes
+// at a time, and the bias is the same for the 32 lanes of a half-wave.  The
+// two products of an element (by the scales' powers of two) are exact in the
+// fp64 unit, which runs its fused multiply-add at the fp32 rate.
+#include "ie_f64.h"
+#include "ie_gemm_impl.h"
+
+namespace ie {
+
+struct EpiAdd {
+    AddEpi e;
+
+    // a row of int8 or int16 results from LDS to memory, 16 bytes per thread
+    template <int ES, int BM, int BN>
+    __device__ __forceinline__ void flush(const int8_t *lds, void *dst, int m0, int n0, int M, int N, bool vec) const {
+        constexpr int PITCH = BN * ES + 16, CPR = BN * ES / 16, EPC = 16 / ES;
+#pragma unroll
+        for (int q0 = 0; q0 < BM * CPR; q0 += NTHR) {
+            const int q = q0 + threadIdx.x, row = q / CPR, cb = q % CPR * 16;
+            const int gr = m0 + row, gc = n0 + cb / ES;
+            if (gr >= M || gc >= N) continue;
+            v4i v = *(const v4i *)(lds + row * PITCH + cb);
+            if (ES == 1 && e.relu) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = (int)relu4((uint32_t)v[k]);
+            }
+            int8_t *g = (int8_t *)dst + ((long long)gr * N + gc) * ES;
+            if (vec && gc + EPC <= N) {
+                *(v4i *)g = v;
+            } else {
+                const int bytes = min(16, (N - gc) * ES);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) store4(g, 4 * k, bytes, (uint32_t)v[k]);
+            }
+        }
+    }
+
+    template <int MI, int NI, int RG, int DI, int AM, int AN>
+    __device__ __forceinline__ void finish(const v16i (&acc)[AM][AN], int8_t *lds, int m0, int n0, int tile_m,
+                                           int tile_n, int M, int N, int TM) const {
+        constexpr int BM = 64 * MI, BN = 64 * NI, RP = BN + 4;  // RP: pitch of the residual tile
+        const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
+        double *cs = (double *)lds, *bs = cs + BN, *red = bs + BN;  // column scales, bias, maxima [2][BM]
+        int8_t *rt = (int8_t *)(red + 2 * BM), *out = rt + BM * RP;
+        static_assert(16 * BN + 16 * BM + BM * RP + BM * (BN * 2 + 16) <= TileLds<LD_K, LD_K, MI, NI, false>::value,
+                      "epilogue exceeds the tile's LDS");
+        static_assert(BM * RP % 16 == 0, "staging alignment");
+        __syncthreads();  // every wave is done with the last stage
+        for (int i = tid; i < BN; i += NTHR) {
+            const int n = n0 + i;
+            // past the last column everything is zero
+            cs[i] = n < N ? pow2((int)e.we[e.w_row ? n : 0]) : 0.0;
+            bs[i] = n < N && e.bias.m ? (double)e.bias.m[n] * pow2((int)e.bias.e[e.bias.per ? n : 0]) : 0.0;
+        }
+        if (e.r) {
+            constexpr int CPR = BN / 16;
+#pragma unroll
+            for (int q0 = 0; q0 < BM * CPR; q0 += NTHR) {
+                const int q = q0 + tid, row = q / CPR, c = q % CPR * 16;
+                uint32_t v[4] = {0, 0, 0, 0};
+                if (m0 + row < M && n0 + c < N) {
+                    const int8_t *src = e.r + (long long)(m0 + row) * N + n0;
+                    if (e.r_vec) {
+                        const v4i w = *(const v4i *)(src + c);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) v[k] = (uint32_t)w[k];
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) v[k] = load4(src, c + 4 * k, N - n0);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) *(uint32_t *)(rt + row * RP + c + 4 * k) = v[k];
+            }
+        }
+        __syncthreads();
+
+        double y[MI][NI][16], sx[MI], sr[MI], mx[MI];
+        int row[MI];
+#pragma unroll
+        for (int a = 0; a < MI; ++a) {
+            row[a] = wm * 32 * MI + a * 32 + (lane & 31);
+            const int m = m0 + row[a];
+            sx[a] = m < M ? pow2((int)e.xe[e.x_row ? m : 0]) : 0.0;
+            sr[a] = e.r && m < M ? pow2((int)e.re[e.r_row ? m : 0]) : 0.0;
+            mx[a] = 0.0;
+        }
+#pragma unroll
+        for (int b = 0; b < NI; ++b)
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                const int c = wn * 32 * NI + b * 32 + 8 * h + 4 * (lane >> 5);
+#pragma unroll
+                for (int a = 0; a < MI; ++a) {
+                    const uint32_t r4 = e.r ? *(const uint32_t *)(rt + row[a] * RP + c) : 0u;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        // each fused step is an exact product and one rounded sum
+                        double v = __builtin_fma((double)acc[a][b][4 * h + k], sx[a] * cs[c + k], bs[c + k]);
+                        if (e.r) v = __builtin_fma((double)byte_of(r4, k), sr[a], v);
+                        y[a][b][4 * h + k] = v;
+                        mx[a] = fmax(mx[a], fabs(v));
+                    }
+                }
+            }
+        // the group's exponent (results in this pass), or the round-to-odd
+        // position two bits below the tile's own need
+        double inv[MI];
+        if constexpr (RG) {
+#pragma unroll
+            for (int a = 0; a < MI; ++a) {
+                mx[a] = fmax(mx[a], __shfl_xor(mx[a], 32));
+                if (lane < 32) red[wn * BM + row[a]] = mx[a];
+            }
+            __syncthreads();
+#pragma unroll
+            for (int a = 0; a < MI; ++a) {
+                const int need = need_f64(fmax(red[row[a]], red[BM + row[a]]), e.q), m = m0 + row[a];
+                const bool first = lane < 32 && wn == 0 && m < M;
+                if constexpr (DI) {
+                    int ex = max(E_MIN, need);
+                    if (first) {
+                        ex = clamp_exp_flag(ex, e.flags);
+                        e.ye[m] = (int8_t)ex;
+                    }
+                    inv[a] = pow2(-min(ex, E_MAX));
+                } else {
+                    if (first) e.p16[(long long)m * ((N + BN - 1) / BN) + tile_n] = (int16_t)(need == NEED_NONE ? P_NONE : need);
+                    inv[a] = need == NEED_NONE ? 0.0 : pow2(2 - need);
+                }
+            }
+        } else {
+            double t = 0.0;
+#pragma unroll
+            for (int a = 0; a < MI; ++a) t = fmax(t, m0 + row[a] < M ? mx[a] : 0.0);
+#pragma unroll
+            for (int s = 1; s < 64; s <<= 1) t = fmax(t, __shfl_xor(t, s));
+            if (lane == 0) red[wave] = t;
+            __syncthreads();
+            const int need = need_f64(fmax(fmax(red[0], red[1]), fmax(red[2], red[3])), e.q);
+            double in;
+            if constexpr (DI) {
+                const int ex = clamp_exp_flag(max(E_MIN, need), e.flags);
+                if (tid == 0) e.ye[0] = (int8_t)ex;
+                in = pow2(-ex);
+            } else {
+                if (tid == 0) e.p16[tile_m + TM * tile_n] = (int16_t)(need == NEED_NONE ? P_NONE : need);
+                in = need == NEED_NONE ? 0.0 : pow2(2 - need);
+            }
+#pragma unroll
+            for (int a = 0; a < MI; ++a) inv[a] = in;
+        }
+#pragma unroll
+        for (int a = 0; a < MI; ++a)
+#pragma unroll
+            for (int b = 0; b < NI; ++b)
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    const int c = wn * 32 * NI + b * 32 + 8 * h + 4 * (lane >> 5);
+                    const double *v = &y[a][b][4 * h];
+                    if constexpr (DI) {
+                        *(uint32_t *)(out + row[a] * (BN + 16) + c) =
+                            pack4(mant_of(v[0], inv[a]), mant_of(v[1], inv[a]), mant_of(v[2], inv[a]),
+                                  mant_of(v[3], inv[a]));
+                    } else {
+                        // floor, with the lowest bit set where anything is cut off
+                        int o[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const double w = v[k] * inv[a], f = __builtin_floor(w);
+                            o[k] = (int)f | (int)(w != f);
+                        }
+                        v2i p = {(o[0] & 0xffff) | o[1] << 16, (o[2] & 0xffff) | o[3] << 16};
+                        *(v2i *)(out + row[a] * (2 * BN + 16) + 2 * c) = p;
+                    }
+                }
+        __syncthreads();
+        if constexpr (DI) flush<1, BM, BN>(out, e.y, m0, n0, M, N, (N & 15) == 0 && ((uintptr_t)e.y & 15) == 0);
+        else flush<2, BM, BN>(out, e.v16, m0, n0, M, N, (N & 7) == 0);
+    }
+};
+
+template <int MI, int NI, int RG, int DI>
+__global__ __launch_bounds__(NTHR, (Occ<MI, NI>::value)) void gemm_add_kernel(Operand A, Operand B, int M, int N, int K,
+                                                                              int TM, EpiAdd ep) {
+    __shared__ __attribute__((aligned(16))) int8_t lds[TileLds<LD_K, LD_K, MI, NI, false>::value];
+    gemm_tile<LD_K, LD_K, MI, NI, false, false, -1, RG, DI>(A, B, M, N, K, K, TM, 1, ep, blockIdx.x, gridDim.x, lds);
+}
+
+template <int MI, int NI>
+static void launch_tile(const Operand &A, const Operand &B, int M, int N, int K, bool direct, const EpiAdd &ep,
+                        hipStream_t st) {
+    const int TM = (M + 64 * MI - 1) / (64 * MI), TN = (N + 64 * NI - 1) / (64 * NI);
+    const dim3 grid(TM * TN), block(NTHR);
+    if (ep.e.y_row) {
+        if (direct) hipLaunchKernelGGL((gemm_add_kernel<MI, NI, 1, 1>), grid, block, 0, st, A, B, M, N, K, TM, ep);
+        else hipLaunchKernelGGL((gemm_add_kernel<MI, NI, 1, 0>), grid, block, 0, st, A, B, M, N, K, TM, ep);
+    } else {
+        if (direct) hipLaunchKernelGGL((gemm_add_kernel<MI, NI, 0, 1>), grid, block, 0, st, A, B, M, N, K, TM, ep);
+        else hipLaunchKernelGGL((gemm_add_kernel<MI, NI, 0, 0>), grid, block, 0, st, A, B, M, N, K, TM, ep);
+    }
+}
+
+hipError_t launch_gemm_add(const Operand &A, const Operand &B, int M, int N, int K, Tile t, bool direct,
+                           const AddEpi &e, hipStream_t st) {
+    const EpiAdd ep{e};
+    prof_begin(st, PROF_GEMM_ADD);
+#define IE_CASE(a, b) \
+    if (t.mi == a && t.ni == b) launch_tile<a, b>(A, B, M, N, K, direct, ep, st);
+    IE_TILES_ADD(IE_CASE)
+#undef IE_CASE
+    prof_end(st, PROF_GEMM_ADD);
+    return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// Split contractions: the int32 partials of `splits` chunks summed (|sum| <
+// 2^30), then the same epilogue, one block per row at a time.
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ double split_value(const AddEpi &e, const int *p, int splits, long long stride, long long m,
+                                              int n, int N, double sx, double sr) {
+    int s = 0;
+    const long long o = m * N + n;
+    for (int i = 0; i < splits; ++i) s += p[i * stride + o];
+    const double bias = e.bias.m ? (double)e.bias.m[n] * pow2((int)e.bias.e[e.bias.per ? n : 0]) : 0.0;
+    double v = __builtin_fma((double)s, sx * pow2((int)e.we[e.w_row ? n : 0]), bias);
+    if (e.r) v = __builtin_fma((double)e.r[o], sr, v);
+    return v;
+}
+
+__global__ __launch_bounds__(1024) void split_add_kernel(AddEpi e, const int *partial, int splits, long long stride,
+                                                         int M, int N, int mode, int *bmax, int n_bmax) {
+    __shared__ int shi[16];
+    __shared__ double shd[16];
+    double inv = 0.0, run = 0.0;
+    if (mode == NORM_ROUND) {
+        int m = NEED_NONE;
+        for (int i = threadIdx.x; i < n_bmax; i += 1024) m = max(m, bmax[i]);
+        m = row_reduce<1024>(m, Max{}, shi);
+        const int ex = clamp_exp_flag(max(E_MIN, m), e.flags);
+        inv = pow2(-ex);
+        if (blockIdx.x == 0 && threadIdx.x == 0) e.ye[0] = (int8_t)ex;
+    }
+    for (int m = blockIdx.x; m < M; m += gridDim.x) {
+        const double sx = pow2((int)e.xe[e.x_row ? m : 0]), sr = e.r ? pow2((int)e.re[e.r_row ? m : 0]) : 0.0;
+        if (mode != NORM_ROUND) {
+            double mx = 0.0;
+            for (long long n = threadIdx.x; n < N; n += 1024)
+                mx = fmax(mx, fabs(split_value(e, partial, splits, stride, m, (int)n, N, sx, sr)));
+            if (mode == NORM_NEED) {
+                run = fmax(run, mx);
+                continue;
+            }
+            mx = row_reduce<1024>(mx, Max{}, shd);
+            int ex = max(E_MIN, need_f64(mx, e.q));
+            if (threadIdx.x == 0) {
+                ex = clamp_exp_flag(ex, e.flags);
+                e.ye[m] = (int8_t)ex;
+            }
+            inv = pow2(-min(ex, E_MAX));
+        }
+        for (long long n = threadIdx.x; n < N; n += 1024) {
+            const int c = (int8_t)mant_of(split_value(e, partial, splits, stride, m, (int)n, N, sx, sr), inv);
+            e.y[(long long)m * N + n] = (int8_t)(e.relu && c < 0 ? 0 : c);
+        }
+    }
+    if (mode == NORM_NEED) {
+        run = row_reduce<1024>(run, Max{}, shd);
+        if (threadIdx.x == 0) bmax[blockIdx.x] = need_f64(run, e.q);
+    }
+}
+
+hipError_t launch_split_add(const AddEpi &e, const int *partial, int splits, int M, int N, int *bmax, hipStream_t st) {
+    const int grid = M < SPLIT_ADD_BLOCKS ? M : SPLIT_ADD_BLOCKS;
+    const long long stride = (long long)M * N;
+    prof_begin(st, PROF_SPLIT_ADD);
+    if (e.y_row) {
+        hipLaunchKernelGGL(split_add_kernel, dim3(grid), dim3(1024), 0, st, e, partial, splits, stride, M, N, NORM_ROWS,
+                           bmax, 0);
+    } else {
+        hipLaunchKernelGGL(split_add_kernel, dim3(grid), dim3(1024), 0, st, e, partial, splits, stride, M, N, NORM_NEED,
+                           bmax, grid);
+        hipLaunchKernelGGL(split_add_kernel, dim3(grid), dim3(1024), 0, st, e, partial, splits, stride, M, N, NORM_ROUND,
+                           bmax, grid);
+    }
+    prof_end(st, PROF_SPLIT_ADD);
+    return hipGetLastError();
+}
+
+}  // namespace ie

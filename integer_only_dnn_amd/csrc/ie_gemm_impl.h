@@ -757,6 +757,14 @@ struct TileLds1 {
     static constexpr int value = v0 > slices ? v0 : slices;
 };
 
+// acc += a . b^T (AB), or its transpose, acc += b . a^T: then a lane's results
+// lie in one row of a.
+template <bool AB>
+__device__ __forceinline__ v16i mfma_ab(const v4i &a, const v4i &b, const v16i &acc) {
+    return AB ? __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, acc, 0, 0, 0)
+              : __builtin_amdgcn_mfma_i32_32x32x32_i8(b, a, acc, 0, 0, 0);
+}
+
 // One workgroup's work item: bid and nblk are its index and the number of
 // workgroups of its grid (or of its part of a paired grid); lds points to
 // TileLds bytes of shared memory (TileLds1 when ONE: a contraction of at
@@ -768,10 +776,14 @@ struct TileLds1 {
 // only ever takes one of them carries no code for the other.  DI likewise
 // for the epilogue: 1 rounds to int8 in this pass (direct, or the second
 // pass of a recomputed product), 0 rounds to odd; -1: ep.mode decides.
-template <int KA, int KB, int MI, int NI, bool PARTIAL, bool ONE = false, int MODE = -1, int RG = -1, int DI = -1>
+// EP: Epi, the epilogues below; any other type takes the accumulators of the
+// transposed matrix instructions (a lane holds one tile row) in its finish().
+template <int KA, int KB, int MI, int NI, bool PARTIAL, bool ONE = false, int MODE = -1, int RG = -1, int DI = -1,
+          class EP = Epi>
 __device__ __forceinline__ int gemm_tile(const Operand &A, const Operand &B, int M_, int N, int K, int k_chunk,
-                                          int TM, int S, const Epi &ep, int bid, int nblk, int8_t *lds) {
+                                          int TM, int S, const EP &ep, int bid, int nblk, int8_t *lds) {
     static_assert(!(ONE && PARTIAL), "one-step tiles have no split form");
+    constexpr bool OWN = std::is_same<EP, Epi>::value;
     constexpr int BMt = 64 * MI, BNt = 64 * NI;
     using LA = Lds<KA, BMt>;
     using LB = Lds<KB, BNt>;
@@ -798,7 +810,7 @@ __device__ __forceinline__ int gemm_tile(const Operand &A, const Operand &B, int
     // contraction, its columns of the phase-sorted weight copy.
     bool phased = false;
     PhaseRec pr{};
-    if constexpr (KA == LD_DGRAD && KB == LD_K) {
+    if constexpr (OWN && KA == LD_DGRAD && KB == LD_K) {
         if (ep.ph.n) {
             // the phases interleave: tile row tile_m is row tile_m / 4 of phase
             // phase_of_tile(tile_m), a rotation within each aligned group of four
@@ -825,8 +837,9 @@ __device__ __forceinline__ int gemm_tile(const Operand &A, const Operand &B, int
     constexpr int CA = Ld<KA, BMt>::CH, CB = Ld<KB, BNt>::CH;
 
     // exponents of this tile's rows and columns, for the epilogue
-    __shared__ int seA[PARTIAL ? 1 : BMt], seB[PARTIAL ? 1 : BNt];
-    if constexpr (!PARTIAL) {
+    __shared__ int seA[PARTIAL || !OWN ? 1 : BMt], seB[PARTIAL || !OWN ? 1 : BNt];
+    if constexpr (!OWN) {
+    } else if constexpr (!PARTIAL) {
         for (int i = tid; i < BMt; i += NTHR) seA[i] = m0 + i < M ? exp_at(ep.ea, m0 + i) : 0;
         for (int i = tid; i < BNt; i += NTHR) seB[i] = n0 + i < N ? exp_at(ep.eb, n0 + i) : 0;
     } else {
@@ -836,7 +849,7 @@ __device__ __forceinline__ int gemm_tile(const Operand &A, const Operand &B, int
     // second pass of a recomputed whole-tensor product: the first pass's
     // maxima, loaded now so that they land during the main loop
     int given = NEED_NONE;
-    if constexpr (!PARTIAL) {
+    if constexpr (OWN && !PARTIAL) {
         if (ep.mode == EPI_GIVEN && !(RG >= 0 ? RG == 1 : ep.row_group))
             for (int i = tid; i < ep.tneed_n; i += NTHR) given = max(given, ep.tneed[i]);
     }
@@ -882,7 +895,7 @@ __device__ __forceinline__ int gemm_tile(const Operand &A, const Operand &B, int
             for (int a = 0; a < 2; ++a)
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
-                    acc[a][b] = __builtin_amdgcn_mfma_i32_32x32x32_i8(af[a], bf[b], acc[a][b], 0, 0, 0);
+                    acc[a][b] = mfma_ab<OWN>(af[a], bf[b], acc[a][b]);
             return;
         }
 #pragma unroll
@@ -896,7 +909,7 @@ __device__ __forceinline__ int gemm_tile(const Operand &A, const Operand &B, int
             for (int a = 0; a < MI; ++a)
 #pragma unroll
                 for (int b = 0; b < NI; ++b)
-                    acc[a][b] = __builtin_amdgcn_mfma_i32_32x32x32_i8(af[a], bf[b], acc[a][b], 0, 0, 0);
+                    acc[a][b] = mfma_ab<OWN>(af[a], bf[b], acc[a][b]);
         }
     };
 
@@ -921,7 +934,7 @@ __device__ __forceinline__ int gemm_tile(const Operand &A, const Operand &B, int
         for (int a = 0; a < MI; ++a)
 #pragma unroll
             for (int b = 0; b < NI; ++b)
-                acc[a][b] = __builtin_amdgcn_mfma_i32_32x32x32_i8(af[a], bf[b], acc[a][b], 0, 0, 0);
+                acc[a][b] = mfma_ab<OWN>(af[a], bf[b], acc[a][b]);
     };
     // the next sub-step's reads first, then this sub-step's MFMAs: a read
     // has a whole sub-step of matrix work to land
@@ -1045,6 +1058,10 @@ __device__ __forceinline__ int gemm_tile(const Operand &A, const Operand &B, int
         acc[0][0] = mine;
     }
 
+    if constexpr (!OWN) {
+        ep.template finish<MI, NI, RG, DI>(acc, lds, m0, n0, tile_m, tile_n, M, N, TM);
+        return NEED_NONE;
+    } else {
     // Element (a, b, r) of this lane sits at tile row / column
     //   TR = 32 MI wm + 32 a + 8 (r/4) + 4 (lane/32) + r%4,   TC = 32 NI wn + 32 b + lane%32.
     const int tr0 = wm * 32 * MI + 4 * (lane >> 5);
@@ -1513,6 +1530,7 @@ __device__ __forceinline__ int gemm_tile(const Operand &A, const Operand &B, int
             flush(ES1{}, ep.out, N, (N & 15) == 0 && ((uintptr_t)ep.out & 15) == 0 && act_aligned(ep.act, 16));
         else flush(ES2{}, ep.v16, N, (N & 7) == 0);
         return NEED_NONE;
+    }
     }
 }
 

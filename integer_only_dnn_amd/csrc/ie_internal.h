@@ -142,6 +142,8 @@ constexpr int PROF_NORM_BWD = 3610;
 constexpr int PROF_COL_SUM = 3620;
 constexpr int PROF_COL_FINISH = 3630;
 constexpr int PROF_DROPOUT = 3700;
+constexpr int PROF_GEMM_ADD = 3800;
+constexpr int PROF_SPLIT_ADD = 3810;
 
 // Auxiliary kernels (ie_aux.hip).
 hipError_t launch_fill_i32(int *p, long long n, int v, hipStream_t st);
@@ -315,5 +317,25 @@ struct DropArgs {
     uint32_t *flags;
 };
 hipError_t launch_dropout(const DropArgs &a, const NormPlan &pl, hipStream_t st);
+
+// Product with bias and residual (ie_gemm_add.hip): rows m at exponent
+// xe, columns n at we, the result in this pass (y, ye) or as round-to-odd
+// values (v16) with the tiles' needs (p16) for launch_rto_finalize.
+struct AddEpi {
+    const int8_t *xe, *we;
+    int x_row, w_row;
+    NormVec bias;
+    const int8_t *r, *re;  // residual, or nullptr
+    int r_row, r_vec;      // r_vec: its rows are 16-byte aligned
+    int8_t *y, *ye;
+    int y_row;
+    int16_t *v16, *p16;
+    int q, relu;
+    uint32_t *flags;
+};
+hipError_t launch_gemm_add(const Operand &A, const Operand &B, int M, int N, int K, Tile t, bool direct,
+                           const AddEpi &e, hipStream_t st);
+// The same epilogue on int32 partial sums [splits][M][N].
+hipError_t launch_split_add(const AddEpi &e, const int *partial, int splits, int M, int N, int *bmax, hipStream_t st);
 
 }  // namespace ie

@@ -228,6 +228,10 @@ bool tile_built(int family, Tile t, bool partial) {
         case FAM_DENSE:
             IE_TILES_DENSE(IE_HAS)
             return false;
+        case FAM_ADD:
+            if (partial) return tile_built(FAM_DENSE, t, true);
+            IE_TILES_ADD(IE_HAS)
+            return false;
         case FAM_IM2COL:
         case FAM_DGRAD:
         case FAM_DGRAD_WT:
@@ -351,6 +355,12 @@ Plan plan_product(long long M, long long N, long long K, int row_group, int fami
     return best;
 }
 
+Plan plan_add(long long M, long long N, long long K, int row_group, const Force &f) {
+    Plan p = plan_product(M, N, K, row_group, FAM_ADD, f);
+    if (!f.on && p.mode == PLAN_RECOMP) p.mode = PLAN_RTO;
+    return p;
+}
+
 DgradPlan plan_dgrad(const ConvGeom &g, int row_group, const Force &f, bool weight_in_place) {
     DgradPlan d;
     memset(&d, 0, sizeof d);
@@ -425,6 +435,7 @@ bool plan_valid(const Plan &pl, long long M, long long N, long long K, int row_g
         return false;
     const bool wg = family == FAM_WGRAD || family == FAM_WGRAD_CONV;
     if (wg && pl.mode != PLAN_SPLIT) return false;
+    if (family == FAM_ADD && pl.mode == PLAN_RECOMP) return false;
     if (!tile_built(family, pl.t, pl.mode == PLAN_SPLIT)) return false;
     if (pl.splits < 1 || pl.k_chunk <= 0 || pl.k_chunk % BK != 0) return false;
     if ((long long)pl.splits * pl.k_chunk < K) return false;
@@ -478,6 +489,13 @@ Needs product_needs(const Plan &pl, long long M, long long N, long long K, int r
             n.gneed = row_group ? (size_t)M : 1;
         }
     }
+    return n;
+}
+
+// The split finalize with bias and residual keeps no sums.
+Needs add_needs(const Plan &pl, long long M, long long N, long long K, int row_group) {
+    Needs n = product_needs(pl, M, N, K, row_group);
+    n.gneed = n.sums = n.tneed = 0;
     return n;
 }
 
@@ -550,6 +568,28 @@ LinearFwdWs carve_linear_fwd(Carve &c, long long M, long long N, long long K, co
         w.wp = c.take<int8_t>((size_t)N * Kp);
     }
     w.pw = carve_product(c, M, N, Kp, FAM_DENSE, f);
+    return w;
+}
+
+LinearFusedWs carve_linear_fused(Carve &c, long long M, long long N, long long K, const Force &f) {
+    LinearFusedWs w{};
+    const long long Kp = r16(K);
+    if (Kp != K) {
+        w.l.xp = c.take<int8_t>((size_t)M * Kp);
+        w.l.wp = c.take<int8_t>((size_t)N * Kp);
+    }
+    Needs n{0, 0, 0, 0, 0, 0};
+    for (int rg = 0; rg < 2; ++rg) {
+        const Needs r = add_needs(plan_add(M, N, Kp, rg, f), M, N, Kp, rg);
+        n.p16 = mx(n.p16, r.p16);
+        n.v16 = mx(n.v16, r.v16);
+        n.partial = mx(n.partial, r.partial);
+    }
+    w.l.pw.p16 = c.take<int16_t>(n.p16);
+    w.l.pw.v16 = c.take<int16_t>(n.v16);
+    w.l.pw.partial = c.take<int>(n.partial);
+    w.l.pw.n = n;
+    w.bmax = c.take<int>(SPLIT_ADD_BLOCKS);
     return w;
 }
 
@@ -732,6 +772,14 @@ size_t linear_fwd_ws(long long M, long long N, long long K, const Force &f) {
     Carve c{nullptr, HEADER};
     carve_linear_fwd(c, M, N, K, f);
     return align256(c.off);
+}
+
+// Also enough for the plain product, which runs when there is neither bias
+// nor residual.
+size_t linear_fused_ws(long long M, long long N, long long K, const Force &f) {
+    Carve c{nullptr, HEADER};
+    carve_linear_fused(c, M, N, K, f);
+    return mx(align256(c.off), linear_fwd_ws(M, N, K, f));
 }
 
 size_t linear_dx_ws(long long M, long long N, long long K, const Force &f) {

@@ -134,9 +134,11 @@ enum Family {
     FAM_DGRAD_WT = 3,    // convolution input gradient, weight read in place
     FAM_WGRAD = 4,       // M-contiguous x M-contiguous (linear weight gradient)
     FAM_WGRAD_CONV = 5,  // convolution weight gradient
+    FAM_ADD = 6,         // dense, with bias and residual in the epilogue (split: the dense partial sums)
 };
 
 #define IE_TILES_DENSE(X) X(2, 2) X(4, 1) X(1, 4) X(2, 1) X(1, 2) X(1, 1)
+#define IE_TILES_ADD(X) X(2, 2) X(1, 4) X(2, 1) X(1, 1)
 #define IE_TILES_CONV(X) X(2, 2) X(4, 1) X(2, 1) X(1, 1)
 #define IE_TILES_WGRAD(X) X(2, 2) X(1, 4) X(4, 1) X(1, 1)
 // Paired convolution backward: (input-gradient tile, weight-gradient tile).
@@ -217,6 +219,11 @@ Plan plan_wgrad(long long M, long long N, long long L, int family, const Force &
 // Batched products (always row groups): tile and epilogue.  kk: A . B^T.
 Plan plan_batched(long long Z, long long M, long long N, bool kk);
 
+// Dense product with bias or residual: plan_product, with the round-to-odd
+// epilogue where that would recompute (the recomputed product is not built
+// with them; a forced one is refused).
+Plan plan_add(long long M, long long N, long long K, int row_group, const Force &f);
+
 // A plan is valid when its kernel is built, its chunks cover the contraction
 // (exact int32 partials for splits), and a direct epilogue holds every group
 // in one tile.
@@ -253,6 +260,7 @@ struct Needs {
 };
 bool split_round_rows_fits(int Nout, int mc, int mcp);
 Needs product_needs(const Plan &pl, long long M, long long N, long long K, int row_group);
+Needs add_needs(const Plan &pl, long long M, long long N, long long K, int row_group);
 Needs wgrad_needs(const Plan &pl, long long N, long long Kg, long long Kout, int mc, int mcp, int row_group);
 Needs batched_needs(const Plan &pl, long long Z, long long M, long long N);
 bool covers(const Needs &have, const Needs &need);
@@ -289,6 +297,13 @@ struct LinearFwdWs {
     ProductWs pw;
 };
 LinearFwdWs carve_linear_fwd(Carve &c, long long M, long long N, long long K, const Force &f);
+
+constexpr int SPLIT_ADD_BLOCKS = 1024;
+struct LinearFusedWs {
+    LinearFwdWs l;
+    int *bmax;  // block maxima of a split whole-tensor result
+};
+LinearFusedWs carve_linear_fused(Carve &c, long long M, long long N, long long K, const Force &f);
 
 struct LinearDxWs {
     int *estar;   // W's common exponent
@@ -375,6 +390,7 @@ size_t norm_bwd_ws(long long rows, long long cols);
 size_t linear_db_ws(long long rows, long long cols);
 size_t dropout_ws(long long rows, long long cols);
 size_t linear_fwd_ws(long long M, long long N, long long K, const Force &f);
+size_t linear_fused_ws(long long M, long long N, long long K, const Force &f);
 size_t linear_dx_ws(long long M, long long N, long long K, const Force &f);
 size_t linear_dw_ws(long long M, long long N, long long K, const Force &fw);
 size_t conv_fwd_ws(const ConvGeom &g, const Force &f);

@@ -83,6 +83,8 @@ EXPORTS = [
     ("ie_layer_norm_bwd_workspace", c_size_t, [c_int64, c_int64]),
     ("ie_layer_norm_bwd", c_int,
      [POINTER(ie_mat)] * 3 + [ie_scalar] + [POINTER(ie_mat)] * 3 + [c_void_p, c_size_t, c_void_p]),
+    ("ie_linear_fwd_fused_workspace", c_size_t, [c_int64, c_int64, c_int64]),
+    ("ie_linear_fwd_fused", c_int, [POINTER(ie_mat)] * 5 + [c_int, c_void_p, c_size_t, c_void_p]),
     ("ie_linear_bwd_db_workspace", c_size_t, [c_int64, c_int64]),
     ("ie_linear_bwd_db", c_int, [POINTER(ie_mat)] * 2 + [c_void_p, c_size_t, c_void_p]),
     ("ie_dropout_workspace", c_size_t, [c_int64, c_int64]),
@@ -394,6 +396,14 @@ def ie_layer_norm_bwd(dY: Mat, X: Mat, gamma: Mat | None, eps, dX: Mat | None, d
     p, b = ws.get(_ws_size("ie_layer_norm_bwd_workspace", x.rows, x.cols))
     _check(lib().ie_layer_norm_bwd(byref(dy), byref(x), _opt(gamma), ie_scalar(*eps), _opt(dX), _opt(dgamma),
                                    _opt(dbeta), p, b, _stream(ws.device)), "ie_layer_norm_bwd")
+
+
+def ie_linear_fwd_fused(X: Mat, W: Mat, bias: Mat | None, R: Mat | None, Y: Mat, act: int, ws: Workspace) -> None:
+    """Y = X . W^T + bias + R, rounded once, with the activation on the rounded mantissas."""
+    x, w, y = X.c(), W.c(), Y.c()
+    p, b = ws.get(_ws_size("ie_linear_fwd_fused_workspace", x.rows, w.rows, x.cols))
+    _check(lib().ie_linear_fwd_fused(byref(x), byref(w), _opt(bias), _opt(R), byref(y), int(act), p, b,
+                                     _stream(ws.device)), "ie_linear_fwd_fused")
 
 
 def ie_linear_bwd_db(dY: Mat, db: Mat, ws: Workspace) -> None:

@@ -238,3 +238,27 @@ def test_dropout_argument_errors():
     assert L.ie_linear_bwd_db(by(_mat(1, wide)), by(_mat(wide, 1, mant=512, exp=512)), 1, 1 << 40, None) == 6
     assert f(by(X), None, by(Y), by(d), None, big, None) == 4 and f(by(X), None, by(Y), by(d), 1, 256, None) == 4
     assert L.ie_dropout_workspace(-1, 4) == 0 and L.ie_dropout_workspace(4, 8) > 256
+
+
+def test_linear_fused_argument_errors():
+    """Shapes, bias and residual, activation, shared buffers, alignment and
+    workspaces are refused before anything is enqueued."""
+    L = ie.lib()
+    by, big, f = ctypes.byref, 1 << 30, L.ie_linear_fwd_fused
+    X, W, Y = _mat(4, 8), _mat(3, 8, mant=512, exp=512), _mat(4, 3, mant=1024, exp=1024)
+    b, D = _mat(3, 1, mant=2048, exp=2048), _mat(4, 3, mant=4096, exp=4096)
+    assert f(None, by(W), by(b), None, by(Y), 0, 1, big, None) == 1
+    assert f(by(X), by(_mat(3, 9, mant=512)), by(b), None, by(Y), 0, 1, big, None) == 2
+    assert f(by(X), by(W), by(_mat(4, 1)), None, by(Y), 0, 1, big, None) == 2
+    assert f(by(X), by(W), by(b), by(_mat(4, 4)), by(Y), 0, 1, big, None) == 2
+    assert f(by(X), by(W), by(b), by(D), by(_mat(4, 4, mant=1024, exp=1024)), 0, 1, big, None) == 2
+    assert f(by(X), by(W), by(b), by(D), by(Y), 2, 1, big, None) == 6
+    assert f(by(X), by(W), by(b), by(D), by(D), 0, 1, big, None) == 6
+    assert f(by(X), by(W), by(_mat(3, 1, mant=1024, exp=9)), None, by(Y), 0, 1, big, None) == 6
+    assert f(by(_mat(4, 8, mant=260)), by(W), by(b), None, by(Y), 0, 1, big, None) == 6
+    assert f(by(_mat(4, 70000)), by(_mat(3, 70000, mant=512)), by(b), None, by(Y), 0, 1, 1 << 40, None) == 6
+    assert f(by(X), by(W), by(b), None, by(Y), 0, None, big, None) == 4
+    assert f(by(X), by(W), by(b), None, by(Y), 0, 1, 256, None) == 4
+    assert f(by(X), by(W), None, None, by(Y), 0, 1, 16, None) == 4
+    size = L.ie_linear_fwd_fused_workspace
+    assert size(-1, 1, 1) == 0 and size(64, 128, 256) >= L.ie_linear_fwd_workspace(64, 128, 256)
