@@ -925,7 +925,7 @@ ie_status ie_layer_norm_fwd(const ie_mat *X, const ie_mat *gamma, const ie_mat *
     if (X->rows == 0 || X->cols == 0) return hip_status(launch_fill_i8(Y->exp, n_exps(Y), E_MIN, st));
     Carve c{(char *)ws, HEADER};
     const NormWs w = carve_norm_fwd(c, X->rows, X->cols);
-    const NormPlan pl = norm_plan(X->rows, X->cols, NORM_FWD_BLOCKS);
+    const NormPlan pl = norm_fwd_plan(X->rows, X->cols);
     NormFwd a;
     memset(&a, 0, sizeof a);
     a.x = X->mant;
@@ -942,6 +942,7 @@ ie_status ie_layer_norm_fwd(const ie_mat *X, const ie_mat *gamma, const ie_mat *
     a.q = mat_q(Y);
     a.bmax = w.bmax;
     a.n_bmax = pl.grid;
+    a.stat = (RowStat *)w.stat;
     a.flags = (uint32_t *)ws;
     a.mode = y_row ? NORM_ROWS : NORM_NEED;
     IE_TRY(launch_norm_fwd(a, pl, st));
@@ -996,11 +997,10 @@ ie_status ie_layer_norm_bwd(const ie_mat *dY, const ie_mat *X, const ie_mat *gam
     if (!dX && !dgamma && !dbeta) return IE_OK;
     Carve c{(char *)ws, HEADER};
     const NormWs w = carve_norm_bwd(c, M, N);
-    const NormPlan pl = norm_plan(M, N, NORM_BWD_BLOCKS);
+    const NormPlan pl = norm_bwd_plan(M, N);
     const bool cols = dgamma || dbeta;
     const bool dx_row = dX && dX->group == IE_GROUP_ROW;
-    IE_TRY(launch_exp_max2(dY->exp, n_exps(dY), w.c.top, gamma ? gamma->exp : nullptr, gamma ? n_exps(gamma) : 0,
-                           w.c.top + 1, st));
+    const int tops = n_tops(M, dY->group == IE_GROUP_ROW);
     NormBwd a;
     memset(&a, 0, sizeof a);
     a.dy = dY->mant;
@@ -1019,24 +1019,33 @@ ie_status ie_layer_norm_bwd(const ie_mat *dY, const ie_mat *X, const ie_mat *gam
     a.q = dX ? mat_q(dX) : 7;
     a.bmax = w.bmax;
     a.n_bmax = pl.grid;
+    a.gstat = (GradStat *)w.stat;
+    a.tops = w.c.tops;
+    a.n_tops = tops;
     a.top = w.c.top;
     a.pf = cols ? w.c.p64 : nullptr;
     a.pb = w.c.p32;
     a.flags = flags;
     if (M > 0) {
+        if (cols && tops) IE_TRY(launch_tops(dY->exp, M, w.c.tops, tops, st));
         a.mode = dx_row ? NORM_ROWS : NORM_NEED;
         IE_TRY(launch_norm_bwd(a, pl, st));
         if (dX && !dx_row) {
             a.mode = NORM_ROUND;
             IE_TRY(launch_norm_bwd(a, pl, st));
         }
-    } else if (dX) {
-        IE_TRY(launch_fill_i8(dX->exp, n_exps(dX), E_MIN, st));
+    } else {
+        // no rows: the sums are empty, and only their groups' exponents remain
+        for (const ie_mat *o : {dX, dgamma, dbeta})
+            if (o) IE_TRY(launch_fill_i8(o->exp, n_exps(o), E_MIN, st));
+        for (const ie_mat *o : {dgamma, dbeta})
+            if (o) IE_TRY(launch_fill_i8(o->mant, N, 0, st));
+        return IE_OK;
     }
     if (!cols) return IE_OK;
     const ColOut f = col_out(dgamma, w.c.p64, nullptr, -20, w.c.sums, w.c.need);
-    const ColOut b = col_out(dbeta, nullptr, w.c.p32, 0, w.c.sums + N, w.c.need + cdiv(N, 64));
-    return hip_status(launch_col_finish(f, b, M > 0 ? pl.grid : 0, (int)N, w.c.top, flags, st));
+    const ColOut b = col_out(dbeta, nullptr, w.c.p32, 0, w.c.sums + N, w.c.need + cdiv(N, 16));
+    return hip_status(launch_col_finish(f, b, pl.grid, (int)N, w.c.top, flags, st));
 }
 
 ie_status ie_linear_bwd_db(const ie_mat *dY, const ie_mat *db, void *ws, size_t ws_bytes, void *stream) {
@@ -1048,16 +1057,19 @@ ie_status ie_linear_bwd_db(const ie_mat *dY, const ie_mat *db, void *ws, size_t 
     if (ws_bytes < linear_db_ws(M, N)) return IE_ERR_WORKSPACE;
     hipStream_t st = (hipStream_t)stream;
     uint32_t *flags = (uint32_t *)ws;
-    if (N == 0) return hip_status(launch_fill_i8(db->exp, n_exps(db), E_MIN, st));
+    if (M == 0 || N == 0) {
+        IE_TRY(launch_fill_i8(db->mant, N, 0, st));
+        return hip_status(launch_fill_i8(db->exp, n_exps(db), E_MIN, st));
+    }
     Carve c{(char *)ws, HEADER};
     const ColWs w = carve_linear_db(c, M, N);
     const ColPlan pl = col_plan(M, N);
-    const bool row = dY->group == IE_GROUP_ROW;
-    IE_TRY(launch_exp_max2(dY->exp, n_exps(dY), w.top, nullptr, 0, nullptr, st));
-    if (M > 0) IE_TRY(launch_col_sum(dY->mant, dY->exp, row, w.top, M, (int)N, pl.chunk, pl.parts, w.p32, st));
+    const int row = dY->group == IE_GROUP_ROW, tops = n_tops(M, row);
+    if (tops) IE_TRY(launch_tops(dY->exp, M, w.tops, tops, st));
+    IE_TRY(launch_col_sum(dY->mant, dY->exp, row, M, (int)N, pl, w.tops, tops, w.top, w.p32, st));
     return hip_status(launch_col_finish(col_out(nullptr, nullptr, nullptr, 0, nullptr, nullptr),
-                                        col_out(db, nullptr, w.p32, 0, w.sums, w.need), M > 0 ? pl.parts : 0, (int)N,
-                                        w.top, flags, st));
+                                        col_out(db, nullptr, w.p32, 0, w.sums, w.need), pl.parts, (int)N, w.top, flags,
+                                        st));
 }
 
 // ---------------------------------------------------------------------------

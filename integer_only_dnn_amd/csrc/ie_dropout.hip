@@ -86,7 +86,6 @@ template <int T, int E>
 __global__ __launch_bounds__(T > 256 ? T : 256) void dropout_kernel(DropArgs p) {
     constexpr int BT = T > 256 ? T : 256, RPB = BT / T, W = E / 8;
     __shared__ int shi[BT / 64];
-    __shared__ double shd[BT / 64];
     const int t = threadIdx.x % T, slot = threadIdx.x / T, n = p.cols;
     Philox g;
     g.init(p);
@@ -99,30 +98,30 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void dropout_kernel(DropArgs p) 
         inv = pow2(-e);
         if (blockIdx.x == 0 && threadIdx.x == 0) p.ye[0] = (int8_t)e;
     }
-    double run = 0.0;
+    int run = 0;  // high word of the largest magnitude (NORM_NEED)
     for (long long r0 = (long long)blockIdx.x * RPB; r0 < p.rows; r0 += (long long)gridDim.x * RPB) {
         const long long row = min(r0 + slot, p.rows - 1);  // threads past the end repeat the last row
         const bool ok = r0 + slot < p.rows;
         const int8_t *x = p.x + row * n, *r = p.r ? p.r + row * n : nullptr;
         const double sx = p.scale * pow2((int)p.xe[p.x_row ? row : 0]);
         const double sr = r ? pow2((int)p.re[p.r_row ? row : 0]) : 0.0;
-        double y[W][8], mx = 0.0;
+        double y[W][8];
+        MaxMag mx;
 #pragma unroll
         for (int i = 0; i < W; ++i) {
             const int c = 8 * (i * T + t);
             if (c < n) {
                 drop8(p, g, x, r, c, (uint32_t)row, sx, sr, y[i]);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) mx = fmax(mx, fabs(y[i][k]));
+                for (int k = 0; k < 8; ++k) mx.add(y[i][k]);
             }
         }
         if (p.mode == NORM_NEED) {
-            run = fmax(run, mx);
+            run = max(run, mx.word());
             continue;
         }
         if (p.mode == NORM_ROWS) {
-            mx = row_reduce<T>(mx, Max{}, shd);
-            int e = max(E_MIN, need_f64(mx, p.q));
+            int e = max(E_MIN, need_word(row_reduce<T>(mx.word(), Max{}, shi), p.q));
             if (ok && t == 0) {
                 e = clamp_exp_flag(e, p.flags);
                 p.ye[row] = (int8_t)e;
@@ -137,8 +136,8 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void dropout_kernel(DropArgs p) 
         }
     }
     if (p.mode == NORM_NEED) {
-        run = row_reduce<BT>(run, Max{}, shd);
-        if (threadIdx.x == 0) p.bmax[blockIdx.x] = need_f64(run, p.q);
+        run = row_reduce<BT>(run, Max{}, shi);
+        if (threadIdx.x == 0) p.bmax[blockIdx.x] = need_word(run, p.q);
     }
 }
 
@@ -146,11 +145,11 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void dropout_kernel(DropArgs p) 
 // value and to round it (a whole-tensor result: once per launch).
 __global__ __launch_bounds__(1024) void dropout_long_kernel(DropArgs p) {
     __shared__ int shi[16];
-    __shared__ double shd[16];
     const int n = p.cols;
     Philox g;
     g.init(p);
-    double inv = 0.0, run = 0.0;
+    double inv = 0.0;
+    int run = 0;
     if (p.mode == NORM_ROUND) {
         int m = NEED_NONE;
         for (int i = threadIdx.x; i < p.n_bmax; i += 1024) m = max(m, p.bmax[i]);
@@ -165,18 +164,17 @@ __global__ __launch_bounds__(1024) void dropout_long_kernel(DropArgs p) {
         const double sr = r ? pow2((int)p.re[p.r_row ? row : 0]) : 0.0;
         double y[8];
         if (p.mode != NORM_ROUND) {
-            double mx = 0.0;
+            MaxMag mx;
             for (long long c = 8ll * threadIdx.x; c < n; c += 8192) {
                 drop8(p, g, x, r, (int)c, (uint32_t)row, sx, sr, y);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) mx = fmax(mx, fabs(y[k]));
+                for (int k = 0; k < 8; ++k) mx.add(y[k]);
             }
             if (p.mode == NORM_NEED) {
-                run = fmax(run, mx);
+                run = max(run, mx.word());
                 continue;
             }
-            mx = row_reduce<1024>(mx, Max{}, shd);
-            int e = max(E_MIN, need_f64(mx, p.q));
+            int e = max(E_MIN, need_word(row_reduce<1024>(mx.word(), Max{}, shi), p.q));
             if (threadIdx.x == 0) {
                 e = clamp_exp_flag(e, p.flags);
                 p.ye[row] = (int8_t)e;
@@ -189,8 +187,8 @@ __global__ __launch_bounds__(1024) void dropout_long_kernel(DropArgs p) {
         }
     }
     if (p.mode == NORM_NEED) {
-        run = row_reduce<1024>(run, Max{}, shd);
-        if (threadIdx.x == 0) p.bmax[blockIdx.x] = need_f64(run, p.q);
+        run = row_reduce<1024>(run, Max{}, shi);
+        if (threadIdx.x == 0) p.bmax[blockIdx.x] = need_word(run, p.q);
     }
 }
 

@@ -19,24 +19,17 @@ constexpr double ROUND_MAGIC = 6755399441055744.0;
 
 __device__ __forceinline__ double rint_magic(double v) { return (v + ROUND_MAGIC) - ROUND_MAGIC; }
 
-// Smallest exponent for the magnitude m >= 0 (NEED_NONE when zero): with m in
-// [2^x, 2^(x+1)) it is x - q + 1, plus one when the q bits below the leading
-// one are all ones (m rounds up to 2^q units).
-__device__ __forceinline__ int need_f64(double m, int q) {
-    if (m == 0.0) return NEED_NONE;
-    const int hi = __double2hiint(m);
-    const int ones = (1 << q) - 1;
-    return (hi >> 20) - 1023 - q + 1 + ((((hi & 0xfffff) >> (20 - q)) == ones) ? 1 : 0);
-}
-
 // The mantissa of v in units of 2^-k (inv = 2^k), half to even, as an int
 // whose low byte is the int8.
 __device__ __forceinline__ int mant_of(double v, double inv) {
     return __double2loint(__builtin_fma(v, inv, ROUND_MAGIC));
 }
 
+// The low bytes of four words.
 __device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
-    return (uint32_t)(a & 255) | (uint32_t)(b & 255) << 8 | (uint32_t)(c & 255) << 16 | (uint32_t)d << 24;
+    const uint32_t lo = __builtin_amdgcn_perm((uint32_t)b, (uint32_t)a, 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm((uint32_t)d, (uint32_t)c, 0x0c0c0400u);
+    return __builtin_amdgcn_perm(hi, lo, 0x05040100u);
 }
 
 // Four neighbours of a row from column c (any alignment); past n: zeros.
@@ -64,29 +57,115 @@ __device__ __forceinline__ void store4(int8_t *row, int c, int n, uint32_t w) {
 
 __device__ __forceinline__ int byte_of(uint32_t w, int k) { return (int)(int8_t)(w >> (8 * k)); }
 
-// A sum or maximum over the T threads of a row (T <= 64: within a wave; more:
-// the whole block), in every thread.  `sh` holds one value per wave.
-template <int T, class V, class F>
-__device__ __forceinline__ V row_reduce(V v, F f, V *sh) {
-#pragma unroll
-    for (int s = 1; s < (T < 64 ? T : 64); s <<= 1) v = f(v, __shfl_xor(v, s));
-    if constexpr (T > 64) {
-        __syncthreads();
-        if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
-        __syncthreads();
-        v = sh[0];
-        for (int i = 1; i < T / 64; ++i) v = f(v, sh[i]);
-    }
-    return v;
-}
-
 struct Add {
     template <class V>
     __device__ __forceinline__ V operator()(V a, V b) const { return a + b; }
 };
 struct Max {
-    __device__ __forceinline__ double operator()(double a, double b) const { return fmax(a, b); }
     __device__ __forceinline__ int operator()(int a, int b) const { return max(a, b); }
 };
+
+template <int CTRL>
+__device__ __forceinline__ int dpp_of(int v) { return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xf, 0xf, true); }
+template <int CTRL>
+__device__ __forceinline__ double dpp_of(double v) {
+    return __hiloint2double(dpp_of<CTRL>(__double2hiint(v)), dpp_of<CTRL>(__double2loint(v)));
+}
+
+// f over a lane and its partner 16 (or 32) lanes away: swapping the odd rows
+// of one copy with the even rows of another leaves both partners' values.
+template <int D, class F>
+__device__ __forceinline__ int swap_reduce(int v, F f) {
+    const auto r = D == 16 ? __builtin_amdgcn_permlane16_swap((uint32_t)v, (uint32_t)v, false, false)
+                           : __builtin_amdgcn_permlane32_swap((uint32_t)v, (uint32_t)v, false, false);
+    return f((int)r[0], (int)r[1]);
+}
+template <int D, class F>
+__device__ __forceinline__ double swap_reduce(double v, F f) {
+    const uint32_t h = (uint32_t)__double2hiint(v), l = (uint32_t)__double2loint(v);
+    const auto a = D == 16 ? __builtin_amdgcn_permlane16_swap(h, h, false, false)
+                           : __builtin_amdgcn_permlane32_swap(h, h, false, false);
+    const auto b = D == 16 ? __builtin_amdgcn_permlane16_swap(l, l, false, false)
+                           : __builtin_amdgcn_permlane32_swap(l, l, false, false);
+    return f(__hiloint2double((int)a[0], (int)b[0]), __hiloint2double((int)a[1], (int)b[1]));
+}
+
+// A sum or maximum over groups of T <= 64 lanes, in every lane of the group
+// (all lanes active): neighbours, pairs, the mirrored half row, the mirrored
+// row, then rows.  Data-parallel moves and swaps, no trip through LDS.
+template <int T, class V, class F>
+__device__ __forceinline__ V lane_reduce(V v, F f) {
+    if constexpr (T >= 2) v = f(v, dpp_of<0xB1>(v));    // lanes 1 0 3 2
+    if constexpr (T >= 4) v = f(v, dpp_of<0x4E>(v));    // lanes 2 3 0 1
+    if constexpr (T >= 8) v = f(v, dpp_of<0x141>(v));   // half row mirrored
+    if constexpr (T >= 16) v = f(v, dpp_of<0x140>(v));  // row mirrored
+    if constexpr (T >= 32) v = swap_reduce<16>(v, f);
+    if constexpr (T >= 64) v = swap_reduce<32>(v, f);
+    return v;
+}
+
+// The same over T threads: within a wave, or over a whole block of T; `sh`
+// holds a value per wave.
+template <int T, class V, class F>
+__device__ __forceinline__ V row_reduce(V v, F f, V *sh) {
+    v = lane_reduce<(T < 64 ? T : 64)>(v, f);
+    if constexpr (T > 64) {
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = sh[0];
+#pragma unroll
+        for (int i = 1; i < T / 64; ++i) v = f(v, sh[i]);
+    }
+    return v;
+}
+
+// Largest magnitude of a run of values, as the high word of its double: the
+// need of a magnitude takes its exponent and leading bits only.  The largest
+// signed word is the largest positive value's, the largest unsigned one the
+// most negative value's.
+struct MaxMag {
+    int hi = 0;
+    uint32_t neg = 0;
+    __device__ __forceinline__ void add(double v) {
+        const int h = __double2hiint(v);
+        hi = max(hi, h);
+        neg = max(neg, (uint32_t)h);
+    }
+    __device__ __forceinline__ int word() const { return max(hi, (int)neg < 0 ? (int)(neg & 0x7fffffffu) : 0); }
+};
+
+// Smallest exponent for the magnitude whose high word is w (NEED_NONE when
+// zero): with m in [2^x, 2^(x+1)) it is x - q + 1, plus one when the q bits
+// below the leading one are all ones (m rounds up to 2^q units).
+__device__ __forceinline__ int need_word(int w, int q) {
+    if (w == 0) return NEED_NONE;
+    const int ones = (1 << q) - 1;
+    return (w >> 20) - 1023 - q + 1 + ((((w & 0xfffff) >> (20 - q)) == ones) ? 1 : 0);
+}
+
+// A run of CH = 4, 8 or 16 mantissas of a row from column c, four to a word;
+// past n: zeros.
+template <int CH>
+__device__ __forceinline__ void load_run(const int8_t *row, int c, int n, uint32_t *w) {
+#pragma unroll
+    for (int k = 0; k < CH / 4; ++k) w[k] = 0;
+    if (c + CH <= n) {
+        __builtin_memcpy(w, row + c, CH);
+    } else if (c < n) {
+#pragma unroll
+        for (int k = 0; k < CH / 4; ++k) w[k] = load4(row, c + 4 * k, n);
+    }
+}
+
+template <int CH>
+__device__ __forceinline__ void store_run(int8_t *row, int c, int n, const uint32_t *w) {
+    if (c + CH <= n) {
+        __builtin_memcpy(row + c, w, CH);
+    } else if (c < n) {
+#pragma unroll
+        for (int k = 0; k < CH / 4; ++k) store4(row, c + 4 * k, n, w[k]);
+    }
+}
 
 }  // namespace ie

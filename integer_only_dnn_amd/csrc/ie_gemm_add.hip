@@ -49,9 +49,10 @@ struct EpiAdd {
                                            int tile_n, int M, int N, int TM) const {
         constexpr int BM = 64 * MI, BN = 64 * NI, RP = BN + 4;  // RP: pitch of the residual tile
         const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
-        double *cs = (double *)lds, *bs = cs + BN, *red = bs + BN;  // column scales, bias, maxima [2][BM]
+        double *cs = (double *)lds, *bs = cs + BN;  // column scales, bias
+        int *red = (int *)(bs + BN);               // maxima [2][BM]
         int8_t *rt = (int8_t *)(red + 2 * BM), *out = rt + BM * RP;
-        static_assert(16 * BN + 16 * BM + BM * RP + BM * (BN * 2 + 16) <= TileLds<LD_K, LD_K, MI, NI, false>::value,
+        static_assert(16 * BN + 8 * BM + BM * RP + BM * (BN * 2 + 16) <= TileLds<LD_K, LD_K, MI, NI, false>::value,
                       "epilogue exceeds the tile's LDS");
         static_assert(BM * RP % 16 == 0, "staging alignment");
         __syncthreads();  // every wave is done with the last stage
@@ -84,7 +85,8 @@ struct EpiAdd {
         }
         __syncthreads();
 
-        double y[MI][NI][16], sx[MI], sr[MI], mx[MI];
+        double y[MI][NI][16], sx[MI], sr[MI];
+        MaxMag mx[MI];
         int row[MI];
 #pragma unroll
         for (int a = 0; a < MI; ++a) {
@@ -92,7 +94,6 @@ struct EpiAdd {
             const int m = m0 + row[a];
             sx[a] = m < M ? pow2((int)e.xe[e.x_row ? m : 0]) : 0.0;
             sr[a] = e.r && m < M ? pow2((int)e.re[e.r_row ? m : 0]) : 0.0;
-            mx[a] = 0.0;
         }
 #pragma unroll
         for (int b = 0; b < NI; ++b)
@@ -108,7 +109,7 @@ struct EpiAdd {
                         double v = __builtin_fma((double)acc[a][b][4 * h + k], sx[a] * cs[c + k], bs[c + k]);
                         if (e.r) v = __builtin_fma((double)byte_of(r4, k), sr[a], v);
                         y[a][b][4 * h + k] = v;
-                        mx[a] = fmax(mx[a], fabs(v));
+                        mx[a].add(v);
                     }
                 }
             }
@@ -118,13 +119,13 @@ struct EpiAdd {
         if constexpr (RG) {
 #pragma unroll
             for (int a = 0; a < MI; ++a) {
-                mx[a] = fmax(mx[a], __shfl_xor(mx[a], 32));
-                if (lane < 32) red[wn * BM + row[a]] = mx[a];
+                const int m = swap_reduce<32>(mx[a].word(), Max{});
+                if (lane < 32) red[wn * BM + row[a]] = m;
             }
             __syncthreads();
 #pragma unroll
             for (int a = 0; a < MI; ++a) {
-                const int need = need_f64(fmax(red[row[a]], red[BM + row[a]]), e.q), m = m0 + row[a];
+                const int need = need_word(max(red[row[a]], red[BM + row[a]]), e.q), m = m0 + row[a];
                 const bool first = lane < 32 && wn == 0 && m < M;
                 if constexpr (DI) {
                     int ex = max(E_MIN, need);
@@ -139,14 +140,13 @@ struct EpiAdd {
                 }
             }
         } else {
-            double t = 0.0;
+            int t = 0;
 #pragma unroll
-            for (int a = 0; a < MI; ++a) t = fmax(t, m0 + row[a] < M ? mx[a] : 0.0);
-#pragma unroll
-            for (int s = 1; s < 64; s <<= 1) t = fmax(t, __shfl_xor(t, s));
+            for (int a = 0; a < MI; ++a) t = max(t, m0 + row[a] < M ? mx[a].word() : 0);
+            t = lane_reduce<64>(t, Max{});
             if (lane == 0) red[wave] = t;
             __syncthreads();
-            const int need = need_f64(fmax(fmax(red[0], red[1]), fmax(red[2], red[3])), e.q);
+            const int need = need_word(max(max(red[0], red[1]), max(red[2], red[3])), e.q);
             double in;
             if constexpr (DI) {
                 const int ex = clamp_exp_flag(max(E_MIN, need), e.flags);
@@ -241,8 +241,8 @@ __device__ __forceinline__ double split_value(const AddEpi &e, const int *p, int
 __global__ __launch_bounds__(1024) void split_add_kernel(AddEpi e, const int *partial, int splits, long long stride,
                                                          int M, int N, int mode, int *bmax, int n_bmax) {
     __shared__ int shi[16];
-    __shared__ double shd[16];
-    double inv = 0.0, run = 0.0;
+    double inv = 0.0;
+    int run = 0;
     if (mode == NORM_ROUND) {
         int m = NEED_NONE;
         for (int i = threadIdx.x; i < n_bmax; i += 1024) m = max(m, bmax[i]);
@@ -254,15 +254,14 @@ __global__ __launch_bounds__(1024) void split_add_kernel(AddEpi e, const int *pa
     for (int m = blockIdx.x; m < M; m += gridDim.x) {
         const double sx = pow2((int)e.xe[e.x_row ? m : 0]), sr = e.r ? pow2((int)e.re[e.r_row ? m : 0]) : 0.0;
         if (mode != NORM_ROUND) {
-            double mx = 0.0;
+            MaxMag mx;
             for (long long n = threadIdx.x; n < N; n += 1024)
-                mx = fmax(mx, fabs(split_value(e, partial, splits, stride, m, (int)n, N, sx, sr)));
+                mx.add(split_value(e, partial, splits, stride, m, (int)n, N, sx, sr));
             if (mode == NORM_NEED) {
-                run = fmax(run, mx);
+                run = max(run, mx.word());
                 continue;
             }
-            mx = row_reduce<1024>(mx, Max{}, shd);
-            int ex = max(E_MIN, need_f64(mx, e.q));
+            int ex = max(E_MIN, need_word(row_reduce<1024>(mx.word(), Max{}, shi), e.q));
             if (threadIdx.x == 0) {
                 ex = clamp_exp_flag(ex, e.flags);
                 e.ye[m] = (int8_t)ex;
@@ -275,8 +274,8 @@ __global__ __launch_bounds__(1024) void split_add_kernel(AddEpi e, const int *pa
         }
     }
     if (mode == NORM_NEED) {
-        run = row_reduce<1024>(run, Max{}, shd);
-        if (threadIdx.x == 0) bmax[blockIdx.x] = need_f64(run, e.q);
+        run = row_reduce<1024>(run, Max{}, shi);
+        if (threadIdx.x == 0) bmax[blockIdx.x] = need_word(run, e.q);
     }
 }
 

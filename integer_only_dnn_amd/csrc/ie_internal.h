@@ -245,6 +245,14 @@ struct NormVec {
 // whole result; NEED leaves the blocks' needs in bmax, ROUND (the rows again)
 // rounds to the largest of them.
 enum NormMode { NORM_ROWS = 0, NORM_NEED = 1, NORM_ROUND = 2 };
+// A row's sum of mantissas and 1 / sqrt(T), and in the backward pass its sums
+// G1 and G2 2^-40; kept for the second pass of a whole-tensor result.
+struct RowStat {
+    double s, r;
+};
+struct GradStat {
+    double s, r, g1, g2;
+};
 struct NormFwd {
     const int8_t *x, *xe;
     int x_row;
@@ -257,6 +265,7 @@ struct NormFwd {
     int q, mode;
     int *bmax;
     int n_bmax;
+    RowStat *stat;
     uint32_t *flags;
 };
 struct NormBwd {
@@ -273,16 +282,21 @@ struct NormBwd {
     int q, mode;
     int *bmax;
     int n_bmax;
-    const int *top;  // largest exponents of dY and gamma
-    long long *pf;   // [grid][cols] partial sums of dgamma and dbeta, or nullptr
+    GradStat *gstat;
+    const int *tops;  // [n_tops] largest exponents of parts of dY (none: every block finds the largest)
+    int n_tops;
+    int *top;         // the largest exponent of dY
+    long long *pf;    // [grid][cols] partial sums of dgamma and dbeta, or nullptr
     int *pb;
     uint32_t *flags;
 };
 hipError_t launch_norm_fwd(const NormFwd &a, const NormPlan &pl, hipStream_t st);
 hipError_t launch_norm_bwd(const NormBwd &a, const NormPlan &pl, hipStream_t st);
-// pb[part][col] = sum of the part's rows of dY, re-expressed at *top.
-hipError_t launch_col_sum(const int8_t *dy, const int8_t *e, int e_row, const int *top, long long rows, int cols,
-                          int chunk, int parts, int *pb, hipStream_t st);
+hipError_t launch_tops(const int8_t *e, long long n, int *tops, int n_tops, hipStream_t st);
+// pb[part][col] = sum of the part's rows of dY, re-expressed at the largest
+// exponent, which goes to *top.
+hipError_t launch_col_sum(const int8_t *dy, const int8_t *e, int e_row, long long rows, int cols, ColPlan pl,
+                          const int *tops, int n_tops, int *top, int *pb, hipStream_t st);
 // A vector of column sums: its partial sums (64 or 32 bits) at exponent
 // base + *top, rounded into m / e (per: one exponent per channel) at width
 // q + 1.  m == nullptr: not wanted.

@@ -28,82 +28,197 @@
 
 namespace ie {
 
-struct RowStat {
-    double s, r;  // sum of the mantissas, 1 / sqrt(T)
+// The columns of a row that a thread holds when T threads share it, E each:
+// runs of CH neighbours (as wide as one load can be), run i of thread t from
+// column CH (i T + t).  Rows are read whole runs at a time: a run that crosses
+// the row's end takes in the next row's first bytes, one past it the row's
+// first ones, and `mask` clears both; only at the matrix's last rows, where
+// nothing may follow, is such a run read byte by byte.
+template <int T, int E>
+struct Cols {
+    static constexpr int CH = E % 16 == 0 ? 16 : E % 8 == 0 ? 8 : 4, NC = E / CH, W = E / 4;
+    int t, n;
+    bool exact;  // every run of every thread lies inside the row
+    int at[NC];
+    uint32_t mask[W];
+    static __device__ __forceinline__ int col(int j, int t) { return CH * (j / CH * T + t) + j % CH; }
+    __device__ __forceinline__ int col(int j) const { return col(j, t); }
+    __device__ __forceinline__ void init(int t_, int n_) {
+        t = t_;
+        n = n_;
+        exact = n == T * E;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) at[i] = CH * (i * T + t) < n ? CH * (i * T + t) : 0;
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            const int left = n - col(4 * i);
+            mask[i] = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+        }
+    }
+    // `whole`: a run may be read past the row's end (CH more rows follow, or
+    // no run crosses it)
+    __device__ __forceinline__ void load(const int8_t *row, bool whole, uint32_t (&w)[W]) const {
+        if (whole) {
+#pragma unroll
+            for (int i = 0; i < NC; ++i) __builtin_memcpy(w + i * CH / 4, row + at[i], CH);
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; ++i) w[i] = col(4 * i) < n ? load4(row, col(4 * i), n) : 0u;
+        }
+    }
+    __device__ __forceinline__ void clear(uint32_t (&w)[W]) const {
+        if (exact) return;
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] &= mask[i];
+    }
+    __device__ __forceinline__ void store(int8_t *row, const uint32_t (&w)[W]) const {
+#pragma unroll
+        for (int i = 0; i < NC; ++i) store_run<CH>(row, CH * (i * T + t), n, w + i * CH / 4);
+    }
 };
 
 // The statistics of a row held four mantissas to a word (zeros past its end).
 template <int T, int W>
-__device__ __forceinline__ RowStat row_stat(const uint32_t (&w)[W], int n, double n2eps, int eps_e, int e, int *shi) {
+__device__ __forceinline__ RowStat row_stat(const uint32_t (&w)[W], int n, double n2eps, int eps_e, int e, int2 *sh) {
     int s = 0, q = 0;
 #pragma unroll
     for (int i = 0; i < W; ++i) {
         s = __builtin_amdgcn_sdot4((int)w[i], 0x01010101, s, false);
         q = __builtin_amdgcn_sdot4((int)w[i], (int)w[i], q, false);
     }
-    s = row_reduce<T>(s, Add{}, shi);
-    q = row_reduce<T>(q, Add{}, shi);
-    const double sd = (double)s, v = (double)n * (double)q - sd * sd;  // exact: V < 2^43
+    s = lane_reduce<(T < 64 ? T : 64)>(s, Add{});
+    q = lane_reduce<(T < 64 ? T : 64)>(q, Add{});
+    if constexpr (T > 64) {
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = make_int2(s, q);
+        __syncthreads();
+        s = q = 0;
+#pragma unroll
+        for (int i = 0; i < T / 64; ++i) {
+            s += sh[i].x;
+            q += sh[i].y;
+        }
+    }
+    const double sd = (double)s, v = __builtin_fma((double)n, (double)q, -sd * sd);  // exact: below 2^43
     const double t = v + n2eps * pow2(eps_e - 2 * e);
     return RowStat{sd, t > 0.0 ? 1.0 / __builtin_sqrt(t) : 0.0};
 }
 
-// The value of channel c of a parameter vector.
-__device__ __forceinline__ double channel(const NormVec &v, int c) {
-    return (double)v.m[c] * pow2((int)v.e[v.per ? c : 0]);
+// The values of four channels of a parameter vector from column c.
+__device__ __forceinline__ void channel4(const NormVec &v, int c, int n, double absent, double (&o)[4]) {
+    if (!v.m) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = c + k < n ? absent : 0.0;
+        return;
+    }
+    const uint32_t m = load4(v.m, c, n), e = v.per ? load4(v.e, c, n) : (uint32_t)(uint8_t)v.e[0] * 0x01010101u;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] = (double)byte_of(m, k) * pow2(byte_of(e, k));
 }
 
-// T threads per row, E elements per thread: thread t holds columns
-// 4 (i T + t) + k, i < E / 4, k < 4.
+// The exponent of a whole-tensor result from the blocks' needs, by a block of
+// BT threads; block 0 stores it.
+template <int BT>
+__device__ __forceinline__ int whole_exp(const int *bmax, int n, int8_t *oe, uint32_t *flags, int *sh) {
+    int m = NEED_NONE;
+    for (int i = threadIdx.x; i < n; i += BT) m = max(m, bmax[i]);
+    m = row_reduce<BT>(m, Max{}, sh);
+    const int e = clamp_exp_flag(max(E_MIN, m), flags);
+    if (blockIdx.x == 0 && threadIdx.x == 0) oe[0] = (int8_t)e;
+    return e;
+}
+
+template <int T>
+constexpr int norm_block() {
+    return T > 256 ? T : 256;
+}
+
+// T threads per row, E elements per thread.  gamma and beta stay in registers
+// (E <= 12, or when a block holds one row) or in LDS; the next row's loads are
+// in flight while a row is computed.
 template <int T, int E>
-__global__ __launch_bounds__(T > 256 ? T : 256) void norm_fwd_kernel(NormFwd p) {
-    constexpr int BT = T > 256 ? T : 256, RPB = BT / T, W = E / 4;
+__global__ __launch_bounds__(norm_block<T>()) void norm_fwd_kernel(NormFwd p) {
+    using C = Cols<T, E>;
+    constexpr int BT = norm_block<T>(), RPB = BT / T, W = E / 4;
+    constexpr bool LDSV = T <= 64 && E > 12;
+    __shared__ int2 sh2[BT / 64];
     __shared__ int shi[BT / 64];
-    __shared__ double shd[BT / 64];
+    __shared__ double2 gb[LDSV ? T * E : 1];
     const int t = threadIdx.x % T, slot = threadIdx.x / T, n = p.cols;
-    double gam[E], bet[E];
+    const long long step = (long long)gridDim.x * RPB;
+    C cols;
+    cols.init(t, n);
+    uint32_t w[W], next[W];
+    int e = 0, e_next = 0;
+    // the rows of a trip from r0; past the end: the last row again
+    auto fetch = [&](long long r0) {
+        const long long r = min(r0 + slot, p.rows - 1);
+        cols.load(p.x + r * n, n % C::CH == 0 || r0 + RPB + C::CH <= p.rows, next);
+        e_next = p.xe[p.x_row ? r : 0];
+    };
+    fetch((long long)blockIdx.x * RPB);
+    double gam[LDSV ? 1 : E], bet[LDSV ? 1 : E];
+    if constexpr (LDSV) {
+        // element-major, so that a row's threads read neighbours
+        for (int x = threadIdx.x; x < T * W; x += BT) {
+            const int j = 4 * (x / T), tt = x % T;
+            double g[4], b[4];
+            channel4(p.gamma, C::col(j, tt), n, 1.0, g);
+            channel4(p.beta, C::col(j, tt), n, 0.0, b);
 #pragma unroll
-    for (int i = 0; i < W; ++i)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int c = 4 * (i * T + t) + k;
-            // past the row both are zero, so y is
-            gam[4 * i + k] = c < n ? (p.gamma.m ? channel(p.gamma, c) : 1.0) : 0.0;
-            bet[4 * i + k] = c < n && p.beta.m ? channel(p.beta, c) : 0.0;
+            for (int k = 0; k < 4; ++k) gb[(j + k) * T + tt] = make_double2(g[k], b[k]);
         }
-    double inv = 0.0;  // of a whole-tensor result
-    if (p.mode == NORM_ROUND) {
-        int m = NEED_NONE;
-        for (int i = threadIdx.x; i < p.n_bmax; i += BT) m = max(m, p.bmax[i]);
-        m = row_reduce<BT>(m, Max{}, shi);
-        const int e = clamp_exp_flag(max(E_MIN, m), p.flags);
-        inv = pow2(-e);
-        if (blockIdx.x == 0 && threadIdx.x == 0) p.oe[0] = (int8_t)e;
+        __syncthreads();
+    } else {
+#pragma unroll
+        for (int j = 0; j < E; j += 4) {
+            double g[4], b[4];
+            channel4(p.gamma, cols.col(j), n, 1.0, g);
+            channel4(p.beta, cols.col(j), n, 0.0, b);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) gam[j + k] = g[k], bet[j + k] = b[k];
+        }
     }
-    double run = 0.0;  // largest magnitude of this thread's rows (NORM_NEED)
-    for (long long r0 = (long long)blockIdx.x * RPB; r0 < p.rows; r0 += (long long)gridDim.x * RPB) {
+    double inv = 0.0;  // of a whole-tensor result
+    if (p.mode == NORM_ROUND) inv = pow2(-whole_exp<BT>(p.bmax, p.n_bmax, p.oe, p.flags, shi));
+    MaxMag run;  // of this thread's rows (NORM_NEED)
+    for (long long r0 = (long long)blockIdx.x * RPB; r0 < p.rows; r0 += step) {
         const long long row = r0 + slot;
         const bool ok = row < p.rows;
-        const int8_t *x = p.x + (ok ? row : 0) * n;
-        uint32_t w[W];
 #pragma unroll
-        for (int i = 0; i < W; ++i) w[i] = ok ? load4(x, 4 * (i * T + t), n) : 0u;
-        const int e = p.xe[p.x_row && ok ? row : 0];
-        const RowStat st = row_stat<T>(w, n, p.n2eps, p.eps_e, e, shi);
-        double y[E], mx = 0.0;
+        for (int i = 0; i < W; ++i) w[i] = next[i];
+        e = e_next;
+        if (r0 + step < p.rows) fetch(r0 + step);
+        if constexpr (LDSV) asm volatile("" ::: "memory");  // gamma and beta stay in LDS
+        cols.clear(w);
+        RowStat st;
+        if (p.mode == NORM_ROUND) {
+            st = p.stat[ok ? row : p.rows - 1];
+        } else {
+            st = row_stat<T>(w, n, p.n2eps, p.eps_e, e, sh2);
+            if (p.mode == NORM_NEED && ok && t == 0) p.stat[row] = st;
+        }
+        double y[E];
+        MaxMag mx;
 #pragma unroll
         for (int j = 0; j < E; ++j) {
             const double d = __builtin_fma((double)byte_of(w[j / 4], j % 4), (double)n, -st.s);
-            y[j] = (d * st.r) * gam[j] + bet[j];
-            mx = fmax(mx, fabs(y[j]));
+            // past the row gamma and beta are zero, and so is y
+            if constexpr (LDSV) {
+                const double2 v = gb[j * T + t];
+                y[j] = (d * st.r) * v.x + v.y;
+            } else {
+                y[j] = (d * st.r) * gam[j] + bet[j];
+            }
+            mx.add(y[j]);
         }
         if (p.mode == NORM_NEED) {
-            if (ok) run = fmax(run, mx);
+                run.hi = max(run.hi, mx.hi);
+            run.neg = max(run.neg, mx.neg);
             continue;
         }
         if (p.mode == NORM_ROWS) {
-            mx = row_reduce<T>(mx, Max{}, shd);
-            int ex = max(E_MIN, need_f64(mx, p.q));
+            int ex = max(E_MIN, need_word(row_reduce<T>(mx.word(), Max{}, shi), p.q));
             if (ok && t == 0) {
                 ex = clamp_exp_flag(ex, p.flags);
                 p.oe[row] = (int8_t)ex;
@@ -112,104 +227,175 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void norm_fwd_kernel(NormFwd p) 
         }
         if (!ok) continue;
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-            const int c = 4 * (i * T + t);
-            if (c < n)
-                store4(p.out + row * n, c, n,
-                       pack4(mant_of(y[4 * i], inv), mant_of(y[4 * i + 1], inv), mant_of(y[4 * i + 2], inv),
-                             mant_of(y[4 * i + 3], inv)));
-        }
+        for (int i = 0; i < W; ++i)
+            w[i] = pack4(mant_of(y[4 * i], inv), mant_of(y[4 * i + 1], inv), mant_of(y[4 * i + 2], inv),
+                         mant_of(y[4 * i + 3], inv));
+        cols.store(p.out + row * n, w);
     }
     if (p.mode == NORM_NEED) {
-        run = row_reduce<BT>(run, Max{}, shd);
-        if (threadIdx.x == 0) p.bmax[blockIdx.x] = need_f64(run, p.q);
+        const int m = row_reduce<BT>(run.word(), Max{}, shi);
+        if (threadIdx.x == 0) p.bmax[blockIdx.x] = need_word(m, p.q);
     }
 }
 
-// Backward: the same layout.  NORM_NEED and NORM_ROWS also add up the columns
-// of dgamma and dbeta (p.pf, p.pb: one row of partial sums per block).
+// The largest of n exponents, by a block of BT threads.
+template <int BT>
+__device__ __forceinline__ int max_exp(const int8_t *e, long long n, int *sh) {
+    int m = E_MIN;
+    for (long long c = 16ll * threadIdx.x; c < n; c += 16ll * BT) {
+        uint32_t w[4] = {0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u};
+        if (c + 16 <= n) {
+            __builtin_memcpy(w, e + c, 16);
+        } else {
+            for (int k = 0; c + k < n; ++k) m = max(m, (int)e[c + k]);
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) m = max(m, byte_of(w[k / 4], k % 4));
+    }
+    return row_reduce<BT>(m, Max{}, sh);
+}
+
+// The largest exponent of dY's rows: found by this block, or the largest of
+// tops_kernel's.
+template <int BT>
+__device__ __forceinline__ int top_exp(const int8_t *e, int e_row, long long rows, const int *tops, int n_tops,
+                                       int *sh) {
+    if (!e_row) return e[0];
+    if (!n_tops) return max_exp<BT>(e, rows, sh);
+    int m = E_MIN;
+    for (int i = 0; i < n_tops; ++i) m = max(m, tops[i]);
+    return m;
+}
+
+// Rows of up to 64 threads share blocks of 512 in the backward pass: the
+// block's partial column sums are one row of p.pf / p.pb whatever its size.
+template <int T>
+constexpr int grad_block() {
+    return T > 64 ? T : 512;
+}
+
+// Backward: NORM_NEED and NORM_ROWS also add up the columns of dgamma and
+// dbeta (p.pf, p.pb: one row of partial sums per block).
 template <int T, int E>
-__global__ __launch_bounds__(T > 256 ? T : 256) void norm_bwd_kernel(NormBwd p) {
-    constexpr int BT = T > 256 ? T : 256, RPB = BT / T, W = E / 4;
+__global__ __launch_bounds__(grad_block<T>()) __attribute__((amdgpu_waves_per_eu(T > 512 ? 4 : 2)))
+void norm_bwd_kernel(NormBwd p) {
+    using C = Cols<T, E>;
+    constexpr int BT = grad_block<T>(), RPB = BT / T, W = E / 4;
+    __shared__ int2 sh2[BT / 64];
     __shared__ int shi[BT / 64];
     __shared__ double shd[BT / 64];
     const int t = threadIdx.x % T, slot = threadIdx.x / T, n = p.cols;
-    const int gtop = p.gamma.m ? p.top[1] : 0;  // exponent of the re-expressed gamma
-    const int dtop = p.top[0];                  // largest exponent of dY
     const bool sums = p.pf && p.mode != NORM_ROUND, grad = p.out != nullptr;
+    const long long step = (long long)gridDim.x * RPB;
+    C cols;
+    cols.init(t, n);
+    uint32_t w[W], v[W], w_next[W], v_next[W];
+    int ex = 0, ey = 0, ex_next = 0, ey_next = 0;
+    auto fetch = [&](long long r0) {
+        const long long r = min(r0 + slot, p.rows - 1);
+        const bool whole = n % C::CH == 0 || r0 + RPB + C::CH <= p.rows;
+        cols.load(p.x + r * n, whole, w_next);
+        cols.load(p.dy + r * n, whole, v_next);
+        ex_next = p.xe[p.x_row ? r : 0];
+        ey_next = p.dye[p.dy_row ? r : 0];
+    };
+    fetch((long long)blockIdx.x * RPB);
+    // the largest exponents of dY and of gamma's channels
+    const int dtop = sums ? top_exp<BT>(p.dye, p.dy_row, p.rows, p.tops, p.n_tops, shi) : 0;
+    if (sums && blockIdx.x == 0 && threadIdx.x == 0) *p.top = dtop;
+    int gtop = 0;
+    if (p.gamma.m) gtop = p.gamma.per ? max_exp<BT>(p.gamma.e, n, shi) : p.gamma.e[0];
+    uint32_t gw[W];   // gamma re-expressed, four mantissas to a word
     double gam[E];
 #pragma unroll
-    for (int i = 0; i < W; ++i)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int c = 4 * (i * T + t) + k;
-            double v = c < n ? 1.0 : 0.0;
-            if (p.gamma.m && c < n) v = (double)rne_shift32(p.gamma.m[c], gtop - (int)p.gamma.e[p.gamma.per ? c : 0]);
-            gam[4 * i + k] = v;
+    for (int i = 0; i < W; ++i) {
+        const int c = cols.col(4 * i);
+        uint32_t m = 0x01010101u & cols.mask[i];
+        if (p.gamma.m) {
+            m = load4(p.gamma.m, c, n);
+            if (p.gamma.per) {
+                const uint32_t e = load4(p.gamma.e, c, n);
+                m = pack4(rne_shift32(byte_of(m, 0), gtop - byte_of(e, 0)), rne_shift32(byte_of(m, 1), gtop - byte_of(e, 1)),
+                          rne_shift32(byte_of(m, 2), gtop - byte_of(e, 2)), rne_shift32(byte_of(m, 3), gtop - byte_of(e, 3)));
+            }
         }
-    double inv = 0.0;
-    if (p.mode == NORM_ROUND) {
-        int m = NEED_NONE;
-        for (int i = threadIdx.x; i < p.n_bmax; i += BT) m = max(m, p.bmax[i]);
-        m = row_reduce<BT>(m, Max{}, shi);
-        const int e = clamp_exp_flag(max(E_MIN, m), p.flags);
-        inv = pow2(-e);
-        if (blockIdx.x == 0 && threadIdx.x == 0) p.oe[0] = (int8_t)e;
+        gw[i] = m;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) gam[4 * i + k] = (double)byte_of(m, k);
     }
+    double inv = 0.0;
+    if (p.mode == NORM_ROUND) inv = pow2(-whole_exp<BT>(p.bmax, p.n_bmax, p.oe, p.flags, shi));
     double af[E];
     int ab[E];
 #pragma unroll
     for (int j = 0; j < E; ++j) af[j] = 0.0, ab[j] = 0;
-    double run = 0.0;
-    for (long long r0 = (long long)blockIdx.x * RPB; r0 < p.rows; r0 += (long long)gridDim.x * RPB) {
+    int run = 0;  // high word of the largest magnitude (NORM_NEED)
+    for (long long r0 = (long long)blockIdx.x * RPB; r0 < p.rows; r0 += step) {
         const long long row = r0 + slot;
         const bool ok = row < p.rows;
-        const long long off = (ok ? row : 0) * n;
-        uint32_t w[W], v[W];
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-            w[i] = ok ? load4(p.x + off, 4 * (i * T + t), n) : 0u;
-            v[i] = ok ? load4(p.dy + off, 4 * (i * T + t), n) : 0u;
+        for (int i = 0; i < W; ++i) w[i] = w_next[i], v[i] = v_next[i];
+        ex = ex_next;
+        ey = ey_next;
+        if (r0 + step < p.rows) fetch(r0 + step);
+        cols.clear(w);
+        cols.clear(v);
+        GradStat gs;
+        if (p.mode == NORM_ROUND) {
+            gs = p.gstat[ok ? row : p.rows - 1];
+        } else {
+            const RowStat st = row_stat<T>(w, n, p.n2eps, p.eps_e, ex, sh2);
+            gs.s = st.s;
+            gs.r = st.r;
         }
-        const int ex = p.xe[p.x_row && ok ? row : 0], ey = p.dye[p.dy_row && ok ? row : 0];
-        const RowStat st = row_stat<T>(w, n, p.n2eps, p.eps_e, ex, shi);
-        const double r20 = st.r * 1048576.0;  // h 2^20 = d (r 2^20)
-        double f[E], g[E], g1 = 0.0, g2 = 0.0;
-        const int sh = dtop - ey;
+        const double r20 = gs.r * 1048576.0;  // h 2^20 = d (r 2^20)
+        // a = dY at its largest exponent: rows past the end count for nothing
+        const double as = ok ? pow2(max(ey - dtop, -64)) : 0.0;
+        double f[E], g[E], g2 = 0.0;
+        int g1 = 0;
 #pragma unroll
         for (int j = 0; j < E; ++j) {
-            const double d = __builtin_fma((double)byte_of(w[j / 4], j % 4), (double)n, -st.s);
-            const int c = byte_of(v[j / 4], j % 4);
+            const double d = __builtin_fma((double)byte_of(w[j / 4], j % 4), (double)n, -gs.s);
+            const double c = (double)byte_of(v[j / 4], j % 4);
             f[j] = rint_magic(d * r20);
-            g[j] = (double)c * gam[j];
-            g1 += g[j];
-            g2 = __builtin_fma(g[j], f[j], g2);
+            g[j] = c * gam[j];
             if (sums) {
-                const int a = rne_shift32(c, sh);
-                af[j] = __builtin_fma((double)a, f[j], af[j]);
-                ab[j] += a;
+                const double a = __builtin_fma(c, as, ROUND_MAGIC);
+                af[j] = __builtin_fma(a - ROUND_MAGIC, f[j], af[j]);
+                ab[j] += __double2loint(a);
             }
         }
         if (!grad) continue;
-        g1 = row_reduce<T>(g1, Add{}, shd);
-        g2 = row_reduce<T>(g2, Add{}, shd) * 0x1p-40;
-        const double k = st.r;
-        double mx = 0.0;
+        if (p.mode != NORM_ROUND) {
+#pragma unroll
+            for (int i = 0; i < W; ++i) g1 = __builtin_amdgcn_sdot4((int)v[i], (int)gw[i], g1, false);
+#pragma unroll
+            for (int j = 0; j < E; ++j) g2 = __builtin_fma(g[j], f[j], g2);
+            gs.g1 = (double)row_reduce<T>(g1, Add{}, shi);
+            gs.g2 = row_reduce<T>(g2, Add{}, shd) * 0x1p-40;
+            if (p.mode == NORM_NEED && ok && t == 0) p.gstat[row] = gs;
+        }
 #pragma unroll
         for (int j = 0; j < E; ++j) {
-            const double z = __builtin_fma(g[j], (double)n, -g1) - f[j] * g2;
-            g[j] = 4 * ((j / 4) * T + t) + j % 4 < n ? z * k : 0.0;
-            mx = fmax(mx, fabs(g[j]));
+            const double z = __builtin_fma(g[j], (double)n, -gs.g1) - f[j] * gs.g2;
+            g[j] = z * gs.r;
         }
+        if (!cols.exact) {
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+                if (!(cols.mask[j / 4] >> (8 * (j % 4)) & 1u)) g[j] = 0.0;
+        }
+        MaxMag mx;
+#pragma unroll
+        for (int j = 0; j < E; ++j) mx.add(g[j]);
         const int scale = ey + gtop - ex;  // the row's results are g 2^scale
         if (p.mode == NORM_NEED) {
-            if (ok) run = fmax(run, mx * pow2(scale));
+            if (mx.word()) run = max(run, mx.word() + (scale << 20));
             continue;
         }
         double in = inv * pow2(scale);
         if (p.mode == NORM_ROWS) {
-            mx = row_reduce<T>(mx, Max{}, shd);
-            const int need = need_f64(mx, p.q);
+            const int need = need_word(row_reduce<T>(mx.word(), Max{}, shi), p.q);
             int eo = need == NEED_NONE ? E_MIN : max(E_MIN, need + scale);
             if (ok && t == 0) {
                 eo = clamp_exp_flag(eo, p.flags);
@@ -219,69 +405,81 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void norm_bwd_kernel(NormBwd p) 
         }
         if (!ok) continue;
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-            const int c = 4 * (i * T + t);
-            if (c < n)
-                store4(p.out + off, c, n,
-                       pack4(mant_of(g[4 * i], in), mant_of(g[4 * i + 1], in), mant_of(g[4 * i + 2], in),
-                             mant_of(g[4 * i + 3], in)));
-        }
+        for (int i = 0; i < W; ++i)
+            w[i] = pack4(mant_of(g[4 * i], in), mant_of(g[4 * i + 1], in), mant_of(g[4 * i + 2], in),
+                         mant_of(g[4 * i + 3], in));
+        cols.store(p.out + row * n, w);
     }
     if (grad && p.mode == NORM_NEED) {
-        run = row_reduce<BT>(run, Max{}, shd);
-        if (threadIdx.x == 0) p.bmax[blockIdx.x] = need_f64(run, p.q);
+        run = row_reduce<BT>(run, Max{}, shi);
+        if (threadIdx.x == 0) p.bmax[blockIdx.x] = need_word(run, p.q);
     }
     if (!sums) return;
-    // the block's column sums: rows of one wave first, then the waves
-    if constexpr (T < 64) {
-#pragma unroll
-        for (int j = 0; j < E; ++j)
-#pragma unroll
-            for (int s = T; s < 64; s <<= 1) {
-                af[j] += __shfl_xor(af[j], s);
-                ab[j] += __shfl_xor(ab[j], s);
-            }
-    }
+    // the block's column sums (a's low words carry nothing of ROUND_MAGIC)
     long long *pf = p.pf + (long long)blockIdx.x * n;
     int *pb = p.pb + (long long)blockIdx.x * n;
-    if constexpr (T <= 64) {
-        __shared__ double lf[4][T * E];
-        __shared__ int lb[4][T * E];
-        const int wave = threadIdx.x >> 6;
-        if ((threadIdx.x & 63) < T) {
-#pragma unroll
-            for (int j = 0; j < E; ++j) {
-                lf[wave][(j / 4 * T + t) * 4 + j % 4] = af[j];
-                lb[wave][(j / 4 * T + t) * 4 + j % 4] = ab[j];
-            }
-        }
-        __syncthreads();
-        for (int c = threadIdx.x; c < n; c += BT) {
-            pf[c] = (long long)(lf[0][c] + lf[1][c] + lf[2][c] + lf[3][c]);
-            pb[c] = lb[0][c] + lb[1][c] + lb[2][c] + lb[3][c];
-        }
-    } else {
+    if constexpr (T > 64) {
 #pragma unroll
         for (int j = 0; j < E; ++j) {
-            const int c = 4 * (j / 4 * T + t) + j % 4;
+            const int c = C::col(j, t);
             if (c < n) {
                 pf[c] = (long long)af[j];
                 pb[c] = ab[j];
             }
         }
+    } else {
+        // integer sums of the waves in LDS, so in any order
+        __shared__ unsigned long long lf[T * E];
+        __shared__ int lb[T * E];
+        for (int c = threadIdx.x; c < T * E; c += BT) lf[c] = 0, lb[c] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            double a = af[j];
+            int b = ab[j];
+            if constexpr (T <= 16) {
+                a = swap_reduce<16>(a, Add{});
+                b = swap_reduce<16>(b, Add{});
+            }
+            if constexpr (T <= 32) {
+                a = swap_reduce<32>(a, Add{});
+                b = swap_reduce<32>(b, Add{});
+            }
+            if ((threadIdx.x & 63) < T) {
+                atomicAdd(&lf[C::col(j, t)], (unsigned long long)(long long)a);
+                atomicAdd(&lb[C::col(j, t)], b);
+            }
+        }
+        __syncthreads();
+        for (int c = threadIdx.x; c < n; c += BT) {
+            pf[c] = (long long)lf[c];
+            pb[c] = lb[c];
+        }
     }
 }
 
-#define IE_NORM_SHAPES(X) \
-    X(16, 4) X(16, 8) X(16, 12) X(16, 16) X(32, 12) X(32, 16) X(64, 12) X(64, 16) X(256, 8) X(256, 12) X(256, 16) \
-    X(1024, 8) X(1024, 12) X(1024, 16)
+// Largest exponents of runs of rows, one per block, for matrices too tall for
+// every block of norm_bwd_kernel to find the largest itself.
+__global__ __launch_bounds__(1024) void tops_kernel(const int8_t *e, long long n, long long run, int *tops) {
+    __shared__ int shi[16];
+    const long long b = blockIdx.x * run;
+    const int m = max_exp<1024>(e + b, min(run, n - b), shi);
+    if (threadIdx.x == 0) tops[blockIdx.x] = m;
+}
+
+#define IE_NORM_FWD(X)                                                                                           \
+    X(16, 4) X(16, 8) X(16, 12) X(16, 16) X(16, 24) X(16, 32) X(16, 48) X(32, 24) X(64, 4) X(64, 8) X(64, 12) X(64, 16)     \
+    X(64, 24) X(64, 32) X(64, 48) X(256, 12) X(256, 16) X(256, 24) X(1024, 8) X(1024, 12) X(1024, 16)
+#define IE_NORM_BWD(X)                                                                                           \
+    X(16, 4) X(16, 8) X(16, 12) X(16, 16) X(64, 4) X(64, 8) X(64, 12) X(64, 16) X(256, 8) X(256, 12) X(256, 16)    \
+    X(512, 12) X(512, 16) X(1024, 12) X(1024, 16)
 
 hipError_t launch_norm_fwd(const NormFwd &a, const NormPlan &pl, hipStream_t st) {
     prof_begin(st, PROF_NORM_FWD);
-#define IE_CASE(T_, E_)                                                                                          \
-    if (pl.t == T_ && pl.e == E_)                                                                                \
-        hipLaunchKernelGGL((norm_fwd_kernel<T_, E_>), dim3(pl.grid), dim3(T_ > 256 ? T_ : 256), 0, st, a);
-    IE_NORM_SHAPES(IE_CASE)
+#define IE_CASE(T_, E_)       \
+    if (pl.t == T_ && pl.e == E_) \
+        hipLaunchKernelGGL((norm_fwd_kernel<T_, E_>), dim3(pl.grid), dim3(norm_block<T_>()), 0, st, a);
+    IE_NORM_FWD(IE_CASE)
 #undef IE_CASE
     prof_end(st, PROF_NORM_FWD);
     return hipGetLastError();
@@ -289,12 +487,18 @@ hipError_t launch_norm_fwd(const NormFwd &a, const NormPlan &pl, hipStream_t st)
 
 hipError_t launch_norm_bwd(const NormBwd &a, const NormPlan &pl, hipStream_t st) {
     prof_begin(st, PROF_NORM_BWD);
-#define IE_CASE(T_, E_)                                                                                          \
-    if (pl.t == T_ && pl.e == E_)                                                                                \
-        hipLaunchKernelGGL((norm_bwd_kernel<T_, E_>), dim3(pl.grid), dim3(T_ > 256 ? T_ : 256), 0, st, a);
-    IE_NORM_SHAPES(IE_CASE)
+#define IE_CASE(T_, E_)       \
+    if (pl.t == T_ && pl.e == E_) \
+        hipLaunchKernelGGL((norm_bwd_kernel<T_, E_>), dim3(pl.grid), dim3(grad_block<T_>()), 0, st, a);
+    IE_NORM_BWD(IE_CASE)
 #undef IE_CASE
     prof_end(st, PROF_NORM_BWD);
+    return hipGetLastError();
+}
+
+hipError_t launch_tops(const int8_t *e, long long n, int *tops, int n_tops, hipStream_t st) {
+    const long long run = (n + n_tops - 1) / n_tops;
+    hipLaunchKernelGGL(tops_kernel, dim3((int)((n + run - 1) / run)), dim3(1024), 0, st, e, n, run, tops);
     return hipGetLastError();
 }
 
@@ -304,66 +508,106 @@ hipError_t launch_norm_bwd(const NormBwd &a, const NormPlan &pl, hipStream_t st)
 
 // Partial column sums of dY at its largest exponent: block (x, y) adds the
 // rows [y chunk, (y + 1) chunk) of columns 256 x .. 256 x + 255, four columns
-// per lane, every fourth row per wave.  |a| <= 128 and at most 2^23 rows a
-// block keep the sums in 32 bits.
-__global__ __launch_bounds__(256) void col_sum_kernel(const int8_t *dy, const int8_t *e, int e_row, const int *top,
-                                                      long long rows, int cols, int chunk, int *pb) {
-    __shared__ int sh[4][256];
+// per lane, every fourth row per wave, eight rows' loads in flight.
+// A mantissa at shift s <= 7 is one conversion (of C + 128, unsigned) and one
+// fp32 fused multiply-add, exact before its only rounding, whose low bits are
+// the rounded integer above those of 1.5 * 2^23; these are summed as they
+// are and the constant taken off at the end (modulo 2^32).  At s >= 8 every
+// |C| <= 128 rounds to 0.  At most 2^23 rows a block keep a sum in 32 bits.
+__global__ __launch_bounds__(256) void col_sum_kernel(const int8_t *dy, const int8_t *e, int e_row, long long rows,
+                                                      int cols, int chunk, const int *tops, int n_tops, int *top,
+                                                      int *pb) {
+    constexpr int U = 8;
+    __shared__ uint32_t sh[4][256];
+    __shared__ int shi[4];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int c = blockIdx.x * 256 + lane * 4;
     const long long r0 = (long long)blockIdx.y * chunk, r1 = min(rows, r0 + chunk);
-    const int dtop = top[0];
-    int a[4] = {0, 0, 0, 0};
-    if (c < cols)
-        for (long long r = r0 + wave; r < r1; r += 4) {
-            const uint32_t w = load4(dy + r * cols, c, cols);
-            const int s = dtop - (int)e[e_row ? r : 0];
+    const int dtop = top_exp<256>(e, e_row, rows, tops, n_tops, shi);
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *top = dtop;
+    // four bytes may be read past a row's end wherever four more rows follow;
+    // sums of columns past the last are not kept
+    const bool whole = cols % 4 == 0 || r1 + 4 <= rows;
+    const int c0 = c < cols ? c : 0;
+    uint32_t a[4] = {0, 0, 0, 0};
+    for (long long r = r0 + wave; r < r1; r += 4 * U) {
+        uint32_t w[U];
+        int s[U];
+        float f[U], k0[U];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) a[k] += rne_shift32(byte_of(w, k), s);
+        for (int u = 0; u < U; ++u) {
+            const long long rr = min(r + 4 * u, r1 - 1);  // past the end: a row that counts for nothing
+            if (whole) __builtin_memcpy(w + u, dy + rr * cols + c0, 4);
+            else w[u] = load4(dy + rr * cols, c, cols);
+            s[u] = e[e_row ? rr : 0];
         }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) sh[wave][lane * 4 + k] = a[k];
+        for (int u = 0; u < U; ++u) {
+            s[u] = r + 4 * u < r1 ? dtop - s[u] : 8;
+            f[u] = s[u] < 8 ? __builtin_ldexpf(1.0f, -s[u]) : 0.0f;
+            k0[u] = 12582912.0f - 128.0f * f[u];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t x = w[u] ^ 0x80808080u;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                a[k] += (uint32_t)__float_as_int(__builtin_fmaf((float)(x >> (8 * k) & 255u), f[u], k0[u]));
+        }
+    }
+    // every trip added U constants
+    const uint32_t n_add = r1 > r0 + wave ? (uint32_t)((r1 - r0 - wave + 4 * U - 1) / (4 * U)) * U : 0u;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sh[wave][lane * 4 + k] = a[k] - n_add * 0x4B400000u;
     __syncthreads();
     const int col = blockIdx.x * 256 + threadIdx.x;
     if (col < cols)
         pb[(long long)blockIdx.y * cols + col] =
-            sh[0][threadIdx.x] + sh[1][threadIdx.x] + sh[2][threadIdx.x] + sh[3][threadIdx.x];
+            (int)(sh[0][threadIdx.x] + sh[1][threadIdx.x] + sh[2][threadIdx.x] + sh[3][threadIdx.x]);
 }
 
-// Sums of `parts` partial rows (64-bit or 32-bit), 64 columns per block, at
-// exponent base + *top: rounded into one group per channel here, or kept for
-// col_round_kernel with the block's need.
+// Sums of `parts` partial rows (64-bit or 32-bit), 16 columns per block and 64
+// partial rows at a time, at exponent base + *top: rounded into one group per
+// channel here, or kept for col_round_kernel with the block's need.
 __global__ __launch_bounds__(1024) void col_finish_kernel(ColOut f, ColOut b, int parts, int cols, const int *top,
                                                           uint32_t *flags) {
-    __shared__ long long sh[16][64];
+    __shared__ long long sh[16][16];
     const ColOut &o = blockIdx.y == 0 ? f : b;
     if (!o.m) return;
-    const int lane = threadIdx.x & 63, grp = threadIdx.x >> 6;
-    const int c = blockIdx.x * 64 + lane;
+    const int lane = threadIdx.x & 15, grp = threadIdx.x >> 4;
+    const long long c = blockIdx.x * 16ll + lane;
     long long s = 0;
     if (c < cols) {
-        if (o.p64)
-            for (int i = grp; i < parts; i += 16) s += o.p64[(long long)i * cols + c];
-        else
-            for (int i = grp; i < parts; i += 16) s += o.p32[(long long)i * cols + c];
+        if (o.p64) {
+#pragma unroll 4
+            for (int i = grp; i < parts; i += 64) s += o.p64[(long long)i * cols + c];
+        } else {
+#pragma unroll 4
+            for (int i = grp; i < parts; i += 64) s += o.p32[(long long)i * cols + c];
+        }
     }
-    sh[grp][lane] = s;
+    s += __shfl_xor(s, 16);
+    s += __shfl_xor(s, 32);
+    if ((threadIdx.x & 63) < 16) sh[threadIdx.x >> 6][lane] = s;
     __syncthreads();
-    if (grp) return;
-#pragma unroll
-    for (int i = 1; i < 16; ++i) s += sh[i][lane];
     const int eps = top[0] + o.base;
-    int need = need64(s, eps, o.q);
-    if (o.per) {
-        if (c >= cols) return;
-        const int e = clamp_exp_flag(max(E_MIN, need), flags);
-        o.m[c] = (int8_t)rne_shift64(s, e - eps);
-        o.e[c] = (int8_t)e;
-        return;
+    if (threadIdx.x < 64) {
+        s = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s += sh[i][lane];
+        int need = c < cols ? need64(s, eps, o.q) : NEED_NONE;
+        if (o.per) {
+            if (threadIdx.x < 16 && c < cols) {
+                const int e = clamp_exp_flag(max(E_MIN, need), flags);
+                o.m[c] = (int8_t)rne_shift64(s, e - eps);
+                o.e[c] = (int8_t)e;
+            }
+        } else {
+            need = lane_reduce<16>(need, Max{});
+            if (threadIdx.x < 16 && c < cols) o.sums[c] = s;
+            if (threadIdx.x == 0) o.need[blockIdx.x] = need;
+        }
     }
-    need = wave_max_dpp(need);
-    if (c < cols) o.sums[c] = s;
-    if (lane == 0) o.need[blockIdx.x] = need;
 }
 
 // One exponent for the whole vector: every block takes the largest need.
@@ -376,28 +620,29 @@ __global__ __launch_bounds__(256) void col_round_kernel(ColOut f, ColOut b, int 
     for (int i = threadIdx.x; i < n_need; i += 256) m = max(m, o.need[i]);
     m = row_reduce<256>(m, Max{}, shi);
     const int e = clamp_exp_flag(max(E_MIN, m), flags), s = e - top[0] - o.base;
-    const int c = blockIdx.x * 256 + threadIdx.x;
-    if (c < cols) o.m[c] = (int8_t)rne_shift64(o.sums[c], s);
-    if (c == 0) o.e[0] = (int8_t)e;
+    for (int c = blockIdx.x * 256 + threadIdx.x; c < cols; c += gridDim.x * 256) o.m[c] = (int8_t)rne_shift64(o.sums[c], s);
+    if (blockIdx.x == 0 && threadIdx.x == 0) o.e[0] = (int8_t)e;
 }
 
-hipError_t launch_col_sum(const int8_t *dy, const int8_t *e, int e_row, const int *top, long long rows, int cols,
-                          int chunk, int parts, int *pb, hipStream_t st) {
+hipError_t launch_col_sum(const int8_t *dy, const int8_t *e, int e_row, long long rows, int cols, ColPlan pl,
+                          const int *tops, int n_tops, int *top, int *pb, hipStream_t st) {
     prof_begin(st, PROF_COL_SUM);
-    hipLaunchKernelGGL(col_sum_kernel, dim3((cols + 255) / 256, parts), dim3(256), 0, st, dy, e, e_row, top, rows, cols,
-                       chunk, pb);
+    hipLaunchKernelGGL(col_sum_kernel, dim3((cols + 255) / 256, pl.parts), dim3(256), 0, st, dy, e, e_row, rows, cols,
+                       pl.chunk, tops, n_tops, top, pb);
     prof_end(st, PROF_COL_SUM);
     return hipGetLastError();
 }
 
 hipError_t launch_col_finish(const ColOut &f, const ColOut &b, int parts, int cols, const int *top, uint32_t *flags,
                              hipStream_t st) {
-    const int nb = (cols + 63) / 64;
+    const int nb = (cols + 15) / 16;
     prof_begin(st, PROF_COL_FINISH);
     hipLaunchKernelGGL(col_finish_kernel, dim3(nb, b.m ? 2 : 1), dim3(1024), 0, st, f, b, parts, cols, top, flags);
-    if ((f.m && !f.per) || (b.m && !b.per))
-        hipLaunchKernelGGL(col_round_kernel, dim3((cols + 255) / 256, b.m ? 2 : 1), dim3(256), 0, st, f, b, nb, cols,
+    if ((f.m && !f.per) || (b.m && !b.per)) {
+        const int g = (cols + 255) / 256;
+        hipLaunchKernelGGL(col_round_kernel, dim3(g < 1024 ? g : 1024, b.m ? 2 : 1), dim3(256), 0, st, f, b, nb, cols,
                            top, flags);
+    }
     prof_end(st, PROF_COL_FINISH);
     return hipGetLastError();
 }

@@ -667,23 +667,51 @@ bool is_vector(const ie_mat *t, long long n) {
     return (t->rows == n && t->cols == 1) || (t->rows == 1 && t->cols == n);
 }
 
-// The fewest threads per row that hold it in at most 16 elements each, and
-// the fewest elements (a multiple of 4) that those threads need.
-NormPlan norm_plan(long long rows, long long cols, int max_blocks) {
-    NormPlan p{16, 4, 1};
-    const int ts[] = {16, 32, 64, 256, 1024};
-    for (int t : ts) {
-        p.t = t;
-        if (cols <= 16ll * t) break;
-    }
-    p.e = 4 * cdiv(cols > 0 ? cols : 1, 4ll * p.t);
-    if (p.e < 8 && p.t > 16) p.e = 8;
-    if (p.e < 12 && (p.t == 32 || p.t == 64)) p.e = 12;
-    const long long rpb = p.t > 256 ? 1 : 256 / p.t;
-    const long long want = (rows + rpb - 1) / rpb;
-    const int cap = p.t > 256 ? max_blocks / 2 : max_blocks;
-    p.grid = (int)(want < 1 ? 1 : want > cap ? cap : want);
-    return p;
+namespace {
+struct RowShape {
+    int t, e;
+};
+// The first of the shapes (in ascending order of t * e) that holds a row.
+RowShape first_fit(const RowShape *s, int n, long long cols) {
+    for (int i = 0; i + 1 < n; ++i)
+        if (cols <= (long long)s[i].t * s[i].e) return s[i];
+    return s[n - 1];
+}
+}  // namespace
+
+// Rows of up to 768 elements take 16 threads (four rows share a wave, its
+// reductions and its square root), longer ones a wave or a block.  With few
+// rows (NORM_FEW) a wave per row has the shorter chain of work.
+NormPlan norm_fwd_plan(long long rows, long long cols) {
+    static const RowShape many[] = {{16, 4},  {16, 8},  {16, 12}, {16, 16},  {16, 24},  {16, 32},   {16, 48}, {64, 16},
+                                    {64, 24}, {64, 32}, {64, 48}, {256, 16}, {256, 24}, {1024, 8}, {1024, 12}, {1024, 16}};
+    static const RowShape few[] = {{64, 4},   {64, 8},   {64, 12},  {64, 16}, {256, 12},
+                                   {256, 16}, {256, 24}, {1024, 8}, {1024, 12}, {1024, 16}};
+    const RowShape s = rows >= NORM_FEW ? first_fit(many, sizeof many / sizeof *many, cols)
+                                        : first_fit(few, sizeof few / sizeof *few, cols);
+    const long long rpb = s.t > 256 ? 1 : 256 / s.t, want = (rows + rpb - 1) / rpb, cap = s.t > 256 ? 512 : 2048;
+    return NormPlan{s.t, s.e, (int)(want < 1 ? 1 : want > cap ? cap : want)};
+}
+
+// Each thread keeps the column sums of its elements, so at most 16; blocks of
+// 512 threads (of one row when it takes more than 64), about one a CU, each
+// leaving one row of partial sums.
+NormPlan norm_bwd_plan(long long rows, long long cols) {
+    static const RowShape many[] = {{16, 4},  {16, 8},   {16, 12},  {16, 16},  {64, 8},    {64, 12},   {64, 16},
+                                    {256, 8}, {256, 12}, {256, 16}, {512, 12}, {512, 16}, {1024, 12}, {1024, 16}};
+    static const RowShape few[] = {{64, 4},    {64, 8},   {64, 12},  {64, 16},   {256, 8},  {256, 12},
+                                   {256, 16}, {512, 12}, {512, 16}, {1024, 12}, {1024, 16}};
+    const RowShape s = rows >= NORM_FEW ? first_fit(many, sizeof many / sizeof *many, cols)
+                                        : first_fit(few, sizeof few / sizeof *few, cols);
+    const long long rpb = s.t > 64 ? 1 : 512 / s.t, want = (rows + rpb - 1) / rpb;
+    const long long cap = s.t == 256 || s.t == 512 ? 2 * NCU : NCU;
+    return NormPlan{s.t, s.e, (int)(want < 1 ? 1 : want > cap ? cap : want)};
+}
+
+int n_tops(long long rows, int e_row) {
+    if (!e_row || rows <= TOPS_ROWS) return 0;
+    const long long n = (rows + TOPS_ROWS - 1) / TOPS_ROWS;
+    return (int)(n > TOPS_MAX ? TOPS_MAX : n);
 }
 
 // The smallest t * e that holds a row, e a multiple of the eight elements
@@ -714,24 +742,27 @@ ColPlan col_plan(long long rows, long long cols) {
 static ColWs carve_cols(Carve &c, long long parts, long long cols, bool wide) {
     ColWs w{};
     const size_t n = (size_t)(cols > 0 ? cols : 1);
-    w.top = c.take<int>(2);
+    w.top = c.take<int>(1);
+    w.tops = c.take<int>(TOPS_MAX);
     if (wide) w.p64 = c.take<long long>((size_t)parts * n);
     w.p32 = c.take<int>((size_t)parts * n);
     w.sums = c.take<long long>(2 * n);
-    w.need = c.take<int>(2 * ((n + 63) / 64));
+    w.need = c.take<int>(2 * ((n + 15) / 16));
     return w;
 }
 
 NormWs carve_norm_fwd(Carve &c, long long rows, long long cols) {
     NormWs w{};
-    w.bmax = c.take<int>((size_t)norm_plan(rows, cols, NORM_FWD_BLOCKS).grid);
+    w.bmax = c.take<int>((size_t)norm_fwd_plan(rows, cols).grid);
+    w.stat = c.take<char>((size_t)rows * 16);
     return w;
 }
 
 NormWs carve_norm_bwd(Carve &c, long long rows, long long cols) {
     NormWs w{};
-    const NormPlan p = norm_plan(rows, cols, NORM_BWD_BLOCKS);
+    const NormPlan p = norm_bwd_plan(rows, cols);
     w.bmax = c.take<int>((size_t)p.grid);
+    w.stat = c.take<char>((size_t)rows * 32);
     w.c = carve_cols(c, p.grid, cols, true);
     return w;
 }

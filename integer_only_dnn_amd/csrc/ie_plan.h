@@ -344,16 +344,16 @@ struct BmmWs {
 BmmWs carve_bmm(Carve &c, int form, long long Z, long long M, long long N, long long K);
 
 // Layer norm: t threads per row with e elements each (t * e >= cols), on a
-// persistent grid of `grid` blocks of max(t, 256) threads.
+// persistent grid of `grid` blocks.
 constexpr long long NORM_COLS_MAX = 16384;
 constexpr long long NORM_ROWS_MAX = 1ll << 27;  // dgamma sums stay below 2^62
 constexpr long long LONG_COLS_MAX = 1ll << 30;  // dropout, column sums: columns are walked in 32 bits
-constexpr int NORM_FWD_BLOCKS = 2048;
-constexpr int NORM_BWD_BLOCKS = 512;  // each leaves one row of partial column sums
 struct NormPlan {
     int t, e, grid;
 };
-NormPlan norm_plan(long long rows, long long cols, int max_blocks);
+constexpr long long NORM_FEW = 4096;
+NormPlan norm_fwd_plan(long long rows, long long cols);
+NormPlan norm_bwd_plan(long long rows, long long cols);
 
 // Dropout: the same split, with e = 0 for rows too long to be held.
 NormPlan dropout_plan(long long rows, long long cols);
@@ -364,17 +364,23 @@ struct ColPlan {
 };
 ColPlan col_plan(long long rows, long long cols);
 
-// 64-column blocks of the column sums' finish, each with its need when the
-// vector has one exponent.
+// The largest exponent of more rows than this is found by a kernel of its own
+// (in parts), of fewer by every block that needs it.
+constexpr long long TOPS_ROWS = 16384;
+constexpr int TOPS_MAX = 64;
+int n_tops(long long rows, int e_row);
+
 struct ColWs {
-    int *top;         // [2]: largest exponents of dY and gamma
+    int *top;         // largest exponent of dY
+    int *tops;        // [TOPS_MAX]
     long long *p64;   // partial sums of dgamma [parts][cols]
     int *p32;         // partial sums of dbeta / db
     long long *sums;  // [2][cols]
-    int *need;        // [2][ceil(cols / 64)]
+    int *need;        // [2][ceil(cols / 16)]
 };
 struct NormWs {
-    int *bmax;  // block maxima of a whole-tensor result
+    int *bmax;   // block maxima of a whole-tensor result
+    void *stat;  // its rows' statistics
     ColWs c;
 };
 NormWs carve_norm_fwd(Carve &c, long long rows, long long cols);
