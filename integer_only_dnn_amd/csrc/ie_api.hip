@@ -1107,15 +1107,18 @@ ie_status ie_linear_fwd_fused(const ie_mat *X, const ie_mat *W, const ie_mat *bi
     Carve c{(char *)ws, HEADER};
     const LinearFusedWs w = carve_linear_fused(c, M, N, K, f);
     const long long Kp = r16(K);
+    const int rows = rows_plan(M, N, Kp, rg, f);
     const Plan pl = plan_add(M, N, Kp, rg, f);
     IE_CHECK(checked_plan(pl, M, N, Kp, rg, FAM_ADD, w.l.pw.n, add_needs(pl, M, N, Kp, rg)));
     log_plan("dense add", M, N, Kp, pl);
     const int8_t *xs = X->mant, *wsrc = W->mant;
     if (Kp != K) {
         IE_TRY(launch_pad_rows(X->mant, M, K, nullptr, 0, nullptr, Kp, w.l.xp, st));
-        IE_TRY(launch_pad_rows(W->mant, N, K, nullptr, 0, nullptr, Kp, w.l.wp, st));
         xs = w.l.xp;
-        wsrc = w.l.wp;
+        if (!rows) {
+            IE_TRY(launch_pad_rows(W->mant, N, K, nullptr, 0, nullptr, Kp, w.l.wp, st));
+            wsrc = w.l.wp;
+        }
     }
     const Operand A{LD_K, xs, Kp, (int)M, {}}, B{LD_K, wsrc, Kp, (int)N, {}};
     AddEpi e;
@@ -1137,6 +1140,7 @@ ie_status ie_linear_fwd_fused(const ie_mat *X, const ie_mat *W, const ie_mat *bi
     e.q = mat_q(Y);
     e.relu = act == IE_ACT_RELU;
     e.flags = (uint32_t *)ws;
+    if (rows) return hip_status(launch_rows_add(xs, W->mant, (int)M, (int)N, (int)K, (int)Kp, w.wt, rows, e, st));
     if (pl.mode == PLAN_SPLIT) {
         Epi ep;
         memset(&ep, 0, sizeof ep);

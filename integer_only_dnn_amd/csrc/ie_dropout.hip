@@ -113,7 +113,7 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void dropout_kernel(DropArgs p) 
             if (c < n) {
                 drop8(p, g, x, r, c, (uint32_t)row, sx, sr, y[i]);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) mx.add(y[i][k]);
+                for (int k = 0; k < 8; k += 2) mx.add(y[i][k], y[i][k + 1]);
             }
         }
         if (p.mode == NORM_NEED) {
@@ -168,7 +168,7 @@ __global__ __launch_bounds__(1024) void dropout_long_kernel(DropArgs p) {
             for (long long c = 8ll * threadIdx.x; c < n; c += 8192) {
                 drop8(p, g, x, r, (int)c, (uint32_t)row, sx, sr, y);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) mx.add(y[k]);
+                for (int k = 0; k < 8; k += 2) mx.add(y[k], y[k + 1]);
             }
             if (p.mode == NORM_NEED) {
                 run = max(run, mx.word());

@@ -120,19 +120,19 @@ __device__ __forceinline__ V row_reduce(V v, F f, V *sh) {
     return v;
 }
 
-// Largest magnitude of a run of values, as the high word of its double: the
-// need of a magnitude takes its exponent and leading bits only.  The largest
-// signed word is the largest positive value's, the largest unsigned one the
-// most negative value's.
+// Largest magnitude of a run of values, as the high word of its double (the
+// need of a magnitude takes its exponent and leading bits only).  High words
+// of magnitudes order like the floats of the same bits, so one three-operand
+// fp32 maximum, its operands' signs dropped, takes two values; no double
+// here reaches the 2^1017 whose high word would be a NaN, or the 2^-1015
+// whose high word would be a denormal.
 struct MaxMag {
-    int hi = 0;
-    uint32_t neg = 0;
-    __device__ __forceinline__ void add(double v) {
-        const int h = __double2hiint(v);
-        hi = max(hi, h);
-        neg = max(neg, (uint32_t)h);
+    float m = 0.0f;
+    __device__ __forceinline__ void add(double a, double b) {
+        const int ha = __double2hiint(a), hb = __double2hiint(b);
+        asm("v_max3_f32 %0, %0, |%1|, |%2|" : "+v"(m) : "v"(ha), "v"(hb));
     }
-    __device__ __forceinline__ int word() const { return max(hi, (int)neg < 0 ? (int)(neg & 0x7fffffffu) : 0); }
+    __device__ __forceinline__ int word() const { return __float_as_int(m); }
 };
 
 // Smallest exponent for the magnitude whose high word is w (NEED_NONE when

@@ -16,6 +16,7 @@
 
 namespace ie {
 
+template <bool RES>
 struct EpiAdd {
     AddEpi e;
 
@@ -48,7 +49,11 @@ struct EpiAdd {
     __device__ __forceinline__ void finish(const v16i (&acc)[AM][AN], int8_t *lds, int m0, int n0, int tile_m,
                                            int tile_n, int M, int N, int TM) const {
         constexpr int BM = 64 * MI, BN = 64 * NI, RP = BN + 4;  // RP: pitch of the residual tile
-        const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
+        int tid = threadIdx.x;
+        // offsets made of the thread's number are made here: kept over the contraction,
+        // they would not fit the registers
+        asm volatile("" : "+v"(tid));
+        const int lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
         double *cs = (double *)lds, *bs = cs + BN;  // column scales, bias
         int *red = (int *)(bs + BN);               // maxima [2][BM]
         int8_t *rt = (int8_t *)(red + 2 * BM), *out = rt + BM * RP;
@@ -62,7 +67,7 @@ struct EpiAdd {
             cs[i] = n < N ? pow2((int)e.we[e.w_row ? n : 0]) : 0.0;
             bs[i] = n < N && e.bias.m ? (double)e.bias.m[n] * pow2((int)e.bias.e[e.bias.per ? n : 0]) : 0.0;
         }
-        if (e.r) {
+        if constexpr (RES) {
             constexpr int CPR = BN / 16;
 #pragma unroll
             for (int q0 = 0; q0 < BM * CPR; q0 += NTHR) {
@@ -93,7 +98,7 @@ struct EpiAdd {
             row[a] = wm * 32 * MI + a * 32 + (lane & 31);
             const int m = m0 + row[a];
             sx[a] = m < M ? pow2((int)e.xe[e.x_row ? m : 0]) : 0.0;
-            sr[a] = e.r && m < M ? pow2((int)e.re[e.r_row ? m : 0]) : 0.0;
+            sr[a] = RES && m < M ? pow2((int)e.re[e.r_row ? m : 0]) : 0.0;
         }
 #pragma unroll
         for (int b = 0; b < NI; ++b)
@@ -102,16 +107,17 @@ struct EpiAdd {
                 const int c = wn * 32 * NI + b * 32 + 8 * h + 4 * (lane >> 5);
 #pragma unroll
                 for (int a = 0; a < MI; ++a) {
-                    const uint32_t r4 = e.r ? *(const uint32_t *)(rt + row[a] * RP + c) : 0u;
+                    const uint32_t r4 = RES ? *(const uint32_t *)(rt + row[a] * RP + c) : 0u;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         // each fused step is an exact product and one rounded sum
                         double v = __builtin_fma((double)acc[a][b][4 * h + k], sx[a] * cs[c + k], bs[c + k]);
-                        if (e.r) v = __builtin_fma((double)byte_of(r4, k), sr[a], v);
+                        if constexpr (RES) v = __builtin_fma((double)byte_of(r4, k), sr[a], v);
                         y[a][b][4 * h + k] = v;
-                        mx[a].add(v);
+                        if (k % 2) mx[a].add(y[a][b][4 * h + k - 1], v);
                     }
                 }
+                if (h & 1) __builtin_amdgcn_sched_barrier(0);
             }
         // the group's exponent (results in this pass), or the round-to-odd
         // position two bits below the tile's own need
@@ -182,6 +188,7 @@ struct EpiAdd {
                         v2i p = {(o[0] & 0xffff) | o[1] << 16, (o[2] & 0xffff) | o[3] << 16};
                         *(v2i *)(out + row[a] * (2 * BN + 16) + 2 * c) = p;
                     }
+                    if (h & 1) __builtin_amdgcn_sched_barrier(0);
                 }
         __syncthreads();
         if constexpr (DI) flush<1, BM, BN>(out, e.y, m0, n0, M, N, (N & 15) == 0 && ((uintptr_t)e.y & 15) == 0);
@@ -189,33 +196,36 @@ struct EpiAdd {
     }
 };
 
-template <int MI, int NI, int RG, int DI>
-__global__ __launch_bounds__(NTHR, (Occ<MI, NI>::value)) void gemm_add_kernel(Operand A, Operand B, int M, int N, int K,
-                                                                              int TM, EpiAdd ep) {
+template <int MI, int NI, int RG, int DI, bool RES>
+__global__ __launch_bounds__(NTHR, (NI == 4 ? 1 : Occ<MI, NI>::value)) void gemm_add_kernel(Operand A, Operand B, int M, int N, int K,
+                                                                              int TM, EpiAdd<RES> ep) {
     __shared__ __attribute__((aligned(16))) int8_t lds[TileLds<LD_K, LD_K, MI, NI, false>::value];
     gemm_tile<LD_K, LD_K, MI, NI, false, false, -1, RG, DI>(A, B, M, N, K, K, TM, 1, ep, blockIdx.x, gridDim.x, lds);
 }
 
-template <int MI, int NI>
-static void launch_tile(const Operand &A, const Operand &B, int M, int N, int K, bool direct, const EpiAdd &ep,
+template <int MI, int NI, bool RES>
+static void launch_tile(const Operand &A, const Operand &B, int M, int N, int K, bool direct, const AddEpi &e,
                         hipStream_t st) {
     const int TM = (M + 64 * MI - 1) / (64 * MI), TN = (N + 64 * NI - 1) / (64 * NI);
     const dim3 grid(TM * TN), block(NTHR);
-    if (ep.e.y_row) {
-        if (direct) hipLaunchKernelGGL((gemm_add_kernel<MI, NI, 1, 1>), grid, block, 0, st, A, B, M, N, K, TM, ep);
-        else hipLaunchKernelGGL((gemm_add_kernel<MI, NI, 1, 0>), grid, block, 0, st, A, B, M, N, K, TM, ep);
+    const EpiAdd<RES> ep{e};
+    if (e.y_row) {
+        if (direct) hipLaunchKernelGGL((gemm_add_kernel<MI, NI, 1, 1, RES>), grid, block, 0, st, A, B, M, N, K, TM, ep);
+        else hipLaunchKernelGGL((gemm_add_kernel<MI, NI, 1, 0, RES>), grid, block, 0, st, A, B, M, N, K, TM, ep);
     } else {
-        if (direct) hipLaunchKernelGGL((gemm_add_kernel<MI, NI, 0, 1>), grid, block, 0, st, A, B, M, N, K, TM, ep);
-        else hipLaunchKernelGGL((gemm_add_kernel<MI, NI, 0, 0>), grid, block, 0, st, A, B, M, N, K, TM, ep);
+        if (direct) hipLaunchKernelGGL((gemm_add_kernel<MI, NI, 0, 1, RES>), grid, block, 0, st, A, B, M, N, K, TM, ep);
+        else hipLaunchKernelGGL((gemm_add_kernel<MI, NI, 0, 0, RES>), grid, block, 0, st, A, B, M, N, K, TM, ep);
     }
 }
 
 hipError_t launch_gemm_add(const Operand &A, const Operand &B, int M, int N, int K, Tile t, bool direct,
                            const AddEpi &e, hipStream_t st) {
-    const EpiAdd ep{e};
     prof_begin(st, PROF_GEMM_ADD);
 #define IE_CASE(a, b) \
-    if (t.mi == a && t.ni == b) launch_tile<a, b>(A, B, M, N, K, direct, ep, st);
+    if (t.mi == a && t.ni == b) {                                              \
+        if (e.r) launch_tile<a, b, true>(A, B, M, N, K, direct, e, st);        \
+        else launch_tile<a, b, false>(A, B, M, N, K, direct, e, st);           \
+    }
     IE_TILES_ADD(IE_CASE)
 #undef IE_CASE
     prof_end(st, PROF_GEMM_ADD);
@@ -256,7 +266,7 @@ __global__ __launch_bounds__(1024) void split_add_kernel(AddEpi e, const int *pa
         if (mode != NORM_ROUND) {
             MaxMag mx;
             for (long long n = threadIdx.x; n < N; n += 1024)
-                mx.add(split_value(e, partial, splits, stride, m, (int)n, N, sx, sr));
+                mx.add(split_value(e, partial, splits, stride, m, (int)n, N, sx, sr), 0.0);
             if (mode == NORM_NEED) {
                 run = max(run, mx.word());
                 continue;

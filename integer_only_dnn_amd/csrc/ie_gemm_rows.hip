@@ -1,0 +1,326 @@
+// Forward product with bias, residual and ReLU whose result rows lie whole
+// inside a workgroup, so that a row's exponent is known before it leaves the
+// registers: one pass, no intermediate result in memory.
+//
+// A workgroup of 8 waves computes 64 rows and 256 NI >= N columns at a time,
+// wave w the columns 32 NI w .. 32 NI (w + 1) - 1 of every row, with
+// v_mfma_i32_32x32x32_i8 run transposed (a lane holds one row of the result).
+// The weight is laid out beforehand in the order the matrix instructions take
+// it (1 KiB for 32 rows and 32 contraction bytes, lane by lane), so a wave
+// streams its share of it from L2 straight into registers, several steps
+// ahead; the 64 rows of X are staged in LDS, up to 1024 contraction bytes at a
+// time.  Nothing in the contraction loop waits for another wave.
+// Workgroups are persistent: the residual of a tile is loaded during its
+// products, the next tile's X while it is stored.
+//
+// The epilogue holds y in fp64, in the registers the accumulators leave, so
+// each value is computed once (NI = 4 has no room and computes it twice).
+//
+// Bound by the fp64 and conversion instructions of the epilogue next to the
+// products (they take turns: the registers hold one workgroup of NI >= 2 per
+// CU), not by memory.  Measured, with the weight's layout: 50432 x 768 x 192
+// 40 us (round to odd by tiles and the pass that closes it: 74), 25216 x 768 x
+// 768 with a residual 45 us (51).
+#include <algorithm>
+#include <type_traits>
+
+#include "ie_f64.h"
+#include "ie_internal.h"
+
+#pragma clang fp contract(off)
+
+namespace ie {
+
+constexpr int ROWS_THR = 512, ROWS_BM = 64;
+
+// W [N x K] -> out[n / 32][k / 32][lane][16], lane l holding row l % 32 and
+// bytes 16 (l / 32) .. + 15 of the 32; zeros past N and K.  A block lays out
+// 32 rows and 128 contraction bytes.
+__global__ __launch_bounds__(256) void tile_weight_kernel(const int8_t *w, int N, int K, int ks, int8_t *out) {
+    const int row = threadIdx.x >> 3, c = threadIdx.x & 7;
+    const int n = blockIdx.x * 32 + row, k = blockIdx.y * 128 + 16 * c, step = k >> 5;
+    uint32_t v[4] = {0, 0, 0, 0};
+    if (n < N) load_run<16>(w + (long long)n * K, k, K, v);
+    *(v4i *)(out + (((long long)blockIdx.x * ks + step) * 64 + (c & 1) * 32 + row) * 16) =
+        v4i{(int)v[0], (int)v[1], (int)v[2], (int)v[3]};
+}
+
+// KC: contraction steps of X in LDS.
+template <int NI, int KC, bool RES>
+struct RowsCfg {
+    static constexpr int BN = 256 * NI, RP = BN + 4;  // RP: pitch of the residual / result tile
+    static constexpr int D = NI == 4 ? 2 : 4;  // steps of the weight in flight
+    static constexpr bool KEEP = NI < 4;
+    static constexpr int A = KC * 2048, CS = A + 16 * BN, RED = CS + 8 * ROWS_BM * 4, LDS = RED + ROWS_BM * RP;
+};
+
+template <int NI, int KC, bool RES>
+__global__ __launch_bounds__(ROWS_THR) __attribute__((amdgpu_waves_per_eu(NI == 1 ? 4 : 2)))
+void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int ks, AddEpi e) {
+    using C = RowsCfg<NI, KC, RES>;
+    constexpr int BN = C::BN, RP = C::RP, D = C::D, U = KC / 4;
+    __shared__ __attribute__((aligned(16))) int8_t lds[C::LDS];
+    double *cs = (double *)(lds + C::A), *bs = cs + BN;  // column scales, bias
+    int *red = (int *)(lds + C::CS);                    // row maxima of the waves [8][64]
+    int8_t *rt = lds + C::RED;                          // the residual, then the result
+    int tid = threadIdx.x;
+    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int tiles = (M + ROWS_BM - 1) / ROWS_BM;
+
+    // X: thread t takes, of row (t / 4) % 64, the 16-byte piece t % 4 + 4 (t / 256)
+    // of every four contraction steps; rows past the last repeat it, bytes past K
+    // meet zeros of the weight
+    auto fetch_x = [&](int tile, int s0, v4i (&an)[U]) {
+        const int arow = (tid >> 2) & 63, aj = (tid & 3) + 4 * (tid >> 8);
+        const int8_t *xr = x + (long long)min(tile * ROWS_BM + arow, M - 1) * K;
+#pragma unroll
+        for (int u = 0; u < U; ++u) an[u] = *(const v4i *)(xr + min((s0 + 4 * u) * 32 + aj * 16, K - 16));
+    };
+    auto store_x = [&](const v4i (&an)[U]) {
+        const int arow = (tid >> 2) & 63, aj = (tid & 3) + 4 * (tid >> 8);
+        int8_t *ad = lds + (((aj >> 1) * 2 + (arow >> 5)) * 64 + (aj & 1) * 32 + (arow & 31)) * 16;
+#pragma unroll
+        for (int u = 0; u < U; ++u) *(v4i *)(ad + u * 8192) = an[u];
+    };
+    // the residual of a tile, 16 bytes at a time (rows that are not aligned so:
+    // four, straight to LDS)
+    constexpr int CPR = BN / 16, RR = ROWS_BM * CPR / ROWS_THR;
+    auto fetch_r = [&](int tile, v4i (&rr)[RR]) {
+        if (!RES || !e.r_vec) return;
+#pragma unroll
+        for (int i = 0; i < RR; ++i) {
+            const int q = i * ROWS_THR + tid, row = q / CPR, c = q % CPR * 16;
+            rr[i] = *(const v4i *)(e.r + (long long)min(tile * ROWS_BM + row, M - 1) * N + (c < N ? c : 0));
+        }
+    };
+    auto store_r = [&](int tile, const v4i (&rr)[RR]) {
+        if (!RES) return;
+        if (e.r_vec) {
+#pragma unroll
+            for (int i = 0; i < RR; ++i) {
+                const int q = i * ROWS_THR + tid, row = q / CPR, c = q % CPR * 16;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) *(uint32_t *)(rt + row * RP + c + 4 * k) = c < N ? (uint32_t)rr[i][k] : 0u;
+            }
+        } else {
+#pragma unroll 1
+            for (int q = tid; q < ROWS_BM * BN / 4; q += ROWS_THR) {
+                const int row = q / (BN / 4), c = q % (BN / 4) * 4;
+                *(uint32_t *)(rt + row * RP + c) = load4(e.r + (long long)min(tile * ROWS_BM + row, M - 1) * N, c, N);
+            }
+        }
+    };
+    const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)(wt + (long long)wave * NI * ks * 1024), (short)0, NI * ks * 1024, 0x00020000);
+    auto wtile = [&](int b, int s) -> v4i {
+        return (v4i)__builtin_amdgcn_raw_buffer_load_b128(wr, lane * 16, (b * ks + s) * 1024, 0);
+    };
+
+    v4i x0[U], r0[RR];
+    fetch_x(blockIdx.x, 0, x0);
+    fetch_r(blockIdx.x, r0);
+    for (int n = tid; n < BN; n += ROWS_THR) {
+        // past the last column everything is zero
+        cs[n] = n < N ? pow2((int)e.we[e.w_row ? n : 0]) : 0.0;
+        bs[n] = n < N && e.bias.m ? (double)e.bias.m[n] * pow2((int)e.bias.e[e.bias.per ? n : 0]) : 0.0;
+    }
+    store_x(x0);
+    store_r(blockIdx.x, r0);
+
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        const int m0 = tile * ROWS_BM;
+        // offsets made of the thread's number are made anew for every tile: kept,
+        // they would not fit the registers
+        asm volatile("" : "+v"(tid));
+        // one word of every 128 bytes of the next tile's rows, so that they are in L2
+        // when they are fetched
+        const int ahead = min(tile + (int)gridDim.x, tiles - 1) * ROWS_BM + (tid >> 3);
+        const long long arow = min(ahead, M - 1);
+        uint32_t warm = 0;
+        for (int c = (tid & 7) * 128; c < min(K, KC * 32); c += 1024) warm |= *(const uint32_t *)(x + arow * K + c);
+        if (RES && e.r_vec)
+            for (int c = (tid & 7) * 128; c < N; c += 1024) warm |= *(const uint32_t *)(e.r + arow * N + c);
+        // this lane's two rows' exponents
+        double sx[2], sr[2];
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+            const int m = min(m0 + a * 32 + (lane & 31), M - 1);
+            sx[a] = pow2((int)e.xe[e.x_row ? m : 0]);
+            sr[a] = RES ? pow2((int)e.re[e.r_row ? m : 0]) : 0.0;
+        }
+        v16i acc[2][NI];
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+            for (int b = 0; b < NI; ++b)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[a][b][r] = 0;
+        v4i bf[D][NI];
+#pragma unroll
+        for (int u = 0; u < D; ++u)
+#pragma unroll
+            for (int b = 0; b < NI; ++b) bf[u][b] = wtile(b, u);
+        __syncthreads();  // X and the residual are there
+
+        const v4i *as = (const v4i *)lds + lane;
+        for (int s0 = 0; s0 < ks; s0 += KC) {
+            if (s0) {
+                v4i an[U];
+                fetch_x(tile, s0, an);
+                __syncthreads();
+                store_x(an);
+                __syncthreads();
+            }
+            const int steps = min(KC, ks - s0);  // a multiple of 4
+            for (int s = 0; s < steps; s += D) {
+#pragma unroll
+                for (int u = 0; u < D; ++u) {
+                    v4i af[2];
+#pragma unroll
+                    for (int a = 0; a < 2; ++a) af[a] = as[((s + u) * 2 + a) * 64];
+                    const int next = min(s0 + s + u + D, ks - 1);  // past the end: loaded, never used
+#pragma unroll
+                    for (int b = 0; b < NI; ++b) {
+#pragma unroll
+                        for (int a = 0; a < 2; ++a)
+                            acc[a][b] = __builtin_amdgcn_mfma_i32_32x32x32_i8(bf[u][b], af[a], acc[a][b], 0, 0, 0);
+                        bf[u][b] = wtile(b, next);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+        }
+        asm volatile("" ::"v"(warm));
+        __syncthreads();  // X is free
+
+        // four neighbours of the result (columns 32 b + 8 h of this lane's own on) of
+        // both rows this lane holds; each fused step is an exact product and one
+        // rounded sum
+        const int c0 = wave * 32 * NI + 4 * (lane >> 5);
+        int ocs = C::A + 8 * c0, ort = C::RED + (lane & 31) * RP + c0;  // of its scales and residuals in LDS
+        asm volatile("" : "+v"(ocs), "+v"(ort));
+        auto quad = [&](int b, int h, double (&y)[2][4]) {
+            const double *s = (const double *)(lds + ocs) + b * 32 + 8 * h, *o = s + BN;
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[a][k] = __builtin_fma((double)acc[a][b][4 * h + k], sx[a] * s[k], o[k]);
+                if constexpr (RES) {
+                    const uint32_t r4 = *(const uint32_t *)(lds + ort + a * 32 * RP + b * 32 + 8 * h);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) y[a][k] = __builtin_fma((double)byte_of(r4, k), sr[a], y[a][k]);
+                }
+            }
+        };
+        double yk[C::KEEP ? NI * 4 : 1][2][4];
+        MaxMag mx[2];
+#pragma unroll
+        for (int b = 0; b < NI; ++b)
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                double(&y)[2][4] = yk[C::KEEP ? b * 4 + h : 0];
+                quad(b, h, y);
+#pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                    mx[a].add(y[a][0], y[a][1]);
+                    mx[a].add(y[a][2], y[a][3]);
+                }
+                if (h & 1) __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+            const int m = swap_reduce<32>(mx[a].word(), Max{});
+            if (lane < 32) red[wave * ROWS_BM + a * 32 + lane] = m;
+        }
+        __syncthreads();
+        const int next = min(tile + (int)gridDim.x, tiles - 1);  // past the end: fetched, never used
+        v4i xn[U], rn[RR];
+        double inv[2];
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+            const int r = a * 32 + (lane & 31), m = m0 + r;
+            int w = red[r];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) w = max(w, red[i * ROWS_BM + r]);
+            int ex = max(E_MIN, need_word(w, e.q));
+            if (tid < 32 && m < M) {
+                ex = clamp_exp_flag(ex, e.flags);
+                e.ye[m] = (int8_t)ex;
+            }
+            inv[a] = pow2(-min(ex, E_MAX));
+        }
+        if constexpr (!C::KEEP) {
+            // nothing of the first pass is kept
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll
+                for (int b = 0; b < NI; ++b) asm volatile("" : "+v"(acc[a][b]));
+        }
+#pragma unroll
+        for (int b = 0; b < NI; ++b)
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                double(&y)[2][4] = yk[C::KEEP ? b * 4 + h : 0];
+                if constexpr (!C::KEEP) quad(b, h, y);
+#pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                    uint32_t o = pack4(mant_of(y[a][0], inv[a]), mant_of(y[a][1], inv[a]), mant_of(y[a][2], inv[a]),
+                                       mant_of(y[a][3], inv[a]));
+                    if (e.relu) o = relu4(o);
+                    *(uint32_t *)(lds + ort + a * 32 * RP + b * 32 + 8 * h) = o;
+                }
+                if (h & 1) __builtin_amdgcn_sched_barrier(0);
+                if (b == NI - 1 && h == 3) {
+                    // most of y is gone: room for the next tile's loads
+                    fetch_x(next, 0, xn);
+                    fetch_r(next, rn);
+                }
+            }
+        __syncthreads();
+        const bool vec = (N & 15) == 0 && ((uintptr_t)e.y & 15) == 0;
+#pragma unroll
+        for (int i = 0; i < RR; ++i) {
+            const int q = i * ROWS_THR + tid, row = q / CPR, c = q % CPR * 16;
+            if (m0 + row < M && c < N) {
+                uint32_t v[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = *(const uint32_t *)(rt + row * RP + c + 4 * k);
+                int8_t *dst = e.y + (long long)(m0 + row) * N;
+                if (vec) *(v4i *)(dst + c) = v4i{(int)v[0], (int)v[1], (int)v[2], (int)v[3]};
+                else store_run<16>(dst, c, N, v);
+            }
+        }
+        __syncthreads();  // the result is stored
+        store_x(xn);
+        store_r(next, rn);
+    }
+}
+
+hipError_t launch_rows_add(const int8_t *x, const int8_t *w, int M, int N, int K, int Kp, int8_t *wt, int ni,
+                           const AddEpi &e, hipStream_t st) {
+    const int ks = rows_steps(Kp), tiles = (M + ROWS_BM - 1) / ROWS_BM;
+    prof_begin(st, PROF_GEMM_ADD);
+    hipLaunchKernelGGL(tile_weight_kernel, dim3(8 * ni, ks / 4), dim3(256), 0, st, w, N, K, ks, wt);
+    const dim3 grid(std::min(tiles, ni == 1 ? 2 * NCU : NCU)), block(ROWS_THR);
+    auto go = [&](auto ni_tag, auto kc_tag) {
+        constexpr int NI = decltype(ni_tag)::value, KC = decltype(kc_tag)::value;
+        if (e.r) hipLaunchKernelGGL((rows_add_kernel<NI, KC, true>), grid, block, 0, st, x, wt, M, N, Kp, ks, e);
+        else hipLaunchKernelGGL((rows_add_kernel<NI, KC, false>), grid, block, 0, st, x, wt, M, N, Kp, ks, e);
+    };
+#define IE_CASE(NI_, KC_) go(std::integral_constant<int, NI_>{}, std::integral_constant<int, KC_>{})
+    // a short contraction takes its steps only
+    const bool brief = ks <= 8;
+    if (ni == 1 && brief) IE_CASE(1, 8);
+    else if (ni == 1) IE_CASE(1, 16);
+    else if (ni == 2 && brief) IE_CASE(2, 8);
+    else if (ni == 2) IE_CASE(2, 32);
+    else if (ni == 3 && brief) IE_CASE(3, 8);
+    else if (ni == 3) IE_CASE(3, 32);
+    else if (brief) IE_CASE(4, 8);
+    else IE_CASE(4, 32);
+#undef IE_CASE
+    prof_end(st, PROF_GEMM_ADD);
+    return hipGetLastError();
+}
+
+}  // namespace ie

@@ -181,7 +181,7 @@ __global__ __launch_bounds__(norm_block<T>()) void norm_fwd_kernel(NormFwd p) {
     }
     double inv = 0.0;  // of a whole-tensor result
     if (p.mode == NORM_ROUND) inv = pow2(-whole_exp<BT>(p.bmax, p.n_bmax, p.oe, p.flags, shi));
-    MaxMag run;  // of this thread's rows (NORM_NEED)
+    int run = 0;  // high word of the largest magnitude (NORM_NEED)
     for (long long r0 = (long long)blockIdx.x * RPB; r0 < p.rows; r0 += step) {
         const long long row = r0 + slot;
         const bool ok = row < p.rows;
@@ -210,11 +210,10 @@ __global__ __launch_bounds__(norm_block<T>()) void norm_fwd_kernel(NormFwd p) {
             } else {
                 y[j] = (d * st.r) * gam[j] + bet[j];
             }
-            mx.add(y[j]);
+            if (j % 2) mx.add(y[j - 1], y[j]);
         }
         if (p.mode == NORM_NEED) {
-                run.hi = max(run.hi, mx.hi);
-            run.neg = max(run.neg, mx.neg);
+                run = max(run, mx.word());
             continue;
         }
         if (p.mode == NORM_ROWS) {
@@ -233,7 +232,7 @@ __global__ __launch_bounds__(norm_block<T>()) void norm_fwd_kernel(NormFwd p) {
         cols.store(p.out + row * n, w);
     }
     if (p.mode == NORM_NEED) {
-        const int m = row_reduce<BT>(run.word(), Max{}, shi);
+        const int m = row_reduce<BT>(run, Max{}, shi);
         if (threadIdx.x == 0) p.bmax[blockIdx.x] = need_word(m, p.q);
     }
 }
@@ -387,7 +386,7 @@ void norm_bwd_kernel(NormBwd p) {
         }
         MaxMag mx;
 #pragma unroll
-        for (int j = 0; j < E; ++j) mx.add(g[j]);
+        for (int j = 0; j < E; j += 2) mx.add(g[j], g[j + 1]);
         const int scale = ey + gtop - ex;  // the row's results are g 2^scale
         if (p.mode == NORM_NEED) {
             if (mx.word()) run = max(run, mx.word() + (scale << 20));

@@ -361,6 +361,18 @@ Plan plan_add(long long M, long long N, long long K, int row_group, const Force 
     return p;
 }
 
+// Rows of 129..1024 results and contractions up to 2048 (a narrower row fits
+// the tiles' direct form: 100000 x 64 x 256, 11.9 us there, 20.4 here; over a
+// longer contraction the weight, streamed again for every 64 rows, takes what
+// the second pass cost: 25216 x 768 x 4096, 113.7 us here, 116.9 there, 8192 x
+// 1024 x 4096, 70.7 and 54.0), from as many rows on as fill the CUs in the time
+// of one workgroup: x 768 x 192, 11.0 us here at 2048 rows, 12.5 by tiles; x
+// 768 x 768, 21.3 here at 6144 rows, 25.1 by tiles, but 21.4 and 19.6 at 4096.
+int rows_plan(long long M, long long N, long long K, int row_group, const Force &f) {
+    if (f.on || !row_group || N <= 128 || N > 1024 || K < 16 || K > 2048) return 0;
+    return M >= (K <= 256 || N <= 256 ? 2048 : 6144) ? cdiv(N, 256) : 0;
+}
+
 DgradPlan plan_dgrad(const ConvGeom &g, int row_group, const Force &f, bool weight_in_place) {
     DgradPlan d;
     memset(&d, 0, sizeof d);
@@ -590,6 +602,7 @@ LinearFusedWs carve_linear_fused(Carve &c, long long M, long long N, long long K
     w.l.pw.partial = c.take<int>(n.partial);
     w.l.pw.n = n;
     w.bmax = c.take<int>(SPLIT_ADD_BLOCKS);
+    if (const int ni = rows_plan(M, N, Kp, 1, f)) w.wt = c.take<int8_t>(rows_weight(ni, Kp));
     return w;
 }
 

@@ -224,6 +224,14 @@ Plan plan_batched(long long Z, long long M, long long N, bool kk);
 // with them; a forced one is refused).
 Plan plan_add(long long M, long long N, long long K, int row_group, const Force &f);
 
+// The product with bias and residual whose workgroups hold whole result rows
+// (256 rows_plan columns; 0: not taken).
+int rows_plan(long long M, long long N, long long K, int row_group, const Force &f);
+// Its contraction steps of 32 bytes, a multiple of 4, and the bytes of the
+// weight in its layout.
+inline int rows_steps(long long K) { return (int)((K + 127) / 128 * 4); }
+inline size_t rows_weight(int ni, long long K) { return (size_t)ni * 256 * 32 * rows_steps(K); }
+
 // A plan is valid when its kernel is built, its chunks cover the contraction
 // (exact int32 partials for splits), and a direct epilogue holds every group
 // in one tile.
@@ -301,6 +309,7 @@ LinearFwdWs carve_linear_fwd(Carve &c, long long M, long long N, long long K, co
 constexpr int SPLIT_ADD_BLOCKS = 1024;
 struct LinearFusedWs {
     LinearFwdWs l;
+    int8_t *wt;  // the weight as the whole-row kernel reads it
     int *bmax;  // block maxima of a split whole-tensor result
 };
 LinearFusedWs carve_linear_fused(Carve &c, long long M, long long N, long long K, const Force &f);

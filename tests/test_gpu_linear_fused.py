@@ -240,3 +240,100 @@ def test_linear_fused_stream_and_graph():
         for (X, D), (M, N, K, yg, W, b, *_, Y) in zip(hosts, cases):
             assert_same(Y, o.linear_fwd_fused(X, W, b, D, yg, True), f"replay {i}")
     assert own.status() == 0
+
+
+# (M, N, K) whose rows lie whole in a workgroup: 1..4 blocks of 256 columns,
+# short and staged contractions (K over 1024 in two stages), one and several
+# tiles to a workgroup, the last one ragged
+ROWS = [(2048, 129, 16), (2049, 256, 1040), (33000, 130, 40), (6145, 300, 1030), (2063, 511, 256), (16500, 512, 33),
+        (6160, 520, 300), (17001, 768, 96), (2100, 770, 192), (6144, 1000, 2048), (16449, 1024, 130)]
+
+
+@pytest.mark.parametrize("shape", ROWS, ids=lambda s: "x".join(map(str, s)))
+def test_linear_fused_many_rows(shape, ws):
+    M, N, K = shape
+    announce(f"linear fused rows {shape}")
+    rng = np.random.default_rng(M + N + K)
+    for xg, wg, dg, relu, some in ((R, R, R, True, 3), (T, R, T, False, 3), (R, T, R, False, 2), (T, T, T, True, 1)):
+        X, W = rand_qt(rng, (M, K), xg), rand_qt(rng, (N, K), wg)
+        X.mant[M // 2] = 0
+        b = vec(rng, N, R if some == 3 else T) if some & 1 else None
+        D = rand_qt(rng, (M, N), dg, -10, 2) if some & 2 else None
+        check(X, W, b, D, R, relu, ws, bits=8 if some & 1 else 5, what=f"{shape} {some}")
+
+
+@pytest.mark.parametrize("gap", [-120, -60, -25, 0, 25, 60, 120])
+@pytest.mark.parametrize("shape", [(2070, 140, 64), (2050, 900, 48)], ids=lambda s: "x".join(map(str, s)))
+def test_linear_fused_many_rows_far_exponents(gap, shape, ws):
+    announce(f"linear fused rows gap {gap} {shape}")
+    M, N, K = shape
+    rng = np.random.default_rng(gap + 300)
+    X, W = rand_qt(rng, (M, K), R, -6, -6), rand_qt(rng, (N, K), R, -6, -6)
+    X.mant[1], W.mant[2], X.mant[3], W.mant[3] = 0, 0, -128, -128
+    e = np.clip(-12 + gap, -128, 110)
+    b = o.QT(rng.integers(-128, 128, (N, 1)).astype(np.int8), np.full(N, e, np.int8), R)
+    b.mant[::3] = 0
+    D = o.QT(rng.integers(-128, 128, (M, N)).astype(np.int8), np.full(M, np.clip(-12 - gap, -128, 110), np.int8), R)
+    D.mant[1], D.mant[:, 5] = 0, 0
+    for bb, dd in ((b, D), (b, None), (None, D)):
+        check(X, W, bb, dd, R, False, ws, what=f"gap {gap}")
+
+
+@pytest.mark.parametrize("k", [0, 1, 2, 8])
+@pytest.mark.parametrize("shape", [(2070, 208, 64), (2070, 323, 32), (17000, 528, 80)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_linear_fused_many_rows_guards(k, shape, ws):
+    """Residual, bias and result at odd addresses; nothing written beside the result."""
+    announce(f"linear fused rows {shape} off by {k}")
+    M, N, K = shape
+    rng = np.random.default_rng(k)
+    X, W = rand_qt(rng, (M, K), R), rand_qt(rng, (N, K), R)
+    b, D = vec(rng, N, R), rand_qt(rng, (M, N), R, -10, 2)
+
+    def at(a, fill=False):
+        buf = torch.full((a.size + 64,), 77, dtype=torch.int8, device="cuda")
+        v = buf[16 + k:16 + k + a.size].view(a.shape)
+        if not fill:
+            v.copy_(torch.from_numpy(a))
+        return buf, v
+    mk = lambda t: ie.Mat(at(t.mant)[1], at(t.exp)[1], t.group)  # noqa: E731
+    (bm, vm), (be, ve) = at(D.mant, True), at(np.zeros(M, np.int8), True)
+    ie.ie_linear_fwd_fused(qt_to_dev(X), qt_to_dev(W), mk(b), mk(D), ie.Mat(vm, ve, R), ie.ACT_RELU, ws)
+    assert_same(ie.Mat(vm, ve, R), o.linear_fwd_fused(X, W, b, D, R, True), str(shape))
+    for buf, n in ((bm, M * N), (be, M)):
+        assert bool((buf[:16 + k] == 77).all()) and bool((buf[16 + k + n:] == 77).all())
+
+
+def test_linear_fused_many_rows_flag_and_graph():
+    """The exponent-range flag, then replays on new inputs, eager work between them."""
+    announce("linear fused rows flag and graph")
+    rng = np.random.default_rng(8)
+    own = ie.Workspace("cuda")
+    M, N, K = 2100, 200, 64
+    W, b = rand_qt(rng, (N, K), R), vec(rng, N, R)
+    Wd, bd = qt_to_dev(W), dev(b)
+    Xd, Dd, Y = ie.Mat.empty(M, K, R), ie.Mat.empty(M, N, R), ie.Mat.empty(M, N, R)
+    X, D = rand_qt(rng, (M, K), R, 126, 127), rand_qt(rng, (M, N), R)
+
+    def put():
+        for d, h in ((Xd, X), (Dd, D)):
+            d.mant.copy_(torch.from_numpy(h.mant))
+            d.exp.copy_(torch.from_numpy(h.exp))
+
+    def run():
+        ie.ie_linear_fwd_fused(Xd, Wd, bd, Dd, Y, ie.ACT_NONE, own)
+    put()
+    W2 = qt_to_dev(o.QT(W.mant, np.full(N, 30, np.int8), R))
+    ie.ie_linear_fwd_fused(Xd, W2, bd, Dd, Y, ie.ACT_NONE, own)
+    assert own.status() == ie.FLAG_EXP_RANGE and own.status() == 0
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+        run()
+    for i in range(3):
+        X, D = rand_qt(rng, (M, K), R), rand_qt(rng, (M, N), R, -10, 2)
+        put()
+        graph.replay()
+        assert_same(Y, o.linear_fwd_fused(X, W, b, D, R), f"replay {i}")
+        check(X, W, b, D, R, True, own)
+    assert own.status() == 0
