@@ -16,7 +16,7 @@ LIB = os.path.join(HERE, "libie.so")
 SOURCES = ["ie_api.hip", "ie_aux.hip", "ie_update.hip", "ie_gemm_kk.hip", "ie_gemm_im2col.hip",
            "ie_gemm_dgrad.hip", "ie_gemm_dgrad_wt.hip", "ie_gemm_wgrad.hip", "ie_gemm_pair.hip",
            "ie_gemm_pair_al.hip", "ie_pointwise.hip", "ie_gemm_batched.hip", "ie_norm.hip", "ie_dropout.hip",
-           "ie_gemm_add.hip", "ie_gemm_rows.hip"]
+           "ie_gemm_add.hip", "ie_gemm_rows.hip", "ie_gemm_few.hip"]
 # host-only C++ (planner, argument checks, workspace layout): no GPU code
 HOST_SOURCES = ["ie_plan.cpp"]
 CXX = os.environ.get("CXX", "g++")

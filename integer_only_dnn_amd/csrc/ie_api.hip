@@ -1108,6 +1108,7 @@ ie_status ie_linear_fwd_fused(const ie_mat *X, const ie_mat *W, const ie_mat *bi
     const LinearFusedWs w = carve_linear_fused(c, M, N, K, f);
     const long long Kp = r16(K);
     const int rows = rows_plan(M, N, Kp, rg, f);
+    const bool few = few_plan(M, N, Kp, f);
     const Plan pl = plan_add(M, N, Kp, rg, f);
     IE_CHECK(checked_plan(pl, M, N, Kp, rg, FAM_ADD, w.l.pw.n, add_needs(pl, M, N, Kp, rg)));
     log_plan("dense add", M, N, Kp, pl);
@@ -1115,7 +1116,7 @@ ie_status ie_linear_fwd_fused(const ie_mat *X, const ie_mat *W, const ie_mat *bi
     if (Kp != K) {
         IE_TRY(launch_pad_rows(X->mant, M, K, nullptr, 0, nullptr, Kp, w.l.xp, st));
         xs = w.l.xp;
-        if (!rows) {
+        if (!rows && !few) {
             IE_TRY(launch_pad_rows(W->mant, N, K, nullptr, 0, nullptr, Kp, w.l.wp, st));
             wsrc = w.l.wp;
         }
@@ -1140,6 +1141,7 @@ ie_status ie_linear_fwd_fused(const ie_mat *X, const ie_mat *W, const ie_mat *bi
     e.q = mat_q(Y);
     e.relu = act == IE_ACT_RELU;
     e.flags = (uint32_t *)ws;
+    if (few) return hip_status(launch_few_add(xs, W->mant, (int)M, (int)N, (int)K, (int)Kp, w.few_acc, w.few_w, e, st));
     if (rows) return hip_status(launch_rows_add(xs, W->mant, (int)M, (int)N, (int)K, (int)Kp, w.wt, rows, e, st));
     if (pl.mode == PLAN_SPLIT) {
         Epi ep;

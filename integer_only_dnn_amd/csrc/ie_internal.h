@@ -353,6 +353,10 @@ hipError_t launch_gemm_add(const Operand &A, const Operand &B, int M, int N, int
 // Kp], w [N x K], wt: rows_weight(ni, Kp) bytes of scratch.
 hipError_t launch_rows_add(const int8_t *x, const int8_t *w, int M, int N, int K, int Kp, int8_t *wt, int ni,
                            const AddEpi &e, hipStream_t st);
+// The same for M <= FEW_ROWS rows (ie_gemm_few.hip): x [M x Kp], w [N x K],
+// acc: M r16(N) ints, word: M r16(N) / 16 ints.
+hipError_t launch_few_add(const int8_t *x, const int8_t *w, int M, int N, int K, int Kp, int *acc, int *word,
+                          const AddEpi &e, hipStream_t st);
 // The same epilogue on int32 partial sums [splits][M][N].
 hipError_t launch_split_add(const AddEpi &e, const int *partial, int splits, int M, int N, int *bmax, hipStream_t st);
 

@@ -355,7 +355,12 @@ Plan plan_product(long long M, long long N, long long K, int row_group, int fami
     return best;
 }
 
+// One 128 x 128 tile over a short contraction rounds in its own pass: 64 x 128
+// x 256 takes 6.8 us, 8.7 in 64 x 64 tiles with the pass that closes them.
+static bool one_tile(long long M, long long N, long long K) { return M <= 128 && N <= 128 && K <= 256; }
+
 Plan plan_add(long long M, long long N, long long K, int row_group, const Force &f) {
+    if (!f.on && one_tile(M, N, K) && (M > 64 || N > 64)) return Plan{Tile{2, 2}, PLAN_DIRECT, 1, chunk_for(K, 1)};
     Plan p = plan_product(M, N, K, row_group, FAM_ADD, f);
     if (!f.on && p.mode == PLAN_RECOMP) p.mode = PLAN_RTO;
     return p;
@@ -371,6 +376,15 @@ Plan plan_add(long long M, long long N, long long K, int row_group, const Force 
 int rows_plan(long long M, long long N, long long K, int row_group, const Force &f) {
     if (f.on || !row_group || N <= 128 || N > 1024 || K < 16 || K > 2048) return 0;
     return M >= (K <= 256 || N <= 256 ? 2048 : 6144) ? cdiv(N, 256) : 0;
+}
+
+// Up to 64 rows, unless their results are so many that the tiles fill the chip
+// (64 x 32000 x 768: 35.8 us here, 29.3 by tiles; 64 x 4096 x 4096: 16.3 and
+// 28.4; 5 x 4096 x 4096: 9.7 and 23.8) or so few columns are so long that
+// splitting them fills more of it (8 x 128 x 16384: 16.6 here, 12.3 split; 4 x
+// 512 x 8192: 10.6 and 12.4); one tile's worth is left to one launch.
+bool few_plan(long long M, long long N, long long K, const Force &f) {
+    return !f.on && M <= FEW_ROWS && K >= 16 && M * N <= 1 << 18 && K <= 32 * N && !one_tile(M, N, K);
 }
 
 DgradPlan plan_dgrad(const ConvGeom &g, int row_group, const Force &f, bool weight_in_place) {
@@ -602,6 +616,10 @@ LinearFusedWs carve_linear_fused(Carve &c, long long M, long long N, long long K
     w.l.pw.partial = c.take<int>(n.partial);
     w.l.pw.n = n;
     w.bmax = c.take<int>(SPLIT_ADD_BLOCKS);
+    if (few_plan(M, N, Kp, f)) {
+        w.few_acc = c.take<int>((size_t)M * r16(N));
+        w.few_w = c.take<int>((size_t)M * (r16(N) / 16));
+    }
     if (const int ni = rows_plan(M, N, Kp, 1, f)) w.wt = c.take<int8_t>(rows_weight(ni, Kp));
     return w;
 }

@@ -232,6 +232,10 @@ int rows_plan(long long M, long long N, long long K, int row_group, const Force 
 inline int rows_steps(long long K) { return (int)((K + 127) / 128 * 4); }
 inline size_t rows_weight(int ni, long long K) { return (size_t)ni * 256 * 32 * rows_steps(K); }
 
+// The product with bias and residual of a few rows that reads the weight once.
+constexpr int FEW_ROWS = 64;
+bool few_plan(long long M, long long N, long long K, const Force &f);
+
 // A plan is valid when its kernel is built, its chunks cover the contraction
 // (exact int32 partials for splits), and a direct epilogue holds every group
 // in one tile.
@@ -309,8 +313,9 @@ LinearFwdWs carve_linear_fwd(Carve &c, long long M, long long N, long long K, co
 constexpr int SPLIT_ADD_BLOCKS = 1024;
 struct LinearFusedWs {
     LinearFwdWs l;
-    int8_t *wt;  // the weight as the whole-row kernel reads it
-    int *bmax;  // block maxima of a split whole-tensor result
+    int8_t *wt;            // the weight as the whole-row kernel reads it
+    int *few_acc, *few_w;  // sums and maxima of a few rows
+    int *bmax;             // block maxima of a split whole-tensor result
 };
 LinearFusedWs carve_linear_fused(Carve &c, long long M, long long N, long long K, const Force &f);
 

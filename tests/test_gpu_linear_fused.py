@@ -337,3 +337,101 @@ def test_linear_fused_many_rows_flag_and_graph():
         assert_same(Y, o.linear_fwd_fused(X, W, b, D, R), f"replay {i}")
         check(X, W, b, D, R, True, own)
     assert own.status() == 0
+
+
+# up to 64 rows: 1, 2 and 4 blocks of 16, short and long contractions, columns
+# off the blocks of 16 and the runs of 4, contractions off the runs of 16;
+# beside them single tiles and splits over several rows
+FEW = [(1, 65, 16), (1, 4096, 4096), (2, 130, 1024), (16, 257, 1025), (17, 300, 2000), (32, 1030, 17), (33, 77, 2064),
+       (64, 129, 63), (64, 1000, 1500), (5, 4099, 4100), (3, 2050, 65536), (16, 16000, 48), (65, 66, 256),
+       (128, 128, 200), (6, 60, 2048), (70, 200, 2048), (100, 333, 1039)]
+
+
+@pytest.mark.parametrize("shape", FEW, ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("yg", [T, R])
+def test_linear_fused_few_rows(shape, yg, ws):
+    M, N, K = shape
+    announce(f"linear fused few rows {shape} {yg}")
+    rng = np.random.default_rng(M + N + K)
+    for xg, wg, dg, some in ((R, R, R, 3), (T, R, T, 2), (R, T, R, 1), (T, T, T, 3)):
+        X, W = rand_qt(rng, (M, K), xg), rand_qt(rng, (N, K), wg)
+        X.mant[M // 2] = 0
+        b = vec(rng, N, R if some == 3 else T) if some & 1 else None
+        D = rand_qt(rng, (M, N), dg, -10, 2) if some & 2 else None
+        check(X, W, b, D, yg, some == 3, ws, bits=8 if some & 1 else 5, what=f"{shape} {some}")
+
+
+@pytest.mark.parametrize("gap", [-120, -60, -25, 0, 25, 60, 120])
+@pytest.mark.parametrize("shape", [(9, 140, 64), (40, 131, 2048), (6, 60, 2048), (70, 130, 128)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_linear_fused_few_rows_far_exponents(gap, shape, ws):
+    announce(f"linear fused few rows gap {gap} {shape}")
+    M, N, K = shape
+    rng = np.random.default_rng(gap + 400)
+    X, W = rand_qt(rng, (M, K), R, -6, -6), rand_qt(rng, (N, K), R, -6, -6)
+    X.mant[1], W.mant[2], X.mant[3], W.mant[3] = 0, 0, -128, -128
+    e = np.clip(-12 + gap, -128, 110)
+    b = o.QT(rng.integers(-128, 128, (N, 1)).astype(np.int8), np.full(N, e, np.int8), R)
+    b.mant[::3] = 0
+    D = o.QT(rng.integers(-128, 128, (M, N)).astype(np.int8), np.full(M, np.clip(-12 - gap, -128, 110), np.int8), R)
+    D.mant[1], D.mant[:, 5] = 0, 0
+    for yg, bb, dd in ((R, b, D), (T, b, D), (R, b, None), (T, None, D)):
+        check(X, W, bb, dd, yg, False, ws, what=f"gap {gap}")
+
+
+@pytest.mark.parametrize("k", [0, 1, 4])
+@pytest.mark.parametrize("shape", [(3, 131, 48), (50, 272, 1200), (7, 31, 2048)], ids=lambda s: "x".join(map(str, s)))
+def test_linear_fused_few_rows_guards(k, shape, ws):
+    """Residual, bias and result at odd addresses; nothing written beside the result."""
+    announce(f"linear fused few rows {shape} off by {k}")
+    M, N, K = shape
+    rng = np.random.default_rng(k)
+    X, W = rand_qt(rng, (M, K), R), rand_qt(rng, (N, K), R)
+    b, D = vec(rng, N, R), rand_qt(rng, (M, N), R, -10, 2)
+
+    def at(a, fill=False):
+        buf = torch.full((a.size + 64,), 77, dtype=torch.int8, device="cuda")
+        v = buf[16 + k:16 + k + a.size].view(a.shape)
+        if not fill:
+            v.copy_(torch.from_numpy(a))
+        return buf, v
+    mk = lambda t: ie.Mat(at(t.mant)[1], at(t.exp)[1], t.group)  # noqa: E731
+    for yg in (T, R):
+        (bm, vm), (be, ve) = at(D.mant, True), at(np.zeros(M if yg == R else 1, np.int8), True)
+        ie.ie_linear_fwd_fused(qt_to_dev(X), qt_to_dev(W), mk(b), mk(D), ie.Mat(vm, ve, yg), ie.ACT_RELU, ws)
+        assert_same(ie.Mat(vm, ve, yg), o.linear_fwd_fused(X, W, b, D, yg, True), str(shape))
+        for buf, n in ((bm, M * N), (be, ve.numel())):
+            assert bool((buf[:16 + k] == 77).all()) and bool((buf[16 + k + n:] == 77).all())
+
+
+@pytest.mark.parametrize("yg", [T, R])
+def test_linear_fused_few_rows_flag_and_graph(yg):
+    """The exponent-range flag, then replays on new inputs, eager work between them."""
+    announce(f"linear fused few rows flag and graph {yg}")
+    rng = np.random.default_rng(9)
+    own = ie.Workspace("cuda")
+    M, N, K = 4, 200, 64
+    W, b = rand_qt(rng, (N, K), R), vec(rng, N, R)
+    Wd, bd = qt_to_dev(W), dev(b)
+    Xd, Dd, Y = ie.Mat.empty(M, K, R), ie.Mat.empty(M, N, R), ie.Mat.empty(M, N, yg)
+    X, D = rand_qt(rng, (M, K), R, 126, 127), rand_qt(rng, (M, N), R)
+
+    def put():
+        for d, h in ((Xd, X), (Dd, D)):
+            d.mant.copy_(torch.from_numpy(h.mant))
+            d.exp.copy_(torch.from_numpy(h.exp))
+    put()
+    W2 = qt_to_dev(o.QT(W.mant, np.full(N, 30, np.int8), R))
+    ie.ie_linear_fwd_fused(Xd, W2, bd, Dd, Y, ie.ACT_NONE, own)
+    assert own.status() == ie.FLAG_EXP_RANGE and own.status() == 0
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(2):
+            ie.ie_linear_fwd_fused(Xd, Wd, bd, Dd, Y, ie.ACT_NONE, own)
+    for i in range(3):
+        X, D = rand_qt(rng, (M, K), R), rand_qt(rng, (M, N), R, -10, 2)
+        put()
+        graph.replay()
+        assert_same(Y, o.linear_fwd_fused(X, W, b, D, yg), f"replay {i}")
+        check(X, W, b, D, yg, True, own)
+    assert own.status() == 0
