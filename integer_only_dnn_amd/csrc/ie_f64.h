@@ -25,6 +25,12 @@ __device__ __forceinline__ int mant_of(double v, double inv) {
     return __double2loint(__builtin_fma(v, inv, ROUND_MAGIC));
 }
 
+// N C - S of byte k of w ^ 0x80808080 (C + 128), s128 = S + 128 N: exact, every
+// term below 2^23, and the byte is taken by the conversion itself.
+__device__ __forceinline__ double centred(uint32_t w, int k, float n, float s128) {
+    return (double)__builtin_fmaf((float)(w >> (8 * k) & 255u), n, -s128);
+}
+
 // The low bytes of four words.
 __device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
     const uint32_t lo = __builtin_amdgcn_perm((uint32_t)b, (uint32_t)a, 0x0c0c0400u);
@@ -111,6 +117,21 @@ __device__ __forceinline__ V row_reduce(V v, F f, V *sh) {
     v = lane_reduce<(T < 64 ? T : 64)>(v, f);
     if constexpr (T > 64) {
         __syncthreads();
+        if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = sh[0];
+#pragma unroll
+        for (int i = 1; i < T / 64; ++i) v = f(v, sh[i]);
+    }
+    return v;
+}
+
+// The same with one barrier: `sh` is not written again before the block has
+// met at another one.
+template <int T, class V, class F>
+__device__ __forceinline__ V row_reduce_once(V v, F f, V *sh) {
+    v = lane_reduce<(T < 64 ? T : 64)>(v, f);
+    if constexpr (T > 64) {
         if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
         __syncthreads();
         v = sh[0];

@@ -78,6 +78,7 @@ struct Cols {
 };
 
 // The statistics of a row held four mantissas to a word (zeros past its end).
+// `sh` is another one than the row's before: threads may still read that.
 template <int T, int W>
 __device__ __forceinline__ RowStat row_stat(const uint32_t (&w)[W], int n, double n2eps, int eps_e, int e, int2 *sh) {
     int s = 0, q = 0;
@@ -89,7 +90,6 @@ __device__ __forceinline__ RowStat row_stat(const uint32_t (&w)[W], int n, doubl
     s = lane_reduce<(T < 64 ? T : 64)>(s, Add{});
     q = lane_reduce<(T < 64 ? T : 64)>(q, Add{});
     if constexpr (T > 64) {
-        __syncthreads();
         if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = make_int2(s, q);
         __syncthreads();
         s = q = 0;
@@ -141,8 +141,8 @@ __global__ __launch_bounds__(norm_block<T>()) void norm_fwd_kernel(NormFwd p) {
     using C = Cols<T, E>;
     constexpr int BT = norm_block<T>(), RPB = BT / T, W = E / 4;
     constexpr bool LDSV = T <= 64 && E > 12;
-    __shared__ int2 sh2[BT / 64];
-    __shared__ int shi[BT / 64];
+    __shared__ int2 sh2[2][BT / 64];
+    __shared__ int shi[BT / 64], shm[BT / 64];
     __shared__ double2 gb[LDSV ? T * E : 1];
     const int t = threadIdx.x % T, slot = threadIdx.x / T, n = p.cols;
     const long long step = (long long)gridDim.x * RPB;
@@ -182,6 +182,7 @@ __global__ __launch_bounds__(norm_block<T>()) void norm_fwd_kernel(NormFwd p) {
     double inv = 0.0;  // of a whole-tensor result
     if (p.mode == NORM_ROUND) inv = pow2(-whole_exp<BT>(p.bmax, p.n_bmax, p.oe, p.flags, shi));
     int run = 0;  // high word of the largest magnitude (NORM_NEED)
+    int turn = 0;
     for (long long r0 = (long long)blockIdx.x * RPB; r0 < p.rows; r0 += step) {
         const long long row = r0 + slot;
         const bool ok = row < p.rows;
@@ -195,14 +196,17 @@ __global__ __launch_bounds__(norm_block<T>()) void norm_fwd_kernel(NormFwd p) {
         if (p.mode == NORM_ROUND) {
             st = p.stat[ok ? row : p.rows - 1];
         } else {
-            st = row_stat<T>(w, n, p.n2eps, p.eps_e, e, sh2);
+            st = row_stat<T>(w, n, p.n2eps, p.eps_e, e, sh2[turn ^= 1]);
             if (p.mode == NORM_NEED && ok && t == 0) p.stat[row] = st;
         }
+        const float nf = (float)n, s128 = (float)st.s + 128.0f * nf;
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] ^= 0x80808080u;
         double y[E];
         MaxMag mx;
 #pragma unroll
         for (int j = 0; j < E; ++j) {
-            const double d = __builtin_fma((double)byte_of(w[j / 4], j % 4), (double)n, -st.s);
+            const double d = centred(w[j / 4], j % 4, nf, s128);
             // past the row gamma and beta are zero, and so is y
             if constexpr (LDSV) {
                 const double2 v = gb[j * T + t];
@@ -213,11 +217,11 @@ __global__ __launch_bounds__(norm_block<T>()) void norm_fwd_kernel(NormFwd p) {
             if (j % 2) mx.add(y[j - 1], y[j]);
         }
         if (p.mode == NORM_NEED) {
-                run = max(run, mx.word());
+            run = max(run, mx.word());
             continue;
         }
         if (p.mode == NORM_ROWS) {
-            int ex = max(E_MIN, need_word(row_reduce<T>(mx.word(), Max{}, shi), p.q));
+            int ex = max(E_MIN, need_word(row_reduce_once<T>(mx.word(), Max{}, shm), p.q));
             if (ok && t == 0) {
                 ex = clamp_exp_flag(ex, p.flags);
                 p.oe[row] = (int8_t)ex;
@@ -266,23 +270,16 @@ __device__ __forceinline__ int top_exp(const int8_t *e, int e_row, long long row
     return m;
 }
 
-// Rows of up to 64 threads share blocks of 512 in the backward pass: the
-// block's partial column sums are one row of p.pf / p.pb whatever its size.
-template <int T>
-constexpr int grad_block() {
-    return T > 64 ? T : 512;
-}
-
 // Backward: NORM_NEED and NORM_ROWS also add up the columns of dgamma and
 // dbeta (p.pf, p.pb: one row of partial sums per block).
 template <int T, int E>
-__global__ __launch_bounds__(grad_block<T>()) __attribute__((amdgpu_waves_per_eu(T > 512 ? 4 : 2)))
+__global__ __launch_bounds__(grad_block(T)) __attribute__((amdgpu_waves_per_eu(T > 512 ? 4 : 2)))
 void norm_bwd_kernel(NormBwd p) {
     using C = Cols<T, E>;
-    constexpr int BT = grad_block<T>(), RPB = BT / T, W = E / 4;
-    __shared__ int2 sh2[BT / 64];
-    __shared__ int shi[BT / 64];
-    __shared__ double shd[BT / 64];
+    constexpr int BT = grad_block(T), RPB = BT / T, W = E / 4;
+    __shared__ int2 sh2[2][BT / 64];
+    __shared__ int shi[BT / 64], shm[BT / 64];
+    __shared__ double shd[2][T > 64 ? BT / 64 : 1];
     const int t = threadIdx.x % T, slot = threadIdx.x / T, n = p.cols;
     const bool sums = p.pf && p.mode != NORM_ROUND, grad = p.out != nullptr;
     const long long step = (long long)gridDim.x * RPB;
@@ -329,6 +326,7 @@ void norm_bwd_kernel(NormBwd p) {
 #pragma unroll
     for (int j = 0; j < E; ++j) af[j] = 0.0, ab[j] = 0;
     int run = 0;  // high word of the largest magnitude (NORM_NEED)
+    int turn = 0;
     for (long long r0 = (long long)blockIdx.x * RPB; r0 < p.rows; r0 += step) {
         const long long row = r0 + slot;
         const bool ok = row < p.rows;
@@ -343,20 +341,23 @@ void norm_bwd_kernel(NormBwd p) {
         if (p.mode == NORM_ROUND) {
             gs = p.gstat[ok ? row : p.rows - 1];
         } else {
-            const RowStat st = row_stat<T>(w, n, p.n2eps, p.eps_e, ex, sh2);
+            const RowStat st = row_stat<T>(w, n, p.n2eps, p.eps_e, ex, sh2[turn ^= 1]);
             gs.s = st.s;
             gs.r = st.r;
         }
         const double r20 = gs.r * 1048576.0;  // h 2^20 = d (r 2^20)
         // a = dY at its largest exponent: rows past the end count for nothing
         const double as = ok ? pow2(max(ey - dtop, -64)) : 0.0;
+        const float nf = (float)n, s128 = (float)gs.s + 128.0f * nf;
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] ^= 0x80808080u;
         double f[E], g[E], g2 = 0.0;
         int g1 = 0;
 #pragma unroll
         for (int j = 0; j < E; ++j) {
-            const double d = __builtin_fma((double)byte_of(w[j / 4], j % 4), (double)n, -gs.s);
+            const double d = centred(w[j / 4], j % 4, nf, s128);
             const double c = (double)byte_of(v[j / 4], j % 4);
-            f[j] = rint_magic(d * r20);
+            f[j] = __builtin_rint(d * r20);
             g[j] = c * gam[j];
             if (sums) {
                 const double a = __builtin_fma(c, as, ROUND_MAGIC);
@@ -370,8 +371,17 @@ void norm_bwd_kernel(NormBwd p) {
             for (int i = 0; i < W; ++i) g1 = __builtin_amdgcn_sdot4((int)v[i], (int)gw[i], g1, false);
 #pragma unroll
             for (int j = 0; j < E; ++j) g2 = __builtin_fma(g[j], f[j], g2);
-            gs.g1 = (double)row_reduce<T>(g1, Add{}, shi);
-            gs.g2 = row_reduce<T>(g2, Add{}, shd) * 0x1p-40;
+            g1 = lane_reduce<(T < 64 ? T : 64)>(g1, Add{});
+            g2 = lane_reduce<(T < 64 ? T : 64)>(g2, Add{});
+            gs.g1 = (double)g1;
+            if constexpr (T > 64) {
+                if ((threadIdx.x & 63) == 0) shd[0][threadIdx.x >> 6] = gs.g1, shd[1][threadIdx.x >> 6] = g2;
+                __syncthreads();
+                gs.g1 = g2 = 0.0;
+#pragma unroll
+                for (int i = 0; i < T / 64; ++i) gs.g1 += shd[0][i], g2 += shd[1][i];
+            }
+            gs.g2 = g2 * 0x1p-40;
             if (p.mode == NORM_NEED && ok && t == 0) p.gstat[row] = gs;
         }
 #pragma unroll
@@ -394,7 +404,7 @@ void norm_bwd_kernel(NormBwd p) {
         }
         double in = inv * pow2(scale);
         if (p.mode == NORM_ROWS) {
-            const int need = need_word(row_reduce<T>(mx.word(), Max{}, shi), p.q);
+            const int need = need_word(row_reduce_once<T>(mx.word(), Max{}, shm), p.q);
             int eo = need == NEED_NONE ? E_MIN : max(E_MIN, need + scale);
             if (ok && t == 0) {
                 eo = clamp_exp_flag(eo, p.flags);
@@ -415,44 +425,64 @@ void norm_bwd_kernel(NormBwd p) {
     }
     if (!sums) return;
     // the block's column sums (a's low words carry nothing of ROUND_MAGIC)
-    long long *pf = p.pf + (long long)blockIdx.x * n;
-    int *pb = p.pb + (long long)blockIdx.x * n;
+    const int np = col_pitch(n);
+    long long *pf = p.pf + (long long)blockIdx.x * np;
+    int *pb = p.pb + (long long)blockIdx.x * np;
+    auto put = [&](int c, const double (&a)[4]) {
+        *(longlong2 *)(pf + c) = longlong2{(long long)a[0], (long long)a[1]};
+        *(longlong2 *)(pf + c + 2) = longlong2{(long long)a[2], (long long)a[3]};
+    };
     if constexpr (T > 64) {
 #pragma unroll
-        for (int j = 0; j < E; ++j) {
-            const int c = C::col(j, t);
-            if (c < n) {
-                pf[c] = (long long)af[j];
-                pb[c] = ab[j];
-            }
+        for (int i = 0; i < W; ++i) {
+            const int c = cols.col(4 * i);
+            if (c >= n) continue;
+            put(c, {af[4 * i], af[4 * i + 1], af[4 * i + 2], af[4 * i + 3]});
+            *(v4i *)(pb + c) = v4i{ab[4 * i], ab[4 * i + 1], ab[4 * i + 2], ab[4 * i + 3]};
         }
     } else {
-        // integer sums of the waves in LDS, so in any order
-        __shared__ unsigned long long lf[T * E];
-        __shared__ int lb[T * E];
-        for (int c = threadIdx.x; c < T * E; c += BT) lf[c] = 0, lb[c] = 0;
+        // the waves' sums meet in LDS, dgamma's and then dbeta's
+        __shared__ double sums_lds[BT / 64][T * E];
+        const int wave = threadIdx.x >> 6;
+        const bool mine = (threadIdx.x & 63) < T;
+        int(*ib)[T * E] = (int(*)[T * E])sums_lds;
+        auto rows_of_wave = [](auto a) {
+            if constexpr (T <= 16) a = swap_reduce<16>(a, Add{});
+            if constexpr (T <= 32) a = swap_reduce<32>(a, Add{});
+            return a;
+        };
+        // element j of thread c / CH % T holds column c
+        auto place = [](int c) { return (c / (C::CH * T) * C::CH + c % C::CH) * T + c / C::CH % T; };
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            const double a = rows_of_wave(af[j]);
+            if (mine) sums_lds[wave][j * T + t] = a;
+        }
+        __syncthreads();
+        for (int c = 4 * threadIdx.x; c < n; c += 4 * BT) {
+            double a[4] = {0.0, 0.0, 0.0, 0.0};
+            const int at = place(c);
+#pragma unroll
+            for (int i = 0; i < BT / 64; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) a[k] += sums_lds[i][at + k * T];
+            put(c, a);
+        }
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < E; ++j) {
-            double a = af[j];
-            int b = ab[j];
-            if constexpr (T <= 16) {
-                a = swap_reduce<16>(a, Add{});
-                b = swap_reduce<16>(b, Add{});
-            }
-            if constexpr (T <= 32) {
-                a = swap_reduce<32>(a, Add{});
-                b = swap_reduce<32>(b, Add{});
-            }
-            if ((threadIdx.x & 63) < T) {
-                atomicAdd(&lf[C::col(j, t)], (unsigned long long)(long long)a);
-                atomicAdd(&lb[C::col(j, t)], b);
-            }
+            const int a = rows_of_wave(ab[j]);
+            if (mine) ib[wave][j * T + t] = a;
         }
         __syncthreads();
-        for (int c = threadIdx.x; c < n; c += BT) {
-            pf[c] = (long long)lf[c];
-            pb[c] = lb[c];
+        for (int c = 4 * threadIdx.x; c < n; c += 4 * BT) {
+            v4i a = {0, 0, 0, 0};
+            const int at = place(c);
+#pragma unroll
+            for (int i = 0; i < BT / 64; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) a[k] += ib[i][at + k * T];
+            *(v4i *)(pb + c) = a;
         }
     }
 }
@@ -466,8 +496,8 @@ __global__ __launch_bounds__(1024) void tops_kernel(const int8_t *e, long long n
     if (threadIdx.x == 0) tops[blockIdx.x] = m;
 }
 
-#define IE_NORM_FWD(X)                                                                                           \
-    X(16, 4) X(16, 8) X(16, 12) X(16, 16) X(16, 24) X(16, 32) X(16, 48) X(32, 24) X(64, 4) X(64, 8) X(64, 12) X(64, 16)     \
+#define IE_NORM_FWD(X)                                                                                          \
+    X(16, 4) X(16, 8) X(16, 12) X(16, 16) X(16, 24) X(16, 32) X(16, 48) X(32, 24) X(64, 4) X(64, 8) X(64, 16)   \
     X(64, 24) X(64, 32) X(64, 48) X(256, 12) X(256, 16) X(256, 24) X(1024, 8) X(1024, 12) X(1024, 16)
 #define IE_NORM_BWD(X)                                                                                           \
     X(16, 4) X(16, 8) X(16, 12) X(16, 16) X(64, 4) X(64, 8) X(64, 12) X(64, 16) X(256, 8) X(256, 12) X(256, 16)    \
@@ -488,7 +518,7 @@ hipError_t launch_norm_bwd(const NormBwd &a, const NormPlan &pl, hipStream_t st)
     prof_begin(st, PROF_NORM_BWD);
 #define IE_CASE(T_, E_)       \
     if (pl.t == T_ && pl.e == E_) \
-        hipLaunchKernelGGL((norm_bwd_kernel<T_, E_>), dim3(pl.grid), dim3(grad_block<T_>()), 0, st, a);
+        hipLaunchKernelGGL((norm_bwd_kernel<T_, E_>), dim3(pl.grid), dim3(grad_block(T_)), 0, st, a);
     IE_NORM_BWD(IE_CASE)
 #undef IE_CASE
     prof_end(st, PROF_NORM_BWD);
@@ -561,7 +591,7 @@ __global__ __launch_bounds__(256) void col_sum_kernel(const int8_t *dy, const in
     __syncthreads();
     const int col = blockIdx.x * 256 + threadIdx.x;
     if (col < cols)
-        pb[(long long)blockIdx.y * cols + col] =
+        pb[(long long)blockIdx.y * col_pitch(cols) + col] =
             (int)(sh[0][threadIdx.x] + sh[1][threadIdx.x] + sh[2][threadIdx.x] + sh[3][threadIdx.x]);
 }
 
@@ -574,15 +604,15 @@ __global__ __launch_bounds__(1024) void col_finish_kernel(ColOut f, ColOut b, in
     const ColOut &o = blockIdx.y == 0 ? f : b;
     if (!o.m) return;
     const int lane = threadIdx.x & 15, grp = threadIdx.x >> 4;
-    const long long c = blockIdx.x * 16ll + lane;
+    const long long c = blockIdx.x * 16ll + lane, pitch = col_pitch(cols);
     long long s = 0;
     if (c < cols) {
         if (o.p64) {
 #pragma unroll 4
-            for (int i = grp; i < parts; i += 64) s += o.p64[(long long)i * cols + c];
+            for (int i = grp; i < parts; i += 64) s += o.p64[(long long)i * pitch + c];
         } else {
 #pragma unroll 4
-            for (int i = grp; i < parts; i += 64) s += o.p32[(long long)i * cols + c];
+            for (int i = grp; i < parts; i += 64) s += o.p32[(long long)i * pitch + c];
         }
     }
     s += __shfl_xor(s, 16);

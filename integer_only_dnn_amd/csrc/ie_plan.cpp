@@ -712,21 +712,28 @@ RowShape first_fit(const RowShape *s, int n, long long cols) {
 
 // Rows of up to 768 elements take 16 threads (four rows share a wave, its
 // reductions and its square root), longer ones a wave or a block.  With few
-// rows (NORM_FEW) a wave per row has the shorter chain of work.
+// rows (NORM_FEW) more threads per row make the shorter chain of work (3000 x
+// 768: 4.9 us with 32 threads, 5.4 with 16; 25216 x 768: 15.1 and 14.7).  As
+// many blocks as are resident, two or four a CU by their registers, so that
+// each keeps its parameters for several rows (25216 x 768 at 512, 1024 and 2048
+// blocks: 14.7, 15.2, 16.8 us; 50432 x 192: 11.5, 10.9, 12.5).
 NormPlan norm_fwd_plan(long long rows, long long cols) {
     static const RowShape many[] = {{16, 4},  {16, 8},  {16, 12}, {16, 16},  {16, 24},  {16, 32},   {16, 48}, {64, 16},
                                     {64, 24}, {64, 32}, {64, 48}, {256, 16}, {256, 24}, {1024, 8}, {1024, 12}, {1024, 16}};
-    static const RowShape few[] = {{64, 4},   {64, 8},   {64, 12},  {64, 16}, {256, 12},
+    static const RowShape few[] = {{64, 4},   {64, 8},   {32, 24},  {64, 16}, {256, 12},
                                    {256, 16}, {256, 24}, {1024, 8}, {1024, 12}, {1024, 16}};
     const RowShape s = rows >= NORM_FEW ? first_fit(many, sizeof many / sizeof *many, cols)
                                         : first_fit(few, sizeof few / sizeof *few, cols);
-    const long long rpb = s.t > 256 ? 1 : 256 / s.t, want = (rows + rpb - 1) / rpb, cap = s.t > 256 ? 512 : 2048;
+    const long long rpb = s.t > 256 ? 1 : 256 / s.t, want = (rows + rpb - 1) / rpb;
+    const long long cap = s.t >= 256 || s.e > 24 ? 2 * NCU : 4 * NCU;
     return NormPlan{s.t, s.e, (int)(want < 1 ? 1 : want > cap ? cap : want)};
 }
 
 // Each thread keeps the column sums of its elements, so at most 16; blocks of
-// 512 threads (of one row when it takes more than 64), about one a CU, each
-// leaving one row of partial sums.
+// 512 threads (of one row when it takes more than 64), eight waves a CU, each
+// block leaving one row of partial sums (50432 x 192 in 128, 256 and 512
+// blocks: 37.2, 26.4, 30.7 us; 4096 x 4096 in 256 and 512 of 256 threads: 56.3
+// and 46.5).
 NormPlan norm_bwd_plan(long long rows, long long cols) {
     static const RowShape many[] = {{16, 4},  {16, 8},   {16, 12},  {16, 16},  {64, 8},    {64, 12},   {64, 16},
                                     {256, 8}, {256, 12}, {256, 16}, {512, 12}, {512, 16}, {1024, 12}, {1024, 16}};
@@ -734,8 +741,8 @@ NormPlan norm_bwd_plan(long long rows, long long cols) {
                                    {256, 16}, {512, 12}, {512, 16}, {1024, 12}, {1024, 16}};
     const RowShape s = rows >= NORM_FEW ? first_fit(many, sizeof many / sizeof *many, cols)
                                         : first_fit(few, sizeof few / sizeof *few, cols);
-    const long long rpb = s.t > 64 ? 1 : 512 / s.t, want = (rows + rpb - 1) / rpb;
-    const long long cap = s.t == 256 || s.t == 512 ? 2 * NCU : NCU;
+    const long long rpb = s.t > 64 ? 1 : grad_block(s.t) / s.t, want = (rows + rpb - 1) / rpb;
+    const long long cap = s.t == 256 ? 2 * NCU : NCU;
     return NormPlan{s.t, s.e, (int)(want < 1 ? 1 : want > cap ? cap : want)};
 }
 
@@ -772,11 +779,11 @@ ColPlan col_plan(long long rows, long long cols) {
 
 static ColWs carve_cols(Carve &c, long long parts, long long cols, bool wide) {
     ColWs w{};
-    const size_t n = (size_t)(cols > 0 ? cols : 1);
+    const size_t n = (size_t)(cols > 0 ? cols : 1), np = (size_t)col_pitch((int)n);
     w.top = c.take<int>(1);
     w.tops = c.take<int>(TOPS_MAX);
-    if (wide) w.p64 = c.take<long long>((size_t)parts * n);
-    w.p32 = c.take<int>((size_t)parts * n);
+    if (wide) w.p64 = c.take<long long>((size_t)parts * np);
+    w.p32 = c.take<int>((size_t)parts * np);
     w.sums = c.take<long long>(2 * n);
     w.need = c.take<int>(2 * ((n + 15) / 16));
     return w;

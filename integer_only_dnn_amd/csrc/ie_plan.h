@@ -362,6 +362,12 @@ BmmWs carve_bmm(Carve &c, int form, long long Z, long long M, long long N, long 
 constexpr long long NORM_COLS_MAX = 16384;
 constexpr long long NORM_ROWS_MAX = 1ll << 27;  // dgamma sums stay below 2^62
 constexpr long long LONG_COLS_MAX = 1ll << 30;  // dropout, column sums: columns are walked in 32 bits
+// A row of partial column sums, in whole runs of four.
+constexpr int col_pitch(int cols) { return (cols + 3) & ~3; }
+// Threads of a block of the backward pass.  Rows of up to 64 threads share
+// one: its partial column sums are one row of partial sums whatever its size.
+constexpr int grad_block(int t) { return t > 64 ? t : 512; }
+
 struct NormPlan {
     int t, e, grid;
 };
@@ -387,7 +393,7 @@ int n_tops(long long rows, int e_row);
 struct ColWs {
     int *top;         // largest exponent of dY
     int *tops;        // [TOPS_MAX]
-    long long *p64;   // partial sums of dgamma [parts][cols]
+    long long *p64;   // partial sums of dgamma [parts][col_pitch(cols)]
     int *p32;         // partial sums of dbeta / db
     long long *sums;  // [2][cols]
     int *need;        // [2][ceil(cols / 16)]
