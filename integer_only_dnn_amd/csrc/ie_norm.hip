@@ -536,8 +536,8 @@ hipError_t launch_tops(const int8_t *e, long long n, int *tops, int n_tops, hipS
 // ---------------------------------------------------------------------------
 
 // Partial column sums of dY at its largest exponent: block (x, y) adds the
-// rows [y chunk, (y + 1) chunk) of columns 256 x .. 256 x + 255, four columns
-// per lane, every fourth row per wave, eight rows' loads in flight.
+// rows [y chunk, (y + 1) chunk) of columns 256 x .. 256 x + 255, 16 columns
+// per thread, four rows to a wave, four loads in flight.
 // A mantissa at shift s <= 7 is one conversion (of C + 128, unsigned) and one
 // fp32 fused multiply-add, exact before its only rounding, whose low bits are
 // the rounded integer above those of 1.5 * 2^23; these are summed as they
@@ -546,48 +546,51 @@ hipError_t launch_tops(const int8_t *e, long long n, int *tops, int n_tops, hipS
 __global__ __launch_bounds__(256) void col_sum_kernel(const int8_t *dy, const int8_t *e, int e_row, long long rows,
                                                       int cols, int chunk, const int *tops, int n_tops, int *top,
                                                       int *pb) {
-    constexpr int U = 8;
+    constexpr int U = 4, RPT = 16;  // rows of a block's trip: a thread takes every 16th
     __shared__ uint32_t sh[4][256];
     __shared__ int shi[4];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int c = blockIdx.x * 256 + lane * 4;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, slot = threadIdx.x >> 4;
+    const int c = blockIdx.x * 256 + (lane & 15) * 16;
     const long long r0 = (long long)blockIdx.y * chunk, r1 = min(rows, r0 + chunk);
     const int dtop = top_exp<256>(e, e_row, rows, tops, n_tops, shi);
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *top = dtop;
-    // four bytes may be read past a row's end wherever four more rows follow;
+    // 16 bytes may be read past a row's end wherever as many more rows follow;
     // sums of columns past the last are not kept
-    const bool whole = cols % 4 == 0 || r1 + 4 <= rows;
+    const bool whole = cols % 16 == 0 || r1 + 16 <= rows;
     const int c0 = c < cols ? c : 0;
-    uint32_t a[4] = {0, 0, 0, 0};
-    for (long long r = r0 + wave; r < r1; r += 4 * U) {
-        uint32_t w[U];
+    uint32_t a[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) a[k] = 0;
+    uint32_t n_add = 0;
+    for (long long r = r0 + slot; r < r1; r += RPT * U) {
+        uint32_t w[U][4];
         int s[U];
-        float f[U], k0[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const long long rr = min(r + 4 * u, r1 - 1);  // past the end: a row that counts for nothing
-            if (whole) __builtin_memcpy(w + u, dy + rr * cols + c0, 4);
-            else w[u] = load4(dy + rr * cols, c, cols);
+            const long long rr = min(r + RPT * u, r1 - 1);  // past the end: a row that counts for nothing
+            if (whole) __builtin_memcpy(w[u], dy + rr * cols + c0, 16);
+            else load_run<16>(dy + rr * cols, c, cols, w[u]);
             s[u] = e[e_row ? rr : 0];
         }
+        n_add += U;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            s[u] = r + 4 * u < r1 ? dtop - s[u] : 8;
-            f[u] = s[u] < 8 ? __builtin_ldexpf(1.0f, -s[u]) : 0.0f;
-            k0[u] = 12582912.0f - 128.0f * f[u];
-        }
+            const int sh = r + RPT * u < r1 ? dtop - s[u] : 8;
+            const float f = sh < 8 ? __builtin_ldexpf(1.0f, -sh) : 0.0f, k0 = 12582912.0f - 128.0f * f;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const uint32_t x = w[u] ^ 0x80808080u;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                a[k] += (uint32_t)__float_as_int(__builtin_fmaf((float)(x >> (8 * k) & 255u), f[u], k0[u]));
+            for (int k = 0; k < 16; ++k) {
+                const uint32_t x = w[u][k / 4] ^ 0x80808080u;
+                a[k] += (uint32_t)__float_as_int(__builtin_fmaf((float)(x >> (8 * (k % 4)) & 255u), f, k0));
+            }
         }
     }
-    // every trip added U constants
-    const uint32_t n_add = r1 > r0 + wave ? (uint32_t)((r1 - r0 - wave + 4 * U - 1) / (4 * U)) * U : 0u;
+    // every addition brought the constant along
 #pragma unroll
-    for (int k = 0; k < 4; ++k) sh[wave][lane * 4 + k] = a[k] - n_add * 0x4B400000u;
+    for (int k = 0; k < 16; ++k) {
+        int v = (int)(a[k] - n_add * 0x4B400000u);
+        v = swap_reduce<32>(swap_reduce<16>(v, Add{}), Add{});
+        if (lane < 16) sh[wave][lane * 16 + k] = (uint32_t)v;
+    }
     __syncthreads();
     const int col = blockIdx.x * 256 + threadIdx.x;
     if (col < cols)
