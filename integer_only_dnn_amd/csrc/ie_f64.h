@@ -189,4 +189,53 @@ __device__ __forceinline__ void store_run(int8_t *row, int c, int n, const uint3
     }
 }
 
+// The columns of a row that a thread holds when T threads share it, E each:
+// runs of CH neighbours (as wide as one load can be), run i of thread t from
+// column CH (i T + t).  Rows are read whole runs at a time: a run that crosses
+// the row's end takes in the next row's first bytes, one past it the row's
+// first ones, and `mask` clears both; only at the matrix's last rows, where
+// nothing may follow, is such a run read byte by byte.
+template <int T, int E>
+struct Cols {
+    static constexpr int CH = E % 16 == 0 ? 16 : E % 8 == 0 ? 8 : 4, NC = E / CH, W = E / 4;
+    int t, n;
+    bool exact;  // every run of every thread lies inside the row
+    int at[NC];
+    uint32_t mask[W];
+    static __device__ __forceinline__ int col(int j, int t) { return CH * (j / CH * T + t) + j % CH; }
+    __device__ __forceinline__ int col(int j) const { return col(j, t); }
+    __device__ __forceinline__ void init(int t_, int n_) {
+        t = t_;
+        n = n_;
+        exact = n == T * E;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) at[i] = CH * (i * T + t) < n ? CH * (i * T + t) : 0;
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            const int left = n - col(4 * i);
+            mask[i] = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+        }
+    }
+    // `whole`: a run may be read past the row's end (CH more rows follow, or
+    // no run crosses it)
+    __device__ __forceinline__ void load(const int8_t *row, bool whole, uint32_t (&w)[W]) const {
+        if (whole) {
+#pragma unroll
+            for (int i = 0; i < NC; ++i) __builtin_memcpy(w + i * CH / 4, row + at[i], CH);
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; ++i) w[i] = col(4 * i) < n ? load4(row, col(4 * i), n) : 0u;
+        }
+    }
+    __device__ __forceinline__ void clear(uint32_t (&w)[W]) const {
+        if (exact) return;
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] &= mask[i];
+    }
+    __device__ __forceinline__ void store(int8_t *row, const uint32_t (&w)[W]) const {
+#pragma unroll
+        for (int i = 0; i < NC; ++i) store_run<CH>(row, CH * (i * T + t), n, w + i * CH / 4);
+    }
+};
+
 }  // namespace ie
