@@ -40,6 +40,7 @@ __global__ __launch_bounds__(256) void tile_weight_kernel(const int8_t *w, int N
     const int row = threadIdx.x >> 3, c = threadIdx.x & 7;
     const int n = blockIdx.x * 32 + row, k = blockIdx.y * 128 + 16 * c, step = k >> 5;
     uint32_t v[4] = {0, 0, 0, 0};
+    if (step >= ks) return;
     if (n < N) load_run<16>(w + (long long)n * K, k, K, v);
     *(v4i *)(out + (((long long)blockIdx.x * ks + step) * 64 + (c & 1) * 32 + row) * 16) =
         v4i{(int)v[0], (int)v[1], (int)v[2], (int)v[3]};
@@ -48,9 +49,11 @@ __global__ __launch_bounds__(256) void tile_weight_kernel(const int8_t *w, int N
 // KC: contraction steps of X in LDS.
 template <int NI, int KC, bool RES>
 struct RowsCfg {
-    static constexpr int BN = 256 * NI, RP = BN + 4;  // RP: pitch of the residual / result tile
-    static constexpr int D = NI == 4 ? 2 : 4;  // steps of the weight in flight
+    static constexpr int BN = 256 * NI, RP = BN + 16;  // RP: pitch of the residual / result tile
+    static constexpr int D = 2;  // steps of the weight in flight
     static constexpr bool KEEP = NI < 4;
+    // the next tile's X is loaded during the products where it fits the registers
+    static constexpr bool EARLY = KC <= 8 && !RES;
     static constexpr int A = KC * 2048, CS = A + 16 * BN, RED = CS + 8 * ROWS_BM * 4, LDS = RED + ROWS_BM * RP;
 };
 
@@ -99,8 +102,7 @@ void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int
 #pragma unroll
             for (int i = 0; i < RR; ++i) {
                 const int q = i * ROWS_THR + tid, row = q / CPR, c = q % CPR * 16;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) *(uint32_t *)(rt + row * RP + c + 4 * k) = c < N ? (uint32_t)rr[i][k] : 0u;
+                *(v4i *)(rt + row * RP + c) = c < N ? rr[i] : v4i{0, 0, 0, 0};
             }
         } else {
 #pragma unroll 1
@@ -128,7 +130,8 @@ void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int
     store_r(blockIdx.x, r0);
 
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const int m0 = tile * ROWS_BM;
+        const int m0 = tile * ROWS_BM, next = min(tile + (int)gridDim.x, tiles - 1);  // past the end: fetched, never used
+        v4i xn[U], rn[RR];
         // offsets made of the thread's number are made anew for every tile: kept,
         // they would not fit the registers
         asm volatile("" : "+v"(tid));
@@ -161,6 +164,7 @@ void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int
 #pragma unroll
             for (int b = 0; b < NI; ++b) bf[u][b] = wtile(b, u);
         __syncthreads();  // X and the residual are there
+        if constexpr (C::EARLY) fetch_x(next, 0, xn);
 
         const v4i *as = (const v4i *)lds + lane;
         for (int s0 = 0; s0 < ks; s0 += KC) {
@@ -171,7 +175,7 @@ void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int
                 store_x(an);
                 __syncthreads();
             }
-            const int steps = min(KC, ks - s0);  // a multiple of 4
+            const int steps = min(KC, ks - s0);  // a multiple of 2
             for (int s = 0; s < steps; s += D) {
 #pragma unroll
                 for (int u = 0; u < D; ++u) {
@@ -233,8 +237,6 @@ void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int
             if (lane < 32) red[wave * ROWS_BM + a * 32 + lane] = m;
         }
         __syncthreads();
-        const int next = min(tile + (int)gridDim.x, tiles - 1);  // past the end: fetched, never used
-        v4i xn[U], rn[RR];
         double inv[2];
 #pragma unroll
         for (int a = 0; a < 2; ++a) {
@@ -272,7 +274,7 @@ void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int
                 if (h & 1) __builtin_amdgcn_sched_barrier(0);
                 if (b == NI - 1 && h == 3) {
                     // most of y is gone: room for the next tile's loads
-                    fetch_x(next, 0, xn);
+                    if constexpr (!C::EARLY) fetch_x(next, 0, xn);
                     fetch_r(next, rn);
                 }
             }
@@ -282,12 +284,14 @@ void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int
         for (int i = 0; i < RR; ++i) {
             const int q = i * ROWS_THR + tid, row = q / CPR, c = q % CPR * 16;
             if (m0 + row < M && c < N) {
-                uint32_t v[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) v[k] = *(const uint32_t *)(rt + row * RP + c + 4 * k);
+                const v4i o = *(const v4i *)(rt + row * RP + c);
                 int8_t *dst = e.y + (long long)(m0 + row) * N;
-                if (vec) *(v4i *)(dst + c) = v4i{(int)v[0], (int)v[1], (int)v[2], (int)v[3]};
-                else store_run<16>(dst, c, N, v);
+                if (vec) {
+                    *(v4i *)(dst + c) = o;
+                } else {
+                    const uint32_t v[4] = {(uint32_t)o[0], (uint32_t)o[1], (uint32_t)o[2], (uint32_t)o[3]};
+                    store_run<16>(dst, c, N, v);
+                }
             }
         }
         __syncthreads();  // the result is stored
@@ -300,7 +304,7 @@ hipError_t launch_rows_add(const int8_t *x, const int8_t *w, int M, int N, int K
                            const AddEpi &e, hipStream_t st) {
     const int ks = rows_steps(Kp), tiles = (M + ROWS_BM - 1) / ROWS_BM;
     prof_begin(st, PROF_GEMM_ADD);
-    hipLaunchKernelGGL(tile_weight_kernel, dim3(8 * ni, ks / 4), dim3(256), 0, st, w, N, K, ks, wt);
+    hipLaunchKernelGGL(tile_weight_kernel, dim3(8 * ni, (ks + 3) / 4), dim3(256), 0, st, w, N, K, ks, wt);
     const dim3 grid(std::min(tiles, ni == 1 ? 2 * NCU : NCU)), block(ROWS_THR);
     auto go = [&](auto ni_tag, auto kc_tag) {
         constexpr int NI = decltype(ni_tag)::value, KC = decltype(kc_tag)::value;

@@ -227,9 +227,9 @@ Plan plan_add(long long M, long long N, long long K, int row_group, const Force 
 // The product with bias and residual whose workgroups hold whole result rows
 // (256 rows_plan columns; 0: not taken).
 int rows_plan(long long M, long long N, long long K, int row_group, const Force &f);
-// Its contraction steps of 32 bytes, a multiple of 4, and the bytes of the
-// weight in its layout.
-inline int rows_steps(long long K) { return (int)((K + 127) / 128 * 4); }
+// Its contraction steps of 32 bytes, in pairs, and the bytes of the weight in
+// its layout.
+inline int rows_steps(long long K) { return (int)((K + 63) / 64 * 2); }
 inline size_t rows_weight(int ni, long long K) { return (size_t)ni * 256 * 32 * rows_steps(K); }
 
 // The product with bias and residual of a few rows that reads the weight once.
