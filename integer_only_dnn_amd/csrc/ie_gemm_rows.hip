@@ -7,11 +7,12 @@
 // v_mfma_i32_32x32x32_i8 run transposed (a lane holds one row of the result).
 // The weight is laid out beforehand in the order the matrix instructions take
 // it (1 KiB for 32 rows and 32 contraction bytes, lane by lane), so a wave
-// streams its share of it from L2 straight into registers, several steps
-// ahead; the 64 rows of X are staged in LDS, up to 1024 contraction bytes at a
+// streams its share of it from L2 straight into registers, two steps ahead; the 64 rows of X are staged in LDS, up to 1024 contraction bytes at a
 // time.  Nothing in the contraction loop waits for another wave.
-// Workgroups are persistent: the residual of a tile is loaded during its
-// products, the next tile's X while it is stored.
+// Workgroups are persistent: the next tile's X is loaded during the products
+// (a long one's, and the residual, while the result is stored, when the
+// registers are free), after one word of each of its lines has brought it into
+// L2.
 //
 // The epilogue holds y in fp64, in the registers the accumulators leave, so
 // each value is computed once (NI = 4 has no room and computes it twice).
@@ -19,8 +20,8 @@
 // Bound by the fp64 and conversion instructions of the epilogue next to the
 // products (they take turns: the registers hold one workgroup of NI >= 2 per
 // CU), not by memory.  Measured, with the weight's layout: 50432 x 768 x 192
-// 40 us (round to odd by tiles and the pass that closes it: 74), 25216 x 768 x
-// 768 with a residual 45 us (51).
+// 34 us, 46 with a residual (round to odd by tiles and the pass that closes it:
+// 74 without), 25216 x 768 x 768 with a residual 39 us (51).
 #include <algorithm>
 #include <type_traits>
 
@@ -46,18 +47,20 @@ __global__ __launch_bounds__(256) void tile_weight_kernel(const int8_t *w, int N
         v4i{(int)v[0], (int)v[1], (int)v[2], (int)v[3]};
 }
 
-// KC: contraction steps of X in LDS.
-template <int NI, int KC, bool RES>
+// KC: contraction steps of X in LDS.  RES: no residual, one with 16-byte aligned
+// rows, any other.
+enum { RES_NONE, RES_VEC, RES_ANY };
+template <int NI, int KC, int RES>
 struct RowsCfg {
     static constexpr int BN = 256 * NI, RP = BN + 16;  // RP: pitch of the residual / result tile
     static constexpr int D = 2;  // steps of the weight in flight
     static constexpr bool KEEP = NI < 4;
     // the next tile's X is loaded during the products where it fits the registers
-    static constexpr bool EARLY = KC <= 8 && !RES;
+    static constexpr bool EARLY = KC <= 8;
     static constexpr int A = KC * 2048, CS = A + 16 * BN, RED = CS + 8 * ROWS_BM * 4, LDS = RED + ROWS_BM * RP;
 };
 
-template <int NI, int KC, bool RES>
+template <int NI, int KC, int RES>
 __global__ __launch_bounds__(ROWS_THR) __attribute__((amdgpu_waves_per_eu(NI == 1 ? 4 : 2)))
 void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int ks, AddEpi e) {
     using C = RowsCfg<NI, KC, RES>;
@@ -85,30 +88,35 @@ void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int
 #pragma unroll
         for (int u = 0; u < U; ++u) *(v4i *)(ad + u * 8192) = an[u];
     };
-    // the residual of a tile, 16 bytes at a time (rows that are not aligned so:
-    // four, straight to LDS)
+    // the residual of a tile, 16 bytes at a time
     constexpr int CPR = BN / 16, RR = ROWS_BM * CPR / ROWS_THR;
     auto fetch_r = [&](int tile, v4i (&rr)[RR]) {
-        if (!RES || !e.r_vec) return;
+        if constexpr (RES == RES_NONE) return;
 #pragma unroll
         for (int i = 0; i < RR; ++i) {
             const int q = i * ROWS_THR + tid, row = q / CPR, c = q % CPR * 16;
-            rr[i] = *(const v4i *)(e.r + (long long)min(tile * ROWS_BM + row, M - 1) * N + (c < N ? c : 0));
+            const int8_t *src = e.r + (long long)min(tile * ROWS_BM + row, M - 1) * N;
+            if constexpr (RES == RES_VEC) {
+                rr[i] = *(const v4i *)(src + (c < N ? c : 0));
+            } else {
+                // a run over the row's end: the row's last 16 bytes, moved down
+                uint64_t v[2];
+                __builtin_memcpy(v, src + min(c, N - 16), 16);
+                if (c > N - 16 && c < N) {
+                    const int s = 8 * (16 - (N & 15));
+                    v[0] = s < 64 ? v[0] >> s | v[1] << (64 - s) : v[1] >> (s - 64);
+                    v[1] = s < 64 ? v[1] >> s : 0;
+                }
+                rr[i] = v4i{(int)v[0], (int)(v[0] >> 32), (int)v[1], (int)(v[1] >> 32)};
+            }
         }
     };
-    auto store_r = [&](int tile, const v4i (&rr)[RR]) {
-        if (!RES) return;
-        if (e.r_vec) {
+    auto store_r = [&](const v4i (&rr)[RR]) {
+        if constexpr (RES != RES_NONE) {
 #pragma unroll
             for (int i = 0; i < RR; ++i) {
                 const int q = i * ROWS_THR + tid, row = q / CPR, c = q % CPR * 16;
                 *(v4i *)(rt + row * RP + c) = c < N ? rr[i] : v4i{0, 0, 0, 0};
-            }
-        } else {
-#pragma unroll 1
-            for (int q = tid; q < ROWS_BM * BN / 4; q += ROWS_THR) {
-                const int row = q / (BN / 4), c = q % (BN / 4) * 4;
-                *(uint32_t *)(rt + row * RP + c) = load4(e.r + (long long)min(tile * ROWS_BM + row, M - 1) * N, c, N);
             }
         }
     };
@@ -127,7 +135,7 @@ void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int
         bs[n] = n < N && e.bias.m ? (double)e.bias.m[n] * pow2((int)e.bias.e[e.bias.per ? n : 0]) : 0.0;
     }
     store_x(x0);
-    store_r(blockIdx.x, r0);
+    store_r(r0);
 
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         const int m0 = tile * ROWS_BM, next = min(tile + (int)gridDim.x, tiles - 1);  // past the end: fetched, never used
@@ -141,7 +149,7 @@ void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int
         const long long arow = min(ahead, M - 1);
         uint32_t warm = 0;
         for (int c = (tid & 7) * 128; c < min(K, KC * 32); c += 1024) warm |= *(const uint32_t *)(x + arow * K + c);
-        if (RES && e.r_vec)
+        if constexpr (RES == RES_VEC)
             for (int c = (tid & 7) * 128; c < N; c += 1024) warm |= *(const uint32_t *)(e.r + arow * N + c);
         // this lane's two rows' exponents
         double sx[2], sr[2];
@@ -266,25 +274,26 @@ void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int
                 if constexpr (!C::KEEP) quad(b, h, y);
 #pragma unroll
                 for (int a = 0; a < 2; ++a) {
-                    uint32_t o = pack4(mant_of(y[a][0], inv[a]), mant_of(y[a][1], inv[a]), mant_of(y[a][2], inv[a]),
+                    const uint32_t o = pack4(mant_of(y[a][0], inv[a]), mant_of(y[a][1], inv[a]), mant_of(y[a][2], inv[a]),
                                        mant_of(y[a][3], inv[a]));
-                    if (e.relu) o = relu4(o);
                     *(uint32_t *)(lds + ort + a * 32 * RP + b * 32 + 8 * h) = o;
                 }
                 if (h & 1) __builtin_amdgcn_sched_barrier(0);
-                if (b == NI - 1 && h == 3) {
-                    // most of y is gone: room for the next tile's loads
-                    if constexpr (!C::EARLY) fetch_x(next, 0, xn);
-                    fetch_r(next, rn);
-                }
             }
         __syncthreads();
+        // y is gone: room for the next tile's loads
+        if constexpr (!C::EARLY) fetch_x(next, 0, xn);
+        fetch_r(next, rn);
         const bool vec = (N & 15) == 0 && ((uintptr_t)e.y & 15) == 0;
 #pragma unroll
         for (int i = 0; i < RR; ++i) {
             const int q = i * ROWS_THR + tid, row = q / CPR, c = q % CPR * 16;
             if (m0 + row < M && c < N) {
-                const v4i o = *(const v4i *)(rt + row * RP + c);
+                v4i o = *(const v4i *)(rt + row * RP + c);
+                if (e.relu) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) o[k] = (int)relu4((uint32_t)o[k]);
+                }
                 int8_t *dst = e.y + (long long)(m0 + row) * N;
                 if (vec) {
                     *(v4i *)(dst + c) = o;
@@ -296,7 +305,7 @@ void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int
         }
         __syncthreads();  // the result is stored
         store_x(xn);
-        store_r(next, rn);
+        store_r(rn);
     }
 }
 
@@ -308,8 +317,9 @@ hipError_t launch_rows_add(const int8_t *x, const int8_t *w, int M, int N, int K
     const dim3 grid(std::min(tiles, ni == 1 ? 2 * NCU : NCU)), block(ROWS_THR);
     auto go = [&](auto ni_tag, auto kc_tag) {
         constexpr int NI = decltype(ni_tag)::value, KC = decltype(kc_tag)::value;
-        if (e.r) hipLaunchKernelGGL((rows_add_kernel<NI, KC, true>), grid, block, 0, st, x, wt, M, N, Kp, ks, e);
-        else hipLaunchKernelGGL((rows_add_kernel<NI, KC, false>), grid, block, 0, st, x, wt, M, N, Kp, ks, e);
+        if (!e.r) hipLaunchKernelGGL((rows_add_kernel<NI, KC, RES_NONE>), grid, block, 0, st, x, wt, M, N, Kp, ks, e);
+        else if (e.r_vec) hipLaunchKernelGGL((rows_add_kernel<NI, KC, RES_VEC>), grid, block, 0, st, x, wt, M, N, Kp, ks, e);
+        else hipLaunchKernelGGL((rows_add_kernel<NI, KC, RES_ANY>), grid, block, 0, st, x, wt, M, N, Kp, ks, e);
     };
 #define IE_CASE(NI_, KC_) go(std::integral_constant<int, NI_>{}, std::integral_constant<int, KC_>{})
     // a short contraction takes its steps only

@@ -369,10 +369,10 @@ Plan plan_add(long long M, long long N, long long K, int row_group, const Force 
 // Rows of 129..1024 results and contractions up to 2048 (a narrower row fits
 // the tiles' direct form: 100000 x 64 x 256, 11.9 us there, 20.4 here; over a
 // longer contraction the weight, streamed again for every 64 rows, takes what
-// the second pass cost: 25216 x 768 x 4096, 113.7 us here, 116.9 there, 8192 x
-// 1024 x 4096, 70.7 and 54.0), from as many rows on as fill the CUs in the time
-// of one workgroup: x 768 x 192, 11.0 us here at 2048 rows, 12.5 by tiles; x
-// 768 x 768, 21.3 here at 6144 rows, 25.1 by tiles, but 21.4 and 19.6 at 4096.
+// the second pass cost: 25216 x 768 x 4096, 111 us here, 116 there, 8192 x 1024
+// x 4096, 71 and 53), from as many rows on as take the tiles longer than one
+// workgroup: x 768 x 192, 10.4 us here at 2048 rows, 12.7 by tiles; x 768 x 768,
+// 20.2 here at 6144 rows, 25.0 by tiles, but 20.0 and 19.3 at 4096.
 int rows_plan(long long M, long long N, long long K, int row_group, const Force &f) {
     if (f.on || !row_group || N <= 128 || N > 1024 || K < 16 || K > 2048) return 0;
     return M >= (K <= 256 || N <= 256 ? 2048 : 6144) ? cdiv(N, 256) : 0;
