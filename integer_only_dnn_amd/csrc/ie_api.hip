@@ -1084,12 +1084,18 @@ size_t ie_linear_fwd_fused_workspace(int64_t M, int64_t N, int64_t K) {
 ie_status ie_linear_fwd_fused(const ie_mat *X, const ie_mat *W, const ie_mat *bias, const ie_mat *R, const ie_mat *Y,
                               int act, void *ws, size_t ws_bytes, void *stream) {
     if (act != IE_ACT_NONE && act != IE_ACT_RELU) return IE_ERR_UNSUPPORTED;
-    if (!bias && !R) return linear_fwd(X, W, Y, ws, ws_bytes, stream, act == IE_ACT_RELU);
     IE_CHECK(check_mat(X));
     IE_CHECK(check_mat(W));
     IE_CHECK(check_mat(Y));
     const long long M = X->rows, K = X->cols, N = W->rows;
     if (W->cols != K || Y->rows != M || Y->cols != N) return IE_ERR_SHAPE;
+    const Force f = force_product();
+    const int rg = Y->group == IE_GROUP_ROW, rows = rows_plan(M, N, r16(K), rg, f);
+    const bool few = few_plan(M, N, r16(K), f);
+    // the plain product takes the tiles, any contraction, alignment and sharing
+    if (!bias && !R &&
+        (!(rows || few) || K > MAX_CONTRACT || !aligned(X->mant, 16) || !aligned(W->mant, 16) || share(Y, X) || share(Y, W)))
+        return linear_fwd(X, W, Y, ws, ws_bytes, stream, act == IE_ACT_RELU);
     if (bias) IE_CHECK(check_vector(bias, N));
     if (R) {
         IE_CHECK(check_mat(R));
@@ -1099,29 +1105,12 @@ ie_status ie_linear_fwd_fused(const ie_mat *X, const ie_mat *W, const ie_mat *bi
     if (!aligned(X->mant, 16) || !aligned(W->mant, 16)) return IE_ERR_UNSUPPORTED;
     if (share(Y, X) || share(Y, W) || share(Y, bias) || share(Y, R)) return IE_ERR_UNSUPPORTED;
     if (!ws) return IE_ERR_WORKSPACE;
-    const Force f = force_product();
     if (ws_bytes < linear_fused_ws(M, N, K, f)) return IE_ERR_WORKSPACE;
     hipStream_t st = (hipStream_t)stream;
-    const int rg = Y->group == IE_GROUP_ROW;
     if (M == 0 || N == 0) return hip_status(launch_fill_i8(Y->exp, n_exps(Y), E_MIN, st));
     Carve c{(char *)ws, HEADER};
     const LinearFusedWs w = carve_linear_fused(c, M, N, K, f);
     const long long Kp = r16(K);
-    const int rows = rows_plan(M, N, Kp, rg, f);
-    const bool few = few_plan(M, N, Kp, f);
-    const Plan pl = plan_add(M, N, Kp, rg, f);
-    IE_CHECK(checked_plan(pl, M, N, Kp, rg, FAM_ADD, w.l.pw.n, add_needs(pl, M, N, Kp, rg)));
-    log_plan("dense add", M, N, Kp, pl);
-    const int8_t *xs = X->mant, *wsrc = W->mant;
-    if (Kp != K) {
-        IE_TRY(launch_pad_rows(X->mant, M, K, nullptr, 0, nullptr, Kp, w.l.xp, st));
-        xs = w.l.xp;
-        if (!rows && !few) {
-            IE_TRY(launch_pad_rows(W->mant, N, K, nullptr, 0, nullptr, Kp, w.l.wp, st));
-            wsrc = w.l.wp;
-        }
-    }
-    const Operand A{LD_K, xs, Kp, (int)M, {}}, B{LD_K, wsrc, Kp, (int)N, {}};
     AddEpi e;
     memset(&e, 0, sizeof e);
     e.xe = X->exp;
@@ -1141,8 +1130,18 @@ ie_status ie_linear_fwd_fused(const ie_mat *X, const ie_mat *W, const ie_mat *bi
     e.q = mat_q(Y);
     e.relu = act == IE_ACT_RELU;
     e.flags = (uint32_t *)ws;
-    if (few) return hip_status(launch_few_add(xs, W->mant, (int)M, (int)N, (int)K, (int)Kp, w.few_acc, w.few_w, e, st));
-    if (rows) return hip_status(launch_rows_add(xs, W->mant, (int)M, (int)N, (int)K, (int)Kp, w.wt, rows, e, st));
+    if (few) return hip_status(launch_few_add(X->mant, W->mant, (int)M, (int)N, (int)K, w.few_acc, w.few_w, e, st));
+    if (rows) return hip_status(launch_rows_add(X->mant, W->mant, (int)M, (int)N, (int)K, w.wt, rows, e, st));
+    const Plan pl = plan_add(M, N, Kp, rg, f);
+    IE_CHECK(checked_plan(pl, M, N, Kp, rg, FAM_ADD, w.l.pw.n, add_needs(pl, M, N, Kp, rg)));
+    log_plan("dense add", M, N, Kp, pl);
+    const int8_t *xs = X->mant, *wsrc = W->mant;
+    if (Kp != K) {
+        IE_TRY(launch_pad_two(X->mant, (int)M, W->mant, (int)N, (int)K, (int)Kp, w.l.xp, w.l.wp, st));
+        xs = w.l.xp;
+        wsrc = w.l.wp;
+    }
+    const Operand A{LD_K, xs, Kp, (int)M, {}}, B{LD_K, wsrc, Kp, (int)N, {}};
     if (pl.mode == PLAN_SPLIT) {
         Epi ep;
         memset(&ep, 0, sizeof ep);
@@ -1155,8 +1154,7 @@ ie_status ie_linear_fwd_fused(const ie_mat *X, const ie_mat *W, const ie_mat *bi
     e.p16 = w.l.pw.p16;
     IE_TRY(launch_gemm_add(A, B, (int)M, (int)N, (int)Kp, pl.t, pl.mode == PLAN_DIRECT, e, st));
     if (pl.mode == PLAN_DIRECT) return IE_OK;
-    return hip_status(launch_rto_finalize(e.v16, e.p16, (int)M, (int)N, pl.t, rg, Y->mant, Y->exp, e.flags, st,
-                                          Act{e.relu, nullptr}));
+    return hip_status(launch_add_round(e, (int)M, (int)N, pl.t, st));
 }
 
 // ---------------------------------------------------------------------------

@@ -179,6 +179,19 @@ __device__ __forceinline__ void load_run(const int8_t *row, int c, int n, uint32
     }
 }
 
+// Bytes c .. c + 15 of a row of n >= 16 (c < n, any alignment; past n: zeros) in
+// one load: at the row's end its last 16 bytes, moved down.
+__device__ __forceinline__ v4i load16(const int8_t *row, int c, int n) {
+    uint64_t v[2];
+    __builtin_memcpy(v, row + min(c, n - 16), 16);
+    if (c > n - 16) {
+        const int s = 8 * (c - (n - 16));
+        v[0] = s < 64 ? v[0] >> s | v[1] << (64 - s) : v[1] >> (s - 64);
+        v[1] = s < 64 ? v[1] >> s : 0;
+    }
+    return v4i{(int)v[0], (int)(v[0] >> 32), (int)v[1], (int)(v[1] >> 32)};
+}
+
 template <int CH>
 __device__ __forceinline__ void store_run(int8_t *row, int c, int n, const uint32_t *w) {
     if (c + CH <= n) {

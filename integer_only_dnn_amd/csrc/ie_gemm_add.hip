@@ -20,10 +20,12 @@ template <bool RES>
 struct EpiAdd {
     AddEpi e;
 
-    // a row of int8 or int16 results from LDS to memory, 16 bytes per thread
+    // a tile of int8 or int16 results from LDS to memory, 16 bytes per thread;
+    // int16 rows are add_pitch(N) apart, zeros past N
     template <int ES, int BM, int BN>
-    __device__ __forceinline__ void flush(const int8_t *lds, void *dst, int m0, int n0, int M, int N, bool vec) const {
+    __device__ __forceinline__ void flush(const int8_t *lds, void *dst, int m0, int n0, int M, int n, bool vec) const {
         constexpr int PITCH = BN * ES + 16, CPR = BN * ES / 16, EPC = 16 / ES;
+        const int N = ES == 2 ? add_pitch(n) : n;
 #pragma unroll
         for (int q0 = 0; q0 < BM * CPR; q0 += NTHR) {
             const int q = q0 + threadIdx.x, row = q / CPR, cb = q % CPR * 16;
@@ -35,7 +37,7 @@ struct EpiAdd {
                 for (int k = 0; k < 4; ++k) v[k] = (int)relu4((uint32_t)v[k]);
             }
             int8_t *g = (int8_t *)dst + ((long long)gr * N + gc) * ES;
-            if (vec && gc + EPC <= N) {
+            if (ES == 2 || (vec && gc + EPC <= N)) {
                 *(v4i *)g = v;
             } else {
                 const int bytes = min(16, (N - gc) * ES);
@@ -80,8 +82,14 @@ struct EpiAdd {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) v[k] = (uint32_t)w[k];
                     } else {
+                        const int8_t *rowp = src - n0;
+                        if (N >= 16) {
+                            const v4i w = load16(rowp, n0 + c, N);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) v[k] = load4(src, c + 4 * k, N - n0);
+                            for (int k = 0; k < 4; ++k) v[k] = (uint32_t)w[k];
+                        } else {
+                            load_run<16>(rowp, n0 + c, N, v);
+                        }
                     }
                 }
 #pragma unroll
@@ -192,7 +200,7 @@ struct EpiAdd {
                 }
         __syncthreads();
         if constexpr (DI) flush<1, BM, BN>(out, e.y, m0, n0, M, N, (N & 15) == 0 && ((uintptr_t)e.y & 15) == 0);
-        else flush<2, BM, BN>(out, e.v16, m0, n0, M, N, (N & 7) == 0);
+        else flush<2, BM, BN>(out, e.v16, m0, n0, M, N, true);
     }
 };
 
@@ -229,6 +237,96 @@ hipError_t launch_gemm_add(const Operand &A, const Operand &B, int M, int N, int
     IE_TILES_ADD(IE_CASE)
 #undef IE_CASE
     prof_end(st, PROF_GEMM_ADD);
+    return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// Round-to-odd results (units of 2^(need - 2), the need of their row in the
+// tile or of the tile) rounded at their group's largest need.  A value has at
+// most 11 bits, so one fp32 fused multiply-add on it rounds half to even into
+// the low bits of the sum.  T lanes per row, eight values each.
+// ---------------------------------------------------------------------------
+
+template <int T>
+__global__ __launch_bounds__(256) void add_round_kernel(AddEpi e, int M, int N, int lbm, int lbn, int TM, int TN) {
+    constexpr int RPB = 256 / T;
+    __shared__ int shi[4];
+    const int t = threadIdx.x % T, slot = threadIdx.x / T;
+    int ex = E_MIN;
+    if (!e.y_row) {
+        int m = NEED_NONE;
+        const long long n = (long long)TM * TN;
+        for (long long i = threadIdx.x; i < n; i += 256) m = max(m, (int)e.p16[i]);
+        m = row_reduce<256>(m, Max{}, shi);
+        ex = clamp_exp_flag(max(E_MIN, m), e.flags);
+        if (blockIdx.x == 0 && threadIdx.x == 0) e.ye[0] = (int8_t)ex;
+    }
+    for (long long r0 = (long long)blockIdx.x * RPB; r0 < M; r0 += (long long)gridDim.x * RPB) {
+        const long long row = min(r0 + slot, (long long)M - 1);
+        const int16_t *v = e.v16 + row * add_pitch(N), *p = e.y_row ? e.p16 + row * TN : e.p16 + (row >> lbm);
+        if (e.y_row) {
+            int m = NEED_NONE;
+            for (int j = t; j < TN; j += T) m = max(m, (int)p[j]);
+            ex = max(E_MIN, lane_reduce<T>(m, Max{}));
+            if (t == 0 && r0 + slot < M) {
+                ex = clamp_exp_flag(ex, e.flags);
+                e.ye[row] = (int8_t)ex;
+            }
+            ex = min(ex, E_MAX);
+        }
+        if (r0 + slot >= M) continue;
+#pragma unroll 2
+        for (int c = 8 * t; c < N; c += 8 * T) {
+            const v4i w = *(const v4i *)(v + c);
+            const int need = p[(long long)(c >> lbn) * (e.y_row ? 1 : TM)];
+            // P_NONE: all zeros, whatever the shift
+            const float s = __builtin_ldexpf(1.0f, max(need - 2 - ex, -100));
+            uint32_t o[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                int b[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int x = i & 1 ? w[2 * k + i / 2] >> 16 : (int)(int16_t)w[2 * k + i / 2];
+                    b[i] = __float_as_int(__builtin_fmaf((float)x, s, 12582912.0f));  // 1.5 * 2^23
+                }
+                o[k] = pack4(b[0], b[1], b[2], b[3]);
+                if (e.relu) o[k] = relu4(o[k]);
+            }
+            store_run<8>(e.y + row * N, c, N, o);
+        }
+    }
+}
+
+hipError_t launch_add_round(const AddEpi &e, int M, int N, Tile t, hipStream_t st) {
+    auto lg = [](int v) { int l = 0; while ((1 << l) < v) ++l; return l; };  // tile sides are powers of two
+    const int lbm = lg(t.bm()), lbn = lg(t.bn()), TM = (M + t.bm() - 1) / t.bm(), TN = (N + t.bn() - 1) / t.bn();
+    auto grid = [&](int rpb) { const int g = (M + rpb - 1) / rpb; return dim3(g < 8 * NCU ? g : 8 * NCU); };
+    prof_begin(st, PROF_RTO_FINALIZE);
+    if (N <= 64) hipLaunchKernelGGL(add_round_kernel<8>, grid(32), dim3(256), 0, st, e, M, N, lbm, lbn, TM, TN);
+    else hipLaunchKernelGGL(add_round_kernel<64>, grid(4), dim3(256), 0, st, e, M, N, lbm, lbn, TM, TN);
+    prof_end(st, PROF_RTO_FINALIZE);
+    return hipGetLastError();
+}
+
+// Both operands' rows to whole runs of 16 bytes, one run per thread.
+__global__ __launch_bounds__(256) void pad_two_kernel(const int8_t *x, long long nx, const int8_t *w, long long nw, int K,
+                                                      int runs, int8_t *xp, int8_t *wp) {
+    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < nx + nw; i += gridDim.x * 256ll) {
+        const bool first = i < nx;
+        const long long j = first ? i : i - nx, row = j / runs;
+        uint32_t v[4];
+        load_run<16>((first ? x : w) + row * K, (int)(j - row * runs) * 16, K, v);
+        *(v4i *)((first ? xp : wp) + j * 16) = v4i{(int)v[0], (int)v[1], (int)v[2], (int)v[3]};
+    }
+}
+
+hipError_t launch_pad_two(const int8_t *x, int M, const int8_t *w, int N, int K, int Kp, int8_t *xp, int8_t *wp,
+                          hipStream_t st) {
+    const int runs = Kp / 16;
+    const long long nx = (long long)M * runs, nw = (long long)N * runs, g = (nx + nw + 255) / 256;
+    hipLaunchKernelGGL(pad_two_kernel, dim3(g < 8 * NCU ? (int)g : 8 * NCU), dim3(256), 0, st, x, nx, w, nw, K, runs, xp,
+                       wp);
     return hipGetLastError();
 }
 

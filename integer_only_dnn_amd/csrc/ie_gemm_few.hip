@@ -56,18 +56,18 @@ __device__ __forceinline__ void few_values(const FewTerms &t, v4i c, int n, int 
     }
 }
 
-// x [M x Kp], zeros from K on; w [N x K]; acc [M x Np] (Np: N in whole groups
+// x [M x K], w [N x K]; acc [M x Np] (Np: N in whole groups
 // of 16), word [M][Np / 16], or [Np / 16] for a whole-tensor result.  U: steps in
-// flight; EVEN: K = Kp, and w is 16-byte aligned.
+// flight; EVEN: rows of whole runs of 16 bytes.
 template <int MT, int U, bool EVEN>
-__global__ __launch_bounds__(FEW_THR) void few_add_kernel(const int8_t *x, const int8_t *w, int M, int N, int K, int Kp,
-                                                          AddEpi e, int *acc, int *word) {
+__global__ __launch_bounds__(FEW_THR) void few_add_kernel(const int8_t *x, const int8_t *w, int M, int N, int K, AddEpi e,
+                                                           int *acc, int *word) {
     __shared__ v4i part[FEW_WV][MT * 64];
     __shared__ int shm[MT];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n0 = blockIdx.x * FEW_BN;
     const int row = lane & 15, kq = 16 * (lane >> 4);
     const int8_t *wr = w + (long long)min(n0 + row, N - 1) * K;
-    const int steps = (Kp + 63) / 64;
+    const int steps = (K + 63) / 64;
     const int m = wave * 16 + row, n = n0 + 4 * (lane >> 4), nb = gridDim.x;
     FewTerms ft;
     if (wave < MT) ft = few_terms(e, min(m, M - 1), n, N);
@@ -92,13 +92,20 @@ __global__ __launch_bounds__(FEW_THR) void few_add_kernel(const int8_t *x, const
             const int k = (s0 + u * FEW_WV) * 64 + kq;
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
-                const int8_t *xr = x + (long long)min(t * 16 + row, M - 1) * Kp;
-                b[u][t] = *(const v4i *)(xr + min(k, Kp - 16));
+                const int8_t *xr = x + (long long)min(t * 16 + row, M - 1) * K;
+                if constexpr (EVEN) {
+                    b[u][t] = *(const v4i *)(xr + min(k, K - 16));
+                } else {
+                    uint32_t v[4];
+                    load_run<16>(xr, k, K, v);
+                    b[u][t] = v4i{(int)v[0], (int)v[1], (int)v[2], (int)v[3]};
+                }
             }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const bool in = (s0 + u * FEW_WV) * 64 + kq < Kp;  // past the end both factors repeat: X counts as zero
+            // past the end of whole runs both factors repeat: X counts as zero
+            const bool in = !EVEN || (s0 + u * FEW_WV) * 64 + kq < K;
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
                 v4i v = b[u][t];
@@ -163,18 +170,18 @@ __global__ __launch_bounds__(FEW_ROUND) void few_round_kernel(AddEpi e, const in
     store4(e.y + (long long)m * N, n, N, o);
 }
 
-hipError_t launch_few_add(const int8_t *x, const int8_t *w, int M, int N, int K, int Kp, int *acc, int *word,
+hipError_t launch_few_add(const int8_t *x, const int8_t *w, int M, int N, int K, int *acc, int *word,
                           const AddEpi &e, hipStream_t st) {
     const int nb = (N + FEW_BN - 1) / FEW_BN;
     prof_begin(st, PROF_GEMM_ADD);
     auto go = [&](auto mt, auto u) {
         constexpr int MT = decltype(mt)::value, U = decltype(u)::value;
         const dim3 grid(nb), block(FEW_THR);
-        if (K == Kp) hipLaunchKernelGGL((few_add_kernel<MT, U, true>), grid, block, 0, st, x, w, M, N, K, Kp, e, acc, word);
-        else hipLaunchKernelGGL((few_add_kernel<MT, U, false>), grid, block, 0, st, x, w, M, N, K, Kp, e, acc, word);
+        if (K % 16 == 0) hipLaunchKernelGGL((few_add_kernel<MT, U, true>), grid, block, 0, st, x, w, M, N, K, e, acc, word);
+        else hipLaunchKernelGGL((few_add_kernel<MT, U, false>), grid, block, 0, st, x, w, M, N, K, e, acc, word);
     };
 #define IE_CASE(MT_, U_) go(std::integral_constant<int, MT_>{}, std::integral_constant<int, U_>{})
-    const bool brief = Kp <= 2 * 64 * FEW_WV;  // two steps a wave
+    const bool brief = K <= 2 * 64 * FEW_WV;  // two steps a wave
     if (M <= 16 && brief) IE_CASE(1, 2);
     else if (M <= 16) IE_CASE(1, 8);
     else if (M <= 32 && brief) IE_CASE(2, 2);

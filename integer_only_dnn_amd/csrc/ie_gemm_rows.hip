@@ -75,12 +75,24 @@ void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int
 
     // X: thread t takes, of row (t / 4) % 64, the 16-byte piece t % 4 + 4 (t / 256)
     // of every four contraction steps; rows past the last repeat it, bytes past K
-    // meet zeros of the weight
+    // (the next row's) meet zeros of the weight, and at the matrix's end its last
+    // 16 bytes are moved down
     auto fetch_x = [&](int tile, int s0, v4i (&an)[U]) {
         const int arow = (tid >> 2) & 63, aj = (tid & 3) + 4 * (tid >> 8);
-        const int8_t *xr = x + (long long)min(tile * ROWS_BM + arow, M - 1) * K;
+        const long long o = (long long)min(tile * ROWS_BM + arow, M - 1) * K, last = (long long)M * K - 16;
 #pragma unroll
-        for (int u = 0; u < U; ++u) an[u] = *(const v4i *)(xr + min((s0 + 4 * u) * 32 + aj * 16, K - 16));
+        for (int u = 0; u < U; ++u) {
+            const int k = (s0 + 4 * u) * 32 + aj * 16;
+            const long long p = o + (k < K ? k : 0), over = p - last;
+            uint64_t v[2];
+            __builtin_memcpy(v, x + min(p, last), 16);
+            if (over > 0) {
+                const int s = 8 * (int)over;
+                v[0] = s < 64 ? v[0] >> s | v[1] << (64 - s) : v[1] >> (s - 64);
+                v[1] = s < 64 ? v[1] >> s : 0;
+            }
+            an[u] = v4i{(int)v[0], (int)(v[0] >> 32), (int)v[1], (int)(v[1] >> 32)};
+        }
     };
     auto store_x = [&](const v4i (&an)[U]) {
         const int arow = (tid >> 2) & 63, aj = (tid & 3) + 4 * (tid >> 8);
@@ -99,15 +111,7 @@ void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int
             if constexpr (RES == RES_VEC) {
                 rr[i] = *(const v4i *)(src + (c < N ? c : 0));
             } else {
-                // a run over the row's end: the row's last 16 bytes, moved down
-                uint64_t v[2];
-                __builtin_memcpy(v, src + min(c, N - 16), 16);
-                if (c > N - 16 && c < N) {
-                    const int s = 8 * (16 - (N & 15));
-                    v[0] = s < 64 ? v[0] >> s | v[1] << (64 - s) : v[1] >> (s - 64);
-                    v[1] = s < 64 ? v[1] >> s : 0;
-                }
-                rr[i] = v4i{(int)v[0], (int)(v[0] >> 32), (int)v[1], (int)(v[1] >> 32)};
+                rr[i] = load16(src, min(c, N - 1), N);
             }
         }
     };
@@ -148,7 +152,7 @@ void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int
         const int ahead = min(tile + (int)gridDim.x, tiles - 1) * ROWS_BM + (tid >> 3);
         const long long arow = min(ahead, M - 1);
         uint32_t warm = 0;
-        for (int c = (tid & 7) * 128; c < min(K, KC * 32); c += 1024) warm |= *(const uint32_t *)(x + arow * K + c);
+        for (int c = (tid & 7) * 128; c < min(K - 3, KC * 32); c += 1024) warm |= *(const uint32_t *)(x + arow * K + c);
         if constexpr (RES == RES_VEC)
             for (int c = (tid & 7) * 128; c < N; c += 1024) warm |= *(const uint32_t *)(e.r + arow * N + c);
         // this lane's two rows' exponents
@@ -309,17 +313,17 @@ void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int
     }
 }
 
-hipError_t launch_rows_add(const int8_t *x, const int8_t *w, int M, int N, int K, int Kp, int8_t *wt, int ni,
+hipError_t launch_rows_add(const int8_t *x, const int8_t *w, int M, int N, int K, int8_t *wt, int ni,
                            const AddEpi &e, hipStream_t st) {
-    const int ks = rows_steps(Kp), tiles = (M + ROWS_BM - 1) / ROWS_BM;
+    const int ks = rows_steps(K), tiles = (M + ROWS_BM - 1) / ROWS_BM;
     prof_begin(st, PROF_GEMM_ADD);
     hipLaunchKernelGGL(tile_weight_kernel, dim3(8 * ni, (ks + 3) / 4), dim3(256), 0, st, w, N, K, ks, wt);
     const dim3 grid(std::min(tiles, ni == 1 ? 2 * NCU : NCU)), block(ROWS_THR);
     auto go = [&](auto ni_tag, auto kc_tag) {
         constexpr int NI = decltype(ni_tag)::value, KC = decltype(kc_tag)::value;
-        if (!e.r) hipLaunchKernelGGL((rows_add_kernel<NI, KC, RES_NONE>), grid, block, 0, st, x, wt, M, N, Kp, ks, e);
-        else if (e.r_vec) hipLaunchKernelGGL((rows_add_kernel<NI, KC, RES_VEC>), grid, block, 0, st, x, wt, M, N, Kp, ks, e);
-        else hipLaunchKernelGGL((rows_add_kernel<NI, KC, RES_ANY>), grid, block, 0, st, x, wt, M, N, Kp, ks, e);
+        if (!e.r) hipLaunchKernelGGL((rows_add_kernel<NI, KC, RES_NONE>), grid, block, 0, st, x, wt, M, N, K, ks, e);
+        else if (e.r_vec) hipLaunchKernelGGL((rows_add_kernel<NI, KC, RES_VEC>), grid, block, 0, st, x, wt, M, N, K, ks, e);
+        else hipLaunchKernelGGL((rows_add_kernel<NI, KC, RES_ANY>), grid, block, 0, st, x, wt, M, N, K, ks, e);
     };
 #define IE_CASE(NI_, KC_) go(std::integral_constant<int, NI_>{}, std::integral_constant<int, KC_>{})
     // a short contraction takes its steps only

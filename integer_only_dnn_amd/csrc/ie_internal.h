@@ -349,13 +349,18 @@ struct AddEpi {
 };
 hipError_t launch_gemm_add(const Operand &A, const Operand &B, int M, int N, int K, Tile t, bool direct,
                            const AddEpi &e, hipStream_t st);
+// Rounds its round-to-odd results v16 [M][add_pitch(N)].
+hipError_t launch_add_round(const AddEpi &e, int M, int N, Tile t, hipStream_t st);
+// x [M x K] and w [N x K] to rows of Kp bytes, zeros from K on.
+hipError_t launch_pad_two(const int8_t *x, int M, const int8_t *w, int N, int K, int Kp, int8_t *xp, int8_t *wp,
+                          hipStream_t st);
 // The same with whole result rows in a workgroup (ie_gemm_rows.hip): x [M x
-// Kp], w [N x K], wt: rows_weight(ni, Kp) bytes of scratch.
-hipError_t launch_rows_add(const int8_t *x, const int8_t *w, int M, int N, int K, int Kp, int8_t *wt, int ni,
+// K], w [N x K], wt: rows_weight(ni, K) bytes of scratch.
+hipError_t launch_rows_add(const int8_t *x, const int8_t *w, int M, int N, int K, int8_t *wt, int ni,
                            const AddEpi &e, hipStream_t st);
-// The same for M <= FEW_ROWS rows (ie_gemm_few.hip): x [M x Kp], w [N x K],
-// acc: M r16(N) ints, word: M r16(N) / 16 ints.
-hipError_t launch_few_add(const int8_t *x, const int8_t *w, int M, int N, int K, int Kp, int *acc, int *word,
+// The same for M <= FEW_ROWS rows (ie_gemm_few.hip): acc: M r16(N) ints, word:
+// M r16(N) / 16 ints.
+hipError_t launch_few_add(const int8_t *x, const int8_t *w, int M, int N, int K, int *acc, int *word,
                           const AddEpi &e, hipStream_t st);
 // The same epilogue on int32 partial sums [splits][M][N].
 hipError_t launch_split_add(const AddEpi &e, const int *partial, int splits, int M, int N, int *bmax, hipStream_t st);

@@ -522,6 +522,7 @@ Needs product_needs(const Plan &pl, long long M, long long N, long long K, int r
 Needs add_needs(const Plan &pl, long long M, long long N, long long K, int row_group) {
     Needs n = product_needs(pl, M, N, K, row_group);
     n.gneed = n.sums = n.tneed = 0;
+    if (n.v16) n.v16 = (size_t)M * add_pitch((int)N);
     return n;
 }
 

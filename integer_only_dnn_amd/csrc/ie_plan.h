@@ -227,6 +227,8 @@ Plan plan_add(long long M, long long N, long long K, int row_group, const Force 
 // The product with bias and residual whose workgroups hold whole result rows
 // (256 rows_plan columns; 0: not taken).
 int rows_plan(long long M, long long N, long long K, int row_group, const Force &f);
+// A row of the tiles' round-to-odd results, in whole runs of 16 bytes.
+constexpr int add_pitch(int cols) { return (cols + 7) & ~7; }
 // Its contraction steps of 32 bytes, in pairs, and the bytes of the weight in
 // its layout.
 inline int rows_steps(long long K) { return (int)((K + 63) / 64 * 2); }
