@@ -921,11 +921,12 @@ ie_status ie_layer_norm_fwd(const ie_mat *X, const ie_mat *gamma, const ie_mat *
     if (!ws) return IE_ERR_WORKSPACE;
     if (ws_bytes < norm_fwd_ws(X->rows, X->cols)) return IE_ERR_WORKSPACE;
     hipStream_t st = (hipStream_t)stream;
-    const int y_row = Y->group == IE_GROUP_ROW;
+    const int y_row = Y->group == IE_GROUP_ROW || X->rows == 1;
     if (X->rows == 0 || X->cols == 0) return hip_status(launch_fill_i8(Y->exp, n_exps(Y), E_MIN, st));
     Carve c{(char *)ws, HEADER};
     const NormWs w = carve_norm_fwd(c, X->rows, X->cols);
-    const NormPlan pl = norm_fwd_plan(X->rows, X->cols);
+    const NormPlan one = norm_one_plan(X->rows, X->cols);
+    const NormPlan pl = !y_row && one.grid ? one : norm_fwd_plan(X->rows, X->cols);
     NormFwd a;
     memset(&a, 0, sizeof a);
     a.x = X->mant;
@@ -944,9 +945,9 @@ ie_status ie_layer_norm_fwd(const ie_mat *X, const ie_mat *gamma, const ie_mat *
     a.n_bmax = pl.grid;
     a.stat = (RowStat *)w.stat;
     a.flags = (uint32_t *)ws;
-    a.mode = y_row ? NORM_ROWS : NORM_NEED;
+    a.mode = y_row ? NORM_ROWS : one.grid ? NORM_ONE : NORM_NEED;
     IE_TRY(launch_norm_fwd(a, pl, st));
-    if (y_row) return IE_OK;
+    if (a.mode != NORM_NEED) return IE_OK;
     a.mode = NORM_ROUND;
     return hip_status(launch_norm_fwd(a, pl, st));
 }
@@ -999,7 +1000,7 @@ ie_status ie_layer_norm_bwd(const ie_mat *dY, const ie_mat *X, const ie_mat *gam
     const NormWs w = carve_norm_bwd(c, M, N);
     const NormPlan pl = norm_bwd_plan(M, N);
     const bool cols = dgamma || dbeta;
-    const bool dx_row = dX && dX->group == IE_GROUP_ROW;
+    const bool dx_row = dX && (dX->group == IE_GROUP_ROW || M == 1);
     const int tops = n_tops(M, dY->group == IE_GROUP_ROW);
     NormBwd a;
     memset(&a, 0, sizeof a);
@@ -1028,9 +1029,10 @@ ie_status ie_layer_norm_bwd(const ie_mat *dY, const ie_mat *X, const ie_mat *gam
     a.flags = flags;
     if (M > 0) {
         if (cols && tops) IE_TRY(launch_tops(dY->exp, M, w.c.tops, tops, st));
-        a.mode = dx_row ? NORM_ROWS : NORM_NEED;
+        // one block of whole rows holds a whole-tensor result
+        a.mode = dx_row ? NORM_ROWS : pl.grid == 1 && pl.t <= 64 ? NORM_ONE : NORM_NEED;
         IE_TRY(launch_norm_bwd(a, pl, st));
-        if (dX && !dx_row) {
+        if (dX && a.mode == NORM_NEED) {
             a.mode = NORM_ROUND;
             IE_TRY(launch_norm_bwd(a, pl, st));
         }
@@ -1207,7 +1209,7 @@ ie_status ie_dropout(const ie_mat *X, const ie_mat *R, const ie_mat *Y, const ie
     a.step = d->step;
     a.step_ptr = d->step_ptr;
     a.flags = (uint32_t *)ws;
-    const bool y_row = Y->group == IE_GROUP_ROW;
+    const bool y_row = Y->group == IE_GROUP_ROW || X->rows == 1;
     a.mode = y_row ? NORM_ROWS : NORM_NEED;
     IE_TRY(launch_dropout(a, pl, st));
     if (y_row) return IE_OK;

@@ -244,7 +244,7 @@ struct NormVec {
 // ROWS: one exponent per result row, in one pass.  NEED / ROUND: one for the
 // whole result; NEED leaves the blocks' needs in bmax, ROUND (the rows again)
 // rounds to the largest of them.
-enum NormMode { NORM_ROWS = 0, NORM_NEED = 1, NORM_ROUND = 2 };
+enum NormMode { NORM_ROWS = 0, NORM_NEED = 1, NORM_ROUND = 2, NORM_ONE = 3 };
 // A row's sum of mantissas and 1 / sqrt(T), and in the backward pass its sums
 // G1 and G2 2^-40; kept for the second pass of a whole-tensor result.
 struct RowStat {

@@ -87,10 +87,10 @@ constexpr int norm_block() {
 // T threads per row, E elements per thread.  gamma and beta stay in registers
 // (E <= 12, or when a block holds one row) or in LDS; the next row's loads are
 // in flight while a row is computed.
-template <int T, int E>
-__global__ __launch_bounds__(norm_block<T>()) void norm_fwd_kernel(NormFwd p) {
+template <int T, int E, int BT>
+__global__ __launch_bounds__(BT) void norm_fwd_kernel(NormFwd p) {
     using C = Cols<T, E>;
-    constexpr int BT = norm_block<T>(), RPB = BT / T, W = E / 4;
+    constexpr int RPB = BT / T, W = E / 4;
     constexpr bool LDSV = T <= 64 && E > 12;
     __shared__ int2 sh2[2][BT / 64];
     __shared__ int shi[BT / 64], shm[BT / 64];
@@ -179,6 +179,12 @@ __global__ __launch_bounds__(norm_block<T>()) void norm_fwd_kernel(NormFwd p) {
             }
             inv = pow2(-min(ex, E_MAX));
         }
+        if (p.mode == NORM_ONE) {
+            // the block holds the matrix (threads past the end a row again)
+            const int ex = clamp_exp_flag(max(E_MIN, need_word(row_reduce<BT>(mx.word(), Max{}, shi), p.q)), p.flags);
+            if (threadIdx.x == 0) p.oe[0] = (int8_t)ex;
+            inv = pow2(-ex);
+        }
         if (!ok) continue;
 #pragma unroll
         for (int i = 0; i < W; ++i)
@@ -192,9 +198,9 @@ __global__ __launch_bounds__(norm_block<T>()) void norm_fwd_kernel(NormFwd p) {
     }
 }
 
-// The largest of n exponents, by a block of BT threads.
+// A thread's share of the largest of n exponents, of BT threads.
 template <int BT>
-__device__ __forceinline__ int max_exp(const int8_t *e, long long n, int *sh) {
+__device__ __forceinline__ int max_exp_part(const int8_t *e, long long n) {
     int m = E_MIN;
     for (long long c = 16ll * threadIdx.x; c < n; c += 16ll * BT) {
         uint32_t w[4] = {0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u};
@@ -206,16 +212,15 @@ __device__ __forceinline__ int max_exp(const int8_t *e, long long n, int *sh) {
 #pragma unroll
         for (int k = 0; k < 16; ++k) m = max(m, byte_of(w[k / 4], k % 4));
     }
-    return row_reduce<BT>(m, Max{}, sh);
+    return m;
 }
 
-// The largest exponent of dY's rows: found by this block, or the largest of
-// tops_kernel's.
+// The same for the largest exponent of dY's rows: found by this block, or the
+// largest of tops_kernel's.
 template <int BT>
-__device__ __forceinline__ int top_exp(const int8_t *e, int e_row, long long rows, const int *tops, int n_tops,
-                                       int *sh) {
+__device__ __forceinline__ int top_part(const int8_t *e, int e_row, long long rows, const int *tops, int n_tops) {
     if (!e_row) return e[0];
-    if (!n_tops) return max_exp<BT>(e, rows, sh);
+    if (!n_tops) return max_exp_part<BT>(e, rows);
     int m = E_MIN;
     for (int i = 0; i < n_tops; ++i) m = max(m, tops[i]);
     return m;
@@ -228,6 +233,7 @@ __global__ __launch_bounds__(grad_block(T)) __attribute__((amdgpu_waves_per_eu(T
 void norm_bwd_kernel(NormBwd p) {
     using C = Cols<T, E>;
     constexpr int BT = grad_block(T), RPB = BT / T, W = E / 4;
+    constexpr bool LEAN = T > 512;  // 128 registers: g is made again where it is used
     __shared__ int2 sh2[2][BT / 64];
     __shared__ int shi[BT / 64], shm[BT / 64];
     __shared__ double shd[2][T > 64 ? BT / 64 : 1];
@@ -247,28 +253,43 @@ void norm_bwd_kernel(NormBwd p) {
         ey_next = p.dye[p.dy_row ? r : 0];
     };
     fetch((long long)blockIdx.x * RPB);
-    // the largest exponents of dY and of gamma's channels
-    const int dtop = sums ? top_exp<BT>(p.dye, p.dy_row, p.rows, p.tops, p.n_tops, shi) : 0;
+    // the largest exponents of dY and of gamma's channels, gamma's loads ahead of them
+    uint32_t gw[W], ge[W];
+    if (p.gamma.m) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            gw[i] = load4(p.gamma.m, cols.col(4 * i), n);
+            ge[i] = p.gamma.per ? load4(p.gamma.e, cols.col(4 * i), n) : 0u;
+        }
+    }
+    int2 top = make_int2(sums ? top_part<BT>(p.dye, p.dy_row, p.rows, p.tops, p.n_tops) : E_MIN,
+                         !p.gamma.m ? 0 : p.gamma.per ? max_exp_part<BT>(p.gamma.e, n) : p.gamma.e[0]);
+    top.x = lane_reduce<64>(top.x, Max{});
+    top.y = lane_reduce<64>(top.y, Max{});
+    if ((threadIdx.x & 63) == 0) sh2[0][threadIdx.x >> 6] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < BT / 64; ++i) {
+        top.x = max(top.x, sh2[0][i].x);
+        top.y = max(top.y, sh2[0][i].y);
+    }
+    const int dtop = top.x, gtop = top.y;
     if (sums && blockIdx.x == 0 && threadIdx.x == 0) *p.top = dtop;
-    int gtop = 0;
-    if (p.gamma.m) gtop = p.gamma.per ? max_exp<BT>(p.gamma.e, n, shi) : p.gamma.e[0];
-    uint32_t gw[W];   // gamma re-expressed, four mantissas to a word
-    double gam[E];
+    // gamma re-expressed, four mantissas to a word
+    double gam[LEAN ? 1 : E];
 #pragma unroll
     for (int i = 0; i < W; ++i) {
-        const int c = cols.col(4 * i);
-        uint32_t m = 0x01010101u & cols.mask[i];
-        if (p.gamma.m) {
-            m = load4(p.gamma.m, c, n);
-            if (p.gamma.per) {
-                const uint32_t e = load4(p.gamma.e, c, n);
-                m = pack4(rne_shift32(byte_of(m, 0), gtop - byte_of(e, 0)), rne_shift32(byte_of(m, 1), gtop - byte_of(e, 1)),
+        if (!p.gamma.m) {
+            gw[i] = 0x01010101u & cols.mask[i];
+        } else if (p.gamma.per) {
+            const uint32_t m = gw[i], e = ge[i];
+            gw[i] = pack4(rne_shift32(byte_of(m, 0), gtop - byte_of(e, 0)), rne_shift32(byte_of(m, 1), gtop - byte_of(e, 1)),
                           rne_shift32(byte_of(m, 2), gtop - byte_of(e, 2)), rne_shift32(byte_of(m, 3), gtop - byte_of(e, 3)));
-            }
         }
-        gw[i] = m;
+        if constexpr (!LEAN) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) gam[4 * i + k] = (double)byte_of(m, k);
+            for (int k = 0; k < 4; ++k) gam[4 * i + k] = (double)byte_of(gw[i], k);
+        }
     }
     double inv = 0.0;
     if (p.mode == NORM_ROUND) inv = pow2(-whole_exp<BT>(p.bmax, p.n_bmax, p.oe, p.flags, shi));
@@ -302,14 +323,15 @@ void norm_bwd_kernel(NormBwd p) {
         const float nf = (float)n, s128 = (float)gs.s + 128.0f * nf;
 #pragma unroll
         for (int i = 0; i < W; ++i) w[i] ^= 0x80808080u;
-        double f[E], g[E], g2 = 0.0;
+        double f[E], g[LEAN ? 1 : E], g2 = 0.0;
+        auto g_of = [&](int j) { return (double)byte_of(v[j / 4], j % 4) * (LEAN ? (double)byte_of(gw[j / 4], j % 4) : gam[LEAN ? 0 : j]); };
         int g1 = 0;
 #pragma unroll
         for (int j = 0; j < E; ++j) {
             const double d = centred(w[j / 4], j % 4, nf, s128);
             const double c = (double)byte_of(v[j / 4], j % 4);
             f[j] = __builtin_rint(d * r20);
-            g[j] = c * gam[j];
+            if constexpr (!LEAN) g[j] = c * gam[j];
             if (sums) {
                 const double a = __builtin_fma(c, as, ROUND_MAGIC);
                 af[j] = __builtin_fma(a - ROUND_MAGIC, f[j], af[j]);
@@ -317,11 +339,18 @@ void norm_bwd_kernel(NormBwd p) {
             }
         }
         if (!grad) continue;
+        auto forget = [&] {  // nothing made of these words before is kept
+            if constexpr (LEAN) {
+#pragma unroll
+                for (int i = 0; i < W; ++i) asm volatile("" : "+v"(v[i]), "+v"(gw[i]));
+            }
+        };
+        forget();
         if (p.mode != NORM_ROUND) {
 #pragma unroll
             for (int i = 0; i < W; ++i) g1 = __builtin_amdgcn_sdot4((int)v[i], (int)gw[i], g1, false);
 #pragma unroll
-            for (int j = 0; j < E; ++j) g2 = __builtin_fma(g[j], f[j], g2);
+            for (int j = 0; j < E; ++j) g2 = __builtin_fma(LEAN ? g_of(j) : g[LEAN ? 0 : j], f[j], g2);
             g1 = lane_reduce<(T < 64 ? T : 64)>(g1, Add{});
             g2 = lane_reduce<(T < 64 ? T : 64)>(g2, Add{});
             gs.g1 = (double)g1;
@@ -335,23 +364,30 @@ void norm_bwd_kernel(NormBwd p) {
             gs.g2 = g2 * 0x1p-40;
             if (p.mode == NORM_NEED && ok && t == 0) p.gstat[row] = gs;
         }
+        forget();
 #pragma unroll
         for (int j = 0; j < E; ++j) {
-            const double z = __builtin_fma(g[j], (double)n, -gs.g1) - f[j] * gs.g2;
-            g[j] = z * gs.r;
+            // the result takes f's place
+            f[j] = (__builtin_fma(LEAN ? g_of(j) : g[LEAN ? 0 : j], (double)n, -gs.g1) - f[j] * gs.g2) * gs.r;
         }
         if (!cols.exact) {
 #pragma unroll
             for (int j = 0; j < E; ++j)
-                if (!(cols.mask[j / 4] >> (8 * (j % 4)) & 1u)) g[j] = 0.0;
+                if (!(cols.mask[j / 4] >> (8 * (j % 4)) & 1u)) f[j] = 0.0;
         }
         MaxMag mx;
 #pragma unroll
-        for (int j = 0; j < E; j += 2) mx.add(g[j], g[j + 1]);
-        const int scale = ey + gtop - ex;  // the row's results are g 2^scale
+        for (int j = 0; j < E; j += 2) mx.add(f[j], f[j + 1]);
+        const int scale = ey + gtop - ex;  // the row's results are f 2^scale
         if (p.mode == NORM_NEED) {
             if (mx.word()) run = max(run, mx.word() + (scale << 20));
             continue;
+        }
+        if (p.mode == NORM_ONE) {
+            const int m = row_reduce<BT>(mx.word() ? mx.word() + (scale << 20) : 0, Max{}, shi);
+            const int eo = clamp_exp_flag(max(E_MIN, need_word(m, p.q)), p.flags);
+            if (threadIdx.x == 0) p.oe[0] = (int8_t)eo;
+            inv = pow2(-eo);
         }
         double in = inv * pow2(scale);
         if (p.mode == NORM_ROWS) {
@@ -366,8 +402,8 @@ void norm_bwd_kernel(NormBwd p) {
         if (!ok) continue;
 #pragma unroll
         for (int i = 0; i < W; ++i)
-            w[i] = pack4(mant_of(g[4 * i], in), mant_of(g[4 * i + 1], in), mant_of(g[4 * i + 2], in),
-                         mant_of(g[4 * i + 3], in));
+            w[i] = pack4(mant_of(f[4 * i], in), mant_of(f[4 * i + 1], in), mant_of(f[4 * i + 2], in),
+                         mant_of(f[4 * i + 3], in));
         cols.store(p.out + row * n, w);
     }
     if (grad && p.mode == NORM_NEED) {
@@ -443,7 +479,7 @@ void norm_bwd_kernel(NormBwd p) {
 __global__ __launch_bounds__(1024) void tops_kernel(const int8_t *e, long long n, long long run, int *tops) {
     __shared__ int shi[16];
     const long long b = blockIdx.x * run;
-    const int m = max_exp<1024>(e + b, min(run, n - b), shi);
+    const int m = row_reduce<1024>(max_exp_part<1024>(e + b, min(run, n - b)), Max{}, shi);
     if (threadIdx.x == 0) tops[blockIdx.x] = m;
 }
 
@@ -451,16 +487,25 @@ __global__ __launch_bounds__(1024) void tops_kernel(const int8_t *e, long long n
     X(16, 4) X(16, 8) X(16, 12) X(16, 16) X(16, 24) X(16, 32) X(16, 48) X(32, 24) X(64, 4) X(64, 8) X(64, 16)   \
     X(64, 24) X(64, 32) X(64, 48) X(256, 12) X(256, 16) X(256, 24) X(1024, 8) X(1024, 12) X(1024, 16)
 #define IE_NORM_BWD(X)                                                                                           \
-    X(16, 4) X(16, 8) X(16, 12) X(16, 16) X(64, 4) X(64, 8) X(64, 12) X(64, 16) X(256, 8) X(256, 12) X(256, 16)    \
+    X(16, 4) X(16, 8) X(16, 12) X(16, 16) X(32, 12) X(64, 4) X(64, 8) X(64, 12) X(64, 16) X(256, 8) X(256, 12) X(256, 16)    \
     X(512, 12) X(512, 16) X(1024, 12) X(1024, 16)
+
+#define IE_NORM_ONE(X) X(16, 4) X(16, 8) X(16, 12) X(16, 16) X(64, 4) X(64, 8) X(64, 16)
 
 hipError_t launch_norm_fwd(const NormFwd &a, const NormPlan &pl, hipStream_t st) {
     prof_begin(st, PROF_NORM_FWD);
-#define IE_CASE(T_, E_)       \
+#define IE_CASE(T_, E_)           \
     if (pl.t == T_ && pl.e == E_) \
-        hipLaunchKernelGGL((norm_fwd_kernel<T_, E_>), dim3(pl.grid), dim3(norm_block<T_>()), 0, st, a);
-    IE_NORM_FWD(IE_CASE)
+        hipLaunchKernelGGL((norm_fwd_kernel<T_, E_, norm_block<T_>()>), dim3(pl.grid), dim3(norm_block<T_>()), 0, st, a);
+#define IE_ONE(T_, E_)            \
+    if (pl.t == T_ && pl.e == E_) hipLaunchKernelGGL((norm_fwd_kernel<T_, E_, 1024>), dim3(1), dim3(1024), 0, st, a);
+    if (a.mode == NORM_ONE) {
+        IE_NORM_ONE(IE_ONE)
+    } else {
+        IE_NORM_FWD(IE_CASE)
+    }
 #undef IE_CASE
+#undef IE_ONE
     prof_end(st, PROF_NORM_FWD);
     return hipGetLastError();
 }
@@ -503,7 +548,7 @@ __global__ __launch_bounds__(256) void col_sum_kernel(const int8_t *dy, const in
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, slot = threadIdx.x >> 4;
     const int c = blockIdx.x * 256 + (lane & 15) * 16;
     const long long r0 = (long long)blockIdx.y * chunk, r1 = min(rows, r0 + chunk);
-    const int dtop = top_exp<256>(e, e_row, rows, tops, n_tops, shi);
+    const int dtop = row_reduce<256>(top_part<256>(e, e_row, rows, tops, n_tops), Max{}, shi);
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *top = dtop;
     // 16 bytes may be read past a row's end wherever as many more rows follow;
     // sums of columns past the last are not kept
@@ -607,6 +652,37 @@ __global__ __launch_bounds__(256) void col_round_kernel(ColOut f, ColOut b, int 
     if (blockIdx.x == 0 && threadIdx.x == 0) o.e[0] = (int8_t)e;
 }
 
+// The same in one launch for a few short partial rows (parts <= COL_FEW, cols
+// <= 4096): a block per vector.
+__global__ __launch_bounds__(1024) void col_few_kernel(ColOut f, ColOut b, int parts, int cols, const int *top,
+                                                       uint32_t *flags) {
+    __shared__ int shi[16];
+    const ColOut &o = blockIdx.y == 0 ? f : b;
+    if (!o.m) return;
+    const int pitch = col_pitch(cols), eps = top[0] + o.base;
+    long long s[4] = {0, 0, 0, 0};
+    int need[4], m = NEED_NONE;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int c = threadIdx.x + 1024 * k;
+        if (c < cols) {
+#pragma unroll 4
+            for (int i = 0; i < parts; ++i) s[k] += o.p64 ? o.p64[i * pitch + c] : (long long)o.p32[i * pitch + c];
+        }
+        need[k] = c < cols ? need64(s[k], eps, o.q) : NEED_NONE;
+        m = max(m, need[k]);
+    }
+    if (!o.per) m = row_reduce<1024>(m, Max{}, shi);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int c = threadIdx.x + 1024 * k;
+        if (c >= cols) continue;
+        const int e = clamp_exp_flag(max(E_MIN, o.per ? need[k] : m), flags);
+        o.m[c] = (int8_t)rne_shift64(s[k], e - eps);
+        if (o.per || c == 0) o.e[c] = (int8_t)e;
+    }
+}
+
 hipError_t launch_col_sum(const int8_t *dy, const int8_t *e, int e_row, long long rows, int cols, ColPlan pl,
                           const int *tops, int n_tops, int *top, int *pb, hipStream_t st) {
     prof_begin(st, PROF_COL_SUM);
@@ -619,9 +695,15 @@ hipError_t launch_col_sum(const int8_t *dy, const int8_t *e, int e_row, long lon
 hipError_t launch_col_finish(const ColOut &f, const ColOut &b, int parts, int cols, const int *top, uint32_t *flags,
                              hipStream_t st) {
     const int nb = (cols + 15) / 16;
+    const bool whole = (f.m && !f.per) || (b.m && !b.per);
     prof_begin(st, PROF_COL_FINISH);
+    if (whole && parts <= COL_FEW && cols <= 4096) {
+        hipLaunchKernelGGL(col_few_kernel, dim3(1, b.m ? 2 : 1), dim3(1024), 0, st, f, b, parts, cols, top, flags);
+        prof_end(st, PROF_COL_FINISH);
+        return hipGetLastError();
+    }
     hipLaunchKernelGGL(col_finish_kernel, dim3(nb, b.m ? 2 : 1), dim3(1024), 0, st, f, b, parts, cols, top, flags);
-    if ((f.m && !f.per) || (b.m && !b.per)) {
+    if (whole) {
         const int g = (cols + 255) / 256;
         hipLaunchKernelGGL(col_round_kernel, dim3(g < 1024 ? g : 1024, b.m ? 2 : 1), dim3(256), 0, st, f, b, nb, cols,
                            top, flags);

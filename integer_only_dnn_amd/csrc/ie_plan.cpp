@@ -730,20 +730,33 @@ NormPlan norm_fwd_plan(long long rows, long long cols) {
     return NormPlan{s.t, s.e, (int)(want < 1 ? 1 : want > cap ? cap : want)};
 }
 
+NormPlan norm_one_plan(long long rows, long long cols) {
+    static const RowShape tall[] = {{16, 4}, {16, 8}, {16, 12}, {16, 16}}, flat[] = {{64, 4}, {64, 8}, {64, 16}};
+    if (rows <= 16 && cols <= 1024) {
+        const RowShape s = first_fit(flat, 3, cols);
+        return NormPlan{s.t, s.e, 1};
+    }
+    if (rows <= 64 && cols <= 256) {
+        const RowShape s = first_fit(tall, 4, cols);
+        return NormPlan{s.t, s.e, 1};
+    }
+    return NormPlan{0, 0, 0};
+}
+
 // Each thread keeps the column sums of its elements, so at most 16; blocks of
 // 512 threads (of one row when it takes more than 64), eight waves a CU, each
 // block leaving one row of partial sums (50432 x 192 in 128, 256 and 512
 // blocks: 37.2, 26.4, 30.7 us; 4096 x 4096 in 256 and 512 of 256 threads: 56.3
-// and 46.5).
+// and 46.5, but 898 x 2327, mostly its partial sums, 20.2 and 23.2).
 NormPlan norm_bwd_plan(long long rows, long long cols) {
-    static const RowShape many[] = {{16, 4},  {16, 8},   {16, 12},  {16, 16},  {64, 8},    {64, 12},   {64, 16},
+    static const RowShape many[] = {{16, 4},  {16, 8},  {16, 12},  {16, 16},  {32, 12},  {64, 8},    {64, 12},  {64, 16},
                                     {256, 8}, {256, 12}, {256, 16}, {512, 12}, {512, 16}, {1024, 12}, {1024, 16}};
     static const RowShape few[] = {{64, 4},    {64, 8},   {64, 12},  {64, 16},   {256, 8},  {256, 12},
                                    {256, 16}, {512, 12}, {512, 16}, {1024, 12}, {1024, 16}};
     const RowShape s = rows >= NORM_FEW ? first_fit(many, sizeof many / sizeof *many, cols)
                                         : first_fit(few, sizeof few / sizeof *few, cols);
     const long long rpb = s.t > 64 ? 1 : grad_block(s.t) / s.t, want = (rows + rpb - 1) / rpb;
-    const long long cap = s.t == 256 ? 2 * NCU : NCU;
+    const long long cap = s.t == 256 && rows > 8 * NCU ? 2 * NCU : NCU;
     return NormPlan{s.t, s.e, (int)(want < 1 ? 1 : want > cap ? cap : want)};
 }
 

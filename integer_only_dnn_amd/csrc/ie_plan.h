@@ -375,7 +375,10 @@ struct NormPlan {
 };
 constexpr long long NORM_FEW = 4096;
 NormPlan norm_fwd_plan(long long rows, long long cols);
+// One block of 1024 threads for a whole-tensor result (grid 0: too large).
+NormPlan norm_one_plan(long long rows, long long cols);
 NormPlan norm_bwd_plan(long long rows, long long cols);
+constexpr int COL_FEW = 16;
 
 // Dropout: the same split, with e = 0 for rows too long to be held.
 NormPlan dropout_plan(long long rows, long long cols);

@@ -263,3 +263,33 @@ def test_norm_leaves_what_is_not_its_own(ws):
         for b in bufs:
             assert bool((b[:64] == 77).all()) and bool((b[-64:] == 77).all())
         assert_same(dX, o.layer_norm_bwd(dY, X, gam, EPS, R, R)[0], "dX")
+
+
+# whole-tensor results that one block holds, and one past each edge of that;
+# few partial rows of column sums; one row
+ONE = [(1, 1), (1, 300), (1, 5000), (16, 1024), (17, 1000), (16, 1025), (64, 256), (65, 250), (64, 257), (50, 61),
+       (40, 130), (8, 777), (9, 900), (33, 192), (128, 1000), (129, 4096), (100, 4097)]
+
+
+@pytest.mark.parametrize("shape", ONE, ids=lambda s: "x".join(map(str, s)))
+def test_norm_small_whole_tensor_results(shape, ws):
+    M, N = shape
+    announce(f"norm one block {shape}")
+    rng = np.random.default_rng(M * 7 + N)
+    for xg, vg in ((o.ROW, o.ROW), (o.TENSOR, o.TENSOR)):
+        X, dY = rand_qt(rng, (M, N), xg), rand_qt(rng, (M, N), xg, -20, 3)
+        X.mant[M // 2], dY.mant[M // 3] = 5, 0
+        g, b = rand_qt(rng, (N, 1), vg, -8, -4), rand_qt(rng, (N, 1), vg, -8, -4)
+        e = (EPS.mant, EPS.exp)
+        Y = ie.Mat.empty(M, N, o.TENSOR)
+        ie.ie_layer_norm_fwd(qt_to_dev(X), qt_to_dev(g), qt_to_dev(b), e, Y, ws)
+        assert_same(Y, o.layer_norm_fwd(X, g, b, EPS, o.TENSOR), f"fwd {shape}")
+        dX, dg, db = ie.Mat.empty(M, N, o.TENSOR), ie.Mat.empty(N, 1, vg), ie.Mat.empty(N, 1, o.TENSOR)
+        ie.ie_layer_norm_bwd(qt_to_dev(dY), qt_to_dev(X), qt_to_dev(g), e, dX, dg, db, ws)
+        want = o.layer_norm_bwd(dY, X, g, EPS, o.TENSOR, vg)[:2] + o.layer_norm_bwd(dY, X, g, EPS, o.TENSOR, o.TENSOR)[2:]
+        for got, w, what in zip((dX, dg, db), want, "xgb"):
+            assert_same(got, w, f"bwd {shape} {what}")
+        s = ie.Mat.empty(N, 1, o.TENSOR)
+        ie.ie_linear_bwd_db(qt_to_dev(dY), s, ws)
+        assert_same(s, o.linear_bwd_db(dY, o.TENSOR), f"sums {shape}")
+    assert ws.status() == 0
