@@ -198,21 +198,21 @@ __global__ __launch_bounds__(BT) void norm_fwd_kernel(NormFwd p) {
     }
 }
 
-// A thread's share of the largest of n exponents, of BT threads.
+// A thread's share of the largest of n exponents, of BT threads; several loads
+// in flight.
 template <int BT>
 __device__ __forceinline__ int max_exp_part(const int8_t *e, long long n) {
     int m = E_MIN;
-    for (long long c = 16ll * threadIdx.x; c < n; c += 16ll * BT) {
-        uint32_t w[4] = {0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u};
-        if (c + 16 <= n) {
-            __builtin_memcpy(w, e + c, 16);
-        } else {
-            for (int k = 0; c + k < n; ++k) m = max(m, (int)e[c + k]);
-        }
+    const long long whole = n / 16;
+#pragma unroll 4
+    for (long long c = threadIdx.x; c < whole; c += BT) {
+        uint32_t w[4];
+        __builtin_memcpy(w, e + 16 * c, 16);
 #pragma unroll
         for (int k = 0; k < 16; ++k) m = max(m, byte_of(w[k / 4], k % 4));
     }
-    return m;
+    const long long c = 16 * whole + threadIdx.x;
+    return c < n ? max(m, (int)e[c]) : m;
 }
 
 // The same for the largest exponent of dY's rows: found by this block, or the

@@ -391,7 +391,7 @@ ColPlan col_plan(long long rows, long long cols);
 
 // The largest exponent of more rows than this is found by a kernel of its own
 // (in parts), of fewer by every block that needs it.
-constexpr long long TOPS_ROWS = 16384;
+constexpr long long TOPS_ROWS = 65536;
 constexpr int TOPS_MAX = 64;
 int n_tops(long long rows, int e_row);
 

@@ -293,3 +293,17 @@ def test_norm_small_whole_tensor_results(shape, ws):
         ie.ie_linear_bwd_db(qt_to_dev(dY), s, ws)
         assert_same(s, o.linear_bwd_db(dY, o.TENSOR), f"sums {shape}")
     assert ws.status() == 0
+
+
+@pytest.mark.parametrize("shape", [(65536, 3), (70001, 7), (131073, 16)], ids=lambda s: "x".join(map(str, s)))
+def test_norm_many_rows(shape, ws):
+    """The rows' largest exponent found by a launch of its own, and one row short of that."""
+    announce(f"norm many rows {shape}")
+    M, N = shape
+    rng = np.random.default_rng(M)
+    X, dY = rand_qt(rng, (M, N), o.ROW), rand_qt(rng, (M, N), o.ROW, -20, -9)
+    dY.exp[M - 1] = -5  # the largest, in the last row
+    check(X, dY, None, None, (o.ROW, o.TENSOR), o.ROW, ws, what=str(shape))
+    s = ie.Mat.empty(N, 1, o.ROW)
+    ie.ie_linear_bwd_db(qt_to_dev(dY), s, ws)
+    assert_same(s, o.linear_bwd_db(dY, o.ROW), str(shape))
