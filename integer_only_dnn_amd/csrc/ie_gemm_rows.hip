@@ -2,13 +2,16 @@
 // inside a workgroup, so that a row's exponent is known before it leaves the
 // registers: one pass, no intermediate result in memory.
 //
-// A workgroup of 8 waves computes 64 rows and 256 NI >= N columns at a time,
-// wave w the columns 32 NI w .. 32 NI (w + 1) - 1 of every row, with
+// A workgroup of 8 waves computes 64 rows and 256 NI >= N columns at a time
+// (NI <= 2: two of 4 waves share the CU with 32 rows each, one's epilogue beside
+// the other's products; wider rows would stream too much weight that way), each
+// wave an equal share of the columns of every row, with
 // v_mfma_i32_32x32x32_i8 run transposed (a lane holds one row of the result).
 // The weight is laid out beforehand in the order the matrix instructions take
 // it (1 KiB for 32 rows and 32 contraction bytes, lane by lane), so a wave
-// streams its share of it from L2 straight into registers, two steps ahead; the 64 rows of X are staged in LDS, up to 1024 contraction bytes at a
-// time.  Nothing in the contraction loop waits for another wave.
+// streams its share of it from L2 straight into registers, two steps ahead;
+// the rows of X are staged in LDS, up to 1024 contraction bytes at a time.
+// Nothing in the contraction loop waits for another wave.
 // Workgroups are persistent: the next tile's X is loaded during the products
 // (a long one's, and the residual, while the result is stored, when the
 // registers are free), after one word of each of its lines has brought it into
@@ -18,8 +21,8 @@
 // each value is computed once (NI = 4 has no room and computes it twice).
 //
 // Bound by the fp64 and conversion instructions of the epilogue next to the
-// products (they take turns: the registers hold one workgroup of NI >= 2 per
-// CU), not by memory.  Measured, with the weight's layout: 50432 x 768 x 192
+// products (they take turns in a workgroup, and the registers hold no second
+// one of NI >= 3), not by memory.  Measured, with the weight's layout: 50432 x 768 x 192
 // 34 us, 46 with a residual (round to odd by tiles and the pass that closes it:
 // 74 without), 25216 x 768 x 768 with a residual 39 us (51).
 #include <algorithm>
@@ -31,8 +34,6 @@
 #pragma clang fp contract(off)
 
 namespace ie {
-
-constexpr int ROWS_THR = 512, ROWS_BM = 64;
 
 // W [N x K] -> out[n / 32][k / 32][lane][16], lane l holding row l % 32 and
 // bytes 16 (l / 32) .. + 15 of the 32; zeros past N and K.  A block lays out
@@ -53,33 +54,37 @@ enum { RES_NONE, RES_VEC, RES_ANY };
 template <int NI, int KC, int RES>
 struct RowsCfg {
     static constexpr int BN = 256 * NI, RP = BN + 16;  // RP: pitch of the residual / result tile
+    // blocks of 32 rows, waves, and a wave's blocks of 32 columns
+    static constexpr int MA = NI <= 2 ? 1 : 2, WV = 4 * MA, NB = 8 * NI / WV, BM = 32 * MA, THR = 64 * WV;
+    static constexpr int PER_CU = NI == 1 ? 4 : NI == 2 ? 2 : 1;  // resident workgroups
     static constexpr int D = 2;  // steps of the weight in flight
     static constexpr bool KEEP = NI < 4;
     // the next tile's X is loaded during the products where it fits the registers
     static constexpr bool EARLY = KC <= 8;
-    static constexpr int A = KC * 2048, CS = A + 16 * BN, RED = CS + 8 * ROWS_BM * 4, LDS = RED + ROWS_BM * RP;
+    static constexpr int A = KC * 1024 * MA, CS = A + 16 * BN, RED = CS + WV * BM * 4, LDS = RED + BM * RP;
 };
 
 template <int NI, int KC, int RES>
-__global__ __launch_bounds__(ROWS_THR) __attribute__((amdgpu_waves_per_eu(NI == 1 ? 4 : 2)))
+__global__ __launch_bounds__((RowsCfg<NI, KC, RES>::THR)) __attribute__((amdgpu_waves_per_eu(NI == 1 ? 4 : 2)))
 void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int ks, AddEpi e) {
     using C = RowsCfg<NI, KC, RES>;
-    constexpr int BN = C::BN, RP = C::RP, D = C::D, U = KC / 4;
+    constexpr int BN = C::BN, RP = C::RP, D = C::D, U = KC / 4, MA = C::MA, NB = C::NB, WV = C::WV;
+    constexpr int BM = C::BM, THR = C::THR;
     __shared__ __attribute__((aligned(16))) int8_t lds[C::LDS];
     double *cs = (double *)(lds + C::A), *bs = cs + BN;  // column scales, bias
-    int *red = (int *)(lds + C::CS);                    // row maxima of the waves [8][64]
+    int *red = (int *)(lds + C::CS);                    // row maxima of the waves [WV][BM]
     int8_t *rt = lds + C::RED;                          // the residual, then the result
     int tid = threadIdx.x;
     const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int tiles = (M + ROWS_BM - 1) / ROWS_BM;
+    const int tiles = (M + BM - 1) / BM;
 
     // X: thread t takes, of row (t / 4) % 64, the 16-byte piece t % 4 + 4 (t / 256)
     // of every four contraction steps; rows past the last repeat it, bytes past K
     // (the next row's) meet zeros of the weight, and at the matrix's end its last
     // 16 bytes are moved down
     auto fetch_x = [&](int tile, int s0, v4i (&an)[U]) {
-        const int arow = (tid >> 2) & 63, aj = (tid & 3) + 4 * (tid >> 8);
-        const long long o = (long long)min(tile * ROWS_BM + arow, M - 1) * K, last = (long long)M * K - 16;
+        const int arow = (tid >> 2) & (BM - 1), aj = (tid & 3) + 4 * (tid / (4 * BM));
+        const long long o = (long long)min(tile * BM + arow, M - 1) * K, last = (long long)M * K - 16;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int k = (s0 + 4 * u) * 32 + aj * 16;
@@ -95,19 +100,19 @@ void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int
         }
     };
     auto store_x = [&](const v4i (&an)[U]) {
-        const int arow = (tid >> 2) & 63, aj = (tid & 3) + 4 * (tid >> 8);
-        int8_t *ad = lds + (((aj >> 1) * 2 + (arow >> 5)) * 64 + (aj & 1) * 32 + (arow & 31)) * 16;
+        const int arow = (tid >> 2) & (BM - 1), aj = (tid & 3) + 4 * (tid / (4 * BM));
+        int8_t *ad = lds + (((aj >> 1) * MA + (arow >> 5)) * 64 + (aj & 1) * 32 + (arow & 31)) * 16;
 #pragma unroll
-        for (int u = 0; u < U; ++u) *(v4i *)(ad + u * 8192) = an[u];
+        for (int u = 0; u < U; ++u) *(v4i *)(ad + u * 4096 * MA) = an[u];
     };
     // the residual of a tile, 16 bytes at a time
-    constexpr int CPR = BN / 16, RR = ROWS_BM * CPR / ROWS_THR;
+    constexpr int CPR = BN / 16, RR = BM * CPR / THR;
     auto fetch_r = [&](int tile, v4i (&rr)[RR]) {
         if constexpr (RES == RES_NONE) return;
 #pragma unroll
         for (int i = 0; i < RR; ++i) {
-            const int q = i * ROWS_THR + tid, row = q / CPR, c = q % CPR * 16;
-            const int8_t *src = e.r + (long long)min(tile * ROWS_BM + row, M - 1) * N;
+            const int q = i * THR + tid, row = q / CPR, c = q % CPR * 16;
+            const int8_t *src = e.r + (long long)min(tile * BM + row, M - 1) * N;
             if constexpr (RES == RES_VEC) {
                 rr[i] = *(const v4i *)(src + (c < N ? c : 0));
             } else {
@@ -119,13 +124,13 @@ void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int
         if constexpr (RES != RES_NONE) {
 #pragma unroll
             for (int i = 0; i < RR; ++i) {
-                const int q = i * ROWS_THR + tid, row = q / CPR, c = q % CPR * 16;
+                const int q = i * THR + tid, row = q / CPR, c = q % CPR * 16;
                 *(v4i *)(rt + row * RP + c) = c < N ? rr[i] : v4i{0, 0, 0, 0};
             }
         }
     };
     const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(
-        (void *)(wt + (long long)wave * NI * ks * 1024), (short)0, NI * ks * 1024, 0x00020000);
+        (void *)(wt + (long long)wave * NB * ks * 1024), (short)0, NB * ks * 1024, 0x00020000);
     auto wtile = [&](int b, int s) -> v4i {
         return (v4i)__builtin_amdgcn_raw_buffer_load_b128(wr, lane * 16, (b * ks + s) * 1024, 0);
     };
@@ -133,7 +138,7 @@ void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int
     v4i x0[U], r0[RR];
     fetch_x(blockIdx.x, 0, x0);
     fetch_r(blockIdx.x, r0);
-    for (int n = tid; n < BN; n += ROWS_THR) {
+    for (int n = tid; n < BN; n += THR) {
         // past the last column everything is zero
         cs[n] = n < N ? pow2((int)e.we[e.w_row ? n : 0]) : 0.0;
         bs[n] = n < N && e.bias.m ? (double)e.bias.m[n] * pow2((int)e.bias.e[e.bias.per ? n : 0]) : 0.0;
@@ -142,39 +147,39 @@ void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int
     store_r(r0);
 
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const int m0 = tile * ROWS_BM, next = min(tile + (int)gridDim.x, tiles - 1);  // past the end: fetched, never used
+        const int m0 = tile * BM, next = min(tile + (int)gridDim.x, tiles - 1);  // past the end: fetched, never used
         v4i xn[U], rn[RR];
         // offsets made of the thread's number are made anew for every tile: kept,
         // they would not fit the registers
         asm volatile("" : "+v"(tid));
         // one word of every 128 bytes of the next tile's rows, so that they are in L2
         // when they are fetched
-        const int ahead = min(tile + (int)gridDim.x, tiles - 1) * ROWS_BM + (tid >> 3);
+        const int ahead = min(tile + (int)gridDim.x, tiles - 1) * BM + (tid >> 3);
         const long long arow = min(ahead, M - 1);
         uint32_t warm = 0;
         for (int c = (tid & 7) * 128; c < min(K - 3, KC * 32); c += 1024) warm |= *(const uint32_t *)(x + arow * K + c);
         if constexpr (RES == RES_VEC)
             for (int c = (tid & 7) * 128; c < N; c += 1024) warm |= *(const uint32_t *)(e.r + arow * N + c);
         // this lane's two rows' exponents
-        double sx[2], sr[2];
+        double sx[MA], sr[MA];
 #pragma unroll
-        for (int a = 0; a < 2; ++a) {
+        for (int a = 0; a < MA; ++a) {
             const int m = min(m0 + a * 32 + (lane & 31), M - 1);
             sx[a] = pow2((int)e.xe[e.x_row ? m : 0]);
             sr[a] = RES ? pow2((int)e.re[e.r_row ? m : 0]) : 0.0;
         }
-        v16i acc[2][NI];
+        v16i acc[MA][NB];
 #pragma unroll
-        for (int a = 0; a < 2; ++a)
+        for (int a = 0; a < MA; ++a)
 #pragma unroll
-            for (int b = 0; b < NI; ++b)
+            for (int b = 0; b < NB; ++b)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) acc[a][b][r] = 0;
-        v4i bf[D][NI];
+        v4i bf[D][NB];
 #pragma unroll
         for (int u = 0; u < D; ++u)
 #pragma unroll
-            for (int b = 0; b < NI; ++b) bf[u][b] = wtile(b, u);
+            for (int b = 0; b < NB; ++b) bf[u][b] = wtile(b, u);
         __syncthreads();  // X and the residual are there
         if constexpr (C::EARLY) fetch_x(next, 0, xn);
 
@@ -191,14 +196,14 @@ void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int
             for (int s = 0; s < steps; s += D) {
 #pragma unroll
                 for (int u = 0; u < D; ++u) {
-                    v4i af[2];
+                    v4i af[MA];
 #pragma unroll
-                    for (int a = 0; a < 2; ++a) af[a] = as[((s + u) * 2 + a) * 64];
+                    for (int a = 0; a < MA; ++a) af[a] = as[((s + u) * MA + a) * 64];
                     const int next = min(s0 + s + u + D, ks - 1);  // past the end: loaded, never used
 #pragma unroll
-                    for (int b = 0; b < NI; ++b) {
+                    for (int b = 0; b < NB; ++b) {
 #pragma unroll
-                        for (int a = 0; a < 2; ++a)
+                        for (int a = 0; a < MA; ++a)
                             acc[a][b] = __builtin_amdgcn_mfma_i32_32x32x32_i8(bf[u][b], af[a], acc[a][b], 0, 0, 0);
                         bf[u][b] = wtile(b, next);
                     }
@@ -212,13 +217,13 @@ void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int
         // four neighbours of the result (columns 32 b + 8 h of this lane's own on) of
         // both rows this lane holds; each fused step is an exact product and one
         // rounded sum
-        const int c0 = wave * 32 * NI + 4 * (lane >> 5);
+        const int c0 = wave * 32 * NB + 4 * (lane >> 5);
         int ocs = C::A + 8 * c0, ort = C::RED + (lane & 31) * RP + c0;  // of its scales and residuals in LDS
         asm volatile("" : "+v"(ocs), "+v"(ort));
-        auto quad = [&](int b, int h, double (&y)[2][4]) {
+        auto quad = [&](int b, int h, double (&y)[MA][4]) {
             const double *s = (const double *)(lds + ocs) + b * 32 + 8 * h, *o = s + BN;
 #pragma unroll
-            for (int a = 0; a < 2; ++a) {
+            for (int a = 0; a < MA; ++a) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) y[a][k] = __builtin_fma((double)acc[a][b][4 * h + k], sx[a] * s[k], o[k]);
                 if constexpr (RES) {
@@ -228,34 +233,34 @@ void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int
                 }
             }
         };
-        double yk[C::KEEP ? NI * 4 : 1][2][4];
-        MaxMag mx[2];
+        double yk[C::KEEP ? NB * 4 : 1][MA][4];
+        MaxMag mx[MA];
 #pragma unroll
-        for (int b = 0; b < NI; ++b)
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
-                double(&y)[2][4] = yk[C::KEEP ? b * 4 + h : 0];
+                double(&y)[MA][4] = yk[C::KEEP ? b * 4 + h : 0];
                 quad(b, h, y);
 #pragma unroll
-                for (int a = 0; a < 2; ++a) {
+                for (int a = 0; a < MA; ++a) {
                     mx[a].add(y[a][0], y[a][1]);
                     mx[a].add(y[a][2], y[a][3]);
                 }
                 if (h & 1) __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
-        for (int a = 0; a < 2; ++a) {
+        for (int a = 0; a < MA; ++a) {
             const int m = swap_reduce<32>(mx[a].word(), Max{});
-            if (lane < 32) red[wave * ROWS_BM + a * 32 + lane] = m;
+            if (lane < 32) red[wave * BM + a * 32 + lane] = m;
         }
         __syncthreads();
-        double inv[2];
+        double inv[MA];
 #pragma unroll
-        for (int a = 0; a < 2; ++a) {
+        for (int a = 0; a < MA; ++a) {
             const int r = a * 32 + (lane & 31), m = m0 + r;
             int w = red[r];
 #pragma unroll
-            for (int i = 1; i < 8; ++i) w = max(w, red[i * ROWS_BM + r]);
+            for (int i = 1; i < WV; ++i) w = max(w, red[i * BM + r]);
             int ex = max(E_MIN, need_word(w, e.q));
             if (tid < 32 && m < M) {
                 ex = clamp_exp_flag(ex, e.flags);
@@ -266,18 +271,18 @@ void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int
         if constexpr (!C::KEEP) {
             // nothing of the first pass is kept
 #pragma unroll
-            for (int a = 0; a < 2; ++a)
+            for (int a = 0; a < MA; ++a)
 #pragma unroll
-                for (int b = 0; b < NI; ++b) asm volatile("" : "+v"(acc[a][b]));
+                for (int b = 0; b < NB; ++b) asm volatile("" : "+v"(acc[a][b]));
         }
 #pragma unroll
-        for (int b = 0; b < NI; ++b)
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
-                double(&y)[2][4] = yk[C::KEEP ? b * 4 + h : 0];
+                double(&y)[MA][4] = yk[C::KEEP ? b * 4 + h : 0];
                 if constexpr (!C::KEEP) quad(b, h, y);
 #pragma unroll
-                for (int a = 0; a < 2; ++a) {
+                for (int a = 0; a < MA; ++a) {
                     const uint32_t o = pack4(mant_of(y[a][0], inv[a]), mant_of(y[a][1], inv[a]), mant_of(y[a][2], inv[a]),
                                        mant_of(y[a][3], inv[a]));
                     *(uint32_t *)(lds + ort + a * 32 * RP + b * 32 + 8 * h) = o;
@@ -291,7 +296,7 @@ void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int
         const bool vec = (N & 15) == 0 && ((uintptr_t)e.y & 15) == 0;
 #pragma unroll
         for (int i = 0; i < RR; ++i) {
-            const int q = i * ROWS_THR + tid, row = q / CPR, c = q % CPR * 16;
+            const int q = i * THR + tid, row = q / CPR, c = q % CPR * 16;
             if (m0 + row < M && c < N) {
                 v4i o = *(const v4i *)(rt + row * RP + c);
                 if (e.relu) {
@@ -315,12 +320,14 @@ void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int
 
 hipError_t launch_rows_add(const int8_t *x, const int8_t *w, int M, int N, int K, int8_t *wt, int ni,
                            const AddEpi &e, hipStream_t st) {
-    const int ks = rows_steps(K), tiles = (M + ROWS_BM - 1) / ROWS_BM;
+    const int ks = rows_steps(K);
     prof_begin(st, PROF_GEMM_ADD);
     hipLaunchKernelGGL(tile_weight_kernel, dim3(8 * ni, (ks + 3) / 4), dim3(256), 0, st, w, N, K, ks, wt);
-    const dim3 grid(std::min(tiles, ni == 1 ? 2 * NCU : NCU)), block(ROWS_THR);
     auto go = [&](auto ni_tag, auto kc_tag) {
         constexpr int NI = decltype(ni_tag)::value, KC = decltype(kc_tag)::value;
+        using C = RowsCfg<NI, KC, RES_NONE>;
+        const int tiles = (M + C::BM - 1) / C::BM;
+        const dim3 grid(std::min(tiles, C::PER_CU * NCU)), block(C::THR);
         if (!e.r) hipLaunchKernelGGL((rows_add_kernel<NI, KC, RES_NONE>), grid, block, 0, st, x, wt, M, N, K, ks, e);
         else if (e.r_vec) hipLaunchKernelGGL((rows_add_kernel<NI, KC, RES_VEC>), grid, block, 0, st, x, wt, M, N, K, ks, e);
         else hipLaunchKernelGGL((rows_add_kernel<NI, KC, RES_ANY>), grid, block, 0, st, x, wt, M, N, K, ks, e);
