@@ -171,16 +171,18 @@ class Workspace:
     def __init__(self, device="cuda"):
         self.device = torch.device(device)
         self.buf = None
+        self._at = (0, 0)  # buf's address and size
 
     def get(self, nbytes: int):
-        if self.buf is None or self.buf.numel() < nbytes:
+        if self.buf is None or self._at[1] < nbytes:
             flags = self.status(clear=False) if self.buf is not None else 0
             self.buf = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=self.device)
-            _check(lib().ie_workspace_init(self.buf.data_ptr(), self.buf.numel(), _stream(self.device)),
+            self._at = (self.buf.data_ptr(), self.buf.numel())
+            _check(lib().ie_workspace_init(*self._at, _stream(self.device)),
                    "ie_workspace_init")
             if flags:
                 raise IeError(5, "workspace flags were set before it grew")
-        return self.buf.data_ptr(), self.buf.numel()
+        return self._at
 
     def status(self, clear: bool = True) -> int:
         if self.buf is None:
@@ -202,13 +204,26 @@ def _ws_size(name: str, *args) -> int:
     """The library's workspace size for a call shape (memoised: the library
     plans the call to answer; the planner's tuning overrides are part of the
     key)."""
-    key = (name, os.environ.get("IE_TILE"), os.environ.get("IE_WTILE")) + tuple((a.n, a.h, a.w, a.c, a.k, a.r, a.s, a.stride, a.pad) if isinstance(a, ie_conv_desc) else a
-                          for a in args)
+    a = args[0]
+    if isinstance(a, ie_conv_desc):
+        shape = (a.n, a.h, a.w, a.c, a.k, a.r, a.s, a.stride, a.pad) + args[1:]
+    else:
+        shape = args
+    key = (name, os.environ.get("IE_TILE"), os.environ.get("IE_WTILE"), shape)
     n = _ws_sizes.get(key)
     if n is None:
         fn = getattr(lib(), name)
         n = fn(*[byref(a) if isinstance(a, ie_conv_desc) else a for a in args])
         _ws_sizes[key] = n
+    return n
+
+
+def _ws_rows(name: str, rows: int, cols: int) -> int:
+    """The same for an entry point that plans by its rows and columns alone."""
+    key = (name, rows, cols)
+    n = _ws_sizes.get(key)
+    if n is None:
+        n = _ws_sizes[key] = getattr(lib(), name)(rows, cols)
     return n
 
 
@@ -387,7 +402,7 @@ def _opt(m: Mat | None):
 def ie_layer_norm_fwd(X: Mat, gamma: Mat | None, beta: Mat | None, eps, Y: Mat, ws: Workspace) -> None:
     """Y = layer norm of X's rows, times gamma plus beta; eps is a (C, e) scalar."""
     x, y = X.c(), Y.c()
-    p, b = ws.get(_ws_size("ie_layer_norm_fwd_workspace", x.rows, x.cols))
+    p, b = ws.get(_ws_rows("ie_layer_norm_fwd_workspace", x.rows, x.cols))
     _check(lib().ie_layer_norm_fwd(byref(x), _opt(gamma), _opt(beta), ie_scalar(*eps), byref(y), p, b,
                                    _stream(ws.device)), "ie_layer_norm_fwd")
 
@@ -396,7 +411,7 @@ def ie_layer_norm_bwd(dY: Mat, X: Mat, gamma: Mat | None, eps, dX: Mat | None, d
                       dbeta: Mat | None, ws: Workspace) -> None:
     """The gradients of ie_layer_norm_fwd's input, gamma and beta (any of them None to skip it)."""
     dy, x = dY.c(), X.c()
-    p, b = ws.get(_ws_size("ie_layer_norm_bwd_workspace", x.rows, x.cols))
+    p, b = ws.get(_ws_rows("ie_layer_norm_bwd_workspace", x.rows, x.cols))
     _check(lib().ie_layer_norm_bwd(byref(dy), byref(x), _opt(gamma), ie_scalar(*eps), _opt(dX), _opt(dgamma),
                                    _opt(dbeta), p, b, _stream(ws.device)), "ie_layer_norm_bwd")
 
@@ -412,7 +427,7 @@ def ie_linear_fwd_fused(X: Mat, W: Mat, bias: Mat | None, R: Mat | None, Y: Mat,
 def ie_linear_bwd_db(dY: Mat, db: Mat, ws: Workspace) -> None:
     """db = the sum of dY's rows (a linear layer's bias gradient)."""
     dy, d = dY.c(), db.c()
-    p, b = ws.get(_ws_size("ie_linear_bwd_db_workspace", dy.rows, dy.cols))
+    p, b = ws.get(_ws_rows("ie_linear_bwd_db_workspace", dy.rows, dy.cols))
     _check(lib().ie_linear_bwd_db(byref(dy), byref(d), p, b, _stream(ws.device)), "ie_linear_bwd_db")
 
 
@@ -427,7 +442,7 @@ def ie_dropout(X: Mat, R: Mat | None, Y: Mat, drop: int, seed: int, step: int, w
         raise ValueError("step_ptr must be an int64 device tensor of one element")
     x, y = X.c(), Y.c()
     d = ie_dropout_desc(seed, step, step_ptr.data_ptr() if step_ptr is not None else None, drop)
-    p, b = ws.get(_ws_size("ie_dropout_workspace", x.rows, x.cols))
+    p, b = ws.get(_ws_rows("ie_dropout_workspace", x.rows, x.cols))
     _check(lib().ie_dropout(byref(x), _opt(R), byref(y), byref(d), p, b, _stream(ws.device)), "ie_dropout")
 
 
