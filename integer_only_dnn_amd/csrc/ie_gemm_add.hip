@@ -11,6 +11,11 @@
 // at a time, and the bias is the same for the 32 lanes of a half-wave.  The
 // two products of an element (by the scales' powers of two) are exact in the
 // fp64 unit, which runs its fused multiply-add at the fp32 rate.
+//
+// Whole-tensor results, and rows that do not lie whole in a workgroup, leave
+// rounded to odd as int16 and take a second pass: 25216 x 768 x 768 with a
+// residual into a whole-tensor result 43 + 11 us, bound by the epilogue's fp64
+// instructions, the int16 values' way through memory and back next.
 #include "ie_f64.h"
 #include "ie_gemm_impl.h"
 
@@ -244,7 +249,8 @@ hipError_t launch_gemm_add(const Operand &A, const Operand &B, int M, int N, int
 // Round-to-odd results (units of 2^(need - 2), the need of their row in the
 // tile or of the tile) rounded at their group's largest need.  A value has at
 // most 11 bits, so one fp32 fused multiply-add on it rounds half to even into
-// the low bits of the sum.  T lanes per row, eight values each.
+// the low bits of the sum.  T lanes per row, eight values each: a stream
+// of three bytes a value, 8591 x 1486 10 us (7.3 at the rate of a large copy).
 // ---------------------------------------------------------------------------
 
 template <int T>

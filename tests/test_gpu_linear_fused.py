@@ -435,3 +435,20 @@ def test_linear_fused_few_rows_flag_and_graph(yg):
         assert_same(Y, o.linear_fwd_fused(X, W, b, D, yg), f"replay {i}")
         check(X, W, b, D, yg, True, own)
     assert own.status() == 0
+
+
+@pytest.mark.parametrize("shape", [(2100, 300, 96), (2048, 257, 33), (7, 300, 77), (64, 640, 1024), (1, 33, 16)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_linear_fused_without_addends_in_few_and_whole_rows(shape, ws):
+    announce(f"linear fused plain {shape}")
+    M, N, K = shape
+    rng = np.random.default_rng(11)
+    for xg, wg, yg in ((R, R, R), (T, R, R), (T, T, T)):
+        X, W = rand_qt(rng, (M, K), xg), rand_qt(rng, (N, K), wg)
+        for act in (ie.ACT_NONE, ie.ACT_RELU):
+            Y, Z = ie.Mat.empty(M, N, yg), ie.Mat.empty(M, N, yg)
+            ie.ie_linear_fwd_fused(qt_to_dev(X), qt_to_dev(W), None, None, Y, act, ws)
+            ie.ie_linear_fwd_act(qt_to_dev(X), qt_to_dev(W), Z, act, ws)
+            torch.cuda.synchronize()
+            assert torch.equal(Y.mant, Z.mant) and torch.equal(Y.exp, Z.exp)
+    assert ws.status() == 0
