@@ -289,14 +289,17 @@ void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int
                 }
                 if (h & 1) __builtin_amdgcn_sched_barrier(0);
             }
-        __syncthreads();
         // y is gone: room for the next tile's loads
         if constexpr (!C::EARLY) fetch_x(next, 0, xn);
         fetch_r(next, rn);
+        // the wave's own columns, 16 bytes per lane: its LDS writes come before its
+        // reads, and no other wave is waited for
         const bool vec = (N & 15) == 0 && ((uintptr_t)e.y & 15) == 0;
+        constexpr int CPW = 2 * NB;
+        __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int i = 0; i < RR; ++i) {
-            const int q = i * THR + tid, row = q / CPR, c = q % CPR * 16;
+        for (int i = 0; i < BM * CPW / 64; ++i) {
+            const int q = i * 64 + (tid & 63), row = q / CPW, c = wave * 32 * NB + q % CPW * 16;
             if (m0 + row < M && c < N) {
                 v4i o = *(const v4i *)(rt + row * RP + c);
                 if (e.relu) {
@@ -312,7 +315,7 @@ void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int
                 }
             }
         }
-        __syncthreads();  // the result is stored
+        if constexpr (RES != RES_NONE) __syncthreads();  // the result is read: room for the next residual
         store_x(xn);
         store_r(rn);
     }
