@@ -20,11 +20,12 @@
 // The epilogue holds y in fp64, in the registers the accumulators leave, so
 // each value is computed once (NI = 4 has no room and computes it twice).
 //
-// Bound by the fp64 and conversion instructions of the epilogue next to the
-// products (they take turns in a workgroup, and the registers hold no second
-// one of NI >= 3), not by memory.  Measured, with the weight's layout: 50432 x 768 x 192
-// 34 us, 46 with a residual (round to odd by tiles and the pass that closes it:
-// 74 without), 25216 x 768 x 768 with a residual 39 us (51).
+// Bound by its phases one after the other: over 50432 x 768 x 192 the cycles
+// are 48 % fp64 and conversion instructions of the epilogue, 40 % LDS (column
+// scales and biases, staging) and 14 % products, and the registers hold no
+// second workgroup of NI >= 3 to set beside.  Measured, with the weight's layout:
+// 50432 x 768 x 192 33 us, 45 with a residual (round to odd by tiles and the pass
+// that closes it: 74 without), 25216 x 768 x 768 with a residual 38 us (51).
 #include <algorithm>
 #include <type_traits>
 
@@ -106,12 +107,13 @@ void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int
         for (int u = 0; u < U; ++u) *(v4i *)(ad + u * 4096 * MA) = an[u];
     };
     // the residual of a tile, 16 bytes at a time
-    constexpr int CPR = BN / 16, RR = BM * CPR / THR;
+    // (16 threads a row, every 16th piece each)
+    constexpr int RPP = THR / 16, RR = BM / RPP * NI;  // rows of a pass, pieces of a thread
     auto fetch_r = [&](int tile, v4i (&rr)[RR]) {
         if constexpr (RES == RES_NONE) return;
 #pragma unroll
         for (int i = 0; i < RR; ++i) {
-            const int q = i * THR + tid, row = q / CPR, c = q % CPR * 16;
+            const int row = i / NI * RPP + (tid >> 4), c = ((tid & 15) + 16 * (i % NI)) * 16;
             const int8_t *src = e.r + (long long)min(tile * BM + row, M - 1) * N;
             if constexpr (RES == RES_VEC) {
                 rr[i] = *(const v4i *)(src + (c < N ? c : 0));
@@ -124,7 +126,7 @@ void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int
         if constexpr (RES != RES_NONE) {
 #pragma unroll
             for (int i = 0; i < RR; ++i) {
-                const int q = i * THR + tid, row = q / CPR, c = q % CPR * 16;
+                const int row = i / NI * RPP + (tid >> 4), c = ((tid & 15) + 16 * (i % NI)) * 16;
                 *(v4i *)(rt + row * RP + c) = c < N ? rr[i] : v4i{0, 0, 0, 0};
             }
         }
@@ -169,12 +171,6 @@ void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int
             sr[a] = RES ? pow2((int)e.re[e.r_row ? m : 0]) : 0.0;
         }
         v16i acc[MA][NB];
-#pragma unroll
-        for (int a = 0; a < MA; ++a)
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) acc[a][b][r] = 0;
         v4i bf[D][NB];
 #pragma unroll
         for (int u = 0; u < D; ++u)
@@ -184,6 +180,32 @@ void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int
         if constexpr (C::EARLY) fetch_x(next, 0, xn);
 
         const v4i *as = (const v4i *)lds + lane;
+        // D steps from step s of the staged ones, k of the contraction; the very first
+        // products start the sums
+        auto go = [&](int s, int k, auto start) {
+#pragma unroll
+            for (int u = 0; u < D; ++u) {
+                v4i af[MA];
+#pragma unroll
+                for (int a = 0; a < MA; ++a) af[a] = as[((s + u) * MA + a) * 64];
+                const int next = min(k + u + D, ks - 1);  // past the end: loaded, never used
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+#pragma unroll
+                    for (int a = 0; a < MA; ++a) {
+                        if constexpr (decltype(start)::value) {
+                            const v16i zero = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+                            acc[a][b] = __builtin_amdgcn_mfma_i32_32x32x32_i8(bf[u][b], af[a], u ? acc[a][b] : zero, 0, 0, 0);
+                        } else {
+                            acc[a][b] = __builtin_amdgcn_mfma_i32_32x32x32_i8(bf[u][b], af[a], acc[a][b], 0, 0, 0);
+                        }
+                    }
+                    bf[u][b] = wtile(b, next);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        go(0, 0, std::true_type{});
         for (int s0 = 0; s0 < ks; s0 += KC) {
             if (s0) {
                 v4i an[U];
@@ -192,24 +214,8 @@ void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int
                 store_x(an);
                 __syncthreads();
             }
-            const int steps = min(KC, ks - s0);  // a multiple of 2
-            for (int s = 0; s < steps; s += D) {
-#pragma unroll
-                for (int u = 0; u < D; ++u) {
-                    v4i af[MA];
-#pragma unroll
-                    for (int a = 0; a < MA; ++a) af[a] = as[((s + u) * MA + a) * 64];
-                    const int next = min(s0 + s + u + D, ks - 1);  // past the end: loaded, never used
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-#pragma unroll
-                        for (int a = 0; a < MA; ++a)
-                            acc[a][b] = __builtin_amdgcn_mfma_i32_32x32x32_i8(bf[u][b], af[a], acc[a][b], 0, 0, 0);
-                        bf[u][b] = wtile(b, next);
-                    }
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-            }
+            const int steps = min(KC, ks - s0);  // a multiple of D
+            for (int s = s0 ? 0 : D; s < steps; s += D) go(s, s0 + s, std::false_type{});
         }
         asm volatile("" ::"v"(warm));
         __syncthreads();  // X is free
@@ -295,23 +301,27 @@ void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int
         // the wave's own columns, 16 bytes per lane: its LDS writes come before its
         // reads, and no other wave is waited for
         const bool vec = (N & 15) == 0 && ((uintptr_t)e.y & 15) == 0;
-        constexpr int CPW = 2 * NB;
+        constexpr int CPW = 2 * NB, LPR = CPW == 6 ? 8 : CPW, RPI = 64 / LPR;  // lanes of a row, rows of a pass
+        static_assert(CPW == 4 || CPW == 6 || CPW == 8, "lanes of a row");
+        const int frow = (tid & 63) / LPR, fc = wave * 32 * NB + (tid & (LPR - 1)) * 16;
+        const bool mine = (tid & (LPR - 1)) < CPW && fc < N;
+        int8_t *dst = e.y + (long long)(m0 + frow) * N + fc;
+        const int8_t *src = rt + frow * RP + fc;
         __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int i = 0; i < BM * CPW / 64; ++i) {
-            const int q = i * 64 + (tid & 63), row = q / CPW, c = wave * 32 * NB + q % CPW * 16;
-            if (m0 + row < M && c < N) {
-                v4i o = *(const v4i *)(rt + row * RP + c);
+        for (int i = 0; i < BM / RPI; ++i) {
+            if (mine && m0 + frow + i * RPI < M) {
+                v4i o = *(const v4i *)(src + i * RPI * RP);
                 if (e.relu) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) o[k] = (int)relu4((uint32_t)o[k]);
                 }
-                int8_t *dst = e.y + (long long)(m0 + row) * N;
+                int8_t *d = dst + (long long)(i * RPI) * N;
                 if (vec) {
-                    *(v4i *)(dst + c) = o;
+                    *(v4i *)d = o;
                 } else {
                     const uint32_t v[4] = {(uint32_t)o[0], (uint32_t)o[1], (uint32_t)o[2], (uint32_t)o[3]};
-                    store_run<16>(dst, c, N, v);
+                    store_run<16>(d - fc, fc, N, v);
                 }
             }
         }
