@@ -60,8 +60,9 @@ struct RowsCfg {
     static constexpr int PER_CU = NI == 1 ? 4 : NI == 2 ? 2 : 1;  // resident workgroups
     static constexpr int D = 2;  // steps of the weight in flight
     static constexpr bool KEEP = NI < 4;
+    static constexpr bool AHEAD = NI < 4 || RES == RES_NONE;  // room for a second quad's terms
     // the next tile's X is loaded during the products where it fits the registers
-    static constexpr bool EARLY = KC <= 8;
+    static constexpr bool EARLY = KC <= 8 && (RES == RES_NONE || NI <= 2);
     static constexpr int A = KC * 1024 * MA, CS = A + 16 * BN, RED = CS + WV * BM * 4, LDS = RED + BM * RP;
 };
 
@@ -226,34 +227,52 @@ void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int
         const int c0 = wave * 32 * NB + 4 * (lane >> 5);
         int ocs = C::A + 8 * c0, ort = C::RED + (lane & 31) * RP + c0;  // of its scales and residuals in LDS
         asm volatile("" : "+v"(ocs), "+v"(ort));
-        auto quad = [&](int b, int h, double (&y)[MA][4]) {
-            const double *s = (const double *)(lds + ocs) + b * 32 + 8 * h, *o = s + BN;
+        // a quad's scales, biases and residuals, read while the one before is computed
+        struct Terms {
+            double s[4], o[4];
+            uint32_t r[MA];
+        };
+        auto terms = [&](int q, Terms &t) {
+            const double *s = (const double *)(lds + ocs) + 8 * q;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) t.s[k] = s[k], t.o[k] = s[BN + k];
+            if constexpr (RES) {
+#pragma unroll
+                for (int a = 0; a < MA; ++a) t.r[a] = *(const uint32_t *)(lds + ort + a * 32 * RP + 8 * q);
+            }
+        };
+        auto quad = [&](int q, const Terms &t, double (&y)[MA][4]) {
 #pragma unroll
             for (int a = 0; a < MA; ++a) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) y[a][k] = __builtin_fma((double)acc[a][b][4 * h + k], sx[a] * s[k], o[k]);
+                for (int k = 0; k < 4; ++k)
+                    y[a][k] = __builtin_fma((double)acc[a][q / 4][4 * (q % 4) + k], sx[a] * t.s[k], t.o[k]);
                 if constexpr (RES) {
-                    const uint32_t r4 = *(const uint32_t *)(lds + ort + a * 32 * RP + b * 32 + 8 * h);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) y[a][k] = __builtin_fma((double)byte_of(r4, k), sr[a], y[a][k]);
+                    for (int k = 0; k < 4; ++k) y[a][k] = __builtin_fma((double)byte_of(t.r[a], k), sr[a], y[a][k]);
                 }
             }
         };
         double yk[C::KEEP ? NB * 4 : 1][MA][4];
         MaxMag mx[MA];
+        Terms tq[2];
+        if constexpr (C::AHEAD) terms(0, tq[0]);
+        auto value = [&](int q, double (&y)[MA][4]) {
+            if constexpr (!C::AHEAD) terms(q, tq[q & 1]);
+            else if (q + 1 < NB * 4) terms(q + 1, tq[(q + 1) & 1]);
+            quad(q, tq[q & 1], y);
+        };
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+        for (int q = 0; q < NB * 4; ++q) {
+            double(&y)[MA][4] = yk[C::KEEP ? q : 0];
+            value(q, y);
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                double(&y)[MA][4] = yk[C::KEEP ? b * 4 + h : 0];
-                quad(b, h, y);
-#pragma unroll
-                for (int a = 0; a < MA; ++a) {
-                    mx[a].add(y[a][0], y[a][1]);
-                    mx[a].add(y[a][2], y[a][3]);
-                }
-                if (h & 1) __builtin_amdgcn_sched_barrier(0);
+            for (int a = 0; a < MA; ++a) {
+                mx[a].add(y[a][0], y[a][1]);
+                mx[a].add(y[a][2], y[a][3]);
             }
+            __builtin_amdgcn_sched_barrier(0);
+        }
 #pragma unroll
         for (int a = 0; a < MA; ++a) {
             const int m = swap_reduce<32>(mx[a].word(), Max{});
@@ -281,20 +300,19 @@ void rows_add_kernel(const int8_t *x, const int8_t *wt, int M, int N, int K, int
 #pragma unroll
                 for (int b = 0; b < NB; ++b) asm volatile("" : "+v"(acc[a][b]));
         }
+        if constexpr (!C::KEEP && C::AHEAD) terms(0, tq[0]);
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+        for (int q = 0; q < NB * 4; ++q) {
+            double(&y)[MA][4] = yk[C::KEEP ? q : 0];
+            if constexpr (!C::KEEP) value(q, y);
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                double(&y)[MA][4] = yk[C::KEEP ? b * 4 + h : 0];
-                if constexpr (!C::KEEP) quad(b, h, y);
-#pragma unroll
-                for (int a = 0; a < MA; ++a) {
-                    const uint32_t o = pack4(mant_of(y[a][0], inv[a]), mant_of(y[a][1], inv[a]), mant_of(y[a][2], inv[a]),
-                                       mant_of(y[a][3], inv[a]));
-                    *(uint32_t *)(lds + ort + a * 32 * RP + b * 32 + 8 * h) = o;
-                }
-                if (h & 1) __builtin_amdgcn_sched_barrier(0);
+            for (int a = 0; a < MA; ++a) {
+                const uint32_t o = pack4(mant_of(y[a][0], inv[a]), mant_of(y[a][1], inv[a]), mant_of(y[a][2], inv[a]),
+                                         mant_of(y[a][3], inv[a]));
+                *(uint32_t *)(lds + ort + a * 32 * RP + 8 * q) = o;
             }
+            if (!C::KEEP || q & 1) __builtin_amdgcn_sched_barrier(0);
+        }
         // y is gone: room for the next tile's loads
         if constexpr (!C::EARLY) fetch_x(next, 0, xn);
         fetch_r(next, rn);
