@@ -1094,9 +1094,11 @@ ie_status ie_linear_fwd_fused(const ie_mat *X, const ie_mat *W, const ie_mat *bi
     const Force f = force_product();
     const int rg = Y->group == IE_GROUP_ROW, rows = rows_plan(M, N, r16(K), rg, f);
     const bool few = few_plan(M, N, r16(K), f);
-    // the plain product takes the tiles, any contraction, alignment and sharing
+    // the plain product takes the tiles (but rows off the runs of eight, which its
+    // second pass rounds one by one: 2687 x 3089 x 1161 81 us there, 44 here), any
+    // contraction, alignment and sharing
     if (!bias && !R &&
-        (!(rows || few) || K > MAX_CONTRACT || !aligned(X->mant, 16) || !aligned(W->mant, 16) || share(Y, X) || share(Y, W)))
+        (!(rows || few || N % 8) || K > MAX_CONTRACT || !aligned(X->mant, 16) || !aligned(W->mant, 16) || share(Y, X) || share(Y, W)))
         return linear_fwd(X, W, Y, ws, ws_bytes, stream, act == IE_ACT_RELU);
     if (bias) IE_CHECK(check_vector(bias, N));
     if (R) {

@@ -382,9 +382,12 @@ int rows_plan(long long M, long long N, long long K, int row_group, const Force 
 // (64 x 32000 x 768: 35.8 us here, 29.3 by tiles; 64 x 4096 x 4096: 16.3 and
 // 28.4; 5 x 4096 x 4096: 9.7 and 23.8) or so few columns are so long that
 // splitting them fills more of it (8 x 128 x 16384: 16.6 here, 12.3 split; 4 x
-// 512 x 8192: 10.6 and 12.4); one tile's worth is left to one launch.
+// 512 x 8192: 10.6 and 12.4), except at up to 16 rows of a single tile, which is
+// not split (8 x 64 x 8192: 11.0 here, 18.6 there; 64 x 64 x 8192: 23.1 and
+// 18.7); one tile's worth is left to one launch.
 bool few_plan(long long M, long long N, long long K, const Force &f) {
-    return !f.on && M <= FEW_ROWS && K >= 16 && M * N <= 1 << 18 && K <= 32 * N && !one_tile(M, N, K);
+    return !f.on && M <= FEW_ROWS && K >= 16 && M * N <= 1 << 18 && (K <= 32 * N || (M <= 16 && N <= 64)) &&
+           !one_tile(M, N, K);
 }
 
 DgradPlan plan_dgrad(const ConvGeom &g, int row_group, const Force &f, bool weight_in_place) {

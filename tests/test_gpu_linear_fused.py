@@ -452,3 +452,36 @@ def test_linear_fused_without_addends_in_few_and_whole_rows(shape, ws):
             torch.cuda.synchronize()
             assert torch.equal(Y.mant, Z.mant) and torch.equal(Y.exp, Z.exp)
     assert ws.status() == 0
+
+
+# contractions split over workgroups, and one tile's few rows that are not
+SPLIT = [(16, 80, 4096), (70, 130, 1100), (40, 70, 4000), (17, 40, 4096), (16, 64, 9000), (5, 1, 7747), (1, 7, 65536)]
+
+
+@pytest.mark.parametrize("shape", SPLIT, ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("yg", [T, R])
+def test_linear_fused_long_contractions(shape, yg, ws):
+    announce(f"linear fused long {shape} {yg}")
+    M, N, K = shape
+    rng = np.random.default_rng(M + N + K)
+    X, W = rand_qt(rng, (M, K), R), rand_qt(rng, (N, K), R)
+    b, D = vec(rng, N, R), rand_qt(rng, (M, N), R, -10, 2)
+    for relu, bb, dd in ((True, b, D), (False, b, None), (False, None, D)):
+        check(X, W, bb, dd, yg, relu, ws, what=f"{shape}")
+
+
+@pytest.mark.parametrize("shape", [(300, 1027, 65), (130, 90, 300), (2500, 1100, 48), (400, 1033, 1040)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_linear_fused_without_addends_off_the_runs(shape, ws):
+    announce(f"linear fused plain {shape}")
+    M, N, K = shape
+    rng = np.random.default_rng(12)
+    for xg, wg, yg in ((R, R, R), (T, T, T)):
+        X, W = rand_qt(rng, (M, K), xg), rand_qt(rng, (N, K), wg)
+        for act in (ie.ACT_NONE, ie.ACT_RELU):
+            Y, Z = ie.Mat.empty(M, N, yg), ie.Mat.empty(M, N, yg)
+            ie.ie_linear_fwd_fused(qt_to_dev(X), qt_to_dev(W), None, None, Y, act, ws)
+            ie.ie_linear_fwd_act(qt_to_dev(X), qt_to_dev(W), Z, act, ws)
+            torch.cuda.synchronize()
+            assert torch.equal(Y.mant, Z.mant) and torch.equal(Y.exp, Z.exp)
+    assert ws.status() == 0
