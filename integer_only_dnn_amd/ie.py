@@ -122,9 +122,12 @@ def _check(code: int, where: str) -> None:
 
 def _stream(dev: torch.device) -> int:
     """The current stream's handle (taken raw: building the stream object costs
-    a third of a short call)."""
-    index = dev.index
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
+    a third of a short call).  Kernels are launched on the current GPU, so work
+    for another one, or on host memory, is refused."""
+    index = torch.cuda.current_device() if dev.type == "cuda" else -1
+    if index < 0 or dev.index not in (None, index):
+        raise ValueError(f"{dev} is not the current GPU")
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 class Mat:
@@ -155,6 +158,8 @@ class Mat:
         hit = self._desc.get(key)
         if hit is not None and hit[0] is self.mant and hit[1] is self.exp:
             return hit[2]
+        if not (self.mant.is_cuda and self.exp.is_cuda):
+            raise ValueError("a matrix in host memory")
         r, c = rows, cols
         if r is None:
             assert self.mant.dim() == 2

@@ -1,0 +1,29 @@
+"""What the Python binding refuses before it calls the library: host tensors,
+and work for another GPU than the one that launches go to."""
+
+import pytest
+import torch
+
+from integer_only_dnn_amd import ie
+
+
+def test_streams_are_those_of_the_current_gpu(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 1000 + index, raising=False)
+    assert ie._stream(torch.device("cuda")) == 1000 and ie._stream(torch.device("cuda:0")) == 1000
+    with pytest.raises(ValueError):
+        ie._stream(torch.device("cpu"))
+    with pytest.raises(ValueError):
+        ie._stream(torch.device("cuda:1"))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    assert ie._stream(torch.device("cuda")) == 1001 and ie._stream(torch.device("cuda:1")) == 1001
+
+
+def test_host_matrices_are_refused():
+    m = ie.Mat.empty(4, 8, ie.ROW, device="cpu")
+    with pytest.raises(ValueError):
+        m.c()
+    with pytest.raises(ValueError):
+        m.c(2, 16)
+    with pytest.raises(ValueError):
+        ie.ie_relu_fwd(m, m)
