@@ -176,13 +176,20 @@ class Workspace:
     def __init__(self, device="cuda"):
         self.device = torch.device(device)
         self.buf = None
-        self._at = (0, 0)  # buf's address and size
+
+    @property
+    def buf(self):
+        return self._buf
+
+    @buf.setter
+    def buf(self, t):
+        self._buf = t
+        self._at = (0, 0) if t is None else (t.data_ptr(), t.numel())  # looked up once per buffer
 
     def get(self, nbytes: int):
-        if self.buf is None or self._at[1] < nbytes:
-            flags = self.status(clear=False) if self.buf is not None else 0
+        if self._buf is None or self._at[1] < nbytes:
+            flags = self.status(clear=False) if self._buf is not None else 0
             self.buf = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=self.device)
-            self._at = (self.buf.data_ptr(), self.buf.numel())
             _check(lib().ie_workspace_init(*self._at, _stream(self.device)),
                    "ie_workspace_init")
             if flags:

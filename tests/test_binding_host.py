@@ -27,3 +27,16 @@ def test_host_matrices_are_refused():
         m.c(2, 16)
     with pytest.raises(ValueError):
         ie.ie_relu_fwd(m, m)
+
+
+def test_workspace_follows_its_buffer():
+    """A buffer that the caller puts in, or takes away, is the one that calls get."""
+    ws = ie.Workspace("cpu")
+    for n in (512, 1024):
+        ws.buf = torch.zeros(n, dtype=torch.uint8)
+        assert ws.get(300) == (ws.buf.data_ptr(), n)
+    ws.buf = None
+    assert ws.status() == 0
+    with pytest.raises(ValueError):  # asked for anew, and refused: host memory
+        ws.get(700)
+    assert ws.buf.numel() == 700
