@@ -28,7 +28,10 @@
  *   - matrices are row-major and contiguous; activations of convolutions are
  *     NHWC, viewed as a matrix [N*H*W x C]; weights are [K x R*S*C] (KRSC);
  *   - outputs are fully overwritten, mantissas and exponents; outputs must not
- *     alias inputs (ie_sgd_update works in place on W and V);
+ *     alias inputs (ie_sgd_update works in place on W and V).  Layer norm,
+ *     the product with bias and residual, the bias gradient and dropout
+ *     refuse an output with a byte of an input or of another output
+ *     (IE_ERR_UNSUPPORTED);
  *   - `ws` is a workspace of at least the size the matching *_workspace_bytes
  *     call returns; its first 256 bytes hold sticky flags and must be zeroed
  *     once (ie_workspace_init) before first use;

@@ -889,9 +889,15 @@ static ie_status check_vector(const ie_mat *v, long long n) {
     return is_vector(v, n) ? IE_OK : IE_ERR_SHAPE;
 }
 
-// Whether two matrices share their mantissas or their exponents.
+// Whether a byte of a's mantissas or exponents is one of b's.
 static bool share(const ie_mat *a, const ie_mat *b) {
-    return a && b && ((a->mant && a->mant == b->mant) || (a->exp && a->exp == b->exp));
+    if (!a || !b) return false;
+    auto meet = [](const int8_t *p, long long n, const int8_t *q, long long m) {
+        return n && m && (uintptr_t)p < (uintptr_t)q + m && (uintptr_t)q < (uintptr_t)p + n;
+    };
+    const long long am = a->rows * a->cols, bm = b->rows * b->cols, ae = n_exps(a), be = n_exps(b);
+    return meet(a->mant, am, b->mant, bm) || meet(a->mant, am, b->exp, be) || meet(a->exp, ae, b->mant, bm) ||
+           meet(a->exp, ae, b->exp, be);
 }
 
 size_t ie_layer_norm_fwd_workspace(int64_t rows, int64_t cols) {
@@ -1094,11 +1100,10 @@ ie_status ie_linear_fwd_fused(const ie_mat *X, const ie_mat *W, const ie_mat *bi
     const Force f = force_product();
     const int rg = Y->group == IE_GROUP_ROW, rows = rows_plan(M, N, r16(K), rg, f);
     const bool few = few_plan(M, N, r16(K), f);
-    // the plain product takes the tiles (but rows off the runs of eight, which its
-    // second pass rounds one by one: 2687 x 3089 x 1161 81 us there, 44 here), any
-    // contraction, alignment and sharing
-    if (!bias && !R &&
-        (!(rows || few || N % 8) || K > MAX_CONTRACT || !aligned(X->mant, 16) || !aligned(W->mant, 16) || share(Y, X) || share(Y, W)))
+    if (share(Y, X) || share(Y, W)) return IE_ERR_UNSUPPORTED;
+    // the plain product takes the tiles, but rows off the runs of eight, which its
+    // second pass rounds one by one: 2687 x 3089 x 1161 81 us there, 44 here
+    if (!bias && !R && !(rows || few || N % 8))
         return linear_fwd(X, W, Y, ws, ws_bytes, stream, act == IE_ACT_RELU);
     if (bias) IE_CHECK(check_vector(bias, N));
     if (R) {
@@ -1107,7 +1112,7 @@ ie_status ie_linear_fwd_fused(const ie_mat *X, const ie_mat *W, const ie_mat *bi
     }
     if (K > MAX_CONTRACT) return IE_ERR_UNSUPPORTED;
     if (!aligned(X->mant, 16) || !aligned(W->mant, 16)) return IE_ERR_UNSUPPORTED;
-    if (share(Y, X) || share(Y, W) || share(Y, bias) || share(Y, R)) return IE_ERR_UNSUPPORTED;
+    if (share(Y, bias) || share(Y, R)) return IE_ERR_UNSUPPORTED;
     if (!ws) return IE_ERR_WORKSPACE;
     if (ws_bytes < linear_fused_ws(M, N, K, f)) return IE_ERR_WORKSPACE;
     hipStream_t st = (hipStream_t)stream;
