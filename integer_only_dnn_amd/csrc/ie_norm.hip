@@ -605,47 +605,54 @@ __global__ __launch_bounds__(256) void col_sum_kernel(const int8_t *dy, const in
             (int)(sh[0][threadIdx.x] + sh[1][threadIdx.x] + sh[2][threadIdx.x] + sh[3][threadIdx.x]);
 }
 
-// Sums of `parts` partial rows (64-bit or 32-bit), 16 columns per block and 64
-// partial rows at a time, at exponent base + *top: rounded into one group per
+// Sums of `parts` partial rows (64-bit or 32-bit), 16 columns at a time per block
+// and 64 partial rows at a time, at exponent base + *top: rounded into one group per
 // channel here, or kept for col_round_kernel with the block's need.
 __global__ __launch_bounds__(1024) void col_finish_kernel(ColOut f, ColOut b, int parts, int cols, const int *top,
                                                           uint32_t *flags) {
     __shared__ long long sh[16][16];
     const ColOut &o = blockIdx.y == 0 ? f : b;
     if (!o.m) return;
-    const int lane = threadIdx.x & 15, grp = threadIdx.x >> 4;
-    const long long c = blockIdx.x * 16ll + lane, pitch = col_pitch(cols);
-    long long s = 0;
-    if (c < cols) {
-        if (o.p64) {
+    const int lane = threadIdx.x & 15, grp = threadIdx.x >> 4, eps = top[0] + o.base;
+    const long long pitch = col_pitch(cols);
+    int block_need = NEED_NONE;
+    for (long long c0 = blockIdx.x * 16ll; c0 < cols; c0 += gridDim.x * 16ll) {
+        const long long c = c0 + lane;
+        long long s = 0;
+        if (c < cols) {
+            if (o.p64) {
 #pragma unroll 4
-            for (int i = grp; i < parts; i += 64) s += o.p64[(long long)i * pitch + c];
-        } else {
+                for (int i = grp; i < parts; i += 64) s += o.p64[(long long)i * pitch + c];
+            } else {
 #pragma unroll 4
-            for (int i = grp; i < parts; i += 64) s += o.p32[(long long)i * pitch + c];
-        }
-    }
-    s += __shfl_xor(s, 16);
-    s += __shfl_xor(s, 32);
-    if ((threadIdx.x & 63) < 16) sh[threadIdx.x >> 6][lane] = s;
-    __syncthreads();
-    const int eps = top[0] + o.base;
-    if (threadIdx.x < 64) {
-        s = 0;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s += sh[i][lane];
-        int need = c < cols ? need64(s, eps, o.q) : NEED_NONE;
-        if (o.per) {
-            if (threadIdx.x < 16 && c < cols) {
-                const int e = clamp_exp_flag(max(E_MIN, need), flags);
-                o.m[c] = (int8_t)rne_shift64(s, e - eps);
-                o.e[c] = (int8_t)e;
+                for (int i = grp; i < parts; i += 64) s += o.p32[(long long)i * pitch + c];
             }
-        } else {
-            need = lane_reduce<16>(need, Max{});
-            if (threadIdx.x < 16 && c < cols) o.sums[c] = s;
-            if (threadIdx.x == 0) o.need[blockIdx.x] = need;
         }
+        s += __shfl_xor(s, 16);
+        s += __shfl_xor(s, 32);
+        if ((threadIdx.x & 63) < 16) sh[threadIdx.x >> 6][lane] = s;
+        __syncthreads();
+        if (threadIdx.x < 64) {
+            s = 0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s += sh[i][lane];
+            const int need = c < cols ? need64(s, eps, o.q) : NEED_NONE;
+            if (threadIdx.x < 16 && c < cols) {
+                if (o.per) {
+                    const int e = clamp_exp_flag(max(E_MIN, need), flags);
+                    o.m[c] = (int8_t)rne_shift64(s, e - eps);
+                    o.e[c] = (int8_t)e;
+                } else {
+                    o.sums[c] = s;
+                }
+            }
+            block_need = max(block_need, need);
+        }
+        __syncthreads();  // the sums are read
+    }
+    if (!o.per && threadIdx.x < 64) {
+        block_need = lane_reduce<16>(block_need, Max{});
+        if (threadIdx.x == 0) o.need[blockIdx.x] = block_need;
     }
 }
 
@@ -705,7 +712,7 @@ hipError_t launch_col_sum(const int8_t *dy, const int8_t *e, int e_row, long lon
 
 hipError_t launch_col_finish(const ColOut &f, const ColOut &b, int parts, int cols, const int *top, uint32_t *flags,
                              hipStream_t st) {
-    const int nb = (cols + 15) / 16;
+    const int nb = col_blocks(cols);
     const bool whole = (f.m && !f.per) || (b.m && !b.per);
     prof_begin(st, PROF_COL_FINISH);
     if (whole && parts <= COL_FEW && cols <= 4096) {

@@ -388,6 +388,10 @@ struct ColPlan {
     int parts, chunk;
 };
 ColPlan col_plan(long long rows, long long cols);
+// Blocks that close column sums: 16 columns each, taking turns over the widest
+// vectors (of 1024 threads, and a launch has fewer than 2^32 of these).
+constexpr long long COL_BLOCKS = 1 << 16;
+constexpr int col_blocks(long long cols) { return (int)(cols < 16 * COL_BLOCKS ? (cols + 15) / 16 : COL_BLOCKS); }
 
 // The largest exponent of more rows than this is found by a kernel of its own
 // (in parts), of fewer by every block that needs it.
