@@ -238,11 +238,8 @@ __global__ __launch_bounds__(1024) void dropout_long_kernel(DropArgs p) {
     }
 }
 
-#define IE_DROP_SHAPES(X) \
-    X(8, 8) X(8, 16) X(8, 24) X(16, 16) X(16, 24) X(32, 16) X(32, 24) X(64, 16) X(64, 24) X(256, 8) X(256, 16) \
-    X(256, 24) X(1024, 8) X(1024, 16)
-
 hipError_t launch_dropout(const DropArgs &a, const NormPlan &pl, hipStream_t st) {
+    if (!dropout_built(pl)) return hipErrorInvalidValue;
     prof_begin(st, PROF_DROPOUT);
     if (pl.e == 0) {
         if (a.r) hipLaunchKernelGGL(dropout_long_kernel<true>, dim3(pl.grid), dim3(1024), 0, st, a);

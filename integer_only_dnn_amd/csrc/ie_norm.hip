@@ -492,16 +492,8 @@ __global__ __launch_bounds__(1024) void tops_kernel(const int8_t *e, long long n
     if (threadIdx.x == 0) tops[blockIdx.x] = m;
 }
 
-#define IE_NORM_FWD(X)                                                                                          \
-    X(16, 4) X(16, 8) X(16, 12) X(16, 16) X(16, 24) X(16, 32) X(16, 48) X(32, 24) X(64, 4) X(64, 8) X(64, 16)   \
-    X(64, 24) X(64, 32) X(64, 48) X(256, 12) X(256, 16) X(256, 24) X(1024, 8) X(1024, 12) X(1024, 16)
-#define IE_NORM_BWD(X)                                                                                           \
-    X(16, 4) X(16, 8) X(16, 12) X(16, 16) X(32, 12) X(64, 4) X(64, 8) X(64, 12) X(64, 16) X(256, 8) X(256, 12) X(256, 16)    \
-    X(512, 12) X(512, 16) X(1024, 12) X(1024, 16)
-
-#define IE_NORM_ONE(X) X(16, 4) X(16, 8) X(16, 12) X(16, 16) X(64, 4) X(64, 8) X(64, 16)
-
 hipError_t launch_norm_fwd(const NormFwd &a, const NormPlan &pl, hipStream_t st) {
+    if (!(a.mode == NORM_ONE ? norm_one_built(pl) : norm_fwd_built(pl))) return hipErrorInvalidValue;
     prof_begin(st, PROF_NORM_FWD);
 #define IE_CASE(T_, E_)           \
     if (pl.t == T_ && pl.e == E_) \
@@ -520,6 +512,7 @@ hipError_t launch_norm_fwd(const NormFwd &a, const NormPlan &pl, hipStream_t st)
 }
 
 hipError_t launch_norm_bwd(const NormBwd &a, const NormPlan &pl, hipStream_t st) {
+    if (!norm_bwd_built(pl)) return hipErrorInvalidValue;
     prof_begin(st, PROF_NORM_BWD);
 #define IE_CASE(T_, E_)       \
     if (pl.t == T_ && pl.e == E_) \

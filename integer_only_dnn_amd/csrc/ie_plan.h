@@ -373,6 +373,24 @@ constexpr int grad_block(int t) { return t > 64 ? t : 512; }
 struct NormPlan {
     int t, e, grid;
 };
+// The splits (t, e) that kernels are built for: forward, a whole-tensor result
+// in one block, backward, dropout (and its e = 0, rows too long to be held).
+#define IE_NORM_FWD(X)                                                                                        \
+    X(16, 4) X(16, 8) X(16, 12) X(16, 16) X(16, 24) X(16, 32) X(16, 48) X(32, 24) X(64, 4) X(64, 8) X(64, 16) \
+    X(64, 24) X(64, 32) X(64, 48) X(256, 12) X(256, 16) X(256, 24) X(1024, 8) X(1024, 12) X(1024, 16)
+#define IE_NORM_ONE(X) X(16, 4) X(16, 8) X(16, 12) X(16, 16) X(64, 4) X(64, 8) X(64, 16)
+#define IE_NORM_BWD(X)                                                                                           \
+    X(16, 4) X(16, 8) X(16, 12) X(16, 16) X(32, 12) X(64, 4) X(64, 8) X(64, 12) X(64, 16) X(256, 8) X(256, 12)   \
+    X(256, 16) X(512, 12) X(512, 16) X(1024, 12) X(1024, 16)
+#define IE_DROP_SHAPES(X) \
+    X(8, 8) X(8, 16) X(8, 24) X(16, 16) X(16, 24) X(32, 16) X(32, 24) X(64, 16) X(64, 24) X(256, 8) X(256, 16) \
+    X(256, 24) X(1024, 8) X(1024, 16)
+#define IE_IS(T_, E_) || (p.t == T_ && p.e == E_)
+inline bool norm_fwd_built(const NormPlan &p) { return false IE_NORM_FWD(IE_IS); }
+inline bool norm_one_built(const NormPlan &p) { return false IE_NORM_ONE(IE_IS); }
+inline bool norm_bwd_built(const NormPlan &p) { return false IE_NORM_BWD(IE_IS); }
+inline bool dropout_built(const NormPlan &p) { return p.e == 0 IE_DROP_SHAPES(IE_IS); }
+#undef IE_IS
 constexpr long long NORM_FEW = 4096;
 NormPlan norm_fwd_plan(long long rows, long long cols);
 // One block of 1024 threads for a whole-tensor result (grid 0: too large).

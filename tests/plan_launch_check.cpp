@@ -1,8 +1,12 @@
 // Host-only check of the launches of the block operators (tests/test_plan_launch.py):
-// a launch has fewer than 2^32 threads along an axis, whatever the shape.
-// Exit status 0 when every check passes.
+// a launch has fewer than 2^32 threads along an axis, whatever the shape; every
+// split of rows over threads that is planned is built, and every one that is
+// built is planned for some shape.  Exit status 0 when every check passes.
 #include <stdio.h>
 #include <stdlib.h>
+
+#include <set>
+#include <utility>
 
 #include "../integer_only_dnn_amd/csrc/ie_plan.h"
 
@@ -30,7 +34,49 @@ static void check_columns(long long cols) {
     REQUIRE((cols + 255) / 256 * 256 < 1ll << 32, "%lld columns", cols);
 }
 
+// The splits planned for rows of each length, over few rows and many.
+using Splits = std::set<std::pair<int, int>>;
+
+static void check_splits() {
+    Splits fwd, one, bwd, drop;
+    for (long long rows : {1ll, 15ll, 16ll, 17ll, 63ll, 64ll, 65ll, 1000ll, NORM_FEW - 1, NORM_FEW, NORM_FEW + 1, 1000000ll})
+        for (long long cols = 1; cols <= 30000; ++cols) {
+            const NormPlan d = dropout_plan(rows, cols);
+            REQUIRE(dropout_built(d), "dropout %lld x %lld: (%d, %d)", rows, cols, d.t, d.e);
+            drop.insert({d.t, d.e});
+            if (cols > NORM_COLS_MAX) continue;
+            const NormPlan f = norm_fwd_plan(rows, cols), o = norm_one_plan(rows, cols), b = norm_bwd_plan(rows, cols);
+            REQUIRE(norm_fwd_built(f), "forward %lld x %lld: (%d, %d)", rows, cols, f.t, f.e);
+            REQUIRE(norm_bwd_built(b), "backward %lld x %lld: (%d, %d)", rows, cols, b.t, b.e);
+            REQUIRE(!o.grid || norm_one_built(o), "one block %lld x %lld: (%d, %d)", rows, cols, o.t, o.e);
+            fwd.insert({f.t, f.e});
+            bwd.insert({b.t, b.e});
+            if (o.grid) one.insert({o.t, o.e});
+        }
+#define IE_PLANNED(T_, E_) REQUIRE(planned.count({T_, E_}), "(%d, %d) is built and never planned", T_, E_);
+    {
+        const Splits &planned = fwd;
+        IE_NORM_FWD(IE_PLANNED)
+    }
+    {
+        const Splits &planned = one;
+        IE_NORM_ONE(IE_PLANNED)
+    }
+    {
+        const Splits &planned = bwd;
+        IE_NORM_BWD(IE_PLANNED)
+    }
+    {
+        const Splits &planned = drop;
+        IE_DROP_SHAPES(IE_PLANNED)
+    }
+#undef IE_PLANNED
+    const NormPlan none{7, 4, 1};
+    REQUIRE(!norm_fwd_built(none) && !norm_one_built(none) && !norm_bwd_built(none) && !dropout_built(none), "(7, 4)");
+}
+
 int main() {
+    check_splits();
     for (long long e = 0; e <= 30; ++e)
         for (long long d = -17; d <= 17; ++d) {
             const long long c = (1ll << e) + d;

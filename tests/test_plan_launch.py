@@ -1,11 +1,14 @@
 """Host-only checks of the block operators' launches: integer_only_dnn_amd/csrc/ie_plan.cpp
 compiled with g++ together with tests/plan_launch_check.cpp."""
 
+import ctypes
 import os
 import shutil
 import subprocess
 
 import pytest
+
+from integer_only_dnn_amd import ie
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 SRC = [os.path.join(ROOT, "tests", "plan_launch_check.cpp"),
@@ -23,3 +26,14 @@ def test_block_launches(tmp_path):
     res = subprocess.run([exe], capture_output=True, text=True, timeout=300, env=env)
     assert res.returncode == 0, (res.stdout + res.stderr)[-4000:]
     assert "plan_launch_check:" in res.stdout
+
+
+@pytest.mark.parametrize("name,args", [("launch_norm_fwd", "7NormFwd"), ("launch_norm_bwd", "7NormBwd"),
+                                       ("launch_dropout", "8DropArgs")])
+def test_a_split_without_a_kernel_is_an_error(name, args):
+    """Nothing launched is not success: hipErrorInvalidValue (1), before any call of the runtime."""
+    launch = getattr(ie.lib(), f"_ZN2ie{len(name)}{name}ERKNS_{args}ERKNS_8NormPlanEP12ihipStream_t")
+    plan = (ctypes.c_int * 3)(7, 4, 1)
+    for mode in range(4):
+        block = (ctypes.c_int * 256)(*[mode] * 256)  # the mode wherever it lies
+        assert launch(block, plan, None) == 1
