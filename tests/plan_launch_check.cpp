@@ -1,9 +1,13 @@
 // Host-only check of the launches of the block operators (tests/test_plan_launch.py):
 // a launch has fewer than 2^32 threads along an axis, whatever the shape; every
 // split of rows over threads that is planned is built, and every one that is
-// built is planned for some shape.  Exit status 0 when every check passes.
+// built is planned for some shape.  With arguments KIND ROWS COLS ROWS COLS ...
+// (KIND forward, backward or dropout) it checks that those shapes take every
+// split whose blocks can take rows in turn to a second trip at least.  Exit
+// status 0 when every check passes.
 #include <stdio.h>
 #include <stdlib.h>
+#include <string.h>
 
 #include <set>
 #include <utility>
@@ -75,7 +79,36 @@ static void check_splits() {
     REQUIRE(!norm_fwd_built(none) && !norm_one_built(none) && !norm_bwd_built(none) && !dropout_built(none), "(7, 4)");
 }
 
-int main() {
+// A block's threads (backward, dropout and forward differ in them) and its trips.
+static long long trips(const char *kind, long long rows, long long cols, NormPlan &p) {
+    long long block = 0;
+    if (!strcmp(kind, "forward")) p = norm_fwd_plan(rows, cols), block = p.t > 256 ? p.t : 256;
+    if (!strcmp(kind, "backward")) p = norm_bwd_plan(rows, cols), block = grad_block(p.t);
+    if (!strcmp(kind, "dropout")) p = dropout_plan(rows, cols), block = p.t > 256 ? p.t : 256;
+    REQUIRE(block, "%s", kind);
+    const long long each = block / p.t * p.grid;
+    return (rows + each - 1) / each;
+}
+
+static void check_trips(const char *kind, int n, char **size) {
+    Splits can, done;
+    NormPlan p;
+    const long long longest = strcmp(kind, "dropout") ? NORM_COLS_MAX : 30000;
+    for (long long rows : {NORM_FEW - 1, 1000000ll})
+        for (long long cols = 1; cols <= longest; ++cols)
+            if (trips(kind, rows, cols, p) > 1) can.insert({p.t, p.e});
+    for (int i = 0; i + 1 < n; i += 2)
+        if (trips(kind, atoll(size[i]), atoll(size[i + 1]), p) > 1) done.insert({p.t, p.e});
+    REQUIRE(!can.empty(), "%s", kind);
+    for (const auto &c : can) REQUIRE(done.count(c), "%s: no shape takes (%d, %d) to a second trip", kind, c.first, c.second);
+}
+
+int main(int argc, char **argv) {
+    if (argc > 1) {
+        check_trips(argv[1], argc - 2, argv + 2);
+        printf("plan_launch_check: %lld checks\n", g_checks);
+        return 0;
+    }
     check_splits();
     for (long long e = 0; e <= 30; ++e)
         for (long long d = -17; d <= 17; ++d) {

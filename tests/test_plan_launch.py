@@ -9,23 +9,39 @@ import subprocess
 import pytest
 
 from integer_only_dnn_amd import ie
+from tests import test_gpu_trips
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 SRC = [os.path.join(ROOT, "tests", "plan_launch_check.cpp"),
        os.path.join(ROOT, "integer_only_dnn_amd", "csrc", "ie_plan.cpp")]
 
 
-def test_block_launches(tmp_path):
+@pytest.fixture(scope="module")
+def check(tmp_path_factory):
+    """Runs the check with the arguments given; it has to pass."""
     cxx = shutil.which(os.environ.get("CXX", "g++"))
     if cxx is None:
         pytest.skip("no host C++ compiler")
-    exe = str(tmp_path / "plan_launch_check")
+    exe = str(tmp_path_factory.mktemp("plan") / "plan_launch_check")
     res = subprocess.run([cxx, "-std=c++17", "-O1", *SRC, "-o", exe], capture_output=True, text=True, timeout=300)
     assert res.returncode == 0, res.stderr[-4000:]
     env = {k: v for k, v in os.environ.items() if k not in ("IE_TILE", "IE_WTILE")}
-    res = subprocess.run([exe], capture_output=True, text=True, timeout=300, env=env)
-    assert res.returncode == 0, (res.stdout + res.stderr)[-4000:]
-    assert "plan_launch_check:" in res.stdout
+
+    def run(*args):
+        res = subprocess.run([exe, *map(str, args)], capture_output=True, text=True, timeout=300, env=env)
+        assert res.returncode == 0, (res.stdout + res.stderr)[-4000:]
+        assert "plan_launch_check:" in res.stdout
+    return run
+
+
+def test_block_launches(check):
+    check()
+
+
+@pytest.mark.parametrize("kind,shapes", [("forward", test_gpu_trips.NORM), ("backward", test_gpu_trips.NORM),
+                                         ("dropout", test_gpu_trips.DROPOUT)], ids=["forward", "backward", "dropout"])
+def test_gpu_shapes_take_every_split_to_a_second_trip(check, kind, shapes):
+    check(kind, *[n for s in shapes for n in s])
 
 
 @pytest.mark.parametrize("name,args", [("launch_norm_fwd", "7NormFwd"), ("launch_norm_bwd", "7NormBwd"),
