@@ -345,7 +345,10 @@ ie_status ie_layer_norm_fwd(const ie_mat *X, const ie_mat *gamma, const ie_mat *
  *   dX = R((g - mean(g) - h mean(g h)) / sqrt(var + eps)),  g = dY gamma,
  * h the normalised row.  As in every contraction, operands whose exponents
  * vary along the summed axis are first re-expressed at the largest one: gamma
- * over its channels, dY over the rows in dgamma and dbeta (not in dX).
+ * over its channels, dY over the rows in dgamma and dbeta (not in dX).  So
+ * where the forward pass multiplies by gamma as it is, dX takes it to half a
+ * unit of its largest exponent, and as zero in channels whose exponents lie
+ * eight or more below that.
  * In the sums over a row and over the rows h is f = R(h 2^20), an integer, so
  * that G1 = sum g, G2 = sum g f and the column sums are exact; then, to 53
  * bits, z = (N g - G1) - f (G2 2^-40) and dX = z r, each operation rounded
