@@ -411,20 +411,28 @@ def _opt(m: Mat | None):
     return byref(m.c()) if m is not None else None
 
 
+def _eps(eps) -> ie_scalar:
+    """A (C, e) scalar whose parts fit their bytes (ctypes would wrap them)."""
+    mant, exp = eps
+    if not (-128 <= mant <= 127 and -128 <= exp <= 127):
+        raise ValueError(f"eps {eps}: mantissa and exponent are 8 bits each")
+    return ie_scalar(mant, exp)
+
+
 def ie_layer_norm_fwd(X: Mat, gamma: Mat | None, beta: Mat | None, eps, Y: Mat, ws: Workspace) -> None:
     """Y = layer norm of X's rows, times gamma plus beta; eps is a (C, e) scalar."""
-    x, y = X.c(), Y.c()
+    e, x, y = _eps(eps), X.c(), Y.c()
     p, b = ws.get(_ws_rows("ie_layer_norm_fwd_workspace", x.rows, x.cols))
-    _check(lib().ie_layer_norm_fwd(byref(x), _opt(gamma), _opt(beta), ie_scalar(*eps), byref(y), p, b,
+    _check(lib().ie_layer_norm_fwd(byref(x), _opt(gamma), _opt(beta), e, byref(y), p, b,
                                    _stream(ws.device)), "ie_layer_norm_fwd")
 
 
 def ie_layer_norm_bwd(dY: Mat, X: Mat, gamma: Mat | None, eps, dX: Mat | None, dgamma: Mat | None,
                       dbeta: Mat | None, ws: Workspace) -> None:
     """The gradients of ie_layer_norm_fwd's input, gamma and beta (any of them None to skip it)."""
-    dy, x = dY.c(), X.c()
+    e, dy, x = _eps(eps), dY.c(), X.c()
     p, b = ws.get(_ws_rows("ie_layer_norm_bwd_workspace", x.rows, x.cols))
-    _check(lib().ie_layer_norm_bwd(byref(dy), byref(x), _opt(gamma), ie_scalar(*eps), _opt(dX), _opt(dgamma),
+    _check(lib().ie_layer_norm_bwd(byref(dy), byref(x), _opt(gamma), e, _opt(dX), _opt(dgamma),
                                    _opt(dbeta), p, b, _stream(ws.device)), "ie_layer_norm_bwd")
 
 

@@ -40,3 +40,12 @@ def test_workspace_follows_its_buffer():
     with pytest.raises(ValueError):  # asked for anew, and refused: host memory
         ws.get(700)
     assert ws.buf.numel() == 700
+
+
+@pytest.mark.parametrize("eps", [(128, 0), (-129, 0), (85, -140), (85, 128), (85,), (1, 2, 3)])
+def test_eps_that_is_no_scalar_is_refused(eps):
+    """A byte would wrap: 85 * 2^-140 would be read as 85 * 2^116."""
+    with pytest.raises(ValueError):
+        ie.ie_layer_norm_fwd(None, None, None, eps, None, None)
+    with pytest.raises(ValueError):
+        ie.ie_layer_norm_bwd(None, None, None, eps, None, None, None, None)
