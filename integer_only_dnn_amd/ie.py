@@ -164,6 +164,8 @@ class Mat:
         if r is None:
             assert self.mant.dim() == 2
             r, c = self.mant.shape
+        if self.mant.numel() < r * c or self.exp.numel() < (r if self.group == ROW else 1):
+            raise ValueError(f"{r} x {c} needs more than {self.mant.numel()} mantissas or {self.exp.numel()} exponents")
         d = ie_mat(self.mant.data_ptr(), self.exp.data_ptr(), r, c, self.group, self.bits)
         self._desc[key] = (self.mant, self.exp, d)
         return d

@@ -49,3 +49,33 @@ def test_eps_that_is_no_scalar_is_refused(eps):
         ie.ie_layer_norm_fwd(None, None, None, eps, None, None)
     with pytest.raises(ValueError):
         ie.ie_layer_norm_bwd(None, None, None, eps, None, None, None, None)
+
+
+class _OnGpu(torch.Tensor):
+    """A host tensor that says it is on the GPU: descriptors only take its address."""
+    is_cuda = property(lambda self: True)
+
+
+def _gpu(*shape):
+    return torch.zeros(shape, dtype=torch.int8).as_subclass(_OnGpu)
+
+
+def test_descriptors_hold_their_matrix():
+    """Fewer exponents than groups, or fewer mantissas than the view, would be read past their end."""
+    for rows, cols, n, group, ok in ((4, 8, 4, ie.ROW, True), (4, 8, 1, ie.ROW, False), (4, 8, 3, ie.ROW, False),
+                                     (4, 8, 1, ie.TENSOR, True), (4, 8, 0, ie.TENSOR, False), (8, 1, 1, ie.ROW, False),
+                                     (1, 8, 1, ie.ROW, True), (0, 8, 0, ie.ROW, True), (0, 8, 0, ie.TENSOR, False)):
+        m = ie.Mat(_gpu(rows, cols), _gpu(n), group)
+        if ok:
+            d = m.c()
+            assert (d.rows, d.cols, d.group) == (rows, cols, group)
+        else:
+            with pytest.raises(ValueError):
+                m.c()
+    image = ie.Mat(_gpu(2, 3, 3, 16), _gpu(1), ie.TENSOR)
+    assert image.c(18, 16).rows == 18
+    for view in ((18, 17), (19, 16)):
+        with pytest.raises(ValueError):
+            image.c(*view)
+    with pytest.raises(ValueError):
+        ie.Mat(_gpu(2, 3, 3, 16), _gpu(2), ie.ROW).c(18, 16)
