@@ -600,7 +600,10 @@ __global__ __launch_bounds__(256) void col_sum_kernel(const int8_t *dy, const in
 
 // Sums of `parts` partial rows (64-bit or 32-bit), 16 columns at a time per block
 // and 64 partial rows at a time, at exponent base + *top: rounded into one group per
-// channel here, or kept for col_round_kernel with the block's need.
+// channel here, or kept for col_round_kernel with the block's need.  TURNS: the
+// blocks take turns, over vectors of 2^20 channels and more (narrower ones do
+// without the barrier between turns: 100 x 524288 120 us, 135 with it).
+template <bool TURNS>
 __global__ __launch_bounds__(1024) void col_finish_kernel(ColOut f, ColOut b, int parts, int cols, const int *top,
                                                           uint32_t *flags) {
     __shared__ long long sh[16][16];
@@ -609,8 +612,7 @@ __global__ __launch_bounds__(1024) void col_finish_kernel(ColOut f, ColOut b, in
     const int lane = threadIdx.x & 15, grp = threadIdx.x >> 4, eps = top[0] + o.base;
     const long long pitch = col_pitch(cols);
     int block_need = NEED_NONE;
-    for (long long c0 = blockIdx.x * 16ll; c0 < cols; c0 += gridDim.x * 16ll) {
-        const long long c = c0 + lane;
+    for (long long c = blockIdx.x * 16ll + lane; c - lane < cols; c += gridDim.x * 16ll) {
         long long s = 0;
         if (c < cols) {
             if (o.p64) {
@@ -641,6 +643,7 @@ __global__ __launch_bounds__(1024) void col_finish_kernel(ColOut f, ColOut b, in
             }
             block_need = max(block_need, need);
         }
+        if constexpr (!TURNS) break;
         __syncthreads();  // the sums are read
     }
     if (!o.per && threadIdx.x < 64) {
@@ -713,7 +716,9 @@ hipError_t launch_col_finish(const ColOut &f, const ColOut &b, int parts, int co
         prof_end(st, PROF_COL_FINISH);
         return hipGetLastError();
     }
-    hipLaunchKernelGGL(col_finish_kernel, dim3(nb, b.m ? 2 : 1), dim3(1024), 0, st, f, b, parts, cols, top, flags);
+    const dim3 grid(nb, b.m ? 2 : 1), block(1024);
+    if (nb < COL_BLOCKS) hipLaunchKernelGGL(col_finish_kernel<false>, grid, block, 0, st, f, b, parts, cols, top, flags);
+    else hipLaunchKernelGGL(col_finish_kernel<true>, grid, block, 0, st, f, b, parts, cols, top, flags);
     if (whole) {
         const int g = (cols + 255) / 256;
         hipLaunchKernelGGL(col_round_kernel, dim3(g < 1024 ? g : 1024, b.m ? 2 : 1), dim3(256), 0, st, f, b, nb, cols,
