@@ -120,14 +120,22 @@ def _check(code: int, where: str) -> None:
         raise IeError(code, where)
 
 
+_gpus = {}  # device -> its index (None: the current one), checked once
+
+
 def _stream(dev: torch.device) -> int:
-    """The current stream's handle (taken raw: building the stream object costs
-    a third of a short call).  Kernels are launched on the current GPU, so work
-    for another one, or on host memory, is refused."""
-    index = torch.cuda.current_device() if dev.type == "cuda" else -1
-    if index < 0 or dev.index not in (None, index):
+    """The current stream's handle (device and stream taken raw: looking them up
+    through their objects costs a third of a short call).  Kernels are launched
+    on the current GPU, so work for another one, or on host memory, is refused."""
+    index = _gpus.get(dev, -1)
+    if index == -1:
+        if dev.type != "cuda":
+            raise ValueError(f"{dev} is not a GPU")
+        index = _gpus[dev] = dev.index
+    now = torch._C._cuda_getDevice()
+    if index is not None and index != now:
         raise ValueError(f"{dev} is not the current GPU")
-    return torch._C._cuda_getCurrentRawStream(index)
+    return torch._C._cuda_getCurrentRawStream(now)
 
 
 class Mat:

@@ -8,14 +8,17 @@ from integer_only_dnn_amd import ie
 
 
 def test_streams_are_those_of_the_current_gpu(monkeypatch):
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 1000 + index, raising=False)
     assert ie._stream(torch.device("cuda")) == 1000 and ie._stream(torch.device("cuda:0")) == 1000
     with pytest.raises(ValueError):
         ie._stream(torch.device("cpu"))
     with pytest.raises(ValueError):
-        ie._stream(torch.device("cuda:1"))
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+        ie._stream(torch.device("cpu:0"))
+    for _ in range(2):
+        with pytest.raises(ValueError):
+            ie._stream(torch.device("cuda:1"))
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)
     assert ie._stream(torch.device("cuda")) == 1001 and ie._stream(torch.device("cuda:1")) == 1001
 
 
