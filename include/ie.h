@@ -368,7 +368,8 @@ ie_status ie_layer_norm_bwd(const ie_mat *dY, const ie_mat *X, const ie_mat *gam
  * ROW, or NULL.  The product is exact; the bias and then R are added to it to
  * 53 bits (each sum exact while its terms span no more, else rounded half to
  * even), and the result is rounded once into Y's groups.  With neither bias
- * nor R it is ie_linear_fwd_act.  Backward: ie_linear_bwd_dx or ie_linear_bwd_dx_act,
+ * nor R it is ie_linear_fwd_act.  K <= 65536 and X and W 16-byte aligned, else
+ * IE_ERR_UNSUPPORTED (the other operands may lie anywhere).  Backward: ie_linear_bwd_dx or ie_linear_bwd_dx_act,
  * ie_linear_bwd_dw and ie_linear_bwd_db on the gradient behind the activation
  * (ie_relu_bwd), which is also R's gradient.
  */

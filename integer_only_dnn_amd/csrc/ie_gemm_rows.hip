@@ -21,11 +21,12 @@
 // each value is computed once (NI = 4 has no room and computes it twice).
 //
 // Bound by its phases one after the other: over 50432 x 768 x 192 the cycles
-// are 48 % fp64 and conversion instructions of the epilogue, 40 % LDS (column
-// scales and biases, staging) and 14 % products, and the registers hold no
-// second workgroup of NI >= 3 to set beside.  Measured, with the weight's layout:
-// 50432 x 768 x 192 33 us, 45 with a residual (round to odd by tiles and the pass
-// that closes it: 74 without), 25216 x 768 x 768 with a residual 38 us (51).
+// are 48 % fp64 and conversion instructions of the epilogue, 42 % LDS (column
+// scales and biases, staging) and 14 % products (25216 x 768 x 768: 32, 32 and
+// 23 %), and the registers hold no second workgroup of NI >= 3 to set beside.
+// Measured, with the weight's layout (3 to 5 us), from box to box: 50432 x 768 x
+// 192 31 to 34 us, 45 to 47 with a residual (round to odd by tiles and the pass
+// that closes it: 74 without), 25216 x 768 x 768 with a residual 37 to 41 us (51).
 #include <algorithm>
 #include <type_traits>
 

@@ -334,7 +334,8 @@ hipError_t launch_dropout(const DropArgs &a, const NormPlan &pl, hipStream_t st)
 
 // Product with bias and residual (ie_gemm_add.hip): rows m at exponent
 // xe, columns n at we, the result in this pass (y, ye) or as round-to-odd
-// values (v16) with the tiles' needs (p16) for launch_rto_finalize.
+// values (v16, rows add_pitch(N) apart) with the tiles' needs (p16) for
+// launch_add_round.
 struct AddEpi {
     const int8_t *xe, *we;
     int x_row, w_row;

@@ -87,10 +87,11 @@ constexpr int norm_block() {
 // T threads per row, E elements per thread.  gamma and beta stay in registers
 // (E <= 12, or when a block holds one row) or in LDS; the next row's loads are
 // in flight while a row is computed.
-// Bound by its instructions, 12 an element (issuing in 59 % of the cycles),
-// beside the stream: 25216 x 768 takes 14.7 us, 7.5 of them its 39 MB at the
-// rate of a large copy; 4096 x 4096 17.9 us, 6.5.  A whole-tensor result reads X
-// twice (25216 x 768: 24.6 us) unless one block holds it.
+// Bound by instructions, 14 an element (issuing in 59 % of the cycles), and by
+// the waits of two blocks a CU for loads and reductions (49 % of the waves'
+// time), beside the stream: 25216 x 768 takes 14.7 us, 7.5 of them its 39 MB at
+// the rate of a large copy; 4096 x 4096 17.2 us, 6.5.  A whole-tensor result
+// reads X twice (25216 x 768: 24.7 us) unless one block holds it.
 template <int T, int E, int BT>
 __global__ __launch_bounds__(BT) void norm_fwd_kernel(NormFwd p) {
     using C = Cols<T, E>;
@@ -232,8 +233,9 @@ __device__ __forceinline__ int top_part(const int8_t *e, int e_row, long long ro
 
 // Backward: NORM_NEED and NORM_ROWS also add up the columns of dgamma and
 // dbeta (p.pf, p.pb: one row of partial sums per block).
-// Bound by its instructions (61 % of the cycles issue one, two waves a SIMD by
-// the registers that hold the sums): 50432 x 192 takes 21 us and its sums' end 4,
+// Bound by its instructions, 45 an element (62 % of the cycles issue one, 49 %
+// where a row takes a block), and its waits (44 and 50 % of the waves' time: two waves a SIMD by the
+// registers that hold the sums): 50432 x 192 takes 21 us and its sums' end 4,
 // 5.6 of them its 29 MB at the rate of a large copy.  Wide rows, one to a block,
 // add their partial sums' way through memory: 4096 x 4096 takes 45 us in all, 9.6
 // of them X, dY and dX.
@@ -541,7 +543,7 @@ hipError_t launch_tops(const int8_t *e, long long n, int *tops, int n_tops, hipS
 // the rounded integer above those of 1.5 * 2^23; these are summed as they
 // are and the constant taken off at the end (modulo 2^32).  At s >= 8 every
 // |C| <= 128 rounds to 0.  At most 2^23 rows a block keep a sum in 32 bits.
-// Bound by its instructions, four an element (71 % of the cycles issue one):
+// Bound by its instructions, six an element (70 % of the cycles issue one):
 // 25216 x 2304 takes 14.2 us, 11 of them its 58 MB at the rate of a large copy.
 __global__ __launch_bounds__(256) void col_sum_kernel(const int8_t *dy, const int8_t *e, int e_row, long long rows,
                                                       int cols, int chunk, const int *tops, int n_tops, int *top,

@@ -355,8 +355,11 @@ Plan plan_product(long long M, long long N, long long K, int row_group, int fami
     return best;
 }
 
-// One 128 x 128 tile over a short contraction rounds in its own pass: 64 x 128
-// x 256 takes 6.8 us, 8.7 in 64 x 64 tiles with the pass that closes them.
+// One 128 x 128 tile over a short contraction rounds in its own pass: over 64 x
+// 128 x 256, 65 x 66 x 16, 65 x 65 x 256, 128 x 64 x 256 and 128 x 128 x 16, 64
+// and 256, both groupings, 6.8 to 7.4 us a call; in 64 x 64 tiles with the pass
+// that closes them 9.7 to 10.4.  100 x 100 x 200, whose rows are padded first,
+// 10.3 and 12.7.
 static bool one_tile(long long M, long long N, long long K) { return M <= 128 && N <= 128 && K <= 256; }
 
 Plan plan_add(long long M, long long N, long long K, int row_group, const Force &f) {
@@ -717,7 +720,10 @@ RowShape first_fit(const RowShape *s, int n, long long cols) {
 // Rows of up to 768 elements take 16 threads (four rows share a wave, its
 // reductions and its square root), longer ones a wave or a block.  With few
 // rows (NORM_FEW) more threads per row make the shorter chain of work (3000 x
-// 768: 4.9 us with 32 threads, 5.4 with 16; 25216 x 768: 15.1 and 14.7).  As
+// 768: 4.9 us with 32 threads, 5.4 with 16; 25216 x 768: 15.1 and 14.7), but at
+// 1025 to 2048 columns the 256 threads that few rows take are no gain (500 x
+// 1500: 5.4 us, 5.3 with 64) or a loss (2000 x 1100: 9.7 and 6.0; 4000 x 2040:
+// 16.2 and 9.9).  As
 // many blocks as are resident, two or four a CU by their registers, so that
 // each keeps its parameters for several rows (25216 x 768 at 512, 1024 and 2048
 // blocks: 14.7, 15.2, 16.8 us; 50432 x 192: 11.5, 10.9, 12.5).

@@ -63,11 +63,13 @@ def _one(pattern: str) -> str:
     return hits[-1]
 
 
-def kernel_stats(trace_dir: str):
+def kernel_stats(trace_dir: str, own: bool = False):
     path = _one(os.path.join(trace_dir, "**", "*kernel_stats.csv"))
     rows = []
     with open(path) as f:
         for r in csv.DictReader(f):
+            if own and "ie::" not in r["Name"]:
+                continue
             rows.append({"name": short_name(r["Name"]), "calls": int(r["Calls"]),
                          "avg_us": float(r["AverageNs"]) / 1e3, "total_ms": float(r["TotalDurationNs"]) / 1e6,
                          "pct": float(r["Percentage"]), "min_us": float(r["MinNs"]) / 1e3,
@@ -75,7 +77,7 @@ def kernel_stats(trace_dir: str):
     return rows
 
 
-def counter_per_kernel(pmc_dir: str):
+def counter_per_kernel(pmc_dir: str, own: bool = False):
     """{kernel: (dispatches, mean counter value per dispatch)} of a --pmc run."""
     path = _one(os.path.join(pmc_dir, "**", "*counter_collection.csv"))
     acc = defaultdict(lambda: [0, 0.0])
@@ -83,6 +85,8 @@ def counter_per_kernel(pmc_dir: str):
     with open(path) as f:
         for r in csv.DictReader(f):
             k = short_name(r["Kernel_Name"])
+            if own and "ie::" not in r["Kernel_Name"] and k != COPY_KERNEL:
+                continue
             if k == COPY_KERNEL:
                 # keep the large calibration copy apart from small runtime copies
                 g = int(r.get("Grid_Size", 0) or 0)
@@ -101,8 +105,8 @@ def _copy_entry(per):
     return max(copies, key=lambda k: per[k][1])
 
 
-def write_stats(trace_dir: str, out: str, cmd: str, top: int = 25) -> None:
-    rows = kernel_stats(trace_dir)
+def write_stats(trace_dir: str, out: str, cmd: str, top: int = 25, own: bool = False) -> None:
+    rows = kernel_stats(trace_dir, own)
     lines = [f"# rocprofv3 kernel statistics: {os.path.splitext(os.path.basename(out))[0]}", "",
              "Command (run from /tmp with TMPDIR=/tmp; bench.py at the repository root):", "", "```",
              cmd, "```", "", f"Library source digest: {source_digest()}", "",
@@ -115,8 +119,9 @@ def write_stats(trace_dir: str, out: str, cmd: str, top: int = 25) -> None:
         f.write("\n".join(lines) + "\n")
 
 
-def write_traffic(fetch_dir: str, write_dir: str, copy_mib: int, workload: str, out: str, cmds) -> None:
-    fetch, write = counter_per_kernel(fetch_dir), counter_per_kernel(write_dir)
+def write_traffic(fetch_dir: str, write_dir: str, copy_mib: int, workload: str, out: str, cmds,
+                  own: bool = False) -> None:
+    fetch, write = counter_per_kernel(fetch_dir, own), counter_per_kernel(write_dir, own)
     copy_kib = copy_mib * 1024.0
     fk, wk = _copy_entry(fetch), _copy_entry(write)
     f_scale = copy_kib / fetch[fk][1]
@@ -153,7 +158,7 @@ def read_traffic(path: str):
     return digest, table
 
 
-def counters_per_kernel(dirs):
+def counters_per_kernel(dirs, own: bool = False):
     """{kernel: {counter: mean value per dispatch}} over several --pmc runs,
     and {kernel: dispatches}."""
     acc = defaultdict(lambda: defaultdict(lambda: [0, 0.0]))
@@ -162,6 +167,8 @@ def counters_per_kernel(dirs):
         path = _one(os.path.join(d, "**", "*counter_collection.csv"))
         with open(path) as f:
             for r in csv.DictReader(f):
+                if own and "ie::" not in r["Kernel_Name"]:
+                    continue
                 k = short_name(r["Kernel_Name"])
                 a = acc[k][r["Counter_Name"]]
                 a[0] += 1
@@ -171,8 +178,8 @@ def counters_per_kernel(dirs):
             {k: len(v) // max(1, len(dirs)) for k, v in disp.items()})
 
 
-def write_counters(dirs, workload: str, out: str, cmds, top: int = 16) -> None:
-    per, ndisp = counters_per_kernel(dirs)
+def write_counters(dirs, workload: str, out: str, cmds, top: int = 16, own: bool = False) -> None:
+    per, ndisp = counters_per_kernel(dirs, own)
 
     def g(cs, name):
         return cs.get(name)
@@ -192,11 +199,13 @@ def write_counters(dirs, workload: str, out: str, cmds, top: int = 16) -> None:
              "Per dispatch, averaged over dispatches.  Columns: waves; instructions per wave (VALU, MFMA, LDS, "
              "vector-memory reads); `wait%` = SQ_WAIT_ANY / SQ_WAVE_CYCLES (wave lifetime waiting on a memory "
              "or LDS counter); `valu%`, `lds%` = SQ_ACTIVE_INST_VALU, SQ_ACTIVE_INST_LDS over SQ_WAVE_CYCLES "
-             "(lifetime issuing); `mfma%` = SQ_VALU_MFMA_BUSY_CYCLES / (SQ_BUSY_CU_CYCLES x 4 SIMDs), the "
+             "(lifetime issuing); `issue%` = SQ_ACTIVE_INST_VALU / SQ_BUSY_CU_CYCLES, the share of busy-CU cycles "
+             "a SIMD issues a vector instruction in, and `ldsbusy%` = SQ_LDS_IDX_ACTIVE / SQ_BUSY_CU_CYCLES; `mfma%` = SQ_VALU_MFMA_BUSY_CYCLES / (SQ_BUSY_CU_CYCLES x 4 SIMDs), the "
              "share of busy-CU cycles the matrix cores work; `bank%` = SQ_LDS_BANK_CONFLICT / "
              "SQ_LDS_IDX_ACTIVE.", "",
-             "| kernel | disp | waves | VALU/w | MFMA/w | LDS/w | VMEMrd/w | wait% | valu% | lds% | mfma% | bank% |",
-             "|---|---:|---:|---:|---:|---:|---:|---:|---:|---:|---:|---:|"]
+             "| kernel | disp | waves | VALU/w | MFMA/w | LDS/w | VMEMrd/w | wait% | valu% | lds% | issue% | ldsbusy% | mfma% | "
+             "bank% |",
+             "|---|---:|---:|---:|---:|---:|---:|---:|---:|---:|---:|---:|---:|---:|"]
     for k, cs in rows[:top]:
         wc = g(cs, "SQ_WAVE_CYCLES")
         lines.append(
@@ -204,6 +213,8 @@ def write_counters(dirs, workload: str, out: str, cmds, top: int = 16) -> None:
             f"{per_wave(cs, 'SQ_INSTS_MFMA')} | {per_wave(cs, 'SQ_INSTS_LDS')} | {per_wave(cs, 'SQ_INSTS_VMEM_RD')} | "
             f"{ratio(g(cs, 'SQ_WAIT_ANY'), wc)} | {ratio(g(cs, 'SQ_ACTIVE_INST_VALU'), wc)} | "
             f"{ratio(g(cs, 'SQ_ACTIVE_INST_LDS'), wc)} | "
+            f"{ratio(g(cs, 'SQ_ACTIVE_INST_VALU'), g(cs, 'SQ_BUSY_CU_CYCLES'))} | "
+            f"{ratio(g(cs, 'SQ_LDS_IDX_ACTIVE'), g(cs, 'SQ_BUSY_CU_CYCLES'))} | "
             f"{ratio(g(cs, 'SQ_VALU_MFMA_BUSY_CYCLES'), g(cs, 'SQ_BUSY_CU_CYCLES'), 0.25)} | "
             f"{ratio(g(cs, 'SQ_LDS_BANK_CONFLICT'), g(cs, 'SQ_LDS_IDX_ACTIVE'))} |")
     lines += ["", "Raw means per dispatch:", ""]
@@ -236,13 +247,15 @@ def main() -> None:
     c.add_argument("--out", required=True)
     c.add_argument("--cmd", action="append", default=[])
     c.add_argument("--top", type=int, default=16)
+    for p in (s, t, c):
+        p.add_argument("--own", action="store_true", help="this library's kernels only")
     a = ap.parse_args()
     if a.what == "stats":
-        write_stats(a.dir, a.out, a.cmd)
+        write_stats(a.dir, a.out, a.cmd, own=a.own)
     elif a.what == "counters":
-        write_counters(a.dir, a.workload, a.out, a.cmd, a.top)
+        write_counters(a.dir, a.workload, a.out, a.cmd, a.top, a.own)
     else:
-        write_traffic(a.fetch, a.write, a.copy_mib, a.workload, a.out, a.cmd)
+        write_traffic(a.fetch, a.write, a.copy_mib, a.workload, a.out, a.cmd, a.own)
 
 
 if __name__ == "__main__":
