@@ -75,6 +75,7 @@ typedef enum {
 typedef enum { IE_GROUP_TENSOR = 0, IE_GROUP_ROW = 1 } ie_group;
 
 #define IE_FLAG_EXP_RANGE 1u
+#define IE_FLAG_INDEX 2u /* an offset, length, position, page or slot read on the device lies outside its range */
 
 /* A (C, e) matrix.  mant: rows*cols bytes, row-major.  exp: 1 byte (TENSOR)
  * or `rows` bytes (ROW).
@@ -411,6 +412,51 @@ typedef struct {
 size_t ie_dropout_workspace(int64_t rows, int64_t cols);
 ie_status ie_dropout(const ie_mat *X, const ie_mat *R, const ie_mat *Y, const ie_dropout_desc *d, void *ws,
                      size_t ws_bytes, void *stream);
+
+/*
+ * Softmax attention of packed sequences (the softmax between the products of
+ * ie_bmm_nt and ie_bmm_nn, and its gradient).  QKV [rows x (heads + 2
+ * kv_heads) * head_dim], as the projection in front writes it: a row is a
+ * token, its columns the query heads, then the key heads, then the value
+ * heads; query head h reads key and value head h / (heads / kv_heads).
+ * Sequence s is rows offsets[s] .. offsets[s + 1] - 1 (a device array of
+ * n_seq + 1, read when the kernels run); offsets NULL and n_seq 0: all rows
+ * are one sequence.  causal: a token sees itself and those before it, else
+ * all of its sequence.  A sequence may be empty.
+ *
+ *   O = softmax(scale Q K^T) V   of every head,  O [rows x heads * head_dim].
+ *
+ * Arithmetic, for row i of a head (e_i its exponent, read clipped to [-48, 16];
+ * an exponent above 16 sets IE_FLAG_EXP_RANGE): t_j = (q_i . k_j) 2^(e_j)
+ * exactly, m = max t_j over the keys that i sees, r = scale log2(e), rounded to
+ * fp32, times 2^(e_i);
+ *   y_j = max(R((t_j - m) r 2^17) 2^-17, -32), t_j - m rounded to fp32 first,
+ *   w_j = 2^floor(y_j) p(y_j - floor(y_j)),
+ *   p(f) = ((2545 f + 7358) f + 22609) f + 32512, every step rounded to fp32
+ * (32512 2^f to 1.1e-4), L = sum R(w_j), E = max e_j over the keys that i sees,
+ *   o = (sum_j R(w_j 2^(e_j - E)) v_j) (1 / L) 2^E,
+ * the sums exact, 1 / L and the product with it rounded to 53 bits; the row is
+ * rounded once into O.  So a weight is held to 15 bits below the largest one,
+ * and a token's result depends on the tokens that it sees and on no others.
+ * O must be ROW (one exponent a token), else IE_ERR_UNSUPPORTED.  Rows before
+ * the first and behind the last sequence are left as they were, mantissas and
+ * exponents.
+ * stats: for the backward pass, 8 bytes for every row and head (a device array
+ * [rows x heads], 8-byte aligned): m and L; NULL where none follows.
+ * Limits (IE_ERR_UNSUPPORTED): head_dim <= 128, 2^-30 <= scale <= 2^30.
+ * Offsets that decrease or leave the matrix, and sequences of more than 131072
+ * tokens, set IE_FLAG_INDEX: the rows they name are undefined, no others.
+ */
+typedef struct {
+    int32_t heads, kv_heads, head_dim;
+    int32_t causal;
+    float scale;
+    int32_t n_seq;
+    const int32_t *offsets;
+} ie_attention_desc;
+size_t ie_attention_fwd_workspace(const ie_attention_desc *d, int64_t rows);
+ie_status ie_attention_fwd(const ie_attention_desc *d, const ie_mat *QKV, const ie_mat *O, void *stats, void *ws,
+                           size_t ws_bytes, void *stream);
 
 /* Wait for `stream`, then copy the workspace's sticky flags to *flags and,
  * if clear != 0, zero them. */

@@ -1224,6 +1224,78 @@ ie_status ie_dropout(const ie_mat *X, const ie_mat *R, const ie_mat *Y, const ie
     return hip_status(launch_dropout(a, pl, st));
 }
 
+// ---------------------------------------------------------------------------
+// Attention
+// ---------------------------------------------------------------------------
+
+static long long att_cols(const ie_attention_desc *d) {
+    return ((long long)d->heads + 2ll * d->kv_heads) * d->head_dim;
+}
+
+// The parts of an attention call that its matrix and its heads give.
+static AttnArgs att_args(const ie_attention_desc *d, const ie_mat *X, void *ws) {
+    AttnArgs a;
+    memset(&a, 0, sizeof a);
+    a.x = X->mant;
+    a.xe = X->exp;
+    a.x_row = X->group == IE_GROUP_ROW && X->rows > 1;
+    a.rows = X->rows;
+    a.heads = d->heads;
+    a.kv = d->kv_heads;
+    a.group = d->heads / d->kv_heads;
+    a.d = d->head_dim;
+    a.width = (int)att_cols(d);
+    a.off = d->offsets;
+    a.n_seq = d->n_seq;
+    a.causal = d->causal != 0;
+    a.vec = d->head_dim % 16 == 0 && aligned(X->mant, 16);
+    a.most = ATT_MOST;
+    a.c = (float)((double)d->scale * 1.4426950408889634);
+    a.scale = (double)d->scale;
+    a.flags = (uint32_t *)ws;
+    return a;
+}
+
+// Whether a byte of m is one of the n at p.
+static bool share_bytes(const ie_mat *m, const void *p, size_t n) {
+    const ie_mat b = {(int8_t *)p, (int8_t *)p, 1, (int64_t)n, IE_GROUP_TENSOR, 0};
+    return p && n && share(m, &b);
+}
+
+size_t ie_attention_fwd_workspace(const ie_attention_desc *d, int64_t rows) {
+    if (!d || rows < 0 || d->heads < 1 || d->head_dim < 1 || d->head_dim > ATT_HEAD_MAX) return 0;
+    return attention_fwd_ws(rows, d->heads, d->head_dim);
+}
+
+ie_status ie_attention_fwd(const ie_attention_desc *d, const ie_mat *QKV, const ie_mat *O, void *stats, void *ws,
+                           size_t ws_bytes, void *stream) {
+    if (!d) return IE_ERR_NULL;
+    IE_CHECK(check_attention(d, QKV, att_cols(d)));
+    IE_CHECK(check_mat(O));
+    if (O->rows != QKV->rows || O->cols != (long long)d->heads * d->head_dim) return IE_ERR_SHAPE;
+    if (O->group != IE_GROUP_ROW || !aligned(stats, 8)) return IE_ERR_UNSUPPORTED;
+    const size_t stat_bytes = stats ? (size_t)O->rows * d->heads * 8 : 0, off_bytes = ((size_t)d->n_seq + 1) * 4;
+    if (share(O, QKV) || share_bytes(O, d->offsets, off_bytes) || share_bytes(O, stats, stat_bytes) ||
+        share_bytes(QKV, stats, stat_bytes))
+        return IE_ERR_UNSUPPORTED;
+    if (!ws) return IE_ERR_WORKSPACE;
+    if (ws_bytes < attention_fwd_ws(QKV->rows, d->heads, d->head_dim)) return IE_ERR_WORKSPACE;
+    if (QKV->rows == 0) return IE_OK;
+    AttnArgs a = att_args(d, QKV, ws);
+    Carve c{(char *)ws, HEADER};
+    const AttFwdWs w = carve_attention_fwd(c, QKV->rows, d->heads, d->head_dim);
+    a.stats = (int2 *)stats;
+    a.v16 = w.v16;
+    a.p16 = w.p16;
+    a.y = O->mant;
+    a.ye = O->exp;
+    a.cols = (int)O->cols;
+    a.parts = d->heads;
+    a.q = mat_q(O);
+    a.out_vec = d->head_dim % 16 == 0 && aligned(O->mant, 8);
+    return hip_status(launch_attention_fwd(a, (hipStream_t)stream));
+}
+
 size_t ie_bmm_workspace(int32_t batch, int64_t M, int64_t N, int64_t K) {
     if (batch < 0 || M < 0 || N < 0 || K < 0) return 0;
     return bmm_ws(batch, M, N, K);

@@ -142,6 +142,15 @@ constexpr int PROF_NORM_BWD = 3610;
 constexpr int PROF_COL_SUM = 3620;
 constexpr int PROF_COL_FINISH = 3630;
 constexpr int PROF_DROPOUT = 3700;
+constexpr int PROF_ROPE = 3900;
+constexpr int PROF_ATT_FWD = 4000;
+constexpr int PROF_ATT_ROUND = 4010;
+constexpr int PROF_ATT_PREP = 4020;
+constexpr int PROF_ATT_DQ = 4030;
+constexpr int PROF_ATT_DKV = 4040;
+constexpr int PROF_CACHE_STORE = 4100;
+constexpr int PROF_ATT_CACHE = 4110;
+constexpr int PROF_ATT_JOIN = 4120;
 constexpr int PROF_GEMM_ADD = 3800;
 constexpr int PROF_SPLIT_ADD = 3810;
 
@@ -331,6 +340,30 @@ struct DropArgs {
     uint32_t *flags;
 };
 hipError_t launch_dropout(const DropArgs &a, const NormPlan &pl, hipStream_t st);
+
+// Attention over packed sequences (ie_attention.hip, ie_attention_bwd.hip):
+// rows of x hold `heads` query heads, then `kv` key heads and `kv` value heads
+// of d elements each.
+struct AttnArgs {
+    const int8_t *x, *xe;
+    int x_row;
+    long long rows;
+    int heads, kv, group, d, width;  // group: query heads to a key head; width: columns of x
+    const int *off;                  // [n_seq + 1], or nullptr: one sequence
+    int n_seq, causal, vec;          // vec: every head's row starts at a multiple of 16 bytes
+    int most;                        // tokens of the longest sequence
+    float c;                         // scale log2(e)
+    double scale;
+    int2 *stats;                     // [rows][heads]: largest score, sum of weights
+    // results: round-to-odd values [rows][cols] and needs [rows][parts] of heads of d
+    int16_t *v16, *p16;
+    int8_t *y, *ye;
+    int cols, parts, q, out_vec;     // out_vec: rows of y can be written eight mantissas at a time
+    uint32_t *flags;
+};
+hipError_t launch_attention_fwd(const AttnArgs &a, hipStream_t st);
+// The rounding of v16, p16 into y by rows.
+hipError_t launch_attention_round(const AttnArgs &a, hipStream_t st);
 
 // Product with bias and residual (ie_gemm_add.hip): rows m at exponent
 // xe, columns n at we, the result in this pass (y, ye) or as round-to-odd

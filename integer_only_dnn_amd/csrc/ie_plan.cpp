@@ -840,6 +840,35 @@ int *carve_dropout(Carve &c, long long rows, long long cols) {
     return c.take<int>((size_t)dropout_plan(rows, cols).grid);
 }
 
+AttFwdWs carve_attention_fwd(Carve &c, long long rows, long long heads, long long d) {
+    AttFwdWs w;
+    w.v16 = c.take<int16_t>((size_t)(rows * heads * d));
+    w.p16 = c.take<int16_t>((size_t)(rows * heads));
+    return w;
+}
+
+size_t attention_fwd_ws(long long rows, long long heads, long long d) {
+    Carve c{nullptr, HEADER};
+    carve_attention_fwd(c, rows, heads, d);
+    return align256(c.off);
+}
+
+// The heads of an attention call and the matrix that holds them.
+ie_status check_attention(const ie_attention_desc *d, const ie_mat *X, long long cols) {
+    if (!d) return IE_ERR_NULL;
+    const ie_status s = check_mat(X);
+    if (s != IE_OK) return s;
+    if (d->heads < 1 || d->kv_heads < 1 || d->head_dim < 1 || d->heads % d->kv_heads || d->n_seq < 0)
+        return IE_ERR_SHAPE;
+    if (X->cols != cols) return IE_ERR_SHAPE;
+    if (!d->offsets != !d->n_seq) return IE_ERR_SHAPE;
+    if (d->head_dim > ATT_HEAD_MAX || (uintptr_t)d->offsets % 4) return IE_ERR_UNSUPPORTED;
+    // 2^-30 .. 2^30: r = scale log2(e) 2^e keeps clear of fp32's ends (a NaN is refused too)
+    if (!(d->scale >= 0x1p-30f && d->scale <= 0x1p30f)) return IE_ERR_UNSUPPORTED;
+    if (att_slots(X->rows, d->n_seq, 64) * d->heads > ATT_ITEMS_MAX) return IE_ERR_UNSUPPORTED;
+    return IE_OK;
+}
+
 size_t dropout_ws(long long rows, long long cols) {
     Carve c{nullptr, HEADER};
     carve_dropout(c, rows, cols);

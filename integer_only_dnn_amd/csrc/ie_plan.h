@@ -435,6 +435,20 @@ NormWs carve_norm_bwd(Carve &c, long long rows, long long cols);
 ColWs carve_linear_db(Carve &c, long long rows, long long cols);
 int *carve_dropout(Carve &c, long long rows, long long cols);  // block maxima
 
+// Attention over packed sequences: tile slots of bm rows (a sequence's first
+// slot is off / bm plus its number), and the tokens of the longest sequence
+// whose int32 sums of digits (at most 127 * 128 each) stay exact.
+constexpr int ATT_MOST = 131072;
+constexpr int ATT_HEAD_MAX = 128;
+constexpr long long ATT_ITEMS_MAX = 1ll << 30;  // workgroups of a launch
+inline long long att_slots(long long rows, long long n_seq, int bm) { return rows / bm + (n_seq > 0 ? n_seq : 1); }
+struct AttFwdWs {
+    int16_t *v16, *p16;  // round-to-odd results and the needs of their heads
+};
+AttFwdWs carve_attention_fwd(Carve &c, long long rows, long long heads, long long d);
+size_t attention_fwd_ws(long long rows, long long heads, long long d);
+ie_status check_attention(const ie_attention_desc *d, const ie_mat *X, long long cols);
+
 // Whether a parameter vector of n channels is [n x 1] or [1 x n].
 bool is_vector(const ie_mat *t, long long n);
 

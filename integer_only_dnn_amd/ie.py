@@ -49,6 +49,11 @@ class ie_dropout_desc(ctypes.Structure):
     _fields_ = [("seed", c_uint64), ("step", c_uint64), ("step_ptr", c_void_p), ("drop", c_uint32)]
 
 
+class ie_attention_desc(ctypes.Structure):
+    _fields_ = [("heads", c_int32), ("kv_heads", c_int32), ("head_dim", c_int32), ("causal", c_int32),
+                ("scale", ctypes.c_float), ("n_seq", c_int32), ("offsets", c_void_p)]
+
+
 EXPORTS = [
     ("ie_linear_fwd_workspace", c_size_t, [c_int64, c_int64, c_int64]),
     ("ie_linear_bwd_dx_workspace", c_size_t, [c_int64, c_int64, c_int64]),
@@ -90,6 +95,9 @@ EXPORTS = [
     ("ie_dropout_workspace", c_size_t, [c_int64, c_int64]),
     ("ie_dropout", c_int,
      [POINTER(ie_mat)] * 3 + [POINTER(ie_dropout_desc), c_void_p, c_size_t, c_void_p]),
+    ("ie_attention_fwd_workspace", c_size_t, [POINTER(ie_attention_desc), c_int64]),
+    ("ie_attention_fwd", c_int,
+     [POINTER(ie_attention_desc)] + [POINTER(ie_mat)] * 2 + [c_void_p, c_void_p, c_size_t, c_void_p]),
     ("ie_device_status", c_int, [c_void_p, c_void_p, POINTER(c_uint32), c_int]),
     ("ie_profile_enable", c_int, [c_int]),
     ("ie_profile_select", c_int, [c_int]),
@@ -474,6 +482,46 @@ def ie_dropout(X: Mat, R: Mat | None, Y: Mat, drop: int, seed: int, step: int, w
     d = ie_dropout_desc(seed, step, step_ptr.data_ptr() if step_ptr is not None else None, drop)
     p, b = ws.get(_ws_rows("ie_dropout_workspace", x.rows, x.cols))
     _check(lib().ie_dropout(byref(x), _opt(R), byref(y), byref(d), p, b, _stream(ws.device)), "ie_dropout")
+
+
+def _device_array(t: torch.Tensor, dtype, what: str, numel=None) -> int:
+    """The address of a contiguous device array of `numel` (None: any number of) `dtype`."""
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or (numel is not None and t.numel() < numel):
+        raise ValueError(f"{what} must be a contiguous {dtype} device tensor" + (f" of {numel}" if numel else ""))
+    return t.data_ptr()
+
+
+class Attention:
+    """The heads and sequences of attention calls.  offsets: an int32 device
+    tensor of one entry more than there are sequences, sequence s being rows
+    offsets[s] .. offsets[s + 1] - 1; None: all rows are one sequence."""
+
+    def __init__(self, heads: int, kv_heads: int, head_dim: int, scale: float, causal: bool = False,
+                 offsets: torch.Tensor | None = None):
+        at, n = None, 0
+        if offsets is not None:
+            at, n = _device_array(offsets, torch.int32, "offsets"), offsets.numel() - 1
+            if n < 1:
+                raise ValueError("offsets needs two entries or more")
+        self.offsets = offsets
+        self.desc = ie_attention_desc(heads, kv_heads, head_dim, int(causal), scale, n, at)
+        self._sizes = {}  # (query, rows) -> workspace bytes
+
+    def _bytes(self, name: str, rows: int) -> int:
+        n = self._sizes.get((name, rows))
+        if n is None:
+            n = self._sizes[(name, rows)] = getattr(lib(), name)(byref(self.desc), rows)
+        return n
+
+
+def ie_attention_fwd(att: Attention, QKV: Mat, O: Mat, ws: Workspace, stats: torch.Tensor | None = None) -> None:
+    """O = softmax(scale Q K^T) V of every head and sequence.  stats: an int32
+    device tensor [rows, heads, 2] for the backward pass, or None."""
+    x, o = QKV.c(), O.c()
+    sp = None if stats is None else _device_array(stats, torch.int32, "stats", 2 * x.rows * att.desc.heads)
+    p, b = ws.get(att._bytes("ie_attention_fwd_workspace", x.rows))
+    _check(lib().ie_attention_fwd(byref(att.desc), byref(x), byref(o), sp, p, b, _stream(ws.device)),
+           "ie_attention_fwd")
 
 
 def ie_profile_enable(on: bool = True) -> None:
