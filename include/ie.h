@@ -458,6 +458,98 @@ size_t ie_attention_fwd_workspace(const ie_attention_desc *d, int64_t rows);
 ie_status ie_attention_fwd(const ie_attention_desc *d, const ie_mat *QKV, const ie_mat *O, void *stats, void *ws,
                            size_t ws_bytes, void *stream);
 
+/*
+ * Rotary positions: Y = R_Y(X with the pairs of its heads turned).  X, Y
+ * [rows x cols], each TENSOR or ROW; the first `heads` heads of head_dim
+ * columns are turned (of QKV: heads + kv_heads), the columns behind them are
+ * not, they only take the row's exponent.  Of a head its first `rot` elements
+ * are turned, in rot / 2 pairs: (2 k, 2 k + 1) if interleaved, else (k, k + rot
+ * / 2):
+ *   (a, b) -> (a c - b s, a s + b c),  (c, s) = table[position][k] 2^-14,
+ * or with -s if `inverse`, which undoes it up to rounding and is its gradient.
+ * The numbers are exact (units of 2^(e - 14)) and rounded once.
+ * pos: a device array of the rows' positions, or NULL for the row's number.  A
+ * position outside 0 .. positions - 1 sets IE_FLAG_INDEX and is read as 0.
+ * table: device memory, [positions x rot / 2] pairs of int16, 16-byte aligned.
+ * rot even and <= IE_ROPE_MAX, head_dim <= 2^15, cols <= 2^30, table 16-byte
+ * and pos 4-byte aligned, else IE_ERR_UNSUPPORTED; rot <= head_dim and heads *
+ * head_dim <= cols, else IE_ERR_SHAPE.
+ *
+ * ie_rope_table fills such a table: c = R(cos(t f_k) 2^14), s = R(sin(t f_k)
+ * 2^14), angles in 64 bits, with f_k = base^(-2 k / rot) u_k for contexts
+ * `factor` times the trained length:
+ *   trained = 0: u_k = 1 / factor (all positions stretched),
+ *   else by parts: u_k = g + (1 - g) / factor, g = (n - low) / (high - low) cut
+ *   to [0, 1], n = trained f / (2 pi) the turns of the unscaled frequency over
+ *   the trained length (fast pairs stay, slow ones are stretched).
+ * base > 0, factor > 0, trained >= 0, low < high if trained > 0, all finite,
+ * else IE_ERR_UNSUPPORTED.
+ */
+#define IE_ROPE_MAX 512
+typedef struct {
+    double base, factor, trained, low, high;
+} ie_rope_freqs;
+ie_status ie_rope_table(const ie_rope_freqs *f, int32_t rot, int64_t positions, int16_t *table, void *stream);
+typedef struct {
+    const int16_t *table;
+    int64_t positions;
+    const int32_t *pos;
+    int32_t heads, head_dim, rot;
+    int32_t interleaved, inverse;
+} ie_rope_desc;
+size_t ie_rope_workspace(int64_t rows, int64_t cols);
+ie_status ie_rope(const ie_rope_desc *d, const ie_mat *X, const ie_mat *Y, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * A cache of keys and values with mantissas of 4 bits (|C| <= 7), in `pages`
+ * pages of `page` slots; all pointers are device memory:
+ *   k, v:         [pages x page x kv_heads x head_dim / 2] bytes, element 2 i of
+ *                 a head in the low half of byte i, element 2 i + 1 in the high
+ *                 half, as 4-bit two's complement numbers;
+ *   k_exp, v_exp: [pages x page x kv_heads] exponents.
+ * page a power of two, head_dim a multiple of 16 and <= 128, k and v 8-byte
+ * aligned, pages * page < 2^31, kv_heads <= 65536, else IE_ERR_UNSUPPORTED.
+ */
+typedef struct {
+    uint8_t *k, *v;
+    int8_t *k_exp, *v_exp;
+    int32_t pages, page;
+    int32_t kv_heads, head_dim;
+} ie_cache;
+
+/*
+ * Store the keys and values of QKV (as in ie_attention_fwd, `heads` query
+ * heads; columns (heads + 2 kv_heads) head_dim) into the cache: row t into slot
+ * slots[t] (slot s is offset s % page of page s / page), each head's key
+ * and value rounded to 4 bits with the smallest exponent that holds it.  A negative slot leaves the row out; one past the cache sets
+ * IE_FLAG_INDEX and leaves it out.  Slots that are not named are left as they
+ * were.  Two rows must not name the same slot (its bytes are then a mixture of
+ * theirs).  ws: at least 256 bytes (the flags).
+ */
+ie_status ie_cache_store(const ie_cache *c, int32_t heads, const ie_mat *QKV, const int32_t *slots, void *ws, size_t ws_bytes,
+                         void *stream);
+
+/*
+ * Attention of one token a sequence over the cache: O = softmax(scale q K^T) V
+ * of every head.  Q [n x heads * head_dim] (or QKV rows, whose further columns
+ * are not read), row i the query of sequence i; d as in ie_attention_fwd with
+ * offsets NULL and n_seq 0 (d->causal is not read: a token sees all keys).
+ * lengths[i] keys of sequence i are in the cache, key j at offset j % page of
+ * page pages[i * per + j / page]: store a step's own key first.
+ * Arithmetic: as in ie_attention_fwd for each run b of 256 keys (positions 256 b
+ * ..), with a maximum m_b, a sum L_b and an exponent E_b of its own (of the
+ * values; keys and values have exponents of their own here), N_b = sum_j
+ * R(w_j 2^(ev_j - E_b)) v_j; then, with a_b the weight of m_b - m, m = max m_b,
+ * E = max E_b, o = (sum_b R(a_b 2^(E_b - E)) N_b) (1 / sum_b R(a_b) L_b) 2^E.
+ * A sequence without keys gives zeros.  A length outside 0 .. per * page sets
+ * IE_FLAG_INDEX and is cut; a page outside the cache sets it and its keys are
+ * left out.  O [n x heads * head_dim] must be ROW, else IE_ERR_UNSUPPORTED.
+ * per * page <= 2^23, else IE_ERR_UNSUPPORTED.
+ */
+size_t ie_attention_cache_workspace(const ie_attention_desc *d, int64_t n, int64_t tokens); /* tokens: per * page */
+ie_status ie_attention_cache(const ie_attention_desc *d, const ie_mat *Q, const ie_cache *c, const int32_t *pages, int32_t per,
+                             const int32_t *lengths, const ie_mat *O, void *ws, size_t ws_bytes, void *stream);
+
 /* Wait for `stream`, then copy the workspace's sticky flags to *flags and,
  * if clear != 0, zero them. */
 ie_status ie_device_status(void *ws, void *stream, uint32_t *flags, int clear);

@@ -3,6 +3,7 @@
 // See include/ie.h.
 #include <stdio.h>
 #include <stdlib.h>
+#include <math.h>
 #include <string.h>
 
 #include <atomic>
@@ -1294,6 +1295,170 @@ ie_status ie_attention_fwd(const ie_attention_desc *d, const ie_mat *QKV, const 
     a.q = mat_q(O);
     a.out_vec = d->head_dim % 16 == 0 && aligned(O->mant, 8);
     return hip_status(launch_attention_fwd(a, (hipStream_t)stream));
+}
+
+ie_status ie_rope_table(const ie_rope_freqs *f, int32_t rot, int64_t positions, int16_t *table, void *stream) {
+    if (!f) return IE_ERR_NULL;
+    if (rot < 0 || positions < 0) return IE_ERR_SHAPE;
+    if (rot % 2 || rot > IE_ROPE_MAX || positions > DIM_MAX || !aligned(table, 16)) return IE_ERR_UNSUPPORTED;
+    if (rot > 0 && positions > 0 && !table) return IE_ERR_NULL;
+    const double inf = INFINITY;
+    if (!(f->base > 0 && f->base < inf && f->factor > 0 && f->factor < inf && f->trained >= 0 && f->trained < inf))
+        return IE_ERR_UNSUPPORTED;
+    if (f->trained > 0 && !(f->high - f->low > 0 && fabs(f->low) < inf && fabs(f->high) < inf)) return IE_ERR_UNSUPPORTED;
+    if (rot == 0 || positions == 0) return IE_OK;
+    double w[IE_ROPE_MAX / 2];
+    for (int k = 0; k < rot / 2; ++k) {
+        const double fk = pow(f->base, -2.0 * k / rot);
+        double keep = 0.0;
+        if (f->trained > 0) {
+            keep = (f->trained * fk / (2.0 * 3.141592653589793) - f->low) / (f->high - f->low);
+            keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
+        }
+        w[k] = fk * (keep + (1.0 - keep) / f->factor);
+    }
+    return hip_status(launch_rope_table(w, rot / 2, positions, table, (hipStream_t)stream));
+}
+
+size_t ie_rope_workspace(int64_t rows, int64_t cols) {
+    if (rows < 0 || cols < 0) return 0;
+    return rope_ws(rows, cols);
+}
+
+ie_status ie_rope(const ie_rope_desc *d, const ie_mat *X, const ie_mat *Y, void *ws, size_t ws_bytes, void *stream) {
+    if (!d) return IE_ERR_NULL;
+    IE_CHECK(check_mat(X));
+    IE_CHECK(check_mat(Y));
+    if (!same_shape(X, Y)) return IE_ERR_SHAPE;
+    if (d->heads < 0 || d->head_dim < 1 || d->rot < 0 || d->rot > d->head_dim || d->positions < 1 ||
+        (long long)d->heads * d->head_dim > X->cols)
+        return IE_ERR_SHAPE;
+    if (!d->table && d->rot > 0) return IE_ERR_NULL;
+    if (d->rot % 2 || d->rot > IE_ROPE_MAX || d->head_dim > (1 << 15) || X->cols > LONG_COLS_MAX || d->positions > DIM_MAX ||
+        !aligned(d->table, 16) || !aligned(d->pos, 4))
+        return IE_ERR_UNSUPPORTED;
+    const size_t table_bytes = (size_t)d->positions * d->rot * 2, pos_bytes = d->pos ? (size_t)X->rows * 4 : 0;
+    if (share(Y, X) || share_bytes(Y, d->table, table_bytes) || share_bytes(Y, d->pos, pos_bytes)) return IE_ERR_UNSUPPORTED;
+    if (!ws) return IE_ERR_WORKSPACE;
+    if (ws_bytes < rope_ws(X->rows, X->cols)) return IE_ERR_WORKSPACE;
+    hipStream_t st = (hipStream_t)stream;
+    if (X->rows == 0 || X->cols == 0) return hip_status(launch_fill_i8(Y->exp, n_exps(Y), E_MIN, st));
+    Carve c{(char *)ws, HEADER};
+    const bool eight = X->cols % 8 == 0 && d->head_dim % 8 == 0 && d->rot % 8 == 0 && aligned(X->mant, 8) && aligned(Y->mant, 8);
+    const RopePlan pl = rope_plan(X->rows, X->cols, eight);
+    RopeArgs a;
+    memset(&a, 0, sizeof a);
+    a.x = X->mant;
+    a.xe = X->exp;
+    a.x_row = X->group == IE_GROUP_ROW;
+    a.y = Y->mant;
+    a.ye = Y->exp;
+    a.rows = X->rows;
+    a.cols = (int)X->cols;
+    a.q = mat_q(Y);
+    a.d = d->head_dim;
+    a.rot = d->rot;
+    a.heads = d->heads;
+    a.interleaved = d->interleaved != 0;
+    a.inverse = d->inverse != 0;
+    a.table = (const int *)d->table;
+    a.positions = d->positions;
+    a.pos = d->pos;
+    a.bmax = carve_rope(c, X->rows, X->cols);
+    a.n_bmax = pl.grid;
+    a.flags = (uint32_t *)ws;
+    const bool y_row = Y->group == IE_GROUP_ROW || X->rows == 1;
+    a.mode = y_row ? NORM_ROWS : NORM_NEED;
+    IE_TRY(launch_rope(a, pl, st));
+    if (y_row) return IE_OK;
+    a.mode = NORM_ROUND;
+    return hip_status(launch_rope(a, pl, st));
+}
+
+static CacheArgs cache_args(const ie_cache *c, void *ws) {
+    CacheArgs a;
+    memset(&a, 0, sizeof a);
+    a.k = c->k;
+    a.v = c->v;
+    a.ke = c->k_exp;
+    a.ve = c->v_exp;
+    a.pages = c->pages;
+    a.page = c->page;
+    for (a.shift = 0; (1ll << a.shift) < c->page;) ++a.shift;
+    a.kv = c->kv_heads;
+    a.d = c->head_dim;
+    a.flags = (uint32_t *)ws;
+    return a;
+}
+
+// Whether a byte of m is one of the cache's.
+static bool share_cache(const ie_mat *m, const ie_cache *c) {
+    const size_t slots = (size_t)c->pages * c->page * c->kv_heads, bytes = slots * (c->head_dim / 2);
+    return share_bytes(m, c->k, bytes) || share_bytes(m, c->v, bytes) || share_bytes(m, c->k_exp, slots) ||
+           share_bytes(m, c->v_exp, slots);
+}
+
+ie_status ie_cache_store(const ie_cache *c, int32_t heads, const ie_mat *QKV, const int32_t *slots, void *ws, size_t ws_bytes,
+                         void *stream) {
+    IE_CHECK(check_cache(c));
+    IE_CHECK(check_mat(QKV));
+    if (heads < 0 || QKV->cols != (heads + 2ll * c->kv_heads) * c->head_dim) return IE_ERR_SHAPE;
+    if (QKV->rows > 0 && !slots) return IE_ERR_NULL;
+    if (!aligned(slots, 4) || share_cache(QKV, c)) return IE_ERR_UNSUPPORTED;
+    if (!ws || ws_bytes < HEADER) return IE_ERR_WORKSPACE;
+    if (QKV->rows == 0) return IE_OK;
+    return hip_status(launch_cache_store(cache_args(c, ws), QKV->rows, QKV->mant, QKV->exp, QKV->group == IE_GROUP_ROW,
+                                         (int)QKV->cols, heads * c->head_dim, slots, (hipStream_t)stream));
+}
+
+size_t ie_attention_cache_workspace(const ie_attention_desc *d, int64_t n, int64_t tokens) {
+    if (!d || n < 0 || tokens < 0 || d->heads < 1 || d->head_dim < 1 || d->head_dim > ATT_HEAD_MAX) return 0;
+    return attention_cache_ws(n, tokens, d->heads, d->head_dim);
+}
+
+ie_status ie_attention_cache(const ie_attention_desc *d, const ie_mat *Q, const ie_cache *c, const int32_t *pages, int32_t per,
+                             const int32_t *lengths, const ie_mat *O, void *ws, size_t ws_bytes, void *stream) {
+    if (!d) return IE_ERR_NULL;
+    IE_CHECK(check_cache(c));
+    const long long cols = (long long)d->heads * d->head_dim;
+    IE_CHECK(check_mat(Q));
+    IE_CHECK(check_attention(d, Q, Q->cols == cols ? cols : att_cols(d)));
+    IE_CHECK(check_mat(O));
+    if (c->kv_heads != d->kv_heads || c->head_dim != d->head_dim || per < 0 || O->rows != Q->rows || O->cols != cols || d->n_seq)
+        return IE_ERR_SHAPE;
+    if (Q->rows > 0 && (!lengths || (per > 0 && !pages))) return IE_ERR_NULL;
+    const long long tokens = (long long)per * c->page, units = d->kv_heads * ((d->heads / d->kv_heads + 15ll) / 16);
+    if (O->group != IE_GROUP_ROW || !aligned(lengths, 4) || !aligned(pages, 4) || tokens > CACHE_TOKENS_MAX ||
+        Q->rows * ((tokens + CACHE_BLOCK - 1) / CACHE_BLOCK + 8) * units > ATT_ITEMS_MAX || Q->rows * d->heads > ATT_ITEMS_MAX)
+        return IE_ERR_UNSUPPORTED;
+    if (share(O, Q) || share_cache(O, c) || share_bytes(O, lengths, (size_t)Q->rows * 4) ||
+        share_bytes(O, pages, (size_t)Q->rows * per * 4))
+        return IE_ERR_UNSUPPORTED;
+    if (!ws) return IE_ERR_WORKSPACE;
+    if (ws_bytes < attention_cache_ws(Q->rows, tokens, d->heads, d->head_dim)) return IE_ERR_WORKSPACE;
+    if (Q->rows == 0) return IE_OK;
+    Carve cv{(char *)ws, HEADER};
+    const CacheWs w = carve_attention_cache(cv, Q->rows, tokens, d->heads, d->head_dim);
+    AttnArgs a = att_args(d, Q, ws);
+    a.width = (int)Q->cols;
+    a.v16 = w.v16;
+    a.p16 = w.p16;
+    a.y = O->mant;
+    a.ye = O->exp;
+    a.cols = (int)cols;
+    a.parts = d->heads;
+    a.q = mat_q(O);
+    CacheArgs ca = cache_args(c, ws);
+    ca.table = pages;
+    ca.lengths = lengths;
+    ca.n = (int)Q->rows;
+    ca.per = per;
+    ca.tokens = (int)tokens;
+    ca.blocks = (int)((tokens + CACHE_BLOCK - 1) / CACHE_BLOCK);
+    ca.num = w.num;
+    ca.top = (int4 *)w.top;
+    ca.count = w.count;
+    return hip_status(launch_cache_attention(ca, a, (hipStream_t)stream));
 }
 
 size_t ie_bmm_workspace(int32_t batch, int64_t M, int64_t N, int64_t K) {

@@ -365,6 +365,41 @@ hipError_t launch_attention_fwd(const AttnArgs &a, hipStream_t st);
 // The rounding of v16, p16 into y by rows.
 hipError_t launch_attention_round(const AttnArgs &a, hipStream_t st);
 
+// Rotary positions (ie_rope.hip); mode as for layer norm.
+struct RopeArgs {
+    const int8_t *x, *xe;
+    int x_row;
+    int8_t *y, *ye;
+    long long rows;
+    int cols, q, mode;
+    int d, rot, heads, interleaved, inverse;
+    const int *table;  // [positions][rot / 2] pairs
+    long long positions;
+    const int *pos;    // [rows], or nullptr: the row's number
+    int *bmax;
+    int n_bmax;
+    uint32_t *flags;
+};
+hipError_t launch_rope(const RopeArgs &a, const RopePlan &pl, hipStream_t st);
+hipError_t launch_rope_table(const double *freqs, int half, long long positions, int16_t *table, hipStream_t st);
+
+// A paged cache of 4-bit mantissas (ie_cache.hip) and, for attention over it,
+// the sequences' pages and lengths and the blocks' sums.
+struct CacheArgs {
+    uint8_t *k, *v;
+    int8_t *ke, *ve;
+    int pages, page, shift, kv, d;
+    const int *table, *lengths;  // [n][per], [n]
+    int n, per, tokens, blocks;  // tokens: per pages; blocks of CACHE_BLOCK in them
+    int *num;                    // [n][blocks][heads][d]
+    int4 *top;                   // [n][blocks][heads]: maximum, sum, exponent
+    int *count;                  // [n]: heads that are done
+    uint32_t *flags;
+};
+hipError_t launch_cache_store(const CacheArgs &c, long long rows, const int8_t *x, const int8_t *xe, int x_row, int width,
+                              int first, const int *slots, hipStream_t st);
+hipError_t launch_cache_attention(const CacheArgs &c, const AttnArgs &a, hipStream_t st);
+
 // Product with bias and residual (ie_gemm_add.hip): rows m at exponent
 // xe, columns n at we, the result in this pass (y, ye) or as round-to-odd
 // values (v16, rows add_pitch(N) apart) with the tiles' needs (p16) for

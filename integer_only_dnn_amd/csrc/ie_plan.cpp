@@ -853,6 +853,56 @@ size_t attention_fwd_ws(long long rows, long long heads, long long d) {
     return align256(c.off);
 }
 
+RopePlan rope_plan(long long rows, long long cols, bool eight) {
+    RopePlan p{256, 0, 1};
+    if (eight) {
+        const long long units = cols / 8;
+#define IE_TRY_(T_, N_)                                                                       \
+    if (units <= (long long)T_ * N_ && (p.nu == 0 || T_ * N_ < p.t * p.nu)) p = RopePlan{T_, N_, 1};
+        IE_ROPE_SHAPES(IE_TRY_)
+#undef IE_TRY_
+    }
+    const long long rpb = p.nu ? 256 / p.t : 1, want = (rows + rpb - 1) / rpb;
+    p.grid = (int)(want < 1 ? 1 : want > ROPE_BLOCKS ? ROPE_BLOCKS : want);
+    return p;
+}
+
+int *carve_rope(Carve &c, long long, long long) { return c.take<int>(ROPE_BLOCKS); }
+
+size_t rope_ws(long long rows, long long cols) {
+    Carve c{nullptr, HEADER};
+    carve_rope(c, rows, cols);
+    return align256(c.off);
+}
+
+CacheWs carve_attention_cache(Carve &c, long long n, long long tokens, long long heads, long long d) {
+    const size_t blocks = (size_t)((tokens + CACHE_BLOCK - 1) / CACHE_BLOCK);
+    CacheWs w;
+    w.num = c.take<int>((size_t)n * blocks * (size_t)(heads * d));
+    w.top = c.take<char>((size_t)n * blocks * (size_t)heads * 16);
+    w.count = c.take<int>((size_t)n);
+    w.v16 = c.take<int16_t>((size_t)n * (size_t)(heads * d));
+    w.p16 = c.take<int16_t>((size_t)n * (size_t)heads);
+    return w;
+}
+
+size_t attention_cache_ws(long long n, long long tokens, long long heads, long long d) {
+    Carve c{nullptr, HEADER};
+    carve_attention_cache(c, n, tokens, heads, d);
+    return align256(c.off);
+}
+
+ie_status check_cache(const ie_cache *c) {
+    if (!c) return IE_ERR_NULL;
+    if (c->pages < 0 || c->page < 1 || c->kv_heads < 1 || c->head_dim < 1) return IE_ERR_SHAPE;
+    if (c->pages > 0 && (!c->k || !c->v || !c->k_exp || !c->v_exp)) return IE_ERR_NULL;
+    if ((c->page & (c->page - 1)) || c->head_dim % 16 || c->head_dim > ATT_HEAD_MAX ||
+        (long long)c->pages * c->page > DIM_MAX || c->kv_heads > (1 << 16))
+        return IE_ERR_UNSUPPORTED;
+    if (((uintptr_t)c->k | (uintptr_t)c->v) % 8) return IE_ERR_UNSUPPORTED;
+    return IE_OK;
+}
+
 // The heads of an attention call and the matrix that holds them.
 ie_status check_attention(const ie_attention_desc *d, const ie_mat *X, long long cols) {
     if (!d) return IE_ERR_NULL;

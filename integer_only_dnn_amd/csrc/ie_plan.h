@@ -447,6 +447,33 @@ struct AttFwdWs {
 };
 AttFwdWs carve_attention_fwd(Carve &c, long long rows, long long heads, long long d);
 size_t attention_fwd_ws(long long rows, long long heads, long long d);
+// Rotary positions: t threads per row with nu runs of eight elements each (nu
+// = 0: rows that do not come in such runs, or too long to be held).
+struct RopePlan {
+    int t, nu, grid;
+};
+#define IE_ROPE_SHAPES(X)                                                                                    \
+    X(16, 1) X(16, 2) X(16, 4) X(16, 6) X(64, 2) X(64, 3) X(64, 4) X(64, 5) X(64, 6) X(64, 8) X(256, 3)      \
+    X(256, 4) X(256, 6) X(256, 8)
+constexpr int ROPE_BLOCKS = 2048;
+// eight: rows, heads and what is rotated of them come in runs of eight.
+RopePlan rope_plan(long long rows, long long cols, bool eight);
+int *carve_rope(Carve &c, long long rows, long long cols);  // block maxima
+size_t rope_ws(long long rows, long long cols);
+
+// Attention over a cache: blocks of keys with a maximum of their own.
+constexpr int CACHE_BLOCK = 256;
+constexpr long long CACHE_TOKENS_MAX = 1ll << 23;  // sums of weighted blocks stay below 2^53
+struct CacheWs {
+    int *num;
+    void *top;  // 16 bytes a block and head
+    int *count;
+    int16_t *v16, *p16;
+};
+CacheWs carve_attention_cache(Carve &c, long long n, long long tokens, long long heads, long long d);
+size_t attention_cache_ws(long long n, long long tokens, long long heads, long long d);
+ie_status check_cache(const ie_cache *c);
+
 ie_status check_attention(const ie_attention_desc *d, const ie_mat *X, long long cols);
 
 // Whether a parameter vector of n channels is [n x 1] or [1 x n].

@@ -1,0 +1,238 @@
+// Rotary positions on the rows of (C, e) matrices, and the table of cosines
+// and sines they read.
+//
+// A pair (a, b) of a head's mantissas becomes (a c - b s, a s + b c), c and s
+// whole numbers in units of 2^-14; what is not rotated is taken 2^14 times.
+// So a row is whole numbers below 2^23 at exponent e - 14, exact in fp32, and
+// rounded once, at the row's (or the whole tensor's) exponent.  The inverse
+// rotation, which is also the gradient, has -s for s.
+//
+// Bound by the stream over X and Y.
+#include "ie_f64.h"
+#include "ie_internal.h"
+
+#pragma clang fp contract(off)
+
+namespace ie {
+
+constexpr float ROPE_MAGIC = 12582912.0f;  // 1.5 * 2^23
+
+// Row t of the table: (cos, sin) of t f_k for the k-th pair, in 64 bits up to
+// the rounding: at position 10^5 a 32-bit angle would be off by 2^-8.
+struct RopeFreqs {
+    double f[IE_ROPE_MAX / 2];
+};
+__global__ __launch_bounds__(256) void rope_table_kernel(RopeFreqs fr, int half, long long positions, int *table) {
+    const long long n = positions * half;
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
+        const long long t = i / half;
+        double s, c;
+        sincos((double)t * fr.f[i - t * half], &s, &c);
+        const int ci = (int)rint(c * 16384.0), si = (int)rint(s * 16384.0);
+        table[i] = (ci & 0xffff) | si << 16;
+    }
+}
+
+// Eight neighbours of a row (or, for the two-halves layout, two runs of four)
+// as the numbers they become.
+struct RopeUnit {
+    int at[2];  // first column of each run of four
+    int k;      // first pair of four, or -1: not rotated
+};
+__device__ __forceinline__ RopeUnit rope_unit(const RopeArgs &p, int u) {
+    const int per = p.d >> 3, head = u / per, k = u - head * per, c0 = head * p.d;
+    RopeUnit r;
+    const bool on = head < p.heads && 8 * k < p.rot;
+    r.k = on ? 4 * k : -1;
+    if (on && !p.interleaved) {
+        r.at[0] = c0 + 4 * k;
+        r.at[1] = c0 + (p.rot >> 1) + 4 * k;
+    } else {
+        r.at[0] = c0 + 8 * k;
+        r.at[1] = c0 + 8 * k + 4;
+    }
+    return r;
+}
+__device__ __forceinline__ void rope8(const RopeArgs &p, const RopeUnit &u, uint32_t lo, uint32_t hi, const int4 &t, float sign,
+                                      float (&y)[8]) {
+    if (u.k < 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            y[i] = 16384.0f * (float)byte_of(lo, i);
+            y[4 + i] = 16384.0f * (float)byte_of(hi, i);
+        }
+        return;
+    }
+    const int w[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float c = (float)(int16_t)w[i], s = sign * (float)(w[i] >> 16);
+        const int ia = p.interleaved ? 2 * i : i, ib = p.interleaved ? 2 * i + 1 : 4 + i;
+        const float a = (float)byte_of(ia < 4 ? lo : hi, ia & 3), b = (float)byte_of(ib < 4 ? lo : hi, ib & 3);
+        y[ia] = a * c - b * s;
+        y[ib] = a * s + b * c;
+    }
+}
+
+__device__ __forceinline__ int rope_position(const RopeArgs &p, long long row, bool tell) {
+    const long long t = p.pos ? (long long)p.pos[row] : row;
+    if (t >= 0 && t < p.positions) return (int)t;
+    if (tell) atomicOr(p.flags, IE_FLAG_INDEX);
+    return 0;
+}
+
+// T threads per row, NU units each.
+template <int T, int NU>
+__global__ __launch_bounds__(256) void rope_kernel(RopeArgs p) {
+    constexpr int RPB = 256 / T;
+    __shared__ int sh[4];
+    const int t = threadIdx.x % T, slot = threadIdx.x / T, units = p.cols >> 3;
+    const float sign = p.inverse ? -1.0f : 1.0f;
+    int run = NEED_NONE;
+    int whole = 0;
+    if (p.mode == NORM_ROUND) {
+        int m = NEED_NONE;
+        for (int i = threadIdx.x; i < p.n_bmax; i += 256) m = max(m, p.bmax[i]);
+        whole = clamp_exp_flag(max(E_MIN, row_reduce<256>(m, Max{}, sh)), p.flags);
+        if (blockIdx.x == 0 && threadIdx.x == 0) p.ye[0] = (int8_t)whole;
+    }
+    for (long long r0 = (long long)blockIdx.x * RPB; r0 < p.rows; r0 += (long long)gridDim.x * RPB) {
+        const bool ok = r0 + slot < p.rows;
+        const long long row = ok ? r0 + slot : p.rows - 1;
+        const int ex = p.xe[p.x_row ? row : 0] - 14;
+        const int *tab = p.table + (long long)rope_position(p, row, ok && t == 0 && p.mode != NORM_ROUND) * (p.rot >> 1);
+        const int8_t *x = p.x + row * p.cols;
+        float y[NU][8];
+        float big = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NU; ++i) {
+            const int u = t + T * i;
+            if (u < units) {
+                const RopeUnit a = rope_unit(p, u);
+                const uint32_t lo = *(const uint32_t *)(x + a.at[0]), hi = *(const uint32_t *)(x + a.at[1]);
+                const int4 w = a.k >= 0 ? *(const int4 *)(tab + a.k) : int4{0, 0, 0, 0};
+                rope8(p, a, lo, hi, w, sign, y[i]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) y[i][k] = 0.0f;
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) big = fmaxf(big, fabsf(y[i][k]));
+        }
+        int e = whole;
+        if (p.mode != NORM_ROUND) {
+            const int m = row_reduce<T>((int)big, Max{}, sh);
+            const int need = need32(m, ex, p.q);
+            if (p.mode == NORM_NEED) {
+                run = max(run, need);
+                continue;
+            }
+            e = max(E_MIN, need);
+            if (ok && t == 0) {
+                e = clamp_exp_flag(e, p.flags);
+                p.ye[row] = (int8_t)e;
+            }
+            e = min(e, E_MAX);
+        }
+        if (!ok) continue;
+        const float inv = __int_as_float((127 + min(max(ex - e, -100), 100)) << 23);
+        int8_t *out = p.y + row * p.cols;
+#pragma unroll
+        for (int i = 0; i < NU; ++i) {
+            const int u = t + T * i;
+            if (u >= units) continue;
+            const RopeUnit a = rope_unit(p, u);
+            int o[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[k] = __float_as_int(__builtin_fmaf(y[i][k], inv, ROPE_MAGIC));
+            *(uint32_t *)(out + a.at[0]) = pack4(o[0], o[1], o[2], o[3]);
+            *(uint32_t *)(out + a.at[1]) = pack4(o[4], o[5], o[6], o[7]);
+        }
+    }
+    if (p.mode == NORM_NEED) {
+        run = row_reduce<256>(run, Max{}, sh);
+        if (threadIdx.x == 0) p.bmax[blockIdx.x] = run;
+    }
+}
+
+// Element c of a row, for heads whose pairs do not come in runs of four.
+__device__ __forceinline__ float rope1(const RopeArgs &p, const int8_t *x, const int *tab, int c, float sign) {
+    const int head = c / p.d, j = c - head * p.d, half = p.rot >> 1;
+    if (head >= p.heads || j >= p.rot) return 16384.0f * (float)x[c];
+    const int k = p.interleaved ? j >> 1 : j < half ? j : j - half;
+    const bool second = p.interleaved ? j & 1 : j >= half;
+    const int step = p.interleaved ? 1 : half;
+    const float co = (float)(int16_t)tab[k], si = sign * (float)(tab[k] >> 16);
+    return second ? (float)x[c - step] * si + (float)x[c] * co : (float)x[c] * co - (float)x[c + step] * si;
+}
+
+// The same for any head size, alignment and length: a block per row, which it
+// walks twice.
+__global__ __launch_bounds__(256) void rope_any_kernel(RopeArgs p) {
+    __shared__ int sh[4];
+    const float sign = p.inverse ? -1.0f : 1.0f;
+    int run = NEED_NONE, e = 0;
+    if (p.mode == NORM_ROUND) {
+        int m = NEED_NONE;
+        for (int i = threadIdx.x; i < p.n_bmax; i += 256) m = max(m, p.bmax[i]);
+        e = clamp_exp_flag(max(E_MIN, row_reduce<256>(m, Max{}, sh)), p.flags);
+        if (blockIdx.x == 0 && threadIdx.x == 0) p.ye[0] = (int8_t)e;
+    }
+    for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        const int ex = p.xe[p.x_row ? row : 0] - 14;
+        const int *tab = p.table + (long long)rope_position(p, row, threadIdx.x == 0 && p.mode != NORM_ROUND) * (p.rot >> 1);
+        const int8_t *x = p.x + row * p.cols;
+        int8_t *out = p.y + row * p.cols;
+        if (p.mode != NORM_ROUND) {
+            float big = 0.0f;
+            for (int c = threadIdx.x; c < p.cols; c += 256) big = fmaxf(big, fabsf(rope1(p, x, tab, c, sign)));
+            const int need = need32(row_reduce<256>((int)big, Max{}, sh), ex, p.q);
+            if (p.mode == NORM_NEED) {
+                run = max(run, need);
+                continue;
+            }
+            e = max(E_MIN, need);
+            if (threadIdx.x == 0) {
+                e = clamp_exp_flag(e, p.flags);
+                p.ye[row] = (int8_t)e;
+            }
+            e = min(e, E_MAX);
+        }
+        const float inv = __int_as_float((127 + min(max(ex - e, -100), 100)) << 23);
+        for (int c = threadIdx.x; c < p.cols; c += 256)
+            out[c] = (int8_t)__float_as_int(__builtin_fmaf(rope1(p, x, tab, c, sign), inv, ROPE_MAGIC));
+    }
+    if (p.mode == NORM_NEED && threadIdx.x == 0) p.bmax[blockIdx.x] = run;
+}
+
+hipError_t launch_rope_table(const double *freqs, int half, long long positions, int16_t *table, hipStream_t st) {
+    RopeFreqs f;
+    for (int k = 0; k < half; ++k) f.f[k] = freqs[k];
+    const long long blocks = (positions * half + 255) / 256;
+    prof_begin(st, PROF_ROPE);
+    hipLaunchKernelGGL(rope_table_kernel, dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, st, f, half, positions,
+                       (int *)table);
+    prof_end(st, PROF_ROPE);
+    return hipGetLastError();
+}
+
+hipError_t launch_rope(const RopeArgs &a, const RopePlan &pl, hipStream_t st) {
+    prof_begin(st, PROF_ROPE);
+    const dim3 grid((unsigned)pl.grid), block(256);
+    bool done = false;
+    if (pl.nu == 0) {
+        hipLaunchKernelGGL(rope_any_kernel, grid, block, 0, st, a);
+        done = true;
+    }
+#define IE_CASE(T_, N_)                                                               \
+    if (pl.t == T_ && pl.nu == N_) {                                                  \
+        hipLaunchKernelGGL((rope_kernel<T_, N_>), grid, block, 0, st, a);             \
+        done = true;                                                                  \
+    }
+    IE_ROPE_SHAPES(IE_CASE)
+#undef IE_CASE
+    prof_end(st, PROF_ROPE);
+    return done ? hipGetLastError() : hipErrorInvalidValue;
+}
+
+}  // namespace ie

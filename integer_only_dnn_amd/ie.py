@@ -18,6 +18,7 @@ import torch
 TENSOR = 0
 ROW = 1
 FLAG_EXP_RANGE = 1
+FLAG_INDEX = 2
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libie.so")
@@ -52,6 +53,20 @@ class ie_dropout_desc(ctypes.Structure):
 class ie_attention_desc(ctypes.Structure):
     _fields_ = [("heads", c_int32), ("kv_heads", c_int32), ("head_dim", c_int32), ("causal", c_int32),
                 ("scale", ctypes.c_float), ("n_seq", c_int32), ("offsets", c_void_p)]
+
+
+class ie_rope_freqs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ("base", "factor", "trained", "low", "high")]
+
+
+class ie_rope_desc(ctypes.Structure):
+    _fields_ = [("table", c_void_p), ("positions", c_int64), ("pos", c_void_p), ("heads", c_int32), ("head_dim", c_int32),
+                ("rot", c_int32), ("interleaved", c_int32), ("inverse", c_int32)]
+
+
+class ie_cache(ctypes.Structure):
+    _fields_ = [("k", c_void_p), ("v", c_void_p), ("k_exp", c_void_p), ("v_exp", c_void_p), ("pages", c_int32),
+                ("page", c_int32), ("kv_heads", c_int32), ("head_dim", c_int32)]
 
 
 EXPORTS = [
@@ -98,6 +113,15 @@ EXPORTS = [
     ("ie_attention_fwd_workspace", c_size_t, [POINTER(ie_attention_desc), c_int64]),
     ("ie_attention_fwd", c_int,
      [POINTER(ie_attention_desc)] + [POINTER(ie_mat)] * 2 + [c_void_p, c_void_p, c_size_t, c_void_p]),
+    ("ie_rope_table", c_int, [POINTER(ie_rope_freqs), c_int32, c_int64, c_void_p, c_void_p]),
+    ("ie_rope_workspace", c_size_t, [c_int64, c_int64]),
+    ("ie_rope", c_int, [POINTER(ie_rope_desc)] + [POINTER(ie_mat)] * 2 + [c_void_p, c_size_t, c_void_p]),
+    ("ie_cache_store", c_int,
+     [POINTER(ie_cache), c_int32, POINTER(ie_mat), c_void_p, c_void_p, c_size_t, c_void_p]),
+    ("ie_attention_cache_workspace", c_size_t, [POINTER(ie_attention_desc), c_int64, c_int64]),
+    ("ie_attention_cache", c_int,
+     [POINTER(ie_attention_desc), POINTER(ie_mat), POINTER(ie_cache), c_void_p, c_int32, c_void_p, POINTER(ie_mat),
+      c_void_p, c_size_t, c_void_p]),
     ("ie_device_status", c_int, [c_void_p, c_void_p, POINTER(c_uint32), c_int]),
     ("ie_profile_enable", c_int, [c_int]),
     ("ie_profile_select", c_int, [c_int]),
@@ -522,6 +546,78 @@ def ie_attention_fwd(att: Attention, QKV: Mat, O: Mat, ws: Workspace, stats: tor
     p, b = ws.get(att._bytes("ie_attention_fwd_workspace", x.rows))
     _check(lib().ie_attention_fwd(byref(att.desc), byref(x), byref(o), sp, p, b, _stream(ws.device)),
            "ie_attention_fwd")
+
+
+class Rope:
+    """A table of angles for ie_rope: `positions` rows for the first `rot`
+    elements of heads of head_dim, f_k = base^(-2 k / rot), for contexts `factor`
+    times the trained length scaled in all (trained = 0) or by parts."""
+
+    def __init__(self, head_dim: int, rot: int, positions: int, interleaved: bool = False, base: float = 10000.0,
+                 factor: float = 1.0, trained: float = 0.0, low: float = 1.0, high: float = 4.0, device="cuda"):
+        self.head_dim, self.rot, self.positions, self.interleaved = head_dim, rot, positions, interleaved
+        self.table = torch.empty((positions, max(rot // 2, 1), 2), dtype=torch.int16, device=device)
+        f = ie_rope_freqs(base, factor, trained, low, high)
+        _check(lib().ie_rope_table(byref(f), rot, positions, self.table.data_ptr(), _stream(self.table.device)),
+               "ie_rope_table")
+
+
+def ie_rope(rope: Rope, X: Mat, pos: torch.Tensor | None, Y: Mat, heads: int, ws: Workspace, inverse: bool = False) -> None:
+    """Y = X with the first `heads` heads of every row turned to the row's
+    position (int32 device tensor `pos`; None: the row's number), or back."""
+    x, y = X.c(), Y.c()
+    at = None if pos is None else _device_array(pos, torch.int32, "pos", x.rows)
+    d = ie_rope_desc(rope.table.data_ptr(), rope.positions, at, heads, rope.head_dim, rope.rot, int(rope.interleaved),
+                     int(inverse))
+    p, b = ws.get(_ws_rows("ie_rope_workspace", x.rows, x.cols))
+    _check(lib().ie_rope(byref(d), byref(x), byref(y), p, b, _stream(ws.device)), "ie_rope")
+
+
+class Cache:
+    """Keys and values with mantissas of 4 bits: k, v uint8 [pages, page,
+    kv_heads, head_dim / 2], their exponents int8 [pages, page, kv_heads]."""
+
+    def __init__(self, k: torch.Tensor, k_exp: torch.Tensor, v: torch.Tensor, v_exp: torch.Tensor):
+        if k.dim() != 4 or v.shape != k.shape or k_exp.shape != k.shape[:3] or v_exp.shape != k.shape[:3]:
+            raise ValueError("k and v are [pages, page, kv_heads, head_dim / 2], their exponents [pages, page, kv_heads]")
+        self.k, self.k_exp, self.v, self.v_exp = k, k_exp, v, v_exp
+        at = [_device_array(t, torch.uint8 if i % 2 == 0 else torch.int8, "a cache's part")
+              for i, t in enumerate((k, k_exp, v, v_exp))]
+        pages, page, kv, half = k.shape
+        self.desc = ie_cache(at[0], at[2], at[1], at[3], pages, page, kv, 2 * half)
+
+    @staticmethod
+    def empty(pages: int, page: int, kv_heads: int, head_dim: int, device="cuda") -> "Cache":
+        k, v = (torch.zeros((pages, page, kv_heads, head_dim // 2), dtype=torch.uint8, device=device) for _ in range(2))
+        e, f = (torch.full((pages, page, kv_heads), -128, dtype=torch.int8, device=device) for _ in range(2))
+        return Cache(k, e, v, f)
+
+
+def ie_cache_store(cache: Cache, QKV: Mat, heads: int, slots: torch.Tensor, ws: Workspace) -> None:
+    """The keys and values of QKV's rows into the slots (int32 device tensor) they name; negative ones are left out."""
+    x = QKV.c()
+    at = _device_array(slots, torch.int32, "slots", x.rows)
+    p, b = ws.get(256)
+    _check(lib().ie_cache_store(byref(cache.desc), heads, byref(x), at, p, b, _stream(ws.device)), "ie_cache_store")
+
+
+def ie_attention_cache(att: Attention, Q: Mat, cache: Cache, pages: torch.Tensor, lengths: torch.Tensor, O: Mat,
+                       ws: Workspace) -> None:
+    """O = attention of every row of Q over the cached keys of its sequence:
+    pages int32 [rows, per], lengths int32 [rows], both on the device."""
+    q, o = Q.c(), O.c()
+    n = q.rows
+    if pages.dim() != 2 or pages.shape[0] < n:
+        raise ValueError("pages is [rows, pages of a sequence]")
+    per = pages.shape[1]
+    tp, lp = _device_array(pages, torch.int32, "pages"), _device_array(lengths, torch.int32, "lengths", n)
+    tokens = per * cache.desc.page
+    size = att._sizes.get((n, tokens))
+    if size is None:
+        size = att._sizes[(n, tokens)] = lib().ie_attention_cache_workspace(byref(att.desc), n, tokens)
+    p, b = ws.get(size)
+    _check(lib().ie_attention_cache(byref(att.desc), byref(q), byref(cache.desc), tp, per, lp, byref(o), p, b,
+                                    _stream(ws.device)), "ie_attention_cache")
 
 
 def ie_profile_enable(on: bool = True) -> None:
