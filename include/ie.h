@@ -444,7 +444,7 @@ ie_status ie_dropout(const ie_mat *X, const ie_mat *R, const ie_mat *Y, const ie
  * stats: for the backward pass, 8 bytes for every row and head (a device array
  * [rows x heads], 8-byte aligned): m and L; NULL where none follows.
  * Limits (IE_ERR_UNSUPPORTED): head_dim <= 128, 2^-30 <= scale <= 2^30.
- * Offsets that decrease or leave the matrix, and sequences of more than 131072
+ * Offsets that decrease or leave the matrix, and sequences of more than 131071
  * tokens, set IE_FLAG_INDEX: the rows they name are undefined, no others.
  */
 typedef struct {
@@ -457,6 +457,37 @@ typedef struct {
 size_t ie_attention_fwd_workspace(const ie_attention_desc *d, int64_t rows);
 ie_status ie_attention_fwd(const ie_attention_desc *d, const ie_mat *QKV, const ie_mat *O, void *stats, void *ws,
                            size_t ws_bytes, void *stream);
+
+/*
+ * Gradient of ie_attention_fwd: dQKV from QKV, the pass's result O and its
+ * stats, and dO.  d, QKV as there; O ROW; dO [rows x heads * head_dim], TENSOR
+ * or ROW; dQKV [rows x (heads + 2 kv_heads) * head_dim] must be ROW (else
+ * IE_ERR_UNSUPPORTED): one exponent for a token's gradients of queries, keys and
+ * values, so that it goes into ie_linear_bwd_dx and ie_linear_bwd_dw as it is.
+ * Rows of no sequence are left as they were.
+ * Arithmetic: with w_ij, L_i of the forward pass and eo_i the exponents of dO
+ * (O's are read clipped as QKV's are),
+ *   u = (dO_i . v_j) 2^(e_j) - (dO_i . O_i) 2^(eO_i), rounded to fp32, s = w u too;
+ *   dQ_i = scale / L_i 2^(eo_i + sigma) sum_j R(s 2^(e_j - sigma)) k_j;
+ *   a_i = 1 / L_i rounded to fp32, times 2^max(eo_i - max eo, -60);
+ *   dV_j = 2^(kappa + max eo) sum_i R((w a_i) 2^(-kappa)) dO_i;
+ *   dK_j = scale 2^(lambda + G - 6 + max eo) sum_i R((s b_i) 2^(6 - lambda)) q_i,
+ *   b_i = a_i 2^(e_i - G) rounded to fp32,
+ * products rounded to fp32, sums over a sequence and, for keys, over the query
+ * heads that share them, exact, the products behind them rounded to 53 bits.
+ * The powers of two come from bounds: with |x| < 2^[x], [x] half the bits of
+ * sum x^2, rounded up, bits n of a whole number, and maxima over a sequence
+ *   nu_j = [v_j] + e_j,  delta_i = bits |dO_i . O_i| + eO_i,
+ *   sigma_i = max([dO_i] + max(nu_j + e_j), delta_i + max e_j) + 1,
+ *   kappa_j = max alpha_i,  lambda_j = max(l_i - G, -96) over the queries (and
+ *   heads) that see j, a_i < 2^(alpha_i) (the smallest), l_i = alpha_i + e_i +
+ *   max([dO_i] + max nu_j, delta_i) + 1, G = max l_i.
+ * Limits as for the forward pass; a sequence's tokens times heads / kv_heads at
+ * most 131071 (else IE_FLAG_INDEX, as there).
+ */
+size_t ie_attention_bwd_workspace(const ie_attention_desc *d, int64_t rows);
+ie_status ie_attention_bwd(const ie_attention_desc *d, const ie_mat *QKV, const ie_mat *O, const ie_mat *dO, const void *stats,
+                           const ie_mat *dQKV, void *ws, size_t ws_bytes, void *stream);
 
 /*
  * Rotary positions: Y = R_Y(X with the pairs of its heads turned).  X, Y

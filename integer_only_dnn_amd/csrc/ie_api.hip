@@ -1297,6 +1297,57 @@ ie_status ie_attention_fwd(const ie_attention_desc *d, const ie_mat *QKV, const 
     return hip_status(launch_attention_fwd(a, (hipStream_t)stream));
 }
 
+size_t ie_attention_bwd_workspace(const ie_attention_desc *d, int64_t rows) {
+    if (!d || rows < 0 || d->heads < 1 || d->kv_heads < 1 || d->head_dim < 1 || d->head_dim > ATT_HEAD_MAX) return 0;
+    return attention_bwd_ws(rows, d->heads, d->kv_heads, d->head_dim);
+}
+
+ie_status ie_attention_bwd(const ie_attention_desc *d, const ie_mat *QKV, const ie_mat *O, const ie_mat *dO, const void *stats,
+                           const ie_mat *dQKV, void *ws, size_t ws_bytes, void *stream) {
+    if (!d) return IE_ERR_NULL;
+    IE_CHECK(check_attention(d, QKV, att_cols(d)));
+    IE_CHECK(check_mat(O));
+    IE_CHECK(check_mat(dO));
+    IE_CHECK(check_mat(dQKV));
+    if (O->rows != QKV->rows || O->cols != (long long)d->heads * d->head_dim || !same_shape(O, dO) || !same_shape(QKV, dQKV))
+        return IE_ERR_SHAPE;
+    if (QKV->rows > 0 && !stats) return IE_ERR_NULL;
+    if (O->group != IE_GROUP_ROW || dQKV->group != IE_GROUP_ROW || !aligned(stats, 8) || d->heads / d->kv_heads > ATT_MOST)
+        return IE_ERR_UNSUPPORTED;
+    if (share(dQKV, QKV) || share(dQKV, O) || share(dQKV, dO) || share_bytes(dQKV, stats, (size_t)O->rows * d->heads * 8) ||
+        share_bytes(dQKV, d->offsets, ((size_t)d->n_seq + 1) * 4))
+        return IE_ERR_UNSUPPORTED;
+    if (!ws) return IE_ERR_WORKSPACE;
+    if (ws_bytes < attention_bwd_ws(QKV->rows, d->heads, d->kv_heads, d->head_dim)) return IE_ERR_WORKSPACE;
+    if (QKV->rows == 0) return IE_OK;
+    AttnArgs a = att_args(d, QKV, ws);
+    Carve c{(char *)ws, HEADER};
+    const AttBwdWs w = carve_attention_bwd(c, QKV->rows, d->heads, d->kv_heads, d->head_dim);
+    a.most = ATT_MOST / a.group;
+    a.stats = (int2 *)stats;
+    a.v16 = w.v16;
+    a.p16 = w.p16;
+    a.y = dQKV->mant;
+    a.ye = dQKV->exp;
+    a.cols = (int)dQKV->cols;
+    a.parts = d->heads + 2 * d->kv_heads;
+    a.q = mat_q(dQKV);
+    a.out_vec = d->head_dim % 16 == 0 && aligned(dQKV->mant, 8);
+    AttnBwd b;
+    memset(&b, 0, sizeof b);
+    b.o = O->mant;
+    b.oe = O->exp;
+    b.dy = dO->mant;
+    b.dye = dO->exp;
+    b.dy_row = dO->group == IE_GROUP_ROW && dO->rows > 1;
+    b.dy_vec = d->head_dim % 16 == 0 && aligned(dO->mant, 16);
+    b.dots = (int2 *)w.dots;
+    b.norm = w.norm;
+    b.row = (AttnRow *)w.row;
+    b.key = (AttnKey *)w.key;
+    return hip_status(launch_attention_bwd(a, b, (hipStream_t)stream));
+}
+
 ie_status ie_rope_table(const ie_rope_freqs *f, int32_t rot, int64_t positions, int16_t *table, void *stream) {
     if (!f) return IE_ERR_NULL;
     if (rot < 0 || positions < 0) return IE_ERR_SHAPE;

@@ -65,6 +65,16 @@ __device__ __forceinline__ void digits4(int a, int b, int c, int d, int &hi, int
     hi = (int)__builtin_amdgcn_perm(t, s, 0x07060302u);
 }
 
+// Three digits of four n + 0x8080 + 2^22 in the low 23 bits, |n| < 2^21: high
+// ones 64 too large, middle and low ones.
+__device__ __forceinline__ void digits3x4(int a, int b, int c, int d, int &hi, int &mid, int &lo) {
+    digits4(a, b, c, d, mid, lo);
+    mid ^= (int)0x80808080u;
+    const uint32_t s = __builtin_amdgcn_perm((uint32_t)b, (uint32_t)a, 0x0c0c0602u);
+    const uint32_t t = __builtin_amdgcn_perm((uint32_t)d, (uint32_t)c, 0x0c0c0602u);
+    hi = (int)__builtin_amdgcn_perm(t, s, 0x05040100u);
+}
+
 __device__ __forceinline__ v16i mfma(v4i a, v4i b, v16i c) { return __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, c, 0, 0, 0); }
 
 __device__ __forceinline__ float half_max(float v) {

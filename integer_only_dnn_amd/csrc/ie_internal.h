@@ -365,6 +365,28 @@ hipError_t launch_attention_fwd(const AttnArgs &a, hipStream_t st);
 // The rounding of v16, p16 into y by rows.
 hipError_t launch_attention_round(const AttnArgs &a, hipStream_t st);
 
+// What the backward pass knows of a query row of a head and of a key (see
+// ie_attention_bwd.hip).
+struct AttnRow {
+    float m, r, dot, a, b, s;
+    int e;       // exponent of its units of dQ
+    uint32_t sum;
+};
+struct AttnKey {
+    int kappa, lambda;
+    int ev, ek;  // exponents of its units of dV and dK
+};
+struct AttnBwd {
+    const int8_t *o, *oe;
+    const int8_t *dy, *dye;
+    int dy_row, dy_vec;
+    int2 *dots;    // [rows][heads]: dO . O, bits of |dO|
+    int8_t *norm;  // [rows][kv]: bits of |v|
+    AttnRow *row;  // [heads][rows]
+    AttnKey *key;  // [kv][rows]
+};
+hipError_t launch_attention_bwd(const AttnArgs &a, const AttnBwd &b, hipStream_t st);
+
 // Rotary positions (ie_rope.hip); mode as for layer norm.
 struct RopeArgs {
     const int8_t *x, *xe;

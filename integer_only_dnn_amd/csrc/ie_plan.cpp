@@ -853,6 +853,23 @@ size_t attention_fwd_ws(long long rows, long long heads, long long d) {
     return align256(c.off);
 }
 
+AttBwdWs carve_attention_bwd(Carve &c, long long rows, long long heads, long long kv, long long d) {
+    AttBwdWs w;
+    w.v16 = c.take<int16_t>((size_t)(rows * (heads + 2 * kv) * d));
+    w.p16 = c.take<int16_t>((size_t)(rows * (heads + 2 * kv)));
+    w.dots = c.take<char>((size_t)(rows * heads * 8));
+    w.norm = c.take<int8_t>((size_t)(rows * kv));
+    w.row = c.take<char>((size_t)(rows * heads * 32));
+    w.key = c.take<char>((size_t)(rows * kv * 16));
+    return w;
+}
+
+size_t attention_bwd_ws(long long rows, long long heads, long long kv, long long d) {
+    Carve c{nullptr, HEADER};
+    carve_attention_bwd(c, rows, heads, kv, d);
+    return align256(c.off);
+}
+
 RopePlan rope_plan(long long rows, long long cols, bool eight) {
     RopePlan p{256, 0, 1};
     if (eight) {

@@ -438,7 +438,7 @@ int *carve_dropout(Carve &c, long long rows, long long cols);  // block maxima
 // Attention over packed sequences: tile slots of bm rows (a sequence's first
 // slot is off / bm plus its number), and the tokens of the longest sequence
 // whose int32 sums of digits (at most 127 * 128 each) stay exact.
-constexpr int ATT_MOST = 131072;
+constexpr int ATT_MOST = 131071;
 constexpr int ATT_HEAD_MAX = 128;
 constexpr long long ATT_ITEMS_MAX = 1ll << 30;  // workgroups of a launch
 inline long long att_slots(long long rows, long long n_seq, int bm) { return rows / bm + (n_seq > 0 ? n_seq : 1); }
@@ -446,6 +446,15 @@ struct AttFwdWs {
     int16_t *v16, *p16;  // round-to-odd results and the needs of their heads
 };
 AttFwdWs carve_attention_fwd(Carve &c, long long rows, long long heads, long long d);
+struct AttBwdWs {
+    int16_t *v16, *p16;
+    void *dots;    // 8 bytes a row and head
+    int8_t *norm;  // a row and key head
+    void *row;     // 32 bytes a row and head
+    void *key;     // 16 bytes a row and key head
+};
+AttBwdWs carve_attention_bwd(Carve &c, long long rows, long long heads, long long kv, long long d);
+size_t attention_bwd_ws(long long rows, long long heads, long long kv, long long d);
 size_t attention_fwd_ws(long long rows, long long heads, long long d);
 // Rotary positions: t threads per row with nu runs of eight elements each (nu
 // = 0: rows that do not come in such runs, or too long to be held).

@@ -113,6 +113,9 @@ EXPORTS = [
     ("ie_attention_fwd_workspace", c_size_t, [POINTER(ie_attention_desc), c_int64]),
     ("ie_attention_fwd", c_int,
      [POINTER(ie_attention_desc)] + [POINTER(ie_mat)] * 2 + [c_void_p, c_void_p, c_size_t, c_void_p]),
+    ("ie_attention_bwd_workspace", c_size_t, [POINTER(ie_attention_desc), c_int64]),
+    ("ie_attention_bwd", c_int,
+     [POINTER(ie_attention_desc)] + [POINTER(ie_mat)] * 3 + [c_void_p, POINTER(ie_mat), c_void_p, c_size_t, c_void_p]),
     ("ie_rope_table", c_int, [POINTER(ie_rope_freqs), c_int32, c_int64, c_void_p, c_void_p]),
     ("ie_rope_workspace", c_size_t, [c_int64, c_int64]),
     ("ie_rope", c_int, [POINTER(ie_rope_desc)] + [POINTER(ie_mat)] * 2 + [c_void_p, c_size_t, c_void_p]),
@@ -546,6 +549,15 @@ def ie_attention_fwd(att: Attention, QKV: Mat, O: Mat, ws: Workspace, stats: tor
     p, b = ws.get(att._bytes("ie_attention_fwd_workspace", x.rows))
     _check(lib().ie_attention_fwd(byref(att.desc), byref(x), byref(o), sp, p, b, _stream(ws.device)),
            "ie_attention_fwd")
+
+
+def ie_attention_bwd(att: Attention, QKV: Mat, O: Mat, dO: Mat, stats: torch.Tensor, dQKV: Mat, ws: Workspace) -> None:
+    """The gradient of ie_attention_fwd's QKV from its result, its stats and dO."""
+    x, o, dy, dx = QKV.c(), O.c(), dO.c(), dQKV.c()
+    sp = _device_array(stats, torch.int32, "stats", 2 * x.rows * att.desc.heads)
+    p, b = ws.get(att._bytes("ie_attention_bwd_workspace", x.rows))
+    _check(lib().ie_attention_bwd(byref(att.desc), byref(x), byref(o), byref(dy), sp, byref(dx), p, b,
+                                  _stream(ws.device)), "ie_attention_bwd")
 
 
 class Rope:
