@@ -41,6 +41,13 @@ R9  layer norm, the product with bias and residual, and dropout hold what is
     order their functions give; the results are rounded into groups from
     there (R2, R3).
 
+R10 attention: a softmax weight is an integer of at most 32512 (15 bits below the
+    row's largest), from an exponent held to 2^-17 and a cubic in fp32; sums of
+    weights and of weighted mantissas are exact; a weight takes its value's
+    exponent in, relative to the largest one that its query sees, so that a
+    token depends on no later one (R5 would align values over the sequence).
+    Keys and values of a cache have 4 bits (R8) and exponents of their own.
+
 Integer contractions use float64 matrix products: every partial sum is an
 integer of magnitude < 2**53 (asserted), where float64 addition is exact in
 any order, so the float64 result is the exact integer sum.
@@ -48,6 +55,7 @@ any order, so the float64 result is the exact integer sum.
 
 from __future__ import annotations
 
+import math
 from dataclasses import dataclass
 from fractions import Fraction
 
@@ -815,6 +823,234 @@ def dropout(X: QT, R, drop: int, seed: int, step: int, y_group: int, bits: int =
     if R is not None:
         y = y + np.ldexp(R.mant.astype(np.float64), R.row_exp()[:, None])
     return requant_f64(y, y_group, bits)
+
+
+# ---------------------------------------------------------------------------
+# Attention, rotary positions and a 4-bit cache (R10)
+# ---------------------------------------------------------------------------
+
+ATT_E = (-48, 16)        # exponents of Q, K, V and O are read clipped to these
+ATT_UNIT = 32512         # a weight of one
+CACHE_BLOCK = 256
+
+
+def _f32(x) -> np.ndarray:
+    """Rounded to fp32 (from exact float64 values), as float64."""
+    return np.asarray(x, dtype=np.float64).astype(np.float32).astype(np.float64)
+
+
+def softmax_weight(d, r) -> np.ndarray:
+    """32512 * 2^(d r), d <= 0, both fp32 values: the exponent at a resolution of
+    2^-17 and at least -32, the fraction's power by a cubic in fp32."""
+    x = np.asarray(d, dtype=np.float64) * np.asarray(r, dtype=np.float64)  # 48 bits: exact
+    y = np.maximum(np.rint(np.ldexp(np.maximum(x, -64.0), 17)), -32.0 * 2 ** 17)
+    n = np.floor(np.ldexp(y, -17))
+    f = np.ldexp(y, -17) - n
+    q = np.full_like(f, 2545.0)
+    for c in (7358.0, 22609.0, 32512.0):
+        q = _f32(q * f + c)  # product and sum exact in 53 bits
+    return np.ldexp(q, n.astype(np.int64))
+
+
+def _att_exp(e) -> np.ndarray:
+    return np.clip(np.asarray(e, dtype=np.int64), *ATT_E)
+
+
+def _att_rate(scale: float) -> float:
+    """scale log2(e) in fp32."""
+    return float(np.float32(np.float64(np.float32(scale)) * 1.4426950408889634))
+
+
+def _att_sequences(offsets, rows: int):
+    return [(0, rows)] if offsets is None else list(zip(offsets[:-1], offsets[1:]))
+
+
+def _att_head(X: QT, col: int, d: int, a: int, b: int) -> np.ndarray:
+    return X.mant[a:b, col * d:(col + 1) * d].astype(np.int64)
+
+
+def _att_scores(q: np.ndarray, k: np.ndarray, e: np.ndarray, causal: bool):
+    """t_ij = (q_i . k_j) 2^(e_j), and which keys a query sees."""
+    t = np.ldexp(_exact_matmul(q, k.T).astype(np.float64), e[None, :])
+    n = len(q)
+    return t, np.tri(n, dtype=bool) if causal else np.ones((n, n), dtype=bool)
+
+
+def _att_weights(t, see, m, r) -> np.ndarray:
+    return np.where(see, softmax_weight(_f32(np.minimum(t - m[:, None], 0.0)), r[:, None]), 0.0)
+
+
+def attention_fwd(X: QT, heads: int, kv: int, d: int, scale: float, causal: bool, offsets=None, bits: int = Q_BITS):
+    """(O, m, L): O by rows, zeros with exponent E_MIN on rows of no sequence;
+    m and L of every row and head."""
+    rows, g = X.mant.shape[0], heads // kv
+    e_all, rate = _att_exp(X.row_exp()), _att_rate(scale)
+    y = np.zeros((rows, heads * d))
+    tops, sums = np.zeros((rows, heads), dtype=np.float32), np.zeros((rows, heads), dtype=np.int64)
+    for a, b in _att_sequences(offsets, rows):
+        if a == b:
+            continue
+        e = e_all[a:b]
+        for h in range(heads):
+            k, v = _att_head(X, heads + h // g, d, a, b), _att_head(X, heads + kv + h // g, d, a, b)
+            t, see = _att_scores(_att_head(X, h, d, a, b), k, e, causal)
+            m = np.where(see, t, -np.inf).max(axis=1)
+            w = _att_weights(t, see, m, rate * np.ldexp(1.0, e))
+            total = np.rint(w).sum(axis=1)
+            top = np.where(see, e[None, :], -1000).max(axis=1)
+            num = np.rint(np.ldexp(w, e[None, :] - top[:, None])) @ v.astype(np.float64)
+            y[a:b, h * d:(h + 1) * d] = np.ldexp(num * (1.0 / total)[:, None], top[:, None])
+            tops[a:b, h], sums[a:b, h] = m, total
+    return requant_f64(y, ROW, bits), tops, sums
+
+
+def _norm_bits(x: np.ndarray) -> np.ndarray:
+    """[x]: the norm of every row is below 2^[x]."""
+    return (_bitlen_np((x * x).sum(axis=1)) + 1) // 2
+
+
+def _reach(z: np.ndarray, causal: bool) -> np.ndarray:
+    """For every key, the largest value of the queries that see it."""
+    return np.maximum.accumulate(z[::-1])[::-1] if causal else np.full_like(z, z.max())
+
+
+def attention_bwd(X: QT, O: QT, dO: QT, tops, sums, heads: int, kv: int, d: int, scale: float, causal: bool, offsets=None,
+                  bits: int = Q_BITS) -> QT:
+    """dQKV by rows (zeros with exponent E_MIN on rows of no sequence)."""
+    rows, g = X.mant.shape[0], heads // kv
+    e_all, eo_all, ed_all = _att_exp(X.row_exp()), _att_exp(O.row_exp()), dO.row_exp()
+    rate, scale = _att_rate(scale), float(np.float32(scale))
+    y = np.zeros((rows, (heads + 2 * kv) * d))
+    for a, b in _att_sequences(offsets, rows):
+        if a == b:
+            continue
+        e, eo, ed = e_all[a:b], eo_all[a:b], ed_all[a:b]
+        most = int(ed.max())
+        for hk in range(kv):
+            k, v = _att_head(X, heads + hk, d, a, b), _att_head(X, heads + kv + hk, d, a, b)
+            nu = _norm_bits(v) + e
+            per = []
+            for h in range(hk * g, (hk + 1) * g):
+                q, dy, o = _att_head(X, h, d, a, b), _att_head(dO, h, d, a, b), _att_head(O, h, d, a, b)
+                t, see = _att_scores(q, k, e, causal)
+                total = sums[a:b, h].astype(np.float64)
+                w = _att_weights(t, see, tops[a:b, h].astype(np.float64), rate * np.ldexp(1.0, e))
+                dot = (dy * o).sum(axis=1)
+                u = _f32(np.ldexp(_exact_matmul(dy, v.T).astype(np.float64), e[None, :])
+                         - np.ldexp(dot.astype(np.float64), eo)[:, None])
+                s = _f32(w * u)
+                delta, size = _bitlen_np(np.abs(dot)) + eo, _norm_bits(dy)
+                sigma = np.maximum(size + (nu + e).max(), delta + e.max()) + 1
+                num = np.rint(np.ldexp(s, e[None, :] - sigma[:, None])) @ k.astype(np.float64)
+                y[a:b, h * d:(h + 1) * d] = np.ldexp(num * (scale / total)[:, None], (sigma + ed)[:, None])
+                share = np.ldexp(_f32(1.0 / total), np.maximum(ed - most, -60))
+                alpha = np.frexp(share)[1].astype(np.int64)
+                per.append((q, dy, w, s, share, alpha, alpha + e + np.maximum(size + nu.max(), delta) + 1))
+            kappa = np.max([_reach(z[5], causal) for z in per], axis=0)
+            lam = np.max([_reach(z[6], causal) for z in per], axis=0)
+            whole = int(max(z[6].max() for z in per))
+            lam = np.maximum(lam - whole, -96)
+            dk, dv = np.zeros((b - a, d)), np.zeros((b - a, d))
+            for q, dy, w, s, share, _, _ in per:
+                dv += np.rint(np.ldexp(_f32(w * share[:, None]), -kappa[None, :])).T @ dy.astype(np.float64)
+                bi = _f32(np.ldexp(share, e - whole))
+                dk += np.rint(np.ldexp(_f32(s * bi[:, None]), 6 - lam[None, :])).T @ q.astype(np.float64)
+            y[a:b, (heads + hk) * d:(heads + hk + 1) * d] = np.ldexp(dk * scale, (lam - 6 + whole + most)[:, None])
+            y[a:b, (heads + kv + hk) * d:(heads + kv + hk + 1) * d] = np.ldexp(dv, (kappa + most)[:, None])
+    return requant_f64(y, ROW, bits)
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, factor: float = 1.0, trained: float = 0.0, low: float = 1.0,
+                     high: float = 4.0) -> list:
+    out = []
+    for k in range(rot // 2):
+        f = math.pow(base, -2.0 * k / rot)
+        keep = 0.0
+        if trained > 0:
+            keep = min(max((trained * f / (2.0 * math.pi) - low) / (high - low), 0.0), 1.0)
+        out.append(f * (keep + (1.0 - keep) / factor))
+    return out
+
+
+def rope_table(freqs, positions: int) -> np.ndarray:
+    """[positions, pairs, 2]: cos and sin in units of 2^-14."""
+    a = np.arange(positions, dtype=np.float64)[:, None] * np.asarray(freqs, dtype=np.float64)[None, :]
+    return np.rint(np.stack([np.cos(a), np.sin(a)], axis=2) * 16384.0).astype(np.int16)
+
+
+def rope(X: QT, pos, table: np.ndarray, heads: int, d: int, rot: int, interleaved: bool, inverse: bool, y_group: int,
+         bits: int = Q_BITS) -> QT:
+    x = X.mant.astype(np.int64)
+    y = x * 16384
+    c, s = table[pos, :, 0].astype(np.int64), table[pos, :, 1].astype(np.int64)
+    s = -s if inverse else s
+    for h in range(heads):
+        for k in range(rot // 2):
+            i, j = (2 * k, 2 * k + 1) if interleaved else (k, k + rot // 2)
+            i, j = h * d + i, h * d + j
+            y[:, i], y[:, j] = x[:, i] * c[:, k] - x[:, j] * s[:, k], x[:, i] * s[:, k] + x[:, j] * c[:, k]
+    return requant_np(y, np.broadcast_to(X.row_exp()[:, None] - 14, y.shape), y_group, bits)
+
+
+def cache_row(x: np.ndarray, e: np.ndarray) -> tuple:
+    """Rows [n x d] of mantissas at exponents e as 4-bit mantissas and exponents."""
+    t = requant_np(x.astype(np.int64), np.broadcast_to(np.asarray(e, dtype=np.int64)[:, None], x.shape), ROW, 4)
+    return t.mant, t.exp
+
+
+def pack4(c: np.ndarray) -> np.ndarray:
+    """4-bit mantissas, two to a byte, the even one in the low half."""
+    u = np.asarray(c, dtype=np.int64) & 15
+    return (u[..., 0::2] | u[..., 1::2] << 4).astype(np.uint8)
+
+
+def unpack4(b: np.ndarray) -> np.ndarray:
+    u = np.stack([b & 15, b >> 4], axis=-1).reshape(*b.shape[:-1], -1).astype(np.int64)
+    return np.where(u > 7, u - 16, u)
+
+
+def cache_store(cache: dict, X: QT, heads: int, kv: int, d: int, slots) -> None:
+    """Keys and values of X's rows into cache["k"], ["ke"], ["v"], ["ve"] ([slots, kv, ..])."""
+    on = np.flatnonzero((np.asarray(slots) >= 0) & (np.asarray(slots) < cache["ke"].shape[0]))
+    at, e = np.asarray(slots)[on], X.row_exp()[on]
+    for name, first in (("k", heads), ("v", heads + kv)):
+        for h in range(kv):
+            c, ex = cache_row(X.mant[on, (first + h) * d:(first + h + 1) * d], e)
+            cache[name][at, h], cache[name + "e"][at, h] = pack4(c), ex
+
+
+def attention_cache(Q: QT, cache: dict, slots, heads: int, kv: int, d: int, scale: float, bits: int = Q_BITS) -> QT:
+    """One query a row; slots[i]: the cache slots of row i's keys, in order (-1: left out)."""
+    g, rate = heads // kv, _att_rate(scale)
+    y = np.zeros((len(slots), heads * d))
+    e = _att_exp(Q.row_exp())
+    for i, row in enumerate(slots):
+        row = np.asarray(row, dtype=np.int64)
+        for h in range(heads):
+            q = Q.mant[i, h * d:(h + 1) * d].astype(np.int64)
+            r = np.float64(rate * np.ldexp(1.0, int(e[i])))
+            parts = []
+            for b in range(0, len(row), CACHE_BLOCK):
+                at = row[b:b + CACHE_BLOCK]
+                at = at[at >= 0]
+                if not len(at):
+                    continue
+                k, v = unpack4(cache["k"][at, h // g]), unpack4(cache["v"][at, h // g])
+                ke, ve = _att_exp(cache["ke"][at, h // g]), _att_exp(cache["ve"][at, h // g])
+                t = np.ldexp((k @ q).astype(np.float64), ke)
+                w = softmax_weight(_f32(t - t.max()), r)
+                num = np.rint(np.ldexp(w, ve - ve.max())) @ v.astype(np.float64)
+                parts.append((t.max(), np.rint(w).sum(), int(ve.max()), num))
+            if not parts:
+                continue
+            m, top = max(z[0] for z in parts), max(z[2] for z in parts)
+            total, num = 0.0, np.zeros(d)
+            for mb, lb, eb, nb in parts:
+                w = softmax_weight(_f32(mb - m), r)
+                total += np.rint(w) * lb
+                num += np.rint(np.ldexp(w, eb - top)) * nb
+            y[i, h * d:(h + 1) * d] = np.ldexp(num * (1.0 / total), top)
+    return requant_f64(y, ROW, bits)
 
 
 # ---------------------------------------------------------------------------
