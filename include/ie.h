@@ -443,7 +443,8 @@ ie_status ie_dropout(const ie_mat *X, const ie_mat *R, const ie_mat *Y, const ie
  * exponents.
  * stats: for the backward pass, 8 bytes for every row and head (a device array
  * [rows x heads], 8-byte aligned): m and L; NULL where none follows.
- * Limits (IE_ERR_UNSUPPORTED): head_dim <= 128, 2^-30 <= scale <= 2^30.
+ * Limits (IE_ERR_UNSUPPORTED): head_dim <= 128, (heads + 2 kv_heads) * head_dim
+ * <= 2^24, 2^-30 <= scale <= 2^30.
  * Offsets that decrease or leave the matrix, and sequences of more than 131071
  * tokens, set IE_FLAG_INDEX: the rows they name are undefined, no others.
  */

@@ -20,37 +20,35 @@
 
 namespace ie {
 
-// A workgroup of four waves takes 128 queries of one head, 32 to a wave, one
-// to a lane pair; keys pass through LDS 64 at a time, the next ones in flight.
+// A workgroup of four waves takes 64 queries of one head, 16 to a wave, one to
+// four lanes; keys pass through LDS 64 at a time, the next ones in flight.
 template <int DP, bool ROW, bool CAUSAL>
-__global__ __launch_bounds__(256) void attn_fwd_kernel(AttnArgs p, int slots) {
+__global__ __launch_bounds__(256, DP > 64 ? 3 : 4) void attn_fwd_kernel(AttnArgs p) {
     using T = HeadTile<DP>;
-    constexpr int NS = DP / 32;
+    constexpr int KS = T::KS, NE = DP / 16;
     __shared__ __align__(16) int8_t sk[2][T::BYTES], sv[2][T::BYTES];
     __shared__ __align__(16) float sf[2][64];
-    const long long item = xcd_item((long long)slots * p.heads);
-    if (item < 0) return;
-    const int gh = (int)(item % p.group), rest = (int)(item / p.group);
-    const int kvh = rest / slots, slot = CAUSAL ? slots - 1 - rest % slots : rest % slots;
-    const int h = kvh * p.group + gh;
-    int q0, seq;
-    const Span sp = slot_span(p, slot, 128, q0, seq);
-    if (q0 >= sp.n) return;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, half = lane >> 5;
-    const int n = sp.n, qw = q0 + 32 * wave, qi = qw + (lane & 31);
-    const bool ok = qi < n;
+    const Item it = att_item(p, p.group);
+    Span sp;
+    int tile;
+    if (!rank_tile<CAUSAL>(p, it.rank, 64, sp, tile)) return;
+    const int h = it.kvh * p.group + it.gh, q0 = 64 * tile;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, quad = lane >> 4;
+    const int n = sp.n, qw = q0 + 16 * wave, qi = qw + (lane & 15);
+    const bool ok = qi < n, idle = qw >= n;
     const int8_t *base = p.x + (long long)sp.a * p.width;
-    const int8_t *kh = base + (p.heads + kvh) * p.d, *vh = kh + (long long)p.kv * p.d;
+    const int8_t *kh = base + (long long)(p.heads + it.kvh) * p.d, *vh = kh + (long long)p.kv * p.d;
     const int8_t *xe = p.xe + (ROW ? sp.a : 0);
     const int eq = clip_e(xe[ROW ? min(qi, n - 1) : 0]);
     const float r = p.c * pow2f(eq) * (ROW ? 1.0f : pow2f(eq));
-    v4i q[NS];
-    head_regs<DP>(base + (long long)qi * p.width + h * p.d, ok, p.d, p.vec, lane, q);
-    const int keys = CAUSAL ? min(n, q0 + 128) : n, tiles = (keys + 63) / 64;
-    const int last = CAUSAL ? min(n, qw + 32) : n;  // keys of this wave
-    const bool idle = qw >= n;
+    v4i q[KS];
+    head_regs<KS>(base + (long long)qi * p.width + h * p.d, ok, p.d, p.vec, lane, q);
+    const int keys = CAUSAL ? min(n, q0 + 64) : n, tiles = (keys + 63) / 64;
+    const int last = CAUSAL ? min(n, qw + 16) : n;  // keys of this wave
 
     T k, v;
+    k.init(p.width, p.d);
+    v.init(p.width, p.d);
     float fe = 0.0f;
     auto fetch = [&](int t, bool values) {
         k.fetch(kh, p.width, 64 * t, keys, p.d, p.vec);
@@ -62,111 +60,125 @@ __global__ __launch_bounds__(256) void attn_fwd_kernel(AttnArgs p, int slots) {
         if (values) v.put(sv[t & 1]);
         if (ROW && tid < 64) sf[t & 1][tid] = fe;
     };
-    // scores of 32 keys from key row `at` of a tile
-    auto scores = [&](const int8_t *s, int at) {
-        v16i acc = {};
+    // scores of 16 keys of a tile
+    auto scores = [&](int t, int z) {
+        v4i acc = {0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < NS; ++i) acc = mfma(T::frag_r(s, at, i, lane), q[i], acc);
+        for (int i = 0; i < KS; ++i) acc = mfma(T::frag_r(sk[t & 1], z, i, lane), q[i], acc);
         return acc;
     };
-    auto sees = [&](int j) { return CAUSAL ? j <= qi : j < n; };
-    // whether every key of 32 from j on is seen by every query of the wave
-    auto whole = [&](int j) { return j + 32 <= (CAUSAL ? qw + 1 : n); };
+    auto factors = [&](int t, int z, float (&f)[4]) {
+        const float4 x = ROW ? *(const float4 *)&sf[t & 1][16 * z + 4 * quad] : float4{1, 1, 1, 1};
+        f[0] = x.x;
+        f[1] = x.y;
+        f[2] = x.z;
+        f[3] = x.w;
+    };
+    // whether every key of a tile is seen by every query of the wave; else keys 16 z + i <= limit are seen
+    auto whole = [&](int t) { return 64 * t + 64 <= (CAUSAL ? qw + 1 : n); };
+    auto limit = [&](int t) { return (CAUSAL ? qi : n - 1) - 64 * t - 4 * quad; };
 
     // first pass: the largest score (an int32 where all rows share an exponent)
     float m = -__builtin_inff(), em = 0.0f;
     int mi = -(1 << 30);
+    auto largest = [&](auto masked, int t) {
+        const int lim = limit(t);
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+            if (masked.value && 64 * t + 16 * z >= last) break;
+            const v4i acc = scores(t, z);
+            float f[4];
+            factors(t, z, f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool on = !masked.value || 16 * z + i <= lim;
+                if (ROW) {
+                    m = fmaxf(m, on ? (float)acc[i] * f[i] : -__builtin_inff());
+                    em = fmaxf(em, on ? f[i] : 0.0f);
+                } else {
+                    mi = max(mi, on ? acc[i] : -(1 << 30));
+                }
+            }
+        }
+    };
     fetch(0, false);
     for (int t = 0; t < tiles; ++t) {
         put(t, false);
         if (t + 1 < tiles) fetch(t + 1, false);
         __syncthreads();
-#pragma unroll
-        for (int b = 0; b < 64; b += 32) {
-            const int j0 = 64 * t + b;
-            if (idle || j0 >= last) continue;
-            const v16i acc = scores(sk[t & 1], b);
-            const bool all = whole(j0);
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const float4 f = ROW ? *(const float4 *)&sf[t & 1][b + 8 * g + 4 * half] : float4{1, 1, 1, 1};
-                const float fs[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bool on = all || sees(j0 + 8 * g + 4 * half + i);
-                    if (ROW) {
-                        m = fmaxf(m, on ? (float)acc[4 * g + i] * fs[i] : -__builtin_inff());
-                        em = fmaxf(em, on ? fs[i] : 0.0f);
-                    } else {
-                        mi = max(mi, on ? acc[4 * g + i] : -(1 << 30));
-                    }
-                }
-            }
-        }
+        if (idle) continue;
+        if (whole(t)) largest(Bool<false>{}, t);
+        else largest(Bool<true>{}, t);
     }
     if (ROW) {
-        m = half_max(m);
-        em = half_max(em);
+        m = col_max(m);
+        em = col_max(em);
     } else {
-        mi = swap_reduce<32>(mi, Max{});
+        mi = col_reduce(mi, Max{});
     }
     const int top = ROW ? (__float_as_int(em) >> 23) - 127 : eq;  // E
     const float down = ROW ? pow2f(-top) : 1.0f;
     __syncthreads();
 
     // second pass: weights and the sums they enter
-    v16i hi[NS] = {}, lo[NS] = {};
-    uint32_t sum = 0;
+    v4i hi[NE] = {}, lo[NE] = {};
+    uint32_t sum = 0, blocks = 0;
+    auto weigh = [&](auto masked, int t, v4i &dh, v4i &dl) {
+        const int lim = limit(t);
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+            dh[z] = 0;
+            dl[z] = 0;
+            if (masked.value && 64 * t + 16 * z >= last) continue;
+            const v4i acc = scores(t, z);
+            float f[4];
+            factors(t, z, f);
+            int bits[4];
+            uint32_t whole_n[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float w = ROW ? weight(__builtin_fmaf((float)acc[i], f[i], -m), r) : weight((float)(acc[i] - mi), r);
+                if (masked.value) w = 16 * z + i <= lim ? w : 0.0f;
+                bits[i] = __float_as_int(ROW ? __builtin_fmaf(w, f[i] * down, RINT_128) : w + RINT_128);
+                whole_n[i] = (uint32_t)(ROW ? __float_as_int(w + RINT_MAGIC) : bits[i]);
+            }
+            sum += whole_n[0] + whole_n[1];
+            sum += whole_n[2] + whole_n[3];
+            ++blocks;
+            int a, c;
+            digits4(bits[0], bits[1], bits[2], bits[3], a, c);
+            dh[z] = a;
+            dl[z] = c;
+        }
+    };
     fetch(0, true);
     for (int t = 0; t < tiles; ++t) {
         put(t, true);
         if (t + 1 < tiles) fetch(t + 1, true);
         __syncthreads();
+        if (idle || 64 * t >= last) continue;
+        v4i dh, dl;
+        if (whole(t)) weigh(Bool<false>{}, t, dh, dl);
+        else weigh(Bool<true>{}, t, dh, dl);
 #pragma unroll
-        for (int b = 0; b < 64; b += 32) {
-            const int j0 = 64 * t + b;
-            if (idle || j0 >= last) continue;
-            const v16i acc = scores(sk[t & 1], b);
-            const bool all = whole(j0);
-            v4i dh, dl;
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const float4 f = ROW ? *(const float4 *)&sf[t & 1][b + 8 * g + 4 * half] : float4{1, 1, 1, 1};
-                const float fs[4] = {f.x, f.y, f.z, f.w};
-                int bits[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float w = ROW ? weight(__builtin_fmaf((float)acc[4 * g + i], fs[i], -m), r)
-                                  : weight((float)(acc[4 * g + i] - mi), r);
-                    if (!all && !sees(j0 + 8 * g + 4 * half + i)) w = 0.0f;
-                    bits[i] = __float_as_int(ROW ? __builtin_fmaf(w, fs[i] * down, RINT_128) : w + RINT_128);
-                    sum += ROW ? (uint32_t)__float_as_int(w + RINT_MAGIC) - (uint32_t)RINT_BITS
-                               : (uint32_t)bits[i] - (uint32_t)(RINT_BITS + 128);
-                }
-                int a, c;
-                digits4(bits[0], bits[1], bits[2], bits[3], a, c);
-                dh[g] = a;
-                dl[g] = c;
-            }
-#pragma unroll
-            for (int s = 0; s < NS; ++s) {
-                const v4i vt = T::frag_t(sv[t & 1], b, s, lane);
-                hi[s] = mfma(vt, dh, hi[s]);
-                lo[s] = mfma(vt, dl, lo[s]);
-            }
+        for (int e = 0; e < NE; ++e) {
+            const v4i vt = T::frag_t(sv[t & 1], e, lane);
+            hi[e] = mfma(vt, dh, hi[e]);
+            lo[e] = mfma(vt, dl, lo[e]);
         }
     }
     if (idle) return;
-    sum = (uint32_t)swap_reduce<32>((int)sum, Add{});
+    sum -= 4 * blocks * (uint32_t)(ROW ? RINT_BITS : RINT_BITS + 128);
+    sum = (uint32_t)col_reduce((int)sum, Add{});
     const double inv = 1.0 / (double)sum;
-    double y[16 * NS];
+    double y[4 * NE];
 #pragma unroll
-    for (int s = 0; s < NS; ++s)
+    for (int e = 0; e < NE; ++e)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) y[16 * s + i] = __builtin_fma((double)hi[s][i], 256.0, (double)lo[s][i]) * inv;
+        for (int i = 0; i < 4; ++i) y[4 * e + i] = __builtin_fma((double)hi[e][i], 256.0, (double)lo[e][i]) * inv;
     const long long row = sp.a + qi;
     store_odd(y, top, p.q, ok, p.d, lane, p.v16 + row * p.cols + h * p.d, p.p16 + row * p.parts + h);
-    if (p.stats && ok && lane < 32)
+    if (p.stats && ok && lane < 16)
         p.stats[row * p.heads + h] = int2{__float_as_int(ROW ? m : (float)mi * pow2f(eq)), (int)sum};
 }
 
@@ -220,26 +232,23 @@ hipError_t launch_attention_round(const AttnArgs &a, hipStream_t st) {
 }
 
 template <int DP>
-static void fwd(const AttnArgs &a, int slots, dim3 grid, hipStream_t st) {
-    const dim3 block(256);
+static void fwd(const AttnArgs &a, hipStream_t st) {
+    const dim3 grid(att_grid(att_slots(a.rows, a.n_seq, 64), a.kv, a.group)), block(256);
     if (a.x_row) {
-        if (a.causal) hipLaunchKernelGGL((attn_fwd_kernel<DP, true, true>), grid, block, 0, st, a, slots);
-        else hipLaunchKernelGGL((attn_fwd_kernel<DP, true, false>), grid, block, 0, st, a, slots);
+        if (a.causal) hipLaunchKernelGGL((attn_fwd_kernel<DP, true, true>), grid, block, 0, st, a);
+        else hipLaunchKernelGGL((attn_fwd_kernel<DP, true, false>), grid, block, 0, st, a);
     } else {
-        if (a.causal) hipLaunchKernelGGL((attn_fwd_kernel<DP, false, true>), grid, block, 0, st, a, slots);
-        else hipLaunchKernelGGL((attn_fwd_kernel<DP, false, false>), grid, block, 0, st, a, slots);
+        if (a.causal) hipLaunchKernelGGL((attn_fwd_kernel<DP, false, true>), grid, block, 0, st, a);
+        else hipLaunchKernelGGL((attn_fwd_kernel<DP, false, false>), grid, block, 0, st, a);
     }
 }
 
 hipError_t launch_attention_fwd(const AttnArgs &a, hipStream_t st) {
-    const int slots = att_slots(a.rows, a.n_seq, 128);
-    const long long total = (long long)slots * a.heads;
-    const dim3 grid((unsigned)((total + 7) / 8 * 8));
     prof_begin(st, PROF_ATT_FWD);
-    if (a.d <= 32) fwd<32>(a, slots, grid, st);
-    else if (a.d <= 64) fwd<64>(a, slots, grid, st);
-    else if (a.d <= 96) fwd<96>(a, slots, grid, st);
-    else fwd<128>(a, slots, grid, st);
+    if (a.d <= 32) fwd<32>(a, st);
+    else if (a.d <= 64) fwd<64>(a, st);
+    else if (a.d <= 96) fwd<96>(a, st);
+    else fwd<128>(a, st);
     prof_end(st, PROF_ATT_FWD);
     const hipError_t e = hipGetLastError();
     return e != hipSuccess ? e : launch_attention_round(a, st);

@@ -141,45 +141,72 @@ __global__ __launch_bounds__(256) void attn_scale_kernel(AttnArgs p, AttnBwd b) 
     }
 }
 
-// dQ: a workgroup of four waves takes 128 queries of a head, one to a lane
-// pair, as in the forward pass; keys and values pass through LDS.
+// dQ: a workgroup of four waves takes 64 queries of a head, 16 to a wave, one
+// to four lanes, as in the forward pass; keys and values pass through LDS.
 template <int DP, bool ROW, bool CAUSAL>
-__global__ __launch_bounds__(256) void attn_dq_kernel(AttnArgs p, AttnBwd bw, int slots) {
+__global__ __launch_bounds__(256, DP > 64 ? 2 : 3) void attn_dq_kernel(AttnArgs p, AttnBwd bw) {
     using T = HeadTile<DP>;
-    constexpr int NS = DP / 32;
+    constexpr int KS = T::KS, NE = DP / 16;
     __shared__ __align__(16) int8_t sk[2][T::BYTES], sv[2][T::BYTES];
     __shared__ __align__(16) float sf[2][64];
-    const long long item = xcd_item((long long)slots * p.heads);
-    if (item < 0) return;
-    const int gh = (int)(item % p.group), rest = (int)(item / p.group);
-    const int kvh = rest / slots, slot = CAUSAL ? slots - 1 - rest % slots : rest % slots;
-    const int h = kvh * p.group + gh;
-    int q0, seq;
-    const Span sp = slot_span(p, slot, 128, q0, seq);
-    if (q0 >= sp.n) return;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, half = lane >> 5;
-    const int n = sp.n, qw = q0 + 32 * wave, qi = qw + (lane & 31);
-    const bool ok = qi < n;
+    const Item it = att_item(p, p.group);
+    Span sp;
+    int tile;
+    if (!rank_tile<CAUSAL>(p, it.rank, 64, sp, tile)) return;
+    const int h = it.kvh * p.group + it.gh, q0 = 64 * tile;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, quad = lane >> 4;
+    const int n = sp.n, qw = q0 + 16 * wave, qi = qw + (lane & 15);
+    const bool ok = qi < n, idle = qw >= n;
     const int8_t *base = p.x + (long long)sp.a * p.width;
-    const int8_t *kh = base + (p.heads + kvh) * p.d, *vh = kh + (long long)p.kv * p.d;
+    const int8_t *kh = base + (long long)(p.heads + it.kvh) * p.d, *vh = kh + (long long)p.kv * p.d;
     const int8_t *xe = p.xe + (ROW ? sp.a : 0);
     const long long row = sp.a + qi;
-    v4i q[NS], g[NS];
-    head_regs<DP>(base + (long long)qi * p.width + h * p.d, ok, p.d, p.vec, lane, q);
-    head_regs<DP>(bw.dy + row * p.heads * p.d + h * p.d, ok, p.d, bw.dy_vec, lane, g);
+    v4i q[KS], g[KS];
+    head_regs<KS>(base + (long long)qi * p.width + h * p.d, ok, p.d, p.vec, lane, q);
+    head_regs<KS>(bw.dy + row * p.heads * p.d + h * p.d, ok, p.d, bw.dy_vec, lane, g);
     const AttnRow st = bw.row[(long long)h * p.rows + sp.a + min(qi, n - 1)];
-    const float fe0 = pow2f(clip_e(xe[0]));
-    const int keys = CAUSAL ? min(n, q0 + 128) : n, tiles = (keys + 63) / 64;
-    const int last = CAUSAL ? min(n, qw + 32) : n;
-    const bool idle = qw >= n;
+    const float fe0 = pow2f(clip_e(xe[0])), fs0 = fe0 * st.s;
+    const int keys = CAUSAL ? min(n, q0 + 64) : n, tiles = (keys + 63) / 64;
+    const int last = CAUSAL ? min(n, qw + 16) : n;
     T k, v;
+    k.init(p.width, p.d);
+    v.init(p.width, p.d);
     float fe = 0.0f;
     auto fetch = [&](int t) {
         k.fetch(kh, p.width, 64 * t, keys, p.d, p.vec);
         v.fetch(vh, p.width, 64 * t, keys, p.d, p.vec);
         if (ROW && tid < 64) fe = pow2f(clip_e(xe[min(64 * t + tid, n - 1)]));
     };
-    v16i hi[NS] = {}, lo[NS] = {};
+    auto weigh = [&](auto masked, int t, v4i &dh, v4i &dl) {
+        const int lim = (CAUSAL ? qi : n - 1) - 64 * t - 4 * quad;  // keys seen: 16 z + i <= lim
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+            dh[z] = 0;
+            dl[z] = 0;
+            if (masked.value && 64 * t + 16 * z >= last) continue;
+            v4i s = {0, 0, 0, 0}, dp = {0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < KS; ++i) {
+                s = mfma(T::frag_r(sk[t & 1], z, i, lane), q[i], s);
+                dp = mfma(T::frag_r(sv[t & 1], z, i, lane), g[i], dp);
+            }
+            const float4 f = ROW ? *(const float4 *)&sf[t & 1][16 * z + 4 * quad] : float4{fe0, fe0, fe0, fe0};
+            const float fs[4] = {f.x, f.y, f.z, f.w};
+            int bits[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float w = weight(__builtin_fmaf((float)s[i], fs[i], -st.m), st.r);
+                if (masked.value) w = 16 * z + i <= lim ? w : 0.0f;
+                const float u = __builtin_fmaf((float)dp[i], fs[i], -st.dot);
+                bits[i] = __float_as_int(__builtin_fmaf(w * u, ROW ? fs[i] * st.s : fs0, RINT_128));
+            }
+            int x, y;
+            digits4(bits[0], bits[1], bits[2], bits[3], x, y);
+            dh[z] = x;
+            dl[z] = y;
+        }
+    };
+    v4i hi[NE] = {}, lo[NE] = {};
     fetch(0);
     for (int t = 0; t < tiles; ++t) {
         k.put(sk[t & 1]);
@@ -187,191 +214,217 @@ __global__ __launch_bounds__(256) void attn_dq_kernel(AttnArgs p, AttnBwd bw, in
         if (ROW && tid < 64) sf[t & 1][tid] = fe;
         if (t + 1 < tiles) fetch(t + 1);
         __syncthreads();
+        if (idle || 64 * t >= last) continue;
+        v4i dh, dl;
+        if (64 * t + 64 <= (CAUSAL ? qw + 1 : n)) weigh(Bool<false>{}, t, dh, dl);
+        else weigh(Bool<true>{}, t, dh, dl);
 #pragma unroll
-        for (int b = 0; b < 64; b += 32) {
-            const int j0 = 64 * t + b;
-            if (idle || j0 >= last) continue;
-            v16i s = {}, dp = {};
-#pragma unroll
-            for (int i = 0; i < NS; ++i) {
-                s = mfma(T::frag_r(sk[t & 1], b, i, lane), q[i], s);
-                dp = mfma(T::frag_r(sv[t & 1], b, i, lane), g[i], dp);
-            }
-            const bool all = j0 + 32 <= (CAUSAL ? qw + 1 : n);
-            v4i dh, dl;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const float4 f = ROW ? *(const float4 *)&sf[t & 1][b + 8 * c + 4 * half] : float4{fe0, fe0, fe0, fe0};
-                const float fs[4] = {f.x, f.y, f.z, f.w};
-                int bits[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int j = j0 + 8 * c + 4 * half + i;
-                    float w = weight(__builtin_fmaf((float)s[4 * c + i], fs[i], -st.m), st.r);
-                    if (!all && !(CAUSAL ? j <= qi : j < n)) w = 0.0f;
-                    const float u = __builtin_fmaf((float)dp[4 * c + i], fs[i], -st.dot);
-                    bits[i] = __float_as_int(__builtin_fmaf(w * u * fs[i], st.s, RINT_128));
-                }
-                int x, y;
-                digits4(bits[0], bits[1], bits[2], bits[3], x, y);
-                dh[c] = x;
-                dl[c] = y;
-            }
-#pragma unroll
-            for (int i = 0; i < NS; ++i) {
-                const v4i kt = T::frag_t(sk[t & 1], b, i, lane);
-                hi[i] = mfma(kt, dh, hi[i]);
-                lo[i] = mfma(kt, dl, lo[i]);
-            }
+        for (int e = 0; e < NE; ++e) {
+            const v4i kt = T::frag_t(sk[t & 1], e, lane);
+            hi[e] = mfma(kt, dh, hi[e]);
+            lo[e] = mfma(kt, dl, lo[e]);
         }
     }
     if (idle) return;
     const double rate = p.scale / (double)st.sum;
-    double y[16 * NS];
+    double y[4 * NE];
 #pragma unroll
-    for (int s = 0; s < NS; ++s)
+    for (int e = 0; e < NE; ++e)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) y[16 * s + i] = __builtin_fma((double)hi[s][i], 256.0, (double)lo[s][i]) * rate;
+        for (int i = 0; i < 4; ++i) y[4 * e + i] = __builtin_fma((double)hi[e][i], 256.0, (double)lo[e][i]) * rate;
     store_odd(y, st.e, p.q, ok, p.d, lane, p.v16 + row * p.cols + h * p.d, p.p16 + row * p.parts + h);
 }
 
-// dK and dV: a workgroup of four waves takes 128 keys, one to a lane pair, and
-// runs over the query heads that share them and their queries.
-template <int DP, bool CAUSAL>
-__global__ __launch_bounds__(256) void attn_dkv_kernel(AttnArgs p, AttnBwd bw, int slots) {
-    using T = HeadTile<DP>;
-    constexpr int NS = DP / 32;
-    __shared__ __align__(16) int8_t sq[2][T::BYTES], sg[2][T::BYTES];
-    __shared__ __align__(16) float sr[2][5][64];
-    const long long item = xcd_item((long long)slots * p.kv);
-    if (item < 0) return;
-    const int kvh = (int)(item / slots), slot = (int)(item % slots);
-    int k0, seq;
-    const Span sp = slot_span(p, slot, 128, k0, seq);
-    if (k0 >= sp.n) return;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, half = lane >> 5;
-    const int n = sp.n, kw = k0 + 32 * wave, kj = kw + (lane & 31);
+// dK and dV: four lanes hold a key, a wave 16; queries, of every query head that
+// shares them, pass through LDS 64 at a time.  SPLIT 1: a workgroup's four waves
+// take 16 keys each and all the queries.  SPLIT 4: they take the same 16 keys
+// and every fourth tile of queries each, staged by the wave itself, and add
+// their sums up in LDS at the end (exact integers): where there are few keys,
+// four times as many workgroups, which stage four times as much.
+template <int DP, bool CAUSAL, int SPLIT>
+__global__ __launch_bounds__(256, DP > 64 ? 1 : 2) void attn_dkv_kernel(AttnArgs p, AttnBwd bw) {
+    using T = HeadTile<DP, 256 / SPLIT>;
+    constexpr int KS = T::KS, NE = DP / 16, KEYS = 64 / SPLIT, NB = SPLIT == 1 ? 2 : 1;
+    __shared__ __align__(16) int8_t sq[NB * SPLIT][T::BYTES], sg[NB * SPLIT][T::BYTES];
+    __shared__ __align__(16) float sr[NB * SPLIT][5][64];
+    const Item it = att_item(p, 1);
+    Span sp;
+    int tile;
+    if (!rank_tile<CAUSAL>(p, it.rank, KEYS, sp, tile)) return;
+    const int n = sp.n;
+    if (CAUSAL) tile = (n + KEYS - 1) / KEYS - 1 - tile;  // the first keys meet the most queries
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, quad = lane >> 4;
+    const int k0 = KEYS * tile, kw = k0 + (SPLIT == 1 ? 16 * wave : 0), kj = kw + (lane & 15);
     const bool ok = kj < n, idle = kw >= n;
     const int8_t *base = p.x + (long long)sp.a * p.width;
     const long long row = sp.a + kj;
-    v4i k[NS], v[NS];
-    head_regs<DP>(base + (long long)kj * p.width + (p.heads + kvh) * p.d, ok, p.d, p.vec, lane, k);
-    head_regs<DP>(base + (long long)kj * p.width + (p.heads + p.kv + kvh) * p.d, ok, p.d, p.vec, lane, v);
-    const AttnKey key = bw.key[(long long)kvh * p.rows + sp.a + min(kj, n - 1)];
+    v4i k[KS], v[KS];
+    head_regs<KS>(base + (long long)kj * p.width + (long long)(p.heads + it.kvh) * p.d, ok, p.d, p.vec, lane, k);
+    head_regs<KS>(base + (long long)kj * p.width + (long long)(p.heads + p.kv + it.kvh) * p.d, ok, p.d, p.vec, lane, v);
+    const AttnKey key = bw.key[(long long)it.kvh * p.rows + sp.a + min(kj, n - 1)];
     const float f = pow2f(clip_e(p.xe[p.x_row ? sp.a + min(kj, n - 1) : 0]));
     const float sv = pow2f(min(-key.kappa, 126)), sk = pow2f(min(6 - key.lambda, 126));
-    const int first = CAUSAL ? k0 / 64 : 0, tiles = (n + 63) / 64 - first, steps = tiles * p.group;
+    const int first = CAUSAL ? k0 / 64 : 0, tiles = (n + 63) / 64 - first, total = tiles * p.group;
+    const int steps = SPLIT == 1 ? total : (total - wave + 3) / 4;
     T q, g;
+    q.init(p.width, p.d);
+    g.init(p.heads * p.d, p.d);
     AttnRow rec;
-    auto fetch = [&](int i) {
-        const int h = kvh * p.group + i / tiles, t = first + i % tiles;
-        q.fetch(base + h * p.d, p.width, 64 * t, n, p.d, p.vec);
-        g.fetch(bw.dy + (long long)sp.a * p.heads * p.d + h * p.d, (long long)p.heads * p.d, 64 * t, n, p.d, bw.dy_vec);
-        if (tid < 64) rec = bw.row[(long long)h * p.rows + sp.a + min(64 * t + tid, n - 1)];
+    int fh = 0, ft = SPLIT == 1 ? 0 : wave;  // head and tile of the step that is fetched next
+    auto wrap = [&](int &hh, int &tt) {
+        while (tt >= tiles) {
+            tt -= tiles;
+            ++hh;
+        }
     };
-    v16i vh[NS] = {}, vl[NS] = {}, c2[NS] = {}, c1[NS] = {}, c0[NS] = {};
+    if (SPLIT > 1) wrap(fh, ft);
+    const int me = SPLIT == 1 ? tid : lane;
+    auto fetch = [&]() {
+        const int h = it.kvh * p.group + fh, t = 64 * (first + ft);
+        q.fetch(base + h * p.d, p.width, t, n, p.d, p.vec);
+        g.fetch(bw.dy + (long long)sp.a * p.heads * p.d + h * p.d, (long long)p.heads * p.d, t, n, p.d, bw.dy_vec);
+        if (me < 64) rec = bw.row[(long long)h * p.rows + sp.a + min(t + me, n - 1)];
+        ft += SPLIT;
+        wrap(fh, ft);
+    };
+    v4i acc[5][NE] = {};  // digits of dV (2) and dK (3), highest first
     const v4i bias = {(int)0xc0c0c0c0u, (int)0xc0c0c0c0u, (int)0xc0c0c0c0u, (int)0xc0c0c0c0u};  // -64
-    fetch(0);
+    auto weigh = [&](auto masked, const int8_t *lq, const int8_t *lg, const float *r, int i0, v4i (&dg)[5]) {
+        // queries that see the key: i0 + 16 z + 4 quad + x in [kj, n) (causal), below n
+        const int lo = kj - i0 - 4 * quad, hi = n - 1 - i0 - 4 * quad;
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+            if (masked.value) {
+                dg[0][z] = dg[1][z] = dg[3][z] = dg[4][z] = 0;
+                dg[2][z] = 0x40404040;
+                if (i0 + 16 * z >= n || (CAUSAL && i0 + 16 * z + 15 < kw)) continue;
+            }
+            v4i s = {0, 0, 0, 0}, dp = {0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < KS; ++i) {
+                s = mfma(T::frag_r(lq, z, i, lane), k[i], s);
+                dp = mfma(T::frag_r(lg, z, i, lane), v[i], dp);
+            }
+            float r5[5][4];
+#pragma unroll
+            for (int y = 0; y < 5; ++y) {
+                const float4 x = *(const float4 *)(r + y * 64 + 16 * z + 4 * quad);
+                r5[y][0] = x.x;
+                r5[y][1] = x.y;
+                r5[y][2] = x.z;
+                r5[y][3] = x.w;
+            }
+            int ab[4], cb[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                float w = weight(__builtin_fmaf((float)s[x], f, -r5[0][x]), r5[1][x]);
+                if (masked.value) w = 16 * z + x <= hi && (!CAUSAL || 16 * z + x >= lo) ? w : 0.0f;
+                const float u = __builtin_fmaf((float)dp[x], f, -r5[2][x]);
+                ab[x] = __float_as_int(__builtin_fmaf(w * r5[3][x], sv, RINT_128));
+                cb[x] = __float_as_int(__builtin_fmaf(w * u * r5[4][x], sk, RINT_MAGIC + 32896.0f));
+            }
+            int x, y, w;
+            digits4(ab[0], ab[1], ab[2], ab[3], x, y);
+            dg[0][z] = x;
+            dg[1][z] = y;
+            digits3x4(cb[0], cb[1], cb[2], cb[3], x, y, w);
+            dg[2][z] = x;
+            dg[3][z] = y;
+            dg[4][z] = w;
+        }
+    };
+    if (steps > 0) fetch();
+    int ct = SPLIT == 1 ? 0 : wave, ch = 0;
+    if (SPLIT > 1) wrap(ch, ct);
     for (int i = 0; i < steps; ++i) {
-        const int buf = i & 1, t = first + i % tiles;
+        const int buf = SPLIT == 1 ? i & 1 : wave;
+        if (SPLIT > 1) __builtin_amdgcn_wave_barrier();
         q.put(sq[buf]);
         g.put(sg[buf]);
-        if (tid < 64) {
-            sr[buf][0][tid] = rec.m;
-            sr[buf][1][tid] = rec.r;
-            sr[buf][2][tid] = rec.dot;
-            sr[buf][3][tid] = rec.a;
-            sr[buf][4][tid] = rec.b;
+        if (me < 64) {
+            sr[buf][0][me] = rec.m;
+            sr[buf][1][me] = rec.r;
+            sr[buf][2][me] = rec.dot;
+            sr[buf][3][me] = rec.a;
+            sr[buf][4][me] = rec.b;
         }
-        if (i + 1 < steps) fetch(i + 1);
-        __syncthreads();
+        const int i0 = 64 * (first + ct);
+        ct += SPLIT;
+        wrap(ch, ct);
+        if (i + 1 < steps) fetch();
+        if (SPLIT == 1) __syncthreads();
+        else __builtin_amdgcn_wave_barrier();
+        if (idle || (CAUSAL && i0 + 63 < kw)) continue;
+        v4i dg[5];
+        if (i0 + 64 <= n && (!CAUSAL || kw + 15 <= i0)) weigh(Bool<false>{}, sq[buf], sg[buf], &sr[buf][0][0], i0, dg);
+        else weigh(Bool<true>{}, sq[buf], sg[buf], &sr[buf][0][0], i0, dg);
 #pragma unroll
-        for (int b = 0; b < 64; b += 32) {
-            const int i0 = 64 * t + b;
-            if (idle || i0 >= n || (CAUSAL && i0 + 31 < kw)) continue;
-            v16i s = {}, dp = {};
-#pragma unroll
-            for (int z = 0; z < NS; ++z) {
-                s = mfma(T::frag_r(sq[buf], b, z, lane), k[z], s);
-                dp = mfma(T::frag_r(sg[buf], b, z, lane), v[z], dp);
-            }
-            const bool all = i0 + 32 <= n && (!CAUSAL || kw + 31 <= i0);
-            v4i ah, al, d2, d1, d0;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                float r5[5][4];
-#pragma unroll
-                for (int z = 0; z < 5; ++z) {
-                    const float4 x = *(const float4 *)&sr[buf][z][b + 8 * c + 4 * half];
-                    r5[z][0] = x.x;
-                    r5[z][1] = x.y;
-                    r5[z][2] = x.z;
-                    r5[z][3] = x.w;
-                }
-                int ab[4], cb[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int qi = i0 + 8 * c + 4 * half + x;
-                    float w = weight(__builtin_fmaf((float)s[4 * c + x], f, -r5[0][x]), r5[1][x]);
-                    if (!all && !(qi < n && (!CAUSAL || kj <= qi))) w = 0.0f;
-                    const float u = __builtin_fmaf((float)dp[4 * c + x], f, -r5[2][x]);
-                    ab[x] = __float_as_int(__builtin_fmaf(w * r5[3][x], sv, RINT_128));
-                    cb[x] = __float_as_int(__builtin_fmaf(w * u * r5[4][x], sk, RINT_MAGIC + 32896.0f));
-                }
-                int x, y, z;
-                digits4(ab[0], ab[1], ab[2], ab[3], x, y);
-                ah[c] = x;
-                al[c] = y;
-                digits3x4(cb[0], cb[1], cb[2], cb[3], x, y, z);
-                d2[c] = x;
-                d1[c] = y;
-                d0[c] = z;
-            }
-#pragma unroll
-            for (int z = 0; z < NS; ++z) {
-                const v4i gt = T::frag_t(sg[buf], b, z, lane), qt = T::frag_t(sq[buf], b, z, lane);
-                vh[z] = mfma(gt, ah, vh[z]);
-                vl[z] = mfma(gt, al, vl[z]);
-                c2[z] = mfma(qt, bias, c2[z]);
-                c2[z] = mfma(qt, d2, c2[z]);
-                c1[z] = mfma(qt, d1, c1[z]);
-                c0[z] = mfma(qt, d0, c0[z]);
-            }
+        for (int e = 0; e < NE; ++e) {
+            const v4i gt = T::frag_t(sg[buf], e, lane), qt = T::frag_t(sq[buf], e, lane);
+            acc[0][e] = mfma(gt, dg[0], acc[0][e]);
+            acc[1][e] = mfma(gt, dg[1], acc[1][e]);
+            acc[2][e] = mfma(qt, bias, acc[2][e]);
+            acc[2][e] = mfma(qt, dg[2], acc[2][e]);
+            acc[3][e] = mfma(qt, dg[3], acc[3][e]);
+            acc[4][e] = mfma(qt, dg[4], acc[4][e]);
         }
+    }
+    if constexpr (SPLIT > 1) {
+        // wave 0 gathers the sums, a digit at a time
+        int *x = (int *)&sq[0][0];
+        static_assert(sizeof sq >= 3 * 4 * NE * 64 * sizeof(int), "a digit's sums fit the tiles");
+#pragma unroll
+        for (int a = 0; a < 5; ++a) {
+            __syncthreads();
+            if (wave)
+#pragma unroll
+                for (int i = 0; i < 4 * NE; ++i) x[((wave - 1) * 4 * NE + i) * 64 + lane] = acc[a][i >> 2][i & 3];
+            __syncthreads();
+            if (!wave)
+#pragma unroll
+                for (int i = 0; i < 4 * NE; ++i)
+                    acc[a][i >> 2][i & 3] += x[i * 64 + lane] + x[(4 * NE + i) * 64 + lane] + x[(8 * NE + i) * 64 + lane];
+        }
+        if (wave) return;
     }
     if (idle) return;
-    double y[16 * NS];
+    double y[4 * NE];
     int16_t *out = p.v16 + row * p.cols, *need = p.p16 + row * p.parts;
 #pragma unroll
-    for (int s = 0; s < NS; ++s)
+    for (int e = 0; e < NE; ++e)
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            y[16 * s + i] = ((double)c2[s][i] * 65536.0 + ((double)c1[s][i] * 256.0 + (double)c0[s][i])) * p.scale;
-    store_odd(y, key.ek, p.q, ok, p.d, lane, out + (p.heads + kvh) * p.d, need + p.heads + kvh);
+        for (int i = 0; i < 4; ++i)
+            y[4 * e + i] = ((double)acc[2][e][i] * 65536.0 + ((double)acc[3][e][i] * 256.0 + (double)acc[4][e][i])) * p.scale;
+    store_odd(y, key.ek, p.q, ok, p.d, lane, out + (p.heads + it.kvh) * p.d, need + p.heads + it.kvh);
 #pragma unroll
-    for (int s = 0; s < NS; ++s)
+    for (int e = 0; e < NE; ++e)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) y[16 * s + i] = (double)vh[s][i] * 256.0 + (double)vl[s][i];
-    store_odd(y, key.ev, p.q, ok, p.d, lane, out + (p.heads + p.kv + kvh) * p.d, need + p.heads + p.kv + kvh);
+        for (int i = 0; i < 4; ++i) y[4 * e + i] = (double)acc[0][e][i] * 256.0 + (double)acc[1][e][i];
+    store_odd(y, key.ev, p.q, ok, p.d, lane, out + (p.heads + p.kv + it.kvh) * p.d, need + p.heads + p.kv + it.kvh);
 }
 
 template <int DP>
-static void dq(const AttnArgs &a, const AttnBwd &b, int slots, dim3 grid, hipStream_t st) {
-    const dim3 block(256);
+static void dq(const AttnArgs &a, const AttnBwd &b, hipStream_t st) {
+    const dim3 grid(att_grid(att_slots(a.rows, a.n_seq, 64), a.kv, a.group)), block(256);
     if (a.x_row) {
-        if (a.causal) hipLaunchKernelGGL((attn_dq_kernel<DP, true, true>), grid, block, 0, st, a, b, slots);
-        else hipLaunchKernelGGL((attn_dq_kernel<DP, true, false>), grid, block, 0, st, a, b, slots);
+        if (a.causal) hipLaunchKernelGGL((attn_dq_kernel<DP, true, true>), grid, block, 0, st, a, b);
+        else hipLaunchKernelGGL((attn_dq_kernel<DP, true, false>), grid, block, 0, st, a, b);
     } else {
-        if (a.causal) hipLaunchKernelGGL((attn_dq_kernel<DP, false, true>), grid, block, 0, st, a, b, slots);
-        else hipLaunchKernelGGL((attn_dq_kernel<DP, false, false>), grid, block, 0, st, a, b, slots);
+        if (a.causal) hipLaunchKernelGGL((attn_dq_kernel<DP, false, true>), grid, block, 0, st, a, b);
+        else hipLaunchKernelGGL((attn_dq_kernel<DP, false, false>), grid, block, 0, st, a, b);
     }
 }
 
 template <int DP>
-static void dkv(const AttnArgs &a, const AttnBwd &b, int slots, dim3 grid, hipStream_t st) {
-    const dim3 block(256);
-    if (a.causal) hipLaunchKernelGGL((attn_dkv_kernel<DP, true>), grid, block, 0, st, a, b, slots);
-    else hipLaunchKernelGGL((attn_dkv_kernel<DP, false>), grid, block, 0, st, a, b, slots);
+static void dkv(const AttnArgs &a, const AttnBwd &b, int split, hipStream_t st) {
+    const dim3 grid(att_grid(att_slots(a.rows, a.n_seq, 64 / split), a.kv, 1)), block(256);
+    if (split == 1) {
+        if (a.causal) hipLaunchKernelGGL((attn_dkv_kernel<DP, true, 1>), grid, block, 0, st, a, b);
+        else hipLaunchKernelGGL((attn_dkv_kernel<DP, false, 1>), grid, block, 0, st, a, b);
+    } else {
+        if (a.causal) hipLaunchKernelGGL((attn_dkv_kernel<DP, true, 4>), grid, block, 0, st, a, b);
+        else hipLaunchKernelGGL((attn_dkv_kernel<DP, false, 4>), grid, block, 0, st, a, b);
+    }
 }
 
 hipError_t launch_attention_bwd(const AttnArgs &a, const AttnBwd &b, hipStream_t st) {
@@ -380,19 +433,18 @@ hipError_t launch_attention_bwd(const AttnArgs &a, const AttnBwd &b, hipStream_t
     hipLaunchKernelGGL(attn_dot_kernel, dim3((unsigned)(items < 16384 ? items : 16384)), dim3(256), 0, st, a, b);
     hipLaunchKernelGGL(attn_scale_kernel, dim3((unsigned)(max(a.n_seq, 1) * a.kv)), dim3(256), 0, st, a, b);
     prof_end(st, PROF_ATT_PREP);
-    const int slots = (int)att_slots(a.rows, a.n_seq, 128);
-    const dim3 gq((unsigned)(((long long)slots * a.heads + 7) / 8 * 8)), gk((unsigned)(((long long)slots * a.kv + 7) / 8 * 8));
     prof_begin(st, PROF_ATT_DQ);
-    if (a.d <= 32) dq<32>(a, b, slots, gq, st);
-    else if (a.d <= 64) dq<64>(a, b, slots, gq, st);
-    else if (a.d <= 96) dq<96>(a, b, slots, gq, st);
-    else dq<128>(a, b, slots, gq, st);
+    if (a.d <= 32) dq<32>(a, b, st);
+    else if (a.d <= 64) dq<64>(a, b, st);
+    else if (a.d <= 96) dq<96>(a, b, st);
+    else dq<128>(a, b, st);
     prof_end(st, PROF_ATT_DQ);
+    const int split = att_slots(a.rows, a.n_seq, 64) * a.kv < 4 * NCU ? 4 : 1;
     prof_begin(st, PROF_ATT_DKV);
-    if (a.d <= 32) dkv<32>(a, b, slots, gk, st);
-    else if (a.d <= 64) dkv<64>(a, b, slots, gk, st);
-    else if (a.d <= 96) dkv<96>(a, b, slots, gk, st);
-    else dkv<128>(a, b, slots, gk, st);
+    if (a.d <= 32) dkv<32>(a, b, split, st);
+    else if (a.d <= 64) dkv<64>(a, b, split, st);
+    else if (a.d <= 96) dkv<96>(a, b, split, st);
+    else dkv<128>(a, b, split, st);
     prof_end(st, PROF_ATT_DKV);
     const hipError_t e = hipGetLastError();
     return e != hipSuccess ? e : launch_attention_round(a, st);

@@ -15,17 +15,19 @@
 //
 // Digits.  A weight enters a product as an integer n = rint(w ...) of at most
 // 32512, as two signed digits n = 256 a + b, a and b int8, so that its sums
-// are exact int32 sums of v_mfma_i32_32x32x32_i8 and the order of keys, of
+// are exact int32 sums of v_mfma_i32_16x16x64_i8 and the order of keys, of
 // tiles and of workgroups is of no account.  n + 128 comes out of the adder of
 // rint (a magic constant), its two low bytes are a and b + 128.
 //
 // Layout.  The matrix instruction's result holds one column per lane (column
-// lane % 32, rows 8 (r / 4) + 4 (lane / 32) + r % 4), its operands 16
-// consecutive steps of the contraction.  Products run with the axis that is
-// summed next (keys, for queries in the columns) along the rows: four
-// neighbouring results of a lane are then four neighbouring bytes of the next
-// product's operand, without a trip through LDS; the other operand of that
-// product takes its steps in the same order (frag_t).
+// lane % 16, rows 4 (lane / 16) + r), its operands 16 consecutive steps of a
+// contraction of 64 (steps 16 (lane / 16) ..).  Products run with the axis that
+// is summed next (keys, for queries in the columns) along the rows: four results
+// of 16 rows are then, lane by lane, the 16 bytes of the next product's operand
+// for a contraction over their 64 rows, without a trip through LDS; that
+// product's other operand takes its steps in the same order (frag_t).  Sixteen
+// columns to a wave, not 32: a wave's sums take half the registers, which is
+// two to four waves to a SIMD where there was one.
 #pragma once
 
 #include "ie_f64.h"
@@ -49,7 +51,8 @@ __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) 
 __device__ __forceinline__ float weight(float d, float r) {
     const float z = fmaxf(__builtin_fmaf(d, r, 96.0f), 64.0f);
     const float f = __builtin_amdgcn_fractf(z);
-    const uint32_t k = (uint32_t)__float_as_int(z) >> 17 & 63u;
+    uint32_t k;  // as written, the compiler takes the field's place by a shift and a mask
+    asm("v_bfe_u32 %0, %1, 17, 6" : "=v"(k) : "v"(z));
     float q = __builtin_fmaf(W_C3, f, W_C2);
     q = __builtin_fmaf(q, f, W_C1);
     q = __builtin_fmaf(q, f, W_C0);
@@ -75,12 +78,24 @@ __device__ __forceinline__ void digits3x4(int a, int b, int c, int d, int &hi, i
     hi = (int)__builtin_amdgcn_perm(t, s, 0x05040100u);
 }
 
-__device__ __forceinline__ v16i mfma(v4i a, v4i b, v16i c) { return __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, c, 0, 0, 0); }
+__device__ __forceinline__ v4i mfma(v4i a, v4i b, v4i c) { return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0); }
 
-__device__ __forceinline__ float half_max(float v) {
-    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+// A maximum over the four lanes of a column.
+__device__ __forceinline__ float col_max(float v) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
+template <class F>
+__device__ __forceinline__ int col_reduce(int v, F f) {
+    return swap_reduce<32>(swap_reduce<16>(v, f), f);
+}
+
+template <bool B>
+struct Bool {
+    static constexpr bool value = B;
+};
 
 // Sequence s of a packed batch: its rows [a, b).  Offsets are read on the
 // device; bounds that lie outside the matrix or before the last one are
@@ -117,12 +132,55 @@ __device__ __forceinline__ Span slot_span(const AttnArgs &p, int slot, int bm, i
     return s;
 }
 
-// Work items (tile slots of every head) as workgroups reach the XCDs
-// (blockIdx % 8): each XCD takes a contiguous run, so that the tiles and the
-// query heads that share keys share its L2.  -1: none.
-__device__ __forceinline__ long long xcd_item(long long total) {
-    const long long per = (total + 7) / 8, i = (long long)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    return (blockIdx.x >> 3) < per && i < total ? i : -1;
+// A launch's items: the tiles of 64 rows of every key head, and of each the
+// `per` query heads that share it.  Workgroups reach the XCDs in turn
+// (blockIdx % 8), so an XCD takes every eighth pair (tile, key head), tiles in
+// order, the heads of a pair one behind the other: they share its L2, and every
+// XCD meets heavy and light tiles alike.
+struct Item {
+    int rank, kvh, gh;
+};
+__device__ __forceinline__ Item att_item(const AttnArgs &p, int per) {
+    const int idx = blockIdx.x >> 3;
+    const int v = idx / per, u = v * 8 + (blockIdx.x & 7);
+    return Item{u / p.kv, u % p.kv, idx - v * per};
+}
+inline unsigned att_grid(long long tiles, int kv, int per) { return (unsigned)((tiles * kv + 7) / 8 * 8 * per); }
+
+// The tile of a rank: its sequence and its number in it; false: none.  Tiles of
+// a causal launch differ in work (the t-th of a sequence meets t + 1 tiles of
+// keys): the heaviest come first, for up to 64 sequences (a lane each); else
+// sequences in order, each with enough ranks for its tiles (see slot_span).
+template <bool HEAVY>
+__device__ __forceinline__ bool rank_tile(const AttnArgs &p, int rank, int bm, Span &sp, int &tile) {
+    if (!HEAVY || !p.off || p.n_seq > 64) {
+        int first, seq;
+        const int slots = (int)(p.rows / bm) + max(p.n_seq, 1);
+        sp = slot_span(p, HEAVY ? slots - 1 - rank : rank, bm, first, seq);
+        tile = first / bm;
+        return rank < slots && first < sp.n;
+    }
+    const int lane = threadIdx.x & 63;
+    const Span mine = lane < p.n_seq ? seq_span(p, lane) : Span{0, 0};
+    const int tiles = (mine.n + bm - 1) / bm;
+    // tiles whose number is t or more: A(t) = sum max(0, tiles - t)
+    auto at_least = [&](int t) { return lane_reduce<64>(max(0, tiles - t), Add{}); };
+    int lo = 0, hi = wave_max_dpp(tiles);  // A(lo) > rank >= A(hi)
+    if (rank >= at_least(0)) return false;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (at_least(mid) > rank) lo = mid;
+        else hi = mid;
+    }
+    // the k-th sequence with a tile of number lo
+    int k = rank - at_least(lo + 1);
+    uint64_t have = __ballot(tiles > lo);
+    while (k-- > 0) have &= have - 1;
+    const int s = __builtin_ctzll(have);
+    sp.a = __builtin_amdgcn_readfirstlane(__shfl(mine.a, s, 64));
+    sp.n = __builtin_amdgcn_readfirstlane(__shfl(mine.n, s, 64));
+    tile = __builtin_amdgcn_readfirstlane(lo);
+    return true;
 }
 
 // 16 mantissas of a head from column 16 c on; past d: zeros.
@@ -138,77 +196,102 @@ __device__ __forceinline__ v4i head16(const int8_t *head, int c, int d, int vec)
     return v4i{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
 }
 
-// A tile of 64 rows of one head, DP bytes each (zeros past d), in LDS: read by
-// rows (frag_r) and transposed (frag_t).  Rows lie DP + PAD bytes apart, which
-// spreads the 16-byte reads of 32 rows and the eight rows of a transposing
-// read over the banks.
-template <int DP>
+// A tile of 64 rows of one head in LDS, read by rows (frag_r: contraction over
+// the head's elements, 64 a step, zeros past d) and transposed (frag_t).  Rows
+// lie 16 bytes more than a multiple of 64 apart, which spreads the reads over
+// the banks.
+//
+// Loads go through a buffer descriptor over the tile's rows, whose bounds are
+// checked in hardware: a thread's chunks keep their offsets from tile to tile
+// (rows past the last one and columns past d lie outside it and read zeros),
+// and only the descriptor, in scalar registers, moves.
+// NT threads share the work: a workgroup, or a wave for a tile of its own.
+template <int DP, int NT = 256>
 struct HeadTile {
-    static constexpr int CH = DP / 16, PITCH = DP + (DP == 32 ? 16 : DP == 64 ? 16 : 16), BYTES = 64 * PITCH;
-    static constexpr int NPT = (64 * CH + 255) / 256;
+    static constexpr int KS = (DP + 63) / 64, CH = 4 * KS, PITCH = 64 * KS + 16, BYTES = 64 * PITCH;
+    static constexpr int NPT = (64 * CH + NT - 1) / NT;
     v4i reg[NPT];
-    // rows first .. of the head whose row 0 is at `head`, `n` rows in all
-    __device__ __forceinline__ void fetch(const int8_t *head, long long width, int first, int n, int d, int vec) {
+    uint32_t at[NPT];
+    __device__ __forceinline__ void init(long long width, int d) {
 #pragma unroll
         for (int i = 0; i < NPT; ++i) {
-            const int c = threadIdx.x + 256 * i, row = c / CH;
+            const int c = threadIdx.x % NT + NT * i;
+            const bool on = c < 64 * CH && c % CH * 16 < d;
+            at[i] = on ? (uint32_t)(c / CH) * (uint32_t)width + c % CH * 16 : 0x80000000u;
+        }
+    }
+    // rows first .. of the head whose row 0 is at `head`, `n` rows in all
+    __device__ __forceinline__ void fetch(const int8_t *head, long long width, int first, int n, int d, int vec) {
+        const int8_t *p = head + first * width;
+        if (vec) {
+            const uint64_t a = (uint64_t)p;
+            const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a), hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
+            const int left = min(64, n - first);  // a tile behind the last row: no bytes
+            const int bytes = __builtin_amdgcn_readfirstlane(left > 0 ? (left - 1) * (int)width + d : 0);
+            const auto r = __builtin_amdgcn_make_buffer_rsrc((void *)(((uint64_t)hi << 32) | lo), (short)0, bytes, 0x00020000);
+#pragma unroll
+            for (int i = 0; i < NPT; ++i) reg[i] = (v4i)__builtin_amdgcn_raw_buffer_load_b128(r, (int)at[i], 0, 0);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < NPT; ++i) {
+            const int c = threadIdx.x % NT + NT * i, row = c / CH;
             reg[i] = v4i{0, 0, 0, 0};
-            if (64 * CH % 256 && c >= 64 * CH) continue;
-            if (first + row < n) reg[i] = head16(head + (first + row) * width, c % CH, d, vec);
+            if (c < 64 * CH && first + row < n) reg[i] = head16(p + row * width, c % CH, d, vec);
         }
     }
     __device__ __forceinline__ void put(int8_t *lds) const {
 #pragma unroll
         for (int i = 0; i < NPT; ++i) {
-            const int c = threadIdx.x + 256 * i;
-            if (64 * CH % 256 && c >= 64 * CH) continue;
+            const int c = threadIdx.x % NT + NT * i;
+            if (64 * CH % NT && c >= 64 * CH) continue;
             *(v4i *)(lds + c / CH * PITCH + c % CH * 16) = reg[i];
         }
     }
-    // Rows row .. row + 31 as an operand whose contraction is the head's
-    // elements 32 s ..: lane l holds row l % 32.
-    static __device__ __forceinline__ v4i frag_r(const int8_t *lds, int row, int s, int lane) {
-        return *(const v4i *)(lds + (row + (lane & 31)) * PITCH + s * 32 + (lane >> 5) * 16);
+    // Rows 16 t .. as an operand: contraction over the head's elements 64 s ..
+    static __device__ __forceinline__ v4i frag_r(const int8_t *lds, int t, int s, int lane) {
+        return *(const v4i *)(lds + (16 * t + (lane & 15)) * PITCH + s * 64 + (lane >> 4) * 16);
     }
-    // Elements 32 s .. as rows of an operand whose contraction are the tile's
-    // rows row .. row + 31, in the order of a product's results.
-    static __device__ __forceinline__ v4i frag_t(const int8_t *lds, int row, int s, int lane) {
+    // Elements 16 e .. as rows of an operand: contraction over the tile's 64
+    // rows, in the order of the products' results (lane group c, byte 4 t + r:
+    // row 16 t + 4 c + r).
+    static __device__ __forceinline__ v4i frag_t(const int8_t *lds, int e, int lane) {
         const int g = lane & 15, k = g >> 1;
-        const int8_t *at = lds + (row + (k >> 2) * 8 + (lane >> 5) * 4 + (k & 3)) * PITCH + s * 32 + (lane & 16) + (g & 1) * 8;
+        const int8_t *at = lds + (16 * (k >> 2) + 4 * (lane >> 4) + (k & 3)) * PITCH + 16 * e + (g & 1) * 8;
         typedef __attribute__((address_space(3))) v2i lds_v2i;
         const v2i lo = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i *)at);
-        const v2i hi = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i *)(at + 16 * PITCH));
+        const v2i hi = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i *)(at + 32 * PITCH));
         return v4i{lo.x, lo.y, hi.x, hi.y};
     }
 };
 
-// The head of a row as the operand that stays in registers: lane l holds row
-// l % 32, elements 32 s + 16 (l / 32) ...
-template <int DP>
-__device__ __forceinline__ void head_regs(const int8_t *head, bool ok, int d, int vec, int lane, v4i (&q)[DP / 32]) {
+// The head of a row as the operand that stays in registers: lane l holds row l
+// % 16, elements 64 s + 16 (l / 16) ...
+template <int KS>
+__device__ __forceinline__ void head_regs(const int8_t *head, bool ok, int d, int vec, int lane, v4i (&q)[KS]) {
 #pragma unroll
-    for (int s = 0; s < DP / 32; ++s) {
+    for (int s = 0; s < KS; ++s) {
         q[s] = v4i{0, 0, 0, 0};
-        if (ok) q[s] = head16(head, 2 * s + (lane >> 5), d, vec);
+        if (ok) q[s] = head16(head, 4 * s + (lane >> 4), d, vec);
     }
 }
 
-// A result row of one head, one column of the transposed product: value
-// y[16 s + r] of lane l is element 32 s + 8 (r / 4) + 4 (l / 32) + r % 4 of row
-// l % 32; the other half of the row lies in the lane 32 away.  Rounded to odd
-// at two bits below what the head alone needs, for a rounding by whole rows.
+// A result row of one head, one column of the transposed product: value y[4 e +
+// r] of lane l is element 16 e + 4 (l / 16) + r of row l % 16; the other three
+// quarters of the row lie 16, 32 and 48 lanes away.  Rounded to odd at two bits
+// below what the head alone needs, for a rounding by whole rows.
 template <int NV>
 __device__ __forceinline__ void store_odd(const double (&y)[NV], int e, int q, bool ok, int d, int lane, int16_t *out,
                                           int16_t *need_out) {
     MaxMag mx;
 #pragma unroll
     for (int i = 0; i < NV; i += 2) mx.add(y[i], y[i + 1]);
-    const int need = need_word(swap_reduce<32>(mx.word(), Max{}), q);
+    const int need = need_word(col_reduce(mx.word(), Max{}), q);
     const double inv = need == NEED_NONE ? 0.0 : pow2(2 - need);
-    if (ok && lane < 32) *need_out = (int16_t)(need == NEED_NONE ? P_NONE : need + e);
+    if (ok && lane < 16) *need_out = (int16_t)(need == NEED_NONE ? P_NONE : need + e);
 #pragma unroll
     for (int g = 0; g < NV / 4; ++g) {
-        const int c = 32 * (g / 4) + 8 * (g % 4) + 4 * (lane >> 5);
+        const int c = 16 * g + 4 * (lane >> 4);
         int v[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {

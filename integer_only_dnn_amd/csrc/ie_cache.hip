@@ -202,11 +202,7 @@ __global__ __launch_bounds__(256) void cache_attention_kernel(CacheArgs p, AttnA
                     m = fmaxf(m, fs[i] > 0.0f ? score[t][i] : -__builtin_inff());
                 }
             }
-            {
-                const auto s16 = __builtin_amdgcn_permlane16_swap(__float_as_uint(m), __float_as_uint(m), false, false);
-                m = fmaxf(__uint_as_float(s16[0]), __uint_as_float(s16[1]));
-                m = half_max(m);
-            }
+            m = col_max(m);
             if (lane < 16) smax[wave][lane] = m;
             // values, unpacked
 #pragma unroll

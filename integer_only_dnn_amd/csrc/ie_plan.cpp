@@ -930,9 +930,11 @@ ie_status check_attention(const ie_attention_desc *d, const ie_mat *X, long long
     if (X->cols != cols) return IE_ERR_SHAPE;
     if (!d->offsets != !d->n_seq) return IE_ERR_SHAPE;
     if (d->head_dim > ATT_HEAD_MAX || (uintptr_t)d->offsets % 4) return IE_ERR_UNSUPPORTED;
+    // 64 rows of a tile within a 32-bit window
+    if (((long long)d->heads + 2ll * d->kv_heads) * d->head_dim > ATT_COLS_MAX) return IE_ERR_UNSUPPORTED;
     // 2^-30 .. 2^30: r = scale log2(e) 2^e keeps clear of fp32's ends (a NaN is refused too)
     if (!(d->scale >= 0x1p-30f && d->scale <= 0x1p30f)) return IE_ERR_UNSUPPORTED;
-    if (att_slots(X->rows, d->n_seq, 64) * d->heads > ATT_ITEMS_MAX) return IE_ERR_UNSUPPORTED;
+    if (att_slots(X->rows, d->n_seq, 16) * d->heads > ATT_ITEMS_MAX) return IE_ERR_UNSUPPORTED;
     return IE_OK;
 }
 

@@ -440,6 +440,7 @@ int *carve_dropout(Carve &c, long long rows, long long cols);  // block maxima
 // whose int32 sums of digits (at most 127 * 128 each) stay exact.
 constexpr int ATT_MOST = 131071;
 constexpr int ATT_HEAD_MAX = 128;
+constexpr long long ATT_COLS_MAX = 1ll << 24;  // columns of QKV
 constexpr long long ATT_ITEMS_MAX = 1ll << 30;  // workgroups of a launch
 inline long long att_slots(long long rows, long long n_seq, int bm) { return rows / bm + (n_seq > 0 ? n_seq : 1); }
 struct AttFwdWs {
