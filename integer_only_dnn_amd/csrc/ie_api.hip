@@ -1245,16 +1245,25 @@ static AttnArgs att_args(const ie_attention_desc *d, const ie_mat *X, void *ws) 
     a.kv = d->kv_heads;
     a.group = d->heads / d->kv_heads;
     a.d = d->head_dim;
-    a.width = (int)att_cols(d);
+    a.dp = (int)r16(d->head_dim);
+    a.width = (int)((d->heads + 2ll * d->kv_heads) * a.dp);
     a.off = d->offsets;
     a.n_seq = d->n_seq;
     a.causal = d->causal != 0;
-    a.vec = d->head_dim % 16 == 0 && aligned(X->mant, 16);
     a.most = ATT_MOST;
     a.c = (float)((double)d->scale * 1.4426950408889634);
     a.scale = (double)d->scale;
     a.flags = (uint32_t *)ws;
     return a;
+}
+
+// m's rows of nh heads of d elements, or where these do not start at multiples
+// of 16 bytes a copy in which they do.
+static hipError_t padded_heads(const ie_mat *m, int nh, const AttnArgs &a, int8_t *copy, const int8_t *&out, hipStream_t st) {
+    out = m->mant;
+    if (a.d == a.dp && aligned(m->mant, 16)) return hipSuccess;
+    out = copy;
+    return launch_attention_pad(m->mant, m->rows, nh, a.d, a.dp, copy, st);
 }
 
 // Whether a byte of m is one of the n at p.
@@ -1264,8 +1273,8 @@ static bool share_bytes(const ie_mat *m, const void *p, size_t n) {
 }
 
 size_t ie_attention_fwd_workspace(const ie_attention_desc *d, int64_t rows) {
-    if (!d || rows < 0 || d->heads < 1 || d->head_dim < 1 || d->head_dim > ATT_HEAD_MAX) return 0;
-    return attention_fwd_ws(rows, d->heads, d->head_dim);
+    if (!d || rows < 0 || d->heads < 1 || d->kv_heads < 1 || d->head_dim < 1 || d->head_dim > ATT_HEAD_MAX) return 0;
+    return attention_fwd_ws(rows, d->heads, d->kv_heads, d->head_dim);
 }
 
 ie_status ie_attention_fwd(const ie_attention_desc *d, const ie_mat *QKV, const ie_mat *O, void *stats, void *ws,
@@ -1280,11 +1289,12 @@ ie_status ie_attention_fwd(const ie_attention_desc *d, const ie_mat *QKV, const 
         share_bytes(QKV, stats, stat_bytes))
         return IE_ERR_UNSUPPORTED;
     if (!ws) return IE_ERR_WORKSPACE;
-    if (ws_bytes < attention_fwd_ws(QKV->rows, d->heads, d->head_dim)) return IE_ERR_WORKSPACE;
+    if (ws_bytes < attention_fwd_ws(QKV->rows, d->heads, d->kv_heads, d->head_dim)) return IE_ERR_WORKSPACE;
     if (QKV->rows == 0) return IE_OK;
     AttnArgs a = att_args(d, QKV, ws);
     Carve c{(char *)ws, HEADER};
-    const AttFwdWs w = carve_attention_fwd(c, QKV->rows, d->heads, d->head_dim);
+    const AttFwdWs w = carve_attention_fwd(c, QKV->rows, d->heads, d->kv_heads, d->head_dim);
+    IE_TRY(padded_heads(QKV, d->heads + 2 * d->kv_heads, a, w.xp, a.x, (hipStream_t)stream));
     a.stats = (int2 *)stats;
     a.v16 = w.v16;
     a.p16 = w.p16;
@@ -1337,10 +1347,10 @@ ie_status ie_attention_bwd(const ie_attention_desc *d, const ie_mat *QKV, const 
     memset(&b, 0, sizeof b);
     b.o = O->mant;
     b.oe = O->exp;
-    b.dy = dO->mant;
+    IE_TRY(padded_heads(QKV, d->heads + 2 * d->kv_heads, a, w.xp, a.x, (hipStream_t)stream));
+    IE_TRY(padded_heads(dO, d->heads, a, w.dyp, b.dy, (hipStream_t)stream));
     b.dye = dO->exp;
     b.dy_row = dO->group == IE_GROUP_ROW && dO->rows > 1;
-    b.dy_vec = d->head_dim % 16 == 0 && aligned(dO->mant, 16);
     b.dots = (int2 *)w.dots;
     b.norm = w.norm;
     b.row = (AttnRow *)w.row;

@@ -20,6 +20,58 @@
 
 namespace ie {
 
+// 16 mantissas of a head from column 16 c on, at any alignment; past d: zeros.
+__device__ __forceinline__ v4i head16(const int8_t *head, int c, int d) {
+    v4i v = {0, 0, 0, 0};
+    const int n = d - 16 * c;
+    const int8_t *p = head + 16 * c;
+    if (n >= 16) {
+        __builtin_memcpy(&v, p, 16);
+    } else if (n > 0) {
+        // n = 8 a + 4 b + 2 c + e, from the top down: each piece shifts the ones above it up
+        uint64_t lo = 0, hi = 0;
+        if (n & 8) __builtin_memcpy(&lo, p, 8);
+        const int8_t *t = p + (n & 8);
+        uint64_t w = 0;
+        if (n & 1) w = (uint8_t)t[n & 6];
+        if (n & 2) {
+            uint16_t x;
+            __builtin_memcpy(&x, t + (n & 4), 2);
+            w = w << 16 | x;
+        }
+        if (n & 4) {
+            uint32_t x;
+            __builtin_memcpy(&x, t, 4);
+            w = w << 32 | x;
+        }
+        if (n & 8) hi = w;
+        else lo = w;
+        v = v4i{(int)(uint32_t)lo, (int)(uint32_t)(lo >> 32), (int)(uint32_t)hi, (int)(uint32_t)(hi >> 32)};
+    }
+    return v;
+}
+
+// Rows of nh heads of d elements into heads of dp (a multiple of 16), zeros in
+// between: what the kernels read where heads do not start at multiples of 16
+// bytes.
+__global__ __launch_bounds__(256) void attn_pad_kernel(const int8_t *x, long long rows, int nh, int d, int dp, int8_t *out) {
+    const int per = dp >> 4, row_chunks = nh * per;
+    const long long n = rows * row_chunks;
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
+        const long long row = i / row_chunks;
+        const int c = (int)(i - row * row_chunks), h = c / per;
+        *(v4i *)(out + i * 16) = head16(x + (row * nh + h) * d, c - h * per, d);
+    }
+}
+
+hipError_t launch_attention_pad(const int8_t *x, long long rows, int nh, int d, int dp, int8_t *out, hipStream_t st) {
+    const long long blocks = (rows * nh * (dp >> 4) + 255) / 256;
+    prof_begin(st, PROF_ATT_PAD);
+    hipLaunchKernelGGL(attn_pad_kernel, dim3((unsigned)(blocks < 16384 ? blocks : 16384)), dim3(256), 0, st, x, rows, nh, d, dp, out);
+    prof_end(st, PROF_ATT_PAD);
+    return hipGetLastError();
+}
+
 // A workgroup of four waves takes 64 queries of one head, 16 to a wave, one to
 // four lanes; keys pass through LDS 64 at a time, the next ones in flight.
 template <int DP, bool ROW, bool CAUSAL>
@@ -37,22 +89,22 @@ __global__ __launch_bounds__(256, DP > 64 ? 3 : 4) void attn_fwd_kernel(AttnArgs
     const int n = sp.n, qw = q0 + 16 * wave, qi = qw + (lane & 15);
     const bool ok = qi < n, idle = qw >= n;
     const int8_t *base = p.x + (long long)sp.a * p.width;
-    const int8_t *kh = base + (long long)(p.heads + it.kvh) * p.d, *vh = kh + (long long)p.kv * p.d;
+    const int8_t *kh = base + (long long)(p.heads + it.kvh) * p.dp, *vh = kh + (long long)p.kv * p.dp;
     const int8_t *xe = p.xe + (ROW ? sp.a : 0);
     const int eq = clip_e(xe[ROW ? min(qi, n - 1) : 0]);
     const float r = p.c * pow2f(eq) * (ROW ? 1.0f : pow2f(eq));
     v4i q[KS];
-    head_regs<KS>(base + (long long)qi * p.width + h * p.d, ok, p.d, p.vec, lane, q);
+    head_regs<KS>(base + (long long)qi * p.width + h * p.dp, ok, p.dp, lane, q);
     const int keys = CAUSAL ? min(n, q0 + 64) : n, tiles = (keys + 63) / 64;
     const int last = CAUSAL ? min(n, qw + 16) : n;  // keys of this wave
 
     T k, v;
-    k.init(p.width, p.d);
-    v.init(p.width, p.d);
+    k.init(p.width, p.dp);
+    v.init(p.width, p.dp);
     float fe = 0.0f;
     auto fetch = [&](int t, bool values) {
-        k.fetch(kh, p.width, 64 * t, keys, p.d, p.vec);
-        if (values) v.fetch(vh, p.width, 64 * t, keys, p.d, p.vec);
+        k.fetch(kh, p.width, 64 * t, keys, p.dp);
+        if (values) v.fetch(vh, p.width, 64 * t, keys, p.dp);
         if (ROW && tid < 64) fe = pow2f(clip_e(xe[min(64 * t + tid, n - 1)]));
     };
     auto put = [&](int t, bool values) {

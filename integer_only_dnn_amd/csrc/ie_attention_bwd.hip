@@ -34,10 +34,10 @@ __global__ __launch_bounds__(256) void attn_dot_kernel(AttnArgs p, AttnBwd b) {
         const int part = i < total ? (int)(i - row * parts) : 0;
         uint32_t x[2] = {0, 0}, y[2] = {0, 0};
         if (part < p.heads) {
-            load_run<8>(b.dy + row * p.heads * p.d + part * p.d, 8 * lane, p.d, x);
-            load_run<8>(b.o + row * p.heads * p.d + part * p.d, 8 * lane, p.d, y);
+            load_run<8>(b.dy + (row * p.heads + part) * p.dp, 8 * lane, p.d, x);
+            load_run<8>(b.o + (row * p.heads + part) * p.d, 8 * lane, p.d, y);
         } else {
-            load_run<8>(p.x + row * p.width + (part + p.kv) * p.d, 8 * lane, p.d, x);
+            load_run<8>(p.x + row * p.width + (long long)(part + p.kv) * p.dp, 8 * lane, p.d, x);
         }
         int dot = 0, sq = 0;
 #pragma unroll
@@ -158,23 +158,23 @@ __global__ __launch_bounds__(256, DP > 64 ? 2 : 3) void attn_dq_kernel(AttnArgs 
     const int n = sp.n, qw = q0 + 16 * wave, qi = qw + (lane & 15);
     const bool ok = qi < n, idle = qw >= n;
     const int8_t *base = p.x + (long long)sp.a * p.width;
-    const int8_t *kh = base + (long long)(p.heads + it.kvh) * p.d, *vh = kh + (long long)p.kv * p.d;
+    const int8_t *kh = base + (long long)(p.heads + it.kvh) * p.dp, *vh = kh + (long long)p.kv * p.dp;
     const int8_t *xe = p.xe + (ROW ? sp.a : 0);
     const long long row = sp.a + qi;
     v4i q[KS], g[KS];
-    head_regs<KS>(base + (long long)qi * p.width + h * p.d, ok, p.d, p.vec, lane, q);
-    head_regs<KS>(bw.dy + row * p.heads * p.d + h * p.d, ok, p.d, bw.dy_vec, lane, g);
+    head_regs<KS>(base + (long long)qi * p.width + h * p.dp, ok, p.dp, lane, q);
+    head_regs<KS>(bw.dy + (row * p.heads + h) * p.dp, ok, p.dp, lane, g);
     const AttnRow st = bw.row[(long long)h * p.rows + sp.a + min(qi, n - 1)];
     const float fe0 = pow2f(clip_e(xe[0])), fs0 = fe0 * st.s;
     const int keys = CAUSAL ? min(n, q0 + 64) : n, tiles = (keys + 63) / 64;
     const int last = CAUSAL ? min(n, qw + 16) : n;
     T k, v;
-    k.init(p.width, p.d);
-    v.init(p.width, p.d);
+    k.init(p.width, p.dp);
+    v.init(p.width, p.dp);
     float fe = 0.0f;
     auto fetch = [&](int t) {
-        k.fetch(kh, p.width, 64 * t, keys, p.d, p.vec);
-        v.fetch(vh, p.width, 64 * t, keys, p.d, p.vec);
+        k.fetch(kh, p.width, 64 * t, keys, p.dp);
+        v.fetch(vh, p.width, 64 * t, keys, p.dp);
         if (ROW && tid < 64) fe = pow2f(clip_e(xe[min(64 * t + tid, n - 1)]));
     };
     auto weigh = [&](auto masked, int t, v4i &dh, v4i &dl) {
@@ -259,16 +259,16 @@ __global__ __launch_bounds__(256, DP > 64 ? 1 : 2) void attn_dkv_kernel(AttnArgs
     const int8_t *base = p.x + (long long)sp.a * p.width;
     const long long row = sp.a + kj;
     v4i k[KS], v[KS];
-    head_regs<KS>(base + (long long)kj * p.width + (long long)(p.heads + it.kvh) * p.d, ok, p.d, p.vec, lane, k);
-    head_regs<KS>(base + (long long)kj * p.width + (long long)(p.heads + p.kv + it.kvh) * p.d, ok, p.d, p.vec, lane, v);
+    head_regs<KS>(base + (long long)kj * p.width + (long long)(p.heads + it.kvh) * p.dp, ok, p.dp, lane, k);
+    head_regs<KS>(base + (long long)kj * p.width + (long long)(p.heads + p.kv + it.kvh) * p.dp, ok, p.dp, lane, v);
     const AttnKey key = bw.key[(long long)it.kvh * p.rows + sp.a + min(kj, n - 1)];
     const float f = pow2f(clip_e(p.xe[p.x_row ? sp.a + min(kj, n - 1) : 0]));
     const float sv = pow2f(min(-key.kappa, 126)), sk = pow2f(min(6 - key.lambda, 126));
     const int first = CAUSAL ? k0 / 64 : 0, tiles = (n + 63) / 64 - first, total = tiles * p.group;
     const int steps = SPLIT == 1 ? total : (total - wave + 3) / 4;
     T q, g;
-    q.init(p.width, p.d);
-    g.init(p.heads * p.d, p.d);
+    q.init(p.width, p.dp);
+    g.init(p.heads * p.dp, p.dp);
     AttnRow rec;
     int fh = 0, ft = SPLIT == 1 ? 0 : wave;  // head and tile of the step that is fetched next
     auto wrap = [&](int &hh, int &tt) {
@@ -281,8 +281,8 @@ __global__ __launch_bounds__(256, DP > 64 ? 1 : 2) void attn_dkv_kernel(AttnArgs
     const int me = SPLIT == 1 ? tid : lane;
     auto fetch = [&]() {
         const int h = it.kvh * p.group + fh, t = 64 * (first + ft);
-        q.fetch(base + h * p.d, p.width, t, n, p.d, p.vec);
-        g.fetch(bw.dy + (long long)sp.a * p.heads * p.d + h * p.d, (long long)p.heads * p.d, t, n, p.d, bw.dy_vec);
+        q.fetch(base + h * p.dp, p.width, t, n, p.dp);
+        g.fetch(bw.dy + ((long long)sp.a * p.heads + h) * p.dp, (long long)p.heads * p.dp, t, n, p.dp);
         if (me < 64) rec = bw.row[(long long)h * p.rows + sp.a + min(t + me, n - 1)];
         ft += SPLIT;
         wrap(fh, ft);

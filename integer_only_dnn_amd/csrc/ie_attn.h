@@ -183,84 +183,63 @@ __device__ __forceinline__ bool rank_tile(const AttnArgs &p, int rank, int bm, S
     return true;
 }
 
-// 16 mantissas of a head from column 16 c on; past d: zeros.
-__device__ __forceinline__ v4i head16(const int8_t *head, int c, int d, int vec) {
-    v4i v = {0, 0, 0, 0};
-    const int n = d - 16 * c;
-    if (n <= 0) return v;
-    if (vec) return *(const v4i *)(head + 16 * c);
-    uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int k = 0; k < 16; ++k)
-        if (k < n) w[k >> 2] |= (uint32_t)(uint8_t)head[16 * c + k] << (8 * (k & 3));
-    return v4i{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
-}
-
 // A tile of 64 rows of one head in LDS, read by rows (frag_r: contraction over
-// the head's elements, 64 a step, zeros past d) and transposed (frag_t).  Rows
-// lie 16 bytes more than a multiple of 64 apart, which spreads the reads over
-// the banks.
+// the head's elements, 64 a step, zeros past its end) and transposed (frag_t).  Rows
+// lie 16 bytes more than a multiple of 64 apart, and every 16 rows another 128
+// bytes: the 16 rows of a frag_r, and the rows 4 c .. 4 c + 3 and 16 + 4 c .. of
+// two lane groups of a frag_t, then fall on banks of their own (without the 128
+// bytes a third of the cycles of LDS were conflicts).
 //
 // Loads go through a buffer descriptor over the tile's rows, whose bounds are
 // checked in hardware: a thread's chunks keep their offsets from tile to tile
-// (rows past the last one and columns past d lie outside it and read zeros),
+// (rows past the last one and columns past the head lie outside it and read zeros),
 // and only the descriptor, in scalar registers, moves.
 // NT threads share the work: a workgroup, or a wave for a tile of its own.
 template <int DP, int NT = 256>
 struct HeadTile {
-    static constexpr int KS = (DP + 63) / 64, CH = 4 * KS, PITCH = 64 * KS + 16, BYTES = 64 * PITCH;
+    static constexpr int KS = (DP + 63) / 64, CH = 4 * KS, PITCH = 64 * KS + 16, BYTES = 64 * PITCH + 3 * 128;
     static constexpr int NPT = (64 * CH + NT - 1) / NT;
     v4i reg[NPT];
     uint32_t at[NPT];
-    __device__ __forceinline__ void init(long long width, int d) {
+    __device__ __forceinline__ void init(long long width, int dp) {
 #pragma unroll
         for (int i = 0; i < NPT; ++i) {
             const int c = threadIdx.x % NT + NT * i;
-            const bool on = c < 64 * CH && c % CH * 16 < d;
+            const bool on = c < 64 * CH && c % CH * 16 < dp;
             at[i] = on ? (uint32_t)(c / CH) * (uint32_t)width + c % CH * 16 : 0x80000000u;
         }
     }
     // rows first .. of the head whose row 0 is at `head`, `n` rows in all
-    __device__ __forceinline__ void fetch(const int8_t *head, long long width, int first, int n, int d, int vec) {
-        const int8_t *p = head + first * width;
-        if (vec) {
-            const uint64_t a = (uint64_t)p;
-            const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a), hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
-            const int left = min(64, n - first);  // a tile behind the last row: no bytes
-            const int bytes = __builtin_amdgcn_readfirstlane(left > 0 ? (left - 1) * (int)width + d : 0);
-            const auto r = __builtin_amdgcn_make_buffer_rsrc((void *)(((uint64_t)hi << 32) | lo), (short)0, bytes, 0x00020000);
+    __device__ __forceinline__ void fetch(const int8_t *head, long long width, int first, int n, int dp) {
+        const uint64_t a = (uint64_t)(head + first * width);
+        const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a), hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
+        const int left = min(64, n - first);  // a tile behind the last row: no bytes
+        const int bytes = __builtin_amdgcn_readfirstlane(left > 0 ? (left - 1) * (int)width + dp : 0);
+        const auto r = __builtin_amdgcn_make_buffer_rsrc((void *)(((uint64_t)hi << 32) | lo), (short)0, bytes, 0x00020000);
 #pragma unroll
-            for (int i = 0; i < NPT; ++i) reg[i] = (v4i)__builtin_amdgcn_raw_buffer_load_b128(r, (int)at[i], 0, 0);
-            return;
-        }
-#pragma unroll
-        for (int i = 0; i < NPT; ++i) {
-            const int c = threadIdx.x % NT + NT * i, row = c / CH;
-            reg[i] = v4i{0, 0, 0, 0};
-            if (c < 64 * CH && first + row < n) reg[i] = head16(p + row * width, c % CH, d, vec);
-        }
+        for (int i = 0; i < NPT; ++i) reg[i] = (v4i)__builtin_amdgcn_raw_buffer_load_b128(r, (int)at[i], 0, 0);
     }
     __device__ __forceinline__ void put(int8_t *lds) const {
 #pragma unroll
         for (int i = 0; i < NPT; ++i) {
             const int c = threadIdx.x % NT + NT * i;
             if (64 * CH % NT && c >= 64 * CH) continue;
-            *(v4i *)(lds + c / CH * PITCH + c % CH * 16) = reg[i];
+            *(v4i *)(lds + c / CH * PITCH + c / CH / 16 * 128 + c % CH * 16) = reg[i];
         }
     }
     // Rows 16 t .. as an operand: contraction over the head's elements 64 s ..
     static __device__ __forceinline__ v4i frag_r(const int8_t *lds, int t, int s, int lane) {
-        return *(const v4i *)(lds + (16 * t + (lane & 15)) * PITCH + s * 64 + (lane >> 4) * 16);
+        return *(const v4i *)(lds + (lane & 15) * PITCH + t * (16 * PITCH + 128) + s * 64 + (lane >> 4) * 16);
     }
     // Elements 16 e .. as rows of an operand: contraction over the tile's 64
     // rows, in the order of the products' results (lane group c, byte 4 t + r:
     // row 16 t + 4 c + r).
     static __device__ __forceinline__ v4i frag_t(const int8_t *lds, int e, int lane) {
         const int g = lane & 15, k = g >> 1;
-        const int8_t *at = lds + (16 * (k >> 2) + 4 * (lane >> 4) + (k & 3)) * PITCH + 16 * e + (g & 1) * 8;
+        const int8_t *at = lds + (4 * (lane >> 4) + (k & 3)) * PITCH + (k >> 2) * (16 * PITCH + 128) + 16 * e + (g & 1) * 8;
         typedef __attribute__((address_space(3))) v2i lds_v2i;
         const v2i lo = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i *)at);
-        const v2i hi = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i *)(at + 32 * PITCH));
+        const v2i hi = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i *)(at + 2 * (16 * PITCH + 128)));
         return v4i{lo.x, lo.y, hi.x, hi.y};
     }
 };
@@ -268,11 +247,12 @@ struct HeadTile {
 // The head of a row as the operand that stays in registers: lane l holds row l
 // % 16, elements 64 s + 16 (l / 16) ...
 template <int KS>
-__device__ __forceinline__ void head_regs(const int8_t *head, bool ok, int d, int vec, int lane, v4i (&q)[KS]) {
+__device__ __forceinline__ void head_regs(const int8_t *head, bool ok, int dp, int lane, v4i (&q)[KS]) {
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
         q[s] = v4i{0, 0, 0, 0};
-        if (ok) q[s] = head16(head, 4 * s + (lane >> 4), d, vec);
+        const int c = 64 * s + (lane >> 4) * 16;
+        if (ok && c < dp) q[s] = *(const v4i *)(head + c);
     }
 }
 

@@ -144,6 +144,7 @@ constexpr int PROF_COL_FINISH = 3630;
 constexpr int PROF_DROPOUT = 3700;
 constexpr int PROF_ROPE = 3900;
 constexpr int PROF_ATT_FWD = 4000;
+constexpr int PROF_ATT_PAD = 4005;
 constexpr int PROF_ATT_ROUND = 4010;
 constexpr int PROF_ATT_PREP = 4020;
 constexpr int PROF_ATT_DQ = 4030;
@@ -348,9 +349,11 @@ struct AttnArgs {
     const int8_t *x, *xe;
     int x_row;
     long long rows;
-    int heads, kv, group, d, width;  // group: query heads to a key head; width: columns of x
+    int heads, kv, group, d;         // group: query heads to a key head
+    int dp;                          // elements from a head to the next, a multiple of 16 (zeros past d)
+    int width;                       // and from a row to the next
     const int *off;                  // [n_seq + 1], or nullptr: one sequence
-    int n_seq, causal, vec;          // vec: every head's row starts at a multiple of 16 bytes
+    int n_seq, causal;
     int most;                        // tokens of the longest sequence
     float c;                         // scale log2(e)
     double scale;
@@ -362,6 +365,8 @@ struct AttnArgs {
     uint32_t *flags;
 };
 hipError_t launch_attention_fwd(const AttnArgs &a, hipStream_t st);
+// Rows of nh heads of d elements into heads of dp elements.
+hipError_t launch_attention_pad(const int8_t *x, long long rows, int nh, int d, int dp, int8_t *out, hipStream_t st);
 // The rounding of v16, p16 into y by rows.
 hipError_t launch_attention_round(const AttnArgs &a, hipStream_t st);
 
@@ -379,7 +384,7 @@ struct AttnKey {
 struct AttnBwd {
     const int8_t *o, *oe;
     const int8_t *dy, *dye;
-    int dy_row, dy_vec;
+    int dy_row;
     int2 *dots;    // [rows][heads]: dO . O, bits of |dO|
     int8_t *norm;  // [rows][kv]: bits of |v|
     AttnRow *row;  // [heads][rows]

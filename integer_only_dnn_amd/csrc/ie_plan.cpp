@@ -840,16 +840,17 @@ int *carve_dropout(Carve &c, long long rows, long long cols) {
     return c.take<int>((size_t)dropout_plan(rows, cols).grid);
 }
 
-AttFwdWs carve_attention_fwd(Carve &c, long long rows, long long heads, long long d) {
+AttFwdWs carve_attention_fwd(Carve &c, long long rows, long long heads, long long kv, long long d) {
     AttFwdWs w;
     w.v16 = c.take<int16_t>((size_t)(rows * heads * d));
     w.p16 = c.take<int16_t>((size_t)(rows * heads));
+    w.xp = c.take<int8_t>((size_t)(rows * (heads + 2 * kv) * r16(d)));
     return w;
 }
 
-size_t attention_fwd_ws(long long rows, long long heads, long long d) {
+size_t attention_fwd_ws(long long rows, long long heads, long long kv, long long d) {
     Carve c{nullptr, HEADER};
-    carve_attention_fwd(c, rows, heads, d);
+    carve_attention_fwd(c, rows, heads, kv, d);
     return align256(c.off);
 }
 
@@ -861,6 +862,8 @@ AttBwdWs carve_attention_bwd(Carve &c, long long rows, long long heads, long lon
     w.norm = c.take<int8_t>((size_t)(rows * kv));
     w.row = c.take<char>((size_t)(rows * heads * 32));
     w.key = c.take<char>((size_t)(rows * kv * 16));
+    w.xp = c.take<int8_t>((size_t)(rows * (heads + 2 * kv) * r16(d)));
+    w.dyp = c.take<int8_t>((size_t)(rows * heads * r16(d)));
     return w;
 }
 
@@ -931,7 +934,7 @@ ie_status check_attention(const ie_attention_desc *d, const ie_mat *X, long long
     if (!d->offsets != !d->n_seq) return IE_ERR_SHAPE;
     if (d->head_dim > ATT_HEAD_MAX || (uintptr_t)d->offsets % 4) return IE_ERR_UNSUPPORTED;
     // 64 rows of a tile within a 32-bit window
-    if (((long long)d->heads + 2ll * d->kv_heads) * d->head_dim > ATT_COLS_MAX) return IE_ERR_UNSUPPORTED;
+    if (((long long)d->heads + 2ll * d->kv_heads) * r16(d->head_dim) > ATT_COLS_MAX) return IE_ERR_UNSUPPORTED;
     // 2^-30 .. 2^30: r = scale log2(e) 2^e keeps clear of fp32's ends (a NaN is refused too)
     if (!(d->scale >= 0x1p-30f && d->scale <= 0x1p30f)) return IE_ERR_UNSUPPORTED;
     if (att_slots(X->rows, d->n_seq, 16) * d->heads > ATT_ITEMS_MAX) return IE_ERR_UNSUPPORTED;

@@ -445,18 +445,20 @@ constexpr long long ATT_ITEMS_MAX = 1ll << 30;  // workgroups of a launch
 inline long long att_slots(long long rows, long long n_seq, int bm) { return rows / bm + (n_seq > 0 ? n_seq : 1); }
 struct AttFwdWs {
     int16_t *v16, *p16;  // round-to-odd results and the needs of their heads
+    int8_t *xp;          // QKV with heads of r16(d), where it is not aligned
 };
-AttFwdWs carve_attention_fwd(Carve &c, long long rows, long long heads, long long d);
+AttFwdWs carve_attention_fwd(Carve &c, long long rows, long long heads, long long kv, long long d);
 struct AttBwdWs {
     int16_t *v16, *p16;
     void *dots;    // 8 bytes a row and head
     int8_t *norm;  // a row and key head
     void *row;     // 32 bytes a row and head
     void *key;     // 16 bytes a row and key head
+    int8_t *xp, *dyp;  // QKV and dO with heads of r16(d), where they are not aligned
 };
 AttBwdWs carve_attention_bwd(Carve &c, long long rows, long long heads, long long kv, long long d);
 size_t attention_bwd_ws(long long rows, long long heads, long long kv, long long d);
-size_t attention_fwd_ws(long long rows, long long heads, long long d);
+size_t attention_fwd_ws(long long rows, long long heads, long long kv, long long d);
 // Rotary positions: t threads per row with nu runs of eight elements each (nu
 // = 0: rows that do not come in such runs, or too long to be held).
 struct RopePlan {

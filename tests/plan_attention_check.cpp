@@ -38,13 +38,14 @@ static void workspaces() {
             for (long long d : d_) {
                 const long long h = hk[0], kv = hk[1];
                 {
-                    std::vector<char> b(attention_fwd_ws(rows, h, d) + 256);
+                    std::vector<char> b(attention_fwd_ws(rows, h, kv, d) + 256);
                     char *base = (char *)(((uintptr_t)b.data() + 255) & ~(uintptr_t)255);
                     Carve c{base, HEADER};
-                    const AttFwdWs w = carve_attention_fwd(c, rows, h, d);
+                    const AttFwdWs w = carve_attention_fwd(c, rows, h, kv, d);
                     touch(w.v16, rows * h * d);
                     touch(w.p16, rows * h);
-                    CHECK(align256(c.off) == attention_fwd_ws(rows, h, d));
+                    touch(w.xp, rows * (h + 2 * kv) * ((d + 15) / 16 * 16));
+                    CHECK(align256(c.off) == attention_fwd_ws(rows, h, kv, d));
                 }
                 {
                     std::vector<char> b(attention_bwd_ws(rows, h, kv, d) + 256);
@@ -57,6 +58,8 @@ static void workspaces() {
                     touch(w.norm, rows * kv);
                     touch((char *)w.row, rows * h * 32);
                     touch((char *)w.key, rows * kv * 16);
+                    touch(w.xp, rows * (h + 2 * kv) * ((d + 15) / 16 * 16));
+                    touch(w.dyp, rows * h * ((d + 15) / 16 * 16));
                     CHECK(align256(c.off) == attention_bwd_ws(rows, h, kv, d));
                 }
                 for (long long tokens : {0ll, 1ll, 255ll, 256ll, 257ll, 5000ll}) {
