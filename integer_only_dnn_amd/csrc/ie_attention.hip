@@ -74,12 +74,18 @@ hipError_t launch_attention_pad(const int8_t *x, long long rows, int nh, int d, 
 
 // A workgroup of four waves takes 64 queries of one head, 16 to a wave, one to
 // four lanes; keys pass through LDS 64 at a time, the next ones in flight.
-template <int DP, bool ROW, bool CAUSAL>
-__global__ __launch_bounds__(256, DP > 64 ? 3 : 4) void attn_fwd_kernel(AttnArgs p) {
+//
+// SHORT, for batches of short sequences: up to 256 keys have their scores kept
+// in registers between the passes (64 of them), so that q and k meet once; all
+// keys are in LDS at once, and the values, loaded with them, take their place.
+template <int DP, bool ROW, bool CAUSAL, bool SHORT>
+__global__ __launch_bounds__(256, DP > 64 ? 2 + !SHORT : 3 + !SHORT) void attn_fwd_kernel(AttnArgs p) {
     using T = HeadTile<DP>;
     constexpr int KS = T::KS, NE = DP / 16;
-    __shared__ __align__(16) int8_t sk[2][T::BYTES], sv[2][T::BYTES];
-    __shared__ __align__(16) float sf[2][64];
+    __shared__ __align__(16) int8_t tiles_lds[4][T::BYTES];
+    __shared__ __align__(16) float factors_lds[256];
+    int8_t(*sk)[T::BYTES] = tiles_lds, (*sv)[T::BYTES] = tiles_lds + 2;
+    float(*sf)[64] = (float(*)[64])factors_lds;
     const Item it = att_item(p, p.group);
     Span sp;
     int tile;
@@ -97,6 +103,127 @@ __global__ __launch_bounds__(256, DP > 64 ? 3 : 4) void attn_fwd_kernel(AttnArgs
     head_regs<KS>(base + (long long)qi * p.width + h * p.dp, ok, p.dp, lane, q);
     const int keys = CAUSAL ? min(n, q0 + 64) : n, tiles = (keys + 63) / 64;
     const int last = CAUSAL ? min(n, qw + 16) : n;  // keys of this wave
+
+    v4i hi[NE] = {}, lo[NE] = {};
+    uint32_t sum = 0, blocks = 0;
+    // the digits of four weights of keys 16 z + 4 quad .., given t - m or the scores' difference
+    auto weigh4 = [&](auto masked, const float (&d)[4], const float (&f)[4], float down, int z, int lim, int &dh, int &dl) {
+        int bits[4];
+        uint32_t whole_n[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float w = weight(d[i], r);
+            if (masked.value) w = 16 * z + i <= lim ? w : 0.0f;
+            bits[i] = __float_as_int(ROW ? __builtin_fmaf(w, f[i] * down, RINT_128) : w + RINT_128);
+            whole_n[i] = (uint32_t)(ROW ? __float_as_int(w + RINT_MAGIC) : bits[i]);
+        }
+        sum += whole_n[0] + whole_n[1];
+        sum += whole_n[2] + whole_n[3];
+        ++blocks;
+        digits4(bits[0], bits[1], bits[2], bits[3], dh, dl);
+    };
+    auto gather = [&](const int8_t *lds, const v4i &dh, const v4i &dl) {
+#pragma unroll
+        for (int e = 0; e < NE; ++e) {
+            const v4i vt = T::frag_t(lds, e, lane);
+            hi[e] = mfma(vt, dh, hi[e]);
+            lo[e] = mfma(vt, dl, lo[e]);
+        }
+    };
+    auto finish = [&](float m, int mi, int top) {
+        sum -= 4 * blocks * (uint32_t)(ROW ? RINT_BITS : RINT_BITS + 128);
+        sum = (uint32_t)col_reduce((int)sum, Add{});
+        const double inv = 1.0 / (double)sum;
+        double y[4 * NE];
+#pragma unroll
+        for (int e = 0; e < NE; ++e)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[4 * e + i] = __builtin_fma((double)hi[e][i], 256.0, (double)lo[e][i]) * inv;
+        const long long row = sp.a + qi;
+        store_odd(y, top, p.q, ok, p.d, lane, p.v16 + row * p.cols + h * p.d, p.p16 + row * p.parts + h);
+        if (p.stats && ok && lane < 16)
+            p.stats[row * p.heads + h] = int2{__float_as_int(ROW ? m : (float)mi * pow2f(eq)), (int)sum};
+    };
+
+    if constexpr (SHORT) {
+        if (n <= 256) {
+            T k[4], v[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                k[t].init(p.width, p.dp);
+                if (64 * t < keys) k[t].fetch(kh, p.width, 64 * t, keys, p.dp);
+            }
+            float fe = 0.0f;
+            if (ROW) fe = pow2f(clip_e(xe[min(tid, n - 1)]));
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                v[t].init(p.width, p.dp);
+                if (64 * t < keys) v[t].fetch(vh, p.width, 64 * t, keys, p.dp);
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                if (64 * t < keys) k[t].put(tiles_lds[t]);
+            if (ROW) factors_lds[tid] = fe;
+            __syncthreads();
+            float s[16][4], m = -__builtin_inff(), em = 0.0f;
+            int mi = -(1 << 30);
+            const int lim = (CAUSAL ? qi : n - 1) - 4 * quad;  // keys 16 z + i <= lim are seen
+            auto whole = [&](int z) { return 16 * z + 16 <= (CAUSAL ? qw + 1 : n); };
+            auto score = [&](auto masked, int z) {
+                v4i acc = {0, 0, 0, 0};
+#pragma unroll
+                for (int i = 0; i < KS; ++i) acc = mfma(T::frag_r(tiles_lds[z >> 2], z & 3, i, lane), q[i], acc);
+                const float4 x = ROW ? *(const float4 *)&factors_lds[16 * z + 4 * quad] : float4{1, 1, 1, 1};
+                const float f[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    s[z][i] = (float)acc[i] * f[i];
+                    const bool on = !masked.value || 16 * z + i <= lim;
+                    m = fmaxf(m, on ? s[z][i] : -__builtin_inff());
+                    if (ROW) em = fmaxf(em, on ? f[i] : 0.0f);
+                }
+            };
+            if (!idle) {
+#pragma unroll
+                for (int z = 0; z < 16; ++z)
+                    if (16 * z < last) {
+                        if (whole(z)) score(Bool<false>{}, z);
+                        else score(Bool<true>{}, z);
+                    }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                if (64 * t < keys) v[t].put(tiles_lds[t]);
+            __syncthreads();
+            if (idle) return;
+            m = col_max(m);
+            em = col_max(em);
+            const int top = ROW ? (__float_as_int(em) >> 23) - 127 : eq;
+            const float down = ROW ? pow2f(-top) : 1.0f;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                if (64 * t >= last) break;
+                v4i dh = {0, 0, 0, 0}, dl = {0, 0, 0, 0};
+#pragma unroll
+                for (int z = 4 * t; z < 4 * t + 4; ++z) {
+                    if (16 * z >= last) continue;
+                    const float4 x = ROW ? *(const float4 *)&factors_lds[16 * z + 4 * quad] : float4{1, 1, 1, 1};
+                    const float f[4] = {x.x, x.y, x.z, x.w};
+                    const float d[4] = {s[z][0] - m, s[z][1] - m, s[z][2] - m, s[z][3] - m};
+                    int a, c;
+                    if (whole(z)) weigh4(Bool<false>{}, d, f, down, z, lim, a, c);
+                    else weigh4(Bool<true>{}, d, f, down, z, lim, a, c);
+                    dh[z & 3] = a;
+                    dl[z & 3] = c;
+                }
+                gather(tiles_lds[t], dh, dl);
+            }
+            mi = (int)m;  // where all rows share an exponent the scores are whole
+            finish(m, mi, top);
+            return;
+        }
+    }
 
     T k, v;
     k.init(p.width, p.dp);
@@ -173,8 +300,6 @@ __global__ __launch_bounds__(256, DP > 64 ? 3 : 4) void attn_fwd_kernel(AttnArgs
     __syncthreads();
 
     // second pass: weights and the sums they enter
-    v4i hi[NE] = {}, lo[NE] = {};
-    uint32_t sum = 0, blocks = 0;
     auto weigh = [&](auto masked, int t, v4i &dh, v4i &dl) {
         const int lim = limit(t);
 #pragma unroll
@@ -183,22 +308,12 @@ __global__ __launch_bounds__(256, DP > 64 ? 3 : 4) void attn_fwd_kernel(AttnArgs
             dl[z] = 0;
             if (masked.value && 64 * t + 16 * z >= last) continue;
             const v4i acc = scores(t, z);
-            float f[4];
+            float f[4], d[4];
             factors(t, z, f);
-            int bits[4];
-            uint32_t whole_n[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float w = ROW ? weight(__builtin_fmaf((float)acc[i], f[i], -m), r) : weight((float)(acc[i] - mi), r);
-                if (masked.value) w = 16 * z + i <= lim ? w : 0.0f;
-                bits[i] = __float_as_int(ROW ? __builtin_fmaf(w, f[i] * down, RINT_128) : w + RINT_128);
-                whole_n[i] = (uint32_t)(ROW ? __float_as_int(w + RINT_MAGIC) : bits[i]);
-            }
-            sum += whole_n[0] + whole_n[1];
-            sum += whole_n[2] + whole_n[3];
-            ++blocks;
+            for (int i = 0; i < 4; ++i) d[i] = ROW ? __builtin_fmaf((float)acc[i], f[i], -m) : (float)(acc[i] - mi);
             int a, c;
-            digits4(bits[0], bits[1], bits[2], bits[3], a, c);
+            weigh4(masked, d, f, down, z, lim, a, c);
             dh[z] = a;
             dl[z] = c;
         }
@@ -212,26 +327,9 @@ __global__ __launch_bounds__(256, DP > 64 ? 3 : 4) void attn_fwd_kernel(AttnArgs
         v4i dh, dl;
         if (whole(t)) weigh(Bool<false>{}, t, dh, dl);
         else weigh(Bool<true>{}, t, dh, dl);
-#pragma unroll
-        for (int e = 0; e < NE; ++e) {
-            const v4i vt = T::frag_t(sv[t & 1], e, lane);
-            hi[e] = mfma(vt, dh, hi[e]);
-            lo[e] = mfma(vt, dl, lo[e]);
-        }
+        gather(sv[t & 1], dh, dl);
     }
-    if (idle) return;
-    sum -= 4 * blocks * (uint32_t)(ROW ? RINT_BITS : RINT_BITS + 128);
-    sum = (uint32_t)col_reduce((int)sum, Add{});
-    const double inv = 1.0 / (double)sum;
-    double y[4 * NE];
-#pragma unroll
-    for (int e = 0; e < NE; ++e)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[4 * e + i] = __builtin_fma((double)hi[e][i], 256.0, (double)lo[e][i]) * inv;
-    const long long row = sp.a + qi;
-    store_odd(y, top, p.q, ok, p.d, lane, p.v16 + row * p.cols + h * p.d, p.p16 + row * p.parts + h);
-    if (p.stats && ok && lane < 16)
-        p.stats[row * p.heads + h] = int2{__float_as_int(ROW ? m : (float)mi * pow2f(eq)), (int)sum};
+    if (!idle) finish(m, mi, top);
 }
 
 // Rows of heads, each rounded to odd at two bits below its own need, into one
@@ -283,16 +381,23 @@ hipError_t launch_attention_round(const AttnArgs &a, hipStream_t st) {
     return hipGetLastError();
 }
 
-template <int DP>
+template <int DP, bool SHORT>
 static void fwd(const AttnArgs &a, hipStream_t st) {
     const dim3 grid(att_grid(att_slots(a.rows, a.n_seq, 64), a.kv, a.group)), block(256);
     if (a.x_row) {
-        if (a.causal) hipLaunchKernelGGL((attn_fwd_kernel<DP, true, true>), grid, block, 0, st, a);
-        else hipLaunchKernelGGL((attn_fwd_kernel<DP, true, false>), grid, block, 0, st, a);
+        if (a.causal) hipLaunchKernelGGL((attn_fwd_kernel<DP, true, true, SHORT>), grid, block, 0, st, a);
+        else hipLaunchKernelGGL((attn_fwd_kernel<DP, true, false, SHORT>), grid, block, 0, st, a);
     } else {
-        if (a.causal) hipLaunchKernelGGL((attn_fwd_kernel<DP, false, true>), grid, block, 0, st, a);
-        else hipLaunchKernelGGL((attn_fwd_kernel<DP, false, false>), grid, block, 0, st, a);
+        if (a.causal) hipLaunchKernelGGL((attn_fwd_kernel<DP, false, true, SHORT>), grid, block, 0, st, a);
+        else hipLaunchKernelGGL((attn_fwd_kernel<DP, false, false, SHORT>), grid, block, 0, st, a);
     }
+}
+
+template <int DP>
+static void fwd(const AttnArgs &a, hipStream_t st) {
+    // sequences of up to 256 tokens on the average: most have their scores in registers
+    if (a.rows <= 256ll * max(a.n_seq, 1)) fwd<DP, true>(a, st);
+    else fwd<DP, false>(a, st);
 }
 
 hipError_t launch_attention_fwd(const AttnArgs &a, hipStream_t st) {
