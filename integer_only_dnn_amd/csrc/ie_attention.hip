@@ -79,7 +79,7 @@ hipError_t launch_attention_pad(const int8_t *x, long long rows, int nh, int d, 
 // in registers between the passes (64 of them), so that q and k meet once; all
 // keys are in LDS at once, and the values, loaded with them, take their place.
 template <int DP, bool ROW, bool CAUSAL, bool SHORT>
-__global__ __launch_bounds__(256, DP > 64 ? 2 + !SHORT : 3 + !SHORT) void attn_fwd_kernel(AttnArgs p) {
+__global__ __launch_bounds__(256, DP > 64 ? 3 : 4) void attn_fwd_kernel(AttnArgs p) {
     using T = HeadTile<DP>;
     constexpr int KS = T::KS, NE = DP / 16;
     __shared__ __align__(16) int8_t tiles_lds[4][T::BYTES];
@@ -168,27 +168,55 @@ __global__ __launch_bounds__(256, DP > 64 ? 2 + !SHORT : 3 + !SHORT) void attn_f
             float s[16][4], m = -__builtin_inff(), em = 0.0f;
             int mi = -(1 << 30);
             const int lim = (CAUSAL ? qi : n - 1) - 4 * quad;  // keys 16 z + i <= lim are seen
-            auto whole = [&](int z) { return 16 * z + 16 <= (CAUSAL ? qw + 1 : n); };
-            auto score = [&](auto masked, int z) {
-                v4i acc = {0, 0, 0, 0};
+            auto whole = [&](int t) { return 64 * t + 64 <= (CAUSAL ? qw + 1 : n); };
+            auto score = [&](auto masked, int t) {
+                v4i acc[4];
+                float4 f[4];
 #pragma unroll
-                for (int i = 0; i < KS; ++i) acc = mfma(T::frag_r(tiles_lds[z >> 2], z & 3, i, lane), q[i], acc);
-                const float4 x = ROW ? *(const float4 *)&factors_lds[16 * z + 4 * quad] : float4{1, 1, 1, 1};
-                const float f[4] = {x.x, x.y, x.z, x.w};
+                for (int z = 0; z < 4; ++z) {
+                    acc[z] = v4i{0, 0, 0, 0};
+                    f[z] = float4{1, 1, 1, 1};
+                    if (masked.value && 64 * t + 16 * z >= last) continue;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    s[z][i] = (float)acc[i] * f[i];
-                    const bool on = !masked.value || 16 * z + i <= lim;
-                    m = fmaxf(m, on ? s[z][i] : -__builtin_inff());
-                    if (ROW) em = fmaxf(em, on ? f[i] : 0.0f);
+                    for (int i = 0; i < KS; ++i) acc[z] = mfma(T::frag_r(tiles_lds[t], z, i, lane), q[i], acc[z]);
+                    if (ROW) f[z] = *(const float4 *)&factors_lds[64 * t + 16 * z + 4 * quad];
+                }
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    if (masked.value && 64 * t + 16 * z >= last) continue;
+                    const float fs[4] = {f[z].x, f[z].y, f[z].z, f[z].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float x = (float)acc[z][i] * fs[i];
+                        const bool on = !masked.value || 64 * t + 16 * z + i <= lim;
+                        s[4 * t + z][i] = x;
+                        m = fmaxf(m, on ? x : -__builtin_inff());
+                        if (ROW) em = fmaxf(em, on ? fs[i] : 0.0f);
+                    }
+                }
+            };
+            auto weigh = [&](auto masked, int t, float down, v4i &dh, v4i &dl) {
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    dh[z] = 0;
+                    dl[z] = 0;
+                    if (masked.value && 64 * t + 16 * z >= last) continue;
+                    const float4 x = ROW ? *(const float4 *)&factors_lds[64 * t + 16 * z + 4 * quad] : float4{1, 1, 1, 1};
+                    const float f[4] = {x.x, x.y, x.z, x.w};
+                    const float(&y)[4] = s[4 * t + z];
+                    const float d[4] = {y[0] - m, y[1] - m, y[2] - m, y[3] - m};
+                    int a, c;
+                    weigh4(masked, d, f, down, 4 * t + z, lim, a, c);
+                    dh[z] = a;
+                    dl[z] = c;
                 }
             };
             if (!idle) {
 #pragma unroll
-                for (int z = 0; z < 16; ++z)
-                    if (16 * z < last) {
-                        if (whole(z)) score(Bool<false>{}, z);
-                        else score(Bool<true>{}, z);
+                for (int t = 0; t < 4; ++t)
+                    if (64 * t < last) {
+                        if (whole(t)) score(Bool<false>{}, t);
+                        else score(Bool<true>{}, t);
                     }
             }
             __syncthreads();
@@ -204,19 +232,9 @@ __global__ __launch_bounds__(256, DP > 64 ? 2 + !SHORT : 3 + !SHORT) void attn_f
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 if (64 * t >= last) break;
-                v4i dh = {0, 0, 0, 0}, dl = {0, 0, 0, 0};
-#pragma unroll
-                for (int z = 4 * t; z < 4 * t + 4; ++z) {
-                    if (16 * z >= last) continue;
-                    const float4 x = ROW ? *(const float4 *)&factors_lds[16 * z + 4 * quad] : float4{1, 1, 1, 1};
-                    const float f[4] = {x.x, x.y, x.z, x.w};
-                    const float d[4] = {s[z][0] - m, s[z][1] - m, s[z][2] - m, s[z][3] - m};
-                    int a, c;
-                    if (whole(z)) weigh4(Bool<false>{}, d, f, down, z, lim, a, c);
-                    else weigh4(Bool<true>{}, d, f, down, z, lim, a, c);
-                    dh[z & 3] = a;
-                    dl[z & 3] = c;
-                }
+                v4i dh, dl;
+                if (whole(t)) weigh(Bool<false>{}, t, down, dh, dl);
+                else weigh(Bool<true>{}, t, down, dh, dl);
                 gather(tiles_lds[t], dh, dl);
             }
             mi = (int)m;  // where all rows share an exponent the scores are whole
