@@ -1302,6 +1302,7 @@ ie_status ie_attention_fwd(const ie_attention_desc *d, const ie_mat *QKV, const 
     a.ye = O->exp;
     a.cols = (int)O->cols;
     a.parts = d->heads;
+    a.part = d->head_dim;
     a.q = mat_q(O);
     a.out_vec = d->head_dim % 16 == 0 && aligned(O->mant, 8);
     return hip_status(launch_attention_fwd(a, (hipStream_t)stream));
@@ -1341,6 +1342,7 @@ ie_status ie_attention_bwd(const ie_attention_desc *d, const ie_mat *QKV, const 
     a.ye = dQKV->exp;
     a.cols = (int)dQKV->cols;
     a.parts = d->heads + 2 * d->kv_heads;
+    a.part = d->head_dim;
     a.q = mat_q(dQKV);
     a.out_vec = d->head_dim % 16 == 0 && aligned(dQKV->mant, 8);
     AttnBwd b;
@@ -1507,8 +1509,8 @@ ie_status ie_attention_cache(const ie_attention_desc *d, const ie_mat *Q, const 
     a.y = O->mant;
     a.ye = O->exp;
     a.cols = (int)cols;
-    a.parts = d->heads;
     a.q = mat_q(O);
+    a.out_vec = aligned(O->mant, 8);
     CacheArgs ca = cache_args(c, ws);
     ca.table = pages;
     ca.lengths = lengths;
@@ -1518,7 +1520,6 @@ ie_status ie_attention_cache(const ie_attention_desc *d, const ie_mat *Q, const 
     ca.blocks = (int)((tokens + CACHE_BLOCK - 1) / CACHE_BLOCK);
     ca.num = w.num;
     ca.top = (int4 *)w.top;
-    ca.count = w.count;
     return hip_status(launch_cache_attention(ca, a, (hipStream_t)stream));
 }
 

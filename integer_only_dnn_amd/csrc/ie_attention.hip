@@ -350,7 +350,7 @@ __global__ __launch_bounds__(256, DP > 64 ? 3 : 4) void attn_fwd_kernel(AttnArgs
     if (!idle) finish(m, mi, top);
 }
 
-// Rows of heads, each rounded to odd at two bits below its own need, into one
+// Rows of parts (heads), each rounded to odd at two bits below its own need, into one
 // exponent a row: a wave per row, eight results a lane and turn.
 __global__ __launch_bounds__(256) void attn_round_kernel(AttnArgs p) {
     const int lane = threadIdx.x & 63;
@@ -377,7 +377,7 @@ __global__ __launch_bounds__(256) void attn_round_kernel(AttnArgs p) {
     int8_t *y = p.y + row * p.cols;
     if (p.out_vec) {
         for (int c = 8 * lane; c < p.cols; c += 512) {
-            const int s = e - ((int)need[c / p.d] - 2);
+            const int s = e - ((int)need[c / p.part] - 2);
             const v4i w = *(const v4i *)(v + c);
             int o[8];
 #pragma unroll
@@ -388,7 +388,7 @@ __global__ __launch_bounds__(256) void attn_round_kernel(AttnArgs p) {
             *(uint2 *)(y + c) = uint2{pack4(o[0], o[1], o[2], o[3]), pack4(o[4], o[5], o[6], o[7])};
         }
     } else {
-        for (int c = lane; c < p.cols; c += 64) y[c] = (int8_t)rne_shift32((int)v[c], e - ((int)need[c / p.d] - 2));
+        for (int c = lane; c < p.cols; c += 64) y[c] = (int8_t)rne_shift32((int)v[c], e - ((int)need[c / p.part] - 2));
     }
 }
 

@@ -358,10 +358,10 @@ struct AttnArgs {
     float c;                         // scale log2(e)
     double scale;
     int2 *stats;                     // [rows][heads]: largest score, sum of weights
-    // results: round-to-odd values [rows][cols] and needs [rows][parts] of heads of d
+    // results: round-to-odd values [rows][cols] and needs [rows][parts] of `part` columns each
     int16_t *v16, *p16;
     int8_t *y, *ye;
-    int cols, parts, q, out_vec;     // out_vec: rows of y can be written eight mantissas at a time
+    int cols, parts, part, q, out_vec;  // out_vec: rows of y can be written eight mantissas at a time
     uint32_t *flags;
 };
 hipError_t launch_attention_fwd(const AttnArgs &a, hipStream_t st);
@@ -420,7 +420,6 @@ struct CacheArgs {
     int n, per, tokens, blocks;  // tokens: per pages; blocks of CACHE_BLOCK in them
     int *num;                    // [n][blocks][heads][d]
     int4 *top;                   // [n][blocks][heads]: maximum, sum, exponent
-    int *count;                  // [n]: heads that are done
     uint32_t *flags;
 };
 hipError_t launch_cache_store(const CacheArgs &c, long long rows, const int8_t *x, const int8_t *xe, int x_row, int width,

@@ -900,9 +900,8 @@ CacheWs carve_attention_cache(Carve &c, long long n, long long tokens, long long
     CacheWs w;
     w.num = c.take<int>((size_t)n * blocks * (size_t)(heads * d));
     w.top = c.take<char>((size_t)n * blocks * (size_t)heads * 16);
-    w.count = c.take<int>((size_t)n);
     w.v16 = c.take<int16_t>((size_t)n * (size_t)(heads * d));
-    w.p16 = c.take<int16_t>((size_t)n * (size_t)heads);
+    w.p16 = c.take<int16_t>((size_t)n * (size_t)(heads * d / 16));  // a need for 16 elements at least
     return w;
 }
 

@@ -479,7 +479,6 @@ constexpr long long CACHE_TOKENS_MAX = 1ll << 23;  // sums of weighted blocks st
 struct CacheWs {
     int *num;
     void *top;  // 16 bytes a block and head
-    int *count;
     int16_t *v16, *p16;
 };
 CacheWs carve_attention_cache(Carve &c, long long n, long long tokens, long long heads, long long d);

@@ -71,9 +71,8 @@ static void workspaces() {
                     const long long blocks = (tokens + CACHE_BLOCK - 1) / CACHE_BLOCK;
                     touch(w.num, rows * blocks * h * d);
                     touch((char *)w.top, rows * blocks * h * 16);
-                    touch(w.count, rows);
                     touch(w.v16, rows * h * d);
-                    touch(w.p16, rows * h);
+                    touch(w.p16, rows * (h * d / 16));
                     CHECK(align256(c.off) == attention_cache_ws(rows, tokens, h, d));
                 }
             }
