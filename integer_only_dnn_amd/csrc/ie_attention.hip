@@ -20,37 +20,6 @@
 
 namespace ie {
 
-// 16 mantissas of a head from column 16 c on, at any alignment; past d: zeros.
-__device__ __forceinline__ v4i head16(const int8_t *head, int c, int d) {
-    v4i v = {0, 0, 0, 0};
-    const int n = d - 16 * c;
-    const int8_t *p = head + 16 * c;
-    if (n >= 16) {
-        __builtin_memcpy(&v, p, 16);
-    } else if (n > 0) {
-        // n = 8 a + 4 b + 2 c + e, from the top down: each piece shifts the ones above it up
-        uint64_t lo = 0, hi = 0;
-        if (n & 8) __builtin_memcpy(&lo, p, 8);
-        const int8_t *t = p + (n & 8);
-        uint64_t w = 0;
-        if (n & 1) w = (uint8_t)t[n & 6];
-        if (n & 2) {
-            uint16_t x;
-            __builtin_memcpy(&x, t + (n & 4), 2);
-            w = w << 16 | x;
-        }
-        if (n & 4) {
-            uint32_t x;
-            __builtin_memcpy(&x, t, 4);
-            w = w << 32 | x;
-        }
-        if (n & 8) hi = w;
-        else lo = w;
-        v = v4i{(int)(uint32_t)lo, (int)(uint32_t)(lo >> 32), (int)(uint32_t)hi, (int)(uint32_t)(hi >> 32)};
-    }
-    return v;
-}
-
 // Rows of nh heads of d elements into heads of dp (a multiple of 16), zeros in
 // between: what the kernels read where heads do not start at multiples of 16
 // bytes.

@@ -25,120 +25,86 @@ namespace ie {
 __device__ __forceinline__ int bits_of(uint32_t n) { return 32 - __clz((int)n); }  // n = 0: 0
 
 // A row's products of dO with O and itself by head, and the norms of its
-// values: 16 lanes a head, eight elements each.
+// values: NL lanes a head, 16 elements each.
+template <int NL>
 __global__ __launch_bounds__(256) void attn_dot_kernel(AttnArgs p, AttnBwd b) {
-    const int lane = threadIdx.x & 15, parts = p.heads + p.kv;
-    const long long total = p.rows * parts;
-    for (long long i = (long long)blockIdx.x * 16 + (threadIdx.x >> 4); i < (total + 15) / 16 * 16; i += (long long)gridDim.x * 16) {
-        const long long row = i < total ? i / parts : 0;
-        const int part = i < total ? (int)(i - row * parts) : 0;
-        uint32_t x[2] = {0, 0}, y[2] = {0, 0};
-        if (part < p.heads) {
-            load_run<8>(b.dy + (row * p.heads + part) * p.dp, 8 * lane, p.d, x);
-            load_run<8>(b.o + (row * p.heads + part) * p.d, 8 * lane, p.d, y);
-        } else {
-            load_run<8>(p.x + row * p.width + (long long)(part + p.kv) * p.dp, 8 * lane, p.d, x);
+    constexpr int PB = 256 / NL;
+    const int lane = threadIdx.x % NL, parts = p.heads + p.kv;
+    const long long total = p.rows * parts, step = (long long)gridDim.x * PB;
+    for (long long i0 = (long long)blockIdx.x * PB; i0 < total; i0 += step) {
+        const long long i = min(i0 + threadIdx.x / NL, total - 1);
+        const long long row = i / parts;
+        const int part = (int)(i - row * parts);
+        const bool head = part < p.heads;
+        v4i x = {0, 0, 0, 0}, y = {0, 0, 0, 0};
+        if (16 * lane < p.dp) {
+            x = *(const v4i *)((head ? b.dy + (row * p.heads + part) * p.dp : p.x + row * p.width + (long long)(part + p.kv) * p.dp) +
+                               16 * lane);
+            if (head) y = head16(b.o + (row * p.heads + part) * p.d, lane, p.d);
         }
         int dot = 0, sq = 0;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            dot = __builtin_amdgcn_sdot4((int)x[k], (int)y[k], dot, false);
-            sq = __builtin_amdgcn_sdot4((int)x[k], (int)x[k], sq, false);
+        for (int k = 0; k < 4; ++k) {
+            dot = __builtin_amdgcn_sdot4(x[k], y[k], dot, false);
+            sq = __builtin_amdgcn_sdot4(x[k], x[k], sq, false);
         }
-        dot = lane_reduce<16>(dot, Add{});
-        sq = lane_reduce<16>(sq, Add{});
-        if (lane || i >= total) continue;
+        dot = lane_reduce<NL>(dot, Add{});
+        sq = lane_reduce<NL>(sq, Add{});
+        if (lane || i != i0 + threadIdx.x / NL) continue;
         const int size = (bits_of((uint32_t)sq) + 1) >> 1;  // |.| < 2^size
-        if (part < p.heads) b.dots[row * p.heads + part] = int2{dot, size};
+        if (head) b.dots[row * p.heads + part] = int2{dot, size};
         else b.norm[row * p.kv + part - p.heads] = (int8_t)size;
     }
 }
 
-// The scales of one sequence and key head: a workgroup each.  Suffix maxima
-// (causal: a key meets the queries from its own on) by runs of a thread.
+// The scales of the queries of one key head, a token a thread (workgroups of
+// 256 tokens of a sequence, each of which finds the sequence's maxima itself),
+// and for its keys the bounds that dK and dV are scaled by.
 __global__ __launch_bounds__(256) void attn_scale_kernel(AttnArgs p, AttnBwd b) {
-    __shared__ int sh[4];
-    __shared__ int ska[256], skl[256];
-    const int seq = blockIdx.x / p.kv, kvh = blockIdx.x - seq * p.kv, tid = threadIdx.x;
-    const Span sp = seq_span(p, seq);
-    if (sp.n <= 0) return;
+    __shared__ int sh[4][4];
+    const Item it = att_item(p, 1);
+    Span sp;
+    int tile;
+    if (!rank_tile<false>(p, it.rank, 256, sp, tile)) return;
+    const int tid = threadIdx.x;
     int e_top = ATT_E_LO, n_top = -4096, r_top = -4096, o_top = E_MIN;
     for (int t = tid; t < sp.n; t += 256) {
         const long long row = sp.a + t;
-        const int e = clip_e(p.xe[p.x_row ? row : 0]), nu = b.norm[row * p.kv + kvh] + e;
+        const int e = clip_e(p.xe[p.x_row ? row : 0]), nu = b.norm[row * p.kv + it.kvh] + e;
         e_top = max(e_top, e);
         n_top = max(n_top, nu);
         r_top = max(r_top, nu + e);
         o_top = max(o_top, (int)b.dye[b.dy_row ? row : 0]);
     }
-    e_top = row_reduce<256>(e_top, Max{}, sh);
-    n_top = row_reduce<256>(n_top, Max{}, sh);
-    r_top = row_reduce<256>(r_top, Max{}, sh);
-    o_top = row_reduce<256>(o_top, Max{}, sh);
-    // alpha and lambda of a query: a_i < 2^alpha, a_i |u| 2^(e_i) < 2^lambda
-    auto query = [&](int t, int g, int &alpha, int &lam, float &a, float &dot, int &rise) {
-        const long long row = sp.a + t;
-        const int h = kvh * p.group + g, e = clip_e(p.xe[p.x_row ? row : 0]);
-        const int2 d = b.dots[row * p.heads + h];
-        const int eo = clip_e(b.oe[row]), delta = bits_of((uint32_t)abs(d.x)) + eo;
-        const uint32_t sum = (uint32_t)p.stats[row * p.heads + h].y;
-        a = (float)(1.0 / (double)sum) * pow2f(max((int)b.dye[b.dy_row ? row : 0] - o_top, -60));
-        alpha = (__float_as_int(a) >> 23) - 126;
-        lam = alpha + e + max(d.y + n_top, delta) + 1;
-        dot = (float)d.x * pow2f(eo);
-        rise = max(d.y + r_top, delta + e_top) + 1;
-    };
-    const int per = (sp.n + 255) / 256, t0 = min(tid * per, sp.n), t1 = min(t0 + per, sp.n);
+    e_top = row_reduce_once<256>(e_top, Max{}, sh[0]);
+    n_top = row_reduce_once<256>(n_top, Max{}, sh[1]);
+    r_top = row_reduce_once<256>(r_top, Max{}, sh[2]);
+    o_top = row_reduce_once<256>(o_top, Max{}, sh[3]);
+    const int t = 256 * tile + tid;
+    if (t >= sp.n) return;
+    const long long row = sp.a + t;
+    const int e = clip_e(p.xe[p.x_row ? row : 0]), eo = clip_e(b.oe[row]), ed = b.dye[b.dy_row ? row : 0];
+    const float down = pow2f(max(ed - o_top, -60)), r = p.c * pow2f(e);
     int ka = -4096, kl = -4096;
-    for (int t = t0; t < t1; ++t)
-        for (int g = 0; g < p.group; ++g) {
-            int alpha, lam, rise;
-            float a, dot;
-            query(t, g, alpha, lam, a, dot, rise);
-            ka = max(ka, alpha);
-            kl = max(kl, lam);
-        }
-    ska[tid] = ka;
-    skl[tid] = kl;
-    __syncthreads();
-    int later_a = -4096, later_l = -4096, all_a = -4096, whole = -4096;
-    for (int i = 0; i < 256; ++i) {
-        all_a = max(all_a, ska[i]);
-        whole = max(whole, skl[i]);
-        if (i > tid) {
-            later_a = max(later_a, ska[i]);
-            later_l = max(later_l, skl[i]);
-        }
+    for (int g = 0; g < p.group; ++g) {
+        const int h = it.kvh * p.group + g;
+        const int2 d = b.dots[row * p.heads + h], st = p.stats[row * p.heads + h];
+        const int delta = bits_of((uint32_t)abs(d.x)) + eo, rise = max(d.y + r_top, delta + e_top) + 1;
+        AttnRow q;
+        q.m = __int_as_float(st.x);
+        q.r = r;
+        q.dot = (float)d.x * pow2f(eo);
+        q.a = (float)(1.0 / (double)(uint32_t)st.y) * down;  // a < 2^alpha
+        q.s = pow2f(max(-rise, -126));
+        q.e = rise + ed;
+        q.o_top = o_top;
+        q.ek = e;
+        b.row[(long long)h * p.rows + row] = q;
+        const int alpha = (__float_as_int(q.a) >> 23) - 126;
+        ka = max(ka, alpha);
+        kl = max(kl, alpha + e + max(d.y + n_top, delta) + 1);  // a |u| 2^e < 2^kl
     }
-    for (int t = t1 - 1; t >= t0; --t) {
-        const long long row = sp.a + t;
-        const int e = clip_e(p.xe[p.x_row ? row : 0]), ed = b.dye[b.dy_row ? row : 0];
-        for (int g = 0; g < p.group; ++g) {
-            int alpha, lam, rise;
-            float a, dot;
-            query(t, g, alpha, lam, a, dot, rise);
-            later_a = max(later_a, alpha);
-            later_l = max(later_l, lam);
-            const int h = kvh * p.group + g;
-            const int2 st = p.stats[row * p.heads + h];
-            AttnRow q;
-            q.m = __int_as_float(st.x);
-            q.r = p.c * pow2f(e);
-            q.dot = dot;
-            q.a = a;
-            q.b = (float)((double)a * pow2(e - whole));
-            q.s = pow2f(max(-rise, -126));
-            q.e = rise + ed;
-            q.sum = (uint32_t)st.y;
-            b.row[(long long)h * p.rows + row] = q;
-        }
-        AttnKey k;
-        k.kappa = p.causal ? later_a : all_a;
-        k.lambda = max((p.causal ? later_l : whole) - whole, -96);
-        k.ev = k.kappa + o_top;
-        k.ek = k.lambda - 6 + whole + o_top;
-        b.key[(long long)kvh * p.rows + row] = k;
-    }
+    b.key[(long long)it.kvh * p.rows + row] = AttnKey{(int16_t)ka, (int16_t)kl};
 }
 
 // dQ: a workgroup of four waves takes 64 queries of a head, 16 to a wave, one
@@ -226,7 +192,7 @@ __global__ __launch_bounds__(256, DP > 64 ? 2 : 3) void attn_dq_kernel(AttnArgs 
         }
     }
     if (idle) return;
-    const double rate = p.scale / (double)st.sum;
+    const double rate = p.scale / (double)(uint32_t)p.stats[min(row, sp.a + n - 1ll) * p.heads + h].y;
     double y[4 * NE];
 #pragma unroll
     for (int e = 0; e < NE; ++e)
@@ -247,6 +213,7 @@ __global__ __launch_bounds__(256, DP > 64 ? 1 : 2) void attn_dkv_kernel(AttnArgs
     constexpr int KS = T::KS, NE = DP / 16, KEYS = 64 / SPLIT, NB = SPLIT == 1 ? 2 : 1;
     __shared__ __align__(16) int8_t sq[NB * SPLIT][T::BYTES], sg[NB * SPLIT][T::BYTES];
     __shared__ __align__(16) float sr[NB * SPLIT][5][64];
+    __shared__ int smark[2][4];
     const Item it = att_item(p, 1);
     Span sp;
     int tile;
@@ -261,9 +228,34 @@ __global__ __launch_bounds__(256, DP > 64 ? 1 : 2) void attn_dkv_kernel(AttnArgs
     v4i k[KS], v[KS];
     head_regs<KS>(base + (long long)kj * p.width + (long long)(p.heads + it.kvh) * p.dp, ok, p.dp, lane, k);
     head_regs<KS>(base + (long long)kj * p.width + (long long)(p.heads + p.kv + it.kvh) * p.dp, ok, p.dp, lane, v);
-    const AttnKey key = bw.key[(long long)it.kvh * p.rows + sp.a + min(kj, n - 1)];
     const float f = pow2f(clip_e(p.xe[p.x_row ? sp.a + min(kj, n - 1) : 0]));
-    const float sv = pow2f(min(-key.kappa, 126)), sk = pow2f(min(6 - key.lambda, 126));
+    // the largest bounds of all queries (none: -4096 each), and of those that see a key
+    const AttnKey *marks = bw.key + (long long)it.kvh * p.rows + sp.a;
+    AttnKey all = ATT_NO_KEY, seen, seen_later = ATT_NO_KEY;
+    for (int t = tid; t < n; t += 256) {
+        const AttnKey x = marks[t];
+        all = __builtin_elementwise_max(all, x);
+        if (CAUSAL && t >= k0 + KEYS) seen_later = __builtin_elementwise_max(seen_later, x);
+    }
+    auto most = [](int x, int y) {
+        return __builtin_bit_cast(int, __builtin_elementwise_max(__builtin_bit_cast(AttnKey, x), __builtin_bit_cast(AttnKey, y)));
+    };
+    all = __builtin_bit_cast(AttnKey, row_reduce_once<256>(__builtin_bit_cast(int, all), most, smark[0]));
+    seen = all;
+    if (CAUSAL) {
+        // queries behind the tile, then those of the tile from the key's own on
+        int later = row_reduce_once<256>(__builtin_bit_cast(int, seen_later), most, smark[1]);
+        int own = lane < KEYS && k0 + lane < n ? __builtin_bit_cast(int, marks[k0 + lane]) : __builtin_bit_cast(int, ATT_NO_KEY);
+#pragma unroll
+        for (int o = 1; o < KEYS; o <<= 1) {
+            const int x = __shfl_down(own, o, 64);
+            own = lane + o < KEYS ? most(own, x) : own;
+        }
+        seen = __builtin_bit_cast(AttnKey, most(later, __shfl(own, kj - k0, 64)));
+    }
+    const int whole = all[1], kappa = seen[0], lambda = max(seen[1] - whole, -96);
+    const int o_top = bw.row[(long long)it.kvh * p.group * p.rows + sp.a].o_top;
+    const float sv = pow2f(min(-kappa, 126)), sk = pow2f(min(6 - lambda, 126));
     const int first = CAUSAL ? k0 / 64 : 0, tiles = (n + 63) / 64 - first, total = tiles * p.group;
     const int steps = SPLIT == 1 ? total : (total - wave + 3) / 4;
     T q, g;
@@ -346,7 +338,7 @@ __global__ __launch_bounds__(256, DP > 64 ? 1 : 2) void attn_dkv_kernel(AttnArgs
             sr[buf][1][me] = rec.r;
             sr[buf][2][me] = rec.dot;
             sr[buf][3][me] = rec.a;
-            sr[buf][4][me] = rec.b;
+            sr[buf][4][me] = (float)((double)rec.a * pow2(rec.ek - whole));
         }
         const int i0 = 64 * (first + ct);
         ct += SPLIT;
@@ -395,12 +387,12 @@ __global__ __launch_bounds__(256, DP > 64 ? 1 : 2) void attn_dkv_kernel(AttnArgs
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             y[4 * e + i] = ((double)acc[2][e][i] * 65536.0 + ((double)acc[3][e][i] * 256.0 + (double)acc[4][e][i])) * p.scale;
-    store_odd(y, key.ek, p.q, ok, p.d, lane, out + (p.heads + it.kvh) * p.d, need + p.heads + it.kvh);
+    store_odd(y, lambda - 6 + whole + o_top, p.q, ok, p.d, lane, out + (p.heads + it.kvh) * p.d, need + p.heads + it.kvh);
 #pragma unroll
     for (int e = 0; e < NE; ++e)
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[4 * e + i] = (double)acc[0][e][i] * 256.0 + (double)acc[1][e][i];
-    store_odd(y, key.ev, p.q, ok, p.d, lane, out + (p.heads + p.kv + it.kvh) * p.d, need + p.heads + p.kv + it.kvh);
+    store_odd(y, kappa + o_top, p.q, ok, p.d, lane, out + (p.heads + p.kv + it.kvh) * p.d, need + p.heads + p.kv + it.kvh);
 }
 
 template <int DP>
@@ -428,10 +420,15 @@ static void dkv(const AttnArgs &a, const AttnBwd &b, int split, hipStream_t st) 
 }
 
 hipError_t launch_attention_bwd(const AttnArgs &a, const AttnBwd &b, hipStream_t st) {
-    const long long items = (a.rows * (a.heads + a.kv) + 15) / 16;
+    const int nl = a.dp <= 16 ? 1 : a.dp <= 32 ? 2 : a.dp <= 64 ? 4 : 8;
+    const long long items = (a.rows * (a.heads + a.kv) + 256 / nl - 1) / (256 / nl);
+    const dim3 gd((unsigned)(items < 8 * NCU ? items : 8 * NCU)), block(256);
     prof_begin(st, PROF_ATT_PREP);
-    hipLaunchKernelGGL(attn_dot_kernel, dim3((unsigned)(items < 16384 ? items : 16384)), dim3(256), 0, st, a, b);
-    hipLaunchKernelGGL(attn_scale_kernel, dim3((unsigned)(max(a.n_seq, 1) * a.kv)), dim3(256), 0, st, a, b);
+    if (nl == 1) hipLaunchKernelGGL(attn_dot_kernel<1>, gd, block, 0, st, a, b);
+    else if (nl == 2) hipLaunchKernelGGL(attn_dot_kernel<2>, gd, block, 0, st, a, b);
+    else if (nl == 4) hipLaunchKernelGGL(attn_dot_kernel<4>, gd, block, 0, st, a, b);
+    else hipLaunchKernelGGL(attn_dot_kernel<8>, gd, block, 0, st, a, b);
+    hipLaunchKernelGGL(attn_scale_kernel, dim3(att_grid(att_slots(a.rows, a.n_seq, 256), a.kv, 1)), block, 0, st, a, b);
     prof_end(st, PROF_ATT_PREP);
     prof_begin(st, PROF_ATT_DQ);
     if (a.d <= 32) dq<32>(a, b, st);

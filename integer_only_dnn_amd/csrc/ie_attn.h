@@ -183,6 +183,37 @@ __device__ __forceinline__ bool rank_tile(const AttnArgs &p, int rank, int bm, S
     return true;
 }
 
+// 16 mantissas of a head from column 16 c on, at any alignment; past d: zeros.
+__device__ __forceinline__ v4i head16(const int8_t *head, int c, int d) {
+    v4i v = {0, 0, 0, 0};
+    const int n = d - 16 * c;
+    const int8_t *p = head + 16 * c;
+    if (n >= 16) {
+        __builtin_memcpy(&v, p, 16);
+    } else if (n > 0) {
+        // n = 8 a + 4 b + 2 c + e, from the top down: each piece shifts the ones above it up
+        uint64_t lo = 0, hi = 0;
+        if (n & 8) __builtin_memcpy(&lo, p, 8);
+        const int8_t *t = p + (n & 8);
+        uint64_t w = 0;
+        if (n & 1) w = (uint8_t)t[n & 6];
+        if (n & 2) {
+            uint16_t x;
+            __builtin_memcpy(&x, t + (n & 4), 2);
+            w = w << 16 | x;
+        }
+        if (n & 4) {
+            uint32_t x;
+            __builtin_memcpy(&x, t, 4);
+            w = w << 32 | x;
+        }
+        if (n & 8) hi = w;
+        else lo = w;
+        v = v4i{(int)(uint32_t)lo, (int)(uint32_t)(lo >> 32), (int)(uint32_t)hi, (int)(uint32_t)(hi >> 32)};
+    }
+    return v;
+}
+
 // A tile of 64 rows of one head in LDS, read by rows (frag_r: contraction over
 // the head's elements, 64 a step, zeros past its end) and transposed (frag_t).  Rows
 // lie 16 bytes more than a multiple of 64 apart, and every 16 rows another 128

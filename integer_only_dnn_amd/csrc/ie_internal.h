@@ -373,14 +373,13 @@ hipError_t launch_attention_round(const AttnArgs &a, hipStream_t st);
 // What the backward pass knows of a query row of a head and of a key (see
 // ie_attention_bwd.hip).
 struct AttnRow {
-    float m, r, dot, a, b, s;
-    int e;       // exponent of its units of dQ
-    uint32_t sum;
+    float m, r, dot, a, s;
+    int e;      // exponent of its units of dQ
+    int ek;     // its row's exponent, clipped
+    int o_top;  // largest exponent of dO in its sequence
 };
-struct AttnKey {
-    int kappa, lambda;
-    int ev, ek;  // exponents of its units of dV and dK
-};
+typedef int16_t AttnKey __attribute__((ext_vector_type(2)));  // bounds kappa, lambda of the queries at a token
+#define ATT_NO_KEY (AttnKey{-4096, -4096})
 struct AttnBwd {
     const int8_t *o, *oe;
     const int8_t *dy, *dye;

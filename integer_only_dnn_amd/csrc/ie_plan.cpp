@@ -861,7 +861,7 @@ AttBwdWs carve_attention_bwd(Carve &c, long long rows, long long heads, long lon
     w.dots = c.take<char>((size_t)(rows * heads * 8));
     w.norm = c.take<int8_t>((size_t)(rows * kv));
     w.row = c.take<char>((size_t)(rows * heads * 32));
-    w.key = c.take<char>((size_t)(rows * kv * 16));
+    w.key = c.take<char>((size_t)(rows * kv * 4));
     w.xp = c.take<int8_t>((size_t)(rows * (heads + 2 * kv) * r16(d)));
     w.dyp = c.take<int8_t>((size_t)(rows * heads * r16(d)));
     return w;

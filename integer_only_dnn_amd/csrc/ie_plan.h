@@ -453,7 +453,7 @@ struct AttBwdWs {
     void *dots;    // 8 bytes a row and head
     int8_t *norm;  // a row and key head
     void *row;     // 32 bytes a row and head
-    void *key;     // 16 bytes a row and key head
+    void *key;     // 4 bytes a row and key head
     int8_t *xp, *dyp;  // QKV and dO with heads of r16(d), where they are not aligned
 };
 AttBwdWs carve_attention_bwd(Carve &c, long long rows, long long heads, long long kv, long long d);

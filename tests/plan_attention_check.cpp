@@ -57,7 +57,7 @@ static void workspaces() {
                     touch((char *)w.dots, rows * h * 8);
                     touch(w.norm, rows * kv);
                     touch((char *)w.row, rows * h * 32);
-                    touch((char *)w.key, rows * kv * 16);
+                    touch((char *)w.key, rows * kv * 4);
                     touch(w.xp, rows * (h + 2 * kv) * ((d + 15) / 16 * 16));
                     touch(w.dyp, rows * h * ((d + 15) / 16 * 16));
                     CHECK(align256(c.off) == attention_bwd_ws(rows, h, kv, d));

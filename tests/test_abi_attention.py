@@ -180,7 +180,7 @@ def test_workspace_queries():
     assert L.ie_rope_workspace(-1, 5) == 0
     a = att()
     assert L.ie_attention_fwd_workspace(by(a), 100) >= 256 + 100 * 128 * 2 + 100 * 4 * 2
-    assert L.ie_attention_bwd_workspace(by(a), 100) >= 100 * (256 * 2 + 8 * 2 + 4 * 8 + 2 + 4 * 32 + 2 * 16)
+    assert L.ie_attention_bwd_workspace(by(a), 100) >= 100 * (256 * 2 + 8 * 2 + 4 * 8 + 2 + 4 * 32 + 2 * 4)
     assert L.ie_attention_cache_workspace(by(a), 3, 1000) >= 3 * 4 * (128 * 4 + 4 * 16)
 
 
