@@ -208,7 +208,7 @@ __global__ __launch_bounds__(256, DP > 64 ? 2 : 3) void attn_dq_kernel(AttnArgs 
 // their sums up in LDS at the end (exact integers): where there are few keys,
 // four times as many workgroups, which stage four times as much.
 template <int DP, bool CAUSAL, int SPLIT>
-__global__ __launch_bounds__(256, DP > 64 ? 1 : 2) void attn_dkv_kernel(AttnArgs p, AttnBwd bw) {
+__global__ __launch_bounds__(256, DP > 64 ? 1 : SPLIT > 1 ? 2 : 3) void attn_dkv_kernel(AttnArgs p, AttnBwd bw) {
     using T = HeadTile<DP, 256 / SPLIT>;
     constexpr int KS = T::KS, NE = DP / 16, KEYS = 64 / SPLIT, NB = SPLIT == 1 ? 2 : 1;
     __shared__ __align__(16) int8_t sq[NB * SPLIT][T::BYTES], sg[NB * SPLIT][T::BYTES];
