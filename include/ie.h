@@ -502,7 +502,8 @@ ie_status ie_attention_bwd(const ie_attention_desc *d, const ie_mat *QKV, const 
  * The numbers are exact (units of 2^(e - 14)) and rounded once.
  * pos: a device array of the rows' positions, or NULL for the row's number.  A
  * position outside 0 .. positions - 1 sets IE_FLAG_INDEX and is read as 0.
- * table: device memory, [positions x rot / 2] pairs of int16, 16-byte aligned.
+ * table: device memory, [positions x rot / 2] pairs of int16 of magnitude at
+ * most 32767.
  * rot even and <= IE_ROPE_MAX, head_dim <= 2^15, cols <= 2^30, table 16-byte
  * and pos 4-byte aligned, else IE_ERR_UNSUPPORTED; rot <= head_dim and heads *
  * head_dim <= cols, else IE_ERR_SHAPE.

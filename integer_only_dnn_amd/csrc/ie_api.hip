@@ -1424,6 +1424,7 @@ ie_status ie_rope(const ie_rope_desc *d, const ie_mat *X, const ie_mat *Y, void 
     a.heads = d->heads;
     a.interleaved = d->interleaved != 0;
     a.inverse = d->inverse != 0;
+    a.per = make_fastdiv(d->head_dim >= 8 ? (uint32_t)d->head_dim / 8 : 1);
     a.table = (const int *)d->table;
     a.positions = d->positions;
     a.pos = d->pos;

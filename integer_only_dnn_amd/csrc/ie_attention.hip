@@ -320,14 +320,17 @@ __global__ __launch_bounds__(256, DP > 64 ? 3 : 4) void attn_fwd_kernel(AttnArgs
 }
 
 // Rows of parts (heads), each rounded to odd at two bits below its own need, into one
-// exponent a row: a wave per row, eight results a lane and turn.
+// exponent a row: T threads per row (a wave, or a workgroup for few rows), eight
+// results a thread and turn.
+template <int T>
 __global__ __launch_bounds__(256) void attn_round_kernel(AttnArgs p) {
-    const int lane = threadIdx.x & 63;
-    const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
+    __shared__ int sh[4];
+    const int lane = threadIdx.x % T;
+    const long long row = (long long)blockIdx.x * (256 / T) + threadIdx.x / T;
     if (row >= p.rows) return;
     if (p.off && row == 0) {
         bool bad = false;
-        for (int s = lane; s < p.n_seq; s += 64) {
+        for (int s = lane; s < p.n_seq; s += T) {
             const long long a = p.off[s], b = p.off[s + 1];
             bad |= a < 0 || b < a || b > p.rows || b - a > p.most;
         }
@@ -336,8 +339,8 @@ __global__ __launch_bounds__(256) void attn_round_kernel(AttnArgs p) {
     if (p.off && (row < p.off[0] || row >= p.off[p.n_seq])) return;  // behind the last sequence: left as it is
     const int16_t *need = p.p16 + row * p.parts;
     int e = P_NONE;
-    for (int i = lane; i < p.parts; i += 64) e = max(e, (int)need[i]);
-    e = clamp_exp_flag(max(E_MIN, wave_max_dpp(e)), p.flags);
+    for (int i = lane; i < p.parts; i += T) e = max(e, (int)need[i]);
+    e = clamp_exp_flag(max(E_MIN, row_reduce<T>(e, Max{}, sh)), p.flags);
     if (lane == 0) {
         p.ye[row] = (int8_t)e;
         if (p.xe[p.x_row ? row : 0] > ATT_E_HI) atomicOr(p.flags, IE_FLAG_EXP_RANGE);
@@ -345,7 +348,7 @@ __global__ __launch_bounds__(256) void attn_round_kernel(AttnArgs p) {
     const int16_t *v = p.v16 + row * p.cols;
     int8_t *y = p.y + row * p.cols;
     if (p.out_vec) {
-        for (int c = 8 * lane; c < p.cols; c += 512) {
+        for (int c = 8 * lane; c < p.cols; c += 8 * T) {
             const int s = e - ((int)need[c / p.part] - 2);
             const v4i w = *(const v4i *)(v + c);
             int o[8];
@@ -357,13 +360,14 @@ __global__ __launch_bounds__(256) void attn_round_kernel(AttnArgs p) {
             *(uint2 *)(y + c) = uint2{pack4(o[0], o[1], o[2], o[3]), pack4(o[4], o[5], o[6], o[7])};
         }
     } else {
-        for (int c = lane; c < p.cols; c += 64) y[c] = (int8_t)rne_shift32((int)v[c], e - ((int)need[c / p.part] - 2));
+        for (int c = lane; c < p.cols; c += T) y[c] = (int8_t)rne_shift32((int)v[c], e - ((int)need[c / p.part] - 2));
     }
 }
 
 hipError_t launch_attention_round(const AttnArgs &a, hipStream_t st) {
     prof_begin(st, PROF_ATT_ROUND);
-    hipLaunchKernelGGL(attn_round_kernel, dim3((unsigned)((a.rows + 3) / 4)), dim3(256), 0, st, a);
+    if (a.rows < 4 * NCU) hipLaunchKernelGGL(attn_round_kernel<256>, dim3((unsigned)a.rows), dim3(256), 0, st, a);
+    else hipLaunchKernelGGL(attn_round_kernel<64>, dim3((unsigned)((a.rows + 3) / 4)), dim3(256), 0, st, a);
     prof_end(st, PROF_ATT_ROUND);
     return hipGetLastError();
 }

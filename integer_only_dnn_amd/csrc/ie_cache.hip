@@ -10,36 +10,42 @@
 
 namespace ie {
 
-// One key or value head of a row: 16 lanes with eight mantissas each.
+constexpr int STORE_ROWS = 4096;  // numbers of a chunk's heads fit 30 bits
+
+// One key or value head of a row: NL lanes with 16 mantissas each.
+template <int NL>
 __global__ __launch_bounds__(256) void cache_store_kernel(CacheArgs p, long long rows, const int8_t *x, const int8_t *xe, int x_row,
-                                                          int width, int first, const int *slots) {
-    const int parts = 2 * p.kv, lane = threadIdx.x & 15;
-    const long long total = rows * parts, slot_max = (long long)p.pages * p.page;
-    for (long long i = (long long)blockIdx.x * 16 + (threadIdx.x >> 4); i < (total + 15) / 16 * 16; i += (long long)gridDim.x * 16) {
-        const bool in = i < total;
-        const long long row = in ? i / parts : 0;
-        const int part = in ? (int)(i - row * parts) : 0;
-        const long long slot = in ? slots[row] : -1;
-        if (slot >= slot_max && lane == 0) atomicOr(p.flags, IE_FLAG_INDEX);
-        const bool on = slot >= 0 && slot < slot_max;
-        const int8_t *src = x + row * width + first + part * p.d + 8 * lane;
-        uint32_t w[2] = {0, 0};
-        if (on && 8 * lane < p.d) __builtin_memcpy(w, src, 8);
+                                                          int width, int first, const int *slots, FastDiv by_parts) {
+    constexpr int PB = 256 / NL;
+    const int parts = 2 * p.kv, lane = threadIdx.x % NL;
+    const long long slot_max = (long long)p.pages * p.page;
+    for (long long row0 = (long long)blockIdx.y * STORE_ROWS; row0 < rows; row0 += (long long)gridDim.y * STORE_ROWS)
+    for (int i0 = blockIdx.x * PB, total = (int)min(rows - row0, (long long)STORE_ROWS) * parts; i0 < total; i0 += gridDim.x * PB) {
+        const int i = min(i0 + (int)threadIdx.x / NL, total - 1);
+        const int r = (int)(((uint64_t)(uint32_t)i * by_parts.m) >> by_parts.s), part = i - r * parts;
+        const long long row = row0 + r, slot = slots[row];
+        const bool mine = i == i0 + (int)threadIdx.x / NL, on = mine && slot >= 0 && slot < slot_max;
+        if (mine && slot >= slot_max && lane == 0) atomicOr(p.flags, IE_FLAG_INDEX);
+        uint32_t w[4] = {0, 0, 0, 0};
+        const bool have = on && 16 * lane < p.d;
+        if (have) __builtin_memcpy(w, x + row * width + first + part * p.d + 16 * lane, 16);
+        const int ex = xe[x_row ? row : 0];
         int m = 0;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) m = max(m, abs(byte_of(w[k >> 2], k & 3)));
-        m = lane_reduce<16>(m, Max{});
-        const int ex = on ? (int)xe[x_row ? row : 0] : 0;
-        int e = max(E_MIN, need32(m, ex, 3));
-        const int s = e - ex;
-        uint32_t o = 0;
+        for (int k = 0; k < 16; ++k) m = max(m, abs(byte_of(w[k >> 2], k & 3)));
+        m = lane_reduce<NL>(m, Max{});
+        const int e = max(E_MIN, need32(m, ex, 3));
+        // C 2^(ex - e) rounded: exact products, at most 7.5
+        const float inv = __int_as_float((127 + min(max(ex - e, -100), 100)) << 23);
+        uint32_t o[2] = {0, 0};
 #pragma unroll
-        for (int k = 0; k < 8; ++k) o |= (uint32_t)(rne_shift32(byte_of(w[k >> 2], k & 3), s) & 15) << (4 * k);
+        for (int k = 0; k < 16; ++k)
+            o[k >> 3] |= ((uint32_t)__float_as_int(__builtin_fmaf((float)byte_of(w[k >> 2], k & 3), inv, RINT_MAGIC)) & 15u) << (4 * (k & 7));
         if (!on) continue;
         const bool val = part >= p.kv;
         const long long at = slot * p.kv + (val ? part - p.kv : part);
         if (lane == 0) (val ? p.ve : p.ke)[at] = (int8_t)clamp_exp_flag(e, p.flags);
-        if (8 * lane < p.d) *(uint32_t *)((val ? p.v : p.k) + at * (p.d >> 1) + 4 * lane) = o;
+        if (have) *(uint2 *)((val ? p.v : p.k) + at * (p.d >> 1) + 8 * lane) = uint2{o[0], o[1]};
     }
 }
 
@@ -373,10 +379,16 @@ __global__ __launch_bounds__(256) void cache_join_kernel(CacheArgs p, AttnArgs a
 
 hipError_t launch_cache_store(const CacheArgs &c, long long rows, const int8_t *x, const int8_t *xe, int x_row, int width, int first,
                               const int *slots, hipStream_t st) {
-    const long long blocks = (rows * 2 * c.kv + 15) / 16;
+    const int nl = c.d <= 16 ? 1 : c.d <= 32 ? 2 : c.d <= 64 ? 4 : 8;
+    const long long chunk = rows < STORE_ROWS ? rows : STORE_ROWS, blocks = (chunk * 2 * c.kv + 256 / nl - 1) / (256 / nl);
+    const long long chunks = (rows + STORE_ROWS - 1) / STORE_ROWS;
+    const dim3 grid((unsigned)(blocks < 8 * NCU ? blocks : 8 * NCU), (unsigned)(chunks < 1024 ? chunks : 1024)), block(256);
+    const FastDiv f = make_fastdiv((uint32_t)(2 * c.kv));
     prof_begin(st, PROF_CACHE_STORE);
-    hipLaunchKernelGGL(cache_store_kernel, dim3((unsigned)(blocks < 16384 ? blocks : 16384)), dim3(256), 0, st, c, rows, x, xe, x_row,
-                       width, first, slots);
+    if (nl == 1) hipLaunchKernelGGL(cache_store_kernel<1>, grid, block, 0, st, c, rows, x, xe, x_row, width, first, slots, f);
+    else if (nl == 2) hipLaunchKernelGGL(cache_store_kernel<2>, grid, block, 0, st, c, rows, x, xe, x_row, width, first, slots, f);
+    else if (nl == 4) hipLaunchKernelGGL(cache_store_kernel<4>, grid, block, 0, st, c, rows, x, xe, x_row, width, first, slots, f);
+    else hipLaunchKernelGGL(cache_store_kernel<8>, grid, block, 0, st, c, rows, x, xe, x_row, width, first, slots, f);
     prof_end(st, PROF_CACHE_STORE);
     return hipGetLastError();
 }

@@ -399,6 +399,7 @@ struct RopeArgs {
     long long rows;
     int cols, q, mode;
     int d, rot, heads, interleaved, inverse;
+    FastDiv per;       // by the runs of eight of a head
     const int *table;  // [positions][rot / 2] pairs
     long long positions;
     const int *pos;    // [rows], or nullptr: the row's number

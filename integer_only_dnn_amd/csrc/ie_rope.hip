@@ -34,43 +34,53 @@ __global__ __launch_bounds__(256) void rope_table_kernel(RopeFreqs fr, int half,
 }
 
 // Eight neighbours of a row (or, for the two-halves layout, two runs of four)
-// as the numbers they become.
+// as the numbers they become, in units of 2^(e - 22): two bytes as the upper
+// halves of 16-bit numbers, one two-element product of 16-bit integers each.
 struct RopeUnit {
     int at[2];  // first column of each run of four
     int k;      // first pair of four, or -1: not rotated
 };
 __device__ __forceinline__ RopeUnit rope_unit(const RopeArgs &p, int u) {
-    const int per = p.d >> 3, head = u / per, k = u - head * per, c0 = head * p.d;
+    const int head = (int)(((uint64_t)(uint32_t)u * p.per.m) >> p.per.s), k = u - head * (p.d >> 3), c0 = head * p.d;
     RopeUnit r;
     const bool on = head < p.heads && 8 * k < p.rot;
     r.k = on ? 4 * k : -1;
-    if (on && !p.interleaved) {
-        r.at[0] = c0 + 4 * k;
-        r.at[1] = c0 + (p.rot >> 1) + 4 * k;
-    } else {
-        r.at[0] = c0 + 8 * k;
-        r.at[1] = c0 + 8 * k + 4;
-    }
+    const bool halves = on && !p.interleaved;
+    r.at[0] = c0 + (halves ? 4 : 8) * k;
+    r.at[1] = halves ? r.at[0] + (p.rot >> 1) : r.at[0] + 4;
     return r;
 }
-__device__ __forceinline__ void rope8(const RopeArgs &p, const RopeUnit &u, uint32_t lo, uint32_t hi, const int4 &t, float sign,
-                                      float (&y)[8]) {
-    if (u.k < 0) {
+typedef short s2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ void rope8(bool on, bool interleaved, s2 sign, uint32_t lo, uint32_t hi, const int4 &t, float (&y)[8]) {
+    if (!on) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            y[i] = 16384.0f * (float)byte_of(lo, i);
-            y[4 + i] = 16384.0f * (float)byte_of(hi, i);
+            y[i] = (float)((int)(lo << (24 - 8 * i)) >> 2 & ~0x3fffff);
+            y[4 + i] = (float)((int)(hi << (24 - 8 * i)) >> 2 & ~0x3fffff);
         }
         return;
     }
     const int w[4] = {t.x, t.y, t.z, t.w};
+    uint32_t ab[4];
+    if (interleaved) {
+        ab[0] = __builtin_amdgcn_perm(lo, lo, 0x010c000cu);
+        ab[1] = __builtin_amdgcn_perm(lo, lo, 0x030c020cu);
+        ab[2] = __builtin_amdgcn_perm(hi, hi, 0x010c000cu);
+        ab[3] = __builtin_amdgcn_perm(hi, hi, 0x030c020cu);
+    } else {
+        ab[0] = __builtin_amdgcn_perm(hi, lo, 0x040c000cu);
+        ab[1] = __builtin_amdgcn_perm(hi, lo, 0x050c010cu);
+        ab[2] = __builtin_amdgcn_perm(hi, lo, 0x060c020cu);
+        ab[3] = __builtin_amdgcn_perm(hi, lo, 0x070c030cu);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float c = (float)(int16_t)w[i], s = sign * (float)(w[i] >> 16);
-        const int ia = p.interleaved ? 2 * i : i, ib = p.interleaved ? 2 * i + 1 : 4 + i;
-        const float a = (float)byte_of(ia < 4 ? lo : hi, ia & 3), b = (float)byte_of(ib < 4 ? lo : hi, ib & 3);
-        y[ia] = a * c - b * s;
-        y[ib] = a * s + b * c;
+        // (c, s) turned forward, (c, -s) back; products with (c, -s) and (s, c)
+        const s2 cs = __builtin_bit_cast(s2, w[i]) * sign, v = __builtin_bit_cast(s2, ab[i]);
+        const s2 minus = {1, -1}, a = cs * minus, b = {cs[1], cs[0]};
+        const int ya = __builtin_amdgcn_sdot2(v, a, 0, false), yb = __builtin_amdgcn_sdot2(v, b, 0, false);
+        y[interleaved ? 2 * i : i] = (float)ya;
+        y[interleaved ? 2 * i + 1 : 4 + i] = (float)yb;
     }
 }
 
@@ -82,14 +92,17 @@ __device__ __forceinline__ int rope_position(const RopeArgs &p, long long row, b
 }
 
 // T threads per row, NU units each.
-template <int T, int NU>
+template <int T, int NU, bool INTER>
 __global__ __launch_bounds__(256) void rope_kernel(RopeArgs p) {
     constexpr int RPB = 256 / T;
     __shared__ int sh[4];
     const int t = threadIdx.x % T, slot = threadIdx.x / T, units = p.cols >> 3;
-    const float sign = p.inverse ? -1.0f : 1.0f;
+    const s2 sign = {1, (short)(p.inverse ? -1 : 1)};
     int run = NEED_NONE;
     int whole = 0;
+    RopeUnit un[NU];
+#pragma unroll
+    for (int i = 0; i < NU; ++i) un[i] = rope_unit(p, min(t + T * i, units - 1));
     if (p.mode == NORM_ROUND) {
         int m = NEED_NONE;
         for (int i = threadIdx.x; i < p.n_bmax; i += 256) m = max(m, p.bmax[i]);
@@ -99,25 +112,24 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs p) {
     for (long long r0 = (long long)blockIdx.x * RPB; r0 < p.rows; r0 += (long long)gridDim.x * RPB) {
         const bool ok = r0 + slot < p.rows;
         const long long row = ok ? r0 + slot : p.rows - 1;
-        const int ex = p.xe[p.x_row ? row : 0] - 14;
+        const int ex = p.xe[p.x_row ? row : 0] - 22;
         const int *tab = p.table + (long long)rope_position(p, row, ok && t == 0 && p.mode != NORM_ROUND) * (p.rot >> 1);
         const int8_t *x = p.x + row * p.cols;
         float y[NU][8];
+        uint32_t lo[NU], hi[NU];
+        int4 w[NU];
+#pragma unroll
+        for (int i = 0; i < NU; ++i) {
+            lo[i] = *(const uint32_t *)(x + un[i].at[0]);
+            hi[i] = *(const uint32_t *)(x + un[i].at[1]);
+            w[i] = un[i].k >= 0 ? *(const int4 *)(tab + un[i].k) : int4{0, 0, 0, 0};
+        }
         float big = 0.0f;
 #pragma unroll
         for (int i = 0; i < NU; ++i) {
-            const int u = t + T * i;
-            if (u < units) {
-                const RopeUnit a = rope_unit(p, u);
-                const uint32_t lo = *(const uint32_t *)(x + a.at[0]), hi = *(const uint32_t *)(x + a.at[1]);
-                const int4 w = a.k >= 0 ? *(const int4 *)(tab + a.k) : int4{0, 0, 0, 0};
-                rope8(p, a, lo, hi, w, sign, y[i]);
-            } else {
+            rope8(un[i].k >= 0, INTER, sign, lo[i], hi[i], w[i], y[i]);  // the last runs of a row may be taken twice
 #pragma unroll
-                for (int k = 0; k < 8; ++k) y[i][k] = 0.0f;
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) big = fmaxf(big, fabsf(y[i][k]));
+            for (int k = 0; k < 8; k += 2) asm("v_max3_f32 %0, %0, |%1|, |%2|" : "+v"(big) : "v"(y[i][k]), "v"(y[i][k + 1]));
         }
         int e = whole;
         if (p.mode != NORM_ROUND) {
@@ -139,14 +151,12 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs p) {
         int8_t *out = p.y + row * p.cols;
 #pragma unroll
         for (int i = 0; i < NU; ++i) {
-            const int u = t + T * i;
-            if (u >= units) continue;
-            const RopeUnit a = rope_unit(p, u);
+            if (t + T * i >= units) continue;
             int o[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) o[k] = __float_as_int(__builtin_fmaf(y[i][k], inv, ROPE_MAGIC));
-            *(uint32_t *)(out + a.at[0]) = pack4(o[0], o[1], o[2], o[3]);
-            *(uint32_t *)(out + a.at[1]) = pack4(o[4], o[5], o[6], o[7]);
+            *(uint32_t *)(out + un[i].at[0]) = pack4(o[0], o[1], o[2], o[3]);
+            *(uint32_t *)(out + un[i].at[1]) = pack4(o[4], o[5], o[6], o[7]);
         }
     }
     if (p.mode == NORM_NEED) {
@@ -226,7 +236,8 @@ hipError_t launch_rope(const RopeArgs &a, const RopePlan &pl, hipStream_t st) {
     }
 #define IE_CASE(T_, N_)                                                               \
     if (pl.t == T_ && pl.nu == N_) {                                                  \
-        hipLaunchKernelGGL((rope_kernel<T_, N_>), grid, block, 0, st, a);             \
+        if (a.interleaved) hipLaunchKernelGGL((rope_kernel<T_, N_, true>), grid, block, 0, st, a); \
+        else hipLaunchKernelGGL((rope_kernel<T_, N_, false>), grid, block, 0, st, a); \
         done = true;                                                                  \
     }
     IE_ROPE_SHAPES(IE_CASE)
