@@ -111,25 +111,33 @@ __device__ __forceinline__ Span seq_span(const AttnArgs &p, int s) {
 }
 // Tiles of BM rows: sequence s owns the slots from off[s] / BM + s on, enough
 // for its ceil(n / BM) tiles whatever the other lengths are, so that a slot
-// finds its sequence by bisection and nothing is laid out beforehand.  Returns
-// the sequence's rows and the tile's first row in it (>= n: no such tile).
-__device__ __forceinline__ Span slot_span(const AttnArgs &p, int slot, int bm, int &first, int &seq) {
-    seq = 0;
+// finds its sequence by a search, 64 offsets a turn, and nothing is laid out
+// beforehand.  Returns the sequence's rows and the tile's first row in it (>= n:
+// no such tile).
+__device__ __forceinline__ Span slot_span(const AttnArgs &p, int slot, int bm, int &first) {
     if (!p.off) {
         first = slot * bm;
         return seq_span(p, 0);
     }
-    int lo = 0, hi = p.n_seq - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (max(p.off[mid], 0) / bm + mid <= slot) lo = mid;
-        else hi = mid - 1;
-    }
-    seq = lo;
-    const Span s = seq_span(p, lo);
-    const int at = slot - (max(p.off[lo], 0) / bm + lo);
-    first = at < 0 || at > s.n / bm ? s.n : at * bm;
-    return s;
+    const int lane = threadIdx.x & 63;
+    int lo = 0, len = p.n_seq, step, x, y, k;
+    do {
+        step = (len + 63) >> 6;
+        const int i = lo + lane * step, in = min(i, p.n_seq - 1);
+        x = p.off[in];
+        y = p.off[in + 1];
+        const uint64_t below = __ballot(lane * step < len && max(x, 0) / bm + i <= slot);
+        k = below ? 63 - __builtin_clzll(below) : 0;
+        lo += k * step;
+        len = min(step, len - k * step);
+    } while (step > 1);
+    const int rows = (int)p.rows;
+    x = __builtin_amdgcn_readlane(x, k);
+    y = __builtin_amdgcn_readlane(y, k);
+    const int a = min(max(x, 0), rows), n = min(min(max(y, a), rows) - a, p.most);
+    const int at = slot - (max(x, 0) / bm + lo);
+    first = at < 0 || at > n / bm ? n : at * bm;
+    return Span{a, n};
 }
 
 // A launch's items: the tiles of 64 rows of every key head, and of each the
@@ -154,9 +162,9 @@ inline unsigned att_grid(long long tiles, int kv, int per) { return (unsigned)((
 template <bool HEAVY>
 __device__ __forceinline__ bool rank_tile(const AttnArgs &p, int rank, int bm, Span &sp, int &tile) {
     if (!HEAVY || !p.off || p.n_seq > 64) {
-        int first, seq;
+        int first;
         const int slots = (int)(p.rows / bm) + max(p.n_seq, 1);
-        sp = slot_span(p, HEAVY ? slots - 1 - rank : rank, bm, first, seq);
+        sp = slot_span(p, HEAVY ? slots - 1 - rank : rank, bm, first);
         tile = first / bm;
         return rank < slots && first < sp.n;
     }
