@@ -53,6 +53,7 @@ __global__ __launch_bounds__(256, DP > 64 ? 3 : 4) void attn_fwd_kernel(AttnArgs
     constexpr int KS = T::KS, NE = DP / 16;
     __shared__ __align__(16) int8_t tiles_lds[4][T::BYTES];
     __shared__ __align__(16) float factors_lds[256];
+    __shared__ __align__(16) float scaled_lds[2][64], most_lds[4];  // factors 2^-E, largest ones
     int8_t(*sk)[T::BYTES] = tiles_lds, (*sv)[T::BYTES] = tiles_lds + 2;
     float(*sf)[64] = (float(*)[64])factors_lds;
     const Item it = att_item(p, p.group);
@@ -75,7 +76,8 @@ __global__ __launch_bounds__(256, DP > 64 ? 3 : 4) void attn_fwd_kernel(AttnArgs
 
     v4i hi[NE] = {}, lo[NE] = {};
     uint32_t sum = 0, blocks = 0;
-    // the digits of four weights of keys 16 z + 4 quad .., given t - m or the scores' difference
+    // the digits of four weights of keys 16 z + 4 quad .., given t - m or the scores' difference, and
+    // 2^(e - E): where every query sees every key E is one number, and f has it already
     auto weigh4 = [&](auto masked, const float (&d)[4], const float (&f)[4], float down, int z, int lim, int &dh, int &dl) {
         int bits[4];
         uint32_t whole_n[4];
@@ -83,7 +85,7 @@ __global__ __launch_bounds__(256, DP > 64 ? 3 : 4) void attn_fwd_kernel(AttnArgs
         for (int i = 0; i < 4; ++i) {
             float w = weight(d[i], r);
             if (masked.value) w = 16 * z + i <= lim ? w : 0.0f;
-            bits[i] = __float_as_int(ROW ? __builtin_fmaf(w, f[i] * down, RINT_128) : w + RINT_128);
+            bits[i] = __float_as_int(ROW ? __builtin_fmaf(w, CAUSAL ? f[i] * down : f[i], RINT_128) : w + RINT_128);
             whole_n[i] = (uint32_t)(ROW ? __float_as_int(w + RINT_MAGIC) : bits[i]);
         }
         sum += whole_n[0] + whole_n[1];
@@ -132,13 +134,18 @@ __global__ __launch_bounds__(256, DP > 64 ? 3 : 4) void attn_fwd_kernel(AttnArgs
 #pragma unroll
             for (int t = 0; t < 4; ++t)
                 if (64 * t < keys) k[t].put(tiles_lds[t]);
-            if (ROW) factors_lds[tid] = fe;
+            if (ROW) {
+                factors_lds[tid] = fe;
+                most_lds[wave] = __int_as_float(wave_max_dpp(__float_as_int(fe)));  // rows behind the last repeat it
+            }
             __syncthreads();
             float s[16][4], m = -__builtin_inff(), em = 0.0f;
             int mi = -(1 << 30);
             const int lim = (CAUSAL ? qi : n - 1) - 4 * quad;  // keys 16 z + i <= lim are seen
             auto whole = [&](int t) { return 64 * t + 64 <= (CAUSAL ? qw + 1 : n); };
             auto score = [&](auto masked, int t) {
+                constexpr bool each = CAUSAL && decltype(masked)::value;
+                if (ROW && !each) em = fmaxf(em, most_lds[t]);
                 v4i acc[4];
                 float4 f[4];
 #pragma unroll
@@ -160,7 +167,7 @@ __global__ __launch_bounds__(256, DP > 64 ? 3 : 4) void attn_fwd_kernel(AttnArgs
                         const bool on = !masked.value || 64 * t + 16 * z + i <= lim;
                         s[4 * t + z][i] = x;
                         m = fmaxf(m, on ? x : -__builtin_inff());
-                        if (ROW) em = fmaxf(em, on ? fs[i] : 0.0f);
+                        if (ROW && each) em = fmaxf(em, on ? fs[i] : 0.0f);
                     }
                 }
             };
@@ -192,10 +199,14 @@ __global__ __launch_bounds__(256, DP > 64 ? 3 : 4) void attn_fwd_kernel(AttnArgs
 #pragma unroll
             for (int t = 0; t < 4; ++t)
                 if (64 * t < keys) v[t].put(tiles_lds[t]);
+            if (ROW && !CAUSAL) {
+                em = fmaxf(fmaxf(most_lds[0], most_lds[1]), fmaxf(most_lds[2], most_lds[3]));
+                factors_lds[tid] = fe * __int_as_float((254 << 23) - __float_as_int(em));
+            }
             __syncthreads();
             if (idle) return;
             m = col_max(m);
-            em = col_max(em);
+            if (CAUSAL) em = col_max(em);
             const int top = ROW ? (__float_as_int(em) >> 23) - 127 : eq;
             const float down = ROW ? pow2f(-top) : 1.0f;
 #pragma unroll
@@ -215,7 +226,7 @@ __global__ __launch_bounds__(256, DP > 64 ? 3 : 4) void attn_fwd_kernel(AttnArgs
     T k, v;
     k.init(p.width, p.dp);
     v.init(p.width, p.dp);
-    float fe = 0.0f;
+    float fe = 0.0f, down = 1.0f;
     auto fetch = [&](int t, bool values) {
         k.fetch(kh, p.width, 64 * t, keys, p.dp);
         if (values) v.fetch(vh, p.width, 64 * t, keys, p.dp);
@@ -224,7 +235,11 @@ __global__ __launch_bounds__(256, DP > 64 ? 3 : 4) void attn_fwd_kernel(AttnArgs
     auto put = [&](int t, bool values) {
         k.put(sk[t & 1]);
         if (values) v.put(sv[t & 1]);
-        if (ROW && tid < 64) sf[t & 1][tid] = fe;
+        if (ROW && tid < 64) {
+            sf[t & 1][tid] = fe;
+            if (!CAUSAL && values) scaled_lds[t & 1][tid] = fe * down;
+            if (!values) most_lds[t & 1] = __int_as_float(wave_max_dpp(__float_as_int(fe)));
+        }
     };
     // scores of 16 keys of a tile
     auto scores = [&](int t, int z) {
@@ -233,8 +248,8 @@ __global__ __launch_bounds__(256, DP > 64 ? 3 : 4) void attn_fwd_kernel(AttnArgs
         for (int i = 0; i < KS; ++i) acc = mfma(T::frag_r(sk[t & 1], z, i, lane), q[i], acc);
         return acc;
     };
-    auto factors = [&](int t, int z, float (&f)[4]) {
-        const float4 x = ROW ? *(const float4 *)&sf[t & 1][16 * z + 4 * quad] : float4{1, 1, 1, 1};
+    auto factors = [&](const float *at, int z, float (&f)[4]) {
+        const float4 x = ROW ? *(const float4 *)(at + 16 * z + 4 * quad) : float4{1, 1, 1, 1};
         f[0] = x.x;
         f[1] = x.y;
         f[2] = x.z;
@@ -248,19 +263,21 @@ __global__ __launch_bounds__(256, DP > 64 ? 3 : 4) void attn_fwd_kernel(AttnArgs
     float m = -__builtin_inff(), em = 0.0f;
     int mi = -(1 << 30);
     auto largest = [&](auto masked, int t) {
+        constexpr bool each = CAUSAL && decltype(masked)::value;
         const int lim = limit(t);
+        if (ROW && !each) em = fmaxf(em, most_lds[t & 1]);
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
             if (masked.value && 64 * t + 16 * z >= last) break;
             const v4i acc = scores(t, z);
             float f[4];
-            factors(t, z, f);
+            factors(sf[t & 1], z, f);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const bool on = !masked.value || 16 * z + i <= lim;
                 if (ROW) {
                     m = fmaxf(m, on ? (float)acc[i] * f[i] : -__builtin_inff());
-                    em = fmaxf(em, on ? f[i] : 0.0f);
+                    if (each) em = fmaxf(em, on ? f[i] : 0.0f);
                 } else {
                     mi = max(mi, on ? acc[i] : -(1 << 30));
                 }
@@ -278,12 +295,12 @@ __global__ __launch_bounds__(256, DP > 64 ? 3 : 4) void attn_fwd_kernel(AttnArgs
     }
     if (ROW) {
         m = col_max(m);
-        em = col_max(em);
+        if (CAUSAL) em = col_max(em);
     } else {
         mi = col_reduce(mi, Max{});
     }
     const int top = ROW ? (__float_as_int(em) >> 23) - 127 : eq;  // E
-    const float down = ROW ? pow2f(-top) : 1.0f;
+    if (ROW) down = pow2f(-top);
     __syncthreads();
 
     // second pass: weights and the sums they enter
@@ -296,10 +313,11 @@ __global__ __launch_bounds__(256, DP > 64 ? 3 : 4) void attn_fwd_kernel(AttnArgs
             if (masked.value && 64 * t + 16 * z >= last) continue;
             const v4i acc = scores(t, z);
             float f[4], d[4];
-            factors(t, z, f);
+            factors(sf[t & 1], z, f);
 #pragma unroll
             for (int i = 0; i < 4; ++i) d[i] = ROW ? __builtin_fmaf((float)acc[i], f[i], -m) : (float)(acc[i] - mi);
             int a, c;
+            if (!CAUSAL) factors(scaled_lds[t & 1], z, f);
             weigh4(masked, d, f, down, z, lim, a, c);
             dh[z] = a;
             dl[z] = c;
@@ -373,7 +391,8 @@ hipError_t launch_attention_round(const AttnArgs &a, hipStream_t st) {
 }
 
 template <int DP, bool SHORT>
-static void fwd(const AttnArgs &a, hipStream_t st) {
+static void fwd(AttnArgs a, hipStream_t st) {
+    a.chunk = att_chunk(a, 64, !a.causal);
     const dim3 grid(att_grid(att_slots(a.rows, a.n_seq, 64), a.kv, a.group)), block(256);
     if (a.x_row) {
         if (a.causal) hipLaunchKernelGGL((attn_fwd_kernel<DP, true, true, SHORT>), grid, block, 0, st, a);

@@ -131,7 +131,8 @@ __global__ __launch_bounds__(256, DP > 64 ? 2 : 3) void attn_dq_kernel(AttnArgs 
     head_regs<KS>(base + (long long)qi * p.width + h * p.dp, ok, p.dp, lane, q);
     head_regs<KS>(bw.dy + (row * p.heads + h) * p.dp, ok, p.dp, lane, g);
     const AttnRow st = bw.row[(long long)h * p.rows + sp.a + min(qi, n - 1)];
-    const float fe0 = pow2f(clip_e(xe[0])), fs0 = fe0 * st.s;
+    const float fe0 = pow2f(clip_e(xe[0]));
+    const Poly scaled = poly(ROW ? st.s : fe0 * st.s);  // 2^-126 .. 2^60: exact products, no subnormal numbers
     const int keys = CAUSAL ? min(n, q0 + 64) : n, tiles = (keys + 63) / 64;
     const int last = CAUSAL ? min(n, qw + 16) : n;
     T k, v;
@@ -161,10 +162,10 @@ __global__ __launch_bounds__(256, DP > 64 ? 2 : 3) void attn_dq_kernel(AttnArgs 
             int bits[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                float w = weight(__builtin_fmaf((float)s[i], fs[i], -st.m), st.r);
+                float w = weight(__builtin_fmaf((float)s[i], fs[i], -st.m), st.r, scaled);
                 if (masked.value) w = 16 * z + i <= lim ? w : 0.0f;
                 const float u = __builtin_fmaf((float)dp[i], fs[i], -st.dot);
-                bits[i] = __float_as_int(__builtin_fmaf(w * u, ROW ? fs[i] * st.s : fs0, RINT_128));
+                bits[i] = __float_as_int(ROW ? __builtin_fmaf(w * u, fs[i], RINT_128) : w * u + RINT_128);
             }
             int x, y;
             digits4(bits[0], bits[1], bits[2], bits[3], x, y);
@@ -396,7 +397,8 @@ __global__ __launch_bounds__(256, DP > 64 ? 1 : SPLIT > 1 ? 2 : 3) void attn_dkv
 }
 
 template <int DP>
-static void dq(const AttnArgs &a, const AttnBwd &b, hipStream_t st) {
+static void dq(AttnArgs a, const AttnBwd &b, hipStream_t st) {
+    a.chunk = att_chunk(a, 64, !a.causal);
     const dim3 grid(att_grid(att_slots(a.rows, a.n_seq, 64), a.kv, a.group)), block(256);
     if (a.x_row) {
         if (a.causal) hipLaunchKernelGGL((attn_dq_kernel<DP, true, true>), grid, block, 0, st, a, b);
@@ -408,7 +410,8 @@ static void dq(const AttnArgs &a, const AttnBwd &b, hipStream_t st) {
 }
 
 template <int DP>
-static void dkv(const AttnArgs &a, const AttnBwd &b, int split, hipStream_t st) {
+static void dkv(AttnArgs a, const AttnBwd &b, int split, hipStream_t st) {
+    a.chunk = att_chunk(a, 64 / split, !a.causal);
     const dim3 grid(att_grid(att_slots(a.rows, a.n_seq, 64 / split), a.kv, 1)), block(256);
     if (split == 1) {
         if (a.causal) hipLaunchKernelGGL((attn_dkv_kernel<DP, true, 1>), grid, block, 0, st, a, b);
@@ -428,7 +431,9 @@ hipError_t launch_attention_bwd(const AttnArgs &a, const AttnBwd &b, hipStream_t
     else if (nl == 2) hipLaunchKernelGGL(attn_dot_kernel<2>, gd, block, 0, st, a, b);
     else if (nl == 4) hipLaunchKernelGGL(attn_dot_kernel<4>, gd, block, 0, st, a, b);
     else hipLaunchKernelGGL(attn_dot_kernel<8>, gd, block, 0, st, a, b);
-    hipLaunchKernelGGL(attn_scale_kernel, dim3(att_grid(att_slots(a.rows, a.n_seq, 256), a.kv, 1)), block, 0, st, a, b);
+    AttnArgs c = a;
+    c.chunk = att_chunk(a, 256, true);
+    hipLaunchKernelGGL(attn_scale_kernel, dim3(att_grid(att_slots(a.rows, a.n_seq, 256), a.kv, 1)), block, 0, st, c, b);
     prof_end(st, PROF_ATT_PREP);
     prof_begin(st, PROF_ATT_DQ);
     if (a.d <= 32) dq<32>(a, b, st);

@@ -47,15 +47,21 @@ constexpr float RINT_128 = RINT_MAGIC + 128.0f;
 __device__ __forceinline__ int clip_e(int e) { return min(max(e, ATT_E_LO), ATT_E_HI); }
 __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
 
+// The polynomial's coefficients, times a power of two where a row has one.
+struct Poly {
+    float c3, c2, c1, c0;
+};
+__device__ __forceinline__ Poly poly(float s) { return Poly{W_C3 * s, W_C2 * s, W_C1 * s, W_C0 * s}; }
+
 // 32512 * 2^(d r), see above (d <= 0).
-__device__ __forceinline__ float weight(float d, float r) {
+__device__ __forceinline__ float weight(float d, float r, const Poly &c = Poly{W_C3, W_C2, W_C1, W_C0}) {
     const float z = fmaxf(__builtin_fmaf(d, r, 96.0f), 64.0f);
     const float f = __builtin_amdgcn_fractf(z);
     uint32_t k;  // as written, the compiler takes the field's place by a shift and a mask
     asm("v_bfe_u32 %0, %1, 17, 6" : "=v"(k) : "v"(z));
-    float q = __builtin_fmaf(W_C3, f, W_C2);
-    q = __builtin_fmaf(q, f, W_C1);
-    q = __builtin_fmaf(q, f, W_C0);
+    float q = __builtin_fmaf(c.c3, f, c.c2);
+    q = __builtin_fmaf(q, f, c.c1);
+    q = __builtin_fmaf(q, f, c.c0);
     return __int_as_float((int)(k << 23) + __float_as_int(q));
 }
 
@@ -140,20 +146,35 @@ __device__ __forceinline__ Span slot_span(const AttnArgs &p, int slot, int bm, i
     return Span{a, n};
 }
 
-// A launch's items: the tiles of 64 rows of every key head, and of each the
-// `per` query heads that share it.  Workgroups reach the XCDs in turn
-// (blockIdx % 8), so an XCD takes every eighth pair (tile, key head), tiles in
-// order, the heads of a pair one behind the other: they share its L2, and every
-// XCD meets heavy and light tiles alike.
+// A launch's items: the tiles of every key head, and of each the `per` query
+// heads that share it.  Workgroups reach the XCDs in turn (blockIdx % 8).  In
+// general an XCD takes every eighth pair (tile, key head), tiles in order, the
+// heads of a pair one behind the other: they share its L2, and every XCD meets
+// heavy and light tiles alike.  Short sequences: it takes `chunk` pairs in a row,
+// then skips the others' seven chunks, so that the few tiles of a sequence read
+// its keys from one L2 (128 x 197 tokens, 12 heads of 64: forward pass 70 -> 67
+// us, dK and dV 135 -> 127).
 struct Item {
     int rank, kvh, gh;
 };
 __device__ __forceinline__ Item att_item(const AttnArgs &p, int per) {
-    const int idx = blockIdx.x >> 3;
-    const int v = idx / per, u = v * 8 + (blockIdx.x & 7);
+    const int idx = blockIdx.x >> 3, xcd = blockIdx.x & 7, v = idx / per;
+    int u = 8 * v + xcd;
+    if (p.chunk) {
+        const int all = gridDim.x / 8 / per, turn = v / p.chunk, at = turn * p.chunk;
+        u = 8 * at + xcd * min(p.chunk, all - at) + v - at;
+    }
     return Item{u / p.kv, u % p.kv, idx - v * per};
 }
 inline unsigned att_grid(long long tiles, int kv, int per) { return (unsigned)((tiles * kv + 7) / 8 * 8 * per); }
+// Pairs of a chunk: equal parts of up to 16 tiles, where sequences have up to 16
+// tiles on the average and all tiles of one are alike; else 0.
+inline int att_chunk(const AttnArgs &a, int bm, bool alike) {
+    const long long slots = att_slots(a.rows, a.n_seq, bm), each = (slots * a.kv + 7) / 8;
+    if (!alike || !a.off || a.rows > 16ll * bm * a.n_seq) return 0;
+    const long long turns = (each + 16 * a.kv - 1) / (16 * a.kv);
+    return (int)((each + turns - 1) / turns);
+}
 
 // The tile of a rank: its sequence and its number in it; false: none.  Tiles of
 // a causal launch differ in work (the t-th of a sequence meets t + 1 tiles of

@@ -363,6 +363,7 @@ struct AttnArgs {
     int8_t *y, *ye;
     int cols, parts, part, q, out_vec;  // out_vec: rows of y can be written eight mantissas at a time
     uint32_t *flags;
+    int chunk;  // of a launch's items, for one XCD (see att_item)
 };
 hipError_t launch_attention_fwd(const AttnArgs &a, hipStream_t st);
 // Rows of nh heads of d elements into heads of dp elements.
