@@ -61,66 +61,87 @@ __global__ __launch_bounds__(256) void cache_store_kernel(CacheArgs p, long long
 //
 // A workgroup takes a block of one key head and up to 16 of its query heads,
 // a wave 64 of the keys: 16x16x64 products with the keys along the rows and
-// the query heads in the columns, so that a lane's 16 weights are 16 bytes of
-// the second product's operand.  Values lie in LDS as they come, two elements
-// to a byte: a transposing read of 16 columns of bytes is unpacked into two
-// operands, the even elements and the odd ones.  Mantissas are unpacked as 16
-// times their value (their four bits in a byte's upper half), which the exact
-// sums drop.  The next block's keys, values and exponents are in flight while
-// one is computed.
-template <int DP>  // head size, up: 64 or 128
+// the query heads in the columns.  Where eight or four columns are enough for
+// the heads, each head has SUB of them, and each of those weighs its share of
+// the wave's keys.  The weights' digits change hands in LDS, and a wave sums
+// 32 (DP 64: 16) of the elements over all keys.  Values lie in LDS as they
+// come, two elements to a byte: a transposing read of 16 columns of bytes is
+// unpacked into two operands, the even elements and the odd ones.  Mantissas
+// are unpacked as 16 times their value (their four bits in a byte's upper half),
+// which the exact sums drop.  The next block's keys, values and exponents are in
+// flight while one is computed.
+template <int SUB>
+__device__ __forceinline__ float heads_max(float v) {
+    v = col_max(v);
+    if (SUB > 1) v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x128, 15, 15, true)));
+    if (SUB > 2) v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x124, 15, 15, true)));
+    return v;
+}
+template <int SUB>
+__device__ __forceinline__ int heads_sum(int v) {
+    v = col_reduce(v, Add{});
+    if (SUB > 1) v += __builtin_amdgcn_update_dpp(0, v, 0x128, 15, 15, true);
+    if (SUB > 2) v += __builtin_amdgcn_update_dpp(0, v, 0x124, 15, 15, true);
+    return v;
+}
+template <int DP, int SUB>  // head size, up: 64 or 128
 __global__ __launch_bounds__(256, 4) void cache_attention_kernel(CacheArgs p, AttnArgs a) {
-    constexpr int NS = DP / 64, NB = DP / 32, PITCH = DP / 2 + 16, NUM = 20;  // NUM: sums' pitch, one bank to a lane
+    constexpr int NS = DP / 64, PITCH = DP / 2 + 16, HC = 16 / SUB, TN = 4 / SUB;
     __shared__ __align__(16) int8_t sv[256 * PITCH];
     __shared__ __align__(16) float sfk[256], sfv[256];
-    __shared__ int scum[256], swave[4], sred[4];
+    __shared__ __align__(16) int sdigit[2][4][16][4][4];  // high and low: wave, head, keys 4 c .., 16 t ..
+    __shared__ __align__(16) int scum[256];
+    __shared__ int slen[256], swave[4], sred[4], ssum[4][16];
     __shared__ float smax[4][16];
-    __shared__ int snum[DP * NUM], ssum[16];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, c = lane >> 4;
+    const int hc = col & (HC - 1), tp = col / HC * TN;  // head of the group, first 16 keys it weighs
     const int gcs = (a.group + 15) / 16, units = a.kv * gcs, hb = a.d >> 1;
-    int s0 = 0, blocks = 0;  // sequences s0 .. s0 + 255 and their blocks of 256 keys
-    long long total = 0, before = 0;
-    // an item: block b of a sequence, a key head and 16 of its query heads; in
+    // Items: block b of a sequence, a key head and 16 of its query heads; in
     // groups of eight blocks, a block's heads eight apart: the heads of a slot
-    // share cache lines, and these workgroups an XCD
+    // share cache lines, and these workgroups an XCD.  A workgroup's items lie
+    // gridDim (a multiple of 8) apart.
+    const unsigned turn = gridDim.x >> 3;
+    const int by_q = (int)turn / units, by_u = (int)turn % units, r8 = blockIdx.x & 7;
+    unsigned before = 0;
+    int s0 = 0, blocks = 0;  // sequences s0 .. s0 + 255 and their blocks of 256 keys
     struct Work {
-        long long it;
+        int q, unit;  // blocks 8 q .., key head and its query heads
         int seq, b, kvh, g0, len;
     };
-    auto locate = [&](long long it, Work &w) {  // the first item from `it` on that there is
-        w.it = it;
-        for (; w.it < total; w.it += gridDim.x) {
-            const int unit = (int)(w.it / 8 % units), blk = (int)(w.it / 8 / units) * 8 + (int)(w.it % 8);
-            if (blk >= blocks) continue;
-            int lo = 0, hi = 255;
-            while (lo < hi) {
-                const int mid = (lo + hi) >> 1;
-                if (scum[mid] > blk) hi = mid;
-                else lo = mid + 1;
+    auto locate = [&](Work &w) {  // the first item from (q, unit) on that there is
+        while (8 * w.q < blocks) {
+            const int blk = 8 * w.q + r8;
+            if (blk < blocks) {
+                const int4 x = ((const int4 *)scum)[lane];
+                const int i = __popcll(__ballot(x.x <= blk)) + __popcll(__ballot(x.y <= blk)) + __popcll(__ballot(x.z <= blk)) +
+                              __popcll(__ballot(x.w <= blk));
+                w.seq = s0 + i;
+                w.b = blk - __builtin_amdgcn_readfirstlane(i ? scum[i - 1] : 0);
+                w.kvh = gcs == 1 ? w.unit : w.unit / gcs;
+                w.g0 = (w.unit - w.kvh * gcs) * 16;
+                w.len = __builtin_amdgcn_readfirstlane(slen[i]);
+                return true;
             }
-            w.seq = __builtin_amdgcn_readfirstlane(s0 + lo);
-            w.b = __builtin_amdgcn_readfirstlane(blk - (lo ? scum[lo - 1] : 0));
-            w.kvh = unit / gcs;
-            w.g0 = unit % gcs * 16;
-            w.len = min(max(p.lengths[w.seq], 0), p.tokens);
-            return true;
+            w.q += by_q;
+            w.unit += by_u;
+            if (w.unit >= units) {
+                w.unit -= units;
+                ++w.q;
+            }
         }
         return false;
+    };
+    auto slot_of = [&](const Work &w) {  // of key 256 b + tid
+        const int j = 256 * w.b + tid;
+        if (j >= w.len) return -1;
+        const int page = p.table[(long long)w.seq * p.per + (j >> p.shift)];
+        return page >= 0 && page < p.pages ? (page << p.shift) + (j & (p.page - 1)) : -2;
     };
     // what is read of a block: lane (col, c) takes 16 bytes (DP 64: 8) of the
     // wave's keys col, 16 + col, ..; thread t the exponents of key t
     uint32_t kw[4][2 * NS], vw[4][2 * NS];
     float fk = 0.0f, fv = 0.0f;
-    auto slot_of = [&](const Work &w, int j) {
-        if (j >= w.len) return -1;
-        const int page = p.table[(long long)w.seq * p.per + (j >> p.shift)];
-        return page >= 0 && page < p.pages ? (page << p.shift) + (j & (p.page - 1)) : -2;
-    };
-    auto fetch = [&](const Work &w) {
-        const int j0 = 256 * w.b, mine = slot_of(w, j0 + tid);
-        int slot[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) slot[t] = slot_of(w, j0 + 64 * wave + 16 * t + col);
+    auto fetch = [&](const Work &w, int mine) {
         fk = fv = 0.0f;
         if (mine >= 0) {
             const long long at = (long long)mine * p.kv + w.kvh;
@@ -130,10 +151,11 @@ __global__ __launch_bounds__(256, 4) void cache_attention_kernel(CacheArgs p, At
         if (mine == -2) atomicOr(p.flags, IE_FLAG_INDEX);
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            const long long at = ((long long)slot[t] * p.kv + w.kvh) * hb + 8 * NS * c;
+            const int slot = __shfl(mine, 16 * t + col, 64);
+            const long long at = ((long long)slot * p.kv + w.kvh) * hb + 8 * NS * c;
 #pragma unroll
             for (int i = 0; i < 2 * NS; ++i) kw[t][i] = vw[t][i] = 0;
-            if (slot[t] < 0) continue;
+            if (slot < 0) continue;
             if (8 * NS * (c + 1) <= hb) {
                 __builtin_memcpy(kw[t], p.k + at, 8 * NS);
                 __builtin_memcpy(vw[t], p.v + at, 8 * NS);
@@ -146,7 +168,8 @@ __global__ __launch_bounds__(256, 4) void cache_attention_kernel(CacheArgs p, At
 
     for (s0 = 0; s0 < p.n; s0 += 256) {
         // blocks of the next 256 sequences, and their running sum
-        int run = s0 + tid < p.n ? (min(max(p.lengths[s0 + tid], 0), p.tokens) + 255) >> 8 : 0;
+        const int len = s0 + tid < p.n ? min(max(p.lengths[s0 + tid], 0), p.tokens) : 0;
+        int run = (len + 255) >> 8;
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
             const int v = __shfl_up(run, o, 64);
@@ -157,38 +180,31 @@ __global__ __launch_bounds__(256, 4) void cache_attention_kernel(CacheArgs p, At
         __syncthreads();
         for (int i = 0; i < wave; ++i) run += swave[i];
         scum[tid] = run;
+        slen[tid] = len;
         __syncthreads();
-        blocks = scum[255];
-        total = (long long)((blocks + 7) / 8) * 8 * units;
-        long long it = (long long)blockIdx.x - before % gridDim.x;
-        if (it < 0) it += gridDim.x;
-        before += total;
+        blocks = __builtin_amdgcn_readfirstlane(scum[255]);
+        const unsigned first = (blockIdx.x / 8 + turn - before) % turn;
+        before = (before + (unsigned)((blocks + 7) / 8) % turn * ((unsigned)units % turn)) % turn;
         Work w;
-        bool more = locate(it, w);
-        if (more) fetch(w);
+        w.q = (int)first / units;
+        w.unit = (int)first - w.q * units;
+        bool more = locate(w);
+        if (more) fetch(w, slot_of(w));
         while (more) {
             const Work now = w;
-            // this block's values and exponents into LDS
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                int8_t *dst = sv + (64 * wave + 16 * t + col) * PITCH + 8 * NS * c;
-                __builtin_memcpy(dst, vw[t], 8 * NS);
-            }
             sfk[tid] = fk;
             sfv[tid] = fv;
             const int em = wave_max_dpp(__float_as_int(fv));
             if (lane == 0) sred[wave] = em;
-            for (int i = tid; i < DP * NUM; i += 256) snum[i] = 0;
-            if (tid < 16) ssum[tid] = 0;
             // the query heads, their bytes in the order of unpacked keys
-            const int ng = min(16, a.group - now.g0), head = now.kvh * a.group + now.g0 + col;
+            const int ng = min(HC, a.group - now.g0), head = now.kvh * a.group + now.g0 + hc;
             const float r = a.c * pow2f(clip_e(a.xe[a.x_row ? now.seq : 0]));
             v4i q[NS];
 #pragma unroll
             for (int i = 0; i < NS; ++i) {
                 q[i] = v4i{0, 0, 0, 0};
                 const int e0 = 16 * NS * c + 16 * i;
-                if (col < ng && e0 < a.d) {
+                if (hc < ng && e0 < a.d) {
                     uint32_t x[4];
                     __builtin_memcpy(x, a.x + (long long)now.seq * a.width + (long long)head * a.d + e0, 16);
 #pragma unroll
@@ -198,6 +214,15 @@ __global__ __launch_bounds__(256, 4) void cache_attention_kernel(CacheArgs p, At
                     }
                 }
             }
+            w.q += by_q;
+            w.unit += by_u;
+            if (w.unit >= units) {
+                w.unit -= units;
+                ++w.q;
+            }
+            more = locate(w);
+            int next = -1;
+            if (more) next = slot_of(w);
             v4i acc[4];
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
@@ -213,89 +238,105 @@ __global__ __launch_bounds__(256, 4) void cache_attention_kernel(CacheArgs p, At
                     acc[t] = mfma(k, q[i], acc[t]);
                 }
             }
-            more = locate(now.it + gridDim.x, w);
-            if (more) fetch(w);
-            __syncthreads();
-            const float fmx = __int_as_float(max(max(sred[0], sred[1]), max(sred[2], sred[3])));
-            const int eb = fmx > 0.0f ? (__float_as_int(fmx) >> 23) - 127 : ATT_E_LO;
-            const float down = pow2f(-eb);
-            float f[4][4], m = -__builtin_inff();
+            float f[TN][4], m = -__builtin_inff();
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const float4 x = *(const float4 *)&sfk[64 * wave + 16 * t + 4 * c];
+            for (int j = 0; j < TN; ++j) {
+                const float4 x = *(const float4 *)&sfk[64 * wave + 16 * (tp + j) + 4 * c];
                 const float fs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    f[t][i] = fs[i] > 0.0f ? (float)acc[t][i] * (0.0625f * fs[i]) : -__builtin_inff();
-                    m = fmaxf(m, f[t][i]);
+                    int s = acc[j][i];
+                    if (SUB == 2) s = tp ? acc[2 + j][i] : s;
+                    if (SUB == 4) s = tp & 2 ? (tp & 1 ? acc[3][i] : acc[2][i]) : (tp & 1 ? acc[1][i] : s);
+                    f[j][i] = fs[i] > 0.0f ? (float)s * (0.0625f * fs[i]) : -__builtin_inff();
+                    m = fmaxf(m, f[j][i]);
                 }
             }
-            m = col_max(m);
+            m = heads_max<SUB>(m);
             if (lane < 16) smax[wave][lane] = m;
             __syncthreads();
-            m = fmaxf(fmaxf(smax[0][col], smax[1][col]), fmaxf(smax[2][col], smax[3][col]));
-            v4i dh, dl;
-            uint32_t sum = 0;
+            // values into LDS: every wave is past the last block's
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                const float4 x = *(const float4 *)&sfv[64 * wave + 16 * t + 4 * c];
+                int8_t *dst = sv + (64 * wave + 16 * t + col) * PITCH + 8 * NS * c;
+                __builtin_memcpy(dst, vw[t], 8 * NS);
+            }
+            if (more) fetch(w, next);
+            const float fmx = __int_as_float(max(max(sred[0], sred[1]), max(sred[2], sred[3])));
+            const int eb = fmx > 0.0f ? (__float_as_int(fmx) >> 23) - 127 : ATT_E_LO;
+            const float down = pow2f(-eb);
+            m = fmaxf(fmaxf(smax[0][col], smax[1][col]), fmaxf(smax[2][col], smax[3][col]));
+            uint32_t sum = 0;
+            int dh[TN], dl[TN];
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                const float4 x = *(const float4 *)&sfv[64 * wave + 16 * (tp + j) + 4 * c];
                 const float fvs[4] = {x.x, x.y, x.z, x.w};
                 int bits[4];
                 uint32_t whole_n[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     // a key that is not there: a score of minus infinity, whose weight rounds to 0, and a factor of 0
-                    const float y = weight(f[t][i] - m, r);
+                    const float y = weight(f[j][i] - m, r);
                     bits[i] = __float_as_int(__builtin_fmaf(y, fvs[i] * down, RINT_128));
                     whole_n[i] = (uint32_t)__float_as_int(y + RINT_MAGIC);
                 }
                 sum += whole_n[0] + whole_n[1];
                 sum += whole_n[2] + whole_n[3];
-                int h4, l4;
-                digits4(bits[0], bits[1], bits[2], bits[3], h4, l4);
-                dh[t] = h4;
-                dl[t] = l4;
+                digits4(bits[0], bits[1], bits[2], bits[3], dh[j], dl[j]);
             }
-            sum = (uint32_t)col_reduce((int)(sum - 16u * (uint32_t)RINT_BITS), Add{});
-            if (lane < ng) atomicAdd(&ssum[lane], (int)sum);
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                sdigit[0][wave][hc][c][tp + j] = dh[j];
+                sdigit[1][wave][hc][c][tp + j] = dl[j];
+            }
+            sum = (uint32_t)heads_sum<SUB>((int)(sum - 4u * TN * (uint32_t)RINT_BITS));
+            if (lane < HC) ssum[wave][lane] = (int)sum;
+            __syncthreads();
             // the second product: rows are bytes' elements, even ones, then odd ones
+            const int e = DP == 128 ? wave : wave >> 1;
+            const bool upper = wave & 1;  // DP 64: the odd elements
+            const long long out = ((long long)now.seq * p.blocks + now.b) * a.heads + now.kvh * a.group + now.g0;
+            if (16 * e < hb) {
+                v4i y[2][2] = {};
 #pragma unroll
-            for (int e = 0; e < NB; ++e) {
-                if (16 * e >= hb) break;
-                const int g = lane & 15, kk = g >> 1;
-                const int8_t *at = sv + (64 * wave + 16 * (kk >> 2) + 4 * c + (kk & 3)) * PITCH + 16 * e + (g & 1) * 8;
-                typedef __attribute__((address_space(3))) v2i lds_v2i;
-                const v2i x0 = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i *)at);
-                const v2i x1 = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i *)(at + 32 * PITCH));
-                const uint32_t xs[4] = {(uint32_t)x0.x, (uint32_t)x0.y, (uint32_t)x1.x, (uint32_t)x1.y};
-                v4i even, odd;
+                for (int s = 0; s < 4; ++s) {
+                    const int g = lane & 15, kk = g >> 1;
+                    const int8_t *at = sv + (64 * s + 16 * (kk >> 2) + 4 * c + (kk & 3)) * PITCH + 16 * e + (g & 1) * 8;
+                    typedef __attribute__((address_space(3))) v2i lds_v2i;
+                    const v2i x0 = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i *)at);
+                    const v2i x1 = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i *)(at + 32 * PITCH));
+                    const uint32_t xs[4] = {(uint32_t)x0.x, (uint32_t)x0.y, (uint32_t)x1.x, (uint32_t)x1.y};
+                    const v4i h4 = *(const v4i *)sdigit[0][s][hc][c], l4 = *(const v4i *)sdigit[1][s][hc][c];
+                    v4i even, odd;
 #pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    even[z] = (int)(xs[z] << 4 & 0xf0f0f0f0u);
-                    odd[z] = (int)(xs[z] & 0xf0f0f0f0u);
-                }
-                const v4i zero = {0, 0, 0, 0};
-                const v4i eh = mfma(even, dh, zero), el = mfma(even, dl, zero), oh = mfma(odd, dh, zero), ol = mfma(odd, dl, zero);
-                if (col < ng) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        atomicAdd(&snum[(32 * e + 4 * c + i) * NUM + col], (eh[i] * 256 + el[i]) >> 4);
-                        atomicAdd(&snum[(32 * e + 16 + 4 * c + i) * NUM + col], (oh[i] * 256 + ol[i]) >> 4);
+                    for (int z = 0; z < 4; ++z) {
+                        even[z] = (int)((DP == 64 && upper ? xs[z] : xs[z] << 4) & 0xf0f0f0f0u);
+                        odd[z] = (int)(xs[z] & 0xf0f0f0f0u);
+                    }
+                    y[0][0] = mfma(even, h4, y[0][0]);
+                    y[0][1] = mfma(even, l4, y[0][1]);
+                    if (DP == 128) {
+                        y[1][0] = mfma(odd, h4, y[1][0]);
+                        y[1][1] = mfma(odd, l4, y[1][1]);
                     }
                 }
-            }
-            __syncthreads();
-            // this block's sums (elements in their own order)
-            const long long out = ((long long)now.seq * p.blocks + now.b) * a.heads + now.kvh * a.group + now.g0;
-            for (int i = tid; i < ng * a.d; i += 256) {
-                const int hd = i / a.d, e = i - hd * a.d, pos = (e >> 5) * 32 + (e & 1) * 16 + (e >> 1 & 15);
-                p.num[out * a.d + i] = snum[pos * NUM + hd];
+                int *to = p.num + (out + hc) * a.d + 32 * e + 8 * c;
+                if (col < ng && 32 * e + 8 * c < a.d) {
+                    int x[8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        x[2 * i] = (y[0][0][i] * 256 + y[0][1][i]) >> 4;
+                        if (DP == 128) x[2 * i + 1] = (y[1][0][i] * 256 + y[1][1][i]) >> 4;
+                        else to[2 * i + upper] = x[2 * i];
+                    }
+                    if (DP == 128) __builtin_memcpy(to, x, 32);
+                }
             }
             if (tid < ng) {
-                const float mt = fmaxf(fmaxf(smax[0][tid], smax[1][tid]), fmaxf(smax[2][tid], smax[3][tid]));
-                p.top[out + tid] = int4{__float_as_int(mt), ssum[tid], eb, 0};
+                const int s = ssum[0][tid] + ssum[1][tid] + ssum[2][tid] + ssum[3][tid];
+                p.top[out + tid] = int4{__float_as_int(m), s, eb, 0};
             }
-            __syncthreads();
         }
     }
 }
@@ -365,6 +406,7 @@ __global__ __launch_bounds__(256) void cache_join_kernel(CacheArgs p, AttnArgs a
     __syncthreads();
     double y = 0.0;
     if (tid < piece) {
+#pragma unroll 8
         for (int i = 0; i < parts; ++i) y += sp[i * quads + (tid >> 2)][tid & 3];
         y = den > 0.0 ? y * (1.0 / den) : 0.0;
     }
@@ -398,8 +440,11 @@ hipError_t launch_cache_attention(const CacheArgs &c, const AttnArgs &a, hipStre
     const long long cap = 4 * NCU;
     const dim3 grid((unsigned)(most < cap ? most : cap));
     prof_begin(st, PROF_ATT_CACHE);
-    if (a.d <= 64) hipLaunchKernelGGL(cache_attention_kernel<64>, grid, dim3(256), 0, st, c, a);
-    else hipLaunchKernelGGL(cache_attention_kernel<128>, grid, dim3(256), 0, st, c, a);
+    const int sub = a.group <= 4 ? 4 : a.group <= 8 ? 2 : 1;
+#define IE_CASE(DP_, SUB_) \
+    if (a.d <= DP_ && a.d > DP_ - 64 && sub == SUB_) hipLaunchKernelGGL((cache_attention_kernel<DP_, SUB_>), grid, dim3(256), 0, st, c, a);
+    IE_CASE(64, 1) IE_CASE(64, 2) IE_CASE(64, 4) IE_CASE(128, 1) IE_CASE(128, 2) IE_CASE(128, 4)
+#undef IE_CASE
     prof_end(st, PROF_ATT_CACHE);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
