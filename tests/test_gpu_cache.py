@@ -92,7 +92,8 @@ def test_lengths(lengths, page):
 
 
 @pytest.mark.parametrize("heads,kv,d", [(1, 1, 16), (2, 2, 32), (16, 1, 48), (17, 1, 64), (40, 2, 64), (6, 3, 80), (12, 12, 96),
-                                        (8, 2, 112), (32, 8, 128), (33, 33, 16)])
+                                        (8, 2, 112), (32, 8, 128), (33, 33, 16), (5, 1, 64), (16, 2, 128), (14, 2, 96), (9, 1, 128),
+                                        (3, 1, 48)])
 @pytest.mark.parametrize("group", [o.ROW, o.TENSOR])
 def test_heads(heads, kv, d, group):
     announce(f"cache attention heads {heads} {kv} {d}")
