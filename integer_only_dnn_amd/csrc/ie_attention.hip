@@ -47,22 +47,22 @@ hipError_t launch_attention_pad(const int8_t *x, long long rows, int nh, int d, 
 // SHORT, for batches of short sequences: up to 256 keys have their scores kept
 // in registers between the passes (64 of them), so that q and k meet once; all
 // keys are in LDS at once, and the values, loaded with them, take their place.
-template <int DP, bool ROW, bool CAUSAL, bool SHORT>
-__global__ __launch_bounds__(256, DP > 64 ? 3 : 4) void attn_fwd_kernel(AttnArgs p) {
-    using T = HeadTile<DP>;
-    constexpr int KS = T::KS, NE = DP / 16;
-    __shared__ __align__(16) int8_t tiles_lds[4][T::BYTES];
+template <int DP, bool ROW, bool CAUSAL, bool SHORT, int SPLIT>
+__global__ __launch_bounds__(256, SPLIT > 1 ? 2 : DP > 64 ? 3 : 4) void attn_fwd_kernel(AttnArgs p) {
+    using T = HeadTile<DP, 256 / SPLIT>;
+    constexpr int KS = T::KS, NE = DP / 16, BM = 64 / SPLIT, NB = SPLIT == 1 ? 2 : SPLIT;
+    __shared__ __align__(16) int8_t tiles_lds[2 * NB][T::BYTES];
     __shared__ __align__(16) float factors_lds[256];
-    __shared__ __align__(16) float scaled_lds[2][64], most_lds[4];  // factors 2^-E, largest ones
-    int8_t(*sk)[T::BYTES] = tiles_lds, (*sv)[T::BYTES] = tiles_lds + 2;
+    __shared__ __align__(16) float scaled_lds[NB][64], most_lds[4];  // factors 2^-E, largest ones
+    int8_t(*sk)[T::BYTES] = tiles_lds, (*sv)[T::BYTES] = tiles_lds + NB;
     float(*sf)[64] = (float(*)[64])factors_lds;
     const Item it = att_item(p, p.group);
     Span sp;
     int tile;
-    if (!rank_tile<CAUSAL>(p, it.rank, 64, sp, tile)) return;
-    const int h = it.kvh * p.group + it.gh, q0 = 64 * tile;
+    if (!rank_tile<CAUSAL>(p, it.rank, BM, sp, tile)) return;
+    const int h = it.kvh * p.group + it.gh, q0 = BM * tile;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, quad = lane >> 4;
-    const int n = sp.n, qw = q0 + 16 * wave, qi = qw + (lane & 15);
+    const int n = sp.n, qw = q0 + (SPLIT == 1 ? 16 * wave : 0), qi = qw + (lane & 15);
     const bool ok = qi < n, idle = qw >= n;
     const int8_t *base = p.x + (long long)sp.a * p.width;
     const int8_t *kh = base + (long long)(p.heads + it.kvh) * p.dp, *vh = kh + (long long)p.kv * p.dp;
@@ -71,7 +71,7 @@ __global__ __launch_bounds__(256, DP > 64 ? 3 : 4) void attn_fwd_kernel(AttnArgs
     const float r = p.c * pow2f(eq) * (ROW ? 1.0f : pow2f(eq));
     v4i q[KS];
     head_regs<KS>(base + (long long)qi * p.width + h * p.dp, ok, p.dp, lane, q);
-    const int keys = CAUSAL ? min(n, q0 + 64) : n, tiles = (keys + 63) / 64;
+    const int keys = CAUSAL ? min(n, q0 + BM) : n, tiles = (keys + 63) / 64;
     const int last = CAUSAL ? min(n, qw + 16) : n;  // keys of this wave
 
     v4i hi[NE] = {}, lo[NE] = {};
@@ -101,9 +101,11 @@ __global__ __launch_bounds__(256, DP > 64 ? 3 : 4) void attn_fwd_kernel(AttnArgs
             lo[e] = mfma(vt, dl, lo[e]);
         }
     };
-    auto finish = [&](float m, int mi, int top) {
+    auto total = [&]() {
         sum -= 4 * blocks * (uint32_t)(ROW ? RINT_BITS : RINT_BITS + 128);
         sum = (uint32_t)col_reduce((int)sum, Add{});
+    };
+    auto finish = [&](float m, int mi, int top) {
         const double inv = 1.0 / (double)sum;
         double y[4 * NE];
 #pragma unroll
@@ -218,6 +220,7 @@ __global__ __launch_bounds__(256, DP > 64 ? 3 : 4) void attn_fwd_kernel(AttnArgs
                 gather(tiles_lds[t], dh, dl);
             }
             mi = (int)m;  // where all rows share an exponent the scores are whole
+            total();
             finish(m, mi, top);
             return;
         }
@@ -227,25 +230,33 @@ __global__ __launch_bounds__(256, DP > 64 ? 3 : 4) void attn_fwd_kernel(AttnArgs
     k.init(p.width, p.dp);
     v.init(p.width, p.dp);
     float fe = 0.0f, down = 1.0f;
+    // SPLIT: a wave takes every fourth tile, and stages it itself
+    const int me = SPLIT == 1 ? tid : lane, first = SPLIT == 1 ? 0 : wave;
+    auto buffer = [&](int t) { return SPLIT == 1 ? t & 1 : wave; };
+    auto fence = [&]() {
+        if (SPLIT == 1) __syncthreads();
+        else __builtin_amdgcn_wave_barrier();
+    };
     auto fetch = [&](int t, bool values) {
         k.fetch(kh, p.width, 64 * t, keys, p.dp);
         if (values) v.fetch(vh, p.width, 64 * t, keys, p.dp);
-        if (ROW && tid < 64) fe = pow2f(clip_e(xe[min(64 * t + tid, n - 1)]));
+        if (ROW && me < 64) fe = pow2f(clip_e(xe[min(64 * t + me, n - 1)]));
     };
     auto put = [&](int t, bool values) {
-        k.put(sk[t & 1]);
-        if (values) v.put(sv[t & 1]);
-        if (ROW && tid < 64) {
-            sf[t & 1][tid] = fe;
-            if (!CAUSAL && values) scaled_lds[t & 1][tid] = fe * down;
-            if (!values) most_lds[t & 1] = __int_as_float(wave_max_dpp(__float_as_int(fe)));
+        if (SPLIT > 1) __builtin_amdgcn_wave_barrier();
+        k.put(sk[buffer(t)]);
+        if (values) v.put(sv[buffer(t)]);
+        if (ROW && me < 64) {
+            sf[buffer(t)][me] = fe;
+            if (!CAUSAL && values) scaled_lds[buffer(t)][me] = fe * down;
+            if (!values) most_lds[buffer(t)] = __int_as_float(wave_max_dpp(__float_as_int(fe)));
         }
     };
     // scores of 16 keys of a tile
     auto scores = [&](int t, int z) {
         v4i acc = {0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < KS; ++i) acc = mfma(T::frag_r(sk[t & 1], z, i, lane), q[i], acc);
+        for (int i = 0; i < KS; ++i) acc = mfma(T::frag_r(sk[buffer(t)], z, i, lane), q[i], acc);
         return acc;
     };
     auto factors = [&](const float *at, int z, float (&f)[4]) {
@@ -265,13 +276,13 @@ __global__ __launch_bounds__(256, DP > 64 ? 3 : 4) void attn_fwd_kernel(AttnArgs
     auto largest = [&](auto masked, int t) {
         constexpr bool each = CAUSAL && decltype(masked)::value;
         const int lim = limit(t);
-        if (ROW && !each) em = fmaxf(em, most_lds[t & 1]);
+        if (ROW && !each) em = fmaxf(em, most_lds[buffer(t)]);
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
             if (masked.value && 64 * t + 16 * z >= last) break;
             const v4i acc = scores(t, z);
             float f[4];
-            factors(sf[t & 1], z, f);
+            factors(sf[buffer(t)], z, f);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const bool on = !masked.value || 16 * z + i <= lim;
@@ -284,11 +295,11 @@ __global__ __launch_bounds__(256, DP > 64 ? 3 : 4) void attn_fwd_kernel(AttnArgs
             }
         }
     };
-    fetch(0, false);
-    for (int t = 0; t < tiles; ++t) {
+    if (first < tiles) fetch(first, false);
+    for (int t = first; t < tiles; t += SPLIT) {
         put(t, false);
-        if (t + 1 < tiles) fetch(t + 1, false);
-        __syncthreads();
+        if (t + SPLIT < tiles) fetch(t + SPLIT, false);
+        fence();
         if (idle) continue;
         if (whole(t)) largest(Bool<false>{}, t);
         else largest(Bool<true>{}, t);
@@ -298,6 +309,20 @@ __global__ __launch_bounds__(256, DP > 64 ? 3 : 4) void attn_fwd_kernel(AttnArgs
         if (CAUSAL) em = col_max(em);
     } else {
         mi = col_reduce(mi, Max{});
+    }
+    if constexpr (SPLIT > 1) {
+        __shared__ float sm[2][4][16];
+        __shared__ int smi[4][16];
+        if (lane < 16) {
+            sm[0][wave][lane] = m;
+            sm[1][wave][lane] = em;
+            smi[wave][lane] = mi;
+        }
+        __syncthreads();
+        const int col = lane & 15;
+        m = fmaxf(fmaxf(sm[0][0][col], sm[0][1][col]), fmaxf(sm[0][2][col], sm[0][3][col]));
+        em = fmaxf(fmaxf(sm[1][0][col], sm[1][1][col]), fmaxf(sm[1][2][col], sm[1][3][col]));
+        mi = max(max(smi[0][col], smi[1][col]), max(smi[2][col], smi[3][col]));
     }
     const int top = ROW ? (__float_as_int(em) >> 23) - 127 : eq;  // E
     if (ROW) down = pow2f(-top);
@@ -313,26 +338,37 @@ __global__ __launch_bounds__(256, DP > 64 ? 3 : 4) void attn_fwd_kernel(AttnArgs
             if (masked.value && 64 * t + 16 * z >= last) continue;
             const v4i acc = scores(t, z);
             float f[4], d[4];
-            factors(sf[t & 1], z, f);
+            factors(sf[buffer(t)], z, f);
 #pragma unroll
             for (int i = 0; i < 4; ++i) d[i] = ROW ? __builtin_fmaf((float)acc[i], f[i], -m) : (float)(acc[i] - mi);
             int a, c;
-            if (!CAUSAL) factors(scaled_lds[t & 1], z, f);
+            if (!CAUSAL) factors(scaled_lds[buffer(t)], z, f);
             weigh4(masked, d, f, down, z, lim, a, c);
             dh[z] = a;
             dl[z] = c;
         }
     };
-    fetch(0, true);
-    for (int t = 0; t < tiles; ++t) {
+    if (first < tiles) fetch(first, true);
+    for (int t = first; t < tiles; t += SPLIT) {
         put(t, true);
-        if (t + 1 < tiles) fetch(t + 1, true);
-        __syncthreads();
+        if (t + SPLIT < tiles) fetch(t + SPLIT, true);
+        fence();
         if (idle || 64 * t >= last) continue;
         v4i dh, dl;
         if (whole(t)) weigh(Bool<false>{}, t, dh, dl);
         else weigh(Bool<true>{}, t, dh, dl);
-        gather(sv[t & 1], dh, dl);
+        gather(sv[buffer(t)], dh, dl);
+    }
+    total();
+    if constexpr (SPLIT > 1) {
+        int *x = (int *)&tiles_lds[0][0];
+        static_assert(sizeof tiles_lds >= 3 * 4 * NE * 64 * sizeof(int), "a digit's sums fit the tiles");
+        gather_waves<4 * NE>(x, hi, wave, lane);
+        gather_waves<4 * NE>(x, lo, wave, lane);
+        v4i s4 = {(int)sum, 0, 0, 0};
+        gather_waves<4>(x, (v4i(&)[1])s4, wave, lane);
+        sum = (uint32_t)s4[0];
+        if (wave) return;
     }
     if (!idle) finish(m, mi, top);
 }
@@ -390,24 +426,25 @@ hipError_t launch_attention_round(const AttnArgs &a, hipStream_t st) {
     return hipGetLastError();
 }
 
-template <int DP, bool SHORT>
+template <int DP, bool SHORT, int SPLIT>
 static void fwd(AttnArgs a, hipStream_t st) {
-    a.chunk = att_chunk(a, 64, !a.causal);
-    const dim3 grid(att_grid(att_slots(a.rows, a.n_seq, 64), a.kv, a.group)), block(256);
+    a.chunk = att_chunk(a, 64 / SPLIT, !a.causal);
+    const dim3 grid(att_grid(att_slots(a.rows, a.n_seq, 64 / SPLIT), a.kv, a.group)), block(256);
     if (a.x_row) {
-        if (a.causal) hipLaunchKernelGGL((attn_fwd_kernel<DP, true, true, SHORT>), grid, block, 0, st, a);
-        else hipLaunchKernelGGL((attn_fwd_kernel<DP, true, false, SHORT>), grid, block, 0, st, a);
+        if (a.causal) hipLaunchKernelGGL((attn_fwd_kernel<DP, true, true, SHORT, SPLIT>), grid, block, 0, st, a);
+        else hipLaunchKernelGGL((attn_fwd_kernel<DP, true, false, SHORT, SPLIT>), grid, block, 0, st, a);
     } else {
-        if (a.causal) hipLaunchKernelGGL((attn_fwd_kernel<DP, false, true, SHORT>), grid, block, 0, st, a);
-        else hipLaunchKernelGGL((attn_fwd_kernel<DP, false, false, SHORT>), grid, block, 0, st, a);
+        if (a.causal) hipLaunchKernelGGL((attn_fwd_kernel<DP, false, true, SHORT, SPLIT>), grid, block, 0, st, a);
+        else hipLaunchKernelGGL((attn_fwd_kernel<DP, false, false, SHORT, SPLIT>), grid, block, 0, st, a);
     }
 }
 
 template <int DP>
 static void fwd(const AttnArgs &a, hipStream_t st) {
     // sequences of up to 256 tokens on the average: most have their scores in registers
-    if (a.rows <= 256ll * max(a.n_seq, 1)) fwd<DP, true>(a, st);
-    else fwd<DP, false>(a, st);
+    if (a.rows <= 256ll * max(a.n_seq, 1)) fwd<DP, true, 1>(a, st);
+    else if (att_slots(a.rows, a.n_seq, 64) * a.heads < 2 * NCU) fwd<DP, false, 4>(a, st);
+    else fwd<DP, false, 1>(a, st);
 }
 
 hipError_t launch_attention_fwd(const AttnArgs &a, hipStream_t st) {

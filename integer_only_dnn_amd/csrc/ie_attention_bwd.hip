@@ -109,19 +109,19 @@ __global__ __launch_bounds__(256) void attn_scale_kernel(AttnArgs p, AttnBwd b) 
 
 // dQ: a workgroup of four waves takes 64 queries of a head, 16 to a wave, one
 // to four lanes, as in the forward pass; keys and values pass through LDS.
-template <int DP, bool ROW, bool CAUSAL>
+template <int DP, bool ROW, bool CAUSAL, int SPLIT>
 __global__ __launch_bounds__(256, DP > 64 ? 2 : 3) void attn_dq_kernel(AttnArgs p, AttnBwd bw) {
-    using T = HeadTile<DP>;
-    constexpr int KS = T::KS, NE = DP / 16;
-    __shared__ __align__(16) int8_t sk[2][T::BYTES], sv[2][T::BYTES];
-    __shared__ __align__(16) float sf[2][64];
+    using T = HeadTile<DP, 256 / SPLIT>;
+    constexpr int KS = T::KS, NE = DP / 16, BM = 64 / SPLIT, NB = SPLIT == 1 ? 2 : SPLIT;
+    __shared__ __align__(16) int8_t sk[NB][T::BYTES], sv[NB][T::BYTES];
+    __shared__ __align__(16) float sf[NB][64];
     const Item it = att_item(p, p.group);
     Span sp;
     int tile;
-    if (!rank_tile<CAUSAL>(p, it.rank, 64, sp, tile)) return;
-    const int h = it.kvh * p.group + it.gh, q0 = 64 * tile;
+    if (!rank_tile<CAUSAL>(p, it.rank, BM, sp, tile)) return;
+    const int h = it.kvh * p.group + it.gh, q0 = BM * tile;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, quad = lane >> 4;
-    const int n = sp.n, qw = q0 + 16 * wave, qi = qw + (lane & 15);
+    const int n = sp.n, qw = q0 + (SPLIT == 1 ? 16 * wave : 0), qi = qw + (lane & 15);
     const bool ok = qi < n, idle = qw >= n;
     const int8_t *base = p.x + (long long)sp.a * p.width;
     const int8_t *kh = base + (long long)(p.heads + it.kvh) * p.dp, *vh = kh + (long long)p.kv * p.dp;
@@ -133,18 +133,19 @@ __global__ __launch_bounds__(256, DP > 64 ? 2 : 3) void attn_dq_kernel(AttnArgs 
     const AttnRow st = bw.row[(long long)h * p.rows + sp.a + min(qi, n - 1)];
     const float fe0 = pow2f(clip_e(xe[0]));
     const Poly scaled = poly(ROW ? st.s : fe0 * st.s);  // 2^-126 .. 2^60: exact products, no subnormal numbers
-    const int keys = CAUSAL ? min(n, q0 + 64) : n, tiles = (keys + 63) / 64;
+    const int keys = CAUSAL ? min(n, q0 + BM) : n, tiles = (keys + 63) / 64;
     const int last = CAUSAL ? min(n, qw + 16) : n;
     T k, v;
     k.init(p.width, p.dp);
     v.init(p.width, p.dp);
     float fe = 0.0f;
+    const int me = SPLIT == 1 ? tid : lane;
     auto fetch = [&](int t) {
         k.fetch(kh, p.width, 64 * t, keys, p.dp);
         v.fetch(vh, p.width, 64 * t, keys, p.dp);
-        if (ROW && tid < 64) fe = pow2f(clip_e(xe[min(64 * t + tid, n - 1)]));
+        if (ROW && me < 64) fe = pow2f(clip_e(xe[min(64 * t + me, n - 1)]));
     };
-    auto weigh = [&](auto masked, int t, v4i &dh, v4i &dl) {
+    auto weigh = [&](auto masked, int t, int buf, v4i &dh, v4i &dl) {
         const int lim = (CAUSAL ? qi : n - 1) - 64 * t - 4 * quad;  // keys seen: 16 z + i <= lim
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
@@ -154,10 +155,10 @@ __global__ __launch_bounds__(256, DP > 64 ? 2 : 3) void attn_dq_kernel(AttnArgs 
             v4i s = {0, 0, 0, 0}, dp = {0, 0, 0, 0};
 #pragma unroll
             for (int i = 0; i < KS; ++i) {
-                s = mfma(T::frag_r(sk[t & 1], z, i, lane), q[i], s);
-                dp = mfma(T::frag_r(sv[t & 1], z, i, lane), g[i], dp);
+                s = mfma(T::frag_r(sk[buf], z, i, lane), q[i], s);
+                dp = mfma(T::frag_r(sv[buf], z, i, lane), g[i], dp);
             }
-            const float4 f = ROW ? *(const float4 *)&sf[t & 1][16 * z + 4 * quad] : float4{fe0, fe0, fe0, fe0};
+            const float4 f = ROW ? *(const float4 *)&sf[buf][16 * z + 4 * quad] : float4{fe0, fe0, fe0, fe0};
             const float fs[4] = {f.x, f.y, f.z, f.w};
             int bits[4];
 #pragma unroll
@@ -174,23 +175,33 @@ __global__ __launch_bounds__(256, DP > 64 ? 2 : 3) void attn_dq_kernel(AttnArgs 
         }
     };
     v4i hi[NE] = {}, lo[NE] = {};
-    fetch(0);
-    for (int t = 0; t < tiles; ++t) {
-        k.put(sk[t & 1]);
-        v.put(sv[t & 1]);
-        if (ROW && tid < 64) sf[t & 1][tid] = fe;
-        if (t + 1 < tiles) fetch(t + 1);
-        __syncthreads();
+    const int first = SPLIT == 1 ? 0 : wave;
+    if (first < tiles) fetch(first);
+    for (int t = first; t < tiles; t += SPLIT) {
+        const int buf = SPLIT == 1 ? t & 1 : wave;
+        if (SPLIT > 1) __builtin_amdgcn_wave_barrier();
+        k.put(sk[buf]);
+        v.put(sv[buf]);
+        if (ROW && me < 64) sf[buf][me] = fe;
+        if (t + SPLIT < tiles) fetch(t + SPLIT);
+        if (SPLIT == 1) __syncthreads();
+        else __builtin_amdgcn_wave_barrier();
         if (idle || 64 * t >= last) continue;
         v4i dh, dl;
-        if (64 * t + 64 <= (CAUSAL ? qw + 1 : n)) weigh(Bool<false>{}, t, dh, dl);
-        else weigh(Bool<true>{}, t, dh, dl);
+        if (64 * t + 64 <= (CAUSAL ? qw + 1 : n)) weigh(Bool<false>{}, t, buf, dh, dl);
+        else weigh(Bool<true>{}, t, buf, dh, dl);
 #pragma unroll
         for (int e = 0; e < NE; ++e) {
-            const v4i kt = T::frag_t(sk[t & 1], e, lane);
+            const v4i kt = T::frag_t(sk[buf], e, lane);
             hi[e] = mfma(kt, dh, hi[e]);
             lo[e] = mfma(kt, dl, lo[e]);
         }
+    }
+    if constexpr (SPLIT > 1) {
+        gather_waves<4 * NE>((int *)&sk[0][0], hi, wave, lane);
+        gather_waves<4 * NE>((int *)&sk[0][0], lo, wave, lane);
+        static_assert(sizeof sk >= 3 * 4 * NE * 64 * sizeof(int), "a digit's sums fit the tiles");
+        if (wave) return;
     }
     if (idle) return;
     const double rate = p.scale / (double)(uint32_t)p.stats[min(row, sp.a + n - 1ll) * p.heads + h].y;
@@ -363,21 +374,9 @@ __global__ __launch_bounds__(256, DP > 64 ? 1 : SPLIT > 1 ? 2 : 3) void attn_dkv
         }
     }
     if constexpr (SPLIT > 1) {
-        // wave 0 gathers the sums, a digit at a time
-        int *x = (int *)&sq[0][0];
         static_assert(sizeof sq >= 3 * 4 * NE * 64 * sizeof(int), "a digit's sums fit the tiles");
 #pragma unroll
-        for (int a = 0; a < 5; ++a) {
-            __syncthreads();
-            if (wave)
-#pragma unroll
-                for (int i = 0; i < 4 * NE; ++i) x[((wave - 1) * 4 * NE + i) * 64 + lane] = acc[a][i >> 2][i & 3];
-            __syncthreads();
-            if (!wave)
-#pragma unroll
-                for (int i = 0; i < 4 * NE; ++i)
-                    acc[a][i >> 2][i & 3] += x[i * 64 + lane] + x[(4 * NE + i) * 64 + lane] + x[(8 * NE + i) * 64 + lane];
-        }
+        for (int a = 0; a < 5; ++a) gather_waves<4 * NE>((int *)&sq[0][0], acc[a], wave, lane);
         if (wave) return;
     }
     if (idle) return;
@@ -396,17 +395,23 @@ __global__ __launch_bounds__(256, DP > 64 ? 1 : SPLIT > 1 ? 2 : 3) void attn_dkv
     store_odd(y, kappa + o_top, p.q, ok, p.d, lane, out + (p.heads + p.kv + it.kvh) * p.d, need + p.heads + p.kv + it.kvh);
 }
 
-template <int DP>
+template <int DP, int SPLIT>
 static void dq(AttnArgs a, const AttnBwd &b, hipStream_t st) {
-    a.chunk = att_chunk(a, 64, !a.causal);
-    const dim3 grid(att_grid(att_slots(a.rows, a.n_seq, 64), a.kv, a.group)), block(256);
+    a.chunk = att_chunk(a, 64 / SPLIT, !a.causal);
+    const dim3 grid(att_grid(att_slots(a.rows, a.n_seq, 64 / SPLIT), a.kv, a.group)), block(256);
     if (a.x_row) {
-        if (a.causal) hipLaunchKernelGGL((attn_dq_kernel<DP, true, true>), grid, block, 0, st, a, b);
-        else hipLaunchKernelGGL((attn_dq_kernel<DP, true, false>), grid, block, 0, st, a, b);
+        if (a.causal) hipLaunchKernelGGL((attn_dq_kernel<DP, true, true, SPLIT>), grid, block, 0, st, a, b);
+        else hipLaunchKernelGGL((attn_dq_kernel<DP, true, false, SPLIT>), grid, block, 0, st, a, b);
     } else {
-        if (a.causal) hipLaunchKernelGGL((attn_dq_kernel<DP, false, true>), grid, block, 0, st, a, b);
-        else hipLaunchKernelGGL((attn_dq_kernel<DP, false, false>), grid, block, 0, st, a, b);
+        if (a.causal) hipLaunchKernelGGL((attn_dq_kernel<DP, false, true, SPLIT>), grid, block, 0, st, a, b);
+        else hipLaunchKernelGGL((attn_dq_kernel<DP, false, false, SPLIT>), grid, block, 0, st, a, b);
     }
+}
+
+template <int DP>
+static void dq(const AttnArgs &a, const AttnBwd &b, hipStream_t st) {
+    if (att_slots(a.rows, a.n_seq, 64) * a.heads < 2 * NCU) dq<DP, 4>(a, b, st);
+    else dq<DP, 1>(a, b, st);
 }
 
 template <int DP>

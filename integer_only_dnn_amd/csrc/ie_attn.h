@@ -316,6 +316,19 @@ __device__ __forceinline__ void head_regs(const int8_t *head, bool ok, int dp, i
     }
 }
 
+// Sums of four waves into the first one's (exact integers), through LDS.
+template <int N>
+__device__ __forceinline__ void gather_waves(int *x, v4i (&acc)[N / 4], int wave, int lane) {
+    __syncthreads();
+    if (wave)
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[((wave - 1) * N + i) * 64 + lane] = acc[i >> 2][i & 3];
+    __syncthreads();
+    if (!wave)
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i >> 2][i & 3] += x[i * 64 + lane] + x[(N + i) * 64 + lane] + x[(2 * N + i) * 64 + lane];
+}
+
 // A result row of one head, one column of the transposed product: value y[4 e +
 // r] of lane l is element 16 e + 4 (l / 16) + r of row l % 16; the other three
 // quarters of the row lie 16, 32 and 48 lanes away.  Rounded to odd at two bits

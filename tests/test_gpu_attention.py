@@ -124,6 +124,30 @@ def test_many_short_sequences():
 
 
 @pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("heads,kv,d,lengths", [(128, 64, 16, [300]), (256, 256, 4, [300]), (130, 2, 128, [290]),
+                                                (8, 8, 64, [280] + 200 * [1]), (8, 8, 128, [1, 259] + 220 * [1]),
+                                                (8, 8, 96, 200 * [2] + [257]), (9, 9, 32, 130 * [0, 3] + [333])],
+                         ids=lambda v: "+".join(map(str, v[:2])) + f"_{len(v)}" if isinstance(v, list) else str(v))
+def test_full_grids(heads, kv, d, lengths, causal):
+    """Tiles enough that no launch splits a tile's keys or queries over its waves."""
+    announce(f"attention full grids {heads} {kv} {d} {len(lengths)} {causal}")
+    rng = np.random.default_rng(heads + d)
+    rows = sum(lengths)
+    X = qkv(rng, rows, heads, kv, d, o.TENSOR if d == 4 else o.ROW)
+    run(X, heads, kv, d, causal, offsets_of(lengths), dO=rand_qt(rng, (rows, heads * d), o.ROW, -12, -9))
+
+
+def test_sequences_in_chunks():
+    """So many tiles that an XCD takes several chunks of them, the last one smaller."""
+    announce("attention chunks")
+    rng = np.random.default_rng(8)
+    lengths = rng.integers(0, 70, 333)
+    rows = int(lengths.sum())
+    X = qkv(rng, rows, 3, 1, 16)
+    run(X, 3, 1, 16, False, offsets_of(lengths), dO=rand_qt(rng, (rows, 48), o.ROW, -12, -9))
+
+
+@pytest.mark.parametrize("causal", [False, True])
 def test_long(causal):
     """Past 1024 keys: several turns of every loop; a peaked row beside flat ones."""
     announce(f"attention long {causal}")
