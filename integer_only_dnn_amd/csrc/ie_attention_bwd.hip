@@ -25,7 +25,8 @@ namespace ie {
 __device__ __forceinline__ int bits_of(uint32_t n) { return 32 - __clz((int)n); }  // n = 0: 0
 
 // A row's products of dO with O and itself by head, and the norms of its
-// values: NL lanes a head, 16 elements each.
+// values: NL lanes a head, 16 elements each.  A stream over dO, O and V: 58 MB of
+// 25216 tokens x 12 heads of 64 in 11.5 us.
 template <int NL>
 __global__ __launch_bounds__(256) void attn_dot_kernel(AttnArgs p, AttnBwd b) {
     constexpr int PB = 256 / NL;
@@ -59,7 +60,9 @@ __global__ __launch_bounds__(256) void attn_dot_kernel(AttnArgs p, AttnBwd b) {
 
 // The scales of the queries of one key head, a token a thread (workgroups of
 // 256 tokens of a sequence, each of which finds the sequence's maxima itself),
-// and for its keys the bounds that dK and dV are scaled by.
+// and for its keys the bounds that dK and dV are scaled by.  Bound by the round
+// trips to memory of a workgroup: 9.9 us at 128 x 197 tokens x 12 heads, 7.5 at
+// 4096 x 4.
 __global__ __launch_bounds__(256) void attn_scale_kernel(AttnArgs p, AttnBwd b) {
     __shared__ int sh[4][4];
     const Item it = att_item(p, 1);
@@ -108,7 +111,12 @@ __global__ __launch_bounds__(256) void attn_scale_kernel(AttnArgs p, AttnBwd b) 
 }
 
 // dQ: a workgroup of four waves takes 64 queries of a head, 16 to a wave, one
-// to four lanes, as in the forward pass; keys and values pass through LDS.
+// to four lanes, as in the forward pass; keys and values pass through LDS.  SPLIT
+// 4: the waves take the same 16 queries and every fourth tile of keys each, and
+// add their sums up at the end.
+// Bound by vector instructions (17 to a weight), 62 % of the cycles at 128 x 197
+// tokens x 12 heads of 64 (71 us), and by the longest rows' way through their keys
+// where tiles are few (4096 tokens in 3 sequences x 16 heads, causal: 51 us, 53 %).
 template <int DP, bool ROW, bool CAUSAL, int SPLIT>
 __global__ __launch_bounds__(256, DP > 64 ? 2 : 3) void attn_dq_kernel(AttnArgs p, AttnBwd bw) {
     using T = HeadTile<DP, 256 / SPLIT>;
@@ -214,17 +222,28 @@ __global__ __launch_bounds__(256, DP > 64 ? 2 : 3) void attn_dq_kernel(AttnArgs 
 }
 
 // dK and dV: four lanes hold a key, a wave 16; queries, of every query head that
-// shares them, pass through LDS 64 at a time.  SPLIT 1: a workgroup's four waves
-// take 16 keys each and all the queries.  SPLIT 4: they take the same 16 keys
-// and every fourth tile of queries each, staged by the wave itself, and add
-// their sums up in LDS at the end (exact integers): where there are few keys,
-// four times as many workgroups, which stage four times as much.
+// shares them, pass through LDS 64 at a time.  By SPLIT:
+// 1: a workgroup's four waves take 16 keys each and all the queries and elements.
+// 4: they take the same 16 keys and every fourth tile of queries each, staged by
+//    the wave itself, and add their sums up in LDS at the end (exact integers):
+//    where there are few keys, four times as many workgroups, which stage four
+//    times as much.
+// 2: two take 16 keys and half of a tile's queries each, the digits of 32 keys and
+//    64 queries change hands in LDS, and each wave sums a quarter of the elements:
+//    half the registers for the sums (five digits to an element and key), which are
+//    160 to a lane otherwise where heads have 128 elements.
+// Bound by vector instructions (21 to a weight beside a sixth of the time in
+// matrix instructions) and, at two to three waves a SIMD, by waits for LDS:
+// 128 x 197 tokens x 12 heads of 64 53 % of the cycles issue one, 129 us.
 template <int DP, bool CAUSAL, int SPLIT>
-__global__ __launch_bounds__(256, DP > 64 ? 1 : SPLIT > 1 ? 2 : 3) void attn_dkv_kernel(AttnArgs p, AttnBwd bw) {
-    using T = HeadTile<DP, 256 / SPLIT>;
-    constexpr int KS = T::KS, NE = DP / 16, KEYS = 64 / SPLIT, NB = SPLIT == 1 ? 2 : 1;
-    __shared__ __align__(16) int8_t sq[NB * SPLIT][T::BYTES], sg[NB * SPLIT][T::BYTES];
-    __shared__ __align__(16) float sr[NB * SPLIT][5][64];
+__global__ __launch_bounds__(256, SPLIT == 2 ? 2 : DP > 64 ? 1 : SPLIT == 4 ? 2 : 3) void attn_dkv_kernel(AttnArgs p, AttnBwd bw) {
+    constexpr bool OWN = SPLIT == 4, SHARE = SPLIT == 2;  // own tiles; shared elements
+    using T = HeadTile<DP, OWN ? 64 : 256>;
+    constexpr int KS = T::KS, NE = DP / 16, KEYS = 64 / SPLIT, NB = OWN ? 4 : 2;
+    constexpr int KG = SHARE ? 2 : 1, ME = SHARE ? (NE + 3) / 4 : NE, NZ = SHARE ? 2 : 4;  // of a wave
+    __shared__ __align__(16) int8_t sq[NB][T::BYTES], sg[NB][T::BYTES];
+    __shared__ __align__(16) float sr[NB][5][64];
+    __shared__ __align__(16) int sd[SHARE ? 5 : 1][KG][16][4][4];  // digits: keys, lane group, queries
     __shared__ int smark[2][4];
     const Item it = att_item(p, 1);
     Span sp;
@@ -233,7 +252,7 @@ __global__ __launch_bounds__(256, DP > 64 ? 1 : SPLIT > 1 ? 2 : 3) void attn_dkv
     const int n = sp.n;
     if (CAUSAL) tile = (n + KEYS - 1) / KEYS - 1 - tile;  // the first keys meet the most queries
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, quad = lane >> 4;
-    const int k0 = KEYS * tile, kw = k0 + (SPLIT == 1 ? 16 * wave : 0), kj = kw + (lane & 15);
+    const int k0 = KEYS * tile, kw = k0 + (OWN ? 0 : 16 * (wave % (KEYS / 16))), kj = kw + (lane & 15);
     const bool ok = kj < n, idle = kw >= n;
     const int8_t *base = p.x + (long long)sp.a * p.width;
     const long long row = sp.a + kj;
@@ -269,38 +288,38 @@ __global__ __launch_bounds__(256, DP > 64 ? 1 : SPLIT > 1 ? 2 : 3) void attn_dkv
     const int o_top = bw.row[(long long)it.kvh * p.group * p.rows + sp.a].o_top;
     const float sv = pow2f(min(-kappa, 126)), sk = pow2f(min(6 - lambda, 126));
     const int first = CAUSAL ? k0 / 64 : 0, tiles = (n + 63) / 64 - first, total = tiles * p.group;
-    const int steps = SPLIT == 1 ? total : (total - wave + 3) / 4;
+    const int steps = OWN ? (total - wave + 3) / 4 : total, z0 = SHARE ? 2 * (wave >> 1) : 0;
     T q, g;
     q.init(p.width, p.dp);
     g.init(p.heads * p.dp, p.dp);
     AttnRow rec;
-    int fh = 0, ft = SPLIT == 1 ? 0 : wave;  // head and tile of the step that is fetched next
+    int fh = 0, ft = OWN ? wave : 0;  // head and tile of the step that is fetched next
     auto wrap = [&](int &hh, int &tt) {
         while (tt >= tiles) {
             tt -= tiles;
             ++hh;
         }
     };
-    if (SPLIT > 1) wrap(fh, ft);
-    const int me = SPLIT == 1 ? tid : lane;
+    if (OWN) wrap(fh, ft);
+    const int me = OWN ? lane : tid;
     auto fetch = [&]() {
         const int h = it.kvh * p.group + fh, t = 64 * (first + ft);
         q.fetch(base + h * p.dp, p.width, t, n, p.dp);
         g.fetch(bw.dy + ((long long)sp.a * p.heads + h) * p.dp, (long long)p.heads * p.dp, t, n, p.dp);
         if (me < 64) rec = bw.row[(long long)h * p.rows + sp.a + min(t + me, n - 1)];
-        ft += SPLIT;
+        ft += OWN ? 4 : 1;
         wrap(fh, ft);
     };
-    v4i acc[5][NE] = {};  // digits of dV (2) and dK (3), highest first
-    const v4i bias = {(int)0xc0c0c0c0u, (int)0xc0c0c0c0u, (int)0xc0c0c0c0u, (int)0xc0c0c0c0u};  // -64
+    v4i acc[KG][5][ME] = {};  // digits of dV (2) and dK (3), highest first
     auto weigh = [&](auto masked, const int8_t *lq, const int8_t *lg, const float *r, int i0, v4i (&dg)[5]) {
         // queries that see the key: i0 + 16 z + 4 quad + x in [kj, n) (causal), below n
         const int lo = kj - i0 - 4 * quad, hi = n - 1 - i0 - 4 * quad;
 #pragma unroll
-        for (int z = 0; z < 4; ++z) {
+        for (int zi = 0; zi < NZ; ++zi) {
+            const int z = z0 + zi;
             if (masked.value) {
-                dg[0][z] = dg[1][z] = dg[3][z] = dg[4][z] = 0;
-                dg[2][z] = 0x40404040;
+#pragma unroll
+                for (int y = 0; y < 5; ++y) dg[y][zi] = 0;
                 if (i0 + 16 * z >= n || (CAUSAL && i0 + 16 * z + 15 < kw)) continue;
             }
             v4i s = {0, 0, 0, 0}, dp = {0, 0, 0, 0};
@@ -329,20 +348,20 @@ __global__ __launch_bounds__(256, DP > 64 ? 1 : SPLIT > 1 ? 2 : 3) void attn_dkv
             }
             int x, y, w;
             digits4(ab[0], ab[1], ab[2], ab[3], x, y);
-            dg[0][z] = x;
-            dg[1][z] = y;
+            dg[0][zi] = x;
+            dg[1][zi] = y;
             digits3x4(cb[0], cb[1], cb[2], cb[3], x, y, w);
-            dg[2][z] = x;
-            dg[3][z] = y;
-            dg[4][z] = w;
+            dg[2][zi] = x;
+            dg[3][zi] = y;
+            dg[4][zi] = w;
         }
     };
     if (steps > 0) fetch();
-    int ct = SPLIT == 1 ? 0 : wave, ch = 0;
-    if (SPLIT > 1) wrap(ch, ct);
+    int ct = OWN ? wave : 0, ch = 0;
+    if (OWN) wrap(ch, ct);
     for (int i = 0; i < steps; ++i) {
-        const int buf = SPLIT == 1 ? i & 1 : wave;
-        if (SPLIT > 1) __builtin_amdgcn_wave_barrier();
+        const int buf = OWN ? wave : i & 1;
+        if (OWN) __builtin_amdgcn_wave_barrier();
         q.put(sq[buf]);
         g.put(sg[buf]);
         if (me < 64) {
@@ -353,46 +372,105 @@ __global__ __launch_bounds__(256, DP > 64 ? 1 : SPLIT > 1 ? 2 : 3) void attn_dkv
             sr[buf][4][me] = (float)((double)rec.a * pow2(rec.ek - whole));
         }
         const int i0 = 64 * (first + ct);
-        ct += SPLIT;
+        ct += OWN ? 4 : 1;
         wrap(ch, ct);
         if (i + 1 < steps) fetch();
-        if (SPLIT == 1) __syncthreads();
-        else __builtin_amdgcn_wave_barrier();
-        if (idle || (CAUSAL && i0 + 63 < kw)) continue;
+        if (OWN) __builtin_amdgcn_wave_barrier();
+        else __syncthreads();
+        const bool none = idle || (CAUSAL && i0 + 63 < kw);
+        if (!SHARE && none) continue;
         v4i dg[5];
-        if (i0 + 64 <= n && (!CAUSAL || kw + 15 <= i0)) weigh(Bool<false>{}, sq[buf], sg[buf], &sr[buf][0][0], i0, dg);
-        else weigh(Bool<true>{}, sq[buf], sg[buf], &sr[buf][0][0], i0, dg);
+        if (SHARE && none) {
 #pragma unroll
-        for (int e = 0; e < NE; ++e) {
-            const v4i gt = T::frag_t(sg[buf], e, lane), qt = T::frag_t(sq[buf], e, lane);
-            acc[0][e] = mfma(gt, dg[0], acc[0][e]);
-            acc[1][e] = mfma(gt, dg[1], acc[1][e]);
-            acc[2][e] = mfma(qt, bias, acc[2][e]);
-            acc[2][e] = mfma(qt, dg[2], acc[2][e]);
-            acc[3][e] = mfma(qt, dg[3], acc[3][e]);
-            acc[4][e] = mfma(qt, dg[4], acc[4][e]);
+            for (int y = 0; y < 5; ++y) dg[y] = v4i{0, 0, 0, 0};
+        } else if (i0 + 64 <= n && (!CAUSAL || kw + 15 <= i0)) {
+            weigh(Bool<false>{}, sq[buf], sg[buf], &sr[buf][0][0], i0, dg);
+        } else {
+            weigh(Bool<true>{}, sq[buf], sg[buf], &sr[buf][0][0], i0, dg);
+        }
+        if constexpr (SHARE) {
+            // the digits of 32 keys change hands: a wave sums a quarter of the elements
+#pragma unroll
+            for (int y = 0; y < 5; ++y) *(int2 *)&sd[y][wave & 1][lane & 15][quad][z0] = int2{dg[y][0], dg[y][1]};
+            __syncthreads();
+        }
+#pragma unroll
+        for (int g2 = 0; g2 < KG; ++g2) {
+            if constexpr (SHARE) {
+#pragma unroll
+                for (int y = 0; y < 5; ++y) dg[y] = *(const v4i *)sd[y][g2][lane & 15][quad];
+            }
+#pragma unroll
+            for (int e = 0; e < ME; ++e) {
+                const int at = SHARE ? wave + 4 * e : e;
+                if (SHARE && NE % 4 && at >= NE) continue;
+                const v4i gt = T::frag_t(sg[buf], at, lane), qt = T::frag_t(sq[buf], at, lane);
+                acc[g2][0][e] = mfma(gt, dg[0], acc[g2][0][e]);
+                acc[g2][1][e] = mfma(gt, dg[1], acc[g2][1][e]);
+#pragma unroll
+                for (int y = 2; y < 5; ++y) acc[g2][y][e] = mfma(qt, dg[y], acc[g2][y][e]);
+            }
         }
     }
-    if constexpr (SPLIT > 1) {
+    if constexpr (OWN) {
         static_assert(sizeof sq >= 3 * 4 * NE * 64 * sizeof(int), "a digit's sums fit the tiles");
 #pragma unroll
-        for (int a = 0; a < 5; ++a) gather_waves<4 * NE>((int *)&sq[0][0], acc[a], wave, lane);
+        for (int a = 0; a < 5; ++a) gather_waves<4 * NE>((int *)&sq[0][0], acc[0][a], wave, lane);
         if (wave) return;
     }
-    if (idle) return;
-    double y[4 * NE];
-    int16_t *out = p.v16 + row * p.cols, *need = p.p16 + row * p.parts;
+    if (!SHARE && idle) return;
+    const int head_k = p.heads + it.kvh, head_v = head_k + p.kv, e_k = lambda - 6 + whole + o_top, e_v = kappa + o_top;
+    auto value = [&](int g2, bool of_k, int e, int i) {
+        const auto &a = acc[g2];
+        return of_k ? ((double)a[2][e][i] * 65536.0 + ((double)a[3][e][i] * 256.0 + (double)a[4][e][i])) * p.scale
+                    : (double)a[0][e][i] * 256.0 + (double)a[1][e][i];
+    };
+    if constexpr (!SHARE) {
+        double y[4 * NE];
+        int16_t *out = p.v16 + row * p.cols, *need = p.p16 + row * p.parts;
 #pragma unroll
-    for (int e = 0; e < NE; ++e)
+        for (int of_v = 0; of_v < 2; ++of_v) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            y[4 * e + i] = ((double)acc[2][e][i] * 65536.0 + ((double)acc[3][e][i] * 256.0 + (double)acc[4][e][i])) * p.scale;
-    store_odd(y, lambda - 6 + whole + o_top, p.q, ok, p.d, lane, out + (p.heads + it.kvh) * p.d, need + p.heads + it.kvh);
+            for (int i = 0; i < 4 * NE; ++i) y[i] = value(0, !of_v, i >> 2, i & 3);
+            const int head = of_v ? head_v : head_k;
+            store_odd(y, of_v ? e_v : e_k, p.q, ok, p.d, lane, out + head * p.d, need + head);
+        }
+    } else {
+        // a head's need is that of four waves' elements; kappa and lambda are those of a key, in lanes of its group
+        __shared__ int sm[4][2][2][16], se[2][2][16];
+        if (lane < 16) {
+            se[0][wave & 1][lane] = e_k;
+            se[1][wave & 1][lane] = e_v;
+        }
+        auto values = [&](int g2, int of_v, double (&y)[4 * ME]) {
 #pragma unroll
-    for (int e = 0; e < NE; ++e)
+            for (int i = 0; i < 4 * ME; ++i) y[i] = value(g2, !of_v, i >> 2, i & 3);  // zeros past the head
+        };
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[4 * e + i] = (double)acc[0][e][i] * 256.0 + (double)acc[1][e][i];
-    store_odd(y, kappa + o_top, p.q, ok, p.d, lane, out + (p.heads + p.kv + it.kvh) * p.d, need + p.heads + p.kv + it.kvh);
+        for (int x = 0; x < 4; ++x) {
+            double y[4 * ME];
+            values(x >> 1, x & 1, y);
+            const int w = max_word(y);
+            if (lane < 16) sm[wave][x >> 1][x & 1][lane] = w;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int g2 = x >> 1, of_v = x & 1, c = lane & 15, key = k0 + 16 * g2 + c, head = of_v ? head_v : head_k;
+            double y[4 * ME];
+            values(g2, of_v, y);
+            const int w = max(max(sm[0][g2][of_v][c], sm[1][g2][of_v][c]), max(sm[2][g2][of_v][c], sm[3][g2][of_v][c]));
+            const int need = need_word(w, p.q);
+            const double inv = odd_scale(need);
+            if (key < n && tid < 16)
+                p.p16[(sp.a + key) * (long long)p.parts + head] = (int16_t)(need == NEED_NONE ? P_NONE : need + se[of_v][g2][c]);
+#pragma unroll
+            for (int e = 0; e < ME; ++e) {
+                const int at = 16 * (wave + 4 * e) + 4 * quad;
+                if (at < DP) write_odd(y + 4 * e, inv, key < n, at, p.d, p.v16 + (sp.a + key) * (long long)p.cols + head * p.d);
+            }
+        }
+    }
 }
 
 template <int DP, int SPLIT>
@@ -408,23 +486,33 @@ static void dq(AttnArgs a, const AttnBwd &b, hipStream_t st) {
     }
 }
 
+// Tiles split where they are fewer than two a CU (us, tokens x heads of 64, causal,
+// split and whole): 1024 x 8 12 and 21; 2048 x 16 (528 tiles) 39 and 45, all keys
+// seen 60 and 46; 4096 x 16 in 3 sequences 66 and 51.
 template <int DP>
 static void dq(const AttnArgs &a, const AttnBwd &b, hipStream_t st) {
     if (att_slots(a.rows, a.n_seq, 64) * a.heads < 2 * NCU) dq<DP, 4>(a, b, st);
     else dq<DP, 1>(a, b, st);
 }
 
+template <int DP, int SPLIT>
+static void dkv(AttnArgs a, const AttnBwd &b, hipStream_t st) {
+    a.chunk = att_chunk(a, 64 / SPLIT, !a.causal);
+    const dim3 grid(att_grid(att_slots(a.rows, a.n_seq, 64 / SPLIT), a.kv, 1)), block(256);
+    if (a.causal) hipLaunchKernelGGL((attn_dkv_kernel<DP, true, SPLIT>), grid, block, 0, st, a, b);
+    else hipLaunchKernelGGL((attn_dkv_kernel<DP, false, SPLIT>), grid, block, 0, st, a, b);
+}
+
+// SPLIT 4 where there are few tiles (us, tokens x key heads, causal).  Heads of
+// 64: 4096 x 4, group of 4, 82 and with SPLIT 1 277; 25216 x 12 (128 sequences,
+// not causal) 315 and 129.  Heads of 128: 2048 x 2 98 and with SPLIT 2 195; 1024 x
+// 8 38 and 32; 4096 x 8, group of 4, 823 and 628 (SPLIT 1, at 440 registers one
+// wave a SIMD, 714).
 template <int DP>
-static void dkv(AttnArgs a, const AttnBwd &b, int split, hipStream_t st) {
-    a.chunk = att_chunk(a, 64 / split, !a.causal);
-    const dim3 grid(att_grid(att_slots(a.rows, a.n_seq, 64 / split), a.kv, 1)), block(256);
-    if (split == 1) {
-        if (a.causal) hipLaunchKernelGGL((attn_dkv_kernel<DP, true, 1>), grid, block, 0, st, a, b);
-        else hipLaunchKernelGGL((attn_dkv_kernel<DP, false, 1>), grid, block, 0, st, a, b);
-    } else {
-        if (a.causal) hipLaunchKernelGGL((attn_dkv_kernel<DP, true, 4>), grid, block, 0, st, a, b);
-        else hipLaunchKernelGGL((attn_dkv_kernel<DP, false, 4>), grid, block, 0, st, a, b);
-    }
+static void dkv(const AttnArgs &a, const AttnBwd &b, hipStream_t st) {
+    const bool few = DP > 64 ? att_slots(a.rows, a.n_seq, 32) * a.kv < NCU : att_slots(a.rows, a.n_seq, 64) * a.kv < 4 * NCU;
+    if (few) dkv<DP, 4>(a, b, st);
+    else dkv<DP, (DP > 64 ? 2 : 1)>(a, b, st);
 }
 
 hipError_t launch_attention_bwd(const AttnArgs &a, const AttnBwd &b, hipStream_t st) {
@@ -446,12 +534,11 @@ hipError_t launch_attention_bwd(const AttnArgs &a, const AttnBwd &b, hipStream_t
     else if (a.d <= 96) dq<96>(a, b, st);
     else dq<128>(a, b, st);
     prof_end(st, PROF_ATT_DQ);
-    const int split = att_slots(a.rows, a.n_seq, 64) * a.kv < 4 * NCU ? 4 : 1;
     prof_begin(st, PROF_ATT_DKV);
-    if (a.d <= 32) dkv<32>(a, b, split, st);
-    else if (a.d <= 64) dkv<64>(a, b, split, st);
-    else if (a.d <= 96) dkv<96>(a, b, split, st);
-    else dkv<128>(a, b, split, st);
+    if (a.d <= 32) dkv<32>(a, b, st);
+    else if (a.d <= 64) dkv<64>(a, b, st);
+    else if (a.d <= 96) dkv<96>(a, b, st);
+    else dkv<128>(a, b, st);
     prof_end(st, PROF_ATT_DKV);
     const hipError_t e = hipGetLastError();
     return e != hipSuccess ? e : launch_attention_round(a, st);

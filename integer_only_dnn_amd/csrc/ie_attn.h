@@ -74,14 +74,14 @@ __device__ __forceinline__ void digits4(int a, int b, int c, int d, int &hi, int
     hi = (int)__builtin_amdgcn_perm(t, s, 0x07060302u);
 }
 
-// Three digits of four n + 0x8080 + 2^22 in the low 23 bits, |n| < 2^21: high
-// ones 64 too large, middle and low ones.
+// Three digits of four n + 0x8080 + 2^22 in the low 23 bits, |n| < 2^21.
 __device__ __forceinline__ void digits3x4(int a, int b, int c, int d, int &hi, int &mid, int &lo) {
     digits4(a, b, c, d, mid, lo);
     mid ^= (int)0x80808080u;
     const uint32_t s = __builtin_amdgcn_perm((uint32_t)b, (uint32_t)a, 0x0c0c0602u);
     const uint32_t t = __builtin_amdgcn_perm((uint32_t)d, (uint32_t)c, 0x0c0c0602u);
-    hi = (int)__builtin_amdgcn_perm(t, s, 0x05040100u);
+    // bytes 64 + h, h from -32 to 32: no byte borrows from the next
+    hi = (int)(((__builtin_amdgcn_perm(t, s, 0x05040100u) | 0x80808080u) - 0x40404040u) ^ 0x80808080u);
 }
 
 __device__ __forceinline__ v4i mfma(v4i a, v4i b, v4i c) { return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0); }
@@ -248,7 +248,8 @@ __device__ __forceinline__ v4i head16(const int8_t *head, int c, int d) {
 // lie 16 bytes more than a multiple of 64 apart, and every 16 rows another 128
 // bytes: the 16 rows of a frag_r, and the rows 4 c .. 4 c + 3 and 16 + 4 c .. of
 // two lane groups of a frag_t, then fall on banks of their own (without the 128
-// bytes a third of the cycles of LDS were conflicts).
+// bytes 41 % of the cycles of LDS were conflicts, with them 30 %; the time is the
+// same).
 //
 // Loads go through a buffer descriptor over the tile's rows, whose bounds are
 // checked in hardware: a thread's chunks keep their offsets from tile to tile
@@ -329,37 +330,42 @@ __device__ __forceinline__ void gather_waves(int *x, v4i (&acc)[N / 4], int wave
         for (int i = 0; i < N; ++i) acc[i >> 2][i & 3] += x[i * 64 + lane] + x[(N + i) * 64 + lane] + x[(2 * N + i) * 64 + lane];
 }
 
-// A result row of one head, one column of the transposed product: value y[4 e +
-// r] of lane l is element 16 e + 4 (l / 16) + r of row l % 16; the other three
-// quarters of the row lie 16, 32 and 48 lanes away.  Rounded to odd at two bits
-// below what the head alone needs, for a rounding by whole rows.
+// Results of one head, columns of a transposed product: value y[4 g + r] of lane
+// l is element 16 e_g + 4 (l / 16) + r of row l % 16; the other three quarters of
+// these elements lie 16, 32 and 48 lanes away.  They are rounded to odd at two
+// bits below what the head alone needs, for a rounding by whole rows.
 template <int NV>
-__device__ __forceinline__ void store_odd(const double (&y)[NV], int e, int q, bool ok, int d, int lane, int16_t *out,
-                                          int16_t *need_out) {
+__device__ __forceinline__ int max_word(const double (&y)[NV]) {
     MaxMag mx;
 #pragma unroll
     for (int i = 0; i < NV; i += 2) mx.add(y[i], y[i + 1]);
-    const int need = need_word(col_reduce(mx.word(), Max{}), q);
-    const double inv = need == NEED_NONE ? 0.0 : pow2(2 - need);
+    return col_reduce(mx.word(), Max{});
+}
+__device__ __forceinline__ void write_odd(const double *y, double inv, bool ok, int c, int d, int16_t *out) {
+    int v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const double t = y[k] * inv, f = floor(t);
+        v[k] = (int)f | (f != t ? 1 : 0);
+    }
+    if (!ok) return;
+    if (d % 4 == 0) {
+        if (c < d) *(int2 *)(out + c) = int2{(v[0] & 0xffff) | v[1] << 16, (v[2] & 0xffff) | v[3] << 16};
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (c + k < d) out[c + k] = (int16_t)v[k];
+    }
+}
+__device__ __forceinline__ double odd_scale(int need) { return need == NEED_NONE ? 0.0 : pow2(2 - need); }
+template <int NV>
+__device__ __forceinline__ void store_odd(const double (&y)[NV], int e, int q, bool ok, int d, int lane, int16_t *out,
+                                          int16_t *need_out) {
+    const int need = need_word(max_word(y), q);
+    const double inv = odd_scale(need);
     if (ok && lane < 16) *need_out = (int16_t)(need == NEED_NONE ? P_NONE : need + e);
 #pragma unroll
-    for (int g = 0; g < NV / 4; ++g) {
-        const int c = 16 * g + 4 * (lane >> 4);
-        int v[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const double t = y[4 * g + k] * inv, f = floor(t);
-            v[k] = (int)f | (f != t ? 1 : 0);
-        }
-        if (!ok) continue;
-        if (d % 4 == 0) {
-            if (c < d) *(int2 *)(out + c) = int2{(v[0] & 0xffff) | v[1] << 16, (v[2] & 0xffff) | v[3] << 16};
-        } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (c + k < d) out[c + k] = (int16_t)v[k];
-        }
-    }
+    for (int g = 0; g < NV / 4; ++g) write_odd(y + 4 * g, inv, ok, 16 * g + 4 * (lane >> 4), d, out);
 }
 
 }  // namespace ie

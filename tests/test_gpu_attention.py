@@ -126,7 +126,8 @@ def test_many_short_sequences():
 @pytest.mark.parametrize("causal", [False, True])
 @pytest.mark.parametrize("heads,kv,d,lengths", [(128, 64, 16, [300]), (256, 256, 4, [300]), (130, 2, 128, [290]),
                                                 (8, 8, 64, [280] + 200 * [1]), (8, 8, 128, [1, 259] + 220 * [1]),
-                                                (8, 8, 96, 200 * [2] + [257]), (9, 9, 32, 130 * [0, 3] + [333])],
+                                                (8, 8, 96, 200 * [2] + [257]), (9, 9, 32, 130 * [0, 3] + [333]),
+                                                (40, 40, 70, [150, 70]), (80, 40, 101, [121, 0, 100])],
                          ids=lambda v: "+".join(map(str, v[:2])) + f"_{len(v)}" if isinstance(v, list) else str(v))
 def test_full_grids(heads, kv, d, lengths, causal):
     """Tiles enough that no launch splits a tile's keys or queries over its waves."""
