@@ -143,6 +143,19 @@ def test_pages_and_lengths_outside():
     assert_same(O, o.attention_cache(Q, host, slots, 4, 2, 32, 0.25), "cut")
 
 
+def test_no_pages():
+    """A table without columns: every sequence is empty, and a length above zero is told."""
+    announce("cache attention without pages")
+    rng = np.random.default_rng(6)
+    _, cache = new_cache(rng, 2, 16, 2, 32)
+    Q, ws, att = qkv(rng, 3, 4, 2, 32), ie.Workspace("cuda"), ie.Attention(4, 2, 32, 0.25)
+    for lengths, flag in (([0, 0, 0], 0), ([0, 1, 0], ie.FLAG_INDEX)):
+        O = filled(3, 128)
+        ie.ie_attention_cache(att, qt_to_dev(Q), cache, torch.zeros((3, 0), dtype=torch.int32, device="cuda"), dev_i32(lengths), O, ws)
+        assert ws.status() == flag
+        assert not O.mant.any() and bool((O.exp == -128).all())
+
+
 def test_shared_pages():
     """Two sequences over the same pages, and one page twice in a sequence."""
     announce("cache attention shared pages")
