@@ -29,9 +29,11 @@
  *     NHWC, viewed as a matrix [N*H*W x C]; weights are [K x R*S*C] (KRSC);
  *   - outputs are fully overwritten, mantissas and exponents; outputs must not
  *     alias inputs (ie_sgd_update works in place on W and V).  Layer norm,
- *     the product with bias and residual, the bias gradient and dropout
- *     refuse an output with a byte of an input or of another output
- *     (IE_ERR_UNSUPPORTED);
+ *     the product with bias and residual, the bias gradient, dropout,
+ *     attention, rotary positions and the cache refuse an output with a byte
+ *     of an input or of another output (IE_ERR_UNSUPPORTED).  Two exceptions
+ *     to the overwriting: rows of a packed batch that belong to no sequence,
+ *     and slots of a cache that no row names, are left as they were;
  *   - `ws` is a workspace of at least the size the matching *_workspace_bytes
  *     call returns; its first 256 bytes hold sticky flags and must be zeroed
  *     once (ie_workspace_init) before first use;
@@ -444,7 +446,8 @@ ie_status ie_dropout(const ie_mat *X, const ie_mat *R, const ie_mat *Y, const ie
  * stats: for the backward pass, 8 bytes for every row and head (a device array
  * [rows x heads], 8-byte aligned): m and L; NULL where none follows.
  * Limits (IE_ERR_UNSUPPORTED): head_dim <= 128, (heads + 2 kv_heads) * head_dim
- * <= 2^24, 2^-30 <= scale <= 2^30.
+ * <= 2^24, 2^-30 <= scale <= 2^30, (rows / 32 + n_seq + 9) * heads < 2^24, rows <
+ * 2^26 - 4, without offsets at most 131071 rows.
  * Offsets that decrease or leave the matrix, and sequences of more than 131071
  * tokens, set IE_FLAG_INDEX: the rows they name are undefined, no others.
  */
@@ -484,7 +487,8 @@ ie_status ie_attention_fwd(const ie_attention_desc *d, const ie_mat *QKV, const 
  *   heads) that see j, a_i < 2^(alpha_i) (the smallest), l_i = alpha_i + e_i +
  *   max([dO_i] + max nu_j, delta_i) + 1, G = max l_i.
  * Limits as for the forward pass; a sequence's tokens times heads / kv_heads at
- * most 131071 (else IE_FLAG_INDEX, as there).
+ * most 131071 (else IE_FLAG_INDEX, or, without offsets, IE_ERR_UNSUPPORTED, as
+ * there).
  */
 size_t ie_attention_bwd_workspace(const ie_attention_desc *d, int64_t rows);
 ie_status ie_attention_bwd(const ie_attention_desc *d, const ie_mat *QKV, const ie_mat *O, const ie_mat *dO, const void *stats,
@@ -577,7 +581,7 @@ ie_status ie_cache_store(const ie_cache *c, int32_t heads, const ie_mat *QKV, co
  * A sequence without keys gives zeros.  A length outside 0 .. per * page sets
  * IE_FLAG_INDEX and is cut; a page outside the cache sets it and its keys are
  * left out.  O [n x heads * head_dim] must be ROW, else IE_ERR_UNSUPPORTED.
- * per * page <= 2^23, else IE_ERR_UNSUPPORTED.
+ * per * page <= 2^23 and n * heads < 2^24, else IE_ERR_UNSUPPORTED.
  */
 size_t ie_attention_cache_workspace(const ie_attention_desc *d, int64_t n, int64_t tokens); /* tokens: per * page */
 ie_status ie_attention_cache(const ie_attention_desc *d, const ie_mat *Q, const ie_cache *c, const int32_t *pages, int32_t per,
@@ -605,8 +609,13 @@ ie_status ie_device_status(void *ws, void *stream, uint32_t *flags, int clear);
  * a convolution's backward pass, 3500 / 3510 ReLU forward / backward, 3520 /
  * 3521 / 3530 the Sum's maximum, rounding and row-grouped passes, 3600 / 3610
  * layer norm forward / backward, 3620 / 3630 column sums and their finish,
- * 3700 dropout, 3800 / 3810 products with bias and residual and their split finalize) and returns how
- * many were recorded since the last read; the records are then cleared.
+ * 3700 dropout, 3800 / 3810 products with bias and residual and their split
+ * finalize, 3900 rotary positions and their table, 4000 / 4005 / 4010 attention
+ * forward, its copy of unaligned heads and its rounding by rows (of the gradient
+ * and of attention over a cache too), 4020 / 4030 / 4040 the gradient's bounds,
+ * dQ, dK and dV, 4100 / 4110 / 4120 the cache's store, attention over its blocks
+ * and their joining) and returns how many were recorded since the last read; the
+ * records are then cleared.
  * The timing records (and their events) are the library's only process-wide
  * state; they are not thread-safe.
  */

@@ -1283,7 +1283,7 @@ ie_status ie_attention_fwd(const ie_attention_desc *d, const ie_mat *QKV, const 
     IE_CHECK(check_attention(d, QKV, att_cols(d)));
     IE_CHECK(check_mat(O));
     if (O->rows != QKV->rows || O->cols != (long long)d->heads * d->head_dim) return IE_ERR_SHAPE;
-    if (O->group != IE_GROUP_ROW || !aligned(stats, 8)) return IE_ERR_UNSUPPORTED;
+    if (O->group != IE_GROUP_ROW || !aligned(stats, 8) || (!d->offsets && QKV->rows > ATT_MOST)) return IE_ERR_UNSUPPORTED;
     const size_t stat_bytes = stats ? (size_t)O->rows * d->heads * 8 : 0, off_bytes = ((size_t)d->n_seq + 1) * 4;
     if (share(O, QKV) || share_bytes(O, d->offsets, off_bytes) || share_bytes(O, stats, stat_bytes) ||
         share_bytes(QKV, stats, stat_bytes))
@@ -1323,7 +1323,8 @@ ie_status ie_attention_bwd(const ie_attention_desc *d, const ie_mat *QKV, const 
     if (O->rows != QKV->rows || O->cols != (long long)d->heads * d->head_dim || !same_shape(O, dO) || !same_shape(QKV, dQKV))
         return IE_ERR_SHAPE;
     if (QKV->rows > 0 && !stats) return IE_ERR_NULL;
-    if (O->group != IE_GROUP_ROW || dQKV->group != IE_GROUP_ROW || !aligned(stats, 8) || d->heads / d->kv_heads > ATT_MOST)
+    if (O->group != IE_GROUP_ROW || dQKV->group != IE_GROUP_ROW || !aligned(stats, 8) || d->heads / d->kv_heads > ATT_MOST ||
+        (!d->offsets && QKV->rows > ATT_MOST / (d->heads / d->kv_heads)))
         return IE_ERR_UNSUPPORTED;
     if (share(dQKV, QKV) || share(dQKV, O) || share(dQKV, dO) || share_bytes(dQKV, stats, (size_t)O->rows * d->heads * 8) ||
         share_bytes(dQKV, d->offsets, ((size_t)d->n_seq + 1) * 4))
@@ -1493,7 +1494,7 @@ ie_status ie_attention_cache(const ie_attention_desc *d, const ie_mat *Q, const 
     if (Q->rows > 0 && (!lengths || (per > 0 && !pages))) return IE_ERR_NULL;
     const long long tokens = (long long)per * c->page, units = d->kv_heads * ((d->heads / d->kv_heads + 15ll) / 16);
     if (O->group != IE_GROUP_ROW || !aligned(lengths, 4) || !aligned(pages, 4) || tokens > CACHE_TOKENS_MAX ||
-        Q->rows * ((tokens + CACHE_BLOCK - 1) / CACHE_BLOCK + 8) * units > ATT_ITEMS_MAX || Q->rows * d->heads > ATT_ITEMS_MAX)
+        Q->rows * ((tokens + CACHE_BLOCK - 1) / CACHE_BLOCK + 8) * units > ATT_ITEMS_MAX || Q->rows * d->heads > ATT_BLOCKS_MAX)
         return IE_ERR_UNSUPPORTED;
     if (share(O, Q) || share_cache(O, c) || share_bytes(O, lengths, (size_t)Q->rows * 4) ||
         share_bytes(O, pages, (size_t)Q->rows * per * 4))

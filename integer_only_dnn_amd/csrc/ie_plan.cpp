@@ -936,7 +936,9 @@ ie_status check_attention(const ie_attention_desc *d, const ie_mat *X, long long
     if (((long long)d->heads + 2ll * d->kv_heads) * r16(d->head_dim) > ATT_COLS_MAX) return IE_ERR_UNSUPPORTED;
     // 2^-30 .. 2^30: r = scale log2(e) 2^e keeps clear of fp32's ends (a NaN is refused too)
     if (!(d->scale >= 0x1p-30f && d->scale <= 0x1p30f)) return IE_ERR_UNSUPPORTED;
-    if (att_slots(X->rows, d->n_seq, 16) * d->heads > ATT_ITEMS_MAX) return IE_ERR_UNSUPPORTED;
+    // tiles of 32 rows and up (those of 16 are few, see ie_attention_bwd.hip), 4 rows a workgroup in the rounding
+    if ((att_slots(X->rows, d->n_seq, 32) + 8) * d->heads > ATT_BLOCKS_MAX || X->rows > 4 * ATT_BLOCKS_MAX)
+        return IE_ERR_UNSUPPORTED;
     return IE_OK;
 }
 

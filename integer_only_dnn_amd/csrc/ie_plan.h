@@ -441,7 +441,8 @@ int *carve_dropout(Carve &c, long long rows, long long cols);  // block maxima
 constexpr int ATT_MOST = 131071;
 constexpr int ATT_HEAD_MAX = 128;
 constexpr long long ATT_COLS_MAX = 1ll << 24;  // columns of QKV
-constexpr long long ATT_ITEMS_MAX = 1ll << 30;  // workgroups of a launch
+constexpr long long ATT_BLOCKS_MAX = (1ll << 24) - 1;  // workgroups of 256 in a launch: 2^32 threads are too many
+constexpr long long ATT_ITEMS_MAX = 1ll << 30;  // blocks of a cache's keys, times heads
 inline long long att_slots(long long rows, long long n_seq, int bm) { return rows / bm + (n_seq > 0 ? n_seq : 1); }
 struct AttFwdWs {
     int16_t *v16, *p16;  // round-to-odd results and the needs of their heads

@@ -64,10 +64,14 @@ def test_attention_forward():
     assert fwd(att(n_seq=1, offsets=(1 << 24) + 1276)) == UNSUPPORTED
     assert fwd(stats=(1 << 24) + 1272) == UNSUPPORTED and fwd(stats=(1 << 20) + 2552) == UNSUPPORTED
     assert fwd(stats=(1 << 20) + 2560) == WORKSPACE and fwd(O=mat(10, 128, (1 << 20) + 2560)) == WORKSPACE
-    # more workgroups than a launch takes
-    assert fwd(X=mat((1 << 31) - 1, 256), O=mat((1 << 31) - 1, 128, 1 << 50)) == WORKSPACE
-    many = att(heads=128, kv=128, d=1)
-    assert fwd(many, mat((1 << 31) - 1, 384), mat((1 << 31) - 1, 128, 1 << 50)) == UNSUPPORTED
+    # more workgroups than a launch takes, and a single sequence that is too long
+    at = dict(n_seq=4, offsets=1 << 45)
+    for heads, rows, want in ((4, (1 << 26) - 4, WORKSPACE), (4, (1 << 26) - 3, UNSUPPORTED), (128, (1 << 22) - 448, WORKSPACE),
+                              (128, 1 << 22, UNSUPPORTED)):
+        assert fwd(att(heads, heads, 1, **at), mat(rows, 3 * heads), mat(rows, heads, 1 << 50)) == want, (heads, rows)
+    assert fwd(att(n_seq=(1 << 22) - 10, offsets=1 << 45)) == WORKSPACE and fwd(att(n_seq=1 << 22, offsets=1 << 45)) == UNSUPPORTED
+    assert fwd(X=mat(131071, 256), O=mat(131071, 128, 1 << 50)) == WORKSPACE
+    assert fwd(X=mat(131072, 256), O=mat(131072, 128, 1 << 50)) == UNSUPPORTED
     # nothing to do
     assert fwd(X=mat(0, 256), O=mat(0, 128, 1 << 24), ws=1) == OK
 
@@ -84,6 +88,8 @@ def test_attention_backward():
         assert bwd(G=mat(10, 256, m)) == UNSUPPORTED, m
     assert bwd(G=mat(10, 256, (1 << 35) + 320)) == WORKSPACE
     assert bwd(att(n_seq=1, offsets=1 << 28)) == UNSUPPORTED
+    for rows, want in ((65535, WORKSPACE), (65536, UNSUPPORTED)):  # two query heads to a key head
+        assert bwd(None, mat(rows, 256), mat(rows, 128, 1 << 50), mat(rows, 128, 1 << 52), mat(rows, 256, 1 << 54), 1 << 56) == want
     wide = att(heads=1 << 18, kv=1, d=1)
     assert bwd(wide, mat(1, (1 << 18) + 2), mat(1, 1 << 18, 1 << 30), mat(1, 1 << 18, 1 << 33), mat(1, (1 << 18) + 2, 1 << 34)) == \
         UNSUPPORTED
@@ -169,6 +175,8 @@ def test_cache_attention():
         assert call(O=mat(10, 128, o)) == UNSUPPORTED, o
     assert call(O=mat(10, 128, (1 << 37) + 40)) == WORKSPACE
     assert call(Q=mat(0, 256), O=mat(0, 128, 1 << 24), ws=1, pages=None, lengths=None) == OK
+    for n, want in (((1 << 22) - 1, WORKSPACE), (1 << 22, UNSUPPORTED)):
+        assert call(Q=mat(n, 128), O=mat(n, 128, 1 << 44), per=0, pages=None, lengths=1 << 50) == want
     big = mat(1 << 20, 256)
     assert call(Q=big, O=mat(1 << 20, 128, 1 << 44), per=1 << 19) == UNSUPPORTED
 
