@@ -71,6 +71,7 @@ __global__ __launch_bounds__(256) void attn_scale_kernel(AttnArgs p, AttnBwd b) 
     if (!rank_tile<false>(p, it.rank, 256, sp, tile)) return;
     const int tid = threadIdx.x;
     int e_top = ATT_E_LO, n_top = -4096, r_top = -4096, o_top = E_MIN;
+#pragma unroll 4
     for (int t = tid; t < sp.n; t += 256) {
         const long long row = sp.a + t;
         const int e = clip_e(p.xe[p.x_row ? row : 0]), nu = b.norm[row * p.kv + it.kvh] + e;
@@ -263,6 +264,7 @@ __global__ __launch_bounds__(256, SPLIT == 2 ? 2 : DP > 64 ? 1 : SPLIT == 4 ? 2 
     // the largest bounds of all queries (none: -4096 each), and of those that see a key
     const AttnKey *marks = bw.key + (long long)it.kvh * p.rows + sp.a;
     AttnKey all = ATT_NO_KEY, seen, seen_later = ATT_NO_KEY;
+#pragma unroll 4
     for (int t = tid; t < n; t += 256) {
         const AttnKey x = marks[t];
         all = __builtin_elementwise_max(all, x);
