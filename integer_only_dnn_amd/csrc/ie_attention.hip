@@ -157,24 +157,17 @@ __global__ __launch_bounds__(256, SPLIT > 1 ? 2 : DP > 64 ? 3 : 4) void attn_fwd
             auto score = [&](auto masked, int t) {
                 constexpr bool each = CAUSAL && decltype(masked)::value;
                 if (ROW && !each) em = fmaxf(em, most_lds[t]);
-                v4i acc[4];
-                float4 f[4];
-#pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    acc[z] = v4i{0, 0, 0, 0};
-                    f[z] = float4{1, 1, 1, 1};
-                    if (masked.value && 64 * t + 16 * z >= last) continue;
-#pragma unroll
-                    for (int i = 0; i < KS; ++i) acc[z] = mfma(T::frag_r(tiles_lds[t], z, i, lane), q[i], acc[z]);
-                    if (ROW) f[z] = *(const float4 *)&factors_lds[64 * t + 16 * z + 4 * quad];
-                }
 #pragma unroll
                 for (int z = 0; z < 4; ++z) {
                     if (masked.value && 64 * t + 16 * z >= last) continue;
-                    const float fs[4] = {f[z].x, f[z].y, f[z].z, f[z].w};
+                    v4i acc = {0, 0, 0, 0};
+#pragma unroll
+                    for (int i = 0; i < KS; ++i) acc = mfma(T::frag_r(tiles_lds[t], z, i, lane), q[i], acc);
+                    const float4 f = ROW ? *(const float4 *)&factors_lds[64 * t + 16 * z + 4 * quad] : float4{1, 1, 1, 1};
+                    const float fs[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float x = (float)acc[z][i] * fs[i];
+                        const float x = (float)acc[i] * fs[i];
                         const bool on = !masked.value || 64 * t + 16 * z + i <= lim;
                         s[4 * t + z][i] = x;
                         m = fmaxf(m, on ? x : -__builtin_inff());

@@ -235,7 +235,7 @@ __global__ __launch_bounds__(256, DP > 64 ? 2 : 3) void attn_dq_kernel(AttnArgs 
 //    160 to a lane otherwise where heads have 128 elements.
 // Bound by vector instructions (21 to a weight beside a sixth of the time in
 // matrix instructions) and, at two to three waves a SIMD, by waits for LDS:
-// 128 x 197 tokens x 12 heads of 64 53 % of the cycles issue one, 129 us.
+// 128 x 197 tokens x 12 heads of 64 54 % of the cycles issue one, 123 us.
 template <int DP, bool CAUSAL, int SPLIT>
 __global__ __launch_bounds__(256, SPLIT == 2 ? 2 : DP > 64 ? 1 : SPLIT == 4 ? 2 : 3) void attn_dkv_kernel(AttnArgs p, AttnBwd bw) {
     constexpr bool OWN = SPLIT == 4, SHARE = SPLIT == 2;  // own tiles; shared elements
