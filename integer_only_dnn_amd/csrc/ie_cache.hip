@@ -69,12 +69,12 @@ __global__ __launch_bounds__(256) void cache_store_kernel(CacheArgs p, long long
 // come, two elements to a byte: a transposing read of 16 columns of bytes is
 // unpacked into two operands, the even elements and the odd ones.  Mantissas
 // are unpacked as 16 times their value (their four bits in a byte's upper half),
-// which the exact sums drop.  The next block's keys, values and exponents are in
-// flight while one is computed.
+// which the exact sums drop.  The next block's keys, values and exponents and the
+// slots of the one behind it are in flight while one is computed.
 //
 // Bound by the stream over the cache, less what two barriers a block keep it from:
-// 48 sequences of up to 8000 tokens, 32 heads on 8 of 128 (196 MB) 49 us, 4.0 TB/s;
-// one of 131072 (136 MB) 34 us.  SUB 1 for these four heads: 51.5 and 36 us.
+// 48 sequences of up to 8000 tokens, 32 heads on 8 of 128 (196 MB) 47 us, 4.2 TB/s;
+// one of 131072 (136 MB) 32 us.  SUB 1 for these four heads takes 5 % longer.
 template <int SUB>
 __device__ __forceinline__ float heads_max(float v) {
     v = col_max(v);
@@ -113,6 +113,14 @@ __global__ __launch_bounds__(256, 4) void cache_attention_kernel(CacheArgs p, At
         int q, unit;  // blocks 8 q .., key head and its query heads
         int seq, b, kvh, g0, len;
     };
+    auto advance = [&](Work &w) {
+        w.q += by_q;
+        w.unit += by_u;
+        if (w.unit >= units) {
+            w.unit -= units;
+            ++w.q;
+        }
+    };
     auto locate = [&](Work &w) {  // the first item from (q, unit) on that there is
         while (8 * w.q < blocks) {
             const int blk = 8 * w.q + r8;
@@ -127,12 +135,7 @@ __global__ __launch_bounds__(256, 4) void cache_attention_kernel(CacheArgs p, At
                 w.len = __builtin_amdgcn_readfirstlane(slen[i]);
                 return true;
             }
-            w.q += by_q;
-            w.unit += by_u;
-            if (w.unit >= units) {
-                w.unit -= units;
-                ++w.q;
-            }
+            advance(w);
         }
         return false;
     };
@@ -146,7 +149,19 @@ __global__ __launch_bounds__(256, 4) void cache_attention_kernel(CacheArgs p, At
     // wave's keys col, 16 + col, ..; thread t the exponents of key t
     uint32_t kw[4][2 * NS], vw[4][2 * NS];
     float fk = 0.0f, fv = 0.0f;
-    auto fetch = [&](const Work &w, int mine) {
+    auto take = [&](const Work &w, int mine, const auto *from, uint32_t (&to)[4][2 * NS]) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int slot = __shfl(mine, 16 * t + col, 64);
+            const long long at = ((long long)slot * p.kv + w.kvh) * hb + 8 * NS * c;
+#pragma unroll
+            for (int i = 0; i < 2 * NS; ++i) to[t][i] = 0;
+            if (slot < 0) continue;
+            if (8 * NS * (c + 1) <= hb) __builtin_memcpy(to[t], from + at, 8 * NS);
+            else if (8 * NS * c < hb) __builtin_memcpy(to[t], from + at, 8);
+        }
+    };
+    auto fetch_keys = [&](const Work &w, int mine) {
         fk = fv = 0.0f;
         if (mine >= 0) {
             const long long at = (long long)mine * p.kv + w.kvh;
@@ -154,21 +169,7 @@ __global__ __launch_bounds__(256, 4) void cache_attention_kernel(CacheArgs p, At
             fv = pow2f(clip_e(p.ve[at]));
         }
         if (mine == -2) atomicOr(p.flags, IE_FLAG_INDEX);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const int slot = __shfl(mine, 16 * t + col, 64);
-            const long long at = ((long long)slot * p.kv + w.kvh) * hb + 8 * NS * c;
-#pragma unroll
-            for (int i = 0; i < 2 * NS; ++i) kw[t][i] = vw[t][i] = 0;
-            if (slot < 0) continue;
-            if (8 * NS * (c + 1) <= hb) {
-                __builtin_memcpy(kw[t], p.k + at, 8 * NS);
-                __builtin_memcpy(vw[t], p.v + at, 8 * NS);
-            } else if (8 * NS * c < hb) {
-                __builtin_memcpy(kw[t], p.k + at, 8);
-                __builtin_memcpy(vw[t], p.v + at, 8);
-            }
-        }
+        take(w, mine, p.k, kw);
     };
 
     for (s0 = 0; s0 < p.n; s0 += 256) {
@@ -193,8 +194,20 @@ __global__ __launch_bounds__(256, 4) void cache_attention_kernel(CacheArgs p, At
         Work w;
         w.q = (int)first / units;
         w.unit = (int)first - w.q * units;
+        // the item in hand (w) has its data on the way, the next one (ahead) its slots
         bool more = locate(w);
-        if (more) fetch(w, slot_of(w));
+        if (more) {
+            const int slot = slot_of(w);
+            fetch_keys(w, slot);
+            take(w, slot, p.v, vw);
+        }
+        Work ahead = w;
+        auto look = [&]() {
+            advance(ahead);
+            return locate(ahead);
+        };
+        bool more_ahead = more && look();
+        int slot = more_ahead ? slot_of(ahead) : -1;
         while (more) {
             const Work now = w;
             sfk[tid] = fk;
@@ -219,15 +232,6 @@ __global__ __launch_bounds__(256, 4) void cache_attention_kernel(CacheArgs p, At
                     }
                 }
             }
-            w.q += by_q;
-            w.unit += by_u;
-            if (w.unit >= units) {
-                w.unit -= units;
-                ++w.q;
-            }
-            more = locate(w);
-            int next = -1;
-            if (more) next = slot_of(w);
             v4i acc[4];
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
@@ -257,6 +261,7 @@ __global__ __launch_bounds__(256, 4) void cache_attention_kernel(CacheArgs p, At
                     m = fmaxf(m, f[j][i]);
                 }
             }
+            if (more_ahead) fetch_keys(ahead, slot);
             m = heads_max<SUB>(m);
             if (lane < 16) smax[wave][lane] = m;
             __syncthreads();
@@ -266,7 +271,11 @@ __global__ __launch_bounds__(256, 4) void cache_attention_kernel(CacheArgs p, At
                 int8_t *dst = sv + (64 * wave + 16 * t + col) * PITCH + 8 * NS * c;
                 __builtin_memcpy(dst, vw[t], 8 * NS);
             }
-            if (more) fetch(w, next);
+            if (more_ahead) take(ahead, slot, p.v, vw);
+            w = ahead;
+            more = more_ahead;
+            more_ahead = more && look();
+            slot = more_ahead ? slot_of(ahead) : -1;
             const float fmx = __int_as_float(max(max(sred[0], sred[1]), max(sred[2], sred[3])));
             const int eb = fmx > 0.0f ? (__float_as_int(fmx) >> 23) - 127 : ATT_E_LO;
             const float down = pow2f(-eb);
