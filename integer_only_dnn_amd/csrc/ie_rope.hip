@@ -9,8 +9,9 @@
 // which is also the gradient, has -s for s.
 //
 // Bound by the stream over X and Y: 25216 rows of 36 heads of 64 (116 MB) back in
-// 26 us, 4.5 TB/s of a large copy's 4.9; 16 rows of 48 heads of 128 in 3.5 us, a
-// launch's time.
+// 24.4 us, 4.8 TB/s of a large copy's 4.9 (with a branch past what is not rotated,
+// which half of every wave's lanes take, 25.9); 16 rows of 48 heads of 128 in 3.3
+// us, a launch's time.
 #include "ie_f64.h"
 #include "ie_internal.h"
 
@@ -54,15 +55,7 @@ __device__ __forceinline__ RopeUnit rope_unit(const RopeArgs &p, int u) {
     return r;
 }
 typedef short s2 __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ void rope8(bool on, bool interleaved, s2 sign, uint32_t lo, uint32_t hi, const int4 &t, float (&y)[8]) {
-    if (!on) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            y[i] = (float)((int)(lo << (24 - 8 * i)) >> 2 & ~0x3fffff);
-            y[4 + i] = (float)((int)(hi << (24 - 8 * i)) >> 2 & ~0x3fffff);
-        }
-        return;
-    }
+__device__ __forceinline__ void rope8(bool interleaved, s2 turn, uint32_t lo, uint32_t hi, const int4 &t, float (&y)[8]) {
     const int w[4] = {t.x, t.y, t.z, t.w};
     uint32_t ab[4];
     if (interleaved) {
@@ -78,9 +71,9 @@ __device__ __forceinline__ void rope8(bool on, bool interleaved, s2 sign, uint32
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        // (c, s) turned forward, (c, -s) back; products with (c, -s) and (s, c)
-        const s2 cs = __builtin_bit_cast(s2, w[i]) * sign, v = __builtin_bit_cast(s2, ab[i]);
-        const s2 minus = {1, -1}, a = cs * minus, b = {cs[1], cs[0]};
+        // products with (c, -s) and (s, c), s of the table times turn's first, -s its second
+        const s2 cs = __builtin_bit_cast(s2, w[i]), v = __builtin_bit_cast(s2, ab[i]);
+        const s2 a = cs * s2{1, turn[1]}, b = s2{cs[1], cs[0]} * s2{turn[0], 1};
         const int ya = __builtin_amdgcn_sdot2(v, a, 0, false), yb = __builtin_amdgcn_sdot2(v, b, 0, false);
         y[interleaved ? 2 * i : i] = (float)ya;
         y[interleaved ? 2 * i + 1 : 4 + i] = (float)yb;
@@ -102,7 +95,8 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs p) {
     constexpr int RPB = 256 / T;
     __shared__ int sh[4];
     const int t = threadIdx.x % T, slot = threadIdx.x / T, units = p.cols >> 3;
-    const s2 sign = {1, (short)(p.inverse ? -1 : 1)};
+    const short way = p.inverse ? -1 : 1;
+    const s2 turn = {way, (short)-way};
     int run = NEED_NONE;
     int whole = 0;
     RopeUnit un[NU];
@@ -127,12 +121,13 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs p) {
         for (int i = 0; i < NU; ++i) {
             lo[i] = *(const uint32_t *)(x + un[i].at[0]);
             hi[i] = *(const uint32_t *)(x + un[i].at[1]);
-            w[i] = un[i].k >= 0 ? *(const int4 *)(tab + un[i].k) : int4{0, 0, 0, 0};
+            w[i] = int4{16384, 16384, 16384, 16384};  // what is not rotated: cos 1, sin 0
+            if (un[i].k >= 0) w[i] = *(const int4 *)(tab + un[i].k);
         }
         float big = 0.0f;
 #pragma unroll
         for (int i = 0; i < NU; ++i) {
-            rope8(un[i].k >= 0, INTER, sign, lo[i], hi[i], w[i], y[i]);  // the last runs of a row may be taken twice
+            rope8(INTER, turn, lo[i], hi[i], w[i], y[i]);  // the last runs of a row may be taken twice
 #pragma unroll
             for (int k = 0; k < 8; k += 2) asm("v_max3_f32 %0, %0, |%1|, |%2|" : "+v"(big) : "v"(y[i][k]), "v"(y[i][k + 1]));
         }
