@@ -1409,7 +1409,8 @@ ie_status ie_rope(const ie_rope_desc *d, const ie_mat *X, const ie_mat *Y, void 
     if (X->rows == 0 || X->cols == 0) return hip_status(launch_fill_i8(Y->exp, n_exps(Y), E_MIN, st));
     Carve c{(char *)ws, HEADER};
     const bool eight = X->cols % 8 == 0 && d->head_dim % 8 == 0 && d->rot % 8 == 0 && aligned(X->mant, 8) && aligned(Y->mant, 8);
-    const RopePlan pl = rope_plan(X->rows, X->cols, eight);
+    const bool y_row = Y->group == IE_GROUP_ROW || X->rows == 1;
+    const RopePlan pl = rope_plan(X->rows, X->cols, eight, !y_row);
     RopeArgs a;
     memset(&a, 0, sizeof a);
     a.x = X->mant;
@@ -1432,7 +1433,6 @@ ie_status ie_rope(const ie_rope_desc *d, const ie_mat *X, const ie_mat *Y, void 
     a.bmax = carve_rope(c, X->rows, X->cols);
     a.n_bmax = pl.grid;
     a.flags = (uint32_t *)ws;
-    const bool y_row = Y->group == IE_GROUP_ROW || X->rows == 1;
     a.mode = y_row ? NORM_ROWS : NORM_NEED;
     IE_TRY(launch_rope(a, pl, st));
     if (y_row) return IE_OK;

@@ -873,7 +873,7 @@ size_t attention_bwd_ws(long long rows, long long heads, long long kv, long long
     return align256(c.off);
 }
 
-RopePlan rope_plan(long long rows, long long cols, bool eight) {
+RopePlan rope_plan(long long rows, long long cols, bool eight, bool whole) {
     RopePlan p{256, 0, 1};
     if (eight) {
         const long long units = cols / 8;
@@ -883,7 +883,8 @@ RopePlan rope_plan(long long rows, long long cols, bool eight) {
 #undef IE_TRY_
     }
     const long long rpb = p.nu ? 256 / p.t : 1, want = (rows + rpb - 1) / rpb;
-    p.grid = (int)(want < 1 ? 1 : want > ROPE_BLOCKS ? ROPE_BLOCKS : want);
+    const int most = whole ? ROPE_BLOCKS : 8 * ROPE_BLOCKS;
+    p.grid = (int)(want < 1 ? 1 : want > most ? most : want);
     return p;
 }
 

@@ -469,8 +469,10 @@ struct RopePlan {
     X(16, 1) X(16, 2) X(16, 4) X(16, 6) X(64, 2) X(64, 3) X(64, 4) X(64, 5) X(64, 6) X(64, 8) X(256, 3)      \
     X(256, 4) X(256, 6) X(256, 8)
 constexpr int ROPE_BLOCKS = 2048;
-// eight: rows, heads and what is rotated of them come in runs of eight.
-RopePlan rope_plan(long long rows, long long cols, bool eight);
+// eight: rows, heads and what is rotated of them come in runs of eight.  whole: an
+// exponent for all rows, to which every workgroup leaves a maximum; else up to
+// eight times as many workgroups (25216 rows from memory: 29.0 us, with 2048 31.3).
+RopePlan rope_plan(long long rows, long long cols, bool eight, bool whole = true);
 int *carve_rope(Carve &c, long long rows, long long cols);  // block maxima
 size_t rope_ws(long long rows, long long cols);
 

@@ -9,7 +9,7 @@
 // which is also the gradient, has -s for s.
 //
 // Bound by the stream over X and Y: 25216 rows of 36 heads of 64 (116 MB) back in
-// 24.4 us, 4.8 TB/s of a large copy's 4.9 (with a branch past what is not rotated,
+// 24.4 us, 4.8 TB/s of a large copy's 4.9, and 29 from memory (with a branch past what is not rotated,
 // which half of every wave's lanes take, 25.9); 16 rows of 48 heads of 128 in 3.3
 // us, a launch's time.
 #include "ie_f64.h"

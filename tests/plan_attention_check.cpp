@@ -119,7 +119,7 @@ static void rope() {
 #undef IE_IS
             CHECK(built);
             CHECK(p.nu == 0 ? cols > 16384 : (long long)p.t * p.nu * 8 >= cols);
-            CHECK(p.grid >= 1 && p.grid <= ROPE_BLOCKS);
+            CHECK(p.grid >= 1 && p.grid <= ROPE_BLOCKS && rope_plan(rows, cols, true, false).grid >= p.grid);
             const RopePlan any = rope_plan(rows, cols, false);
             CHECK(any.nu == 0 && any.grid >= 1 && any.grid <= ROPE_BLOCKS);
         }
