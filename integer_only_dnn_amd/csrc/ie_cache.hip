@@ -435,6 +435,103 @@ __global__ __launch_bounds__(256) void cache_join_kernel(CacheArgs p, AttnArgs a
     }
 }
 
+// The same for few blocks: a workgroup joins all heads of a sequence and rounds
+// the row itself.  Thread (head, block) finds a weight (SPAN, the most blocks of a
+// sequence up to a power of two, times the heads are at most 256), then threads add
+// up runs of four neighbouring elements, rows of up to 4096.
+constexpr int JOIN_COLS = 4096;
+__global__ __launch_bounds__(256) void cache_join_row_kernel(CacheArgs p, AttnArgs a, int span) {
+    constexpr int NJ = JOIN_COLS / 1024;
+    __shared__ float sw[256];
+    __shared__ double sinv[256];
+    __shared__ int sem[256], sh[4];
+    const int tid = threadIdx.x, seq = blockIdx.x;
+    const int len = min(max(p.lengths[seq], 0), p.tokens), nb = (len + 255) >> 8;
+    if (tid == 0 && p.lengths[seq] != len) atomicOr(p.flags, IE_FLAG_INDEX);
+    const int ex = a.xe[a.x_row ? seq : 0];
+    const float r = a.c * pow2f(clip_e(ex));
+    // the sums' first blocks are on the way while the weights are found
+    const int *num = p.num + (long long)seq * p.blocks * a.cols + 4 * tid;
+    v4i x[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+        x[j] = v4i{0, 0, 0, 0};
+        if (nb > 0 && 4 * tid + 1024 * j < a.cols) x[j] = *(const v4i *)(num + 1024 * j);
+    }
+    const int head = tid / span, b = tid - head * span;
+    float m = -__builtin_inff();
+    int n = 0, e = 0;
+    if (head < a.heads && b < nb) {
+        const int4 t = p.top[((long long)seq * p.blocks + b) * a.heads + head];
+        m = __int_as_float(t.x);
+        n = t.y;
+        e = t.z;
+    }
+    float top = n ? m : -__builtin_inff();
+    int em = n ? max(e, ATT_E_LO) : ATT_E_LO;
+    for (int o = 1; o < span; o <<= 1) {  // a head's threads lie in one wave
+        top = fmaxf(top, __shfl_xor(top, o, 64));
+        em = max(em, __shfl_xor(em, o, 64));
+    }
+    float w = 0.0f;
+    double den = 0.0;
+    if (n) {
+        const float y = weight(m - top, r);
+        den = (double)(y + RINT_MAGIC - RINT_MAGIC) * (double)n;
+        w = __builtin_fmaf(y, pow2f(e - em), RINT_MAGIC) - RINT_MAGIC;
+    }
+    for (int o = 1; o < span; o <<= 1) den += __shfl_xor(den, o, 64);
+    sw[tid] = w;
+    if (b == 0) {
+        sinv[head] = den > 0.0 ? 1.0 / den : 0.0;
+        sem[head] = em;
+    }
+    __syncthreads();
+    double y[NJ][4];
+    int need = NEED_NONE;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+        const int c = 4 * tid + 1024 * j, h = c / a.d;
+        if (c >= a.cols) break;
+        double s[4] = {0, 0, 0, 0};
+        for (int i = 0; i < nb; ++i) {
+            const v4i v = x[j];
+            if (i + 1 < nb) x[j] = *(const v4i *)(num + 1024 * j + (long long)(i + 1) * a.cols);
+            const double wt = (double)sw[h * span + i];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s[k] = __builtin_fma(wt, (double)v[k], s[k]);
+        }
+        MaxMag mx;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[j][k] = s[k] * sinv[h];
+        mx.add(y[j][0], y[j][1]);
+        mx.add(y[j][2], y[j][3]);
+        const int own = need_word(mx.word(), a.q);
+        if (own != NEED_NONE) need = max(need, own + sem[h]);
+    }
+    const int row_e = clamp_exp_flag(max(E_MIN, row_reduce<256>(need, Max{}, sh)), p.flags);
+    if (tid == 0) {
+        a.ye[seq] = (int8_t)row_e;
+        if (ex > ATT_E_HI) atomicOr(p.flags, IE_FLAG_EXP_RANGE);
+    }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+        const int c = 4 * tid + 1024 * j;
+        if (c >= a.cols) break;
+        const double scale = pow2(sem[c / a.d] - row_e);
+        int8_t *out = a.y + (long long)seq * a.cols + c;
+        int o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = __double2loint(__builtin_fma(y[j][k], scale, 6755399441055744.0));  // 1.5 * 2^52
+        if (a.out_vec) {
+            *(uint32_t *)out = pack4(o[0], o[1], o[2], o[3]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) out[k] = (int8_t)o[k];
+        }
+    }
+}
+
 hipError_t launch_cache_store(const CacheArgs &c, long long rows, const int8_t *x, const int8_t *xe, int x_row, int width, int first,
                               const int *slots, hipStream_t st) {
     const int nl = c.d <= 16 ? 1 : c.d <= 32 ? 2 : c.d <= 64 ? 4 : 8;
@@ -464,6 +561,17 @@ hipError_t launch_cache_attention(const CacheArgs &c, const AttnArgs &a, hipStre
     prof_end(st, PROF_ATT_CACHE);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+    // A workgroup to a sequence where it adds up to eight runs of 1024 sums one after the other (us,
+    // that kernel, and joining and rounding with a launch between them: 4 blocks of 8 heads of 64
+    // 4.4 and 7; of 32 of 128 9.0 and 8.3, 8 blocks 14 and 8.2)
+    int span = 1;
+    while (span < c.blocks) span <<= 1;
+    if ((a.cols + 1023ll) / 1024 * c.blocks <= 8 && (long long)span * a.heads <= 256 && a.cols <= JOIN_COLS) {
+        prof_begin(st, PROF_ATT_JOIN);
+        hipLaunchKernelGGL(cache_join_row_kernel, dim3((unsigned)c.n), dim3(256), 0, st, c, a, span);
+        prof_end(st, PROF_ATT_JOIN);
+        return hipGetLastError();
+    }
     // whole heads, or, where these are fewer than two workgroups a CU, 16 elements each (one
     // sequence of 131072 tokens, 32 heads of 128: 9.6 us, whole heads 25; 48 sequences 31 and 8.7)
     AttnArgs r = a;

@@ -115,11 +115,21 @@ def test_widths_and_alignment(bits, by):
     attend(np.random.default_rng(bits), [77, 290], 4, 1, 64, 16, bits=bits, by=by)
 
 
-def test_many_sequences():
-    """More sequences than a workgroup scans at once, short ones and empty ones among them."""
-    announce("cache attention many")
+@pytest.mark.parametrize("page,spare", [(8, 0), (256, 9)])
+def test_many_sequences(page, spare):
+    """More sequences than a workgroup scans at once, short ones and empty ones among them; tables of one and of ten blocks."""
+    announce(f"cache attention many {page}")
     rng = np.random.default_rng(21)
-    attend(rng, list(rng.integers(0, 40, 600)), 2, 1, 16, 8, spare=0)
+    attend(rng, list(rng.integers(0, 40, 600)), 2, 1, 16, page, spare=spare)
+
+
+@pytest.mark.parametrize("blocks", [1, 2, 4, 8, 9])
+@pytest.mark.parametrize("heads,kv,d", [(8, 8, 64), (32, 4, 128), (64, 2, 16), (255, 51, 16), (257, 1, 16), (20, 4, 48)])
+def test_few_blocks(heads, kv, d, blocks):
+    """Tables of up to eight blocks, with the last one full, begun and empty."""
+    announce(f"cache attention {blocks} blocks {heads} {kv} {d}")
+    rng = np.random.default_rng(heads + blocks)
+    attend(rng, [256 * blocks, 256 * blocks - 255, 256 * (blocks - 1), 1, 0], heads, kv, d, 256, spare=0)
 
 
 def test_pages_and_lengths_outside():
