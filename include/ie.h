@@ -440,11 +440,19 @@ ie_status ie_dropout(const ie_mat *X, const ie_mat *R, const ie_mat *Y, const ie
  * the sums exact, 1 / L and the product with it rounded to 53 bits; the row is
  * rounded once into O.  So a weight is held to 15 bits below the largest one,
  * and a token's result depends on the tokens that it sees and on no others.
+ * Of N keys rounding takes at most N / 2 units of L, which is 32512 at least, and
+ * N / 2 units times 128 of a sum of values: up to 2032 keys at most 1 / 32 of both.
+ * A row of a head that sees more keys has fine weights where that is not enough:
+ * where sum R(2^7 w) and 2^7 L differ by more than 2^7 L / 32, or no sum of
+ * values reaches 64 N.  Then L = sum R(2^14 w) and o = (sum_j R(2^14 w_j
+ * 2^(e_j - E)) v_j) (1 / L) 2^E: weights to 29 bits below the largest, less the
+ * bits by which a value's exponent lies below E.
  * O must be ROW (one exponent a token), else IE_ERR_UNSUPPORTED.  Rows before
  * the first and behind the last sequence are left as they were, mantissas and
  * exponents.
  * stats: for the backward pass, 8 bytes for every row and head (a device array
- * [rows x heads], 8-byte aligned): m and L; NULL where none follows.
+ * [rows x heads], 8-byte aligned): m and L (of a row of fine weights R(2^-14 L), and
+ * m's last bit is set, which is no part of it); NULL where none follows.
  * Limits (IE_ERR_UNSUPPORTED): head_dim <= 128, (heads + 2 kv_heads) * head_dim
  * <= 2^24, 2^-30 <= scale <= 2^30, (rows / 32 + n_seq + 9) * heads < 2^24, rows <
  * 2^26 - 4, without offsets at most 131071 rows.

@@ -3,7 +3,8 @@
 //   t_ij = (q_i . k_j) 2^(e_j),  m_i = max_j t_ij over the keys that i sees,
 //   P_ij = rint(w_ij), L_i = sum_j P_ij,  E_i = max e_j over the same keys,
 //   P'_ij = rint(w_ij 2^(e_j - E_i)),  o_i = (sum_j P'_ij v_j) 2^(E_i) / L_i
-// with w_ij the weight of t_ij - m_i (ie_attn.h).  Sums over keys are exact
+// with w_ij the weight of t_ij - m_i (ie_attn.h), in finer units for the rows of
+// many small weights.  Sums over keys are exact
 // integers, so a row's result depends on the keys it sees alone, and not on
 // how they are split into tiles.  The division by L (a product with 1 / L) is
 // held to 53 bits; a row's heads are rounded into its one exponent at the end,
@@ -87,15 +88,21 @@ __global__ __launch_bounds__(256, SPLIT > 1 ? 2 : DP > 64 ? 3 : 4) void attn_fwd
     uint32_t sum = 0, blocks = 0;
     // the digits of four weights of keys 16 z + 4 quad .., given t - m or the scores' difference, and
     // 2^(e - E): where every query sees every key E is one number, and f has it already
-    auto weigh4 = [&](auto masked, const float (&d)[4], const float (&f)[4], float down, int z, int lim, int &dh, int &dl) {
+    uint32_t part = 0;  // the weights in units of 2^-7, modulo 2^32
+    auto weigh4 = [&](auto masked, auto checked, const float (&d)[4], const float (&f)[4], float down, int z, int lim, int &dh, int &dl) {
         int bits[4];
-        uint32_t whole_n[4];
+        uint32_t whole_n[4], seventh[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float w = weight(d[i], r);
             if (masked.value) w = 16 * z + i <= lim ? w : 0.0f;
             bits[i] = __float_as_int(ROW ? __builtin_fmaf(w, CAUSAL ? f[i] * down : f[i], RINT_128) : w + RINT_128);
             whole_n[i] = (uint32_t)(ROW ? __float_as_int(w + RINT_MAGIC) : bits[i]);
+            if (checked.value) seventh[i] = (uint32_t)__float_as_int(__builtin_fmaf(w, 128.0f, RINT_MAGIC));
+        }
+        if (checked.value) {  // modulo 2^32
+            part += seventh[0] + seventh[1];
+            part += seventh[2] + seventh[3];
         }
         sum += whole_n[0] + whole_n[1];
         sum += whole_n[2] + whole_n[3];
@@ -114,17 +121,32 @@ __global__ __launch_bounds__(256, SPLIT > 1 ? 2 : DP > 64 ? 3 : 4) void attn_fwd
         sum -= 4 * blocks * (uint32_t)(ROW ? RINT_BITS : RINT_BITS + 128);
         sum = (uint32_t)col_reduce((int)sum, Add{});
     };
-    auto finish = [&](float m, int mi, int top) {
+    // lost: what rounding took of the weights, in units of 2^-7
+    auto finish = [&](float m, int mi, int top, int lost = 0) {
         const double inv = 1.0 / (double)sum;
-        double y[4 * NE];
+        double y[4 * NE], big = 0.0;
 #pragma unroll
         for (int e = 0; e < NE; ++e)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) y[4 * e + i] = __builtin_fma((double)hi[e][i], 256.0, (double)lo[e][i]) * inv;
+            for (int i = 0; i < 4; ++i) y[4 * e + i] = __builtin_fma((double)hi[e][i], 256.0, (double)lo[e][i]);
+        bool fine = false;
+        if (keys > ATT_CHECK) {
+#pragma unroll
+            for (int i = 0; i < 4 * NE; ++i) big = fmax(big, fabs(y[i]));
+            big = swap_reduce<32>(swap_reduce<16>(big, MaxD{}), MaxD{});
+            const int seen = CAUSAL ? qi + 1 : n;
+            fine = ok && seen > ATT_CHECK && (32ll * abs(lost) > 128ll * sum || big < 64.0 * seen);
+        }
+#pragma unroll
+        for (int i = 0; i < 4 * NE; ++i) y[i] *= inv;
         const long long row = sp.a + qi;
         store_odd(y, top, p.q, ok, p.d, lane, p.v16 + row * p.cols + h * p.d, p.p16 + row * p.parts + h);
         if (p.stats && ok && lane < 16)
             p.stats[row * p.heads + h] = int2{__float_as_int(ROW ? m : (float)mi * pow2f(eq)), (int)sum};
+        if (fine && lane < 16) {
+            p.p16[row * p.parts + h] = P_FINE;
+            atomicOr(p.flags + FINE_WORD, 1u);
+        }
     };
 
     if constexpr (SHORT) {
@@ -186,7 +208,7 @@ __global__ __launch_bounds__(256, SPLIT > 1 ? 2 : DP > 64 ? 3 : 4) void attn_fwd
                     const float(&y)[4] = s[4 * t + z];
                     const float d[4] = {y[0] - m, y[1] - m, y[2] - m, y[3] - m};
                     int a, c;
-                    weigh4(masked, d, f, down, 4 * t + z, lim, a, c);
+                    weigh4(masked, Bool<false>{}, d, f, down, 4 * t + z, lim, a, c);
                     dh[z] = a;
                     dl[z] = c;
                 }
@@ -331,7 +353,7 @@ __global__ __launch_bounds__(256, SPLIT > 1 ? 2 : DP > 64 ? 3 : 4) void attn_fwd
     __syncthreads();
 
     // second pass: weights and the sums they enter
-    auto weigh = [&](auto masked, int t, v4i &dh, v4i &dl) {
+    auto weigh = [&](auto masked, auto checked, int t, v4i &dh, v4i &dl) {
         const int lim = limit(t);
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
@@ -345,21 +367,32 @@ __global__ __launch_bounds__(256, SPLIT > 1 ? 2 : DP > 64 ? 3 : 4) void attn_fwd
             for (int i = 0; i < 4; ++i) d[i] = ROW ? __builtin_fmaf((float)acc[i], f[i], -m) : (float)(acc[i] - mi);
             int a, c;
             if (!CAUSAL) factors(scaled_lds[buffer(t)], z, f);
-            weigh4(masked, d, f, down, z, lim, a, c);
+            weigh4(masked, checked, d, f, down, z, lim, a, c);
             dh[z] = a;
             dl[z] = c;
         }
     };
-    if (first < tiles) fetch(first, true);
-    for (int t = first; t < tiles; t += SPLIT) {
-        put(t, true);
-        if (t + SPLIT < tiles) fetch(t + SPLIT, true);
-        fence();
-        if (idle || 64 * t >= last) continue;
-        v4i dh, dl;
-        if (whole(t)) weigh(Bool<false>{}, t, dh, dl);
-        else weigh(Bool<true>{}, t, dh, dl);
-        gather(sv[buffer(t)], dh, dl);
+    auto weigh_all = [&](auto checked) {
+        if (first < tiles) fetch(first, true);
+        for (int t = first; t < tiles; t += SPLIT) {
+            put(t, true);
+            if (t + SPLIT < tiles) fetch(t + SPLIT, true);
+            fence();
+            if (idle || 64 * t >= last) continue;
+            v4i dh, dl;
+            if (whole(t)) weigh(Bool<false>{}, checked, t, dh, dl);
+            else weigh(Bool<true>{}, checked, t, dh, dl);
+            gather(sv[buffer(t)], dh, dl);
+        }
+    };
+    const bool check = keys > ATT_CHECK;  // rows may need fine weights
+    if (check) weigh_all(Bool<true>{});
+    else weigh_all(Bool<false>{});
+    int lost = 0;
+    if (check) {
+        const uint32_t n4 = 4 * blocks;
+        lost = (int)(part - n4 * (uint32_t)RINT_BITS - 128 * (sum - n4 * (uint32_t)(ROW ? RINT_BITS : RINT_BITS + 128)));
+        lost = col_reduce(lost, Add{});
     }
     total();
     if constexpr (SPLIT > 1) {
@@ -367,12 +400,137 @@ __global__ __launch_bounds__(256, SPLIT > 1 ? 2 : DP > 64 ? 3 : 4) void attn_fwd
         static_assert(sizeof tiles_lds >= 3 * 4 * NE * 64 * sizeof(int), "a digit's sums fit the tiles");
         gather_waves<4 * NE>(x, hi, wave, lane);
         gather_waves<4 * NE>(x, lo, wave, lane);
-        v4i s4 = {(int)sum, 0, 0, 0};
+        v4i s4 = {(int)sum, lost, 0, 0};
         gather_waves<4>(x, (v4i(&)[1])s4, wave, lane);
         sum = (uint32_t)s4[0];
+        lost = s4[1];
         if (wave) return;
     }
-    if (!idle) finish(m, mi, top);
+    if (!idle) finish(m, mi, top, lost);
+}
+
+// The rows that the kernel above has marked, with fine weights: the same tiles,
+// the sums in four digits.  Launched where a sequence may be long enough for such a
+// row; a call without one ends at its first load.  With them in the kernel above,
+// behind its sums, its registers ran over (8192 tokens, heads of 128: 667 us for 290).
+template <int DP, bool ROW, bool CAUSAL>
+__global__ __launch_bounds__(256, DP > 64 ? 1 : 2) void attn_fwd_fine_kernel(AttnArgs p, int items) {
+    using T = HeadTile<DP>;
+    constexpr int KS = T::KS, NE = DP / 16;
+    __shared__ __align__(16) int8_t sk[2][T::BYTES], sv[2][T::BYTES];
+    __shared__ __align__(16) float sf[2][64];
+    __shared__ int any_lds[4];
+    if (!p.flags[FINE_WORD]) return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, quad = lane >> 4;
+    T k, v;
+    k.init(p.width, p.dp);
+    v.init(p.width, p.dp);
+    for (int idx = blockIdx.x; idx < items; idx += gridDim.x) {
+        const int at = idx >> 3, pair = 8 * (at / p.group) + (idx & 7);
+        const int kvh = pair % p.kv, h = kvh * p.group + at % p.group;
+        Span sp;
+        int tile;
+        if (!rank_tile<CAUSAL>(p, pair / p.kv, 64, sp, tile)) continue;
+        const int n = sp.n, q0 = 64 * tile, qw = q0 + 16 * wave, qi = qw + (lane & 15);
+        const long long row = sp.a + qi;
+        const bool fine = qi < n && p.p16[row * p.parts + h] == P_FINE;
+        const bool some = __ballot(fine) != 0;
+        __syncthreads();  // the tiles before are read
+        if (lane == 0) any_lds[wave] = some;
+        __syncthreads();
+        if (!(any_lds[0] | any_lds[1] | any_lds[2] | any_lds[3])) continue;
+        const int8_t *base = p.x + (long long)sp.a * p.width;
+        const int8_t *kh = base + (long long)(p.heads + kvh) * p.dp, *vh = kh + (long long)p.kv * p.dp;
+        const int8_t *xe = p.xe + (ROW ? sp.a : 0);
+        const int eq = clip_e(xe[ROW ? min(qi, n - 1) : 0]);
+        const float r = p.c * pow2f(eq) * (ROW ? 1.0f : pow2f(eq));
+        v4i q[KS];
+        head_regs<KS>(base + (long long)qi * p.width + h * p.dp, qi < n, p.dp, lane, q);
+        const int keys = CAUSAL ? min(n, q0 + 64) : n, tiles = (keys + 63) / 64, lim = CAUSAL ? qi : n - 1;
+        float fe = 0.0f;
+        auto fetch = [&](int t, bool values) {
+            k.fetch(kh, p.width, 64 * t, keys, p.dp);
+            if (values) v.fetch(vh, p.width, 64 * t, keys, p.dp);
+            if (tid < 64) fe = ROW ? pow2f(clip_e(xe[min(64 * t + tid, n - 1)])) : 1.0f;
+        };
+        auto put = [&](int t, bool values) {
+            k.put(sk[t & 1]);
+            if (values) v.put(sv[t & 1]);
+            if (tid < 64) sf[t & 1][tid] = fe;
+        };
+        auto scores = [&](int t, int z) {
+            v4i acc = {0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < KS; ++i) acc = mfma(T::frag_r(sk[t & 1], z, i, lane), q[i], acc);
+            return acc;
+        };
+        // the largest score, and the largest factor of the keys seen
+        float m = -__builtin_inff(), em = 0.0f;
+        fetch(0, false);
+        for (int t = 0; t < tiles; ++t) {
+            put(t, false);
+            if (t + 1 < tiles) fetch(t + 1, false);
+            __syncthreads();
+            if (!some) continue;
+            for (int z = 0; z < 4; ++z) {
+                const v4i acc = scores(t, z);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const bool on = 64 * t + 16 * z + 4 * quad + i <= lim;
+                    const float f = sf[t & 1][16 * z + 4 * quad + i];
+                    m = fmaxf(m, on ? (float)acc[i] * f : -__builtin_inff());
+                    em = fmaxf(em, on ? f : 0.0f);
+                }
+            }
+        }
+        m = col_max(m);
+        em = col_max(em);
+        const int top = ROW ? (__float_as_int(em) >> 23) - 127 : eq;
+        const float down = pow2f(ROW ? -top : 0) * FINE_UNIT;
+        __syncthreads();
+        v4i acc[4][NE] = {};
+        long long count = 0;
+        fetch(0, true);
+        for (int t = 0; t < tiles; ++t) {
+            put(t, true);
+            if (t + 1 < tiles) fetch(t + 1, true);
+            __syncthreads();
+            if (!some) continue;
+            v4i dg[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+                const v4i s = scores(t, z);
+                int n4[4], o[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float f = sf[t & 1][16 * z + 4 * quad + i];
+                    float w = weight(__builtin_fmaf((float)s[i], f, -m), r);
+                    w = 64 * t + 16 * z + 4 * quad + i <= lim ? w : 0.0f;
+                    count += (int)__builtin_rintf(w * FINE_UNIT);
+                    n4[i] = (int)__builtin_rintf(w * (f * down));
+                }
+                digits4x4(n4, o);
+#pragma unroll
+                for (int g = 0; g < 4; ++g) dg[g][z] = o[g];
+            }
+#pragma unroll
+            for (int e = 0; e < NE; ++e) {
+                const v4i vt = T::frag_t(sv[t & 1], e, lane);
+#pragma unroll
+                for (int g = 0; g < 4; ++g) acc[g][e] = mfma(vt, dg[g], acc[g][e]);
+            }
+        }
+        if (!some) continue;
+        const double total = swap_reduce<32>(swap_reduce<16>((double)count, Add{}), Add{}), inv = 1.0 / total;
+        double y[4 * NE];
+#pragma unroll
+        for (int e = 0; e < NE; ++e)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[4 * e + i] = whole4(acc[0][e][i], acc[1][e][i], acc[2][e][i], acc[3][e][i]) * inv;
+        store_odd(y, top, p.q, fine, p.d, lane, p.v16 + row * p.cols + h * p.d, p.p16 + row * p.parts + h);
+        if (p.stats && fine && lane < 16)
+            p.stats[row * p.heads + h] = int2{__float_as_int(ROW ? m : m * pow2f(eq)) | 1, (int)(uint32_t)rint(total * (1.0 / 16384.0))};
+    }
 }
 
 // Rows of parts (heads), each rounded to odd at two bits below its own need, into one
@@ -385,6 +543,7 @@ __global__ __launch_bounds__(256) void attn_round_kernel(AttnArgs p) {
     const int lane = threadIdx.x % T;
     const long long row = (long long)blockIdx.x * (256 / T) + threadIdx.x / T;
     if (row >= p.rows) return;
+    if (row == 0 && lane == 0) p.flags[FINE_WORD] = 0;
     if (p.off && row == 0) {
         bool bad = false;
         for (int s = lane; s < p.n_seq; s += T) {
@@ -429,6 +588,19 @@ hipError_t launch_attention_round(const AttnArgs &a, hipStream_t st) {
     return hipGetLastError();
 }
 
+template <int DP>
+static void fwd_fine(const AttnArgs &a, hipStream_t st) {
+    const unsigned items = att_grid(att_slots(a.rows, a.n_seq, 64), a.kv, a.group);
+    const dim3 grid(items < 4 * NCU ? items : 4 * NCU), block(256);
+    if (a.x_row) {
+        if (a.causal) hipLaunchKernelGGL((attn_fwd_fine_kernel<DP, true, true>), grid, block, 0, st, a, (int)items);
+        else hipLaunchKernelGGL((attn_fwd_fine_kernel<DP, true, false>), grid, block, 0, st, a, (int)items);
+    } else {
+        if (a.causal) hipLaunchKernelGGL((attn_fwd_fine_kernel<DP, false, true>), grid, block, 0, st, a, (int)items);
+        else hipLaunchKernelGGL((attn_fwd_fine_kernel<DP, false, false>), grid, block, 0, st, a, (int)items);
+    }
+}
+
 template <int DP, bool SHORT, int SPLIT>
 static void fwd(AttnArgs a, hipStream_t st) {
     a.chunk = att_chunk(a, 64 / SPLIT, !a.causal);
@@ -451,6 +623,7 @@ static void fwd(const AttnArgs &a, hipStream_t st) {
     if (a.rows <= 256ll * max(a.n_seq, 1)) fwd<DP, true, 1>(a, st);
     else if (att_slots(a.rows, a.n_seq, 64) * a.heads < 2 * NCU) fwd<DP, false, 4>(a, st);
     else fwd<DP, false, 1>(a, st);
+    if (a.rows > ATT_CHECK) fwd_fine<DP>(a, st);
 }
 
 hipError_t launch_attention_fwd(const AttnArgs &a, hipStream_t st) {

@@ -95,7 +95,7 @@ __global__ __launch_bounds__(256) void attn_scale_kernel(AttnArgs p, AttnBwd b) 
         const int2 d = b.dots[row * p.heads + h], st = p.stats[row * p.heads + h];
         const int delta = bits_of((uint32_t)abs(d.x)) + eo, rise = max(d.y + r_top, delta + e_top) + 1;
         AttnRow q;
-        q.m = __int_as_float(st.x);
+        q.m = __int_as_float(st.x & ~1);  // its last bit: a row of fine weights
         q.r = r;
         q.dot = (float)d.x * pow2f(eo);
         q.a = (float)(1.0 / (double)(uint32_t)st.y) * down;  // a < 2^alpha

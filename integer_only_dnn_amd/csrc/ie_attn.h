@@ -19,6 +19,20 @@
 // tiles and of workgroups is of no account.  n + 128 comes out of the adder of
 // rint (a magic constant), its two low bytes are a and b + 128.
 //
+// Fine weights.  Where many weights of a row are small beside its largest, as in
+// a long row with one key far ahead of the others, R(w) takes too much of them:
+// every weight below half a unit counts as nothing.  Up to ATT_CHECK keys that is
+// less than 32512 / 32 in all.  A row that sees more has its sum L taken in units
+// of 2^-7 beside it (whole numbers, exact modulo 2^32).  Where the two differ by
+// more than a 32nd, or where the head's largest sum of values is below 64 a key, half a
+// unit times 128, so that rounding may reach it, all weights of the row are
+// taken again with ATT_FINE bits behind their unit, in four digits (the sums
+// of 131071 keys stay below 2^53).  The mark of such a row is the last bit of its
+// maximum (scores have 21 bits of the 24), so that the gradient knows it.  The second
+// condition takes no instruction a weight; counting what rounding takes of the value
+// weights w 2^(e - E) too costs three, and registers that heads of 128 do not have (8192
+// tokens below: 361 us for 290).
+//
 // Layout.  The matrix instruction's result holds one column per lane (column
 // lane % 16, rows 4 (lane / 16) + r), its operands 16 consecutive steps of a
 // contraction of 64 (steps 16 (lane / 16) ..).  Products run with the axis that
@@ -43,6 +57,10 @@ constexpr float W_C3 = 2545.0f * 0x1p-32f, W_C2 = 7358.0f * 0x1p-32f, W_C1 = 226
 constexpr float RINT_MAGIC = 12582912.0f;  // 1.5 * 2^23: a sum's low bits are a whole number
 constexpr int RINT_BITS = 0x4B400000;
 constexpr float RINT_128 = RINT_MAGIC + 128.0f;
+constexpr int ATT_CHECK = 2032, ATT_FINE = 14;
+constexpr float FINE_UNIT = 16384.0f;  // 2^ATT_FINE
+constexpr int16_t P_FINE = -31000;     // in the place of a need: the head's fine weights are still to be taken
+constexpr int FINE_WORD = 8;           // of the workspace's header: whether there is such a head; zero between calls
 
 __device__ __forceinline__ int clip_e(int e) { return min(max(e, ATT_E_LO), ATT_E_HI); }
 __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
@@ -82,6 +100,22 @@ __device__ __forceinline__ void digits3x4(int a, int b, int c, int d, int &hi, i
     const uint32_t t = __builtin_amdgcn_perm((uint32_t)d, (uint32_t)c, 0x0c0c0602u);
     // bytes 64 + h, h from -32 to 32: no byte borrows from the next
     hi = (int)(((__builtin_amdgcn_perm(t, s, 0x05040100u) | 0x80808080u) - 0x40404040u) ^ 0x80808080u);
+}
+
+// Four digits of four n: of the highest bytes on, a word of four bytes each.
+__device__ __forceinline__ void digits4x4(const int (&n)[4], int (&out)[4]) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = (uint32_t)n[i] + 0x808080u;
+    const uint32_t s = __builtin_amdgcn_perm(u[1], u[0], 0x05010400u), t = __builtin_amdgcn_perm(u[3], u[2], 0x05010400u);
+    const uint32_t v = __builtin_amdgcn_perm(u[1], u[0], 0x07030602u), w = __builtin_amdgcn_perm(u[3], u[2], 0x07030602u);
+    out[0] = (int)__builtin_amdgcn_perm(w, v, 0x07060302u);
+    out[1] = (int)(__builtin_amdgcn_perm(w, v, 0x05040100u) ^ 0x80808080u);
+    out[2] = (int)(__builtin_amdgcn_perm(t, s, 0x07060302u) ^ 0x80808080u);
+    out[3] = (int)(__builtin_amdgcn_perm(t, s, 0x05040100u) ^ 0x80808080u);
+}
+__device__ __forceinline__ double whole4(int a, int b, int c, int d) {
+    return __builtin_fma(__builtin_fma(__builtin_fma((double)a, 256.0, (double)b), 256.0, (double)c), 256.0, (double)d);
 }
 
 __device__ __forceinline__ v4i mfma(v4i a, v4i b, v4i c) { return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0); }

@@ -71,6 +71,10 @@ struct Max {
     __device__ __forceinline__ int operator()(int a, int b) const { return max(a, b); }
 };
 
+struct MaxD {
+    __device__ __forceinline__ double operator()(double a, double b) const { return fmax(a, b); }
+};
+
 template <int CTRL>
 __device__ __forceinline__ int dpp_of(int v) { return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xf, 0xf, true); }
 template <int CTRL>

@@ -42,7 +42,8 @@ R9  layer norm, the product with bias and residual, and dropout hold what is
     there (R2, R3).
 
 R10 attention: a softmax weight is an integer of at most 32512 (15 bits below the
-    row's largest), from an exponent held to 2^-17 and a cubic in fp32; sums of
+    row's largest, 14 more in long rows whose small weights rounding would take
+    too much of), from an exponent held to 2^-17 and a cubic in fp32; sums of
     weights and of weighted mantissas are exact; a weight takes its value's
     exponent in, relative to the largest one that its query sees, so that a
     token depends on no later one (R5 would align values over the sequence).
@@ -831,6 +832,8 @@ def dropout(X: QT, R, drop: int, seed: int, step: int, y_group: int, bits: int =
 
 ATT_E = (-48, 16)        # exponents of Q, K, V and O are read clipped to these
 ATT_UNIT = 32512         # a weight of one
+ATT_CHECK = 2032         # rows that see more keys are checked for what rounding their weights takes: 2032 / 2 = ATT_UNIT / 32
+ATT_FINE = 14            # bits that a weight has behind its unit in rows that it takes too much of
 CACHE_BLOCK = 256
 
 
@@ -880,9 +883,24 @@ def _att_weights(t, see, m, r) -> np.ndarray:
     return np.where(see, softmax_weight(_f32(np.minimum(t - m[:, None], 0.0)), r[:, None]), 0.0)
 
 
+def _att_fine(w, see, num) -> np.ndarray:
+    """Rows that rounding may take too much of, of more than ATT_CHECK keys: R(w) changes their sum L by more than a 32nd
+    (weights taken in units of 2^-7), or the largest sum of values is below 64 for every key, so that half a unit of each
+    weight, times 128, may reach it."""
+    seen, whole = see.sum(axis=1), np.rint(w).sum(axis=1)
+    lost = np.abs(np.rint(np.ldexp(w, 7)).sum(axis=1) - np.ldexp(whole, 7))
+    return (seen > ATT_CHECK) & ((32 * lost > np.ldexp(whole, 7)) | (np.abs(num).max(axis=1) < 64 * seen))
+
+
+def _att_marks(tops) -> tuple:
+    """Largest scores and the rows whose weights are fine, from the stats: scores have at most 21 bits, the last of the 24 is the mark."""
+    bits = tops.view(np.int32)
+    return (bits & ~np.int32(1)).view(np.float32).astype(np.float64), (bits & 1).astype(bool)
+
+
 def attention_fwd(X: QT, heads: int, kv: int, d: int, scale: float, causal: bool, offsets=None, bits: int = Q_BITS):
     """(O, m, L): O by rows, zeros with exponent E_MIN on rows of no sequence;
-    m and L of every row and head."""
+    m and L of every row and head (m's last bit set: a row of fine weights)."""
     rows, g = X.mant.shape[0], heads // kv
     e_all, rate = _att_exp(X.row_exp()), _att_rate(scale)
     y = np.zeros((rows, heads * d))
@@ -898,9 +916,15 @@ def attention_fwd(X: QT, heads: int, kv: int, d: int, scale: float, causal: bool
             w = _att_weights(t, see, m, rate * np.ldexp(1.0, e))
             total = np.rint(w).sum(axis=1)
             top = np.where(see, e[None, :], -1000).max(axis=1)
-            num = np.rint(np.ldexp(w, e[None, :] - top[:, None])) @ v.astype(np.float64)
+            x = np.ldexp(w, e[None, :] - top[:, None])
+            num = np.rint(x) @ v.astype(np.float64)
+            fine = _att_fine(w, see, num)
+            if fine.any():
+                total[fine] = np.rint(np.ldexp(w[fine], ATT_FINE)).sum(axis=1)
+                num[fine] = np.rint(np.ldexp(x[fine], ATT_FINE)) @ v.astype(np.float64)
             y[a:b, h * d:(h + 1) * d] = np.ldexp(num * (1.0 / total)[:, None], top[:, None])
-            tops[a:b, h], sums[a:b, h] = m, total
+            tops[a:b, h] = (m.astype(np.float32).view(np.int32) | fine).view(np.float32)
+            sums[a:b, h] = np.where(fine, np.rint(np.ldexp(total, -ATT_FINE)), total)
     return requant_f64(y, ROW, bits), tops, sums
 
 
@@ -934,7 +958,8 @@ def attention_bwd(X: QT, O: QT, dO: QT, tops, sums, heads: int, kv: int, d: int,
                 q, dy, o = _att_head(X, h, d, a, b), _att_head(dO, h, d, a, b), _att_head(O, h, d, a, b)
                 t, see = _att_scores(q, k, e, causal)
                 total = sums[a:b, h].astype(np.float64)
-                w = _att_weights(t, see, tops[a:b, h].astype(np.float64), rate * np.ldexp(1.0, e))
+                m, _ = _att_marks(tops[a:b, h].copy())
+                w = _att_weights(t, see, m, rate * np.ldexp(1.0, e))
                 dot = (dy * o).sum(axis=1)
                 u = _f32(np.ldexp(_exact_matmul(dy, v.T).astype(np.float64), e[None, :])
                          - np.ldexp(dot.astype(np.float64), eo)[:, None])
