@@ -487,6 +487,9 @@ ie_status ie_attention_fwd(const ie_attention_desc *d, const ie_mat *QKV, const 
  *   b_i = a_i 2^(e_i - G) rounded to fp32,
  * products rounded to fp32, sums over a sequence and, for keys, over the query
  * heads that share them, exact, the products behind them rounded to 53 bits.
+ * A row of fine weights has its sum for dQ in units of 2^-14 (R(s 2^(e_j - sigma
+ * + 14)), times 2^-14 behind it), and so have, for dV and dK (there in the place of
+ * 2^6), all keys of a sequence and key head of which a query's weights are fine.
  * The powers of two come from bounds: with |x| < 2^[x], [x] half the bits of
  * sum x^2, rounded up, bits n of a whole number, and maxima over a sequence
  *   nu_j = [v_j] + e_j,  delta_i = bits |dO_i . O_i| + eO_i,

@@ -591,7 +591,7 @@ hipError_t launch_attention_round(const AttnArgs &a, hipStream_t st) {
 template <int DP>
 static void fwd_fine(const AttnArgs &a, hipStream_t st) {
     const unsigned items = att_grid(att_slots(a.rows, a.n_seq, 64), a.kv, a.group);
-    const dim3 grid(items < 4 * NCU ? items : 4 * NCU), block(256);
+    const dim3 grid(items < 2 * NCU ? items : 2 * NCU), block(256);
     if (a.x_row) {
         if (a.causal) hipLaunchKernelGGL((attn_fwd_fine_kernel<DP, true, true>), grid, block, 0, st, a, (int)items);
         else hipLaunchKernelGGL((attn_fwd_fine_kernel<DP, true, false>), grid, block, 0, st, a, (int)items);

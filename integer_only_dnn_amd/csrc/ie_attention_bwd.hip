@@ -15,7 +15,9 @@
 // by the product of the norms), taken over the rows that meet in the sum, so
 // |A|, |B| <= 32512 and |C| <= 64 * 32512: two and three int8 digits.  C has
 // three, as it sums rows whose sizes differ most: with two, the bounds left it
-// a root mean square of four units.
+// a root mean square of four units.  Rows of fine weights (ie_attn.h) have theirs with
+// 2^14 in the place of 1 and 2^6, and so have the keys that share a sequence and
+// a key head with one: four digits, |n| <= 2^14 32512.
 #include "ie_attn.h"
 
 #pragma clang fp contract(off)
@@ -89,13 +91,14 @@ __global__ __launch_bounds__(256) void attn_scale_kernel(AttnArgs p, AttnBwd b) 
     const long long row = sp.a + t;
     const int e = clip_e(p.xe[p.x_row ? row : 0]), eo = clip_e(b.oe[row]), ed = b.dye[b.dy_row ? row : 0];
     const float down = pow2f(max(ed - o_top, -60)), r = p.c * pow2f(e);
-    int ka = -4096, kl = -4096;
+    int ka = -4096, kl = -4096, fine = 0;
     for (int g = 0; g < p.group; ++g) {
         const int h = it.kvh * p.group + g;
         const int2 d = b.dots[row * p.heads + h], st = p.stats[row * p.heads + h];
         const int delta = bits_of((uint32_t)abs(d.x)) + eo, rise = max(d.y + r_top, delta + e_top) + 1;
         AttnRow q;
         q.m = __int_as_float(st.x & ~1);  // its last bit: a row of fine weights
+        fine |= st.x & 1;
         q.r = r;
         q.dot = (float)d.x * pow2f(eo);
         q.a = (float)(1.0 / (double)(uint32_t)st.y) * down;  // a < 2^alpha
@@ -109,6 +112,38 @@ __global__ __launch_bounds__(256) void attn_scale_kernel(AttnArgs p, AttnBwd b) 
         kl = max(kl, alpha + e + max(d.y + n_top, delta) + 1);  // a |u| 2^e < 2^kl
     }
     b.key[(long long)it.kvh * p.rows + row] = AttnKey{(int16_t)ka, (int16_t)kl};
+    if (fine) atomicOr(p.flags + FINE_WORD, 1u);
+}
+
+// The largest bounds of all queries of a sequence (none: -4096 each), and of those that see
+// key kj of the tile of KEYS from k0 on.
+template <bool CAUSAL, int KEYS>
+__device__ __forceinline__ void key_bounds(const AttnKey *marks, int n, int k0, int kj, int (&sh)[2][4], AttnKey &all, AttnKey &seen) {
+    const int tid = threadIdx.x, lane = tid & 63;
+    AttnKey seen_later = ATT_NO_KEY;
+    all = ATT_NO_KEY;
+#pragma unroll 4
+    for (int t = tid; t < n; t += 256) {
+        const AttnKey x = marks[t];
+        all = __builtin_elementwise_max(all, x);
+        if (CAUSAL && t >= k0 + KEYS) seen_later = __builtin_elementwise_max(seen_later, x);
+    }
+    auto most = [](int x, int y) {
+        return __builtin_bit_cast(int, __builtin_elementwise_max(__builtin_bit_cast(AttnKey, x), __builtin_bit_cast(AttnKey, y)));
+    };
+    all = __builtin_bit_cast(AttnKey, row_reduce_once<256>(__builtin_bit_cast(int, all), most, sh[0]));
+    seen = all;
+    if (CAUSAL) {
+        // queries behind the tile, then those of the tile from the key's own on
+        int later = row_reduce_once<256>(__builtin_bit_cast(int, seen_later), most, sh[1]);
+        int own = lane < KEYS && k0 + lane < n ? __builtin_bit_cast(int, marks[k0 + lane]) : __builtin_bit_cast(int, ATT_NO_KEY);
+#pragma unroll
+        for (int o = 1; o < KEYS; o <<= 1) {
+            const int x = __shfl_down(own, o, 64);
+            own = lane + o < KEYS ? most(own, x) : own;
+        }
+        seen = __builtin_bit_cast(AttnKey, most(later, __shfl(own, kj - k0, 64)));
+    }
 }
 
 // dQ: a workgroup of four waves takes 64 queries of a head, 16 to a wave, one
@@ -261,31 +296,8 @@ __global__ __launch_bounds__(256, SPLIT == 2 ? 2 : DP > 64 ? 1 : SPLIT == 4 ? 2 
     head_regs<KS>(base + (long long)kj * p.width + (long long)(p.heads + it.kvh) * p.dp, ok, p.dp, lane, k);
     head_regs<KS>(base + (long long)kj * p.width + (long long)(p.heads + p.kv + it.kvh) * p.dp, ok, p.dp, lane, v);
     const float f = pow2f(clip_e(p.xe[p.x_row ? sp.a + min(kj, n - 1) : 0]));
-    // the largest bounds of all queries (none: -4096 each), and of those that see a key
-    const AttnKey *marks = bw.key + (long long)it.kvh * p.rows + sp.a;
-    AttnKey all = ATT_NO_KEY, seen, seen_later = ATT_NO_KEY;
-#pragma unroll 4
-    for (int t = tid; t < n; t += 256) {
-        const AttnKey x = marks[t];
-        all = __builtin_elementwise_max(all, x);
-        if (CAUSAL && t >= k0 + KEYS) seen_later = __builtin_elementwise_max(seen_later, x);
-    }
-    auto most = [](int x, int y) {
-        return __builtin_bit_cast(int, __builtin_elementwise_max(__builtin_bit_cast(AttnKey, x), __builtin_bit_cast(AttnKey, y)));
-    };
-    all = __builtin_bit_cast(AttnKey, row_reduce_once<256>(__builtin_bit_cast(int, all), most, smark[0]));
-    seen = all;
-    if (CAUSAL) {
-        // queries behind the tile, then those of the tile from the key's own on
-        int later = row_reduce_once<256>(__builtin_bit_cast(int, seen_later), most, smark[1]);
-        int own = lane < KEYS && k0 + lane < n ? __builtin_bit_cast(int, marks[k0 + lane]) : __builtin_bit_cast(int, ATT_NO_KEY);
-#pragma unroll
-        for (int o = 1; o < KEYS; o <<= 1) {
-            const int x = __shfl_down(own, o, 64);
-            own = lane + o < KEYS ? most(own, x) : own;
-        }
-        seen = __builtin_bit_cast(AttnKey, most(later, __shfl(own, kj - k0, 64)));
-    }
+    AttnKey all, seen;
+    key_bounds<CAUSAL, KEYS>(bw.key + (long long)it.kvh * p.rows + sp.a, n, k0, kj, smark, all, seen);
     const int whole = all[1], kappa = seen[0], lambda = max(seen[1] - whole, -96);
     const int o_top = bw.row[(long long)it.kvh * p.group * p.rows + sp.a].o_top;
     const float sv = pow2f(min(-kappa, 126)), sk = pow2f(min(6 - lambda, 126));
@@ -475,6 +487,215 @@ __global__ __launch_bounds__(256, SPLIT == 2 ? 2 : DP > 64 ? 1 : SPLIT == 4 ? 2 
     }
 }
 
+// The same with fine weights: dQ of the rows that the forward pass has marked, and dK
+// and dV of their sequences and key heads, in four digits (dV first, then dK: their
+// sums in the same registers), into the places that the kernels above have
+// filled.  A call without such a row ends at its first load.
+template <int DP>
+struct FineLds {
+    using T = HeadTile<DP>;
+    int8_t a[2][T::BYTES], b[2][T::BYTES];
+    float f[2][5][64];
+    int mark[2][4], any[4];
+};
+
+// Whether a thread of the workgroup says so; the workgroup's LDS is free behind it.
+__device__ __forceinline__ bool any_of(bool mine, int (&sh)[4]) {
+    const bool some = __ballot(mine) != 0;
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = some;
+    __syncthreads();
+    return sh[0] | sh[1] | sh[2] | sh[3];
+}
+
+template <int DP, bool CAUSAL>
+__device__ __forceinline__ void fine_dq(const AttnArgs &p, const AttnBwd &bw, int idx, FineLds<DP> &lds) {
+    using T = HeadTile<DP>;
+    constexpr int KS = T::KS, NE = DP / 16;
+    const int at = idx >> 3, pair = 8 * (at / p.group) + (idx & 7), kvh = pair % p.kv, h = kvh * p.group + at % p.group;
+    Span sp;
+    int tile;
+    if (!rank_tile<CAUSAL>(p, pair / p.kv, 64, sp, tile)) return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, quad = lane >> 4;
+    const int n = sp.n, q0 = 64 * tile, qi = q0 + 16 * wave + (lane & 15);
+    const long long row = sp.a + qi;
+    const bool fine = qi < n && (p.stats[row * p.heads + h].x & 1);
+    if (!any_of(fine, lds.any)) return;
+    const int8_t *base = p.x + (long long)sp.a * p.width;
+    const int8_t *kh = base + (long long)(p.heads + kvh) * p.dp, *vh = kh + (long long)p.kv * p.dp;
+    v4i q[KS], g[KS];
+    head_regs<KS>(base + (long long)qi * p.width + h * p.dp, qi < n, p.dp, lane, q);
+    head_regs<KS>(bw.dy + (row * p.heads + h) * p.dp, qi < n, p.dp, lane, g);
+    const AttnRow st = bw.row[(long long)h * p.rows + sp.a + min(qi, n - 1)];
+    const Poly scaled = poly(st.s);
+    const int keys = CAUSAL ? min(n, q0 + 64) : n, tiles = (keys + 63) / 64, lim = CAUSAL ? qi : n - 1;
+    T k, v;
+    k.init(p.width, p.dp);
+    v.init(p.width, p.dp);
+    float fe = 0.0f;
+    auto fetch = [&](int t) {
+        k.fetch(kh, p.width, 64 * t, keys, p.dp);
+        v.fetch(vh, p.width, 64 * t, keys, p.dp);
+        if (tid < 64) fe = pow2f(clip_e(p.xe[p.x_row ? sp.a + min(64 * t + tid, n - 1) : 0]));
+    };
+    v4i acc[4][NE] = {};
+    fetch(0);
+    for (int t = 0; t < tiles; ++t) {
+        const int buf = t & 1;
+        k.put(lds.a[buf]);
+        v.put(lds.b[buf]);
+        if (tid < 64) lds.f[buf][0][tid] = fe;
+        if (t + 1 < tiles) fetch(t + 1);
+        __syncthreads();
+        v4i dg[4];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+            v4i s = {0, 0, 0, 0}, dp = {0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < KS; ++i) {
+                s = mfma(T::frag_r(lds.a[buf], z, i, lane), q[i], s);
+                dp = mfma(T::frag_r(lds.b[buf], z, i, lane), g[i], dp);
+            }
+            int n4[4], o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float f = lds.f[buf][0][16 * z + 4 * quad + i];
+                float w = weight(__builtin_fmaf((float)s[i], f, -st.m), st.r, scaled);
+                w = 64 * t + 16 * z + 4 * quad + i <= lim ? w : 0.0f;
+                const float u = __builtin_fmaf((float)dp[i], f, -st.dot);
+                n4[i] = (int)__builtin_rintf(w * u * f * FINE_UNIT);
+            }
+            digits4x4(n4, o);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) dg[y][z] = o[y];
+        }
+#pragma unroll
+        for (int e = 0; e < NE; ++e) {
+            const v4i kt = T::frag_t(lds.a[buf], e, lane);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) acc[y][e] = mfma(kt, dg[y], acc[y][e]);
+        }
+    }
+    const double rate = p.scale / (double)(uint32_t)p.stats[(sp.a + min(qi, n - 1)) * (long long)p.heads + h].y;
+    double y[4 * NE];
+#pragma unroll
+    for (int e = 0; e < NE; ++e)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[4 * e + i] = whole4(acc[0][e][i], acc[1][e][i], acc[2][e][i], acc[3][e][i]) * rate;
+    store_odd(y, st.e - ATT_FINE, p.q, fine, p.d, lane, p.v16 + row * p.cols + h * p.d, p.p16 + row * p.parts + h);
+}
+
+template <int DP, bool CAUSAL>
+__device__ __forceinline__ void fine_dkv(const AttnArgs &p, const AttnBwd &bw, int idx, FineLds<DP> &lds) {
+    using T = HeadTile<DP>;
+    constexpr int KS = T::KS, NE = DP / 16;
+    const int kvh = idx % p.kv;
+    Span sp;
+    int tile;
+    if (!rank_tile<CAUSAL>(p, idx / p.kv, 64, sp, tile)) return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, quad = lane >> 4;
+    const int n = sp.n;
+    bool fine = false;
+    for (int t = tid; t < n; t += 256)
+        for (int g = 0; g < p.group; ++g) fine |= p.stats[(long long)(sp.a + t) * p.heads + kvh * p.group + g].x & 1;
+    if (!any_of(fine, lds.any)) return;
+    if (CAUSAL) tile = (n + 63) / 64 - 1 - tile;
+    const int k0 = 64 * tile, kj = k0 + 16 * wave + (lane & 15);
+    const bool ok = kj < n;
+    const int8_t *base = p.x + (long long)sp.a * p.width;
+    const long long row = sp.a + kj;
+    v4i k[KS], v[KS];
+    head_regs<KS>(base + (long long)kj * p.width + (long long)(p.heads + kvh) * p.dp, ok, p.dp, lane, k);
+    head_regs<KS>(base + (long long)kj * p.width + (long long)(p.heads + p.kv + kvh) * p.dp, ok, p.dp, lane, v);
+    const float f = pow2f(clip_e(p.xe[p.x_row ? sp.a + min(kj, n - 1) : 0]));
+    AttnKey all, seen;
+    key_bounds<CAUSAL, 64>(bw.key + (long long)kvh * p.rows + sp.a, n, k0, kj, lds.mark, all, seen);
+    const int whole = all[1], kappa = seen[0], lambda = max(seen[1] - whole, -96);
+    const int o_top = bw.row[(long long)kvh * p.group * p.rows + sp.a].o_top;
+    const int first = CAUSAL ? k0 / 64 : 0, tiles = (n + 63) / 64 - first, steps = tiles * p.group;
+    T q, g;
+    q.init(p.width, p.dp);
+    g.init(p.heads * p.dp, p.dp);
+    auto sweep = [&](auto of_k) {
+        const float unit = pow2f(min(ATT_FINE - (of_k.value ? lambda : kappa), 126));
+        AttnRow rec;
+        auto fetch = [&](int i) {
+            const int h = kvh * p.group + i / tiles, t = 64 * (first + i % tiles);
+            q.fetch(base + h * p.dp, p.width, t, n, p.dp);
+            g.fetch(bw.dy + ((long long)sp.a * p.heads + h) * p.dp, (long long)p.heads * p.dp, t, n, p.dp);
+            if (tid < 64) rec = bw.row[(long long)h * p.rows + sp.a + min(t + tid, n - 1)];
+        };
+        v4i acc[4][NE] = {};
+        fetch(0);
+        for (int i = 0; i < steps; ++i) {
+            const int buf = i & 1, i0 = 64 * (first + i % tiles);
+            q.put(lds.a[buf]);
+            g.put(lds.b[buf]);
+            if (tid < 64) {
+                lds.f[buf][0][tid] = rec.m;
+                lds.f[buf][1][tid] = rec.r;
+                lds.f[buf][2][tid] = rec.dot;
+                lds.f[buf][3][tid] = rec.a;
+                lds.f[buf][4][tid] = (float)((double)rec.a * pow2(rec.ek - whole));
+            }
+            if (i + 1 < steps) fetch(i + 1);
+            __syncthreads();
+            v4i dg[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+                v4i s = {0, 0, 0, 0}, dp = {0, 0, 0, 0};
+#pragma unroll
+                for (int c = 0; c < KS; ++c) {
+                    s = mfma(T::frag_r(lds.a[buf], z, c, lane), k[c], s);
+                    if (of_k.value) dp = mfma(T::frag_r(lds.b[buf], z, c, lane), v[c], dp);
+                }
+                int n4[4], o[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int j = 16 * z + 4 * quad + x, query = i0 + j;
+                    float w = weight(__builtin_fmaf((float)s[x], f, -lds.f[buf][0][j]), lds.f[buf][1][j]);
+                    w = query < n && (!CAUSAL || query >= kj) ? w : 0.0f;
+                    const float u = __builtin_fmaf((float)dp[x], f, -lds.f[buf][2][j]);
+                    n4[x] = (int)__builtin_rintf((of_k.value ? w * u * lds.f[buf][4][j] : w * lds.f[buf][3][j]) * unit);
+                }
+                digits4x4(n4, o);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) dg[y][z] = o[y];
+            }
+#pragma unroll
+            for (int e = 0; e < NE; ++e) {
+                const v4i xt = T::frag_t(of_k.value ? lds.a[buf] : lds.b[buf], e, lane);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) acc[y][e] = mfma(xt, dg[y], acc[y][e]);
+            }
+        }
+        double y[4 * NE];
+#pragma unroll
+        for (int e = 0; e < NE; ++e)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                y[4 * e + i] = whole4(acc[0][e][i], acc[1][e][i], acc[2][e][i], acc[3][e][i]);
+                if (of_k.value) y[4 * e + i] *= p.scale;
+            }
+        const int head = p.heads + kvh + (of_k.value ? 0 : p.kv), e = (of_k.value ? lambda + whole : kappa) + o_top - ATT_FINE;
+        store_odd(y, e, p.q, ok, p.d, lane, p.v16 + row * p.cols + head * p.d, p.p16 + row * p.parts + head);
+        __syncthreads();  // the tiles are read
+    };
+    sweep(Bool<false>{});
+    sweep(Bool<true>{});
+}
+
+template <int DP, bool CAUSAL>
+__global__ __launch_bounds__(256, DP > 64 ? 1 : 2) void attn_bwd_fine_kernel(AttnArgs p, AttnBwd bw, int of_q, int of_k) {
+    __shared__ __align__(16) FineLds<DP> lds;
+    if (!p.flags[FINE_WORD]) return;
+    for (int idx = blockIdx.x; idx < of_q + of_k; idx += gridDim.x) {
+        __syncthreads();
+        if (idx < of_k) fine_dkv<DP, CAUSAL>(p, bw, idx, lds);
+        else fine_dq<DP, CAUSAL>(p, bw, idx - of_k, lds);
+    }
+}
+
 template <int DP, int SPLIT>
 static void dq(AttnArgs a, const AttnBwd &b, hipStream_t st) {
     a.chunk = att_chunk(a, 64 / SPLIT, !a.causal);
@@ -517,6 +738,15 @@ static void dkv(const AttnArgs &a, const AttnBwd &b, hipStream_t st) {
     else dkv<DP, (DP > 64 ? 2 : 1)>(a, b, st);
 }
 
+template <int DP>
+static void bwd_fine(const AttnArgs &a, const AttnBwd &b, hipStream_t st) {
+    const long long slots = att_slots(a.rows, a.n_seq, 64);
+    const unsigned of_q = att_grid(slots, a.kv, a.group), of_k = (unsigned)(slots * a.kv), items = of_q + of_k;
+    const dim3 grid(items < 2 * NCU ? items : 2 * NCU), block(256);
+    if (a.causal) hipLaunchKernelGGL((attn_bwd_fine_kernel<DP, true>), grid, block, 0, st, a, b, (int)of_q, (int)of_k);
+    else hipLaunchKernelGGL((attn_bwd_fine_kernel<DP, false>), grid, block, 0, st, a, b, (int)of_q, (int)of_k);
+}
+
 hipError_t launch_attention_bwd(const AttnArgs &a, const AttnBwd &b, hipStream_t st) {
     const int nl = a.dp <= 16 ? 1 : a.dp <= 32 ? 2 : a.dp <= 64 ? 4 : 8;
     const long long items = (a.rows * (a.heads + a.kv) + 256 / nl - 1) / (256 / nl);
@@ -541,6 +771,12 @@ hipError_t launch_attention_bwd(const AttnArgs &a, const AttnBwd &b, hipStream_t
     else if (a.d <= 64) dkv<64>(a, b, st);
     else if (a.d <= 96) dkv<96>(a, b, st);
     else dkv<128>(a, b, st);
+    if (a.rows > ATT_CHECK) {
+        if (a.d <= 32) bwd_fine<32>(a, b, st);
+        else if (a.d <= 64) bwd_fine<64>(a, b, st);
+        else if (a.d <= 96) bwd_fine<96>(a, b, st);
+        else bwd_fine<128>(a, b, st);
+    }
     prof_end(st, PROF_ATT_DKV);
     const hipError_t e = hipGetLastError();
     return e != hipSuccess ? e : launch_attention_round(a, st);

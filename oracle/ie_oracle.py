@@ -953,12 +953,13 @@ def attention_bwd(X: QT, O: QT, dO: QT, tops, sums, heads: int, kv: int, d: int,
         for hk in range(kv):
             k, v = _att_head(X, heads + hk, d, a, b), _att_head(X, heads + kv + hk, d, a, b)
             nu = _norm_bits(v) + e
-            per = []
+            per, any_fine = [], False
             for h in range(hk * g, (hk + 1) * g):
                 q, dy, o = _att_head(X, h, d, a, b), _att_head(dO, h, d, a, b), _att_head(O, h, d, a, b)
                 t, see = _att_scores(q, k, e, causal)
                 total = sums[a:b, h].astype(np.float64)
-                m, _ = _att_marks(tops[a:b, h].copy())
+                m, fine = _att_marks(tops[a:b, h].copy())
+                any_fine |= bool(fine.any())
                 w = _att_weights(t, see, m, rate * np.ldexp(1.0, e))
                 dot = (dy * o).sum(axis=1)
                 u = _f32(np.ldexp(_exact_matmul(dy, v.T).astype(np.float64), e[None, :])
@@ -966,8 +967,9 @@ def attention_bwd(X: QT, O: QT, dO: QT, tops, sums, heads: int, kv: int, d: int,
                 s = _f32(w * u)
                 delta, size = _bitlen_np(np.abs(dot)) + eo, _norm_bits(dy)
                 sigma = np.maximum(size + (nu + e).max(), delta + e.max()) + 1
-                num = np.rint(np.ldexp(s, e[None, :] - sigma[:, None])) @ k.astype(np.float64)
-                y[a:b, h * d:(h + 1) * d] = np.ldexp(num * (scale / total)[:, None], (sigma + ed)[:, None])
+                more = ATT_FINE * fine
+                num = np.rint(np.ldexp(s, e[None, :] + (more - sigma)[:, None])) @ k.astype(np.float64)
+                y[a:b, h * d:(h + 1) * d] = np.ldexp(num * (scale / total)[:, None], (sigma - more + ed)[:, None])
                 share = np.ldexp(_f32(1.0 / total), np.maximum(ed - most, -60))
                 alpha = np.frexp(share)[1].astype(np.int64)
                 per.append((q, dy, w, s, share, alpha, alpha + e + np.maximum(size + nu.max(), delta) + 1))
@@ -975,13 +977,14 @@ def attention_bwd(X: QT, O: QT, dO: QT, tops, sums, heads: int, kv: int, d: int,
             lam = np.max([_reach(z[6], causal) for z in per], axis=0)
             whole = int(max(z[6].max() for z in per))
             lam = np.maximum(lam - whole, -96)
+            of_v, of_k = (ATT_FINE, ATT_FINE) if any_fine else (0, 6)  # bits behind the units of dV's and dK's integers
             dk, dv = np.zeros((b - a, d)), np.zeros((b - a, d))
             for q, dy, w, s, share, _, _ in per:
-                dv += np.rint(np.ldexp(_f32(w * share[:, None]), -kappa[None, :])).T @ dy.astype(np.float64)
+                dv += np.rint(np.ldexp(_f32(w * share[:, None]), of_v - kappa[None, :])).T @ dy.astype(np.float64)
                 bi = _f32(np.ldexp(share, e - whole))
-                dk += np.rint(np.ldexp(_f32(s * bi[:, None]), 6 - lam[None, :])).T @ q.astype(np.float64)
-            y[a:b, (heads + hk) * d:(heads + hk + 1) * d] = np.ldexp(dk * scale, (lam - 6 + whole + most)[:, None])
-            y[a:b, (heads + kv + hk) * d:(heads + kv + hk + 1) * d] = np.ldexp(dv, (kappa + most)[:, None])
+                dk += np.rint(np.ldexp(_f32(s * bi[:, None]), of_k - lam[None, :])).T @ q.astype(np.float64)
+            y[a:b, (heads + hk) * d:(heads + hk + 1) * d] = np.ldexp(dk * scale, (lam - of_k + whole + most)[:, None])
+            y[a:b, (heads + kv + hk) * d:(heads + kv + hk + 1) * d] = np.ldexp(dv, (kappa - of_v + most)[:, None])
     return requant_f64(y, ROW, bits)
 
 

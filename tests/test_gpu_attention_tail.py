@@ -125,3 +125,51 @@ def test_captured_and_replayed():
         graph.replay()
         assert_rows(O, wants[turn], (0, n), f"input {turn}")
     assert int(ws.buf[4:256].sum()) == 0 and ws.status() == 0
+
+
+def gradient(X, heads, kv, d, scale, causal, offsets, seed=0):
+    rng = np.random.default_rng(seed)
+    rows, ws = X.mant.shape[0], ie.Workspace("cuda")
+    want, m, L = o.attention_fwd(X, heads, kv, d, scale, causal, offsets)
+    dO = o.QT(rng.integers(-128, 128, (rows, heads * d)).astype(np.int8), rng.integers(-16, -11, rows).astype(np.int8), o.ROW)
+    wantG = o.attention_bwd(X, want, dO, m, L, heads, kv, d, scale, causal, offsets)
+    covered = (0, rows) if offsets is None else (offsets[0], offsets[-1])
+    ws.get(1 << 16)
+    ws.buf[256:].fill_(0x5a)
+    att, Xd, Yd = ie.Attention(heads, kv, d, scale, causal, None if offsets is None else dev_i32(offsets)), to_dev(X), to_dev(dO)
+    O, stats, G = filled(rows, heads * d), stats_of(rows, heads), filled(rows, (heads + 2 * kv) * d)
+    ie.ie_attention_fwd(att, Xd, O, ws, stats)
+    for turn in range(2):
+        ie.ie_attention_bwd(att, Xd, O, Yd, stats, G, ws)
+        assert_rows(G, wantG, covered, f"dQKV {turn}")
+    assert ws.status() == 0 and int(ws.buf[4:256].sum()) == 0
+    return marks(m)
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("n,gap,lift,group", [(2033, 10.6, 0, o.ROW), (2200, 12.0, 3, o.ROW), (2100, 11.0, 0, o.TENSOR)])
+def test_gradient_of_sinks(n, gap, lift, group, causal):
+    announce(f"attention tail gradient {n} {gap} {lift} {group} {causal}")
+    X, scale = sink(np.random.default_rng(n), n, gap, lift=lift, mean=10.0, group=group)
+    assert gradient(X, 1, 1, 16, scale, causal, None).any()
+
+
+@pytest.mark.parametrize("heads,kv,d", [(2, 1, 7), (1, 1, 40), (3, 3, 64), (2, 1, 80), (2, 2, 96), (4, 1, 128), (16, 1, 33)])
+def test_gradient_heads(heads, kv, d):
+    announce(f"attention tail gradient heads {heads} {kv} {d}")
+    X, scale = sink(np.random.default_rng(d), 2064, 10.8, heads, kv, d, lift=1, flat_rows=True)
+    assert gradient(X, heads, kv, d, scale, heads % 2 == 0, None).any()
+
+
+@pytest.mark.parametrize("causal", [False, True])
+def test_gradient_packed(causal):
+    """Sequences with and without such rows, one key head with and one without them; rows of none."""
+    announce(f"attention tail gradient packed {causal}")
+    rng = np.random.default_rng(6)
+    a, scale = sink(rng, 2100, 11.0, 4, 2, 32)
+    flat = qkv(rng, 2050, 4, 2, 32, elo=-9, ehi=-9)
+    a.mant[:, 2 * 32:4 * 32] = flat.mant[:1, 2 * 32:4 * 32] // 16  # the second key head's queries: all scores alike
+    few = [qkv(rng, t, 4, 2, 32) for t in (2, 65, 3)]
+    X = packed([few[0], a, few[1], flat, few[2]])
+    fine = gradient(X, 4, 2, 32, scale, causal, [2, 2102, 2167, 4217])
+    assert fine[2034:2102, :2].all() and not fine[:, 2:].any() and not fine[2102:].any()

@@ -3,6 +3,7 @@ softmax in 64 bits."""
 
 import numpy as np
 import pytest
+import torch
 
 import oracle as o
 from tests.attention_tail import marks, sink
@@ -62,3 +63,48 @@ def test_rows_of_few_keys_stay_coarse():
     t = (X.mant[:, :16].astype(float) @ X.mant[:, 16:32].astype(float).T) * 2.0 ** (2 * int(X.exp[0])) * scale
     den = np.exp(t - t.max(axis=1, keepdims=True)).sum(axis=1) * o.ATT_UNIT
     assert np.all(np.abs(sums[:, 0] - den) <= den * (W_ERR + 1e-5) + o.ATT_UNIT / 32)
+
+
+def backward_tolerances(X, O, dO, o64, p, v, k, q, L, fine, scale, d):
+    """Elementwise bounds of the errors of dQ, dK, dV of one head over one sequence, before the last rounding: weights off by W_ERR
+    relative twice and by half a unit of L (and by its rounding to whole units), D from the rounded O, fp32 roundings, and half a
+    unit of every integer that enters a sum."""
+    n, small = p.shape[0], 2.0 ** -o.ATT_FINE
+    e, ed = X.row_exp(), dO.row_exp()
+    dy, unit = values(dO), np.where(fine, small, 1.0)
+    dD = (np.abs(dy) * np.abs(values(O) - o64)).sum(axis=1)
+    dP = dy @ v.T
+    mean = (p * dP).sum(axis=1, keepdims=True)
+    big = np.abs(dP) + np.abs(mean)
+    perr = p * (2 * W_ERR + (0.5 * n * unit / L)[:, None] + (0.5 / L)[:, None] + 2.0 ** -22)
+    serr = perr * big + (p + perr) * (dD[:, None] + 2.0 ** -22 * big)
+    dq, dk, dv = scale * serr @ np.abs(k), scale * serr.T @ np.abs(q), perr.T @ np.abs(dy)
+    # the integers' scales: powers of two at most 2^2 times the norms' products they stand for
+    vn, dn = 2 * np.linalg.norm(v, axis=1).max(), 2 * np.linalg.norm(dy, axis=1)
+    dot = 2 * np.abs((dy * values(O)).sum(axis=1))
+    top = 2 * np.maximum(dn * vn, dot) * 127 * np.ldexp(1.0, int(e.max()))
+    dq += (scale * 0.5 * top * unit * n / L)[:, None]
+    am = (2.0 ** np.maximum(ed - ed.max(), -60) / L).max() * 2 * 2.0 ** ed.max()
+    dv += 0.5 * am * small * np.abs(dO.mant.astype(np.float64)).max() * n
+    lm = (2.0 ** np.maximum(ed - ed.max(), -60) / L * 4 * np.maximum(dn / 2.0 ** ed * vn, dot / 2.0 ** ed) * 2.0 ** e).max() * 2.0 ** ed.max()
+    dk += scale * 0.5 * lm * small * 127 * n
+    return dq, dk, dv
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("n,gap,lift,mean", [(3000, 10.6, 0, 0.0), (2600, 10.5, 2, 0.0), (2600, 12.0, 0, 20.0)])
+def test_gradient_keeps_the_tail(n, gap, lift, mean, causal):
+    rng = np.random.default_rng(int(10 * gap) + lift)
+    X, scale = sink(rng, n, gap, lift=lift, mean=mean)
+    O, tops, sums = o.attention_fwd(X, 1, 1, 16, scale, causal, [0, n])
+    dO = o.QT(np.clip(np.rint(rng.normal(10, 40, (n, 16))), -127, 127).astype(np.int8), rng.integers(-16, -13, n).astype(np.int8), o.ROW)
+    G = values(o.attention_bwd(X, O, dO, tops, sums, 1, 1, 16, scale, causal, [0, n]))
+    x, y, ((_, _, p, v, k, q),) = softmax64(X, 1, 1, 16, scale, causal, [0, n])
+    want = torch.autograd.grad((y * torch.from_numpy(values(dO))).sum(), x)[0].numpy()
+    tol = np.concatenate(backward_tolerances(X, O, dO, y.detach().numpy(), p[0], v[0], k[0], q[0], sums[:, 0].astype(np.float64),
+                                             marks(tops)[:, 0], scale, 16), axis=1)
+    half = 0.5 * np.ldexp(1.0, o.requant_f64(G, o.ROW).row_exp())[:, None]
+    assert np.all(np.abs(G - want) <= tol + half)
+    # most of a token's dV is not rounding: with one digit less it is nothing at all
+    size = np.abs(want[:, 32:]).max(axis=1)
+    assert np.median((tol[:, 32:].max(axis=1) / size)[1:o.ATT_CHECK]) < 0.25
