@@ -57,8 +57,9 @@ __global__ __launch_bounds__(256) void cache_store_kernel(CacheArgs p, long long
 // a block enters the whole with the weight of its maximum, another such
 // integer: a_b = W(m_b - m),  L = sum R(a_b) L_b,  E = max E_b,
 //   o = (sum R(a_b 2^(E_b - E)) N_b) (1 / L) 2^E.
-// All sums are exact (below 2^53), so that how blocks are shared out is of no
-// account, and each key and value is read once.
+// All sums are exact (in 64 bits: 2^23 keys with values of 8 units come to 32512^2 2^26 <
+// 2^56), so that how blocks are shared out is of no account, and each key and
+// value is read once.
 //
 // A workgroup takes a block of one key head and up to 16 of its query heads,
 // a wave 64 of the keys: 16x16x64 products with the keys along the rows and
@@ -363,8 +364,8 @@ __global__ __launch_bounds__(256, 4) void cache_attention_kernel(CacheArgs p, At
 // 9.6 for one of 131072.
 __global__ __launch_bounds__(256) void cache_join_kernel(CacheArgs p, AttnArgs a, int piece) {
     __shared__ int sh[4];
-    __shared__ float sw[256];
-    __shared__ double sp[256][4], sden[4];
+    __shared__ int sw[256];
+    __shared__ long long sp[256][4], sden[4];
     const int pieces = a.d / piece, tid = threadIdx.x;
     const int part_of = blockIdx.x % (a.heads * pieces), seq = blockIdx.x / (a.heads * pieces), head = part_of / pieces;
     const int len = min(max(p.lengths[seq], 0), p.tokens), nb = (len + 255) >> 8;
@@ -387,17 +388,17 @@ __global__ __launch_bounds__(256) void cache_join_kernel(CacheArgs p, AttnArgs a
     m = __int_as_float(best >= 0 ? best : best ^ 0x7fffffff);
     const float r = a.c * pow2f(clip_e(a.xe[a.x_row ? seq : 0]));
     const int quads = piece >> 2, parts = 256 / quads, part = tid / quads, e = 4 * (tid - part * quads);
-    double s[4] = {0, 0, 0, 0}, den = 0.0;
+    long long s[4] = {0, 0, 0, 0}, den = 0;
     for (int b0 = 0; b0 < nb; b0 += 256) {
         const int nc = min(256, nb - b0);
         __syncthreads();
         if (tid < nc) {
             const int4 t = top[(long long)(b0 + tid) * a.heads];
-            float w = 0.0f;
+            int w = 0;
             if (t.y) {
                 const float x = weight(__int_as_float(t.x) - m, r);
-                den += (double)(x + RINT_MAGIC - RINT_MAGIC) * (double)t.y;
-                w = __builtin_fmaf(x, pow2f(t.z - em), RINT_MAGIC) - RINT_MAGIC;
+                den += (long long)(int)__builtin_rintf(x) * t.y;
+                w = (int)__builtin_rintf(x * pow2f(t.z - em));
             }
             sw[tid] = w;
         }
@@ -407,24 +408,24 @@ __global__ __launch_bounds__(256) void cache_join_kernel(CacheArgs p, AttnArgs a
             for (int b = part; b < nc; b += parts) {
                 int4 x;
                 __builtin_memcpy(&x, num + (long long)(b0 + b) * a.cols + e, 16);
-                const double w = (double)sw[b];
-                s[0] = __builtin_fma(w, (double)x.x, s[0]);
-                s[1] = __builtin_fma(w, (double)x.y, s[1]);
-                s[2] = __builtin_fma(w, (double)x.z, s[2]);
-                s[3] = __builtin_fma(w, (double)x.w, s[3]);
+                const long long w = sw[b];
+                s[0] += w * x.x;
+                s[1] += w * x.y;
+                s[2] += w * x.z;
+                s[3] += w * x.w;
             }
         }
     }
-    // exact sums below 2^53, in any order
 #pragma unroll
     for (int k = 0; k < 4; ++k) sp[tid][k] = s[k];
     den = row_reduce<256>(den, Add{}, sden);
     __syncthreads();
     double y = 0.0;
     if (tid < piece) {
+        long long sum = 0;
 #pragma unroll 8
-        for (int i = 0; i < parts; ++i) y += sp[i * quads + (tid >> 2)][tid & 3];
-        y = den > 0.0 ? y * (1.0 / den) : 0.0;
+        for (int i = 0; i < parts; ++i) sum += sp[i * quads + (tid >> 2)][tid & 3];
+        y = den > 0 ? (double)sum * (1.0 / (double)den) : 0.0;
     }
     const int need = need_word(row_reduce<256>(__double2hiint(y) & 0x7fffffff, Max{}, sh), a.q);
     const long long at = (long long)seq * a.heads * pieces + part_of;

@@ -81,6 +81,10 @@ template <int CTRL>
 __device__ __forceinline__ double dpp_of(double v) {
     return __hiloint2double(dpp_of<CTRL>(__double2hiint(v)), dpp_of<CTRL>(__double2loint(v)));
 }
+template <int CTRL>
+__device__ __forceinline__ long long dpp_of(long long v) {
+    return (long long)dpp_of<CTRL>((int)(v >> 32)) << 32 | (uint32_t)dpp_of<CTRL>((int)v);
+}
 
 // f over a lane and its partner 16 (or 32) lanes away: swapping the odd rows
 // of one copy with the even rows of another leaves both partners' values.
@@ -98,6 +102,12 @@ __device__ __forceinline__ double swap_reduce(double v, F f) {
     const auto b = D == 16 ? __builtin_amdgcn_permlane16_swap(l, l, false, false)
                            : __builtin_amdgcn_permlane32_swap(l, l, false, false);
     return f(__hiloint2double((int)a[0], (int)b[0]), __hiloint2double((int)a[1], (int)b[1]));
+}
+template <int D, class F>
+__device__ __forceinline__ long long swap_reduce(long long v, F f) {
+    return __double_as_longlong(swap_reduce<D>(__longlong_as_double(v), [f](double a, double b) {
+        return __longlong_as_double(f(__double_as_longlong(a), __double_as_longlong(b)));
+    }));
 }
 
 // A sum or maximum over groups of T <= 64 lanes, in every lane of the group

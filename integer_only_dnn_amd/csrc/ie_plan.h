@@ -478,7 +478,7 @@ size_t rope_ws(long long rows, long long cols);
 
 // Attention over a cache: blocks of keys with a maximum of their own.
 constexpr int CACHE_BLOCK = 256;
-constexpr long long CACHE_TOKENS_MAX = 1ll << 23;  // sums of weighted blocks stay below 2^53
+constexpr long long CACHE_TOKENS_MAX = 1ll << 23;  // the weights' sum stays below 2^53, values' below 2^56
 struct CacheWs {
     int *num;
     void *top;  // 16 bytes a block and head

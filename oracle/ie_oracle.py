@@ -1047,6 +1047,17 @@ def cache_store(cache: dict, X: QT, heads: int, kv: int, d: int, slots) -> None:
             cache[name][at, h], cache[name + "e"][at, h] = pack4(c), ex
 
 
+def cache_join(parts, r) -> tuple:
+    """Blocks (m_b, L_b, E_b, N_b) of one head together: (sum of weights, sums of values, E), whole numbers."""
+    m, top = max(z[0] for z in parts), max(z[2] for z in parts)
+    w = softmax_weight(_f32(np.array([z[0] for z in parts]) - m), r)
+    x = np.rint(np.ldexp(w, np.array([z[2] for z in parts]) - top)).astype(np.int64)
+    total = np.rint(w).astype(np.int64) @ np.array([z[1] for z in parts], dtype=np.int64)
+    nums = np.array([z[3] for z in parts], dtype=np.int64)
+    assert float(np.abs(x) @ np.abs(nums).max(axis=1).astype(np.float64)) < 2.0 ** 62
+    return total, x @ nums, top
+
+
 def attention_cache(Q: QT, cache: dict, slots, heads: int, kv: int, d: int, scale: float, bits: int = Q_BITS) -> QT:
     """One query a row; slots[i]: the cache slots of row i's keys, in order (-1: left out)."""
     g, rate = heads // kv, _att_rate(scale)
@@ -1071,13 +1082,8 @@ def attention_cache(Q: QT, cache: dict, slots, heads: int, kv: int, d: int, scal
                 parts.append((t.max(), np.rint(w).sum(), int(ve.max()), num))
             if not parts:
                 continue
-            m, top = max(z[0] for z in parts), max(z[2] for z in parts)
-            total, num = 0.0, np.zeros(d)
-            for mb, lb, eb, nb in parts:
-                w = softmax_weight(_f32(mb - m), r)
-                total += np.rint(w) * lb
-                num += np.rint(np.ldexp(w, eb - top)) * nb
-            y[i, h * d:(h + 1) * d] = np.ldexp(num * (1.0 / total), top)
+            total, num, top = cache_join(parts, r)
+            y[i, h * d:(h + 1) * d] = np.ldexp(num.astype(np.float64) * (1.0 / np.float64(total)), top)
     return requant_f64(y, ROW, bits)
 
 
