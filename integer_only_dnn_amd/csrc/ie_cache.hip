@@ -10,6 +10,7 @@
 
 namespace ie {
 
+constexpr int CACHE_CHECK = 8;  // blocks whose weights are rounded without a check
 constexpr int STORE_ROWS = 4096;  // numbers of a chunk's heads fit 30 bits
 
 // One key or value head of a row: NL lanes with 16 mantissas each.  8192 rows of 8
@@ -56,7 +57,8 @@ __global__ __launch_bounds__(256) void cache_store_kernel(CacheArgs p, long long
 //   L_b = sum R(w_j),  N_b = sum R(w_j 2^(ev_j - E_b)) v_j;
 // a block enters the whole with the weight of its maximum, another such
 // integer: a_b = W(m_b - m),  L = sum R(a_b) L_b,  E = max E_b,
-//   o = (sum R(a_b 2^(E_b - E)) N_b) (1 / L) 2^E.
+//   o = (sum R(a_b 2^(E_b - E)) N_b) (1 / L) 2^E
+// (in finer units where that rounding takes too much, see cache_join_kernel).
 // All sums are exact (in 64 bits: 2^23 keys with values of 8 units come to 32512^2 2^26 <
 // 2^56), so that how blocks are shared out is of no account, and each key and
 // value is read once.
@@ -362,10 +364,17 @@ __global__ __launch_bounds__(256, 4) void cache_attention_kernel(CacheArgs p, At
 // four neighbouring elements add up a share of the blocks each.  Bound by its few
 // round trips to memory: 8.7 us for the 21 MB of 48 sequences of up to 8000 tokens,
 // 9.6 for one of 131072.
+//
+// Fine weights, as in attention over a prompt: a block's weight takes half a unit of
+// its sums at most, of eight blocks (the largest's weight is exact) less than 7 * 128 /
+// 32512 = 1 / 36 in all.  With more of them the weights' sum is taken in units of 2^-6 too;
+// where that changes it by more than a 32nd, or where none of 16 neighbouring
+// elements reaches half a unit of all blocks' sums of weights with values of 8, these
+// elements are summed again with 2^14 units to one, in two halves of the weights.
 __global__ __launch_bounds__(256) void cache_join_kernel(CacheArgs p, AttnArgs a, int piece) {
     __shared__ int sh[4];
     __shared__ int sw[256];
-    __shared__ long long sp[256][4], sden[4];
+    __shared__ long long sp[256][4], sn[3][4];
     const int pieces = a.d / piece, tid = threadIdx.x;
     const int part_of = blockIdx.x % (a.heads * pieces), seq = blockIdx.x / (a.heads * pieces), head = part_of / pieces;
     const int len = min(max(p.lengths[seq], 0), p.tokens), nb = (len + 255) >> 8;
@@ -388,46 +397,76 @@ __global__ __launch_bounds__(256) void cache_join_kernel(CacheArgs p, AttnArgs a
     m = __int_as_float(best >= 0 ? best : best ^ 0x7fffffff);
     const float r = a.c * pow2f(clip_e(a.xe[a.x_row ? seq : 0]));
     const int quads = piece >> 2, parts = 256 / quads, part = tid / quads, e = 4 * (tid - part * quads);
-    long long s[4] = {0, 0, 0, 0}, den = 0;
-    for (int b0 = 0; b0 < nb; b0 += 256) {
-        const int nc = min(256, nb - b0);
-        __syncthreads();
-        if (tid < nc) {
-            const int4 t = top[(long long)(b0 + tid) * a.heads];
-            int w = 0;
-            if (t.y) {
-                const float x = weight(__int_as_float(t.x) - m, r);
-                den += (long long)(int)__builtin_rintf(x) * t.y;
-                w = (int)__builtin_rintf(x * pow2f(t.z - em));
+    // one element's sum over the blocks (threads past the piece: 0), and sums of a thread's numbers of its blocks
+    auto join = [&](auto weigh, long long (&n)[3]) {
+        long long s[4] = {0, 0, 0, 0};
+        n[0] = n[1] = n[2] = 0;
+        for (int b0 = 0; b0 < nb; b0 += 256) {
+            const int nc = min(256, nb - b0);
+            __syncthreads();
+            if (tid < nc) {
+                const int4 t = top[(long long)(b0 + tid) * a.heads];
+                sw[tid] = t.y ? weigh(weight(__int_as_float(t.x) - m, r), pow2f(t.z - em), t.y, n) : 0;
             }
-            sw[tid] = w;
-        }
-        __syncthreads();
-        if (part < parts) {
+            __syncthreads();
+            if (part < parts) {
 #pragma unroll 4
-            for (int b = part; b < nc; b += parts) {
-                int4 x;
-                __builtin_memcpy(&x, num + (long long)(b0 + b) * a.cols + e, 16);
-                const long long w = sw[b];
-                s[0] += w * x.x;
-                s[1] += w * x.y;
-                s[2] += w * x.z;
-                s[3] += w * x.w;
+                for (int b = part; b < nc; b += parts) {
+                    int4 x;
+                    __builtin_memcpy(&x, num + (long long)(b0 + b) * a.cols + e, 16);
+                    const long long w = sw[b];
+                    s[0] += w * x.x;
+                    s[1] += w * x.y;
+                    s[2] += w * x.z;
+                    s[3] += w * x.w;
+                }
             }
         }
-    }
+        __syncthreads();
 #pragma unroll
-    for (int k = 0; k < 4; ++k) sp[tid][k] = s[k];
-    den = row_reduce<256>(den, Add{}, sden);
-    __syncthreads();
-    double y = 0.0;
-    if (tid < piece) {
+        for (int k = 0; k < 4; ++k) sp[tid][k] = s[k];
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            n[k] = lane_reduce<64>(n[k], Add{});
+            if ((tid & 63) == 0) sn[k][tid >> 6] = n[k];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 3; ++k) n[k] = sn[k][0] + sn[k][1] + sn[k][2] + sn[k][3];
         long long sum = 0;
+        if (tid < piece) {
 #pragma unroll 8
-        for (int i = 0; i < parts; ++i) sum += sp[i * quads + (tid >> 2)][tid & 3];
-        y = den > 0 ? (double)sum * (1.0 / (double)den) : 0.0;
+            for (int i = 0; i < parts; ++i) sum += sp[i * quads + (tid >> 2)][tid & 3];
+        }
+        return sum;
+    };
+    long long n[3];  // the weights' sum, what rounding took of it in units of 2^-6, the sum of the blocks' own sums
+    const long long sum = join([](float x, float f, int l, long long (&n)[3]) {
+        const int w = (int)__builtin_rintf(x);
+        n[0] += (long long)w * l;
+        n[1] += (long long)((int)__builtin_rintf(x * 64.0f) - 64 * w) * l;
+        n[2] += l;
+        return (int)__builtin_rintf(x * f);
+    }, n);
+    double y = n[0] > 0 ? (double)sum * (1.0 / (double)n[0]) : 0.0;
+    const long long big = lane_reduce<16>(sum < 0 ? -sum : sum, [](long long x, long long z) { return x > z ? x : z; });
+    const bool fine = nb > CACHE_CHECK && n[0] > 0 && ((n[1] < 0 ? -n[1] : n[1]) > 2 * n[0] || big < 4 * n[2]) && tid < piece;
+    constexpr int SOME = 0x7fffffff;  // no result has such a high word
+    int word = row_reduce<256>(fine ? SOME : __double2hiint(y) & 0x7fffffff, Max{}, sh);
+    if (word == SOME) {
+        long long hi_n[3], lo_n[3];
+        const long long hi = join([](float x, float f, int l, long long (&n)[3]) {
+            n[0] += (long long)((int)__builtin_rintf(x * FINE_UNIT) >> 15) * l;
+            return (int)__builtin_rintf(x * f * FINE_UNIT) >> 15;
+        }, hi_n);
+        const long long lo = join([](float x, float f, int l, long long (&n)[3]) {
+            n[0] += (long long)((int)__builtin_rintf(x * FINE_UNIT) & 32767) * l;
+            return (int)__builtin_rintf(x * f * FINE_UNIT) & 32767;
+        }, lo_n);
+        if (fine) y = ((double)hi * 32768.0 + (double)lo) * (1.0 / ((double)hi_n[0] * 32768.0 + (double)lo_n[0]));
+        word = row_reduce<256>(__double2hiint(y) & 0x7fffffff, Max{}, sh);
     }
-    const int need = need_word(row_reduce<256>(__double2hiint(y) & 0x7fffffff, Max{}, sh), a.q);
+    const int need = need_word(word, a.q);
     const long long at = (long long)seq * a.heads * pieces + part_of;
     if (tid == 0) a.p16[at] = (int16_t)(need == NEED_NONE ? P_NONE : need + em);
     if (tid < piece) {

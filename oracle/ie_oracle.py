@@ -1047,15 +1047,36 @@ def cache_store(cache: dict, X: QT, heads: int, kv: int, d: int, slots) -> None:
             cache[name][at, h], cache[name + "e"][at, h] = pack4(c), ex
 
 
-def cache_join(parts, r) -> tuple:
-    """Blocks (m_b, L_b, E_b, N_b) of one head together: (sum of weights, sums of values, E), whole numbers."""
+CACHE_CHECK = 8          # blocks that are joined without a check of what rounding their weights takes
+
+
+def cache_join(parts, r, blocks: int = 0) -> np.ndarray:
+    """Blocks (m_b, L_b, E_b, N_b) of one head together, `blocks` with those that hold no key: its result in units of 2^E."""
+    return _cache_result(*cache_sums(parts, r), blocks)
+
+
+def cache_sums(parts, r) -> tuple:
+    """(sum of weights, sums of values, the same of the weights in units of 2^-6, sum of L_b, of fine weights and values, in two
+    halves at bit 15): whole numbers below 2^62."""
     m, top = max(z[0] for z in parts), max(z[2] for z in parts)
-    w = softmax_weight(_f32(np.array([z[0] for z in parts]) - m), r)
-    x = np.rint(np.ldexp(w, np.array([z[2] for z in parts]) - top)).astype(np.int64)
-    total = np.rint(w).astype(np.int64) @ np.array([z[1] for z in parts], dtype=np.int64)
-    nums = np.array([z[3] for z in parts], dtype=np.int64)
-    assert float(np.abs(x) @ np.abs(nums).max(axis=1).astype(np.float64)) < 2.0 ** 62
-    return total, x @ nums, top
+    a = softmax_weight(_f32(np.array([z[0] for z in parts]) - m), r)
+    x = np.ldexp(a, np.array([z[2] for z in parts]) - top)
+    lb, nb = np.array([z[1] for z in parts], dtype=np.int64), np.array([z[3] for z in parts], dtype=np.int64)
+    whole = lambda z, s: np.rint(np.ldexp(z, s)).astype(np.int64)  # noqa: E731
+    assert len(parts) <= 1 << 15 and lb.max() <= 256 * ATT_UNIT and np.abs(nb).max() <= 8 * 256 * ATT_UNIT
+    halves = [(f(whole(a, ATT_FINE)) @ lb, f(whole(x, ATT_FINE)) @ nb) for f in (lambda z: z >> 15, lambda z: z & 32767)]
+    return whole(a, 0) @ lb, whole(x, 0) @ nb, whole(a, 6) @ lb, lb.sum(), halves
+
+
+def _cache_result(total, num, sixth, every, halves, blocks) -> np.ndarray:
+    y = num.astype(np.float64) * (1.0 / np.float64(total))
+    if blocks <= CACHE_CHECK:
+        return y
+    big = np.abs(num).reshape(-1, 16).max(axis=1).repeat(16)
+    fine = (np.abs(sixth - 64 * total) > 2 * total) | (big < 4 * every)
+    (d_hi, hi), (d_lo, lo) = halves
+    den = np.float64(d_hi) * 32768.0 + np.float64(d_lo)
+    return np.where(fine, (hi.astype(np.float64) * 32768.0 + lo.astype(np.float64)) * (1.0 / den), y)
 
 
 def attention_cache(Q: QT, cache: dict, slots, heads: int, kv: int, d: int, scale: float, bits: int = Q_BITS) -> QT:
@@ -1082,8 +1103,8 @@ def attention_cache(Q: QT, cache: dict, slots, heads: int, kv: int, d: int, scal
                 parts.append((t.max(), np.rint(w).sum(), int(ve.max()), num))
             if not parts:
                 continue
-            total, num, top = cache_join(parts, r)
-            y[i, h * d:(h + 1) * d] = np.ldexp(num.astype(np.float64) * (1.0 / np.float64(total)), top)
+            out = cache_join(parts, r, -(-len(row) // CACHE_BLOCK))
+            y[i, h * d:(h + 1) * d] = np.ldexp(out, max(z[2] for z in parts))
     return requant_f64(y, ROW, bits)
 
 

@@ -69,3 +69,48 @@ def test_many_blocks_of_values_that_cancel(n, heads, d):
     m, e = from_dev(O)
     for at, row in enumerate([0, n - 1] if n > 1 else [0]):
         assert e[row] == want.exp[at] and np.array_equal(m[row], want.mant[at]), row
+
+
+def sinks(rng, n, gap, heads, kv, d, page, spread):
+    """A cache whose first key is `gap` nats ahead of the others for every head, its value zero; pages out of order."""
+    pages = -(-n // page) + 2
+    k, v = rng.integers(-1, 2, (pages, page, kv, d)), np.clip(np.rint(rng.normal(1, 3, (pages, page, kv, d))), -7, 7).astype(int)
+    k[..., 0] = 0
+    order = rng.permutation(pages)[:-(-n // page)]
+    ke, ve = np.full((pages, page, kv), -6), rng.integers(-2 - spread, -1, (pages, page, kv))
+    k[order[0], 0], v[order[0], 0] = 0, 0
+    k[order[0], 0, :, 0] = 7
+    ke[order[0], 0], ve[order[0], 0] = 0, -128
+    Q = rng.integers(-60, 61, (1, heads, d))
+    Q[:, :, 0] = 100
+    return cache_of(k, v, ke, ve), order, o.QT(Q.reshape(1, -1).astype(np.int8), np.array([-8], np.int8), o.ROW), gap / (7 * 100 / 256)
+
+
+@pytest.mark.parametrize("n,gap,heads,kv,d,page,spread", [(2305, 11.5, 1, 1, 16, 16, 0), (4000, 10.5, 4, 2, 64, 64, 2), (70000, 12.0, 2, 2, 32, 256, 4),
+                                                          (131072, 13.0, 4, 1, 128, 256, 0), (9000, 11.0, 3, 3, 48, 1, 1)])
+def test_sinks(n, gap, heads, kv, d, page, spread):
+    announce(f"cache tail {n} {gap} {heads} {kv} {d}")
+    (host, cache), order, Q, scale = sinks(np.random.default_rng(n), n, gap, heads, kv, d, page, spread)
+    O, want = attend(host, cache, Q, order[None], [n], heads, kv, d, float(np.float32(scale)))
+    assert_same(O, want, "O")
+
+
+def test_sinks_among_others():
+    """More heads than a workgroup's shares: whole heads to a workgroup; sequences with and without a sink, short and empty ones."""
+    announce("cache tail batch")
+    rng = np.random.default_rng(3)
+    (host, cache), order, Q, scale = sinks(rng, 3000, 11.0, 4, 2, 32, 16, 1)
+    n = 140
+    lengths = rng.integers(0, 2900, n)
+    lengths[:4] = [3000, 0, 2049, 2048]
+    table = np.tile(order, (n, 1))
+    for i in range(5, n, 2):
+        table[i] = np.roll(order, -1)  # no sink
+    X = qkv(rng, n, 4, 0, 32, elo=-8, ehi=-8)
+    X.mant[:] = Q.mant
+    X.mant[6::4] //= 8
+    rows = [0, 1, 2, 3, 4, 5, 6, 7, 10, 139]
+    O, want = attend(host, cache, X, table, [int(t) for t in lengths], 4, 2, 32, float(np.float32(scale)), rows)
+    m, e = from_dev(O)
+    for at, row in enumerate(rows):
+        assert e[row] == want.exp[at] and np.array_equal(m[row], want.mant[at]), row
