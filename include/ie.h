@@ -586,7 +586,8 @@ ie_status ie_cache_store(const ie_cache *c, int32_t heads, const ie_mat *QKV, co
  * page pages[i * per + j / page]: store a step's own key first.
  * Arithmetic: as in ie_attention_fwd for each run b of 256 keys (positions 256 b
  * ..), with a maximum m_b, a sum L_b and an exponent E_b of its own (of the
- * values; keys and values have exponents of their own here), N_b = sum_j
+ * values; keys and values have exponents of their own here, up to 21, what
+ * ie_cache_store makes of 16; larger ones set IE_FLAG_EXP_RANGE), N_b = sum_j
  * R(w_j 2^(ev_j - E_b)) v_j; then, with a_b the weight of m_b - m, m = max m_b,
  * E = max E_b, o = (sum_b R(a_b 2^(E_b - E)) N_b) (1 / sum_b R(a_b) L_b) 2^E.
  * So rounding takes at most 128 of 32512 units of a run's weights (1 / 254), and

@@ -52,6 +52,7 @@
 namespace ie {
 
 constexpr int ATT_E_LO = -48, ATT_E_HI = 16;
+constexpr int CACHE_E_HI = ATT_E_HI + 5;  // 8-bit mantissas in 4 bits: the largest, 128, is 4 2^5
 constexpr float W_C3 = 2545.0f * 0x1p-32f, W_C2 = 7358.0f * 0x1p-32f, W_C1 = 22609.0f * 0x1p-32f,
                 W_C0 = 32512.0f * 0x1p-32f;
 constexpr float RINT_MAGIC = 12582912.0f;  // 1.5 * 2^23: a sum's low bits are a whole number
@@ -62,7 +63,7 @@ constexpr float FINE_UNIT = 16384.0f;  // 2^ATT_FINE
 constexpr int16_t P_FINE = -31000;     // in the place of a need: the head's fine weights are still to be taken
 constexpr int FINE_WORD = 8;           // of the workspace's header: whether there is such a head; zero between calls
 
-__device__ __forceinline__ int clip_e(int e) { return min(max(e, ATT_E_LO), ATT_E_HI); }
+__device__ __forceinline__ int clip_e(int e, int most = ATT_E_HI) { return min(max(e, ATT_E_LO), most); }
 __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
 
 // The polynomial's coefficients, times a power of two where a row has one.

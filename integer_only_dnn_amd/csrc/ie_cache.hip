@@ -168,8 +168,10 @@ __global__ __launch_bounds__(256, 4) void cache_attention_kernel(CacheArgs p, At
         fk = fv = 0.0f;
         if (mine >= 0) {
             const long long at = (long long)mine * p.kv + w.kvh;
-            fk = pow2f(clip_e(p.ke[at]));
-            fv = pow2f(clip_e(p.ve[at]));
+            const int ek = p.ke[at], ev = p.ve[at];
+            fk = pow2f(clip_e(ek, CACHE_E_HI));
+            fv = pow2f(clip_e(ev, CACHE_E_HI));
+            if (max(ek, ev) > CACHE_E_HI) atomicOr(p.flags, IE_FLAG_EXP_RANGE);
         }
         if (mine == -2) atomicOr(p.flags, IE_FLAG_INDEX);
         take(w, mine, p.k, kw);

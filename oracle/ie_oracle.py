@@ -831,6 +831,7 @@ def dropout(X: QT, R, drop: int, seed: int, step: int, y_group: int, bits: int =
 # ---------------------------------------------------------------------------
 
 ATT_E = (-48, 16)        # exponents of Q, K, V and O are read clipped to these
+CACHE_E = (-48, 21)      # of a cache's keys and values: 4 bits take up to 5 more than 8 bits
 ATT_UNIT = 32512         # a weight of one
 ATT_CHECK = 2032         # rows that see more keys are checked for what rounding their weights takes: 2032 / 2 = ATT_UNIT / 32
 ATT_FINE = 14            # bits that a weight has behind its unit in rows that it takes too much of
@@ -1096,7 +1097,7 @@ def attention_cache(Q: QT, cache: dict, slots, heads: int, kv: int, d: int, scal
                 if not len(at):
                     continue
                 k, v = unpack4(cache["k"][at, h // g]), unpack4(cache["v"][at, h // g])
-                ke, ve = _att_exp(cache["ke"][at, h // g]), _att_exp(cache["ve"][at, h // g])
+                ke, ve = (np.clip(cache[z][at, h // g].astype(np.int64), *CACHE_E) for z in ("ke", "ve"))
                 t = np.ldexp((k @ q).astype(np.float64), ke)
                 w = softmax_weight(_f32(t - t.max()), r)
                 num = np.rint(np.ldexp(w, ve - ve.max())) @ v.astype(np.float64)

@@ -1,0 +1,56 @@
+"""Attention and the cache at the ends of the exponents' range, against the oracle bit for bit, and the flags they set."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle as o
+from integer_only_dnn_amd import ie
+from tests.attention_util import dev_i32, filled, qkv
+from tests.gpu_util import announce, assert_same, qt_to_dev
+from tests.test_gpu_cache import attend, new_cache
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("exps", [(12, 21), (17, 21), (-10, 21)])
+@pytest.mark.parametrize("scale", [2.0 ** -30, 2.0 ** -8, 1.0])
+def test_large_exponents_of_a_cache(exps, scale):
+    announce(f"cache exponents {exps} {scale}")
+    rng = np.random.default_rng(exps[0] + 30)
+    attend(rng, [300, 40, 2600], 4, 2, 64, 32, exps=exps, scale=scale)
+
+
+def test_stored_rows_of_large_exponents():
+    """Rows of exponents 12 to 16, which no flag is set for, stored and attended to."""
+    announce("cache of large rows")
+    rng = np.random.default_rng(2)
+    host, cache = new_cache(rng, 4, 16, 2, 32)
+    X = qkv(rng, 64, 4, 2, 32, elo=12, ehi=16)
+    X.mant[:, 128:] = rng.choice([-128, 127, 100, -90, 1], X.mant[:, 128:].shape)
+    ws, O = ie.Workspace("cuda"), filled(2, 128)
+    slots = rng.permutation(64)
+    ie.ie_cache_store(cache, qt_to_dev(X), 4, dev_i32(slots), ws)
+    o.cache_store(host, X, 4, 2, 32, slots)
+    assert host["ve"].max() == 21
+    Q = qkv(rng, 2, 4, 0, 32, elo=-30, ehi=-25)
+    ie.ie_attention_cache(ie.Attention(4, 2, 32, 0.25), qt_to_dev(Q), cache, dev_i32([[0, 1, 2, 3], [3, 1, 0, 2]]), dev_i32([64, 50]), O, ws)
+    at = np.arange(64)
+    table = np.array([[0, 1, 2, 3], [3, 1, 0, 2]])
+    assert_same(O, o.attention_cache(Q, host, [table[0, at // 16] * 16 + at % 16, (table[1, at // 16] * 16 + at % 16)[:50]], 4, 2, 32, 0.25), "O")
+    assert ws.status() == 0
+
+
+@pytest.mark.parametrize("which", ["ke", "ve"])
+def test_larger_ones_are_flagged(which):
+    announce(f"cache flag {which}")
+    rng = np.random.default_rng(3)
+    host, cache = new_cache(rng, 2, 16, 1, 16)
+    (cache.k_exp if which == "ke" else cache.v_exp)[1, 3, 0] = 22
+    host[which][19] = 22
+    Q, ws, att = qkv(rng, 1, 1, 0, 16, elo=-30, ehi=-30), ie.Workspace("cuda"), ie.Attention(1, 1, 16, 0.25)
+    for length, flag in ((19, 0), (20, ie.FLAG_EXP_RANGE)):
+        O = filled(1, 16)
+        ie.ie_attention_cache(att, qt_to_dev(Q), cache, dev_i32([[0, 1]]), dev_i32([length]), O, ws)
+        assert_same(O, o.attention_cache(Q, host, [np.arange(length)], 1, 1, 16, 0.25), "O")
+        assert ws.status() == flag

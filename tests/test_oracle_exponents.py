@@ -1,0 +1,38 @@
+"""The oracle's attention at the ends of the exponents' range, against the values themselves."""
+
+import numpy as np
+import pytest
+
+import oracle as o
+
+
+@pytest.mark.parametrize("e", [11, 12, 14, 16])
+def test_large_rows_through_the_cache(e):
+    """Rows of large exponents become larger ones in 4 bits; attention over one key is its value, up to the 4 bits."""
+    X = o.QT(np.full((1, 3 * 16), 127, np.int8), np.array([e], np.int8), o.ROW)
+    X.mant[0, 32:] = np.arange(-128, 128, 16)
+    cache = dict(k=np.zeros((1, 1, 8), np.uint8), v=np.zeros((1, 1, 8), np.uint8), ke=np.zeros((1, 1), np.int8), ve=np.zeros((1, 1), np.int8))
+    o.cache_store(cache, X, 1, 1, 16, [0])
+    assert int(cache["ve"][0, 0]) == e + 5 and int(cache["ke"][0, 0]) == e + 5
+    O = o.attention_cache(X, cache, [np.array([0])], 1, 1, 16, 0.25)
+    want, got = X.mant[0, 32:].astype(float) * 2.0 ** e, O.mant[0].astype(float) * 2.0 ** int(O.exp[0])
+    assert np.all(np.abs(got - want) <= 0.5 * 2.0 ** (e + 5) + 0.5 * 2.0 ** int(O.exp[0]))
+
+
+def test_large_keys_order_the_softmax():
+    """Two keys, stored from exponent 16: scores 2^5 apart from what a clipped exponent gives."""
+    X = o.QT(np.zeros((2, 3 * 16), np.int8), np.full(2, 16, np.int8), o.ROW)
+    X.mant[:, 16], X.mant[:, 17] = 127, [0, 64]  # 4 2^21 and 2 2^21
+    X.mant[:, 32] = [64, -64]
+    cache = dict(k=np.zeros((2, 1, 8), np.uint8), v=np.zeros((2, 1, 8), np.uint8), ke=np.zeros((2, 1), np.int8), ve=np.zeros((2, 1), np.int8))
+    o.cache_store(cache, X, 1, 1, 16, [0, 1])
+    Q = o.QT(np.zeros((1, 16), np.int8), np.array([-22], np.int8), o.ROW)
+    Q.mant[0, 1] = 4
+    k = np.ldexp(o.unpack4(cache["k"][:, 0]).astype(float), cache["ke"].astype(int))
+    v = np.ldexp(o.unpack4(cache["v"][:, 0]).astype(float), cache["ve"].astype(int))
+    p = np.exp(k @ (Q.mant[0] * 2.0 ** -22) * 0.25)
+    assert k[1, 1] > 0 and 2 < p[1] / p[0] < 2.0 ** 8
+    want, O = p / p.sum() @ v, o.attention_cache(Q, cache, [np.arange(2)], 1, 1, 16, 0.25)
+    # two weights, each off by half a unit of 32512 and 1.2e-4 relative, twice
+    tol = 2 * (1.2e-4 + 0.5 / 32512 * 2) * np.abs(v).max() + 0.5 * 2.0 ** int(O.exp[0])
+    assert np.all(np.abs(O.mant[0].astype(float) * 2.0 ** int(O.exp[0]) - want) <= tol)
