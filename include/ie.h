@@ -478,7 +478,7 @@ ie_status ie_attention_fwd(const ie_attention_desc *d, const ie_mat *QKV, const 
  * values, so that it goes into ie_linear_bwd_dx and ie_linear_bwd_dw as it is.
  * Rows of no sequence are left as they were.
  * Arithmetic: with w_ij, L_i of the forward pass and eo_i the exponents of dO
- * (O's are read clipped as QKV's are),
+ * (O's are read clipped to [-126, 40]),
  *   u = (dO_i . v_j) 2^(e_j) - (dO_i . O_i) 2^(eO_i), rounded to fp32, s = w u too;
  *   dQ_i = scale / L_i 2^(eo_i + sigma) sum_j R(s 2^(e_j - sigma)) k_j;
  *   a_i = 1 / L_i rounded to fp32, times 2^max(eo_i - max eo, -60);

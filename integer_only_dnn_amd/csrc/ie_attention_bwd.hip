@@ -60,6 +60,9 @@ __global__ __launch_bounds__(256) void attn_dot_kernel(AttnArgs p, AttnBwd b) {
     }
 }
 
+// O's exponents: below those of V where its mantissas cancel, above them where they have fewer bits.
+constexpr int O_E_LO = -126, O_E_HI = 40;
+
 // The scales of the queries of one key head, a token a thread (workgroups of
 // 256 tokens of a sequence, each of which finds the sequence's maxima itself),
 // and for its keys the bounds that dK and dV are scaled by.  Bound by the round
@@ -89,7 +92,7 @@ __global__ __launch_bounds__(256) void attn_scale_kernel(AttnArgs p, AttnBwd b) 
     const int t = 256 * tile + tid;
     if (t >= sp.n) return;
     const long long row = sp.a + t;
-    const int e = clip_e(p.xe[p.x_row ? row : 0]), eo = clip_e(b.oe[row]), ed = b.dye[b.dy_row ? row : 0];
+    const int e = clip_e(p.xe[p.x_row ? row : 0]), eo = min(max((int)b.oe[row], O_E_LO), O_E_HI), ed = b.dye[b.dy_row ? row : 0];
     const float down = pow2f(max(ed - o_top, -60)), r = p.c * pow2f(e);
     int ka = -4096, kl = -4096, fine = 0;
     for (int g = 0; g < p.group; ++g) {

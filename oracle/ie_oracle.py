@@ -830,7 +830,8 @@ def dropout(X: QT, R, drop: int, seed: int, step: int, y_group: int, bits: int =
 # Attention, rotary positions and a 4-bit cache (R10)
 # ---------------------------------------------------------------------------
 
-ATT_E = (-48, 16)        # exponents of Q, K, V and O are read clipped to these
+ATT_E = (-48, 16)        # exponents of Q, K and V are read clipped to these
+O_E = (-126, 40)         # and of O, in the gradient, to these
 CACHE_E = (-48, 21)      # of a cache's keys and values: 4 bits take up to 5 more than 8 bits
 ATT_UNIT = 32512         # a weight of one
 ATT_CHECK = 2032         # rows that see more keys are checked for what rounding their weights takes: 2032 / 2 = ATT_UNIT / 32
@@ -943,7 +944,7 @@ def attention_bwd(X: QT, O: QT, dO: QT, tops, sums, heads: int, kv: int, d: int,
                   bits: int = Q_BITS) -> QT:
     """dQKV by rows (zeros with exponent E_MIN on rows of no sequence)."""
     rows, g = X.mant.shape[0], heads // kv
-    e_all, eo_all, ed_all = _att_exp(X.row_exp()), _att_exp(O.row_exp()), dO.row_exp()
+    e_all, eo_all, ed_all = _att_exp(X.row_exp()), np.clip(O.row_exp(), *O_E), dO.row_exp()
     rate, scale = _att_rate(scale), float(np.float32(scale))
     y = np.zeros((rows, (heads + 2 * kv) * d))
     for a, b in _att_sequences(offsets, rows):

@@ -7,7 +7,8 @@ import torch
 import oracle as o
 from integer_only_dnn_amd import ie
 from tests.attention_util import dev_i32, filled, qkv
-from tests.gpu_util import announce, assert_same, qt_to_dev
+from tests.gpu_util import announce, assert_same, qt_to_dev, rand_qt
+from tests.test_gpu_attention import run
 from tests.test_gpu_cache import attend, new_cache
 
 pytestmark = pytest.mark.gpu
@@ -54,3 +55,14 @@ def test_larger_ones_are_flagged(which):
         ie.ie_attention_cache(att, qt_to_dev(Q), cache, dev_i32([[0, 1]]), dev_i32([length]), O, ws)
         assert_same(O, o.attention_cache(Q, host, [np.arange(length)], 1, 1, 16, 0.25), "O")
         assert ws.status() == flag
+
+
+@pytest.mark.parametrize("bits", [2, 3, 8])
+@pytest.mark.parametrize("exps", [(16, 16), (-48, -48), (10, 16)])
+def test_gradient_from_narrow_results(bits, exps):
+    """O's exponents lie above 16 where its mantissas have few bits, and below -48 where small values cancel."""
+    announce(f"gradient, O of {bits} bits, exponents {exps}")
+    rng = np.random.default_rng(bits)
+    X = qkv(rng, 70, 2, 1, 32, o.ROW, *exps)
+    X.mant[:, 96:] = np.clip(X.mant[:, 96:], -2, 2) if exps[0] < 0 else np.abs(X.mant[:, 96:] // 2) + 64
+    run(X, 2, 1, 32, True, None, scale=2.0 ** (-30 if exps[0] > 0 else 30), bits=bits, dO=rand_qt(rng, (70, 64), o.ROW, -20, -14))

@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 
 import oracle as o
+from tests.test_oracle_attention import softmax64, values
 
 
 @pytest.mark.parametrize("e", [11, 12, 14, 16])
@@ -36,3 +37,29 @@ def test_large_keys_order_the_softmax():
     # two weights, each off by half a unit of 32512 and 1.2e-4 relative, twice
     tol = 2 * (1.2e-4 + 0.5 / 32512 * 2) * np.abs(v).max() + 0.5 * 2.0 ** int(O.exp[0])
     assert np.all(np.abs(O.mant[0].astype(float) * 2.0 ** int(O.exp[0]) - want) <= tol)
+
+
+def gradient_errors(X, bits, scale, seed, ed=-20):
+    """The gradient's relative errors by row (norms of dQ, dK and dV together) against autograd, heads of 16, one sequence."""
+    rng, n = np.random.default_rng(seed), X.mant.shape[0]
+    O, tops, sums = o.attention_fwd(X, 1, 1, 16, scale, False, None, bits)
+    dO = o.QT(rng.integers(-127, 128, (n, 16)).astype(np.int8), np.full(n, ed, np.int8), o.ROW)
+    G = values(o.attention_bwd(X, O, dO, tops, sums, 1, 1, 16, scale, False))
+    x, _, ((_, _, p, v, k, q),) = softmax64(X, 1, 1, 16, scale, False, [0, n])
+    # the definition with D from the O that the pass has rounded
+    dy = values(dO)
+    u = dy @ v[0].T - (dy * values(O)).sum(axis=1)[:, None]
+    s = p[0] * u
+    want = np.concatenate([scale * s @ k[0], scale * s.T @ q[0], p[0].T @ dy], axis=1)
+    return O, np.linalg.norm(G - want, axis=0).reshape(3, 16), np.linalg.norm(want, axis=0).reshape(3, 16)
+
+
+def test_gradient_of_a_narrow_result():
+    """O in 2 bits at the largest exponents: its own lie 6 above 16."""
+    rng = np.random.default_rng(9)
+    X = o.QT(rng.integers(-127, 128, (40, 48)).astype(np.int8), np.full(40, 16, np.int8), o.ROW)
+    X.mant[:, 32:] = rng.integers(100, 128, (40, 16))
+    O, err, size = gradient_errors(X, 2, 2.0 ** -30, 7)
+    assert O.row_exp().min() > 16
+    # half a unit of 2^-7 of a row's largest element, which is at most 6 of its root mean square: 0.024; weights of 1.2e-4, twice
+    assert np.all(err <= 0.025 * size.max())
