@@ -428,7 +428,7 @@ ie_status ie_dropout(const ie_mat *X, const ie_mat *R, const ie_mat *Y, const ie
  *
  *   O = softmax(scale Q K^T) V   of every head,  O [rows x heads * head_dim].
  *
- * Arithmetic, for row i of a head (e_i its exponent, read clipped to [-48, 16];
+ * Arithmetic, for row i of a head (e_i its exponent, read clipped to [-126, 16];
  * an exponent above 16 sets IE_FLAG_EXP_RANGE): t_j = (q_i . k_j) 2^(e_j)
  * exactly, m = max t_j over the keys that i sees, r = scale log2(e), rounded to
  * fp32, times 2^(e_i);
@@ -478,7 +478,8 @@ ie_status ie_attention_fwd(const ie_attention_desc *d, const ie_mat *QKV, const 
  * values, so that it goes into ie_linear_bwd_dx and ie_linear_bwd_dw as it is.
  * Rows of no sequence are left as they were.
  * Arithmetic: with w_ij, L_i of the forward pass and eo_i the exponents of dO
- * (O's are read clipped to [-126, 40]),
+ * (O's are read as they are, clipped to 126 below and 40 above the largest of
+ * QKV's in the sequence, and QKV's to 126 below it),
  *   u = (dO_i . v_j) 2^(e_j) - (dO_i . O_i) 2^(eO_i), rounded to fp32, s = w u too;
  *   dQ_i = scale / L_i 2^(eo_i + sigma) sum_j R(s 2^(e_j - sigma)) k_j;
  *   a_i = 1 / L_i rounded to fp32, times 2^max(eo_i - max eo, -60);

@@ -486,7 +486,7 @@ __global__ __launch_bounds__(256, DP > 64 ? 1 : 2) void attn_fwd_fine_kernel(Att
         m = col_max(m);
         em = col_max(em);
         const int top = ROW ? (__float_as_int(em) >> 23) - 127 : eq;
-        const float down = pow2f(ROW ? -top : 0) * FINE_UNIT;
+        const float down = pow2f(ROW ? -top : 0);
         __syncthreads();
         v4i acc[4][NE] = {};
         long long count = 0;
@@ -507,7 +507,7 @@ __global__ __launch_bounds__(256, DP > 64 ? 1 : 2) void attn_fwd_fine_kernel(Att
                     float w = weight(__builtin_fmaf((float)s[i], f, -m), r);
                     w = 64 * t + 16 * z + 4 * quad + i <= lim ? w : 0.0f;
                     count += (int)__builtin_rintf(w * FINE_UNIT);
-                    n4[i] = (int)__builtin_rintf(w * (f * down));
+                    n4[i] = (int)__builtin_rintf(w * (ROW ? f * down : 1.0f) * FINE_UNIT);
                 }
                 digits4x4(n4, o);
 #pragma unroll

@@ -15,7 +15,9 @@
 // by the product of the norms), taken over the rows that meet in the sum, so
 // |A|, |B| <= 32512 and |C| <= 64 * 32512: two and three int8 digits.  C has
 // three, as it sums rows whose sizes differ most: with two, the bounds left it
-// a root mean square of four units.  Rows of fine weights (ie_attn.h) have theirs with
+// a root mean square of four units.  All of it runs on exponents relative to the
+// sequence's largest one, so that a sequence of the smallest exponents is as exact as any
+// (a score's two factors take that power of two between them).  Rows of fine weights (ie_attn.h) have theirs with
 // 2^14 in the place of 1 and 2^6, and so have the keys that share a sequence and
 // a key head with one: four digits, |n| <= 2^14 32512.
 #include "ie_attn.h"
@@ -60,8 +62,10 @@ __global__ __launch_bounds__(256) void attn_dot_kernel(AttnArgs p, AttnBwd b) {
     }
 }
 
-// O's exponents: below those of V where its mantissas cancel, above them where they have fewer bits.
+// O's exponents, relative: below those of V where its mantissas cancel, above them where they have fewer bits.
 constexpr int O_E_LO = -126, O_E_HI = 40;
+// 2^(e - top), a key's factor.
+__device__ __forceinline__ float rel_pow2(int e, int top) { return pow2_down(clip_e(e) - top); }
 
 // The scales of the queries of one key head, a token a thread (workgroups of
 // 256 tokens of a sequence, each of which finds the sequence's maxima itself),
@@ -86,33 +90,34 @@ __global__ __launch_bounds__(256) void attn_scale_kernel(AttnArgs p, AttnBwd b) 
         o_top = max(o_top, (int)b.dye[b.dy_row ? row : 0]);
     }
     e_top = row_reduce_once<256>(e_top, Max{}, sh[0]);
-    n_top = row_reduce_once<256>(n_top, Max{}, sh[1]);
-    r_top = row_reduce_once<256>(r_top, Max{}, sh[2]);
+    n_top = row_reduce_once<256>(n_top, Max{}, sh[1]) - e_top;
+    r_top = row_reduce_once<256>(r_top, Max{}, sh[2]) - 2 * e_top;
     o_top = row_reduce_once<256>(o_top, Max{}, sh[3]);
     const int t = 256 * tile + tid;
     if (t >= sp.n) return;
     const long long row = sp.a + t;
-    const int e = clip_e(p.xe[p.x_row ? row : 0]), eo = min(max((int)b.oe[row], O_E_LO), O_E_HI), ed = b.dye[b.dy_row ? row : 0];
-    const float down = pow2f(max(ed - o_top, -60)), r = p.c * pow2f(e);
+    const int e = clip_e(p.xe[p.x_row ? row : 0]), eo = min(max((int)b.oe[row] - e_top, O_E_LO), O_E_HI);
+    const int ed = b.dye[b.dy_row ? row : 0];
+    const float down = pow2f(max(ed - o_top, -60)), r = p.c * pow2f(e) * pow2f(e_top);
     int ka = -4096, kl = -4096, fine = 0;
     for (int g = 0; g < p.group; ++g) {
         const int h = it.kvh * p.group + g;
         const int2 d = b.dots[row * p.heads + h], st = p.stats[row * p.heads + h];
-        const int delta = bits_of((uint32_t)abs(d.x)) + eo, rise = max(d.y + r_top, delta + e_top) + 1;
+        const int delta = bits_of((uint32_t)abs(d.x)) + eo, rise = max(d.y + r_top, delta) + 1;
         AttnRow q;
-        q.m = __int_as_float(st.x & ~1);  // its last bit: a row of fine weights
+        q.m = __int_as_float(st.x & ~1) * pow2f(-e_top);  // the last bit: a row of fine weights
         fine |= st.x & 1;
         q.r = r;
         q.dot = (float)d.x * pow2f(eo);
         q.a = (float)(1.0 / (double)(uint32_t)st.y) * down;  // a < 2^alpha
-        q.s = pow2f(max(-rise, -126));
-        q.e = rise + ed;
-        q.o_top = o_top;
-        q.ek = e;
+        q.s = pow2f(-rise);
+        q.e = rise + ed + 2 * e_top;
+        q.tops = o_top << 8 | (e_top & 0xff);
+        q.ek = e - e_top;
         b.row[(long long)h * p.rows + row] = q;
         const int alpha = (__float_as_int(q.a) >> 23) - 126;
         ka = max(ka, alpha);
-        kl = max(kl, alpha + e + max(d.y + n_top, delta) + 1);  // a |u| 2^e < 2^kl
+        kl = max(kl, alpha + e - e_top + max(d.y + n_top, delta) + 1);  // a |u| 2^e < 2^kl
     }
     b.key[(long long)it.kvh * p.rows + row] = AttnKey{(int16_t)ka, (int16_t)kl};
     if (fine) atomicOr(p.flags + FINE_WORD, 1u);
@@ -178,8 +183,9 @@ __global__ __launch_bounds__(256, DP > 64 ? 2 : 3) void attn_dq_kernel(AttnArgs 
     head_regs<KS>(base + (long long)qi * p.width + h * p.dp, ok, p.dp, lane, q);
     head_regs<KS>(bw.dy + (row * p.heads + h) * p.dp, ok, p.dp, lane, g);
     const AttnRow st = bw.row[(long long)h * p.rows + sp.a + min(qi, n - 1)];
-    const float fe0 = pow2f(clip_e(xe[0]));
-    const Poly scaled = poly(ROW ? st.s : fe0 * st.s);  // 2^-126 .. 2^60: exact products, no subnormal numbers
+    const int e_top = (int8_t)st.tops;
+    const float fe0 = 1.0f;  // where all rows share an exponent
+    const Poly scaled = poly(st.s);  // 2^-70 .. 2^-1: exact products, no subnormal numbers
     const int keys = CAUSAL ? min(n, q0 + BM) : n, tiles = (keys + 63) / 64;
     const int last = CAUSAL ? min(n, qw + 16) : n;
     T k, v;
@@ -190,7 +196,7 @@ __global__ __launch_bounds__(256, DP > 64 ? 2 : 3) void attn_dq_kernel(AttnArgs 
     auto fetch = [&](int t) {
         k.fetch(kh, p.width, 64 * t, keys, p.dp);
         v.fetch(vh, p.width, 64 * t, keys, p.dp);
-        if (ROW && me < 64) fe = pow2f(clip_e(xe[min(64 * t + me, n - 1)]));
+        if (ROW && me < 64) fe = rel_pow2(xe[min(64 * t + me, n - 1)], e_top);
     };
     auto weigh = [&](auto masked, int t, int buf, v4i &dh, v4i &dl) {
         const int lim = (CAUSAL ? qi : n - 1) - 64 * t - 4 * quad;  // keys seen: 16 z + i <= lim
@@ -298,11 +304,11 @@ __global__ __launch_bounds__(256, SPLIT == 2 ? 2 : DP > 64 ? 1 : SPLIT == 4 ? 2 
     v4i k[KS], v[KS];
     head_regs<KS>(base + (long long)kj * p.width + (long long)(p.heads + it.kvh) * p.dp, ok, p.dp, lane, k);
     head_regs<KS>(base + (long long)kj * p.width + (long long)(p.heads + p.kv + it.kvh) * p.dp, ok, p.dp, lane, v);
-    const float f = pow2f(clip_e(p.xe[p.x_row ? sp.a + min(kj, n - 1) : 0]));
     AttnKey all, seen;
     key_bounds<CAUSAL, KEYS>(bw.key + (long long)it.kvh * p.rows + sp.a, n, k0, kj, smark, all, seen);
     const int whole = all[1], kappa = seen[0], lambda = max(seen[1] - whole, -96);
-    const int o_top = bw.row[(long long)it.kvh * p.group * p.rows + sp.a].o_top;
+    const int tops = bw.row[(long long)it.kvh * p.group * p.rows + sp.a].tops, o_top = tops >> 8, e_top = (int8_t)tops;
+    const float f = rel_pow2(p.xe[p.x_row ? sp.a + min(kj, n - 1) : 0], e_top);
     const float sv = pow2f(min(-kappa, 126)), sk = pow2f(min(6 - lambda, 126));
     const int first = CAUSAL ? k0 / 64 : 0, tiles = (n + 63) / 64 - first, total = tiles * p.group;
     const int steps = OWN ? (total - wave + 3) / 4 : total, z0 = SHARE ? 2 * (wave >> 1) : 0;
@@ -436,7 +442,7 @@ __global__ __launch_bounds__(256, SPLIT == 2 ? 2 : DP > 64 ? 1 : SPLIT == 4 ? 2 
         if (wave) return;
     }
     if (!SHARE && idle) return;
-    const int head_k = p.heads + it.kvh, head_v = head_k + p.kv, e_k = lambda - 6 + whole + o_top, e_v = kappa + o_top;
+    const int head_k = p.heads + it.kvh, head_v = head_k + p.kv, e_k = lambda - 6 + whole + 2 * e_top + o_top, e_v = kappa + o_top;
     auto value = [&](int g2, bool of_k, int e, int i) {
         const auto &a = acc[g2];
         return of_k ? ((double)a[2][e][i] * 65536.0 + ((double)a[3][e][i] * 256.0 + (double)a[4][e][i])) * p.scale
@@ -530,6 +536,7 @@ __device__ __forceinline__ void fine_dq(const AttnArgs &p, const AttnBwd &bw, in
     head_regs<KS>(base + (long long)qi * p.width + h * p.dp, qi < n, p.dp, lane, q);
     head_regs<KS>(bw.dy + (row * p.heads + h) * p.dp, qi < n, p.dp, lane, g);
     const AttnRow st = bw.row[(long long)h * p.rows + sp.a + min(qi, n - 1)];
+    const int e_top = (int8_t)st.tops;
     const Poly scaled = poly(st.s);
     const int keys = CAUSAL ? min(n, q0 + 64) : n, tiles = (keys + 63) / 64, lim = CAUSAL ? qi : n - 1;
     T k, v;
@@ -539,7 +546,7 @@ __device__ __forceinline__ void fine_dq(const AttnArgs &p, const AttnBwd &bw, in
     auto fetch = [&](int t) {
         k.fetch(kh, p.width, 64 * t, keys, p.dp);
         v.fetch(vh, p.width, 64 * t, keys, p.dp);
-        if (tid < 64) fe = pow2f(clip_e(p.xe[p.x_row ? sp.a + min(64 * t + tid, n - 1) : 0]));
+        if (tid < 64) fe = rel_pow2(p.xe[p.x_row ? sp.a + min(64 * t + tid, n - 1) : 0], e_top);
     };
     v4i acc[4][NE] = {};
     fetch(0);
@@ -610,11 +617,11 @@ __device__ __forceinline__ void fine_dkv(const AttnArgs &p, const AttnBwd &bw, i
     v4i k[KS], v[KS];
     head_regs<KS>(base + (long long)kj * p.width + (long long)(p.heads + kvh) * p.dp, ok, p.dp, lane, k);
     head_regs<KS>(base + (long long)kj * p.width + (long long)(p.heads + p.kv + kvh) * p.dp, ok, p.dp, lane, v);
-    const float f = pow2f(clip_e(p.xe[p.x_row ? sp.a + min(kj, n - 1) : 0]));
     AttnKey all, seen;
     key_bounds<CAUSAL, 64>(bw.key + (long long)kvh * p.rows + sp.a, n, k0, kj, lds.mark, all, seen);
     const int whole = all[1], kappa = seen[0], lambda = max(seen[1] - whole, -96);
-    const int o_top = bw.row[(long long)kvh * p.group * p.rows + sp.a].o_top;
+    const int tops = bw.row[(long long)kvh * p.group * p.rows + sp.a].tops, o_top = tops >> 8, e_top = (int8_t)tops;
+    const float f = rel_pow2(p.xe[p.x_row ? sp.a + min(kj, n - 1) : 0], e_top);
     const int first = CAUSAL ? k0 / 64 : 0, tiles = (n + 63) / 64 - first, steps = tiles * p.group;
     T q, g;
     q.init(p.width, p.dp);
@@ -680,7 +687,7 @@ __device__ __forceinline__ void fine_dkv(const AttnArgs &p, const AttnBwd &bw, i
                 y[4 * e + i] = whole4(acc[0][e][i], acc[1][e][i], acc[2][e][i], acc[3][e][i]);
                 if (of_k.value) y[4 * e + i] *= p.scale;
             }
-        const int head = p.heads + kvh + (of_k.value ? 0 : p.kv), e = (of_k.value ? lambda + whole : kappa) + o_top - ATT_FINE;
+        const int head = p.heads + kvh + (of_k.value ? 0 : p.kv), e = (of_k.value ? lambda + whole + 2 * e_top : kappa) + o_top - ATT_FINE;
         store_odd(y, e, p.q, ok, p.d, lane, p.v16 + row * p.cols + head * p.d, p.p16 + row * p.parts + head);
         __syncthreads();  // the tiles are read
     };

@@ -51,7 +51,7 @@
 
 namespace ie {
 
-constexpr int ATT_E_LO = -48, ATT_E_HI = 16;
+constexpr int ATT_E_LO = -126, ATT_E_HI = 16;  // exponents of fp32's normal numbers
 constexpr int CACHE_E_HI = ATT_E_HI + 5;  // 8-bit mantissas in 4 bits: the largest, 128, is 4 2^5
 constexpr float W_C3 = 2545.0f * 0x1p-32f, W_C2 = 7358.0f * 0x1p-32f, W_C1 = 22609.0f * 0x1p-32f,
                 W_C0 = 32512.0f * 0x1p-32f;
@@ -65,6 +65,7 @@ constexpr int FINE_WORD = 8;           // of the workspace's header: whether the
 
 __device__ __forceinline__ int clip_e(int e, int most = ATT_E_HI) { return min(max(e, ATT_E_LO), most); }
 __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
+__device__ __forceinline__ float pow2_down(int e) { return pow2f(max(e, -126)); }        // e <= 0: what is less rounds to 0
 
 // The polynomial's coefficients, times a power of two where a row has one.
 struct Poly {

@@ -408,7 +408,7 @@ __global__ __launch_bounds__(256) void cache_join_kernel(CacheArgs p, AttnArgs a
             __syncthreads();
             if (tid < nc) {
                 const int4 t = top[(long long)(b0 + tid) * a.heads];
-                sw[tid] = t.y ? weigh(weight(__int_as_float(t.x) - m, r), pow2f(t.z - em), t.y, n) : 0;
+                sw[tid] = t.y ? weigh(weight(__int_as_float(t.x) - m, r), pow2_down(t.z - em), t.y, n) : 0;
             }
             __syncthreads();
             if (part < parts) {
@@ -520,7 +520,7 @@ __global__ __launch_bounds__(256) void cache_join_row_kernel(CacheArgs p, AttnAr
     if (n) {
         const float y = weight(m - top, r);
         den = (double)(y + RINT_MAGIC - RINT_MAGIC) * (double)n;
-        w = __builtin_fmaf(y, pow2f(e - em), RINT_MAGIC) - RINT_MAGIC;
+        w = __builtin_fmaf(y, pow2_down(e - em), RINT_MAGIC) - RINT_MAGIC;
     }
     for (int o = 1; o < span; o <<= 1) den += __shfl_xor(den, o, 64);
     sw[tid] = w;

@@ -374,10 +374,10 @@ hipError_t launch_attention_round(const AttnArgs &a, hipStream_t st);
 // What the backward pass knows of a query row of a head and of a key (see
 // ie_attention_bwd.hip).
 struct AttnRow {
-    float m, r, dot, a, s;
-    int e;      // exponent of its units of dQ
-    int ek;     // its row's exponent, clipped
-    int o_top;  // largest exponent of dO in its sequence
+    float m, r, dot, a, s;  // in units of 2^(the largest exponent of its sequence)
+    int e;                  // exponent of its units of dQ
+    int ek;                 // its row's exponent, below that largest one
+    int tops;               // largest exponents of its sequence, of dO (from bit 8 on) and of QKV
 };
 typedef int16_t AttnKey __attribute__((ext_vector_type(2)));  // bounds kappa, lambda of the queries at a token
 #define ATT_NO_KEY (AttnKey{-4096, -4096})

@@ -830,9 +830,9 @@ def dropout(X: QT, R, drop: int, seed: int, step: int, y_group: int, bits: int =
 # Attention, rotary positions and a 4-bit cache (R10)
 # ---------------------------------------------------------------------------
 
-ATT_E = (-48, 16)        # exponents of Q, K and V are read clipped to these
-O_E = (-126, 40)         # and of O, in the gradient, to these
-CACHE_E = (-48, 21)      # of a cache's keys and values: 4 bits take up to 5 more than 8 bits
+ATT_E = (-126, 16)       # exponents of Q, K and V are read clipped to these
+O_E = (-126, 40)         # and of O, in the gradient, to these above the largest of its sequence
+CACHE_E = (-126, 21)     # of a cache's keys and values: 4 bits take up to 5 more than 8 bits
 ATT_UNIT = 32512         # a weight of one
 ATT_CHECK = 2032         # rows that see more keys are checked for what rounding their weights takes: 2032 / 2 = ATT_UNIT / 32
 ATT_FINE = 14            # bits that a weight has behind its unit in rows that it takes too much of
@@ -944,17 +944,19 @@ def attention_bwd(X: QT, O: QT, dO: QT, tops, sums, heads: int, kv: int, d: int,
                   bits: int = Q_BITS) -> QT:
     """dQKV by rows (zeros with exponent E_MIN on rows of no sequence)."""
     rows, g = X.mant.shape[0], heads // kv
-    e_all, eo_all, ed_all = _att_exp(X.row_exp()), np.clip(O.row_exp(), *O_E), dO.row_exp()
+    e_all, eo_all, ed_all = _att_exp(X.row_exp()), O.row_exp(), dO.row_exp()
     rate, scale = _att_rate(scale), float(np.float32(scale))
     y = np.zeros((rows, (heads + 2 * kv) * d))
     for a, b in _att_sequences(offsets, rows):
         if a == b:
             continue
-        e, eo, ed = e_all[a:b], eo_all[a:b], ed_all[a:b]
-        most = int(ed.max())
+        e, ed = e_all[a:b], ed_all[a:b]
+        most, top = int(ed.max()), int(e.max())
+        # all but the scores in units of the sequence's largest exponent
+        eq, ek, eo = e - top, np.maximum(e - top, -126), np.clip(eo_all[a:b] - top, *O_E)
         for hk in range(kv):
             k, v = _att_head(X, heads + hk, d, a, b), _att_head(X, heads + kv + hk, d, a, b)
-            nu = _norm_bits(v) + e
+            nu = _norm_bits(v) + ek
             per, any_fine = [], False
             for h in range(hk * g, (hk + 1) * g):
                 q, dy, o = _att_head(X, h, d, a, b), _att_head(dO, h, d, a, b), _att_head(O, h, d, a, b)
@@ -964,17 +966,17 @@ def attention_bwd(X: QT, O: QT, dO: QT, tops, sums, heads: int, kv: int, d: int,
                 any_fine |= bool(fine.any())
                 w = _att_weights(t, see, m, rate * np.ldexp(1.0, e))
                 dot = (dy * o).sum(axis=1)
-                u = _f32(np.ldexp(_exact_matmul(dy, v.T).astype(np.float64), e[None, :])
+                u = _f32(np.ldexp(_exact_matmul(dy, v.T).astype(np.float64), ek[None, :])
                          - np.ldexp(dot.astype(np.float64), eo)[:, None])
                 s = _f32(w * u)
                 delta, size = _bitlen_np(np.abs(dot)) + eo, _norm_bits(dy)
-                sigma = np.maximum(size + (nu + e).max(), delta + e.max()) + 1
+                sigma = np.maximum(size + (nu + ek).max(), delta) + 1
                 more = ATT_FINE * fine
-                num = np.rint(np.ldexp(s, e[None, :] + (more - sigma)[:, None])) @ k.astype(np.float64)
-                y[a:b, h * d:(h + 1) * d] = np.ldexp(num * (scale / total)[:, None], (sigma - more + ed)[:, None])
+                num = np.rint(np.ldexp(s, ek[None, :] + (more - sigma)[:, None])) @ k.astype(np.float64)
+                y[a:b, h * d:(h + 1) * d] = np.ldexp(num * (scale / total)[:, None], (sigma - more + ed + 2 * top)[:, None])
                 share = np.ldexp(_f32(1.0 / total), np.maximum(ed - most, -60))
                 alpha = np.frexp(share)[1].astype(np.int64)
-                per.append((q, dy, w, s, share, alpha, alpha + e + np.maximum(size + nu.max(), delta) + 1))
+                per.append((q, dy, w, s, share, alpha, alpha + eq + np.maximum(size + nu.max(), delta) + 1))
             kappa = np.max([_reach(z[5], causal) for z in per], axis=0)
             lam = np.max([_reach(z[6], causal) for z in per], axis=0)
             whole = int(max(z[6].max() for z in per))
@@ -983,9 +985,9 @@ def attention_bwd(X: QT, O: QT, dO: QT, tops, sums, heads: int, kv: int, d: int,
             dk, dv = np.zeros((b - a, d)), np.zeros((b - a, d))
             for q, dy, w, s, share, _, _ in per:
                 dv += np.rint(np.ldexp(_f32(w * share[:, None]), of_v - kappa[None, :])).T @ dy.astype(np.float64)
-                bi = _f32(np.ldexp(share, e - whole))
+                bi = _f32(np.ldexp(share, eq - whole))
                 dk += np.rint(np.ldexp(_f32(s * bi[:, None]), of_k - lam[None, :])).T @ q.astype(np.float64)
-            y[a:b, (heads + hk) * d:(heads + hk + 1) * d] = np.ldexp(dk * scale, (lam - of_k + whole + most)[:, None])
+            y[a:b, (heads + hk) * d:(heads + hk + 1) * d] = np.ldexp(dk * scale, (lam - of_k + whole + most + 2 * top)[:, None])
             y[a:b, (heads + kv + hk) * d:(heads + kv + hk + 1) * d] = np.ldexp(dv, (kappa - of_v + most)[:, None])
     return requant_f64(y, ROW, bits)
 

@@ -6,6 +6,7 @@ import torch
 
 import oracle as o
 from integer_only_dnn_amd import ie
+from tests.attention_tail import sink
 from tests.attention_util import dev_i32, filled, qkv
 from tests.gpu_util import announce, assert_same, qt_to_dev, rand_qt
 from tests.test_gpu_attention import run
@@ -66,3 +67,31 @@ def test_gradient_from_narrow_results(bits, exps):
     X = qkv(rng, 70, 2, 1, 32, o.ROW, *exps)
     X.mant[:, 96:] = np.clip(X.mant[:, 96:], -2, 2) if exps[0] < 0 else np.abs(X.mant[:, 96:] // 2) + 64
     run(X, 2, 1, 32, True, None, scale=2.0 ** (-30 if exps[0] > 0 else 30), bits=bits, dO=rand_qt(rng, (70, 64), o.ROW, -20, -14))
+
+
+@pytest.mark.parametrize("exps", [(-60, -50), (-126, -100), (-128, 16), (-126, -126), (-120, -30)])
+@pytest.mark.parametrize("group", [o.ROW, o.TENSOR])
+@pytest.mark.parametrize("scale", [2.0 ** -30, 1.0, 2.0 ** 30])
+def test_small_rows(exps, group, scale):
+    """Forward and gradient, short sequences and longer ones, heads of every kernel; gradients of far exponents."""
+    announce(f"attention exponents {exps} {group} {scale}")
+    rng = np.random.default_rng(-exps[0] + exps[1])
+    for causal, rows, d in ((False, 50, 16), (True, 300, 64), (False, 290, 128)):
+        X = qkv(rng, rows, 2, 1, d, group, *exps, flat=True)
+        run(X, 2, 1, d, causal, [0, 1, rows], scale=scale, dO=rand_qt(rng, (rows, 2 * d), o.ROW, -128, 20))
+
+
+@pytest.mark.parametrize("exps", [(-128, -100), (-128, 21), (-70, -49), (-126, -126)])
+@pytest.mark.parametrize("scale", [2.0 ** -30, 1.0, 2.0 ** 30])
+def test_small_exponents_of_a_cache(exps, scale):
+    announce(f"cache exponents {exps} {scale}")
+    attend(np.random.default_rng(exps[1] + 130), [300, 40, 2600], 4, 2, 64, 32, exps=exps, scale=scale)
+
+
+def test_fine_weights_of_small_rows():
+    announce("attention tail of small rows")
+    X, scale = sink(np.random.default_rng(5), 2100, 10.8, lift=2)
+    X.exp[:] -= 12
+    run(X, 1, 1, 16, True, None, scale=scale * 2.0 ** 24, dO=rand_qt(np.random.default_rng(6), (2100, 16), o.ROW, -20, -14))
+    Y = o.QT(X.mant, (X.exp.astype(int) - 100).astype(np.int8), o.ROW)  # all weights alike: every sum is large, none is fine
+    run(Y, 1, 1, 16, True, None, scale=scale, dO=rand_qt(np.random.default_rng(6), (2100, 16), o.ROW, -20, -14))

@@ -63,3 +63,31 @@ def test_gradient_of_a_narrow_result():
     assert O.row_exp().min() > 16
     # half a unit of 2^-7 of a row's largest element, which is at most 6 of its root mean square: 0.024; weights of 1.2e-4, twice
     assert np.all(err <= 0.025 * size.max())
+
+
+@pytest.mark.parametrize("exps", [(-60, -50), (-110, -104), (-126, -119)])
+def test_small_rows(exps):
+    """Tokens of the smallest exponents: their results and the gradient of their values are as exact as any others'."""
+    rng = np.random.default_rng(-exps[0])
+    X = o.QT(rng.integers(-127, 128, (50, 48)).astype(np.int8), rng.integers(exps[0], exps[1] + 1, 50).astype(np.int8), o.ROW)
+    O, tops, sums = o.attention_fwd(X, 1, 1, 16, 1.0, True)
+    x, y, ((_, _, p, v, _, _),) = softmax64(X, 1, 1, 16, 1.0, True, [0, 50])
+    # all scores are alike: a weight is 32512, its value's exponent takes half a unit of the largest one's
+    tol = 0.5 * 127 * 2.0 ** exps[1] / 32512 + 0.5 * np.ldexp(1.0, O.row_exp())
+    assert np.all(np.abs(values(O) - y.detach().numpy()).max(axis=1) <= tol)
+    dO = o.QT(rng.integers(-127, 128, (50, 16)).astype(np.int8), np.full(50, -12, np.int8), o.ROW)
+    G = values(o.attention_bwd(X, O, dO, tops, sums, 1, 1, 16, 1.0, True))
+    want = p[0].T @ values(dO)
+    half = 0.5 * np.ldexp(1.0, o.requant_f64(G, o.ROW).row_exp())[:, None]
+    # 1 / L in fp32 and half a unit of each of 50 integers of at least 16256 / 50
+    assert np.all(np.abs(G[:, 32:] - want) <= half + 127 * 2.0 ** -12 * 50 * 0.5 / 16256)
+
+
+def test_small_values_in_a_cache():
+    rng = np.random.default_rng(4)
+    cache = dict(k=rng.integers(0, 256, (300, 1, 8)).astype(np.uint8), v=rng.integers(0, 256, (300, 1, 8)).astype(np.uint8),
+                 ke=rng.integers(-100, -60, (300, 1)).astype(np.int8), ve=rng.integers(-66, -60, (300, 1)).astype(np.int8))
+    Q = o.QT(rng.integers(-127, 128, (1, 16)).astype(np.int8), np.array([-8], np.int8), o.ROW)
+    O = o.attention_cache(Q, cache, [np.arange(300)], 1, 1, 16, 0.25)
+    v = np.ldexp(o.unpack4(cache["v"][:, 0]).astype(float), cache["ve"].astype(int))
+    assert np.all(np.abs(O.mant[0] * 2.0 ** int(O.exp[0]) - v.mean(axis=0)) <= 0.5 * 8 * 2.0 ** -61 / 32512 + 0.5 * 2.0 ** int(O.exp[0]))
