@@ -456,8 +456,11 @@ ie_status ie_dropout(const ie_mat *X, const ie_mat *R, const ie_mat *Y, const ie
  * Limits (IE_ERR_UNSUPPORTED): head_dim <= 128, (heads + 2 kv_heads) * head_dim
  * <= 2^24, 2^-30 <= scale <= 2^30, (rows / 32 + n_seq + 9) * heads < 2^24, rows <
  * 2^26 - 4, without offsets at most 131071 rows.
- * Offsets that decrease or leave the matrix, and sequences of more than 131071
- * tokens, set IE_FLAG_INDEX: the rows they name are undefined, no others.
+ * Offsets that leave the matrix, and sequences of more than 131071 tokens, set
+ * IE_FLAG_INDEX: the rows they name are undefined, no others.  Offsets that
+ * decrease set it too, and leave all rows of the call undefined.  Undefined rows
+ * may set IE_FLAG_EXP_RANGE; nothing outside the outputs and the workspace is
+ * written.
  */
 typedef struct {
     int32_t heads, kv_heads, head_dim;
