@@ -1266,6 +1266,11 @@ static hipError_t padded_heads(const ie_mat *m, int nh, const AttnArgs &a, int8_
     return launch_attention_pad(m->mant, m->rows, nh, a.d, a.dp, copy, st);
 }
 
+// Whether the n bytes at p and the m at q have one in common.
+static bool meet_bytes(const void *p, size_t n, const void *q, size_t m) {
+    return n && m && (uintptr_t)p < (uintptr_t)q + m && (uintptr_t)q < (uintptr_t)p + n;
+}
+
 // Whether a byte of m is one of the n at p.
 static bool share_bytes(const ie_mat *m, const void *p, size_t n) {
     const ie_mat b = {(int8_t *)p, (int8_t *)p, 1, (int64_t)n, IE_GROUP_TENSOR, 0};
@@ -1286,7 +1291,7 @@ ie_status ie_attention_fwd(const ie_attention_desc *d, const ie_mat *QKV, const 
     if (O->group != IE_GROUP_ROW || !aligned(stats, 8) || (!d->offsets && QKV->rows > ATT_MOST)) return IE_ERR_UNSUPPORTED;
     const size_t stat_bytes = stats ? (size_t)O->rows * d->heads * 8 : 0, off_bytes = ((size_t)d->n_seq + 1) * 4;
     if (share(O, QKV) || share_bytes(O, d->offsets, off_bytes) || share_bytes(O, stats, stat_bytes) ||
-        share_bytes(QKV, stats, stat_bytes))
+        share_bytes(QKV, stats, stat_bytes) || (stats && d->offsets && meet_bytes(stats, stat_bytes, d->offsets, off_bytes)))
         return IE_ERR_UNSUPPORTED;
     if (!ws) return IE_ERR_WORKSPACE;
     if (ws_bytes < attention_fwd_ws(QKV->rows, d->heads, d->kv_heads, d->head_dim)) return IE_ERR_WORKSPACE;
@@ -1456,11 +1461,30 @@ static CacheArgs cache_args(const ie_cache *c, void *ws) {
     return a;
 }
 
-// Whether a byte of m is one of the cache's.
-static bool share_cache(const ie_mat *m, const ie_cache *c) {
+// A cache's arrays, and whether a byte of m is one of theirs.
+struct CacheBytes {
+    const void *p[4];
+    size_t n[4];
+};
+static CacheBytes cache_bytes(const ie_cache *c) {
     const size_t slots = (size_t)c->pages * c->page * c->kv_heads, bytes = slots * (c->head_dim / 2);
-    return share_bytes(m, c->k, bytes) || share_bytes(m, c->v, bytes) || share_bytes(m, c->k_exp, slots) ||
-           share_bytes(m, c->v_exp, slots);
+    return CacheBytes{{c->k, c->v, c->k_exp, c->v_exp}, {bytes, bytes, slots, slots}};
+}
+static bool share_cache(const ie_mat *m, const ie_cache *c) {
+    const CacheBytes b = cache_bytes(c);
+    bool any = false;
+    for (int i = 0; i < 4; ++i) any |= share_bytes(m, b.p[i], b.n[i]);
+    return any;
+}
+// Whether two of a cache's arrays, or one and the n bytes at p, have a byte in common.
+static bool cache_meets(const ie_cache *c, const void *p, size_t n) {
+    const CacheBytes b = cache_bytes(c);
+    bool any = false;
+    for (int i = 0; i < 4; ++i) {
+        any |= meet_bytes(b.p[i], b.n[i], p, n);
+        for (int j = 0; j < i; ++j) any |= meet_bytes(b.p[i], b.n[i], b.p[j], b.n[j]);
+    }
+    return any;
 }
 
 ie_status ie_cache_store(const ie_cache *c, int32_t heads, const ie_mat *QKV, const int32_t *slots, void *ws, size_t ws_bytes,
@@ -1469,7 +1493,7 @@ ie_status ie_cache_store(const ie_cache *c, int32_t heads, const ie_mat *QKV, co
     IE_CHECK(check_mat(QKV));
     if (heads < 0 || QKV->cols != (heads + 2ll * c->kv_heads) * c->head_dim) return IE_ERR_SHAPE;
     if (QKV->rows > 0 && !slots) return IE_ERR_NULL;
-    if (!aligned(slots, 4) || share_cache(QKV, c)) return IE_ERR_UNSUPPORTED;
+    if (!aligned(slots, 4) || share_cache(QKV, c) || cache_meets(c, slots, (size_t)QKV->rows * 4)) return IE_ERR_UNSUPPORTED;
     if (!ws || ws_bytes < HEADER) return IE_ERR_WORKSPACE;
     if (QKV->rows == 0) return IE_OK;
     return hip_status(launch_cache_store(cache_args(c, ws), QKV->rows, QKV->mant, QKV->exp, QKV->group == IE_GROUP_ROW,
