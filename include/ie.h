@@ -534,8 +534,8 @@ ie_status ie_attention_bwd(const ie_attention_desc *d, const ie_mat *QKV, const 
  *   else by parts: u_k = g + (1 - g) / factor, g = (n - low) / (high - low) cut
  *   to [0, 1], n = trained f / (2 pi) the turns of the unscaled frequency over
  *   the trained length (fast pairs stay, slow ones are stretched).
- * base > 0, factor > 0, trained >= 0, low < high if trained > 0, all finite,
- * else IE_ERR_UNSUPPORTED.
+ * base > 0, factor > 0, trained >= 0, low < high if trained > 0, all finite, and
+ * all angles too, else IE_ERR_UNSUPPORTED.
  */
 #define IE_ROPE_MAX 512
 typedef struct {

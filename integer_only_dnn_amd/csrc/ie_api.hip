@@ -1385,6 +1385,7 @@ ie_status ie_rope_table(const ie_rope_freqs *f, int32_t rot, int64_t positions, 
             keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
         }
         w[k] = fk * (keep + (1.0 - keep) / f->factor);
+        if (!(w[k] * (double)positions < inf)) return IE_ERR_UNSUPPORTED;  // an angle that is no number
     }
     return hip_status(launch_rope_table(w, rot / 2, positions, table, (hipStream_t)stream));
 }
