@@ -426,11 +426,11 @@ __global__ __launch_bounds__(256, DP > 64 ? 1 : 2) void attn_fwd_fine_kernel(Att
     k.init(p.width, p.dp);
     v.init(p.width, p.dp);
     for (int idx = blockIdx.x; idx < items; idx += gridDim.x) {
-        const int at = idx >> 3, pair = 8 * (at / p.group) + (idx & 7);
-        const int kvh = pair % p.kv, h = kvh * p.group + at % p.group;
+        const Item it = att_item(p, p.group, idx, items);
+        const int kvh = it.kvh, h = kvh * p.group + it.gh;
         Span sp;
         int tile;
-        if (!rank_tile<CAUSAL>(p, pair / p.kv, 64, sp, tile)) continue;
+        if (!rank_tile<CAUSAL>(p, it.rank, 64, sp, tile)) continue;
         const int n = sp.n, q0 = 64 * tile, qw = q0 + 16 * wave, qi = qw + (lane & 15);
         const long long row = sp.a + qi;
         const bool fine = qi < n && p.p16[row * p.parts + h] == P_FINE;

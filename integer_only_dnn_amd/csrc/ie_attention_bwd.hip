@@ -518,13 +518,14 @@ __device__ __forceinline__ bool any_of(bool mine, int (&sh)[4]) {
 }
 
 template <int DP, bool CAUSAL>
-__device__ __forceinline__ void fine_dq(const AttnArgs &p, const AttnBwd &bw, int idx, FineLds<DP> &lds) {
+__device__ __forceinline__ void fine_dq(const AttnArgs &p, const AttnBwd &bw, int idx, int of_q, FineLds<DP> &lds) {
     using T = HeadTile<DP>;
     constexpr int KS = T::KS, NE = DP / 16;
-    const int at = idx >> 3, pair = 8 * (at / p.group) + (idx & 7), kvh = pair % p.kv, h = kvh * p.group + at % p.group;
+    const Item it = att_item(p, p.group, idx, of_q);
+    const int kvh = it.kvh, h = kvh * p.group + it.gh;
     Span sp;
     int tile;
-    if (!rank_tile<CAUSAL>(p, pair / p.kv, 64, sp, tile)) return;
+    if (!rank_tile<CAUSAL>(p, it.rank, 64, sp, tile)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, quad = lane >> 4;
     const int n = sp.n, q0 = 64 * tile, qi = q0 + 16 * wave + (lane & 15);
     const long long row = sp.a + qi;
@@ -702,7 +703,7 @@ __global__ __launch_bounds__(256, DP > 64 ? 1 : 2) void attn_bwd_fine_kernel(Att
     for (int idx = blockIdx.x; idx < of_q + of_k; idx += gridDim.x) {
         __syncthreads();
         if (idx < of_k) fine_dkv<DP, CAUSAL>(p, bw, idx, lds);
-        else fine_dq<DP, CAUSAL>(p, bw, idx - of_k, lds);
+        else fine_dq<DP, CAUSAL>(p, bw, idx - of_k, of_q, lds);
     }
 }
 

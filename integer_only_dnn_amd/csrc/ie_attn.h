@@ -44,6 +44,7 @@
 // two to four waves to a SIMD where there was one.
 #pragma once
 
+#include "ie_attn_index.h"
 #include "ie_f64.h"
 #include "ie_internal.h"
 
@@ -139,114 +140,24 @@ struct Bool {
     static constexpr bool value = B;
 };
 
-// Sequence s of a packed batch: its rows [a, b).  Offsets are read on the
-// device; bounds that lie outside the matrix or before the last one are
-// clipped, a sequence longer than `most` is cut there.
-struct Span {
-    int a, n;
+// The lanes of a wave, as the search for a tile uses them (ie_attn_index.h).
+struct WaveLanes {
+    using Int = int;
+    template <class F>
+    __device__ __forceinline__ int each(F f) const { return f((int)(threadIdx.x & 63)); }
+    template <class F>
+    __device__ __forceinline__ uint64_t ballot(F f) const { return __ballot(f((int)(threadIdx.x & 63))); }
+    __device__ __forceinline__ int of(int x, int) const { return x; }
+    __device__ __forceinline__ int at(int x, int lane) const { return __builtin_amdgcn_readlane(x, lane); }
+    __device__ __forceinline__ int sum(int x) const { return __builtin_amdgcn_readfirstlane(lane_reduce<64>(x, Add{})); }
+    __device__ __forceinline__ int max(int x) const { return wave_max_dpp(x); }
 };
-__device__ __forceinline__ Span seq_span(const AttnArgs &p, int s) {
-    if (!p.off) return Span{0, (int)min(p.rows, (long long)p.most)};
-    const int rows = (int)p.rows;
-    const int a = min(max(p.off[s], 0), rows), b = min(max(p.off[s + 1], a), rows);
-    return Span{a, min(b - a, p.most)};
-}
-// Tiles of BM rows: sequence s owns the slots from off[s] / BM + s on, enough
-// for its ceil(n / BM) tiles whatever the other lengths are, so that a slot
-// finds its sequence by a search, 64 offsets a turn, and nothing is laid out
-// beforehand.  Returns the sequence's rows and the tile's first row in it (>= n:
-// no such tile).
-__device__ __forceinline__ Span slot_span(const AttnArgs &p, int slot, int bm, int &first) {
-    if (!p.off) {
-        first = slot * bm;
-        return seq_span(p, 0);
-    }
-    const int lane = threadIdx.x & 63;
-    int lo = 0, len = p.n_seq, step, x, y, k;
-    do {
-        step = (len + 63) >> 6;
-        const int i = lo + lane * step, in = min(i, p.n_seq - 1);
-        x = p.off[in];
-        y = p.off[in + 1];
-        const uint64_t below = __ballot(lane * step < len && max(x, 0) / bm + i <= slot);
-        k = below ? 63 - __builtin_clzll(below) : 0;
-        lo += k * step;
-        len = min(step, len - k * step);
-    } while (step > 1);
-    const int rows = (int)p.rows;
-    x = __builtin_amdgcn_readlane(x, k);
-    y = __builtin_amdgcn_readlane(y, k);
-    const int a = min(max(x, 0), rows), n = min(min(max(y, a), rows) - a, p.most);
-    const int at = slot - (max(x, 0) / bm + lo);
-    first = at < 0 || at > n / bm ? n : at * bm;
-    return Span{a, n};
-}
-
-// A launch's items: the tiles of every key head, and of each the `per` query
-// heads that share it.  Workgroups reach the XCDs in turn (blockIdx % 8).  In
-// general an XCD takes every eighth pair (tile, key head), tiles in order, the
-// heads of a pair one behind the other: they share its L2, and every XCD meets
-// heavy and light tiles alike.  Short sequences: it takes `chunk` pairs in a row,
-// then skips the others' seven chunks, so that the few tiles of a sequence read
-// its keys from one L2 (128 x 197 tokens, 12 heads of 64: forward pass 70 -> 67
-// us, dK and dV 135 -> 127).
-struct Item {
-    int rank, kvh, gh;
-};
-__device__ __forceinline__ Item att_item(const AttnArgs &p, int per) {
-    const int idx = blockIdx.x >> 3, xcd = blockIdx.x & 7, v = idx / per;
-    int u = 8 * v + xcd;
-    if (p.chunk) {
-        const int all = gridDim.x / 8 / per, turn = v / p.chunk, at = turn * p.chunk;
-        u = 8 * at + xcd * min(p.chunk, all - at) + v - at;
-    }
-    return Item{u / p.kv, u % p.kv, idx - v * per};
-}
-inline unsigned att_grid(long long tiles, int kv, int per) { return (unsigned)((tiles * kv + 7) / 8 * 8 * per); }
-// Pairs of a chunk: equal parts of up to 16 tiles, where sequences have up to 16
-// tiles on the average and all tiles of one are alike; else 0.
-inline int att_chunk(const AttnArgs &a, int bm, bool alike) {
-    const long long slots = att_slots(a.rows, a.n_seq, bm), each = (slots * a.kv + 7) / 8;
-    if (!alike || !a.off || a.rows > 16ll * bm * a.n_seq) return 0;
-    const long long turns = (each + 16 * a.kv - 1) / (16 * a.kv);
-    return (int)((each + turns - 1) / turns);
-}
-
-// The tile of a rank: its sequence and its number in it; false: none.  Tiles of
-// a causal launch differ in work (the t-th of a sequence meets t + 1 tiles of
-// keys): the heaviest come first, for up to 64 sequences (a lane each); else
-// sequences in order, each with enough ranks for its tiles (see slot_span).
+__device__ __forceinline__ Item att_item(const AttnArgs &p, int per) { return att_item(p, per, (int)blockIdx.x, (int)gridDim.x); }
 template <bool HEAVY>
 __device__ __forceinline__ bool rank_tile(const AttnArgs &p, int rank, int bm, Span &sp, int &tile) {
-    if (!HEAVY || !p.off || p.n_seq > 64) {
-        int first;
-        const int slots = (int)(p.rows / bm) + max(p.n_seq, 1);
-        sp = slot_span(p, HEAVY ? slots - 1 - rank : rank, bm, first);
-        tile = first / bm;
-        return rank < slots && first < sp.n;
-    }
-    const int lane = threadIdx.x & 63;
-    const Span mine = lane < p.n_seq ? seq_span(p, lane) : Span{0, 0};
-    const int tiles = (mine.n + bm - 1) / bm;
-    // tiles whose number is t or more: A(t) = sum max(0, tiles - t)
-    auto at_least = [&](int t) { return lane_reduce<64>(max(0, tiles - t), Add{}); };
-    int lo = 0, hi = wave_max_dpp(tiles);  // A(lo) > rank >= A(hi)
-    if (rank >= at_least(0)) return false;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (at_least(mid) > rank) lo = mid;
-        else hi = mid;
-    }
-    // the k-th sequence with a tile of number lo
-    int k = rank - at_least(lo + 1);
-    uint64_t have = __ballot(tiles > lo);
-    while (k-- > 0) have &= have - 1;
-    const int s = __builtin_ctzll(have);
-    sp.a = __builtin_amdgcn_readfirstlane(__shfl(mine.a, s, 64));
-    sp.n = __builtin_amdgcn_readfirstlane(__shfl(mine.n, s, 64));
-    tile = __builtin_amdgcn_readfirstlane(lo);
-    return true;
+    return rank_tile<HEAVY>(WaveLanes{}, p, rank, bm, sp, tile);
 }
+inline int att_chunk(const AttnArgs &a, int bm, bool alike) { return att_chunk(a.rows, a.n_seq, a.kv, bm, alike && a.off); }
 
 // 16 mantissas of a head from column 16 c on, at any alignment; past d: zeros.
 __device__ __forceinline__ v4i head16(const int8_t *head, int c, int d) {
