@@ -35,7 +35,8 @@
  *     to the overwriting: rows of a packed batch that belong to no sequence,
  *     and slots of a cache that no row names, are left as they were;
  *   - `ws` is a workspace of at least the size the matching *_workspace_bytes
- *     call returns; its first 256 bytes hold sticky flags and must be zeroed
+ *     call returns; its first 256 bytes hold sticky flags (and words that are
+ *     zero again behind every call) and must be zeroed
  *     once (ie_workspace_init) before first use;
  *   - work is enqueued on `stream` (a hipStream_t; NULL = default stream) and
  *     runs asynchronously; calls sharing one workspace must be ordered on one
@@ -441,7 +442,8 @@ ie_status ie_dropout(const ie_mat *X, const ie_mat *R, const ie_mat *Y, const ie
  * rounded once into O.  So a weight is held to 15 bits below the largest one,
  * and a token's result depends on the tokens that it sees and on no others.
  * Of N keys rounding takes at most N / 2 units of L, which is 32512 at least, and
- * N / 2 units times 128 of a sum of values: up to 2032 keys at most 1 / 32 of both.
+ * N / 2 units times 128 of a sum of values: up to 2032 keys a 32nd of 32512 and of
+ * 32512 times 128 (in units of 2^E).
  * A row of a head that sees more keys has fine weights where that is not enough:
  * where sum R(2^7 w) and 2^7 L differ by more than 2^7 L / 32, or no sum of
  * values reaches 64 N.  Then L = sum R(2^14 w) and o = (sum_j R(2^14 w_j
@@ -494,6 +496,9 @@ ie_status ie_attention_fwd(const ie_attention_desc *d, const ie_mat *QKV, const 
  * A row of fine weights has its sum for dQ in units of 2^-14 (R(s 2^(e_j - sigma
  * + 14)), times 2^-14 behind it), and so have, for dV and dK (there in the place of
  * 2^6), all keys of a sequence and key head of which a query's weights are fine.
+ * Without fine weights N integers are off by half a unit each: an element of dV by
+ * at most N / 32512 of the largest |dO| (a 16th at 2032 tokens), one of dQ by N
+ * scale 2^(eo_i + sigma) / (2 L_i) times the largest |k_j|.
  * The powers of two come from bounds: with |x| < 2^[x], [x] half the bits of
  * sum x^2, rounded up, bits n of a whole number, and maxima over a sequence
  *   nu_j = [v_j] + e_j,  delta_i = bits |dO_i . O_i| + eO_i,

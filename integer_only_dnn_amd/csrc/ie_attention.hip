@@ -52,11 +52,14 @@ hipError_t launch_attention_pad(const int8_t *x, long long rows, int nh, int d, 
 // staged by the wave itself; they share the maximum after the first pass and add
 // their sums up after the second.
 //
-// Bound by vector instructions: 128 x 197 tokens x 12 heads of 64 68 us, 66 % of the
-// cycles issue one; 5 sequences of 8192 tokens x 32 heads of 128, causal, 288 us (142
-// G operations: 0.49 POP/s), 70 %, and 23 % in matrix instructions.  Eight waves to
-// a workgroup, which halves the loads, waits longer at its barriers (74 and 357 us);
-// 32 x 32 products need twice the registers.
+// Bound by vector instructions: 128 x 197 tokens x 12 heads of 64 65 us, 82 % of the
+// cycles in which a CU is busy issue one; 5 sequences of 8192 tokens x 32 heads of 128,
+// causal, 290 us (142 G operations: 0.49 POP/s), 75 %, and 24 % in matrix instructions.
+// Of 29 and 26 instructions to a pair of tokens 15 are the second pass's and 6 the first
+// one's, 17 in all where scores are kept; the others are masked keys and queries past a
+// sequence's end, the search, and the results' products and rounding in fp64.  Eight waves
+// to a workgroup, which halves the loads, waits longer at its barriers (74 and 357 us); 32 x
+// 32 products need twice the registers.
 template <int DP, bool ROW, bool CAUSAL, bool SHORT, int SPLIT>
 __global__ __launch_bounds__(256, SPLIT > 1 ? 2 : DP > 64 ? 3 : 4) void attn_fwd_kernel(AttnArgs p) {
     using T = HeadTile<DP, 256 / SPLIT>;
@@ -145,7 +148,7 @@ __global__ __launch_bounds__(256, SPLIT > 1 ? 2 : DP > 64 ? 3 : 4) void attn_fwd
             p.stats[row * p.heads + h] = int2{__float_as_int(ROW ? m : (float)mi * pow2f(eq)), (int)sum};
         if (fine && lane < 16) {
             p.p16[row * p.parts + h] = P_FINE;
-            atomicOr(p.flags + FINE_WORD, 1u);
+            p.flags[FINE_WORD] = 1;  // the same from every lane that says so
         }
     };
 

@@ -120,7 +120,7 @@ __global__ __launch_bounds__(256) void attn_scale_kernel(AttnArgs p, AttnBwd b) 
         kl = max(kl, alpha + e - e_top + max(d.y + n_top, delta) + 1);  // a |u| 2^e < 2^kl
     }
     b.key[(long long)it.kvh * p.rows + row] = AttnKey{(int16_t)ka, (int16_t)kl};
-    if (fine) atomicOr(p.flags + FINE_WORD, 1u);
+    if (fine) p.flags[FINE_WORD] = 1;  // the same from every thread that says so
 }
 
 // The largest bounds of all queries of a sequence (none: -4096 each), and of those that see
@@ -158,9 +158,10 @@ __device__ __forceinline__ void key_bounds(const AttnKey *marks, int n, int k0, 
 // to four lanes, as in the forward pass; keys and values pass through LDS.  SPLIT
 // 4: the waves take the same 16 queries and every fourth tile of keys each, and
 // add their sums up at the end.
-// Bound by vector instructions (17 to a weight), 62 % of the cycles at 128 x 197
-// tokens x 12 heads of 64 (71 us), and by the longest rows' way through their keys
-// where tiles are few (4096 tokens in 3 sequences x 16 heads, causal: 51 us, 53 %).
+// Bound by vector instructions (17 to a weight, 29 and 20 to a pair of tokens with all that
+// lies around them), 75 % of the cycles in which a CU is busy at 128 x 197 tokens x 12
+// heads of 64 (72 us), and by the longest rows' way through their keys where tiles are
+// few (4096 tokens in 3 sequences x 16 heads, causal: 51 us, 74 %).
 template <int DP, bool ROW, bool CAUSAL, int SPLIT>
 __global__ __launch_bounds__(256, DP > 64 ? 2 : 3) void attn_dq_kernel(AttnArgs p, AttnBwd bw) {
     using T = HeadTile<DP, 256 / SPLIT>;
@@ -277,9 +278,10 @@ __global__ __launch_bounds__(256, DP > 64 ? 2 : 3) void attn_dq_kernel(AttnArgs 
 //    64 queries change hands in LDS, and each wave sums a quarter of the elements:
 //    half the registers for the sums (five digits to an element and key), which are
 //    160 to a lane otherwise where heads have 128 elements.
-// Bound by vector instructions (21 to a weight beside a sixth of the time in
-// matrix instructions) and, at two to three waves a SIMD, by waits for LDS:
-// 128 x 197 tokens x 12 heads of 64 54 % of the cycles issue one, 123 us.
+// Bound by vector instructions (21 to a weight, 48 to a pair at 197 tokens and 32 at up
+// to 2230, with masked pairs, the marks and the results in fp64, beside a sixth of the time
+// in matrix instructions) and, at two to three waves a SIMD, by waits for LDS:
+// 128 x 197 tokens x 12 heads of 64 70 % of the cycles in which a CU is busy, 125 us.
 template <int DP, bool CAUSAL, int SPLIT>
 __global__ __launch_bounds__(256, SPLIT == 2 ? 2 : DP > 64 ? 1 : SPLIT == 4 ? 2 : 3) void attn_dkv_kernel(AttnArgs p, AttnBwd bw) {
     constexpr bool OWN = SPLIT == 4, SHARE = SPLIT == 2;  // own tiles; shared elements

@@ -10,7 +10,7 @@
 // in one fused multiply-add leaves y in the low bits of a float in [64, 96],
 // whose bits 17..22 are floor(y) + 32 and whose fraction is y's: ten
 // instructions a weight from the int32 product on, the exponential itself
-// seven.  The unit resolution of 2^-17 and the polynomial's error are an
+// eight.  The unit resolution of 2^-17 and the polynomial's error are an
 // order below half a step of the 7-bit mantissas that come out.
 //
 // Digits.  A weight enters a product as an integer n = rint(w ...) of at most

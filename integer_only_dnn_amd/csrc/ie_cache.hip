@@ -75,9 +75,11 @@ __global__ __launch_bounds__(256) void cache_store_kernel(CacheArgs p, long long
 // which the exact sums drop.  The next block's keys, values and exponents and the
 // slots of the one behind it are in flight while one is computed.
 //
-// Bound by the stream over the cache, less what two barriers a block keep it from:
-// 48 sequences of up to 8000 tokens, 32 heads on 8 of 128 (196 MB) 47 us, 4.2 TB/s;
-// one of 131072 (136 MB) 32 us.  SUB 1 for these four heads takes 5 % longer.
+// 48 sequences of up to 8000 tokens, 32 heads on 8 of 128 (196 MB) 45 us where the cache's
+// last level holds them, 4.3 TB/s, and 60 from memory; one of 131072 (136 MB) 32 and 42.
+// Waits are 56 % of a wave's life, vector instructions 48 % of the busy cycles: neither the
+// stream nor the instructions alone.  A key head's 64 bytes are half a line, whose
+// other half another workgroup reads.  SUB 1 for these four heads takes 5 % longer.
 template <int SUB>
 __device__ __forceinline__ float heads_max(float v) {
     v = col_max(v);
