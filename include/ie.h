@@ -603,8 +603,9 @@ ie_status ie_cache_store(const ie_cache *c, int32_t heads, const ie_mat *QKV, co
  * half a unit of a run's sums behind that, of eight runs less than 1 / 36 in all.
  * Over more runs 16 neighbouring elements of a head (from a multiple of 16 on) are
  * taken with fine weights, R(2^14 a_b) and R(2^14 a_b 2^(E_b - E)), where sum
- * R(2^6 a_b) L_b differs from 2^6 sum R(a_b) L_b by more than a 32nd of it, or
- * where none of their sums reaches 4 sum_b L_b (both sums then held to 53 bits).
+ * R(2^14 a_b) L_b differs from 2^14 sum R(a_b) L_b by more than a 32nd of it, or
+ * sum R(2^14 a_b 2^(E_b - E)) L_b from 2^14 sum R(a_b 2^(E_b - E)) L_b by more
+ * than 512 times the largest of their sums (both sums then held to 53 bits).
  * A sequence without keys gives zeros.  A length outside 0 .. per * page sets
  * IE_FLAG_INDEX and is cut; a page outside the cache sets it and its keys are
  * left out.  O [n x heads * head_dim] must be ROW, else IE_ERR_UNSUPPORTED.

@@ -371,10 +371,11 @@ __global__ __launch_bounds__(256, 4) void cache_attention_kernel(CacheArgs p, At
 //
 // Fine weights, as in attention over a prompt: a block's weight takes half a unit of
 // its sums at most, of eight blocks (the largest's weight is exact) less than 7 * 128 /
-// 32512 = 1 / 36 in all.  With more of them the weights' sum is taken in units of 2^-6 too;
-// where that changes it by more than a 32nd, or where none of 16 neighbouring
-// elements reaches half a unit of all blocks' sums of weights with values of 8, these
-// elements are summed again with 2^14 units to one, in two halves of the weights.
+// 32512 = 1 / 36 in all.  With more of them the weights' sum, and that of the values'
+// weights a_b 2^(E_b - E), are taken in units of 2^-14 too; where that changes the first
+// by more than a 32nd, or the second by so much that with values of 8 it is a fourth of
+// the largest of 16 neighbouring elements, these elements are summed again in such units,
+// in two halves of the weights.
 __global__ __launch_bounds__(256) void cache_join_kernel(CacheArgs p, AttnArgs a, int piece) {
     __shared__ int sh[4];
     __shared__ int sw[256];
@@ -444,17 +445,19 @@ __global__ __launch_bounds__(256) void cache_join_kernel(CacheArgs p, AttnArgs a
         }
         return sum;
     };
-    long long n[3];  // the weights' sum, what rounding took of it in units of 2^-6, the sum of the blocks' own sums
+    long long n[3];  // the weights' sum, what rounding took of it in units of 2^-14, and of the values' weights
     const long long sum = join([](float x, float f, int l, long long (&n)[3]) {
-        const int w = (int)__builtin_rintf(x);
+        const int w = (int)__builtin_rintf(x), v = (int)__builtin_rintf(x * f);
         n[0] += (long long)w * l;
-        n[1] += (long long)((int)__builtin_rintf(x * 64.0f) - 64 * w) * l;
-        n[2] += l;
-        return (int)__builtin_rintf(x * f);
+        n[1] += (long long)((int)__builtin_rintf(x * FINE_UNIT) - (w << ATT_FINE)) * l;
+        n[2] += (long long)((int)__builtin_rintf(x * f * FINE_UNIT) - (v << ATT_FINE)) * l;
+        return v;
     }, n);
     double y = n[0] > 0 ? (double)sum * (1.0 / (double)n[0]) : 0.0;
     const long long big = lane_reduce<16>(sum < 0 ? -sum : sum, [](long long x, long long z) { return x > z ? x : z; });
-    const bool fine = nb > CACHE_CHECK && n[0] > 0 && ((n[1] < 0 ? -n[1] : n[1]) > 2 * n[0] || big < 4 * n[2]) && tid < piece;
+    // 512 = 2^14 / 32; 512 big may not fit 64 bits
+    const bool much = (n[1] < 0 ? -n[1] : n[1]) > 512 * n[0] || ((n[2] < 0 ? -n[2] : n[2]) + 511) >> 9 > big;
+    const bool fine = nb > CACHE_CHECK && n[0] > 0 && much && tid < piece;
     constexpr int SOME = 0x7fffffff;  // no result has such a high word
     int word = row_reduce<256>(fine ? SOME : __double2hiint(y) & 0x7fffffff, Max{}, sh);
     if (word == SOME) {

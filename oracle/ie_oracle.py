@@ -1060,8 +1060,8 @@ def cache_join(parts, r, blocks: int = 0) -> np.ndarray:
 
 
 def cache_sums(parts, r) -> tuple:
-    """(sum of weights, sums of values, the same of the weights in units of 2^-6, sum of L_b, of fine weights and values, in two
-    halves at bit 15): whole numbers below 2^62."""
+    """(sum of weights, sums of values; what rounding takes, in units of 2^-14, of the weights' sum and of that of the values'
+    weights; sums of fine weights and of values with them, in two halves at bit 15): whole numbers below 2^62."""
     m, top = max(z[0] for z in parts), max(z[2] for z in parts)
     a = softmax_weight(_f32(np.array([z[0] for z in parts]) - m), r)
     x = np.ldexp(a, np.array([z[2] for z in parts]) - top)
@@ -1069,15 +1069,16 @@ def cache_sums(parts, r) -> tuple:
     whole = lambda z, s: np.rint(np.ldexp(z, s)).astype(np.int64)  # noqa: E731
     assert len(parts) <= 1 << 15 and lb.max() <= 256 * ATT_UNIT and np.abs(nb).max() <= 8 * 256 * ATT_UNIT
     halves = [(f(whole(a, ATT_FINE)) @ lb, f(whole(x, ATT_FINE)) @ nb) for f in (lambda z: z >> 15, lambda z: z & 32767)]
-    return whole(a, 0) @ lb, whole(x, 0) @ nb, whole(a, 6) @ lb, lb.sum(), halves
+    lost = [abs(int((whole(z, ATT_FINE) - (whole(z, 0) << ATT_FINE)) @ lb)) for z in (a, x)]
+    return whole(a, 0) @ lb, whole(x, 0) @ nb, *lost, halves
 
 
-def _cache_result(total, num, sixth, every, halves, blocks) -> np.ndarray:
+def _cache_result(total, num, lost, lost_x, halves, blocks) -> np.ndarray:
     y = num.astype(np.float64) * (1.0 / np.float64(total))
     if blocks <= CACHE_CHECK:
         return y
     big = np.abs(num).reshape(-1, 16).max(axis=1).repeat(16)
-    fine = (np.abs(sixth - 64 * total) > 2 * total) | (big < 4 * every)
+    fine = (lost > 512 * total) | ((lost_x + 511) // 512 > big)
     (d_hi, hi), (d_lo, lo) = halves
     den = np.float64(d_hi) * 32768.0 + np.float64(d_lo)
     return np.where(fine, (hi.astype(np.float64) * 32768.0 + lo.astype(np.float64)) * (1.0 / den), y)

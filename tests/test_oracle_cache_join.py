@@ -74,3 +74,24 @@ def test_few_blocks_stay_coarse():
             assert s < 1 / 32 and np.allclose(got, 1.0, rtol=1e-15)
         else:  # a weight's error and half a unit of 2^-14 of 0.46
             assert np.allclose(got, (1 + 2 * s) / (1 + s), rtol=W_ERR + 0.5 * 2.0 ** -14 / 0.46)
+
+
+def test_a_small_tail_that_is_the_whole_result():
+    """A tail of a 45th of the weight, beside a key whose value is zero: the weights' sum hardly changes, the values' is all there
+    is.  Tolerances as above, a key's rounding taking no more than its weight."""
+    rng, n = np.random.default_rng(8), 131072
+    cache, Q, scale = sink_cache(rng, n, 15.6, mean=2)
+    O = o.attention_cache(Q, cache, [np.arange(n)], 1, 1, 16, scale)
+    k = np.ldexp(o.unpack4(cache["k"][:, 0]).astype(float), cache["ke"].astype(int))
+    v = np.ldexp(o.unpack4(cache["v"][:, 0]).astype(float), cache["ve"].astype(int))
+    t = k @ (Q.mant[0].astype(float) / 256) * float(np.float32(scale))
+    p = np.exp(t - t.max())
+    want = p / p.sum() @ v
+    assert 0.01 < (p.sum() - 1) / p.sum() < 1 / 32
+    at = np.arange(0, n, 256)
+    m, size = np.maximum.reduceat(p, at), np.add.reduceat(p, at)
+    vm = 7 * 2.0 ** -2
+    tol = 4 * W_ERR * (p / p.sum() @ np.abs(v)).max() + 2 * np.minimum(m.repeat(256) * 0.5 / 32512, p).sum() / p.sum() * vm
+    tol += 2 * (0.5 * 2.0 ** -14 / 32512 * size / m).sum() / p.sum() * vm
+    assert np.all(np.abs(O.mant[0] * 2.0 ** int(O.exp[0]) - want) <= tol + 0.5 * 2.0 ** int(O.exp[0]))
+    assert tol < 0.5 * np.abs(want).max()
